@@ -1,6 +1,7 @@
 """GB300 speculative-decoding verify/accept and MTP shift/insert.
 
-A thin ctypes binding over libspecdec.so (include/specdec.h).  The functions
+A thin ctypes binding over libspecdec.so (include/specdec.h; the operators
+around the verify step, include/specdec_step.h, are in step.py).  The functions
 keep the C names; they only marshal torch tensors into device pointers, sizes
 and the current CUDA stream.  Every step of the computation runs in the
 library's kernels; there is no fallback: if the library is missing or no GPU
@@ -20,6 +21,8 @@ __all__ = [
     "spec_verify", "spec_verify_packed", "spec_verify_early_exit", "spec_verify_sharded",
     "spec_verify_shard_rank", "ShardOps", "shard_exchange_buffers", "bytes_read", "mtp_shift_insert", "get_error", "launch_shape", "F32", "BF16",
     "DEV_ERR_TOKEN", "DEV_ERR_DRAFT_LEN", "DEV_ERR_TEMPERATURE", "DEV_ERR_TIMEOUT", "DEV_ERR_SEGMENT",
+    "kv_block_step", "BlockStep", "kv_append", "spec_attention", "new_attention_workspace", "spec_process_logits",
+    "DEV_ERR_BLOCKS", "DEV_ERR_PENALTY", "ATTENTION_WORKSPACE_BYTES",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -103,6 +106,10 @@ def load_library(path: Optional[str] = None):
         if hasattr(L, "spec_verify_no_alloc"):
             L.spec_verify_no_alloc.argtypes = [P, P, ctypes.c_int, i32, i32, i32, P, P, P, u64, P, P, P, P]
             L.spec_verify_no_alloc.restype = ctypes.c_int
+        if hasattr(L, "kv_block_step"):
+            from . import step as _step
+
+            _step.declare(L)
         if path is None:
             _lib = L
         return L
@@ -554,3 +561,7 @@ def get_error(workspace: torch.Tensor) -> int:
     if st not in (0, 5, 6):
         _check(st, "specdec_get_error")
     return bits.value
+
+
+from .step import (ATTENTION_WORKSPACE_BYTES, DEV_ERR_BLOCKS, DEV_ERR_PENALTY, BlockStep, kv_append,  # noqa: E402
+                   kv_block_step, new_attention_workspace, spec_attention, spec_process_logits)

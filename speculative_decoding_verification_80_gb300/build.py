@@ -47,8 +47,8 @@ def source_digest(skip=()) -> str:
     """Hash of the code the library is built from (kernels, headers, flags),
     comments aside, so an edit to comments keeps the recorded measurements of
     the same code valid.  `skip` leaves out source files by name (the verify
-    kernel's digest leaves out the MTP kernel's and the sharded verify's
-    files, which it does not include)."""
+    kernel's digest leaves out the files of the MTP kernel, of the sharded
+    verify and of the operators around the step, which it does not include)."""
     h = hashlib.sha256()
     files = sorted(glob.glob(os.path.join(CSRC, "*"))) + sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
     for f in files:
@@ -63,7 +63,8 @@ def source_digest(skip=()) -> str:
 
 def verify_digest() -> str:
     """Digest of the sources the verify kernel is built from."""
-    return source_digest(skip=("mtp_kernel.cuh", "shard_kernels.cuh", "shard_api.cu", "specdec_shard.h"))
+    return source_digest(skip=("mtp_kernel.cuh", "shard_kernels.cuh", "shard_api.cu", "specdec_shard.h", "step_api.cu",
+                               "attention_kernel.cuh", "kv_kernels.cuh", "logits_kernel.cuh", "specdec_step.h"))
 
 
 def _up_to_date() -> bool:

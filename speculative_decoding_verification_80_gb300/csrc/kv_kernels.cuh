@@ -1,0 +1,340 @@
+// kv_kernels.cuh — the paged cache's bookkeeping (kv_block_step) and the
+// writer of its 8-bit blocks (kv_append).
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+namespace specdec {
+
+// ------------------------------------------------------------ kv_block_step
+struct BlockArgs {
+  int32_t B, bs, max_blocks, num_blocks, capacity;
+  const int32_t* kv_len;
+  const int32_t* accepted_len;
+  const int32_t* new_tokens;
+  const int32_t* held;
+  int32_t* table;
+  int32_t* ring;
+  const int32_t* ring_state;
+  int32_t* kv_len_out;
+  int32_t* held_out;
+  int32_t* ring_state_out;
+  int32_t* cu_tokens;
+  int32_t* cu_blocks;
+  int32_t* slot_map;
+  int32_t* positions;
+  uint32_t* err;
+  int32_t fill;  // 1: the plan kernel also writes tables and slots
+};
+
+constexpr int kBlockThreads = 1024;
+
+// Exclusive prefix sum over the block of one value a thread; `total` is the
+// sum.  `part` holds a warp's sum each.
+__device__ __forceinline__ long long block_prefix(long long x, long long* part, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long s = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xFFFFFFFFu, s, d);
+    if (lane >= d) s += o;
+  }
+  __syncthreads();  // the last use of `part` is over
+  if (lane == 31) part[warp] = s;
+  __syncthreads();
+  if (warp == 0) {
+    long long w = lane < kBlockThreads / 32 ? part[lane] : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xFFFFFFFFu, w, d);
+      if (lane >= d) w += o;
+    }
+    part[lane] = w;
+  }
+  __syncthreads();
+  *total = part[kBlockThreads / 32 - 1];
+  return s - x + (warp > 0 ? part[warp - 1] : 0);
+}
+
+// The index b in [0, n) with cu[b] <= t < cu[b + 1]; cu is non-decreasing,
+// cu[0] <= t < cu[n].
+__device__ __forceinline__ int owner_of(const int32_t* cu, int n, int t) {
+  int lo = 0, hi = n;  // cu[lo] <= t < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// Slot and position of new token t of request b, and the table entries that
+// the step fills; both read the ring and the entries that were there before.
+__device__ __forceinline__ void fill_token(const BlockArgs& a, int head, int t, int total) {
+  if (t >= total) {
+    a.slot_map[t] = -1;
+    a.positions[t] = -1;
+    return;
+  }
+  const int b = owner_of(a.cu_tokens, a.B, t);
+  const int p = a.kv_len_out[b] + (t - a.cu_tokens[b]);
+  const int j = p / a.bs;
+  const int taken = a.cu_blocks[b + 1] - a.cu_blocks[b];
+  const int before = a.held_out[b] - taken;
+  int block;
+  if (taken > 0 && j >= before)
+    block = a.ring[static_cast<int>((static_cast<long long>(head) + a.cu_blocks[b] + (j - before)) % a.num_blocks)];
+  else
+    block = a.table[static_cast<long long>(b) * a.max_blocks + j];
+  a.slot_map[t] = block * a.bs + p % a.bs;
+  a.positions[t] = p;
+}
+__device__ __forceinline__ void fill_block(const BlockArgs& a, int head, int i) {
+  const int b = owner_of(a.cu_blocks, a.B, i);
+  const int k = i - a.cu_blocks[b];
+  const int before = a.held_out[b] - (a.cu_blocks[b + 1] - a.cu_blocks[b]);
+  a.table[static_cast<long long>(b) * a.max_blocks + before + k] =
+      a.ring[static_cast<int>((static_cast<long long>(head) + i) % a.num_blocks)];
+}
+
+// One CTA: lengths, grants and their prefix sums, and the blocks that go back.
+__global__ void __launch_bounds__(kBlockThreads) block_plan_kernel(const BlockArgs a) {
+  __shared__ long long part[32];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int N = a.num_blocks;
+  int head = a.ring_state[0], count = a.ring_state[1];
+  uint32_t bad = 0;
+  if (head < 0 || head >= N || count < 0 || count > N) {
+    bad = 1;
+    head = head < 0 || head >= N ? 0 : head;
+    count = max(0, min(count, N));
+  }
+  long long asked = 0, took = 0, gave = 0, tokens = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kBlockThreads) {
+    const int b = b0 + tid;
+    const bool in = b < a.B;
+    int kept = 0, want = 0, held = 0, need = 0;
+    if (in) {
+      const int fresh = a.new_tokens[b];
+      held = a.held[b];
+      if (held < 0 || held > a.max_blocks) {
+        bad = 1;
+        held = max(0, min(held, a.max_blocks));
+      }
+      want = max(fresh, 0);
+      if (fresh >= 0) {
+        long long k = a.kv_len[b];
+        if (a.accepted_len != nullptr) k += max(a.accepted_len[b], -1) + 1LL;
+        if (k < 0 || k > static_cast<long long>(held) * a.bs) {
+          bad = 1;
+          k = max(0LL, min(k, static_cast<long long>(held) * a.bs));
+        }
+        kept = static_cast<int>(k);
+      }
+      need = static_cast<int>(min(0x7FFFFFFFLL, (static_cast<long long>(kept) + want + a.bs - 1) / a.bs));
+    }
+    const bool fits = need <= a.max_blocks;
+    const int grow = fits ? max(need - held, 0) : 0;
+    long long sum;
+    const long long at = asked + block_prefix(grow, part, &sum);
+    asked += sum;
+    const bool granted = in && fits && (grow == 0 || at + grow <= count);
+    if (in && !granted) bad = 1;
+    const int taken = granted ? grow : 0;
+    const int given = granted ? max(held - need, 0) : 0;
+    const long long tok_at = tokens + block_prefix(granted ? want : 0, part, &sum);
+    tokens += sum;
+    const long long give_at = gave + block_prefix(given, part, &sum);
+    gave += sum;
+    // grants are a prefix of the requests that ask for blocks, so the blocks
+    // taken before b are those asked for before it while grants last
+    const long long take_at = took + block_prefix(taken, part, &sum);
+    took += sum;
+    if (in) {
+      if (tok_at + want > a.capacity && granted) bad = 1;
+      a.kv_len_out[b] = kept;
+      a.held_out[b] = held + taken - given;
+      a.cu_tokens[b] = static_cast<int>(min(tok_at, static_cast<long long>(a.capacity)));
+      a.cu_blocks[b] = static_cast<int>(take_at);
+    }
+    // blocks that go back, a warp to a request
+    uint32_t m = __ballot_sync(0xFFFFFFFFu, given > 0);
+    while (m) {
+      const int src = __ffs(m) - 1;
+      m &= m - 1;
+      const int n = __shfl_sync(0xFFFFFFFFu, given, src);
+      const int from = __shfl_sync(0xFFFFFFFFu, held - given, src);
+      const long long to = __shfl_sync(0xFFFFFFFFu, give_at, src);
+      const long long row = static_cast<long long>(b - lane + src) * a.max_blocks;
+      for (int i = lane; i < n; i += 32)
+        a.ring[static_cast<int>((static_cast<long long>(head) + count + to + i) % N)] = a.table[row + from + i];
+    }
+  }
+  if (tid == 0) {
+    a.cu_tokens[a.B] = static_cast<int>(min(tokens, static_cast<long long>(a.capacity)));
+    a.cu_blocks[a.B] = static_cast<int>(took);
+    a.ring_state_out[0] = static_cast<int>((head + took) % N);
+    a.ring_state_out[1] = static_cast<int>(min(static_cast<long long>(N), count - took + gave));
+  }
+  if (bad && a.err != nullptr) atomicOr(a.err, SPECDEC_DEV_ERR_BLOCKS);
+  if (!a.fill) return;
+  __syncthreads();
+  const int total = a.cu_tokens[a.B], blocks = a.cu_blocks[a.B];
+  for (int t = tid; t < a.capacity; t += kBlockThreads) fill_token(a, head, t, total);
+  for (int i = tid; i < blocks; i += kBlockThreads) fill_block(a, head, i);
+}
+
+// Many CTAs: the same for long prompts.
+__global__ void block_fill_kernel(const BlockArgs a) {
+  const int total = a.cu_tokens[a.B], blocks = a.cu_blocks[a.B];
+  const int N = a.num_blocks;
+  const int head = static_cast<int>((static_cast<long long>(a.ring_state_out[0]) + N - blocks) % N);
+  const int t = static_cast<int>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (t < a.capacity) fill_token(a, head, t, total);
+  for (int i = t; i < blocks; i += static_cast<int>(gridDim.x) * blockDim.x) fill_block(a, head, i);
+}
+
+// ---------------------------------------------------------------- kv_append
+struct AppendArgs {
+  const void* x[2];  // k, v
+  long long token_stride[2], head_stride[2];  // bytes
+  uint8_t* cache[2];
+  float* scale[2];
+  const int32_t* slot_map;
+  int32_t T, H, bs, num_blocks;
+  int32_t window;  // tokens whose runs' starts one CTA takes
+};
+
+constexpr int kAppendThreads = 128;
+constexpr int kMaxBlockSize = 128;
+
+// The least power of two s with amax <= 448 s, for a finite amax > 0; 0 of 0.
+// amax = f 2^e with f in [1, 2): 448 = 1.75 * 2^8, so s = 2^(e - 8), twice
+// that for f > 1.75.  Subnormal amax counts as the least normal number.
+__device__ __forceinline__ float pow2_scale(float amax) {
+  if (!(amax > 0.f)) return 0.f;
+  const uint32_t u = __float_as_uint(amax);
+  const int e = max(static_cast<int>(u >> 23), 1) + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0) - 8;
+  return __uint_as_float(static_cast<uint32_t>(max(e, 1)) << 23);
+}
+// The least power of two at or above a block's scale (its own, where this
+// writer set it); 0 for what is no scale.
+__device__ __forceinline__ float pow2_ceil(float s) {
+  if (!(s > 0.f) || isinf(s)) return 0.f;
+  const uint32_t u = __float_as_uint(s);
+  const uint32_t e = (u >> 23) + ((u & 0x7FFFFFu) != 0 ? 1 : 0);
+  return __uint_as_float(min(max(e, 1u), 253u) << 23);
+}
+// 1 / s of a power of two s (0 of 0): exact.
+__device__ __forceinline__ float pow2_inverse(float s) {
+  return s > 0.f ? __uint_as_float((254u << 23) - __float_as_uint(s)) : 0.f;
+}
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 e4m3_values(uint32_t pair) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(pair), __NV_E4M3);
+  return __half22float2(__half2(h));
+}
+
+template <typename Elt>
+__device__ __forceinline__ void unpack16(const uint4& q, float* f);
+template <>
+__device__ __forceinline__ void unpack16<float>(const uint4& q, float* f) {
+  f[0] = __uint_as_float(q.x), f[1] = __uint_as_float(q.y), f[2] = __uint_as_float(q.z), f[3] = __uint_as_float(q.w);
+}
+template <>
+__device__ __forceinline__ void unpack16<__nv_bfloat16>(const uint4& q, float* f) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+// Simple form: a CTA per (window of tokens, head, k or v) goes through the
+// runs that start in its window.
+template <typename Elt, int D>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+  constexpr int E = 16 / sizeof(Elt);  // values of a 16-byte load
+  constexpr int VR = D / E;            // loads of a row
+  __shared__ int32_t slots[kMaxBlockSize * 2 + 1];
+  __shared__ float red[kAppendThreads / 32];
+  const int tid = threadIdx.x;
+  const int h = blockIdx.y, which = blockIdx.z;
+  const long long t0 = static_cast<long long>(blockIdx.x) * a.window;
+  const int span = static_cast<int>(min(static_cast<long long>(a.window) + a.bs, a.T - t0));  // tokens looked at
+  const long long most = static_cast<long long>(a.num_blocks) * a.bs;
+  for (int i = tid; i <= span; i += kAppendThreads) {
+    const long long t = t0 + i - 1;
+    int s = t >= 0 ? __ldg(a.slot_map + t) : -1;
+    if (s >= most) s = -1;
+    slots[i] = s;
+  }
+  __syncthreads();
+  const char* x = static_cast<const char*>(a.x[which]) + h * a.head_stride[which];
+  const int owned = min(a.window, span);
+  for (int i = 0; i < owned;) {
+    const int s = slots[i + 1], before = slots[i];
+    const int block = s / a.bs, off = s - block * a.bs;
+    if (s < 0 || (before >= 0 && before + 1 == s && off != 0)) {  // none, or inside a run
+      ++i;
+      continue;
+    }
+    int n = 1;
+    while (i + n < span && off + n < a.bs && slots[i + n + 1] == s + n) ++n;
+    const char* row = x + (t0 + i) * a.token_stride[which];
+    float amax = 0.f;
+    for (int k = tid; k < n * VR; k += kAppendThreads) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + (k / VR) * a.token_stride[which]) + k % VR);
+      float f[E];
+      unpack16<Elt>(q, f);
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (isfinite(f[e])) amax = fmaxf(amax, fabsf(f[e]));
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+    __syncthreads();
+    if ((tid & 31) == 0) red[tid >> 5] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, red[w]);
+    float* sp = a.scale[which] + static_cast<long long>(block) * a.H + h;
+    const float old = off > 0 ? *sp : 0.f;
+    const float now = fmaxf(pow2_scale(amax), pow2_ceil(old));
+    const float inv = pow2_inverse(now);
+    uint8_t* tile = a.cache[which] + (static_cast<long long>(block) * a.H + h) * a.bs * D;
+    if (off > 0 && now > old) {  // the older tokens move to the new scale
+      const float ratio = old * inv;
+      for (int k = tid; k < off * (D / 2); k += kAppendThreads) {
+        uint16_t* c = reinterpret_cast<uint16_t*>(tile) + k;
+        const float2 f = e4m3_values(*c);
+        *c = static_cast<uint16_t>(e4m3_pair(f.x * ratio, f.y * ratio));
+      }
+    }
+    __syncthreads();  // everyone has read the old scale
+    if (tid == 0) *sp = now;
+    for (int k = tid; k < n * VR; k += kAppendThreads) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + (k / VR) * a.token_stride[which]) + k % VR);
+      float f[E];
+      unpack16<Elt>(q, f);
+      uint8_t* c = tile + (off + k / VR) * D + (k % VR) * E;
+      uint32_t w[E / 4];
+#pragma unroll
+      for (int e = 0; e < E / 4; ++e)
+        w[e] = e4m3_pair(f[4 * e] * inv, f[4 * e + 1] * inv) | (e4m3_pair(f[4 * e + 2] * inv, f[4 * e + 3] * inv) << 16);
+      if (E == 8)
+        *reinterpret_cast<uint2*>(c) = make_uint2(w[0], w[E / 4 - 1]);
+      else
+        *reinterpret_cast<uint32_t*>(c) = w[0];
+    }
+    i += n;
+  }
+}
+
+}  // namespace specdec

@@ -1,0 +1,268 @@
+// step_api.cu — the C ABI of the operators around the verify step: argument
+// checks, launch shapes and launches.  The declarations, with the meaning of
+// every argument, are in include/specdec_step.h.
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "specdec_step.h"
+
+#include "attention_kernel.cuh"
+#include "kv_kernels.cuh"
+#include "logits_kernel.cuh"
+
+namespace specdec {
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+specdec_status_t launched() { return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA; }
+
+bool block_size_ok(int32_t bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128; }
+
+// The cache's shape: INVALID_ARG, UNSUPPORTED or OK.
+specdec_status_t check_cache(int32_t num_blocks, int32_t block_size, int32_t H, int32_t D) {
+  if (num_blocks <= 0 || block_size <= 0 || H <= 0 || D <= 0) return SPECDEC_ERR_INVALID_ARG;
+  if (!block_size_ok(block_size) || (D != 64 && D != 128)) return SPECDEC_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_blocks) * block_size > INT32_MAX || H > 65535) return SPECDEC_ERR_UNSUPPORTED;
+  return SPECDEC_OK;
+}
+
+template <typename Elt, bool kVec>
+cudaError_t launch_logits(const LogitArgs& a, cudaStream_t st) {
+  const int smem = a.share * 4;
+  static bool ready[64] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev]) {
+    e = cudaFuncSetAttribute(process_logits_kernel<Elt, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             SPECDEC_MAX_VOCAB / kLogitCtas * 4);
+    if (e != cudaSuccess) return e;
+    ready[dev] = true;
+  }
+  process_logits_kernel<Elt, kVec>
+      <<<dim3(static_cast<unsigned>(a.B) * kLogitCtas, static_cast<unsigned>(a.row_step)), kLogitThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace specdec
+
+using namespace specdec;
+
+extern "C" specdec_status_t spec_process_logits(
+    const void* logits, void* out, specdec_dtype_t dtype, int32_t B, int32_t n_max, int32_t V, const int32_t* history,
+    int32_t history_stride, const int32_t* prompt_len, const int32_t* history_len, const int32_t* draft_tokens,
+    const int32_t* draft_len, const float* repetition, const float* presence, const float* frequency,
+    const int32_t* bias_offsets, const int32_t* bias_ids, const float* bias_values, int32_t num_bias,
+    const uint32_t* mask, int32_t mask_count, const int32_t* mask_rows, uint32_t* error_word, void* stream) {
+  if (dtype != SPECDEC_F32 && dtype != SPECDEC_BF16) return SPECDEC_ERR_INVALID_ARG;
+  if (B < 0 || n_max < 0 || V <= 0 || history_stride < 0 || num_bias < 0 || mask_count < 0) return SPECDEC_ERR_INVALID_ARG;
+  if (V > SPECDEC_MAX_VOCAB || n_max > SPECDEC_MAX_DRAFT || B > SPECDEC_MAX_BATCH) return SPECDEC_ERR_UNSUPPORTED;
+  if (B == 0) return SPECDEC_OK;
+  if (logits == nullptr || out == nullptr) return SPECDEC_ERR_INVALID_ARG;
+  const uintptr_t elt = dtype == SPECDEC_F32 ? 4 : 2;
+  if (!aligned(logits, elt) || !aligned(out, elt)) return SPECDEC_ERR_INVALID_ARG;
+  if (history_stride > 0 && (history == nullptr || prompt_len == nullptr || history_len == nullptr))
+    return SPECDEC_ERR_INVALID_ARG;
+  if (n_max > 0 && draft_tokens == nullptr) return SPECDEC_ERR_INVALID_ARG;
+  if (bias_offsets != nullptr && num_bias > 0 && (bias_ids == nullptr || bias_values == nullptr))
+    return SPECDEC_ERR_INVALID_ARG;
+  if ((mask == nullptr || mask_count == 0) != (mask_rows == nullptr)) return SPECDEC_ERR_INVALID_ARG;
+
+  LogitArgs a;
+  memset(&a, 0, sizeof a);
+  a.logits = logits;
+  a.out = out;
+  a.B = B;
+  a.n_max = n_max;
+  a.V = V;
+  a.history_stride = history_stride;
+  a.history = history;
+  a.prompt_len = prompt_len;
+  a.history_len = history_len;
+  a.draft_tokens = draft_tokens;
+  a.draft_len = draft_len;
+  a.repetition = repetition;
+  a.presence = presence;
+  a.frequency = frequency;
+  a.bias_offsets = num_bias > 0 ? bias_offsets : nullptr;
+  a.bias_ids = bias_ids;
+  a.bias_values = bias_values;
+  a.num_bias = num_bias;
+  a.mask = mask;
+  a.mask_count = mask_count;
+  a.mask_words = (V + 31) / 32;
+  a.mask_rows = mask_rows;
+  a.err = error_word;
+  a.share = ((V + kLogitCtas - 1) / kLogitCtas + 31) / 32 * 32;
+  a.row_step = 1;
+  const bool vec = static_cast<uintptr_t>(V) * elt % 16 == 0 && aligned(logits, 16) && aligned(out, 16);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (dtype == SPECDEC_F32)
+    e = vec ? launch_logits<float, true>(a, st) : launch_logits<float, false>(a, st);
+  else
+    e = vec ? launch_logits<__nv_bfloat16, true>(a, st) : launch_logits<__nv_bfloat16, false>(a, st);
+  return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+}
+
+// Capacity up to which one CTA writes the slots too.
+constexpr int32_t kFillInPlan = 8192;
+
+extern "C" specdec_status_t kv_block_step(int32_t B, int32_t block_size, int32_t max_blocks, int32_t num_blocks,
+                                          const int32_t* kv_len, const int32_t* accepted_len,
+                                          const int32_t* new_tokens, const int32_t* held, int32_t* block_table,
+                                          int32_t* free_ring, const int32_t* ring_state, int32_t* kv_len_out,
+                                          int32_t* held_out, int32_t* ring_state_out, int32_t* cu_tokens,
+                                          int32_t* cu_blocks, int32_t* slot_map, int32_t* positions,
+                                          int32_t capacity, uint32_t* error_word, void* stream) {
+  if (B < 0 || block_size <= 0 || max_blocks <= 0 || num_blocks <= 0 || capacity < 0) return SPECDEC_ERR_INVALID_ARG;
+  if (!block_size_ok(block_size) || B > SPECDEC_MAX_BATCH) return SPECDEC_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_blocks) * block_size > INT32_MAX ||
+      static_cast<int64_t>(max_blocks) * block_size > INT32_MAX)
+    return SPECDEC_ERR_UNSUPPORTED;
+  if (B == 0) return SPECDEC_OK;
+  if (kv_len == nullptr || new_tokens == nullptr || held == nullptr || block_table == nullptr || free_ring == nullptr ||
+      ring_state == nullptr || kv_len_out == nullptr || held_out == nullptr || ring_state_out == nullptr ||
+      cu_tokens == nullptr || cu_blocks == nullptr)
+    return SPECDEC_ERR_INVALID_ARG;
+  if (capacity > 0 && (slot_map == nullptr || positions == nullptr)) return SPECDEC_ERR_INVALID_ARG;
+  BlockArgs a;
+  memset(&a, 0, sizeof a);
+  a.B = B;
+  a.bs = block_size;
+  a.max_blocks = max_blocks;
+  a.num_blocks = num_blocks;
+  a.capacity = capacity;
+  a.kv_len = kv_len;
+  a.accepted_len = accepted_len;
+  a.new_tokens = new_tokens;
+  a.held = held;
+  a.table = block_table;
+  a.ring = free_ring;
+  a.ring_state = ring_state;
+  a.kv_len_out = kv_len_out;
+  a.held_out = held_out;
+  a.ring_state_out = ring_state_out;
+  a.cu_tokens = cu_tokens;
+  a.cu_blocks = cu_blocks;
+  a.slot_map = slot_map;
+  a.positions = positions;
+  a.err = error_word;
+  a.fill = capacity <= kFillInPlan ? 1 : 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  block_plan_kernel<<<1, kBlockThreads, 0, st>>>(a);
+  if (!a.fill) {
+    if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
+    block_fill_kernel<<<static_cast<unsigned>((capacity + 255) / 256), 256, 0, st>>>(a);
+  }
+  return launched();
+}
+
+extern "C" specdec_status_t kv_append(const void* k, const void* v, specdec_dtype_t dtype, int32_t T, int32_t H,
+                                      int32_t D, int64_t k_token_stride, int64_t k_head_stride,
+                                      int64_t v_token_stride, int64_t v_head_stride, const int32_t* slot_map,
+                                      int32_t num_blocks, int32_t block_size, void* k_cache, void* v_cache,
+                                      float* k_scale, float* v_scale, void* stream) {
+  if (dtype != SPECDEC_F32 && dtype != SPECDEC_BF16) return SPECDEC_ERR_INVALID_ARG;
+  if (T < 0) return SPECDEC_ERR_INVALID_ARG;
+  const specdec_status_t chk = check_cache(num_blocks, block_size, H, D);
+  if (chk != SPECDEC_OK) return chk;
+  if (T == 0) return SPECDEC_OK;
+  if (k == nullptr || v == nullptr || slot_map == nullptr || k_cache == nullptr || v_cache == nullptr ||
+      k_scale == nullptr || v_scale == nullptr)
+    return SPECDEC_ERR_INVALID_ARG;
+  const int64_t elt = dtype == SPECDEC_F32 ? 4 : 2;
+  const int64_t strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
+  for (int64_t s : strides)
+    if (s < 0 || s > (INT64_MAX >> 4) || s * elt % 16 != 0) return SPECDEC_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16)) return SPECDEC_ERR_INVALID_ARG;
+  AppendArgs a;
+  memset(&a, 0, sizeof a);
+  a.x[0] = k;
+  a.x[1] = v;
+  for (int i = 0; i < 2; ++i) {
+    a.token_stride[i] = strides[2 * i] * elt;
+    a.head_stride[i] = strides[2 * i + 1] * elt;
+  }
+  a.cache[0] = static_cast<uint8_t*>(k_cache);
+  a.cache[1] = static_cast<uint8_t*>(v_cache);
+  a.scale[0] = k_scale;
+  a.scale[1] = v_scale;
+  a.slot_map = slot_map;
+  a.T = T;
+  a.H = H;
+  a.bs = block_size;
+  a.num_blocks = num_blocks;
+  // A few thousand CTAs where there are tokens for them.
+  const int64_t w = static_cast<int64_t>(T) * H * 2 / 4096;
+  a.window = static_cast<int32_t>(w < 1 ? 1 : (w > block_size ? block_size : w));
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(T) + a.window - 1) / a.window), static_cast<unsigned>(H), 2);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == SPECDEC_F32) {
+    if (D == 64)
+      append_kernel<float, 64><<<grid, kAppendThreads, 0, st>>>(a);
+    else
+      append_kernel<float, 128><<<grid, kAppendThreads, 0, st>>>(a);
+  } else {
+    if (D == 64)
+      append_kernel<__nv_bfloat16, 64><<<grid, kAppendThreads, 0, st>>>(a);
+    else
+      append_kernel<__nv_bfloat16, 128><<<grid, kAppendThreads, 0, st>>>(a);
+  }
+  return launched();
+}
+
+extern "C" specdec_status_t spec_attention(const void* q, int64_t q_token_stride, int32_t T, int32_t Hq, int32_t H,
+                                           int32_t D, int32_t B, const int32_t* cu_tokens, const int32_t* kv_len,
+                                           const int32_t* block_table, int32_t max_blocks, int32_t num_blocks,
+                                           int32_t block_size, const void* k_cache, const void* v_cache,
+                                           const float* k_scale, const float* v_scale, float scale, void* out,
+                                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (T < 0 || B < 0 || Hq <= 0 || max_blocks <= 0) return SPECDEC_ERR_INVALID_ARG;
+  const specdec_status_t chk = check_cache(num_blocks, block_size, H, D);
+  if (chk != SPECDEC_OK) return chk;
+  if (Hq % H != 0 || !(scale >= 0.f) || scale > 3e38f) return SPECDEC_ERR_INVALID_ARG;
+  if (B > SPECDEC_MAX_BATCH || static_cast<int64_t>(max_blocks) * block_size > INT32_MAX) return SPECDEC_ERR_UNSUPPORTED;
+  if (T == 0 || B == 0) return SPECDEC_OK;
+  if (q == nullptr || cu_tokens == nullptr || kv_len == nullptr || block_table == nullptr || k_cache == nullptr ||
+      v_cache == nullptr || k_scale == nullptr || v_scale == nullptr || out == nullptr)
+    return SPECDEC_ERR_INVALID_ARG;
+  if (q_token_stride < static_cast<int64_t>(Hq) * D || q_token_stride % 8 != 0 || !aligned(q, 16) || !aligned(out, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return SPECDEC_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < SPECDEC_ATTENTION_WORKSPACE_BYTES)
+    return SPECDEC_ERR_WORKSPACE;
+  AttnArgs a;
+  memset(&a, 0, sizeof a);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_stride = q_token_stride;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.T = T;
+  a.Hq = Hq;
+  a.H = H;
+  a.B = B;
+  a.cu_tokens = cu_tokens;
+  a.kv_len = kv_len;
+  a.table = block_table;
+  a.max_blocks = max_blocks;
+  a.num_blocks = num_blocks;
+  a.bs = block_size;
+  a.k_cache = static_cast<const uint8_t*>(k_cache);
+  a.v_cache = static_cast<const uint8_t*>(v_cache);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.scale = scale > 0.f ? scale : (D == 64 ? 0.125f : 0.08838834764831845f);
+  const int64_t rows = static_cast<int64_t>(T) * Hq;
+  if ((rows + 3) / 4 > INT32_MAX) return SPECDEC_ERR_UNSUPPORTED;
+  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (D == 64)
+    attention_simple_kernel<64><<<grid, 128, 0, st>>>(a);
+  else
+    attention_simple_kernel<128><<<grid, 128, 0, st>>>(a);
+  return launched();
+}

@@ -1,10 +1,42 @@
 // attention_kernel.cuh — attention of new tokens over the 8-bit paged cache
 // (spec_attention).
+//
+// For one request and key head, the rows of Q are its new tokens times the
+// query heads of the group.  Positions go in tiles of 128:
+//
+//   S^T [128 positions x rows]  = K [positions x D] Q^T         (K: A operand)
+//   O^T [D x rows]             += V^T [D x positions] P^T       (V: A operand)
+//
+// Positions are the M of the first product and D the M of the second, so that
+// few rows cost little (they are the N), and a thread's values all belong to
+// one position: its scales are two numbers.
+//
+// First product: e4m3 x e4m3 with 32-bit sums.  K goes from HBM to the tensor
+// cores as it lies in the cache.  Q, bf16 scaled by a power of two a row, is
+// the sum of two e4m3 numbers: a value of 8 significant bits is its nearest
+// number of 4 bits plus a remainder of 4 (exact to 2^-18 of the row's largest).
+//
+// Second product: f16 x f16.  An e4m3 V is exact in f16, and one group of
+// warps turns V's tiles over while the softmax is at work; P in f16 has 11
+// bits down to 2^-20 of its reference and 2^-31 of it is lost.  (P as two e4m3
+// numbers needs no such step, but loses what is below 2^-22 of the largest,
+// which a faint tail after one strong position is, and costs twice the
+// arithmetic a probability.)
+//
+// The reference of a row is its largest score when it was last looked for: in
+// the first tile, and whenever a later score lies more than 2^9 above it.  So
+// O stays in tensor memory, and most tiles need no search for a maximum.
+//
+// The tiles of all requests, heads and row groups form one list that is cut
+// into equal parts, one for each CTA; what a cut separates is joined by the
+// CTA that finishes last, in the order of the parts.
 #pragma once
 #include <cuda_bf16.h>
 #include <stdint.h>
 
 #include "kv_kernels.cuh"
+#include "ptx.cuh"
+#include "tcgen05.cuh"
 
 namespace specdec {
 
@@ -17,62 +49,815 @@ struct AttnArgs {
   const int32_t* kv_len;
   const int32_t* table;
   int32_t max_blocks, num_blocks, bs;
-  const uint8_t* k_cache;
-  const uint8_t* v_cache;
   const float* k_scale;
   const float* v_scale;
-  float scale;
+  float scale_log2e;
+  uint32_t* err;
+  uint32_t* counters;  // one for each CTA, zero between calls
+  float* partial;      // two records for each CTA
+  int32_t ring;        // tiles of K, and of V, in shared memory
+  int32_t rows;        // most rows of a tile, a multiple of 16
 };
 
-// Simple form: a warp per query row, one position at a time.
+constexpr int kTile = 128;      // positions of a tile
+constexpr int kAttnRows = 64;   // most rows of a tile
+// Warps: 0-3 and 4-7 softmax of half of the rows each, 8-11 V to f16, 12-15 Q
+// and O, 16 copies, 17 products.
+constexpr int kAttnThreads = 576;
+constexpr int kScaleRing = 8;
+constexpr int kMaxRing = 8;     // tiles of K, and of V, in shared memory
+constexpr int kMaxPages = 8;    // blocks of a tile
+constexpr uint32_t kTmemCols = 256;  // S twice, O twice
+constexpr int kPartialFloats = kAttnRows * 128 + 2 * kAttnRows;
+// P = 2^kPScale at the reference score; a score may pass it by 2^kSlack
+// before P would leave f16.
+constexpr float kPScale = 64.f;
+constexpr float kSlack = 9.f;
+#ifndef SPECDEC_WAIT_BUDGET_CYCLES
+#define SPECDEC_WAIT_BUDGET_CYCLES 4000000000LL
+#endif
+
+// Part of a (request, head, row group) that one CTA works on.
+struct Segment {
+  int b, h, row0, rows;       // rows of this group
+  int q0, kv, len;            // first token, positions before it, positions of the group
+  int tile0, tile1, tiles;    // tiles of this part, and of the whole
+  long long first;            // unit of the whole's first tile
+};
+
+// Goes through the segments of units [u, end).
+struct Walker {
+  const AttnArgs& a;
+  long long u, end, ub;  // ub: first unit of request b
+  int b, G, q0, q, kv;
+  long long per_head;
+
+  __device__ Walker(const AttnArgs& args, long long u0, long long u1, int b0, long long ub0)
+      : a(args), u(u0), end(u1), ub(ub0), b(b0), G(args.Hq / args.H) {
+    if (u < end) load();
+  }
+  // positions of the row group that ends before row `last`
+  static __device__ int length(const AttnArgs& a, int kv, int G, int row_end) {
+    const long long n = static_cast<long long>(kv) + (row_end - 1) / G + 1;
+    const long long cap = static_cast<long long>(a.max_blocks) * a.bs;
+    return static_cast<int>(n < 0 ? 0 : (n < cap ? n : cap));
+  }
+  static __device__ int tiles_of(int len) { return len <= 0 ? 1 : (len + kTile - 1) / kTile; }
+  static __device__ long long units_per_head(const AttnArgs& a, int kv, int G, int q) {
+    long long n = 0;
+    for (int r = 0; r < q * G; r += a.rows) n += tiles_of(length(a, kv, G, min(q * G, r + a.rows)));
+    return n;
+  }
+  static __device__ void request(const AttnArgs& a, int b, int& q0, int& q, int& kv) {
+    q0 = max(0, min(__ldg(a.cu_tokens + b), a.T));
+    const int q1 = max(0, min(__ldg(a.cu_tokens + b + 1), a.T));
+    q = max(0, q1 - q0);
+    kv = __ldg(a.kv_len + b);
+  }
+  __device__ void load() {
+    request(a, b, q0, q, kv);
+    per_head = units_per_head(a, kv, G, q);
+  }
+  __device__ bool next(Segment& s) {
+    if (u >= end) return false;
+    while (u >= ub + per_head * a.H) {
+      ub += per_head * a.H;
+      ++b;
+      load();
+    }
+    const long long o = u - ub;
+    s.b = b;
+    s.h = static_cast<int>(o / per_head);
+    long long rem = o - s.h * per_head;
+    s.q0 = q0;
+    s.kv = kv;
+    for (s.row0 = 0;; s.row0 += a.rows) {
+      const int row_end = min(q * G, s.row0 + a.rows);
+      s.rows = row_end - s.row0;
+      s.len = length(a, kv, G, row_end);
+      s.tiles = tiles_of(s.len);
+      if (rem < s.tiles) break;
+      rem -= s.tiles;
+    }
+    s.tile0 = static_cast<int>(rem);
+    s.tile1 = static_cast<int>(min(static_cast<long long>(s.tiles), rem + (end - u)));
+    s.first = u - rem;
+    u += s.tile1 - s.tile0;
+    return true;
+  }
+};
+
+struct ScaleEntry {
+  float ks[kMaxPages];   // key scale times the scores' factor
+  float vs[kMaxPages];   // value scale
+  float vmax;            // the tile's largest
+};
+
+struct AttnShared {
+  uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
+  uint64_t s_full[2], s_empty[2], p_full[2], f_full[2], pv_done[2], o_full[2], o_empty[2];
+  uint64_t q_full, q_empty, meta_full[2], l_full[2];
+  uint64_t sc_full[kScaleRing], sc_empty[kScaleRing], done;
+  uint32_t tmem;
+  int32_t b0;
+  long long ub0;
+  long long part[32];
+  alignas(16) float2 col[kAttnRows];  // {row scale, reference} of each row
+  float wmax[2][4][kAttnRows / 2];    // a warp's largest score of each row of its half
+  float qs[2][kAttnRows];
+  int32_t limit[2][kAttnRows];        // last position a row attends to
+  float lsum[2][4][kAttnRows];        // sums of the softmax warps
+  float mrun[2][kAttnRows];
+  float vref[2];
+  int32_t nanpos[2][128];             // first new position whose value is NaN in a dimension
+  ScaleEntry scales[kScaleRing];
+  int32_t last;
+};
+
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// Whether `x` holds for any thread of the barrier.
+__device__ __forceinline__ bool named_any(int id, int threads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x)), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
+// A wait that gives up once; after that the thread goes on without waiting, so
+// that every barrier still gets its arrivals and the CTA ends.
+struct Waiter {
+  bool dead = false;
+  __device__ void operator()(const uint64_t& bar, uint32_t parity) {
+    if (!dead && !ptx::mbar_wait_bounded(ptx::smem_addr(&bar), parity, SPECDEC_WAIT_BUDGET_CYCLES)) dead = true;
+  }
+};
+__device__ __forceinline__ void arrive(uint64_t& bar) { ptx::mbar_arrive(ptx::smem_addr(&bar)); }
+
+// Nearest number of 4 significant bits; the remainder of a number of 8 has 4.
+__device__ __forceinline__ float top4(float x) {
+  return __uint_as_float((__float_as_uint(x) + 0x80000u) & 0xFFF00000u);
+}
+
+// Byte x of row t in a tile of K or V (rows of D bytes) as the copies swizzle it.
 template <int D>
-__global__ void __launch_bounds__(128) attention_simple_kernel(const AttnArgs a) {
-  constexpr int E = D / 32;
+__device__ __forceinline__ int swizzled(int t, int x) {
+  return D == 128 ? t * 128 + (x ^ ((t & 7) << 4)) : t * 64 + (x ^ (((t >> 1) & 3) << 4));
+}
+
+// Sums of 8 values over the warp: lane i gets that of value i >> 2.
+__device__ __forceinline__ float warp_sums8(const float* v) {
   const int lane = threadIdx.x & 31;
-  const long long row = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (row >= static_cast<long long>(a.T) * a.Hq) return;
-  const int t = static_cast<int>(row / a.Hq), hq = static_cast<int>(row % a.Hq);
-  const int total = min(a.cu_tokens[a.B], a.T);
-  if (t >= total || t < a.cu_tokens[0]) return;
-  const int b = owner_of(a.cu_tokens, a.B, t);
-  const long long last = min(static_cast<long long>(a.kv_len[b]) + (t - a.cu_tokens[b]),
-                             static_cast<long long>(a.max_blocks) * a.bs - 1);
-  const int h = hq / (a.Hq / a.H);
-  float q[E], o[E], m = -INFINITY, l = 0.f;
+  float a[4], b[2];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(a.q[t * a.q_stride + hq * D + lane * E + e]) * a.scale;
-    o[e] = 0.f;
-  }
-  for (long long p = 0; p <= last; ++p) {
-    const int block = a.table[static_cast<long long>(b) * a.max_blocks + p / a.bs];
-    const bool there = block >= 0 && block < a.num_blocks;
-    const long long tile = there ? static_cast<long long>(block) * a.H + h : 0;
-    const long long at = (tile * a.bs + p % a.bs) * D + lane * E;
-    const float ks = there ? a.k_scale[tile] : 0.f, vs = there ? a.v_scale[tile] : 0.f;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 f = there ? e4m3_values(*reinterpret_cast<const uint16_t*>(a.k_cache + at + e)) : make_float2(0.f, 0.f);
-      s += q[e] * f.x + q[e + 1] * f.y;
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    s *= ks;
-    const float m2 = fmaxf(m, s);
-    const float f = expf(m - m2), w = expf(s - m2);
-    m = m2;
-    l = l * f + w;
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 x = there ? e4m3_values(*reinterpret_cast<const uint16_t*>(a.v_cache + at + e)) : make_float2(0.f, 0.f);
-      o[e] = o[e] * f + w * (x.x * vs);
-      o[e + 1] = o[e + 1] * f + w * (x.y * vs);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const bool up = lane & 16;
+    a[i] = (up ? v[i + 4] : v[i]) + __shfl_xor_sync(0xFFFFFFFFu, up ? v[i] : v[i + 4], 16);
   }
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    a.out[row * D + lane * E + e] = __float2bfloat16_rn(last >= 0 ? o[e] / l : 0.f);
+  for (int i = 0; i < 2; ++i) {
+    const bool up = lane & 8;
+    b[i] = (up ? a[i + 2] : a[i]) + __shfl_xor_sync(0xFFFFFFFFu, up ? a[i] : a[i + 2], 8);
+  }
+  const bool up = lane & 4;
+  float s = (up ? b[1] : b[0]) + __shfl_xor_sync(0xFFFFFFFFu, up ? b[0] : b[1], 4);
+  s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
+  return s + __shfl_xor_sync(0xFFFFFFFFu, s, 1);
+}
+
+template <int D>
+struct AttnLayout {
+  static constexpr int kTileBytes = kTile * D;       // of K or V
+  static constexpr int kHalfBytes = kTile * D * 2;   // of V in f16
+  static __host__ __device__ int q_bytes(int rows) { return rows * D; }          // of one half
+  static __host__ __device__ int p_bytes(int rows) { return rows * kTile * 2; }  // of one buffer
+  static __host__ __device__ int tiles_at() { return (static_cast<int>(sizeof(AttnShared)) + 1023) / 1024 * 1024; }
+  static __host__ __device__ int bytes(int ring, int rows) {
+    return 1024 + tiles_at() + 2 * ring * kTileBytes + 2 * kHalfBytes + 2 * q_bytes(rows) + 2 * p_bytes(rows);
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+  using L = AttnLayout<D>;
+  extern __shared__ __align__(16) unsigned char raw[];
+  unsigned char* base = raw + ((1024u - (ptx::smem_addr(raw) & 1023u)) & 1023u);
+  AttnShared& sh = *reinterpret_cast<AttnShared*>(base);
+  unsigned char* k_tiles = base + L::tiles_at();
+  unsigned char* v_tiles = k_tiles + a.ring * L::kTileBytes;
+  unsigned char* v_half = v_tiles + a.ring * L::kTileBytes;
+  unsigned char* q_hi = v_half + 2 * L::kHalfBytes;
+  unsigned char* q_lo = q_hi + L::q_bytes(a.rows);
+  unsigned char* p_at = q_lo + L::q_bytes(a.rows);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = a.Hq / a.H;
+
+  if (tid == 0) {
+    auto init = [](uint64_t& bar, uint32_t n) { ptx::mbar_init(ptx::smem_addr(&bar), n); };
+    for (int i = 0; i < a.ring; ++i) {
+      init(sh.k_full[i], 1);
+      init(sh.k_empty[i], 1);
+      init(sh.v_full[i], 1);
+      init(sh.v_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      init(sh.s_full[i], 1);
+      init(sh.s_empty[i], 8);
+      init(sh.p_full[i], 256);
+      init(sh.f_full[i], 128);
+      init(sh.pv_done[i], 1);
+      init(sh.o_full[i], 1);
+      init(sh.o_empty[i], 128);
+      init(sh.meta_full[i], 128);
+      init(sh.l_full[i], 256 + 128);
+    }
+    for (int i = 0; i < kScaleRing; ++i) {
+      init(sh.sc_full[i], 32);
+      init(sh.sc_empty[i], 8);
+    }
+    init(sh.q_full, 128);
+    init(sh.q_empty, 1);
+    init(sh.done, 1);
+    ptx::fence_mbarrier_init();
+    sh.b0 = 0;
+    sh.ub0 = 0;
+  }
+  if (warp == 17) tc::alloc(ptx::smem_addr(&sh.tmem), kTmemCols);
+
+  // Units of all requests, and where this CTA's begin.
+  long long u0, u1, chunk;
+  {
+    const int per = (a.B + kAttnThreads - 1) / kAttnThreads;
+    const int lo = min(a.B, tid * per), hi = min(a.B, lo + per);
+    long long mine = 0;
+    for (int b = lo; b < hi; ++b) {
+      int q0, q, kv;
+      Walker::request(a, b, q0, q, kv);
+      mine += Walker::units_per_head(a, kv, G, q) * a.H;
+    }
+    long long s = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xFFFFFFFFu, s, d);
+      if (lane >= d) s += o;
+    }
+    if (lane == 31) sh.part[warp] = s;
+    __syncthreads();
+    long long before = s - mine, total = 0;
+    for (int w = 0; w < kAttnThreads / 32; ++w) {
+      if (w < warp) before += sh.part[w];
+      total += sh.part[w];
+    }
+    chunk = (total + gridDim.x - 1) / gridDim.x;
+    u0 = min(total, static_cast<long long>(blockIdx.x) * chunk);
+    u1 = min(total, u0 + chunk);
+    if (u0 < u1 && before <= u0 && u0 < before + mine) {  // one thread
+      long long at = before;
+      for (int b = lo; b < hi; ++b) {
+        int q0, q, kv;
+        Walker::request(a, b, q0, q, kv);
+        const long long n = Walker::units_per_head(a, kv, G, q) * a.H;
+        if (u0 < at + n) {
+          sh.b0 = b;
+          sh.ub0 = at;
+          break;
+        }
+        at += n;
+      }
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+  }
+  const uint32_t tmem = sh.tmem;
+  const int b0 = sh.b0;
+  const long long ub0 = sh.ub0;
+  Waiter wait;
+  Segment seg;
+  const int pages_per_tile = kTile / a.bs;
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    // A thread has one position and half of the rows.
+    constexpr int kHalfRows = kAttnRows / 2;
+    const int grp = warp >> 2, t_in = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    float x[kHalfRows], l[kHalfRows];
+    Walker walk(a, u0, u1, b0, ub0);
+    int k = 0;  // tiles so far
+    for (int n_seg = 0; walk.next(seg); ++n_seg) {
+      const int par = n_seg & 1;
+      const int eights = (seg.rows + 15) / 16;  // groups of 8 rows of this half
+      const int r0 = grp * eights * 8;
+      float vref = 1.f;
+#pragma unroll
+      for (int r = 0; r < kHalfRows; ++r) l[r] = 0.f;
+      wait(sh.meta_full[par], (n_seg >> 1) & 1);
+      named_barrier(1 + grp, 128);  // the last segment's rows are no longer read
+      if (t_in < eights * 8) sh.col[r0 + t_in] = make_float2(sh.qs[par][r0 + t_in], 0.f);
+      named_barrier(1 + grp, 128);
+      const int all_see = seg.kv + seg.row0 / G;  // last position that all rows attend to
+      const uint32_t o_at = tmem + lanes + (2 + par) * kAttnRows + r0;
+      for (int t = seg.tile0; t < seg.tile1; ++t, ++k) {
+        const int pos0 = t * kTile, pos = pos0 + t_in;
+        const bool masked = pos0 + kTile - 1 > all_see || pos0 + kTile > seg.len;
+        const bool first = t == seg.tile0;
+        const ScaleEntry& sc = sh.scales[k % kScaleRing];
+        wait(sh.sc_full[k % kScaleRing], (k / kScaleRing) & 1);
+        const float ks = sc.ks[t_in / a.bs], vs = sc.vs[t_in / a.bs], vmax = sc.vmax;
+        __syncwarp();
+        if (lane == 0) arrive(sh.sc_empty[k % kScaleRing]);
+        const bool raise_v = first || vmax > 4.f * vref;
+        const float vref_was = vref;
+        if (raise_v) vref = vmax > 0.f ? vmax : 0x1p-100f;
+        const float ratio = vs / vref, vr = ratio * kPScale;
+        wait(sh.s_full[k & 1], (k >> 1) & 1);
+        tc::fence_after();
+        // scores over the rows' references
+        const uint32_t s_at = tmem + lanes + (k & 1) * kAttnRows + r0;
+#pragma unroll
+        for (int c = 0; c < kHalfRows / 8; ++c)
+          if (c < eights) tc::ld8(s_at + c * 8, x + c * 8);
+        tc::wait_ld();
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kHalfRows / 8; ++c) {
+          if (c >= eights) break;
+          tc::ready(x + c * 8);
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const int r = c * 8 + e;
+            const float4 w = *reinterpret_cast<const float4*>(&sh.col[r0 + r]);
+            x[r] = fmaf(x[r] * ks, w.x, -w.y);
+            x[r + 1] = fmaf(x[r + 1] * ks, w.z, -w.w);
+          }
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (pos > sh.limit[par][r0 + c * 8 + e]) x[c * 8 + e] = -INFINITY;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, x[c * 8 + e]);
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(sh.s_empty[k & 1]);
+        // does P stay within f16 (and the sum within 32 bits)?
+        const bool over = top > fminf(kSlack - __log2f(ratio), 60.f);
+        if (named_any(1 + grp, 128, over) || raise_v) {
+          // New references: the rows' largest scores so far.
+#pragma unroll
+          for (int c = 0; c < kHalfRows / 8; ++c) {
+            if (c >= eights) break;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float m = tc::warp_max(x[c * 8 + e]);
+              if (lane == 0) sh.wmax[grp][warp & 3][c * 8 + e] = m;
+            }
+          }
+          if (!first) wait(sh.pv_done[(k - 1) & 1], ((k - 1) >> 1) & 1);  // O rests
+          tc::fence_after();
+          named_barrier(1 + grp, 128);
+          const float v_ratio = first ? 1.f : vref_was / vref;
+#pragma unroll
+          for (int c = 0; c < kHalfRows / 8; ++c) {
+            if (c >= eights) break;
+            float o[8];
+            if (!first) {
+              tc::ld8(o_at + c * 8, o);
+              tc::wait_ld();
+              tc::ready(o);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int r = c * 8 + e;
+              float m = fmaxf(fmaxf(sh.wmax[grp][0][r], sh.wmax[grp][1][r]), fmaxf(sh.wmax[grp][2][r], sh.wmax[grp][3][r]));
+              if (first ? !(m > -INFINITY) : !(m > 0.f)) m = 0.f;  // nothing above the reference
+              x[r] -= m;
+              if (!first) {
+                const float f = tc::ex2(-m);
+                l[r] *= f;
+                o[e] *= f * v_ratio;
+              }
+            }
+            if (!first) tc::st8(o_at + c * 8, o);
+          }
+          tc::wait_st();
+          tc::fence_before();
+          if (t_in < eights * 8) {
+            float m = fmaxf(fmaxf(sh.wmax[grp][0][t_in], sh.wmax[grp][1][t_in]), fmaxf(sh.wmax[grp][2][t_in], sh.wmax[grp][3][t_in]));
+            if (first ? !(m > -INFINITY) : !(m > 0.f)) m = 0.f;
+            sh.col[r0 + t_in].y += m;
+          }
+          named_barrier(1 + grp, 128);
+        }
+        if (k >= 2) wait(sh.pv_done[k & 1], ((k >> 1) - 1) & 1);
+        // probabilities
+        unsigned char* p = p_at + (k & 1) * L::p_bytes(a.rows) + (r0 / 8) * (16 * kTile) + t_in * 16;
+#pragma unroll
+        for (int c = 0; c < kHalfRows / 8; ++c) {
+          if (c >= eights) break;
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const int r = c * 8 + e;
+            const float p0 = tc::ex2(x[r]), p1 = tc::ex2(x[r + 1]);
+            l[r] += p0;
+            l[r + 1] += p1;
+            w[e >> 1] = tc::f16x2(p0 * vr, p1 * vr);
+          }
+          *reinterpret_cast<uint4*>(p + c * (16 * kTile)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        tc::fence_smem();
+        arrive(sh.p_full[k & 1]);
+      }
+      // sums and references for the output warps
+#pragma unroll
+      for (int c = 0; c < kHalfRows / 8; ++c) {
+        if (c >= eights) break;
+        const float s = warp_sums8(l + c * 8);
+        if ((lane & 3) == 0) sh.lsum[par][warp & 3][r0 + c * 8 + (lane >> 2)] = s;
+      }
+      if (t_in < eights * 8) sh.mrun[par][r0 + t_in] = sh.col[r0 + t_in].y;
+      if (tid == 0) sh.vref[par] = vref / kPScale;
+      arrive(sh.l_full[par]);
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------ V to f16
+    // A thread has one position.  Values past the last position are no numbers
+    // of the request's: zeros.  New positions are not seen by all rows: their
+    // NaN leave the product, where 0 times NaN would spoil rows that do not
+    // see them, and are noted for the output.
+    const int t_in = tid - 256;
+    Walker walk(a, u0, u1, b0, ub0);
+    int k = 0, slot = 0, round = 0;
+    for (int n_seg = 0; walk.next(seg); ++n_seg) {
+      const int par = n_seg & 1;
+      wait(sh.meta_full[par], (n_seg >> 1) & 1);  // nanpos is set
+      for (int t = seg.tile0; t < seg.tile1; ++t, ++k) {
+        const int pos0 = t * kTile, pos = pos0 + t_in;
+        const unsigned char* from = v_tiles + slot * L::kTileBytes;
+        unsigned char* to = v_half + (k & 1) * L::kHalfBytes;
+        wait(sh.v_full[slot], round & 1);
+        uint4 c[D / 16];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) c[i] = *reinterpret_cast<const uint4*>(from + swizzled<D>(t_in, i * 16));
+        __syncwarp();
+        if (lane == 0) arrive(sh.v_empty[slot]);
+        if (++slot == a.ring) slot = 0, ++round;
+        if (pos0 + kTile > min(seg.kv, seg.len)) {
+          if (pos >= seg.len) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) c[i] = make_uint4(0, 0, 0, 0);
+          } else if (pos >= seg.kv) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                for (int e = 0; e < 4; ++e)
+                  if (((w[j] >> (8 * e)) & 0x7F) == 0x7F) {
+                    w[j] &= ~(0xFFu << (8 * e));
+                    atomicMin(&sh.nanpos[par][i * 16 + j * 4 + e], pos);
+                  }
+              c[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        if (k >= 2) wait(sh.pv_done[k & 1], ((k >> 1) - 1) & 1);
+        // rows of 64 values (128 bytes), swizzled; the two halves of D one after the other
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 q = c[i >> 1];
+          const uint32_t lo = (i & 1) ? q.z : q.x, hi = (i & 1) ? q.w : q.y;
+          const uint4 h = make_uint4(tc::f16x2_of_e4m3x2(lo & 0xFFFFu), tc::f16x2_of_e4m3x2(lo >> 16),
+                                     tc::f16x2_of_e4m3x2(hi & 0xFFFFu), tc::f16x2_of_e4m3x2(hi >> 16));
+          *reinterpret_cast<uint4*>(to + (i >> 3) * (kTile * 128) + t_in * 128 + (((i & 7) ^ (t_in & 7)) << 4)) = h;
+        }
+        tc::fence_smem();
+        arrive(sh.f_full[k & 1]);
+      }
+      arrive(sh.l_full[par]);
+    }
+  } else if (warp < 16) {
+    // ------------------------------------------------------------- Q and O
+    const int ot = tid - 384, ow = ot >> 5;
+    const int d = D == 128 ? ot : 16 * ow + (lane & 15);
+    const bool owns = D == 128 || lane < 16;
+    constexpr int kVec = D / 16;  // 16-byte loads of half a row
+    uint4 qv[kVec];
+    const int qr = ot >> 1, half = ot & 1;  // two threads a row of Q
+    auto load_q = [&](const Segment& s) {
+      if (qr < s.rows) {
+        const int row = s.row0 + qr;
+        const uint4* p = reinterpret_cast<const uint4*>(a.q + (s.q0 + row / G) * a.q_stride + (s.h * G + row % G) * D +
+                                                        half * (D / 2));
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) qv[i] = __ldg(p + i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) qv[i] = make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto store_q = [&](const Segment& s, int par) {
+      if (qr < (s.rows + 15) / 16 * 16) {
+        float amax = 0.f;
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          float f[8];
+          unpack16<__nv_bfloat16>(qv[i], f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            bad |= !isfinite(f[e]);
+            amax = fmaxf(amax, fabsf(f[e]));
+          }
+        }
+        const uint32_t pair = 3u << (lane & 30);
+        amax = fmaxf(amax, __shfl_xor_sync(pair, amax, 1));
+        bad = __shfl_xor_sync(pair, static_cast<int>(bad), 1) || bad;
+        const float sc = pow2_scale(amax), inv = bad ? 0.f : pow2_inverse(sc);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          float f[8];
+          uint32_t hw[2] = {0, 0}, lw[2] = {0, 0};
+          if (!bad) {
+            unpack16<__nv_bfloat16>(qv[i], f);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const float u = f[e] * inv, v = f[e + 1] * inv;
+              const float uh = top4(u), vh = top4(v);
+              hw[e >> 2] |= tc::e4m3x2(uh, vh) << (8 * (e & 2));
+              lw[e >> 2] |= tc::e4m3x2(u - uh, v - vh) << (8 * (e & 2));
+            }
+          }
+          // 8 rows x 16 bytes lie together, then the rows' next 16 bytes
+          const int at_x = half * (D / 2) + i * 8;
+          const int at = (qr >> 3) * (8 * D) + (at_x >> 4) * 128 + (qr & 7) * 16 + (at_x & 15);
+          *reinterpret_cast<uint2*>(q_hi + at) = make_uint2(hw[0], hw[1]);
+          *reinterpret_cast<uint2*>(q_lo + at) = make_uint2(lw[0], lw[1]);
+        }
+        if (half == 0) {
+          sh.qs[par][qr] = bad ? __uint_as_float(0x7FFFFFFFu) : (sc > 0.f ? sc : 1.f);
+          sh.limit[par][qr] = qr < s.rows ? min(s.kv + (s.row0 + qr) / G, s.len - 1) : -1;
+        }
+      }
+      sh.nanpos[par][ot] = 0x7FFFFFFF;
+      tc::fence_smem();
+      arrive(sh.q_full);
+      arrive(sh.meta_full[par]);
+    };
+    Walker walk(a, u0, u1, b0, ub0);
+    Segment nxt;
+    bool more = walk.next(nxt);
+    if (more) {
+      load_q(nxt);
+      store_q(nxt, 0);
+    }
+    for (int n_seg = 0; more; ++n_seg) {
+      const int par = n_seg & 1;
+      seg = nxt;
+      more = walk.next(nxt);
+      if (more) {
+        load_q(nxt);
+        wait(sh.q_empty, n_seg & 1);
+        store_q(nxt, par ^ 1);
+      }
+      wait(sh.l_full[par], (n_seg >> 1) & 1);
+      wait(sh.o_full[par], (n_seg >> 1) & 1);
+      tc::fence_after();
+      const int nan_at = sh.nanpos[par][d];
+      const float vref = sh.vref[par];
+      const bool whole = seg.tile0 == 0 && seg.tile1 == seg.tiles;
+      const int slot = static_cast<int>(blockIdx.x) * 2 + (n_seg == 0 ? 0 : 1);
+      float* rec = a.partial + static_cast<long long>(slot) * kPartialFloats;
+      const uint32_t o_at = tmem + (static_cast<uint32_t>(ow * 32) << 16) + (2 + par) * kAttnRows;
+      int tok = seg.row0 / G, g = seg.row0 % G;  // of row r
+      for (int c = 0; c * 8 < seg.rows; ++c) {
+        float o[8];
+        tc::ld8(o_at + c * 8, o);
+        tc::wait_ld();
+        tc::ready(o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int r = c * 8 + e;
+          if (r >= seg.rows) break;
+          float v = o[e] * vref;
+          if (nan_at <= seg.kv + tok) v = __uint_as_float(0x7FFFFFFFu);
+          const float sum = (sh.lsum[par][0][r] + sh.lsum[par][1][r]) + (sh.lsum[par][2][r] + sh.lsum[par][3][r]);
+          if (whole) {
+            if (owns)
+              a.out[(static_cast<long long>(seg.q0 + tok) * a.Hq + seg.h * G + g) * D + d] =
+                  __float2bfloat16_rn(sum == 0.f ? 0.f : v / sum);
+          } else {
+            if (owns) rec[r * D + d] = v;
+            if (ot == 0) {
+              rec[kAttnRows * 128 + r] = sh.mrun[par][r];
+              rec[kAttnRows * 128 + kAttnRows + r] = sum;
+            }
+          }
+          if (++g == G) g = 0, ++tok;
+        }
+      }
+      tc::fence_before();
+      arrive(sh.o_empty[par]);
+      if (!whole) {
+        // the last of the item's CTAs joins the parts
+        const long long c0 = seg.first / chunk, c1 = (seg.first + seg.tiles - 1) / chunk;
+        __threadfence();
+        named_barrier(3, 128);
+        if (ot == 0) sh.last = ptx::atom_add_acq_rel(a.counters + c0, 1u) == static_cast<uint32_t>(c1 - c0);
+        named_barrier(3, 128);
+        if (sh.last) {
+          __threadfence();
+          const int pieces = static_cast<int>(c1 - c0) + 1;
+          const int first_slot = static_cast<int>(c0) * 2 + (seg.first % chunk == 0 ? 0 : 1);
+          auto record = [&](int p) {
+            return a.partial + static_cast<long long>(p == 0 ? first_slot : (c0 + p) * 2) * kPartialFloats;
+          };
+          for (int r = ow; r < seg.rows; r += 4) {
+            const int row = seg.row0 + r;
+            // a piece whose sum is 0 has nothing, whatever its reference
+            float M = -INFINITY;
+            for (int p = lane; p < pieces; p += 32) {
+              const float* q = record(p) + kAttnRows * 128;
+              if (__ldcg(q + kAttnRows + r) != 0.f) M = fmaxf(M, __ldcg(q + r));
+            }
+            M = tc::warp_max(M);
+            float sum = 0.f, acc[D / 32];
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+#pragma unroll 4
+            for (int p = 0; p < pieces; ++p) {
+              const float* q = record(p);
+              const float n = __ldcg(q + kAttnRows * 128 + kAttnRows + r);
+              const float w = n != 0.f ? tc::ex2(__ldcg(q + kAttnRows * 128 + r) - M) : 0.f;
+              sum += w * n;
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i) acc[i] += w * __ldcg(q + r * D + i * 32 + lane);
+            }
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+              a.out[(static_cast<long long>(seg.q0 + row / G) * a.Hq + seg.h * G + row % G) * D + i * 32 + lane] =
+                  __float2bfloat16_rn(sum == 0.f ? 0.f : acc[i] / sum);
+          }
+          if (ot == 0) ptx::st_relaxed_u32(a.counters + c0, 0u);
+        }
+        named_barrier(3, 128);
+      }
+    }
+  } else if (warp == 16) {
+    // ------------------------------------------------------------- copies
+    // Block ids are loaded two tiles ahead and their scales one tile ahead.
+    struct Ahead {
+      int h, pages, id;
+      float ks, vs;
+      bool there;
+    } t0, t1, t2;
+    Walker walk(a, u0, u1, b0, ub0);
+    int tile = 0, tile_end = 0;
+    auto load_ids = [&](Ahead& x) {
+      x.there = false;
+      if (tile >= tile_end) {
+        if (!walk.next(seg)) return;
+        tile = seg.tile0;
+        tile_end = seg.tile1;
+      }
+      x.there = true;
+      x.h = seg.h;
+      const int page0 = tile * pages_per_tile;
+      x.pages = max(0, min(pages_per_tile, (seg.len + a.bs - 1) / a.bs - page0));
+      x.id = -1;
+      if (lane < x.pages) x.id = __ldg(a.table + static_cast<long long>(seg.b) * a.max_blocks + page0 + lane);
+      ++tile;
+    };
+    auto load_scales = [&](Ahead& x) {
+      x.ks = x.vs = 0.f;
+      if (x.there && x.id >= 0 && x.id < a.num_blocks) {
+        x.ks = __ldg(a.k_scale + static_cast<long long>(x.id) * a.H + x.h);
+        x.vs = __ldg(a.v_scale + static_cast<long long>(x.id) * a.H + x.h);
+      }
+    };
+    if (lane == 0) {
+      tc::prefetch_map(&k_map);
+      tc::prefetch_map(&v_map);
+    }
+    load_ids(t0);
+    load_scales(t0);
+    load_ids(t1);
+    int slot = 0, round = 0;
+    for (int k = 0; t0.there; ++k) {
+      load_scales(t1);
+      load_ids(t2);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        if (round > 0) wait(kv ? sh.v_empty[slot] : sh.k_empty[slot], (round - 1) & 1);
+        const uint32_t bar = ptx::smem_addr(kv ? &sh.v_full[slot] : &sh.k_full[slot]);
+        if (lane == 0) ptx::mbar_arrive_expect_tx(bar, t0.pages * a.bs * D);
+        __syncwarp();
+        if (lane < t0.pages)
+          tc::load_4d(ptx::smem_addr((kv ? v_tiles : k_tiles) + slot * L::kTileBytes + lane * a.bs * D), kv ? &v_map : &k_map,
+                      0, 0, t0.h, t0.id, bar);
+      }
+      if (++slot == a.ring) slot = 0, ++round;
+      const int sr = k % kScaleRing;
+      if (k >= kScaleRing) wait(sh.sc_empty[sr], (k / kScaleRing - 1) & 1);
+      const float vmax = tc::warp_max(t0.vs);
+      if (lane < kMaxPages) {
+        sh.scales[sr].ks[lane] = t0.ks * a.scale_log2e;
+        sh.scales[sr].vs[lane] = t0.vs;
+      }
+      if (lane == 0) sh.scales[sr].vmax = vmax;
+      arrive(sh.sc_full[sr]);
+      t0 = t1;
+      t1 = t2;
+    }
+    // no copy is in flight when the CTA ends: every slot used has been filled
+    Waiter drain;
+    const int used = round > 0 ? a.ring : slot;
+    for (int i = 0; i < used; ++i) {
+      drain(sh.k_full[i], (i < slot ? round : round - 1) & 1);
+      drain(sh.v_full[i], (i < slot ? round : round - 1) & 1);
+    }
+    wait.dead |= drain.dead;
+  } else if (lane == 0) {
+    // ------------------------------------------------------------ products
+    // Scores go one tile ahead, into the next segment too where its Q is there.
+    const uint64_t swz = D == 128 ? tc::kSwizzle128 : tc::kSwizzle64;
+    Walker walk(a, u0, u1, b0, ub0), ahead(a, u0, u1, b0, ub0);
+    Segment s_seg;
+    int s_k = 0, s_tile = 0, s_end = 0, s_n = -1, slot = 0, round = 0;  // next tile of scores
+    int k = 0;
+    for (int n_seg = 0; walk.next(seg); ++n_seg) {
+      const int par = n_seg & 1;
+      const int n = (seg.rows + 15) / 16 * 16;
+      const uint32_t io = tc::instr(D, n, true, true);
+      for (int t = seg.tile0; t < seg.tile1; ++t, ++k) {
+        while (s_k <= k + 1) {
+          if (s_tile >= s_end) {
+            if (s_end < 0 || !ahead.next(s_seg)) {
+              s_end = -1;
+              break;
+            }
+            s_tile = s_seg.tile0;
+            s_end = s_seg.tile1;
+            ++s_n;
+          }
+          if (s_tile == s_seg.tile0) {  // a new Q
+            if (s_k <= k)
+              wait(sh.q_full, s_n & 1);
+            else if (!ptx::mbar_test_wait(ptx::smem_addr(&sh.q_full), s_n & 1))
+              break;
+          }
+          wait(sh.k_full[slot], round & 1);
+          if (s_k >= 2) wait(sh.s_empty[s_k & 1], ((s_k >> 1) - 1) & 1);
+          tc::fence_after();
+          const uint32_t is = tc::instr(kTile, (s_seg.rows + 15) / 16 * 16, false, false);
+          const uint64_t kd = tc::smem_desc(ptx::smem_addr(k_tiles + slot * L::kTileBytes), 16, 8 * D, swz);
+          const uint32_t dst = tmem + (s_k & 1) * kAttnRows;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint64_t qd = tc::smem_desc(ptx::smem_addr(h ? q_lo : q_hi), 128, 8 * D, tc::kSwizzleNone);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) tc::mma_e4m3(dst, kd + i * 2, qd + i * 16, is, h > 0 || i > 0);
+          }
+          tc::commit(ptx::smem_addr(&sh.k_empty[slot]));
+          tc::commit(ptx::smem_addr(&sh.s_full[s_k & 1]));
+          if (++slot == a.ring) slot = 0, ++round;
+          ++s_k;
+          if (++s_tile == s_end) tc::commit(ptx::smem_addr(&sh.q_empty));
+        }
+        if (t == seg.tile0 && n_seg >= 2) wait(sh.o_empty[par], ((n_seg >> 1) - 1) & 1);
+        wait(sh.f_full[k & 1], (k >> 1) & 1);
+        wait(sh.p_full[k & 1], (k >> 1) & 1);
+        tc::fence_after();
+        const uint64_t vd = tc::smem_desc(ptx::smem_addr(v_half + (k & 1) * L::kHalfBytes), kTile * 128, 1024, tc::kSwizzle128);
+        const uint64_t pd = tc::smem_desc(ptx::smem_addr(p_at + (k & 1) * L::p_bytes(a.rows)), 128, 16 * kTile, tc::kSwizzleNone);
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i)
+          tc::mma_f16(tmem + (2 + par) * kAttnRows, vd + i * 128, pd + i * 16, io, t > seg.tile0 || i > 0);
+        tc::commit(ptx::smem_addr(&sh.pv_done[k & 1]));
+      }
+      tc::commit(ptx::smem_addr(&sh.o_full[par]));
+    }
+    // all products are done before the tensor memory goes back
+    Waiter drain;
+    tc::commit(ptx::smem_addr(&sh.done));
+    drain(sh.done, 0);
+    wait.dead |= drain.dead;
+  }
+  __syncwarp();
+  if (wait.dead) atomicOr(a.err, SPECDEC_DEV_ERR_TIMEOUT);
+  __syncthreads();
+  if (warp == 17) tc::dealloc(tmem, kTmemCols);
 }
 
 }  // namespace specdec

@@ -47,6 +47,65 @@ cudaError_t launch_logits(const LogitArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+// Map of a cache [num_blocks, H, bs, D]: a box is one head of one block, its
+// rows swizzled as the matrix descriptors read them.
+cudaError_t cache_map(CUtensorMap* map, const void* cache, int D, int bs, int H, int num_blocks) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static Encode encode = nullptr;
+  if (encode == nullptr) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess || fn == nullptr) return cudaErrorNotSupported;
+    encode = reinterpret_cast<Encode>(fn);
+  }
+  const cuuint64_t row = static_cast<cuuint64_t>(D);
+  const cuuint64_t dims[4] = {row, static_cast<cuuint64_t>(bs), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(num_blocks)};
+  const cuuint64_t strides[3] = {row, row * bs, row * bs * H};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(bs), 1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(cache), dims, strides, box, one,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+constexpr size_t kPartialAt = 64 * 1024;  // of the workspace; the counters are before it
+constexpr int kAttnMaxCtas = 1000;        // two records each fit the workspace
+static_assert(kPartialAt + static_cast<size_t>(kAttnMaxCtas) * 2 * kPartialFloats * 4 <= SPECDEC_ATTENTION_WORKSPACE_BYTES,
+              "the workspace holds every CTA's records");
+constexpr int kAttnSmem = 227 * 1024;     // one CTA an SM
+
+template <int D>
+cudaError_t launch_attention(AttnArgs a, const void* k_cache, const void* v_cache, cudaStream_t st) {
+  CUtensorMap km, vm;
+  cudaError_t e = cache_map(&km, k_cache, D, a.bs, a.H, a.num_blocks);
+  if (e == cudaSuccess) e = cache_map(&vm, v_cache, D, a.bs, a.H, a.num_blocks);
+  if (e != cudaSuccess) return e;
+  static int sms[64] = {0};
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (sms[dev] == 0) {
+    e = cudaFuncSetAttribute(attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem);
+    if (e != cudaSuccess) return e;
+    int n = 0;
+    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    sms[dev] = n;
+  }
+  using L = AttnLayout<D>;
+  const int fit = (kAttnSmem - L::bytes(0, a.rows)) / (2 * L::kTileBytes);
+  a.ring = fit < kMaxRing ? fit : kMaxRing;
+  const int grid = sms[dev] < kAttnMaxCtas ? sms[dev] : kAttnMaxCtas;
+  attention_kernel<D><<<grid, kAttnThreads, L::bytes(a.ring, a.rows), st>>>(a, km, vm);
+  return cudaGetLastError();
+}
+
 }  // namespace
 }  // namespace specdec
 
@@ -251,18 +310,18 @@ extern "C" specdec_status_t spec_attention(const void* q, int64_t q_token_stride
   a.max_blocks = max_blocks;
   a.num_blocks = num_blocks;
   a.bs = block_size;
-  a.k_cache = static_cast<const uint8_t*>(k_cache);
-  a.v_cache = static_cast<const uint8_t*>(v_cache);
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  a.scale = scale > 0.f ? scale : (D == 64 ? 0.125f : 0.08838834764831845f);
-  const int64_t rows = static_cast<int64_t>(T) * Hq;
-  if ((rows + 3) / 4 > INT32_MAX) return SPECDEC_ERR_UNSUPPORTED;
-  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
+  a.scale_log2e = (scale > 0.f ? scale : (D == 64 ? 0.125f : 0.08838834764831845f)) * 1.4426950408889634f;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  a.err = reinterpret_cast<uint32_t*>(ws);
+  a.counters = reinterpret_cast<uint32_t*>(ws + 256);
+  a.partial = reinterpret_cast<float*>(ws + kPartialAt);
+  // A row group is as long as the call's rows allow: fewer rows leave more
+  // shared memory to the tiles in flight.
+  const int64_t rows = static_cast<int64_t>(T) * (Hq / H);
+  a.rows = static_cast<int32_t>(rows >= kAttnRows ? kAttnRows : (rows + 15) / 16 * 16);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (D == 64)
-    attention_simple_kernel<64><<<grid, 128, 0, st>>>(a);
-  else
-    attention_simple_kernel<128><<<grid, 128, 0, st>>>(a);
-  return launched();
+  const cudaError_t e = D == 64 ? launch_attention<64>(a, k_cache, v_cache, st) : launch_attention<128>(a, k_cache, v_cache, st);
+  return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }

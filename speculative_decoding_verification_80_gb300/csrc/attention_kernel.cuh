@@ -27,6 +27,12 @@
 // the first tile, and whenever a later score lies more than 2^9 above it.  So
 // O stays in tensor memory, and most tiles need no search for a maximum.
 //
+// Two groups of four warps do the softmax.  Up to 32 rows each takes every
+// other tile, with references, sums and an O of its own, which the output
+// warps add up: a tile then has the time of two.  Above 32 rows each takes
+// half of the rows of every tile, so that a thread's scores and sums stay in
+// registers.
+//
 // The tiles of all requests, heads and row groups form one list that is cut
 // into equal parts, one for each CTA; what a cut separates is joined by the
 // CTA that finishes last, in the order of the parts.
@@ -61,6 +67,7 @@ struct AttnArgs {
 
 constexpr int kTile = 128;      // positions of a tile
 constexpr int kAttnRows = 64;   // most rows of a tile
+constexpr int kHalfRows = kAttnRows / 2;  // most of a softmax group
 // Warps: 0-3 and 4-7 softmax of half of the rows each, 8-11 V to f16, 12-15 Q
 // and O, 16 copies, 17 products.
 constexpr int kAttnThreads = 576;
@@ -162,13 +169,14 @@ struct AttnShared {
   int32_t b0;
   long long ub0;
   long long part[32];
-  alignas(16) float2 col[kAttnRows];  // {row scale, reference} of each row
-  float wmax[2][4][kAttnRows / 2];    // a warp's largest score of each row of its half
+  alignas(16) float2 col[2][kHalfRows];  // {row scale, reference} of each group's rows
+  float wmax[2][4][kHalfRows];        // a warp's largest score of each of its group's rows
   float qs[2][kAttnRows];
   int32_t limit[2][kAttnRows];        // last position a row attends to
-  float lsum[2][4][kAttnRows];        // sums of the softmax warps
-  float mrun[2][kAttnRows];
-  float vref[2];
+  float lsum[2][8][kHalfRows];        // sums of the softmax warps
+  float mrun[2][2][kHalfRows];        // and their groups' references
+  float vref[2][2];
+  alignas(16) float4 fin[kAttnRows];  // {factor of one group's O, of the other's, sum (or its inverse), reference}
   int32_t nanpos[2][128];             // first new position whose value is NaN in a dimension
   ScaleEntry scales[kScaleRing];
   int32_t last;
@@ -199,7 +207,12 @@ struct Waiter {
     if (!dead && !ptx::mbar_wait_bounded(ptx::smem_addr(&bar), parity, SPECDEC_WAIT_BUDGET_CYCLES)) dead = true;
   }
 };
-__device__ __forceinline__ void arrive(uint64_t& bar) { ptx::mbar_arrive(ptx::smem_addr(&bar)); }
+// Arrivals for the warp, after what all its threads did before.
+__device__ __forceinline__ void warp_arrive(uint64_t& bar, uint32_t n = 1) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0)
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(ptx::smem_addr(&bar)), "r"(n) : "memory");
+}
 
 // Nearest number of 4 significant bits; the remainder of a number of 8 has 4.
 __device__ __forceinline__ float top4(float x) {
@@ -271,19 +284,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     for (int i = 0; i < 2; ++i) {
       init(sh.s_full[i], 1);
       init(sh.s_empty[i], 8);
-      init(sh.p_full[i], 256);
-      init(sh.f_full[i], 128);
+      init(sh.p_full[i], 8);
+      init(sh.f_full[i], 4);
       init(sh.pv_done[i], 1);
       init(sh.o_full[i], 1);
-      init(sh.o_empty[i], 128);
-      init(sh.meta_full[i], 128);
-      init(sh.l_full[i], 256 + 128);
+      init(sh.o_empty[i], 4);
+      init(sh.meta_full[i], 4);
+      init(sh.l_full[i], 12);
     }
     for (int i = 0; i < kScaleRing; ++i) {
-      init(sh.sc_full[i], 32);
+      init(sh.sc_full[i], 1);
       init(sh.sc_empty[i], 8);
     }
-    init(sh.q_full, 128);
+    init(sh.q_full, 4);
     init(sh.q_empty, 1);
     init(sh.done, 1);
     ptx::fence_mbarrier_init();
@@ -346,35 +359,40 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
-    // A thread has one position and half of the rows.
-    constexpr int kHalfRows = kAttnRows / 2;
+    // A thread has one position and the rows of its group.
     const int grp = warp >> 2, t_in = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     float x[kHalfRows], l[kHalfRows];
+    const float4* col = reinterpret_cast<const float4*>(sh.col[grp]);
     Walker walk(a, u0, u1, b0, ub0);
-    int k = 0;  // tiles so far
+    int k0 = 0;  // tiles of the segments before
     for (int n_seg = 0; walk.next(seg); ++n_seg) {
       const int par = n_seg & 1;
-      const int eights = (seg.rows + 15) / 16;  // groups of 8 rows of this half
-      const int r0 = grp * eights * 8;
+      const bool by_rows = seg.rows > kHalfRows;
+      const int step = by_rows ? 1 : 2;
+      // groups of 8 rows, and the first row
+      const int eights = by_rows ? (seg.rows + 15) / 16 : (seg.rows + 15) / 16 * 2;
+      const int r0 = by_rows ? grp * eights * 8 : 0;
+      const int tiles = seg.tile1 - seg.tile0;
       float vref = 1.f;
 #pragma unroll
       for (int r = 0; r < kHalfRows; ++r) l[r] = 0.f;
       wait(sh.meta_full[par], (n_seg >> 1) & 1);
       named_barrier(1 + grp, 128);  // the last segment's rows are no longer read
-      if (t_in < eights * 8) sh.col[r0 + t_in] = make_float2(sh.qs[par][r0 + t_in], 0.f);
+      if (t_in < eights * 8) sh.col[grp][t_in] = make_float2(sh.qs[par][r0 + t_in], 0.f);
       named_barrier(1 + grp, 128);
       const int all_see = seg.kv + seg.row0 / G;  // last position that all rows attend to
-      const uint32_t o_at = tmem + lanes + (2 + par) * kAttnRows + r0;
-      for (int t = seg.tile0; t < seg.tile1; ++t, ++k) {
-        const int pos0 = t * kTile, pos = pos0 + t_in;
+      const uint32_t o_at = tmem + lanes + (2 + par) * kAttnRows + (by_rows ? r0 : grp * kHalfRows);
+      bool first = true;
+      // by tiles: those whose number is of the group's parity
+      for (int i = by_rows ? 0 : ((k0 ^ grp) & 1); i < tiles; i += step) {
+        const int k = k0 + i;
+        const int pos0 = (seg.tile0 + i) * kTile, pos = pos0 + t_in;
         const bool masked = pos0 + kTile - 1 > all_see || pos0 + kTile > seg.len;
-        const bool first = t == seg.tile0;
         const ScaleEntry& sc = sh.scales[k % kScaleRing];
         wait(sh.sc_full[k % kScaleRing], (k / kScaleRing) & 1);
         const float ks = sc.ks[t_in / a.bs], vs = sc.vs[t_in / a.bs], vmax = sc.vmax;
-        __syncwarp();
-        if (lane == 0) arrive(sh.sc_empty[k % kScaleRing]);
+        warp_arrive(sh.sc_empty[k % kScaleRing], step);
         const bool raise_v = first || vmax > 4.f * vref;
         const float vref_was = vref;
         if (raise_v) vref = vmax > 0.f ? vmax : 0x1p-100f;
@@ -395,7 +413,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
             const int r = c * 8 + e;
-            const float4 w = *reinterpret_cast<const float4*>(&sh.col[r0 + r]);
+            const float4 w = col[r >> 1];
             x[r] = fmaf(x[r] * ks, w.x, -w.y);
             x[r + 1] = fmaf(x[r + 1] * ks, w.z, -w.w);
           }
@@ -408,8 +426,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           for (int e = 0; e < 8; ++e) top = fmaxf(top, x[c * 8 + e]);
         }
         tc::fence_before();
-        __syncwarp();
-        if (lane == 0) arrive(sh.s_empty[k & 1]);
+        warp_arrive(sh.s_empty[k & 1], step);
         // does P stay within f16 (and the sum within 32 bits)?
         const bool over = top > fminf(kSlack - __log2f(ratio), 60.f);
         if (named_any(1 + grp, 128, over) || raise_v) {
@@ -423,7 +440,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               if (lane == 0) sh.wmax[grp][warp & 3][c * 8 + e] = m;
             }
           }
-          if (!first) wait(sh.pv_done[(k - 1) & 1], ((k - 1) >> 1) & 1);  // O rests
+          if (!first) wait(sh.pv_done[(k - step) & 1], ((k - step) >> 1) & 1);  // O rests
           tc::fence_after();
           named_barrier(1 + grp, 128);
           const float v_ratio = first ? 1.f : vref_was / vref;
@@ -455,10 +472,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (t_in < eights * 8) {
             float m = fmaxf(fmaxf(sh.wmax[grp][0][t_in], sh.wmax[grp][1][t_in]), fmaxf(sh.wmax[grp][2][t_in], sh.wmax[grp][3][t_in]));
             if (first ? !(m > -INFINITY) : !(m > 0.f)) m = 0.f;
-            sh.col[r0 + t_in].y += m;
+            sh.col[grp][t_in].y += m;
           }
           named_barrier(1 + grp, 128);
         }
+        first = false;
         if (k >= 2) wait(sh.pv_done[k & 1], ((k >> 1) - 1) & 1);
         // probabilities
         unsigned char* p = p_at + (k & 1) * L::p_bytes(a.rows) + (r0 / 8) * (16 * kTile) + t_in * 16;
@@ -477,18 +495,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           *reinterpret_cast<uint4*>(p + c * (16 * kTile)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         tc::fence_smem();
-        arrive(sh.p_full[k & 1]);
+        warp_arrive(sh.p_full[k & 1], step);
       }
+      k0 += tiles;
       // sums and references for the output warps
 #pragma unroll
       for (int c = 0; c < kHalfRows / 8; ++c) {
         if (c >= eights) break;
         const float s = warp_sums8(l + c * 8);
-        if ((lane & 3) == 0) sh.lsum[par][warp & 3][r0 + c * 8 + (lane >> 2)] = s;
+        if ((lane & 3) == 0) sh.lsum[par][warp][c * 8 + (lane >> 2)] = s;
       }
-      if (t_in < eights * 8) sh.mrun[par][r0 + t_in] = sh.col[r0 + t_in].y;
-      if (tid == 0) sh.vref[par] = vref / kPScale;
-      arrive(sh.l_full[par]);
+      if (t_in < eights * 8) sh.mrun[par][grp][t_in] = sh.col[grp][t_in].y;
+      if (t_in == 0) sh.vref[par][grp] = vref / kPScale;
+      warp_arrive(sh.l_full[par]);
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ V to f16
@@ -510,8 +529,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         uint4 c[D / 16];
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) c[i] = *reinterpret_cast<const uint4*>(from + swizzled<D>(t_in, i * 16));
-        __syncwarp();
-        if (lane == 0) arrive(sh.v_empty[slot]);
+        warp_arrive(sh.v_empty[slot]);
         if (++slot == a.ring) slot = 0, ++round;
         if (pos0 + kTile > min(seg.kv, seg.len)) {
           if (pos >= seg.len) {
@@ -543,9 +561,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           *reinterpret_cast<uint4*>(to + (i >> 3) * (kTile * 128) + t_in * 128 + (((i & 7) ^ (t_in & 7)) << 4)) = h;
         }
         tc::fence_smem();
-        arrive(sh.f_full[k & 1]);
+        warp_arrive(sh.f_full[k & 1]);
       }
-      arrive(sh.l_full[par]);
+      warp_arrive(sh.l_full[par]);
     }
   } else if (warp < 16) {
     // ------------------------------------------------------------- Q and O
@@ -612,8 +630,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       sh.nanpos[par][ot] = 0x7FFFFFFF;
       tc::fence_smem();
-      arrive(sh.q_full);
-      arrive(sh.meta_full[par]);
+      warp_arrive(sh.q_full);
+      warp_arrive(sh.meta_full[par]);
     };
     Walker walk(a, u0, u1, b0, ub0);
     Segment nxt;
@@ -632,44 +650,79 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         store_q(nxt, par ^ 1);
       }
       wait(sh.l_full[par], (n_seg >> 1) & 1);
+      const bool by_rows = seg.rows > kHalfRows;
+      const bool whole = seg.tile0 == 0 && seg.tile1 == seg.tiles;
+      if (ot < seg.rows) {
+        // a group whose sum is 0 has nothing, whatever its reference and O
+        const int half_rows = by_rows ? (seg.rows + 15) / 16 * 8 : kAttnRows;
+        const int r = ot % half_rows, own_grp = ot / half_rows;
+        float s[2] = {0.f, 0.f}, m[2] = {0.f, 0.f}, M = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (by_rows && g != own_grp) continue;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) s[g] += sh.lsum[par][g * 4 + w][r];
+          m[g] = sh.mrun[par][g][r];
+          if (s[g] != 0.f) M = fmaxf(M, m[g]);
+        }
+        float f[2], sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float w = s[g] != 0.f ? tc::ex2(m[g] - M) : 0.f;
+          sum += w * s[g];
+          f[g] = s[g] != 0.f ? w * sh.vref[par][g] : 0.f;
+        }
+        if (by_rows) f[0] += f[1];  // one of them
+        if (whole) sum = sum == 0.f ? 0.f : 1.f / sum;
+        sh.fin[ot] = make_float4(f[0], f[1], sum, M);
+      }
+      named_barrier(3, 128);
       wait(sh.o_full[par], (n_seg >> 1) & 1);
       tc::fence_after();
       const int nan_at = sh.nanpos[par][d];
-      const float vref = sh.vref[par];
-      const bool whole = seg.tile0 == 0 && seg.tile1 == seg.tiles;
       const int slot = static_cast<int>(blockIdx.x) * 2 + (n_seg == 0 ? 0 : 1);
       float* rec = a.partial + static_cast<long long>(slot) * kPartialFloats;
       const uint32_t o_at = tmem + (static_cast<uint32_t>(ow * 32) << 16) + (2 + par) * kAttnRows;
       int tok = seg.row0 / G, g = seg.row0 % G;  // of row r
+      __nv_bfloat16* dst = a.out + (static_cast<long long>(seg.q0 + tok) * a.Hq + seg.h * G + g) * D + d;
+      const long long next_tok = static_cast<long long>(a.Hq - (G - 1)) * D;  // from a token's last head to the next's first
       for (int c = 0; c * 8 < seg.rows; ++c) {
-        float o[8];
+        float o[8], o2[8];
         tc::ld8(o_at + c * 8, o);
+        if (!by_rows) tc::ld8(o_at + kHalfRows + c * 8, o2);
         tc::wait_ld();
         tc::ready(o);
+        if (!by_rows) tc::ready(o2);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int r = c * 8 + e;
-          if (r >= seg.rows) break;
-          float v = o[e] * vref;
-          if (nan_at <= seg.kv + tok) v = __uint_as_float(0x7FFFFFFFu);
-          const float sum = (sh.lsum[par][0][r] + sh.lsum[par][1][r]) + (sh.lsum[par][2][r] + sh.lsum[par][3][r]);
-          if (whole) {
-            if (owns)
-              a.out[(static_cast<long long>(seg.q0 + tok) * a.Hq + seg.h * G + g) * D + d] =
-                  __float2bfloat16_rn(sum == 0.f ? 0.f : v / sum);
-          } else {
-            if (owns) rec[r * D + d] = v;
-            if (ot == 0) {
-              rec[kAttnRows * 128 + r] = sh.mrun[par][r];
-              rec[kAttnRows * 128 + kAttnRows + r] = sum;
+          if (r < seg.rows) {
+            const float4 f = sh.fin[r];
+            float v = f.x != 0.f ? o[e] * f.x : 0.f;
+            if (!by_rows && f.y != 0.f) v = fmaf(o2[e], f.y, v);
+            if (nan_at <= seg.kv + tok) v = __uint_as_float(0x7FFFFFFFu);
+            if (whole) {
+              if (owns) *dst = __float2bfloat16_rn(v * f.z);
+            } else if (owns) {
+              rec[r * D + d] = v;
+            }
+            if (++g == G) {
+              g = 0;
+              ++tok;
+              dst += next_tok;
+            } else {
+              dst += D;
             }
           }
-          if (++g == G) g = 0, ++tok;
         }
       }
       tc::fence_before();
-      arrive(sh.o_empty[par]);
+      warp_arrive(sh.o_empty[par]);
       if (!whole) {
+        if (ot < seg.rows) {
+          rec[kAttnRows * 128 + ot] = sh.fin[ot].w;
+          rec[kAttnRows * 128 + kAttnRows + ot] = sh.fin[ot].z;
+        }
         // the last of the item's CTAs joins the parts
         const long long c0 = seg.first / chunk, c1 = (seg.first + seg.tiles - 1) / chunk;
         __threadfence();
@@ -685,63 +738,90 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           };
           for (int r = ow; r < seg.rows; r += 4) {
             const int row = seg.row0 + r;
-            // a piece whose sum is 0 has nothing, whatever its reference
-            float M = -INFINITY;
-            for (int p = lane; p < pieces; p += 32) {
-              const float* q = record(p) + kAttnRows * 128;
-              if (__ldcg(q + kAttnRows + r) != 0.f) M = fmaxf(M, __ldcg(q + r));
+            constexpr int E = D / 32;  // a lane's values
+            float M = -INFINITY, sum = 0.f, acc[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) acc[i] = 0.f;
+            for (int p0 = 0; p0 < pieces; p0 += 32) {
+              // a lane for each piece: its reference and sum
+              float m = -INFINITY, n = 0.f;
+              if (p0 + lane < pieces) {
+                const float* q = record(p0 + lane) + kAttnRows * 128;
+                n = __ldcg(q + kAttnRows + r);
+                if (n != 0.f) m = __ldcg(q + r);
+              }
+              const float M_new = fmaxf(M, tc::warp_max(m));
+              const float f = M > -INFINITY ? tc::ex2(M - M_new) : 0.f;
+              const float w = n != 0.f ? tc::ex2(m - M_new) : 0.f;
+              M = M_new;
+              float part = w * n;
+#pragma unroll
+              for (int s = 16; s > 0; s >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, s);
+              sum = fmaf(sum, f, part);
+#pragma unroll
+              for (int i = 0; i < E; ++i) acc[i] *= f;
+              const int here = min(32, pieces - p0);
+#pragma unroll 8
+              for (int p = 0; p < here; ++p) {
+                const float wp = __shfl_sync(0xFFFFFFFFu, w, p);
+                const float* q = record(p0 + p) + r * D + lane * E;
+                float v[E];
+                if constexpr (D == 128) {
+                  const float4 y = __ldcg(reinterpret_cast<const float4*>(q));
+                  v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+                } else {
+                  const float2 y = __ldcg(reinterpret_cast<const float2*>(q));
+                  v[0] = y.x, v[1] = y.y;
+                }
+#pragma unroll
+                for (int i = 0; i < E; ++i) acc[i] = fmaf(wp, v[i], acc[i]);
+              }
             }
-            M = tc::warp_max(M);
-            float sum = 0.f, acc[D / 32];
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            uint32_t* to = reinterpret_cast<uint32_t*>(
+                a.out + (static_cast<long long>(seg.q0 + row / G) * a.Hq + seg.h * G + row % G) * D + lane * E);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
-#pragma unroll 4
-            for (int p = 0; p < pieces; ++p) {
-              const float* q = record(p);
-              const float n = __ldcg(q + kAttnRows * 128 + kAttnRows + r);
-              const float w = n != 0.f ? tc::ex2(__ldcg(q + kAttnRows * 128 + r) - M) : 0.f;
-              sum += w * n;
-#pragma unroll
-              for (int i = 0; i < D / 32; ++i) acc[i] += w * __ldcg(q + r * D + i * 32 + lane);
+            for (int i = 0; i < E; i += 2) {
+              const __nv_bfloat162 y = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
+              to[i / 2] = *reinterpret_cast<const uint32_t*>(&y);
             }
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-              a.out[(static_cast<long long>(seg.q0 + row / G) * a.Hq + seg.h * G + row % G) * D + i * 32 + lane] =
-                  __float2bfloat16_rn(sum == 0.f ? 0.f : acc[i] / sum);
           }
           if (ot == 0) ptx::st_relaxed_u32(a.counters + c0, 0u);
         }
-        named_barrier(3, 128);
       }
+      named_barrier(3, 128);  // sh.fin and sh.last are no longer read
     }
   } else if (warp == 16) {
     // ------------------------------------------------------------- copies
-    // Block ids are loaded two tiles ahead and their scales one tile ahead.
-    struct Ahead {
-      int h, pages, id;
+    // A lane holds a block: 32 block ids, then their scales, are loaded at a
+    // time, a batch of whole tiles ahead of the one in use.
+    struct Batch {
+      int h, tiles, pages;  // tiles of the batch, blocks of its segment from its first on
+      int id;
       float ks, vs;
-      bool there;
-    } t0, t1, t2;
+    } now, nxt;
     Walker walk(a, u0, u1, b0, ub0);
     int tile = 0, tile_end = 0;
-    auto load_ids = [&](Ahead& x) {
-      x.there = false;
+    const int per_batch = 32 / pages_per_tile;
+    auto load_ids = [&](Batch& x) {
+      x.tiles = 0;
       if (tile >= tile_end) {
         if (!walk.next(seg)) return;
         tile = seg.tile0;
         tile_end = seg.tile1;
       }
-      x.there = true;
+      x.tiles = min(per_batch, tile_end - tile);
       x.h = seg.h;
       const int page0 = tile * pages_per_tile;
-      x.pages = max(0, min(pages_per_tile, (seg.len + a.bs - 1) / a.bs - page0));
+      x.pages = max(0, (seg.len + a.bs - 1) / a.bs - page0);
       x.id = -1;
-      if (lane < x.pages) x.id = __ldg(a.table + static_cast<long long>(seg.b) * a.max_blocks + page0 + lane);
-      ++tile;
+      if (lane < x.pages && lane < x.tiles * pages_per_tile)
+        x.id = __ldg(a.table + static_cast<long long>(seg.b) * a.max_blocks + page0 + lane);
+      tile += x.tiles;
     };
-    auto load_scales = [&](Ahead& x) {
+    auto load_scales = [&](Batch& x) {
       x.ks = x.vs = 0.f;
-      if (x.there && x.id >= 0 && x.id < a.num_blocks) {
+      if (x.tiles > 0 && x.id >= 0 && x.id < a.num_blocks) {
         x.ks = __ldg(a.k_scale + static_cast<long long>(x.id) * a.H + x.h);
         x.vs = __ldg(a.v_scale + static_cast<long long>(x.id) * a.H + x.h);
       }
@@ -750,35 +830,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       tc::prefetch_map(&k_map);
       tc::prefetch_map(&v_map);
     }
-    load_ids(t0);
-    load_scales(t0);
-    load_ids(t1);
-    int slot = 0, round = 0;
-    for (int k = 0; t0.there; ++k) {
-      load_scales(t1);
-      load_ids(t2);
+    load_ids(now);
+    load_scales(now);
+    int slot = 0, round = 0, k = 0;
+    while (now.tiles > 0) {
+      load_ids(nxt);
+      for (int i = 0; i < now.tiles; ++i, ++k) {
+        const int pages = max(0, min(pages_per_tile, now.pages - i * pages_per_tile));
+        const int src = (i * pages_per_tile + lane) & 31;
+        const int id = __shfl_sync(0xFFFFFFFFu, now.id, src);
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        if (round > 0) wait(kv ? sh.v_empty[slot] : sh.k_empty[slot], (round - 1) & 1);
-        const uint32_t bar = ptx::smem_addr(kv ? &sh.v_full[slot] : &sh.k_full[slot]);
-        if (lane == 0) ptx::mbar_arrive_expect_tx(bar, t0.pages * a.bs * D);
-        __syncwarp();
-        if (lane < t0.pages)
-          tc::load_4d(ptx::smem_addr((kv ? v_tiles : k_tiles) + slot * L::kTileBytes + lane * a.bs * D), kv ? &v_map : &k_map,
-                      0, 0, t0.h, t0.id, bar);
+        for (int kv = 0; kv < 2; ++kv) {
+          if (round > 0) wait(kv ? sh.v_empty[slot] : sh.k_empty[slot], (round - 1) & 1);
+          const uint32_t bar = ptx::smem_addr(kv ? &sh.v_full[slot] : &sh.k_full[slot]);
+          if (lane == 0) ptx::mbar_arrive_expect_tx(bar, pages * a.bs * D);
+          __syncwarp();
+          if (lane < pages)
+            tc::load_4d(ptx::smem_addr((kv ? v_tiles : k_tiles) + slot * L::kTileBytes + lane * a.bs * D),
+                        kv ? &v_map : &k_map, 0, 0, now.h, id, bar);
+        }
+        if (++slot == a.ring) slot = 0, ++round;
+        if (i == 0) load_scales(nxt);  // its ids have had a tile's time
+        const int sr = k % kScaleRing;
+        if (k >= kScaleRing) wait(sh.sc_empty[sr], (k / kScaleRing - 1) & 1);
+        const float ks = __shfl_sync(0xFFFFFFFFu, now.ks, src), vs = __shfl_sync(0xFFFFFFFFu, now.vs, src);
+        const float vmax = tc::warp_max(lane < pages_per_tile ? vs : 0.f);
+        if (lane < pages_per_tile) {
+          sh.scales[sr].ks[lane] = ks * a.scale_log2e;
+          sh.scales[sr].vs[lane] = vs;
+        }
+        if (lane == 0) sh.scales[sr].vmax = vmax;
+        warp_arrive(sh.sc_full[sr]);
       }
-      if (++slot == a.ring) slot = 0, ++round;
-      const int sr = k % kScaleRing;
-      if (k >= kScaleRing) wait(sh.sc_empty[sr], (k / kScaleRing - 1) & 1);
-      const float vmax = tc::warp_max(t0.vs);
-      if (lane < kMaxPages) {
-        sh.scales[sr].ks[lane] = t0.ks * a.scale_log2e;
-        sh.scales[sr].vs[lane] = t0.vs;
-      }
-      if (lane == 0) sh.scales[sr].vmax = vmax;
-      arrive(sh.sc_full[sr]);
-      t0 = t1;
-      t1 = t2;
+      now = nxt;
     }
     // no copy is in flight when the CTA ends: every slot used has been filled
     Waiter drain;
@@ -788,69 +872,84 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       drain(sh.v_full[i], (i < slot ? round : round - 1) & 1);
     }
     wait.dead |= drain.dead;
-  } else if (lane == 0) {
+  } else {
     // ------------------------------------------------------------ products
-    // Scores go one tile ahead, into the next segment too where its Q is there.
+    // Scores go up to two tiles ahead, into the next segment too, as soon as
+    // their K, Q and place in tensor memory are there.
     const uint64_t swz = D == 128 ? tc::kSwizzle128 : tc::kSwizzle64;
+    const uint64_t kd0 = tc::smem_desc(ptx::smem_addr(k_tiles), 16, 8 * D, swz);
+    const uint64_t qd0 = tc::smem_desc(ptx::smem_addr(q_hi), 128, 8 * D, tc::kSwizzleNone);
+    const uint64_t qd1 = tc::smem_desc(ptx::smem_addr(q_lo), 128, 8 * D, tc::kSwizzleNone);
+    const uint64_t vd0 = tc::smem_desc(ptx::smem_addr(v_half), kTile * 128, 1024, tc::kSwizzle128);
+    const uint64_t pd0 = tc::smem_desc(ptx::smem_addr(p_at), 128, 16 * kTile, tc::kSwizzleNone);
     Walker walk(a, u0, u1, b0, ub0), ahead(a, u0, u1, b0, ub0);
     Segment s_seg;
-    int s_k = 0, s_tile = 0, s_end = 0, s_n = -1, slot = 0, round = 0;  // next tile of scores
+    int s_k = 0, s_n = 0, slot = 0, round = 0;  // next tile of scores
+    bool s_more = ahead.next(s_seg);
+    int s_tile = s_more ? s_seg.tile0 : 0;
+    auto is_done = [&](const uint64_t& bar, uint32_t parity) {  // the same for all lanes
+      return __shfl_sync(0xFFFFFFFFu, static_cast<int>(ptx::mbar_test_wait(ptx::smem_addr(&bar), parity)), 0) != 0;
+    };
+    auto try_scores = [&]() {
+      if (!s_more || !is_done(sh.k_full[slot], round & 1)) return false;
+      if (s_tile == s_seg.tile0 && !is_done(sh.q_full, s_n & 1)) return false;
+      if (s_k >= 2 && !is_done(sh.s_empty[s_k & 1], ((s_k >> 1) - 1) & 1)) return false;
+      tc::fence_after();
+      const uint32_t is = tc::instr(kTile, (s_seg.rows + 15) / 16 * 16, false, false);
+      const uint64_t kd = kd0 + slot * (L::kTileBytes / 16);
+      const uint32_t dst = tmem + (s_k & 1) * kAttnRows;
+      const bool last = s_tile + 1 == s_seg.tile1;
+      if (tc::elect()) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) tc::mma_e4m3(dst, kd + i * 2, qd0 + i * 16, is, i > 0);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) tc::mma_e4m3(dst, kd + i * 2, qd1 + i * 16, is, true);
+        tc::commit(ptx::smem_addr(&sh.s_full[s_k & 1]));
+        tc::commit(ptx::smem_addr(&sh.k_empty[slot]));
+        if (last) tc::commit(ptx::smem_addr(&sh.q_empty));
+      }
+      __syncwarp();
+      if (++slot == a.ring) slot = 0, ++round;
+      ++s_k;
+      ++s_tile;
+      if (last) {
+        s_more = ahead.next(s_seg);
+        s_tile = s_seg.tile0;
+        ++s_n;
+      }
+      return true;
+    };
     int k = 0;
     for (int n_seg = 0; walk.next(seg); ++n_seg) {
       const int par = n_seg & 1;
-      const int n = (seg.rows + 15) / 16 * 16;
-      const uint32_t io = tc::instr(D, n, true, true);
+      const bool by_rows = seg.rows > kHalfRows;
+      const uint32_t io = tc::instr(D, (seg.rows + 15) / 16 * 16, true, true);
+      if (n_seg >= 2) wait(sh.o_empty[par], ((n_seg >> 1) - 1) & 1);
       for (int t = seg.tile0; t < seg.tile1; ++t, ++k) {
-        while (s_k <= k + 1) {
-          if (s_tile >= s_end) {
-            if (s_end < 0 || !ahead.next(s_seg)) {
-              s_end = -1;
-              break;
-            }
-            s_tile = s_seg.tile0;
-            s_end = s_seg.tile1;
-            ++s_n;
-          }
-          if (s_tile == s_seg.tile0) {  // a new Q
-            if (s_k <= k)
-              wait(sh.q_full, s_n & 1);
-            else if (!ptx::mbar_test_wait(ptx::smem_addr(&sh.q_full), s_n & 1))
-              break;
-          }
-          wait(sh.k_full[slot], round & 1);
-          if (s_k >= 2) wait(sh.s_empty[s_k & 1], ((s_k >> 1) - 1) & 1);
-          tc::fence_after();
-          const uint32_t is = tc::instr(kTile, (s_seg.rows + 15) / 16 * 16, false, false);
-          const uint64_t kd = tc::smem_desc(ptx::smem_addr(k_tiles + slot * L::kTileBytes), 16, 8 * D, swz);
-          const uint32_t dst = tmem + (s_k & 1) * kAttnRows;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint64_t qd = tc::smem_desc(ptx::smem_addr(h ? q_lo : q_hi), 128, 8 * D, tc::kSwizzleNone);
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) tc::mma_e4m3(dst, kd + i * 2, qd + i * 16, is, h > 0 || i > 0);
-          }
-          tc::commit(ptx::smem_addr(&sh.k_empty[slot]));
-          tc::commit(ptx::smem_addr(&sh.s_full[s_k & 1]));
-          if (++slot == a.ring) slot = 0, ++round;
-          ++s_k;
-          if (++s_tile == s_end) tc::commit(ptx::smem_addr(&sh.q_empty));
+        const long long since = clock64();
+        while (!wait.dead) {
+          if (s_k <= k + 2 && try_scores()) continue;
+          if (s_k > k && is_done(sh.f_full[k & 1], (k >> 1) & 1) && is_done(sh.p_full[k & 1], (k >> 1) & 1)) break;
+          if (__any_sync(0xFFFFFFFFu, clock64() - since > SPECDEC_WAIT_BUDGET_CYCLES)) wait.dead = true;
         }
-        if (t == seg.tile0 && n_seg >= 2) wait(sh.o_empty[par], ((n_seg >> 1) - 1) & 1);
-        wait(sh.f_full[k & 1], (k >> 1) & 1);
-        wait(sh.p_full[k & 1], (k >> 1) & 1);
         tc::fence_after();
-        const uint64_t vd = tc::smem_desc(ptx::smem_addr(v_half + (k & 1) * L::kHalfBytes), kTile * 128, 1024, tc::kSwizzle128);
-        const uint64_t pd = tc::smem_desc(ptx::smem_addr(p_at + (k & 1) * L::p_bytes(a.rows)), 128, 16 * kTile, tc::kSwizzleNone);
+        const uint64_t vd = vd0 + (k & 1) * (L::kHalfBytes / 16);
+        const uint64_t pd = pd0 + (k & 1) * (L::p_bytes(a.rows) / 16);
+        const uint32_t dst = tmem + (2 + par) * kAttnRows + (by_rows ? 0 : (k & 1) * kHalfRows);
+        const bool add = t >= seg.tile0 + (by_rows ? 1 : 2);
+        if (tc::elect()) {
 #pragma unroll
-        for (int i = 0; i < kTile / 16; ++i)
-          tc::mma_f16(tmem + (2 + par) * kAttnRows, vd + i * 128, pd + i * 16, io, t > seg.tile0 || i > 0);
-        tc::commit(ptx::smem_addr(&sh.pv_done[k & 1]));
+          for (int i = 0; i < kTile / 16; ++i) tc::mma_f16(dst, vd + i * 128, pd + i * 16, io, add || i > 0);
+          tc::commit(ptx::smem_addr(&sh.pv_done[k & 1]));
+          if (t + 1 == seg.tile1) tc::commit(ptx::smem_addr(&sh.o_full[par]));
+        }
+        __syncwarp();
       }
-      tc::commit(ptx::smem_addr(&sh.o_full[par]));
     }
     // all products are done before the tensor memory goes back
     Waiter drain;
-    tc::commit(ptx::smem_addr(&sh.done));
+    if (tc::elect()) tc::commit(ptx::smem_addr(&sh.done));
+    __syncwarp();
     drain(sh.done, 0);
     wait.dead |= drain.dead;
   }

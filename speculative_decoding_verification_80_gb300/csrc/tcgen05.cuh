@@ -91,6 +91,17 @@ __device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* m, int 
       : "memory");
 }
 
+// One thread of a converged warp, always the same.
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // -------------------------------------------------------------- arithmetic
 __device__ __forceinline__ float ex2(float x) {
   float y;

@@ -54,7 +54,7 @@ struct AttnArgs {
   const int32_t* cu_tokens;
   const int32_t* kv_len;
   const int32_t* table;
-  int32_t max_blocks, num_blocks, bs;
+  int32_t max_blocks, num_blocks, bs, bs_log2;
   const float* k_scale;
   const float* v_scale;
   float scale_log2e;
@@ -68,9 +68,14 @@ struct AttnArgs {
 constexpr int kTile = 128;      // positions of a tile
 constexpr int kAttnRows = 64;   // most rows of a tile
 constexpr int kHalfRows = kAttnRows / 2;  // most of a softmax group
-// Warps: 0-3 and 4-7 softmax of half of the rows each, 8-11 V to f16, 12-15 Q
-// and O, 16 copies, 17 products.
-constexpr int kAttnThreads = 576;
+// Warps: 0-3 and 4-7 softmax, 8-11 V to f16, 12-15 Q and O, 16 copies, 17
+// products (18 and 19 fill the warpgroup).
+constexpr int kAttnThreads = 640;
+// Registers a thread: 96 at launch, moved to the softmax, whose scores and
+// sums are 64 of them: 128 (256 + 64 + 80 + 72) <= 96 * 640.
+constexpr int kRegsSoftmax = 128, kRegsValues = 64, kRegsOutput = 80, kRegsRest = 72;
+static_assert(256 * kRegsSoftmax + 128 * (kRegsValues + kRegsOutput + kRegsRest) <= 96 * kAttnThreads,
+              "the warpgroups' registers are those of the launch");
 constexpr int kScaleRing = 8;
 constexpr int kMaxRing = 8;     // tiles of K, and of V, in shared memory
 constexpr int kMaxPages = 8;    // blocks of a tile
@@ -360,8 +365,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
     // A thread has one position and the rows of its group.
+    tc::more_registers<kRegsSoftmax>();
     const int grp = warp >> 2, t_in = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int page = t_in >> a.bs_log2;
     float x[kHalfRows], l[kHalfRows];
     const float4* col = reinterpret_cast<const float4*>(sh.col[grp]);
     Walker walk(a, u0, u1, b0, ub0);
@@ -374,7 +381,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int eights = by_rows ? (seg.rows + 15) / 16 : (seg.rows + 15) / 16 * 2;
       const int r0 = by_rows ? grp * eights * 8 : 0;
       const int tiles = seg.tile1 - seg.tile0;
-      float vref = 1.f;
+      float vref = 1.f, vinv = 1.f;
 #pragma unroll
       for (int r = 0; r < kHalfRows; ++r) l[r] = 0.f;
       wait(sh.meta_full[par], (n_seg >> 1) & 1);
@@ -391,12 +398,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const bool masked = pos0 + kTile - 1 > all_see || pos0 + kTile > seg.len;
         const ScaleEntry& sc = sh.scales[k % kScaleRing];
         wait(sh.sc_full[k % kScaleRing], (k / kScaleRing) & 1);
-        const float ks = sc.ks[t_in / a.bs], vs = sc.vs[t_in / a.bs], vmax = sc.vmax;
+        const float ks = sc.ks[page], vs = sc.vs[page], vmax = sc.vmax;
         warp_arrive(sh.sc_empty[k % kScaleRing], step);
         const bool raise_v = first || vmax > 4.f * vref;
         const float vref_was = vref;
-        if (raise_v) vref = vmax > 0.f ? vmax : 0x1p-100f;
-        const float ratio = vs / vref, vr = ratio * kPScale;
+        if (raise_v) {
+          vref = vmax > 0x1p-100f ? vmax : 0x1p-100f;
+          vinv = 1.f / vref;
+        }
+        const float ratio = vs * vinv, vr = ratio * kPScale;
         wait(sh.s_full[k & 1], (k >> 1) & 1);
         tc::fence_after();
         // scores over the rows' references
@@ -515,6 +525,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // of the request's: zeros.  New positions are not seen by all rows: their
     // NaN leave the product, where 0 times NaN would spoil rows that do not
     // see them, and are noted for the output.
+    tc::fewer_registers<kRegsValues>();
     const int t_in = tid - 256;
     Walker walk(a, u0, u1, b0, ub0);
     int k = 0, slot = 0, round = 0;
@@ -567,6 +578,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
   } else if (warp < 16) {
     // ------------------------------------------------------------- Q and O
+    tc::fewer_registers<kRegsOutput>();
     const int ot = tid - 384, ow = ot >> 5;
     const int d = D == 128 ? ot : 16 * ow + (lane & 15);
     const bool owns = D == 128 || lane < 16;
@@ -736,54 +748,74 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           auto record = [&](int p) {
             return a.partial + static_cast<long long>(p == 0 ? first_slot : (c0 + p) * 2) * kPartialFloats;
           };
-          for (int r = ow; r < seg.rows; r += 4) {
-            const int row = seg.row0 + r;
-            constexpr int E = D / 32;  // a lane's values
-            float M = -INFINITY, sum = 0.f, acc[E];
+          constexpr int E = D / 32;  // a lane's values
+          for (int r4 = 0; r4 < seg.rows; r4 += 16) {
+            // rows r4 + ow, + 4, + 8, + 12 at once, for their loads' sake
+            float M[4], sum[4], acc[4][E];
 #pragma unroll
-            for (int i = 0; i < E; ++i) acc[i] = 0.f;
+            for (int j = 0; j < 4; ++j) {
+              M[j] = -INFINITY;
+              sum[j] = 0.f;
+#pragma unroll
+              for (int i = 0; i < E; ++i) acc[j][i] = 0.f;
+            }
             for (int p0 = 0; p0 < pieces; p0 += 32) {
-              // a lane for each piece: its reference and sum
-              float m = -INFINITY, n = 0.f;
-              if (p0 + lane < pieces) {
-                const float* q = record(p0 + lane) + kAttnRows * 128;
-                n = __ldcg(q + kAttnRows + r);
-                if (n != 0.f) m = __ldcg(q + r);
+              // a lane for each piece: its references and sums
+              float m[4], n[4], w[4];
+              const float* q = record(min(p0 + lane, pieces - 1)) + kAttnRows * 128 + r4 + ow;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const bool in = p0 + lane < pieces && r4 + ow + 4 * j < seg.rows;
+                m[j] = in ? __ldcg(q + 4 * j) : 0.f;
+                n[j] = in ? __ldcg(q + kAttnRows + 4 * j) : 0.f;
               }
-              const float M_new = fmaxf(M, tc::warp_max(m));
-              const float f = M > -INFINITY ? tc::ex2(M - M_new) : 0.f;
-              const float w = n != 0.f ? tc::ex2(m - M_new) : 0.f;
-              M = M_new;
-              float part = w * n;
 #pragma unroll
-              for (int s = 16; s > 0; s >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, s);
-              sum = fmaf(sum, f, part);
+              for (int j = 0; j < 4; ++j) {
+                const float M_new = fmaxf(M[j], tc::warp_max(n[j] != 0.f ? m[j] : -INFINITY));
+                const float f = M[j] > -INFINITY ? tc::ex2(M[j] - M_new) : 0.f;
+                w[j] = n[j] != 0.f ? tc::ex2(m[j] - M_new) : 0.f;
+                M[j] = M_new;
+                float part = w[j] * n[j];
 #pragma unroll
-              for (int i = 0; i < E; ++i) acc[i] *= f;
+                for (int s = 16; s > 0; s >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, s);
+                sum[j] = fmaf(sum[j], f, part);
+#pragma unroll
+                for (int i = 0; i < E; ++i) acc[j][i] *= f;
+              }
               const int here = min(32, pieces - p0);
-#pragma unroll 8
+#pragma unroll 2
               for (int p = 0; p < here; ++p) {
-                const float wp = __shfl_sync(0xFFFFFFFFu, w, p);
-                const float* q = record(p0 + p) + r * D + lane * E;
-                float v[E];
-                if constexpr (D == 128) {
-                  const float4 y = __ldcg(reinterpret_cast<const float4*>(q));
-                  v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
-                } else {
-                  const float2 y = __ldcg(reinterpret_cast<const float2*>(q));
-                  v[0] = y.x, v[1] = y.y;
-                }
+                const float* y = record(p0 + p) + (r4 + ow) * D + lane * E;
 #pragma unroll
-                for (int i = 0; i < E; ++i) acc[i] = fmaf(wp, v[i], acc[i]);
+                for (int j = 0; j < 4; ++j) {
+                  const float wp = __shfl_sync(0xFFFFFFFFu, w[j], p);
+                  if (r4 + ow + 4 * j < seg.rows) {
+                    float v[E];
+                    if constexpr (D == 128) {
+                      const float4 z = __ldcg(reinterpret_cast<const float4*>(y + 4 * j * D));
+                      v[0] = z.x, v[1] = z.y, v[2] = z.z, v[3] = z.w;
+                    } else {
+                      const float2 z = __ldcg(reinterpret_cast<const float2*>(y + 4 * j * D));
+                      v[0] = z.x, v[1] = z.y;
+                    }
+#pragma unroll
+                    for (int i = 0; i < E; ++i) acc[j][i] = fmaf(wp, v[i], acc[j][i]);
+                  }
+                }
               }
             }
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            uint32_t* to = reinterpret_cast<uint32_t*>(
-                a.out + (static_cast<long long>(seg.q0 + row / G) * a.Hq + seg.h * G + row % G) * D + lane * E);
 #pragma unroll
-            for (int i = 0; i < E; i += 2) {
-              const __nv_bfloat162 y = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
-              to[i / 2] = *reinterpret_cast<const uint32_t*>(&y);
+            for (int j = 0; j < 4; ++j) {
+              const int row = seg.row0 + r4 + ow + 4 * j;
+              if (r4 + ow + 4 * j >= seg.rows) break;
+              const float inv = sum[j] == 0.f ? 0.f : 1.f / sum[j];
+              uint32_t* to = reinterpret_cast<uint32_t*>(
+                  a.out + (static_cast<long long>(seg.q0 + row / G) * a.Hq + seg.h * G + row % G) * D + lane * E);
+#pragma unroll
+              for (int i = 0; i < E; i += 2) {
+                const __nv_bfloat162 y = __floats2bfloat162_rn(acc[j][i] * inv, acc[j][i + 1] * inv);
+                to[i / 2] = *reinterpret_cast<const uint32_t*>(&y);
+              }
             }
           }
           if (ot == 0) ptx::st_relaxed_u32(a.counters + c0, 0u);
@@ -791,7 +823,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       named_barrier(3, 128);  // sh.fin and sh.last are no longer read
     }
-  } else if (warp == 16) {
+  } else {
+    tc::fewer_registers<kRegsRest>();
+    if (warp == 16) {
     // ------------------------------------------------------------- copies
     // A lane holds a block: 32 block ids, then their scales, are loaded at a
     // time, a batch of whole tiles ahead of the one in use.
@@ -872,7 +906,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       drain(sh.v_full[i], (i < slot ? round : round - 1) & 1);
     }
     wait.dead |= drain.dead;
-  } else {
+    } else if (warp == 17) {
     // ------------------------------------------------------------ products
     // Scores go up to two tiles ahead, into the next segment too, as soon as
     // their K, Q and place in tensor memory are there.
@@ -952,6 +986,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncwarp();
     drain(sh.done, 0);
     wait.dead |= drain.dead;
+    }
   }
   __syncwarp();
   if (wait.dead) atomicOr(a.err, SPECDEC_DEV_ERR_TIMEOUT);

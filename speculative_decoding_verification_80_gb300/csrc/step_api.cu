@@ -310,6 +310,7 @@ extern "C" specdec_status_t spec_attention(const void* q, int64_t q_token_stride
   a.max_blocks = max_blocks;
   a.num_blocks = num_blocks;
   a.bs = block_size;
+  a.bs_log2 = block_size == 16 ? 4 : block_size == 32 ? 5 : block_size == 64 ? 6 : 7;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.scale_log2e = (scale > 0.f ? scale : (D == 64 ? 0.125f : 0.08838834764831845f)) * 1.4426950408889634f;

@@ -91,6 +91,15 @@ __device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* m, int 
       : "memory");
 }
 
+// Registers a thread of this warpgroup from here on (all four warps).
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 // One thread of a converged warp, always the same.
 __device__ __forceinline__ bool elect() {
   uint32_t r;

@@ -68,15 +68,16 @@ struct AttnArgs {
 constexpr int kTile = 128;      // positions of a tile
 constexpr int kAttnRows = 64;   // most rows of a tile
 constexpr int kHalfRows = kAttnRows / 2;  // most of a softmax group
-// Warps: 0-3 and 4-7 softmax, 8-11 V to f16, 12-15 Q and O, 16 copies, 17
-// products (18 and 19 fill the warpgroup).
+// Warps: 0-3 and 4-7 softmax, 8-11 V to f16, 12-15 Q and O, 16 copies, 17 first
+// products, 18 second products, 19 the list of segments.
 constexpr int kAttnThreads = 640;
 // Registers a thread: 96 at launch, moved to the softmax, whose scores and
-// sums are 64 of them: 128 (256 + 64 + 80 + 72) <= 96 * 640.
-constexpr int kRegsSoftmax = 128, kRegsValues = 64, kRegsOutput = 80, kRegsRest = 72;
+// sums are 64 of them.
+constexpr int kRegsSoftmax = 120, kRegsValues = 72, kRegsOutput = 96, kRegsRest = 64;
 static_assert(256 * kRegsSoftmax + 128 * (kRegsValues + kRegsOutput + kRegsRest) <= 96 * kAttnThreads,
               "the warpgroups' registers are those of the launch");
 constexpr int kScaleRing = 8;
+constexpr int kSegRing = 4;
 constexpr int kMaxRing = 8;     // tiles of K, and of V, in shared memory
 constexpr int kMaxPages = 8;    // blocks of a tile
 constexpr uint32_t kTmemCols = 256;  // S twice, O twice
@@ -85,11 +86,13 @@ constexpr int kPartialFloats = kAttnRows * 128 + 2 * kAttnRows;
 // before P would leave f16.
 constexpr float kPScale = 64.f;
 constexpr float kSlack = 9.f;
-#ifndef SPECDEC_WAIT_BUDGET_CYCLES
-#define SPECDEC_WAIT_BUDGET_CYCLES 4000000000LL
+// A wait gives up after this many tries of at most a microsecond each.
+#ifndef SPECDEC_ATTN_WAIT_TRIES
+#define SPECDEC_ATTN_WAIT_TRIES 2000000u
 #endif
 
-// Part of a (request, head, row group) that one CTA works on.
+// Part of a (request, head, row group) that one CTA works on.  tile1 < 0 ends
+// the list.
 struct Segment {
   int b, h, row0, rows;       // rows of this group
   int q0, kv, len;            // first token, positions before it, positions of the group
@@ -169,13 +172,15 @@ struct AttnShared {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
   uint64_t s_full[2], s_empty[2], p_full[2], f_full[2], pv_done[2], o_full[2], o_empty[2];
   uint64_t q_full, q_empty, meta_full[2], l_full[2];
-  uint64_t sc_full[kScaleRing], sc_empty[kScaleRing], done;
+  uint64_t sc_full[kScaleRing], sc_empty[kScaleRing], seg_full[kSegRing], seg_empty[kSegRing], done[2];
   uint32_t tmem;
   int32_t b0;
   long long ub0;
+  Segment seg[kSegRing];
   long long part[32];
   alignas(16) float2 col[2][kHalfRows];  // {row scale, reference} of each group's rows
   float wmax[2][4][kHalfRows];        // a warp's largest score of each of its group's rows
+  float fac[2][kHalfRows];            // factors from a row's reference to its next
   float qs[2][kAttnRows];
   int32_t limit[2][kAttnRows];        // last position a row attends to
   float lsum[2][8][kHalfRows];        // sums of the softmax warps
@@ -205,11 +210,18 @@ __device__ __forceinline__ bool named_any(int id, int threads, bool x) {
 }
 
 // A wait that gives up once; after that the thread goes on without waiting, so
-// that every barrier still gets its arrivals and the CTA ends.
+// that every barrier still gets its arrivals, to the end of its segment.  What
+// decides how often a group of warps meets at a barrier is agreed on at one.
 struct Waiter {
   bool dead = false;
-  __device__ void operator()(const uint64_t& bar, uint32_t parity) {
-    if (!dead && !ptx::mbar_wait_bounded(ptx::smem_addr(&bar), parity, SPECDEC_WAIT_BUDGET_CYCLES)) dead = true;
+  __device__ __forceinline__ void operator()(const uint64_t& bar, uint32_t parity) {
+    if (dead) return;
+    const uint32_t at = ptx::smem_addr(&bar);
+    for (uint32_t n = SPECDEC_ATTN_WAIT_TRIES; !tc::try_wait(at, parity);)
+      if (--n == 0) {
+        dead = true;
+        break;
+      }
   }
 };
 // Arrivals for the warp, after what all its threads did before.
@@ -303,7 +315,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     init(sh.q_full, 4);
     init(sh.q_empty, 1);
-    init(sh.done, 1);
+    init(sh.done[0], 1);
+    init(sh.done[1], 1);
+    for (int i = 0; i < kSegRing; ++i) {
+      init(sh.seg_full[i], 1);
+      init(sh.seg_empty[i], 19);
+    }
     ptx::fence_mbarrier_init();
     sh.b0 = 0;
     sh.ub0 = 0;
@@ -356,11 +373,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tc::fence_after();
   }
   const uint32_t tmem = sh.tmem;
-  const int b0 = sh.b0;
-  const long long ub0 = sh.ub0;
   Waiter wait;
-  Segment seg;
-  const int pages_per_tile = kTile / a.bs;
+  // The n-th segment, or null at the list's end; and the warp is done with it.
+  auto segment = [&](int n) -> const Segment* {
+    wait(sh.seg_full[n % kSegRing], (n / kSegRing) & 1);
+    wait.dead = __any_sync(0xFFFFFFFFu, wait.dead);
+    const Segment* s = &sh.seg[n % kSegRing];
+    return wait.dead || s->tile1 < 0 ? nullptr : s;
+  };
+  auto leave = [&](int n) { warp_arrive(sh.seg_empty[n % kSegRing]); };
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
@@ -371,121 +392,129 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int page = t_in >> a.bs_log2;
     float x[kHalfRows], l[kHalfRows];
     const float4* col = reinterpret_cast<const float4*>(sh.col[grp]);
-    Walker walk(a, u0, u1, b0, ub0);
     int k0 = 0;  // tiles of the segments before
-    for (int n_seg = 0; walk.next(seg); ++n_seg) {
+    for (int n_seg = 0;; ++n_seg) {
+      const Segment* seg = segment(n_seg);
+      // (and the last segment's rows are no longer read)
+      if (named_any(1 + grp, 128, seg == nullptr)) break;
       const int par = n_seg & 1;
-      const bool by_rows = seg.rows > kHalfRows;
+      const bool by_rows = seg->rows > kHalfRows;
       const int step = by_rows ? 1 : 2;
       // groups of 8 rows, and the first row
-      const int eights = by_rows ? (seg.rows + 15) / 16 : (seg.rows + 15) / 16 * 2;
+      const int eights = by_rows ? (seg->rows + 15) / 16 : (seg->rows + 15) / 16 * 2;
       const int r0 = by_rows ? grp * eights * 8 : 0;
-      const int tiles = seg.tile1 - seg.tile0;
+      const int tiles = seg->tile1 - seg->tile0, len = seg->len;
+      const int all_see = seg->kv + seg->row0 / G;  // last position that all rows attend to
+      int pos0 = seg->tile0 * kTile;
+      const uint32_t o_at = tmem + lanes + (2 + par) * kAttnRows + (by_rows ? r0 : grp * kHalfRows);
       float vref = 1.f, vinv = 1.f;
 #pragma unroll
       for (int r = 0; r < kHalfRows; ++r) l[r] = 0.f;
       wait(sh.meta_full[par], (n_seg >> 1) & 1);
-      named_barrier(1 + grp, 128);  // the last segment's rows are no longer read
       if (t_in < eights * 8) sh.col[grp][t_in] = make_float2(sh.qs[par][r0 + t_in], 0.f);
       named_barrier(1 + grp, 128);
-      const int all_see = seg.kv + seg.row0 / G;  // last position that all rows attend to
-      const uint32_t o_at = tmem + lanes + (2 + par) * kAttnRows + (by_rows ? r0 : grp * kHalfRows);
       bool first = true;
       // by tiles: those whose number is of the group's parity
-      for (int i = by_rows ? 0 : ((k0 ^ grp) & 1); i < tiles; i += step) {
-        const int k = k0 + i;
-        const int pos0 = (seg.tile0 + i) * kTile, pos = pos0 + t_in;
-        const bool masked = pos0 + kTile - 1 > all_see || pos0 + kTile > seg.len;
+      int i = by_rows ? 0 : ((k0 ^ grp) & 1);
+      pos0 += i * kTile;
+      for (; i < tiles; i += step, pos0 += step * kTile) {
+        const int k = k0 + i, pos = pos0 + t_in;
+        const bool masked = pos0 + kTile - 1 > all_see || pos0 + kTile > len;
         const ScaleEntry& sc = sh.scales[k % kScaleRing];
         wait(sh.sc_full[k % kScaleRing], (k / kScaleRing) & 1);
         const float ks = sc.ks[page], vs = sc.vs[page], vmax = sc.vmax;
         warp_arrive(sh.sc_empty[k % kScaleRing], step);
-        const bool raise_v = first || vmax > 4.f * vref;
-        const float vref_was = vref;
-        if (raise_v) {
-          vref = vmax > 0x1p-100f ? vmax : 0x1p-100f;
-          vinv = 1.f / vref;
-        }
-        const float ratio = vs * vinv, vr = ratio * kPScale;
+        bool renew = first;
         wait(sh.s_full[k & 1], (k >> 1) & 1);
         tc::fence_after();
-        // scores over the rows' references
         const uint32_t s_at = tmem + lanes + (k & 1) * kAttnRows + r0;
+        for (;;) {
+          if (renew) {
+            // New references: the rows' largest scores so far, and the largest
+            // value scale where it has grown.
+            const float vref_was = vref;
+            if (first || vmax > 4.f * vref) {
+              vref = vmax > 0x1p-100f ? vmax : 0x1p-100f;
+              vinv = 1.f / vref;
+            }
+#pragma unroll 1
+            for (int c = 0; c < eights; ++c) {
+              float v[8], mine = -INFINITY;
+              tc::ld8(s_at + c * 8, v);
+              tc::wait_ld();
+              tc::ready(v);
 #pragma unroll
-        for (int c = 0; c < kHalfRows / 8; ++c)
-          if (c < eights) tc::ld8(s_at + c * 8, x + c * 8);
-        tc::wait_ld();
-        float top = -INFINITY;
+              for (int e = 0; e < 8; ++e) {
+                float y = v[e] * ks * sh.col[grp][c * 8 + e].x;
+                if (masked && pos > sh.limit[par][r0 + c * 8 + e]) y = -INFINITY;
+                y = tc::warp_max(y);
+                if (lane == e) mine = y;
+              }
+              if (lane < 8) sh.wmax[grp][warp & 3][c * 8 + lane] = mine;
+            }
+            if (!first) wait(sh.pv_done[(k - step) & 1], ((k - step) >> 1) & 1);  // O rests
+            tc::fence_after();
+            named_barrier(1 + grp, 128);
+            if (t_in < eights * 8) {
+              const float m = fmaxf(fmaxf(sh.wmax[grp][0][t_in], sh.wmax[grp][1][t_in]),
+                                    fmaxf(sh.wmax[grp][2][t_in], sh.wmax[grp][3][t_in]));
+              const float was = sh.col[grp][t_in].y;
+              const float now = first ? (m > -INFINITY ? m : 0.f) : fmaxf(was, m);
+              sh.col[grp][t_in].y = now;
+              sh.fac[grp][t_in] = tc::ex2(was - now);
+            }
+            named_barrier(1 + grp, 128);
+            if (!first) {
 #pragma unroll
-        for (int c = 0; c < kHalfRows / 8; ++c) {
-          if (c >= eights) break;
-          tc::ready(x + c * 8);
+              for (int r = 0; r < kHalfRows; ++r)
+                if (r < eights * 8) l[r] *= sh.fac[grp][r];
+              const float v_ratio = vref_was * vinv;
+#pragma unroll 1
+              for (int c = 0; c < eights; ++c) {
+                float o[8];
+                tc::ld8(o_at + c * 8, o);
+                tc::wait_ld();
+                tc::ready(o);
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const int r = c * 8 + e;
-            const float4 w = col[r >> 1];
-            x[r] = fmaf(x[r] * ks, w.x, -w.y);
-            x[r + 1] = fmaf(x[r + 1] * ks, w.z, -w.w);
+                for (int e = 0; e < 8; ++e) o[e] *= sh.fac[grp][c * 8 + e] * v_ratio;
+                tc::st8(o_at + c * 8, o);
+              }
+              tc::wait_st();
+              tc::fence_before();
+            }
           }
-          if (masked) {
+          // scores over the rows' references
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (pos > sh.limit[par][r0 + c * 8 + e]) x[c * 8 + e] = -INFINITY;
+          for (int c = 0; c < kHalfRows / 8; ++c)
+            if (c < eights) tc::ld8(s_at + c * 8, x + c * 8);
+          tc::wait_ld();
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kHalfRows / 8; ++c) {
+            if (c >= eights) break;
+            tc::ready(x + c * 8);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const int r = c * 8 + e;
+              const float4 w = col[r >> 1];
+              x[r] = fmaf(x[r] * ks, w.x, -w.y);
+              x[r + 1] = fmaf(x[r + 1] * ks, w.z, -w.w);
+            }
+            if (masked) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (pos > sh.limit[par][r0 + c * 8 + e]) x[c * 8 + e] = -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, x[c * 8 + e]);
           }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) top = fmaxf(top, x[c * 8 + e]);
+          // does P stay within f16 (and the sum within 32 bits)?
+          if (renew || !named_any(1 + grp, 128, top > fminf(kSlack - __log2f(vs * vinv), 60.f) || vmax > 4.f * vref)) break;
+          renew = true;
         }
+        const float vr = vs * vinv * kPScale;
         tc::fence_before();
         warp_arrive(sh.s_empty[k & 1], step);
-        // does P stay within f16 (and the sum within 32 bits)?
-        const bool over = top > fminf(kSlack - __log2f(ratio), 60.f);
-        if (named_any(1 + grp, 128, over) || raise_v) {
-          // New references: the rows' largest scores so far.
-#pragma unroll
-          for (int c = 0; c < kHalfRows / 8; ++c) {
-            if (c >= eights) break;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float m = tc::warp_max(x[c * 8 + e]);
-              if (lane == 0) sh.wmax[grp][warp & 3][c * 8 + e] = m;
-            }
-          }
-          if (!first) wait(sh.pv_done[(k - step) & 1], ((k - step) >> 1) & 1);  // O rests
-          tc::fence_after();
-          named_barrier(1 + grp, 128);
-          const float v_ratio = first ? 1.f : vref_was / vref;
-#pragma unroll
-          for (int c = 0; c < kHalfRows / 8; ++c) {
-            if (c >= eights) break;
-            float o[8];
-            if (!first) {
-              tc::ld8(o_at + c * 8, o);
-              tc::wait_ld();
-              tc::ready(o);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int r = c * 8 + e;
-              float m = fmaxf(fmaxf(sh.wmax[grp][0][r], sh.wmax[grp][1][r]), fmaxf(sh.wmax[grp][2][r], sh.wmax[grp][3][r]));
-              if (first ? !(m > -INFINITY) : !(m > 0.f)) m = 0.f;  // nothing above the reference
-              x[r] -= m;
-              if (!first) {
-                const float f = tc::ex2(-m);
-                l[r] *= f;
-                o[e] *= f * v_ratio;
-              }
-            }
-            if (!first) tc::st8(o_at + c * 8, o);
-          }
-          tc::wait_st();
-          tc::fence_before();
-          if (t_in < eights * 8) {
-            float m = fmaxf(fmaxf(sh.wmax[grp][0][t_in], sh.wmax[grp][1][t_in]), fmaxf(sh.wmax[grp][2][t_in], sh.wmax[grp][3][t_in]));
-            if (first ? !(m > -INFINITY) : !(m > 0.f)) m = 0.f;
-            sh.col[grp][t_in].y += m;
-          }
-          named_barrier(1 + grp, 128);
-        }
         first = false;
         if (k >= 2) wait(sh.pv_done[k & 1], ((k >> 1) - 1) & 1);
         // probabilities
@@ -518,6 +547,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (t_in < eights * 8) sh.mrun[par][grp][t_in] = sh.col[grp][t_in].y;
       if (t_in == 0) sh.vref[par][grp] = vref / kPScale;
       warp_arrive(sh.l_full[par]);
+      leave(n_seg);
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ V to f16
@@ -527,12 +557,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // see them, and are noted for the output.
     tc::fewer_registers<kRegsValues>();
     const int t_in = tid - 256;
-    Walker walk(a, u0, u1, b0, ub0);
     int k = 0, slot = 0, round = 0;
-    for (int n_seg = 0; walk.next(seg); ++n_seg) {
-      const int par = n_seg & 1;
+    for (int n_seg = 0;; ++n_seg) {
+      const Segment* seg = segment(n_seg);
+      if (seg == nullptr) break;
+      const int par = n_seg & 1, tile1 = seg->tile1, kv = seg->kv, len = seg->len;
       wait(sh.meta_full[par], (n_seg >> 1) & 1);  // nanpos is set
-      for (int t = seg.tile0; t < seg.tile1; ++t, ++k) {
+      for (int t = seg->tile0; t < tile1; ++t, ++k) {
         const int pos0 = t * kTile, pos = pos0 + t_in;
         const unsigned char* from = v_tiles + slot * L::kTileBytes;
         unsigned char* to = v_half + (k & 1) * L::kHalfBytes;
@@ -542,11 +573,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int i = 0; i < D / 16; ++i) c[i] = *reinterpret_cast<const uint4*>(from + swizzled<D>(t_in, i * 16));
         warp_arrive(sh.v_empty[slot]);
         if (++slot == a.ring) slot = 0, ++round;
-        if (pos0 + kTile > min(seg.kv, seg.len)) {
-          if (pos >= seg.len) {
+        if (pos0 + kTile > min(kv, len)) {
+          if (pos >= len) {
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) c[i] = make_uint4(0, 0, 0, 0);
-          } else if (pos >= seg.kv) {
+          } else if (pos >= kv) {
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
               uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
@@ -575,6 +606,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         warp_arrive(sh.f_full[k & 1]);
       }
       warp_arrive(sh.l_full[par]);
+      leave(n_seg);
     }
   } else if (warp < 16) {
     // ------------------------------------------------------------- Q and O
@@ -645,21 +677,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       warp_arrive(sh.q_full);
       warp_arrive(sh.meta_full[par]);
     };
-    Walker walk(a, u0, u1, b0, ub0);
-    Segment nxt;
-    bool more = walk.next(nxt);
-    if (more) {
-      load_q(nxt);
-      store_q(nxt, 0);
+    const Segment* nxt = segment(0);
+    if (nxt != nullptr) {
+      load_q(*nxt);
+      store_q(*nxt, 0);
     }
-    for (int n_seg = 0; more; ++n_seg) {
+    for (int n_seg = 0;; ++n_seg) {
+      if (named_any(3, 128, nxt == nullptr)) break;
       const int par = n_seg & 1;
-      seg = nxt;
-      more = walk.next(nxt);
-      if (more) {
-        load_q(nxt);
+      const Segment seg = *nxt;
+      nxt = segment(n_seg + 1);
+      if (nxt != nullptr) {
+        load_q(*nxt);
         wait(sh.q_empty, n_seg & 1);
-        store_q(nxt, par ^ 1);
+        store_q(*nxt, par ^ 1);
       }
       wait(sh.l_full[par], (n_seg >> 1) & 1);
       const bool by_rows = seg.rows > kHalfRows;
@@ -821,7 +852,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (ot == 0) ptx::st_relaxed_u32(a.counters + c0, 0u);
         }
       }
-      named_barrier(3, 128);  // sh.fin and sh.last are no longer read
+      leave(n_seg);
     }
   } else {
     tc::fewer_registers<kRegsRest>();
@@ -834,23 +865,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       int id;
       float ks, vs;
     } now, nxt;
-    Walker walk(a, u0, u1, b0, ub0);
-    int tile = 0, tile_end = 0;
+    const int pages_per_tile = kTile >> a.bs_log2;
+    int n_seg = -1, tile = 0, tile_end = 0, seg_b = 0, seg_h = 0, seg_pages = 0;
+    bool more = true;
     const int per_batch = 32 / pages_per_tile;
     auto load_ids = [&](Batch& x) {
       x.tiles = 0;
       if (tile >= tile_end) {
-        if (!walk.next(seg)) return;
-        tile = seg.tile0;
-        tile_end = seg.tile1;
+        if (n_seg >= 0 && more) leave(n_seg);
+        const Segment* s = more ? segment(++n_seg) : nullptr;
+        if (s == nullptr) {
+          more = false;
+          return;
+        }
+        tile = s->tile0;
+        tile_end = s->tile1;
+        seg_b = s->b;
+        seg_h = s->h;
+        seg_pages = (s->len + a.bs - 1) >> a.bs_log2;
       }
       x.tiles = min(per_batch, tile_end - tile);
-      x.h = seg.h;
+      x.h = seg_h;
       const int page0 = tile * pages_per_tile;
-      x.pages = max(0, (seg.len + a.bs - 1) / a.bs - page0);
+      x.pages = max(0, seg_pages - page0);
       x.id = -1;
       if (lane < x.pages && lane < x.tiles * pages_per_tile)
-        x.id = __ldg(a.table + static_cast<long long>(seg.b) * a.max_blocks + page0 + lane);
+        x.id = __ldg(a.table + static_cast<long long>(seg_b) * a.max_blocks + page0 + lane);
       tile += x.tiles;
     };
     auto load_scales = [&](Batch& x) {
@@ -907,85 +947,92 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     wait.dead |= drain.dead;
     } else if (warp == 17) {
-    // ------------------------------------------------------------ products
-    // Scores go up to two tiles ahead, into the next segment too, as soon as
-    // their K, Q and place in tensor memory are there.
-    const uint64_t swz = D == 128 ? tc::kSwizzle128 : tc::kSwizzle64;
-    const uint64_t kd0 = tc::smem_desc(ptx::smem_addr(k_tiles), 16, 8 * D, swz);
-    const uint64_t qd0 = tc::smem_desc(ptx::smem_addr(q_hi), 128, 8 * D, tc::kSwizzleNone);
-    const uint64_t qd1 = tc::smem_desc(ptx::smem_addr(q_lo), 128, 8 * D, tc::kSwizzleNone);
-    const uint64_t vd0 = tc::smem_desc(ptx::smem_addr(v_half), kTile * 128, 1024, tc::kSwizzle128);
-    const uint64_t pd0 = tc::smem_desc(ptx::smem_addr(p_at), 128, 16 * kTile, tc::kSwizzleNone);
-    Walker walk(a, u0, u1, b0, ub0), ahead(a, u0, u1, b0, ub0);
-    Segment s_seg;
-    int s_k = 0, s_n = 0, slot = 0, round = 0;  // next tile of scores
-    bool s_more = ahead.next(s_seg);
-    int s_tile = s_more ? s_seg.tile0 : 0;
-    auto is_done = [&](const uint64_t& bar, uint32_t parity) {  // the same for all lanes
-      return __shfl_sync(0xFFFFFFFFu, static_cast<int>(ptx::mbar_test_wait(ptx::smem_addr(&bar), parity)), 0) != 0;
-    };
-    auto try_scores = [&]() {
-      if (!s_more || !is_done(sh.k_full[slot], round & 1)) return false;
-      if (s_tile == s_seg.tile0 && !is_done(sh.q_full, s_n & 1)) return false;
-      if (s_k >= 2 && !is_done(sh.s_empty[s_k & 1], ((s_k >> 1) - 1) & 1)) return false;
-      tc::fence_after();
-      const uint32_t is = tc::instr(kTile, (s_seg.rows + 15) / 16 * 16, false, false);
-      const uint64_t kd = kd0 + slot * (L::kTileBytes / 16);
-      const uint32_t dst = tmem + (s_k & 1) * kAttnRows;
-      const bool last = s_tile + 1 == s_seg.tile1;
-      if (tc::elect()) {
+      // --------------------------------------------------- first products
+      const uint64_t swz = D == 128 ? tc::kSwizzle128 : tc::kSwizzle64;
+      const uint64_t kd0 = tc::smem_desc(ptx::smem_addr(k_tiles), 16, 8 * D, swz);
+      const uint64_t qd0 = tc::smem_desc(ptx::smem_addr(q_hi), 128, 8 * D, tc::kSwizzleNone);
+      const uint64_t qd1 = tc::smem_desc(ptx::smem_addr(q_lo), 128, 8 * D, tc::kSwizzleNone);
+      int k = 0, slot = 0, round = 0;
+      for (int n_seg = 0;; ++n_seg) {
+        const Segment* seg = segment(n_seg);
+        if (seg == nullptr) break;
+        const uint32_t is = tc::instr(kTile, (seg->rows + 15) / 16 * 16, false, false);
+        const int tiles = seg->tile1 - seg->tile0;
+        wait(sh.q_full, n_seg & 1);
+        for (int i = 0; i < tiles; ++i, ++k) {
+          const uint64_t kd = kd0 + slot * (L::kTileBytes / 16);
+          const uint32_t dst = tmem + (k & 1) * kAttnRows;
+          wait(sh.k_full[slot], round & 1);
+          if (k >= 2) wait(sh.s_empty[k & 1], ((k >> 1) - 1) & 1);
+          tc::fence_after();
+          if (tc::elect()) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) tc::mma_e4m3(dst, kd + i * 2, qd0 + i * 16, is, i > 0);
+            for (int j = 0; j < D / 32; ++j) tc::mma_e4m3(dst, kd + j * 2, qd0 + j * 16, is, j > 0);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) tc::mma_e4m3(dst, kd + i * 2, qd1 + i * 16, is, true);
-        tc::commit(ptx::smem_addr(&sh.s_full[s_k & 1]));
-        tc::commit(ptx::smem_addr(&sh.k_empty[slot]));
-        if (last) tc::commit(ptx::smem_addr(&sh.q_empty));
+            for (int j = 0; j < D / 32; ++j) tc::mma_e4m3(dst, kd + j * 2, qd1 + j * 16, is, true);
+            tc::commit(ptx::smem_addr(&sh.s_full[k & 1]));
+            tc::commit(ptx::smem_addr(&sh.k_empty[slot]));
+            if (i + 1 == tiles) tc::commit(ptx::smem_addr(&sh.q_empty));
+          }
+          __syncwarp();
+          if (++slot == a.ring) slot = 0, ++round;
+        }
+        leave(n_seg);
       }
+      // all products are done before the tensor memory goes back
+      Waiter drain;
+      if (tc::elect()) tc::commit(ptx::smem_addr(&sh.done[0]));
       __syncwarp();
-      if (++slot == a.ring) slot = 0, ++round;
-      ++s_k;
-      ++s_tile;
-      if (last) {
-        s_more = ahead.next(s_seg);
-        s_tile = s_seg.tile0;
-        ++s_n;
-      }
-      return true;
-    };
-    int k = 0;
-    for (int n_seg = 0; walk.next(seg); ++n_seg) {
-      const int par = n_seg & 1;
-      const bool by_rows = seg.rows > kHalfRows;
-      const uint32_t io = tc::instr(D, (seg.rows + 15) / 16 * 16, true, true);
-      if (n_seg >= 2) wait(sh.o_empty[par], ((n_seg >> 1) - 1) & 1);
-      for (int t = seg.tile0; t < seg.tile1; ++t, ++k) {
-        const long long since = clock64();
-        while (!wait.dead) {
-          if (s_k <= k + 2 && try_scores()) continue;
-          if (s_k > k && is_done(sh.f_full[k & 1], (k >> 1) & 1) && is_done(sh.p_full[k & 1], (k >> 1) & 1)) break;
-          if (__any_sync(0xFFFFFFFFu, clock64() - since > SPECDEC_WAIT_BUDGET_CYCLES)) wait.dead = true;
-        }
-        tc::fence_after();
-        const uint64_t vd = vd0 + (k & 1) * (L::kHalfBytes / 16);
-        const uint64_t pd = pd0 + (k & 1) * (L::p_bytes(a.rows) / 16);
-        const uint32_t dst = tmem + (2 + par) * kAttnRows + (by_rows ? 0 : (k & 1) * kHalfRows);
-        const bool add = t >= seg.tile0 + (by_rows ? 1 : 2);
-        if (tc::elect()) {
+      drain(sh.done[0], 0);
+      wait.dead |= drain.dead;
+    } else if (warp == 18) {
+      // -------------------------------------------------- second products
+      const uint64_t vd0 = tc::smem_desc(ptx::smem_addr(v_half), kTile * 128, 1024, tc::kSwizzle128);
+      const uint64_t pd0 = tc::smem_desc(ptx::smem_addr(p_at), 128, 16 * kTile, tc::kSwizzleNone);
+      int k = 0;
+      for (int n_seg = 0;; ++n_seg) {
+        const Segment* seg = segment(n_seg);
+        if (seg == nullptr) break;
+        const int par = n_seg & 1;
+        const bool by_rows = seg->rows > kHalfRows;
+        const uint32_t io = tc::instr(D, (seg->rows + 15) / 16 * 16, true, true);
+        const int tiles = seg->tile1 - seg->tile0;
+        if (n_seg >= 2) wait(sh.o_empty[par], ((n_seg >> 1) - 1) & 1);
+        for (int i = 0; i < tiles; ++i, ++k) {
+          const uint64_t vd = vd0 + (k & 1) * (L::kHalfBytes / 16);
+          const uint64_t pd = pd0 + (k & 1) * (L::p_bytes(a.rows) / 16);
+          const uint32_t dst = tmem + (2 + par) * kAttnRows + (by_rows ? 0 : (k & 1) * kHalfRows);
+          const bool add = i >= (by_rows ? 1 : 2);
+          wait(sh.f_full[k & 1], (k >> 1) & 1);
+          wait(sh.p_full[k & 1], (k >> 1) & 1);
+          tc::fence_after();
+          if (tc::elect()) {
 #pragma unroll
-          for (int i = 0; i < kTile / 16; ++i) tc::mma_f16(dst, vd + i * 128, pd + i * 16, io, add || i > 0);
-          tc::commit(ptx::smem_addr(&sh.pv_done[k & 1]));
-          if (t + 1 == seg.tile1) tc::commit(ptx::smem_addr(&sh.o_full[par]));
+            for (int j = 0; j < kTile / 16; ++j) tc::mma_f16(dst, vd + j * 128, pd + j * 16, io, add || j > 0);
+            tc::commit(ptx::smem_addr(&sh.pv_done[k & 1]));
+            if (i + 1 == tiles) tc::commit(ptx::smem_addr(&sh.o_full[par]));
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        leave(n_seg);
       }
-    }
-    // all products are done before the tensor memory goes back
-    Waiter drain;
-    if (tc::elect()) tc::commit(ptx::smem_addr(&sh.done));
-    __syncwarp();
-    drain(sh.done, 0);
-    wait.dead |= drain.dead;
+      Waiter drain;
+      if (tc::elect()) tc::commit(ptx::smem_addr(&sh.done[1]));
+      __syncwarp();
+      drain(sh.done[1], 0);
+      wait.dead |= drain.dead;
+    } else {
+      // -------------------------------------------------- list of segments
+      Walker walk(a, u0, u1, sh.b0, sh.ub0);
+      for (int n_seg = 0;; ++n_seg) {
+        if (n_seg >= kSegRing) wait(sh.seg_empty[n_seg % kSegRing], (n_seg / kSegRing - 1) & 1);
+        Segment s;
+        const bool more = walk.next(s);
+        if (!more) s.tile1 = -1;
+        if (lane == 0) sh.seg[n_seg % kSegRing] = s;
+        warp_arrive(sh.seg_full[n_seg % kSegRing]);
+        if (!more) break;
+      }
     }
   }
   __syncwarp();

@@ -27,11 +27,12 @@
 // the first tile, and whenever a later score lies more than 2^9 above it.  So
 // O stays in tensor memory, and most tiles need no search for a maximum.
 //
-// Two groups of four warps do the softmax.  Up to 32 rows each takes every
-// other tile, with references, sums and an O of its own, which the output
-// warps add up: a tile then has the time of two.  Above 32 rows each takes
-// half of the rows of every tile, so that a thread's scores and sums stay in
-// registers.
+// Four groups of four warps do the softmax, a group 16 rows of a tile: up to 16
+// rows each takes every fourth tile, up to 32 a pair every second one, above
+// that the rows of every tile are divided among them.  Groups of different
+// tiles have references, sums and an O of their own, which the output warps
+// add up.  A tile thus has the time of several (its steps are short and wait
+// for one another), and a thread's scores and sums are 32 registers.
 //
 // The tiles of all requests, heads and row groups form one list that is cut
 // into equal parts, one for each CTA; what a cut separates is joined by the
@@ -67,17 +68,19 @@ struct AttnArgs {
 
 constexpr int kTile = 128;      // positions of a tile
 constexpr int kAttnRows = 64;   // most rows of a tile
-constexpr int kHalfRows = kAttnRows / 2;  // most of a softmax group
-// Warps: 0-3 and 4-7 softmax, 8-11 V to f16, 12-15 Q and O, 16 copies, 17 first
-// products, 18 second products, 19 the list of segments.
-constexpr int kAttnThreads = 640;
-// Registers a thread: 96 at launch, moved to the softmax, whose scores and
-// sums are 64 of them.
-constexpr int kRegsSoftmax = 120, kRegsValues = 72, kRegsOutput = 96, kRegsRest = 64;
-static_assert(256 * kRegsSoftmax + 128 * (kRegsValues + kRegsOutput + kRegsRest) <= 96 * kAttnThreads,
+constexpr int kGroupRows = 16;  // of a softmax group
+constexpr int kGroups = 4;
+// Warps: 0-15 softmax, 16-19 V to f16, 20-23 Q and O, 24 copies of K, 25 first
+// products, 26 second products and the list of segments, 27 copies of V.
+constexpr int kValueWarp = 16, kOutputWarp = 20, kCopyWarp = 24;
+constexpr int kAttnThreads = 28 * 32;
+// Registers a thread: 72 at launch, moved to where they are needed.
+constexpr int kRegsValues = 72, kRegsOutput = 80, kRegsRest = 64;
+static_assert(512 * 72 + 128 * (kRegsValues + kRegsOutput + kRegsRest) <= 72 * kAttnThreads,
               "the warpgroups' registers are those of the launch");
 constexpr int kScaleRing = 8;
-constexpr int kSegRing = 4;
+constexpr int kSegRing = 8;
+constexpr int kSegAhead = 6;    // segments listed ahead of the second products'
 constexpr int kMaxRing = 8;     // tiles of K, and of V, in shared memory
 constexpr int kMaxPages = 8;    // blocks of a tile
 constexpr uint32_t kTmemCols = 256;  // S twice, O twice
@@ -168,9 +171,38 @@ struct ScaleEntry {
   float vmax;            // the tile's largest
 };
 
+// How the tiles of a segment go over the softmax groups and their buffers.
+struct Mode {
+  int m;        // 16s of rows
+  int by_tile;  // groups of different tiles: 4, 2 or 1
+  int buffers;  // of S and P: 4 of up to 32 rows, or 2
+  __device__ explicit Mode(int rows) : m((rows + 15) / 16) {
+    by_tile = m == 1 ? 4 : (m == 2 ? 2 : 1);
+    buffers = m <= 2 ? 4 : 2;
+  }
+  __device__ int buffer(int i) const { return i & (buffers - 1); }
+  // columns of a buffer of S, and of one of a parity's Os
+  __device__ int s_cols() const { return buffers == 4 ? 32 : 64; }
+  __device__ int o_cols() const { return kAttnRows / by_tile; }
+  // Arrivals of a group's warp: all of a tile's make 16.
+  __device__ uint32_t weight(int part) const { return m == 3 ? (part == 0 ? 2 : 1) : 4 / m; }
+};
+
+// Parities of four barriers that are used in turn, buffer i % buffers for tile
+// i of a segment; what every role of the CTA knows without asking.
+struct Turns {
+  uint32_t bits = 0;
+  __device__ uint32_t of(const Mode& mode, int i) const {
+    return ((bits >> mode.buffer(i)) ^ static_cast<uint32_t>(i / mode.buffers)) & 1;
+  }
+  __device__ void pass(const Mode& mode, int tiles) {
+    for (int b = 0; b < mode.buffers; ++b) bits ^= static_cast<uint32_t>(((tiles + mode.buffers - 1 - b) / mode.buffers) & 1) << b;
+  }
+};
+
 struct AttnShared {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
-  uint64_t s_full[2], s_empty[2], p_full[2], f_full[2], pv_done[2], o_full[2], o_empty[2];
+  uint64_t s_full[4], s_empty[4], p_full[4], pv_done[4], f_full[2], f_empty[2], o_full[2], o_empty[2];
   uint64_t q_full, q_empty, meta_full[2], l_full[2];
   uint64_t sc_full[kScaleRing], sc_empty[kScaleRing], seg_full[kSegRing], seg_empty[kSegRing], done[2];
   uint32_t tmem;
@@ -178,16 +210,17 @@ struct AttnShared {
   long long ub0;
   Segment seg[kSegRing];
   long long part[32];
-  alignas(16) float2 col[2][kHalfRows];  // {row scale, reference} of each group's rows
-  float wmax[2][4][kHalfRows];        // a warp's largest score of each of its group's rows
-  float fac[2][kHalfRows];            // factors from a row's reference to its next
+  alignas(16) float2 col[kGroups][kGroupRows];  // {row scale, reference} of each group's rows
+  float wmax[kGroups][4][kGroupRows];  // a warp's largest score of each of its group's rows
+  float fac[kGroups][kGroupRows];      // factors from a row's reference to its next
   float qs[2][kAttnRows];
-  int32_t limit[2][kAttnRows];        // last position a row attends to
-  float lsum[2][8][kHalfRows];        // sums of the softmax warps
-  float mrun[2][2][kHalfRows];        // and their groups' references
-  float vref[2][2];
-  alignas(16) float4 fin[kAttnRows];  // {factor of one group's O, of the other's, sum (or its inverse), reference}
-  int32_t nanpos[2][128];             // first new position whose value is NaN in a dimension
+  int32_t limit[2][kAttnRows];         // last position a row attends to
+  float lsum[2][kGroups][4][kGroupRows];  // sums of the softmax warps
+  float mrun[2][kGroups][kGroupRows];  // and their groups' references
+  float vref[2][kGroups];
+  alignas(16) float4 of[kAttnRows];    // factors of the groups' Os
+  float2 fin[kAttnRows];               // {sum (or its inverse), reference}
+  int32_t nanpos[2][128];              // first new position whose value is NaN in a dimension
   ScaleEntry scales[kScaleRing];
   int32_t last;
 };
@@ -242,23 +275,27 @@ __device__ __forceinline__ int swizzled(int t, int x) {
   return D == 128 ? t * 128 + (x ^ ((t & 7) << 4)) : t * 64 + (x ^ (((t >> 1) & 3) << 4));
 }
 
-// Sums of 8 values over the warp: lane i gets that of value i >> 2.
-__device__ __forceinline__ float warp_sums8(const float* v) {
+// Sums of 16 values over the warp: lane i gets that of value i >> 1.
+__device__ __forceinline__ float warp_sums16(const float* v) {
   const int lane = threadIdx.x & 31;
-  float a[4], b[2];
+  float a[8], b[4], c[2];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool up = lane & 16;
+    a[i] = (up ? v[i + 8] : v[i]) + __shfl_xor_sync(0xFFFFFFFFu, up ? v[i] : v[i + 8], 16);
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const bool up = lane & 16;
-    a[i] = (up ? v[i + 4] : v[i]) + __shfl_xor_sync(0xFFFFFFFFu, up ? v[i] : v[i + 4], 16);
+    const bool up = lane & 8;
+    b[i] = (up ? a[i + 4] : a[i]) + __shfl_xor_sync(0xFFFFFFFFu, up ? a[i] : a[i + 4], 8);
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const bool up = lane & 8;
-    b[i] = (up ? a[i + 2] : a[i]) + __shfl_xor_sync(0xFFFFFFFFu, up ? a[i] : a[i + 2], 8);
+    const bool up = lane & 4;
+    c[i] = (up ? b[i + 2] : b[i]) + __shfl_xor_sync(0xFFFFFFFFu, up ? b[i] : b[i + 2], 4);
   }
-  const bool up = lane & 4;
-  float s = (up ? b[1] : b[0]) + __shfl_xor_sync(0xFFFFFFFFu, up ? b[0] : b[1], 4);
-  s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
+  const bool up = lane & 2;
+  const float s = (up ? c[1] : c[0]) + __shfl_xor_sync(0xFFFFFFFFu, up ? c[0] : c[1], 2);
   return s + __shfl_xor_sync(0xFFFFFFFFu, s, 1);
 }
 
@@ -267,10 +304,11 @@ struct AttnLayout {
   static constexpr int kTileBytes = kTile * D;       // of K or V
   static constexpr int kHalfBytes = kTile * D * 2;   // of V in f16
   static __host__ __device__ int q_bytes(int rows) { return rows * D; }          // of one half
-  static __host__ __device__ int p_bytes(int rows) { return rows * kTile * 2; }  // of one buffer
+  // of all buffers: four of up to 32 rows or two of 64
+  static __host__ __device__ int p_bytes(int rows) { return (rows <= 32 ? 4 * rows : 2 * rows) * kTile * 2; }
   static __host__ __device__ int tiles_at() { return (static_cast<int>(sizeof(AttnShared)) + 1023) / 1024 * 1024; }
   static __host__ __device__ int bytes(int ring, int rows) {
-    return 1024 + tiles_at() + 2 * ring * kTileBytes + 2 * kHalfBytes + 2 * q_bytes(rows) + 2 * p_bytes(rows);
+    return 1024 + tiles_at() + 2 * ring * kTileBytes + 2 * kHalfBytes + 2 * q_bytes(rows) + p_bytes(rows);
   }
 };
 
@@ -298,20 +336,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       init(sh.v_full[i], 1);
       init(sh.v_empty[i], 4);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       init(sh.s_full[i], 1);
-      init(sh.s_empty[i], 8);
-      init(sh.p_full[i], 8);
-      init(sh.f_full[i], 4);
+      init(sh.s_empty[i], 16);
+      init(sh.p_full[i], 16);
       init(sh.pv_done[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      init(sh.f_full[i], 4);
+      init(sh.f_empty[i], 1);
       init(sh.o_full[i], 1);
       init(sh.o_empty[i], 4);
       init(sh.meta_full[i], 4);
-      init(sh.l_full[i], 12);
+      init(sh.l_full[i], 20);
     }
     for (int i = 0; i < kScaleRing; ++i) {
-      init(sh.sc_full[i], 1);
-      init(sh.sc_empty[i], 8);
+      init(sh.sc_full[i], 2);
+      init(sh.sc_empty[i], 16);
     }
     init(sh.q_full, 4);
     init(sh.q_empty, 1);
@@ -319,13 +360,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     init(sh.done[1], 1);
     for (int i = 0; i < kSegRing; ++i) {
       init(sh.seg_full[i], 1);
-      init(sh.seg_empty[i], 19);
+      init(sh.seg_empty[i], 28);
     }
     ptx::fence_mbarrier_init();
     sh.b0 = 0;
     sh.ub0 = 0;
   }
-  if (warp == 17) tc::alloc(ptx::smem_addr(&sh.tmem), kTmemCols);
+  if (warp == kCopyWarp) tc::alloc(ptx::smem_addr(&sh.tmem), kTmemCols);
 
   // Units of all requests, and where this CTA's begin.
   long long u0, u1, chunk;
@@ -381,53 +422,52 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const Segment* s = &sh.seg[n % kSegRing];
     return wait.dead || s->tile1 < 0 ? nullptr : s;
   };
+  // bytes of a buffer of P
+  auto p_stride = [&](const Mode& mode) { return (mode.buffers == 4 ? min(a.rows, 32) : kAttnRows) * (kTile * 2); };
   auto leave = [&](int n) { warp_arrive(sh.seg_empty[n % kSegRing]); };
 
-  if (warp < 8) {
+  if (warp < kValueWarp) {
     // ------------------------------------------------------------ softmax
-    // A thread has one position and the rows of its group.
-    tc::more_registers<kRegsSoftmax>();
-    const int grp = warp >> 2, t_in = tid & 127;
+    // A thread has one position and the 16 rows of its group.
+    const int grp = warp >> 2, t_in = tid & 127, page = t_in >> a.bs_log2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int page = t_in >> a.bs_log2;
-    float x[kHalfRows], l[kHalfRows];
+    float x[kGroupRows], l[kGroupRows];
     const float4* col = reinterpret_cast<const float4*>(sh.col[grp]);
+    Turns turns;
     int k0 = 0;  // tiles of the segments before
     for (int n_seg = 0;; ++n_seg) {
       const Segment* seg = segment(n_seg);
       // (and the last segment's rows are no longer read)
       if (named_any(1 + grp, 128, seg == nullptr)) break;
       const int par = n_seg & 1;
-      const bool by_rows = seg->rows > kHalfRows;
-      const int step = by_rows ? 1 : 2;
-      // groups of 8 rows, and the first row
-      const int eights = by_rows ? (seg->rows + 15) / 16 : (seg->rows + 15) / 16 * 2;
-      const int r0 = by_rows ? grp * eights * 8 : 0;
+      const Mode mode(seg->rows);
+      const int part = grp & (kGroups / mode.by_tile - 1);  // of the rows
+      const int turn = mode.by_tile == 1 ? 0 : (mode.by_tile == 2 ? grp >> 1 : grp);
+      const int r0 = part * kGroupRows;
+      const uint32_t weight = mode.weight(part);
       const int tiles = seg->tile1 - seg->tile0, len = seg->len;
       const int all_see = seg->kv + seg->row0 / G;  // last position that all rows attend to
-      int pos0 = seg->tile0 * kTile;
-      const uint32_t o_at = tmem + lanes + (2 + par) * kAttnRows + (by_rows ? r0 : grp * kHalfRows);
+      const int pos_first = seg->tile0 * kTile;
+      const uint32_t o_at = tmem + lanes + (2 + par) * kAttnRows + turn * mode.o_cols() + r0;
       float vref = 1.f, vinv = 1.f;
 #pragma unroll
-      for (int r = 0; r < kHalfRows; ++r) l[r] = 0.f;
+      for (int r = 0; r < kGroupRows; ++r) l[r] = 0.f;
       wait(sh.meta_full[par], (n_seg >> 1) & 1);
-      if (t_in < eights * 8) sh.col[grp][t_in] = make_float2(sh.qs[par][r0 + t_in], 0.f);
+      if (t_in < kGroupRows) sh.col[grp][t_in] = make_float2(sh.qs[par][r0 + t_in], 0.f);
       named_barrier(1 + grp, 128);
       bool first = true;
-      // by tiles: those whose number is of the group's parity
-      int i = by_rows ? 0 : ((k0 ^ grp) & 1);
-      pos0 += i * kTile;
-      for (; i < tiles; i += step, pos0 += step * kTile) {
-        const int k = k0 + i, pos = pos0 + t_in;
+      for (int i = part < mode.m ? turn : tiles; i < tiles; i += mode.by_tile) {
+        const int k = k0 + i, buf = mode.buffer(i), pos0 = pos_first + i * kTile, pos = pos0 + t_in;
+        const uint32_t phase = turns.of(mode, i);
         const bool masked = pos0 + kTile - 1 > all_see || pos0 + kTile > len;
         const ScaleEntry& sc = sh.scales[k % kScaleRing];
         wait(sh.sc_full[k % kScaleRing], (k / kScaleRing) & 1);
         const float ks = sc.ks[page], vs = sc.vs[page], vmax = sc.vmax;
-        warp_arrive(sh.sc_empty[k % kScaleRing], step);
-        bool renew = first;
-        wait(sh.s_full[k & 1], (k >> 1) & 1);
+        warp_arrive(sh.sc_empty[k % kScaleRing], weight);
+        wait(sh.s_full[buf], phase);
         tc::fence_after();
-        const uint32_t s_at = tmem + lanes + (k & 1) * kAttnRows + r0;
+        const uint32_t s_at = tmem + lanes + buf * mode.s_cols() + r0;
+        bool renew = first;
         for (;;) {
           if (renew) {
             // New references: the rows' largest scores so far, and the largest
@@ -438,24 +478,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               vinv = 1.f / vref;
             }
 #pragma unroll 1
-            for (int c = 0; c < eights; ++c) {
+            for (int c = 0; c < kGroupRows; c += 8) {
               float v[8], mine = -INFINITY;
-              tc::ld8(s_at + c * 8, v);
+              tc::ld8(s_at + c, v);
               tc::wait_ld();
               tc::ready(v);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                float y = v[e] * ks * sh.col[grp][c * 8 + e].x;
-                if (masked && pos > sh.limit[par][r0 + c * 8 + e]) y = -INFINITY;
+                float y = v[e] * ks * sh.col[grp][c + e].x;
+                if (masked && pos > sh.limit[par][r0 + c + e]) y = -INFINITY;
                 y = tc::warp_max(y);
                 if (lane == e) mine = y;
               }
-              if (lane < 8) sh.wmax[grp][warp & 3][c * 8 + lane] = mine;
+              if (lane < 8) sh.wmax[grp][warp & 3][c + lane] = mine;
             }
-            if (!first) wait(sh.pv_done[(k - step) & 1], ((k - step) >> 1) & 1);  // O rests
+            if (!first) wait(sh.pv_done[mode.buffer(i - mode.by_tile)], turns.of(mode, i - mode.by_tile));  // O rests
             tc::fence_after();
             named_barrier(1 + grp, 128);
-            if (t_in < eights * 8) {
+            if (t_in < kGroupRows) {
               const float m = fmaxf(fmaxf(sh.wmax[grp][0][t_in], sh.wmax[grp][1][t_in]),
                                     fmaxf(sh.wmax[grp][2][t_in], sh.wmax[grp][3][t_in]));
               const float was = sh.col[grp][t_in].y;
@@ -466,97 +506,85 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             named_barrier(1 + grp, 128);
             if (!first) {
 #pragma unroll
-              for (int r = 0; r < kHalfRows; ++r)
-                if (r < eights * 8) l[r] *= sh.fac[grp][r];
+              for (int r = 0; r < kGroupRows; ++r) l[r] *= sh.fac[grp][r];
               const float v_ratio = vref_was * vinv;
 #pragma unroll 1
-              for (int c = 0; c < eights; ++c) {
+              for (int c = 0; c < kGroupRows; c += 8) {
                 float o[8];
-                tc::ld8(o_at + c * 8, o);
+                tc::ld8(o_at + c, o);
                 tc::wait_ld();
                 tc::ready(o);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] *= sh.fac[grp][c * 8 + e] * v_ratio;
-                tc::st8(o_at + c * 8, o);
+                for (int e = 0; e < 8; ++e) o[e] *= sh.fac[grp][c + e] * v_ratio;
+                tc::st8(o_at + c, o);
               }
               tc::wait_st();
               tc::fence_before();
             }
           }
           // scores over the rows' references
-#pragma unroll
-          for (int c = 0; c < kHalfRows / 8; ++c)
-            if (c < eights) tc::ld8(s_at + c * 8, x + c * 8);
+          tc::ld8(s_at, x);
+          tc::ld8(s_at + 8, x + 8);
           tc::wait_ld();
-          float top = -INFINITY;
+          tc::ready(x);
+          tc::ready(x + 8);
 #pragma unroll
-          for (int c = 0; c < kHalfRows / 8; ++c) {
-            if (c >= eights) break;
-            tc::ready(x + c * 8);
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const int r = c * 8 + e;
-              const float4 w = col[r >> 1];
-              x[r] = fmaf(x[r] * ks, w.x, -w.y);
-              x[r + 1] = fmaf(x[r + 1] * ks, w.z, -w.w);
-            }
-            if (masked) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (pos > sh.limit[par][r0 + c * 8 + e]) x[c * 8 + e] = -INFINITY;
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, x[c * 8 + e]);
+          for (int r = 0; r < kGroupRows; r += 2) {
+            const float4 w = col[r >> 1];
+            x[r] = fmaf(x[r] * ks, w.x, -w.y);
+            x[r + 1] = fmaf(x[r + 1] * ks, w.z, -w.w);
           }
+          if (masked) {
+#pragma unroll
+            for (int r = 0; r < kGroupRows; ++r)
+              if (pos > sh.limit[par][r0 + r]) x[r] = -INFINITY;
+          }
+          float top[2] = {x[0], x[1]};
+#pragma unroll
+          for (int r = 2; r < kGroupRows; ++r) top[r & 1] = fmaxf(top[r & 1], x[r]);
           // does P stay within f16 (and the sum within 32 bits)?
-          if (renew || !named_any(1 + grp, 128, top > fminf(kSlack - __log2f(vs * vinv), 60.f) || vmax > 4.f * vref)) break;
+          const bool over = fmaxf(top[0], top[1]) > fminf(kSlack - __log2f(vs * vinv), 60.f) || vmax > 4.f * vref;
+          if (renew || !named_any(1 + grp, 128, over)) break;
           renew = true;
         }
-        const float vr = vs * vinv * kPScale;
         tc::fence_before();
-        warp_arrive(sh.s_empty[k & 1], step);
+        warp_arrive(sh.s_empty[buf], weight);
         first = false;
-        if (k >= 2) wait(sh.pv_done[k & 1], ((k >> 1) - 1) & 1);
+        const float vr = vs * vinv * kPScale;
         // probabilities
-        unsigned char* p = p_at + (k & 1) * L::p_bytes(a.rows) + (r0 / 8) * (16 * kTile) + t_in * 16;
+        uint32_t w[kGroupRows / 2];
 #pragma unroll
-        for (int c = 0; c < kHalfRows / 8; ++c) {
-          if (c >= eights) break;
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const int r = c * 8 + e;
-            const float p0 = tc::ex2(x[r]), p1 = tc::ex2(x[r + 1]);
-            l[r] += p0;
-            l[r + 1] += p1;
-            w[e >> 1] = tc::f16x2(p0 * vr, p1 * vr);
-          }
-          *reinterpret_cast<uint4*>(p + c * (16 * kTile)) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int r = 0; r < kGroupRows; r += 2) {
+          const float p0 = tc::ex2(x[r]), p1 = tc::ex2(x[r + 1]);
+          l[r] += p0;
+          l[r + 1] += p1;
+          w[r >> 1] = tc::f16x2(p0 * vr, p1 * vr);
         }
+        wait(sh.pv_done[buf], phase ^ 1);
+        unsigned char* p = p_at + buf * p_stride(mode) + (r0 / 8) * (16 * kTile) + t_in * 16;
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(p + 16 * kTile) = make_uint4(w[4], w[5], w[6], w[7]);
         tc::fence_smem();
-        warp_arrive(sh.p_full[k & 1], step);
+        warp_arrive(sh.p_full[buf], weight);
       }
       k0 += tiles;
+      turns.pass(mode, tiles);
       // sums and references for the output warps
-#pragma unroll
-      for (int c = 0; c < kHalfRows / 8; ++c) {
-        if (c >= eights) break;
-        const float s = warp_sums8(l + c * 8);
-        if ((lane & 3) == 0) sh.lsum[par][warp][c * 8 + (lane >> 2)] = s;
-      }
-      if (t_in < eights * 8) sh.mrun[par][grp][t_in] = sh.col[grp][t_in].y;
+      const float s = warp_sums16(l);
+      if ((lane & 1) == 0) sh.lsum[par][grp][warp & 3][lane >> 1] = s;
+      if (t_in < kGroupRows) sh.mrun[par][grp][t_in] = sh.col[grp][t_in].y;
       if (t_in == 0) sh.vref[par][grp] = vref / kPScale;
       warp_arrive(sh.l_full[par]);
       leave(n_seg);
     }
-  } else if (warp < 12) {
+  } else if (warp < kOutputWarp) {
     // ------------------------------------------------------------ V to f16
     // A thread has one position.  Values past the last position are no numbers
     // of the request's: zeros.  New positions are not seen by all rows: their
     // NaN leave the product, where 0 times NaN would spoil rows that do not
     // see them, and are noted for the output.
     tc::fewer_registers<kRegsValues>();
-    const int t_in = tid - 256;
+    const int t_in = tid - 32 * kValueWarp;
     int k = 0, slot = 0, round = 0;
     for (int n_seg = 0;; ++n_seg) {
       const Segment* seg = segment(n_seg);
@@ -592,7 +620,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
           }
         }
-        if (k >= 2) wait(sh.pv_done[k & 1], ((k >> 1) - 1) & 1);
+        if (k >= 2) wait(sh.f_empty[k & 1], ((k >> 1) - 1) & 1);
         // rows of 64 values (128 bytes), swizzled; the two halves of D one after the other
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
@@ -608,10 +636,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       warp_arrive(sh.l_full[par]);
       leave(n_seg);
     }
-  } else if (warp < 16) {
+  } else if (warp < kCopyWarp) {
     // ------------------------------------------------------------- Q and O
-    tc::fewer_registers<kRegsOutput>();
-    const int ot = tid - 384, ow = ot >> 5;
+    tc::more_registers<kRegsOutput>();
+    const int ot = tid - 32 * kOutputWarp, ow = ot >> 5;
     const int d = D == 128 ? ot : 16 * ow + (lane & 15);
     const bool owns = D == 128 || lane < 16;
     constexpr int kVec = D / 16;  // 16-byte loads of half a row
@@ -683,7 +711,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       store_q(*nxt, 0);
     }
     for (int n_seg = 0;; ++n_seg) {
-      if (named_any(3, 128, nxt == nullptr)) break;
+      if (named_any(5, 128, nxt == nullptr)) break;
       const int par = n_seg & 1;
       const Segment seg = *nxt;
       nxt = segment(n_seg + 1);
@@ -693,33 +721,37 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         store_q(*nxt, par ^ 1);
       }
       wait(sh.l_full[par], (n_seg >> 1) & 1);
-      const bool by_rows = seg.rows > kHalfRows;
+      const Mode mode(seg.rows);
       const bool whole = seg.tile0 == 0 && seg.tile1 == seg.tiles;
       if (ot < seg.rows) {
         // a group whose sum is 0 has nothing, whatever its reference and O
-        const int half_rows = by_rows ? (seg.rows + 15) / 16 * 8 : kAttnRows;
-        const int r = ot % half_rows, own_grp = ot / half_rows;
-        float s[2] = {0.f, 0.f}, m[2] = {0.f, 0.f}, M = -INFINITY;
+        const int r = ot % kGroupRows, part = ot / kGroupRows, parts = kGroups / mode.by_tile;
+        float s[kGroups], M = -INFINITY, f[kGroups], sum = 0.f;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          if (by_rows && g != own_grp) continue;
+        for (int j = 0; j < kGroups; ++j) {
+          s[j] = 0.f;
+          const int g = j * parts + part;  // of turn j
+          if (j < mode.by_tile) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) s[g] += sh.lsum[par][g * 4 + w][r];
-          m[g] = sh.mrun[par][g][r];
-          if (s[g] != 0.f) M = fmaxf(M, m[g]);
+            for (int w = 0; w < 4; ++w) s[j] += sh.lsum[par][g][w][r];
+            if (s[j] != 0.f) M = fmaxf(M, sh.mrun[par][g][r]);
+          }
         }
-        float f[2], sum = 0.f;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const float w = s[g] != 0.f ? tc::ex2(m[g] - M) : 0.f;
-          sum += w * s[g];
-          f[g] = s[g] != 0.f ? w * sh.vref[par][g] : 0.f;
+        for (int j = 0; j < kGroups; ++j) {
+          f[j] = 0.f;
+          const int g = j * parts + part;
+          if (s[j] != 0.f) {
+            const float w = tc::ex2(sh.mrun[par][g][r] - M);
+            sum += w * s[j];
+            f[j] = w * sh.vref[par][g];
+          }
         }
-        if (by_rows) f[0] += f[1];  // one of them
         if (whole) sum = sum == 0.f ? 0.f : 1.f / sum;
-        sh.fin[ot] = make_float4(f[0], f[1], sum, M);
+        sh.of[ot] = make_float4(f[0], f[1], f[2], f[3]);
+        sh.fin[ot] = make_float2(sum, M);
       }
-      named_barrier(3, 128);
+      named_barrier(5, 128);
       wait(sh.o_full[par], (n_seg >> 1) & 1);
       tc::fence_after();
       const int nan_at = sh.nanpos[par][d];
@@ -729,25 +761,37 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       int tok = seg.row0 / G, g = seg.row0 % G;  // of row r
       __nv_bfloat16* dst = a.out + (static_cast<long long>(seg.q0 + tok) * a.Hq + seg.h * G + g) * D + d;
       const long long next_tok = static_cast<long long>(a.Hq - (G - 1)) * D;  // from a token's last head to the next's first
-      for (int c = 0; c * 8 < seg.rows; ++c) {
-        float o[8], o2[8];
-        tc::ld8(o_at + c * 8, o);
-        if (!by_rows) tc::ld8(o_at + kHalfRows + c * 8, o2);
+      for (int c = 0; c < seg.rows; c += 8) {
+        float o[8];
+        tc::ld8(o_at + c, o);
         tc::wait_ld();
         tc::ready(o);
-        if (!by_rows) tc::ready(o2);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int r = c * 8 + e;
-          if (r < seg.rows) {
-            const float4 f = sh.fin[r];
-            float v = f.x != 0.f ? o[e] * f.x : 0.f;
-            if (!by_rows && f.y != 0.f) v = fmaf(o2[e], f.y, v);
+          const float f = sh.of[c + e].x;
+          o[e] = f != 0.f ? o[e] * f : 0.f;
+        }
+#pragma unroll 1
+        for (int j = 1; j < mode.by_tile; ++j) {
+          float y[8];
+          tc::ld8(o_at + j * mode.o_cols() + c, y);
+          tc::wait_ld();
+          tc::ready(y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float f = reinterpret_cast<const float*>(&sh.of[c + e])[j];
+            if (f != 0.f) o[e] = fmaf(y[e], f, o[e]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (c + e < seg.rows) {
+            float v = o[e];
             if (nan_at <= seg.kv + tok) v = __uint_as_float(0x7FFFFFFFu);
             if (whole) {
-              if (owns) *dst = __float2bfloat16_rn(v * f.z);
+              if (owns) *dst = __float2bfloat16_rn(v * sh.fin[c + e].x);
             } else if (owns) {
-              rec[r * D + d] = v;
+              rec[(c + e) * D + d] = v;
             }
             if (++g == G) {
               g = 0;
@@ -763,15 +807,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       warp_arrive(sh.o_empty[par]);
       if (!whole) {
         if (ot < seg.rows) {
-          rec[kAttnRows * 128 + ot] = sh.fin[ot].w;
-          rec[kAttnRows * 128 + kAttnRows + ot] = sh.fin[ot].z;
+          rec[kAttnRows * 128 + ot] = sh.fin[ot].y;
+          rec[kAttnRows * 128 + kAttnRows + ot] = sh.fin[ot].x;
         }
         // the last of the item's CTAs joins the parts
         const long long c0 = seg.first / chunk, c1 = (seg.first + seg.tiles - 1) / chunk;
         __threadfence();
-        named_barrier(3, 128);
+        named_barrier(5, 128);
         if (ot == 0) sh.last = ptx::atom_add_acq_rel(a.counters + c0, 1u) == static_cast<uint32_t>(c1 - c0);
-        named_barrier(3, 128);
+        named_barrier(5, 128);
         if (sh.last) {
           __threadfence();
           const int pieces = static_cast<int>(c1 - c0) + 1;
@@ -814,24 +858,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 for (int i = 0; i < E; ++i) acc[j][i] *= f;
               }
               const int here = min(32, pieces - p0);
-#pragma unroll 2
+#pragma unroll 4
               for (int p = 0; p < here; ++p) {
                 const float* y = record(p0 + p) + (r4 + ow) * D + lane * E;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                   const float wp = __shfl_sync(0xFFFFFFFFu, w[j], p);
-                  if (r4 + ow + 4 * j < seg.rows) {
-                    float v[E];
-                    if constexpr (D == 128) {
-                      const float4 z = __ldcg(reinterpret_cast<const float4*>(y + 4 * j * D));
-                      v[0] = z.x, v[1] = z.y, v[2] = z.z, v[3] = z.w;
-                    } else {
-                      const float2 z = __ldcg(reinterpret_cast<const float2*>(y + 4 * j * D));
-                      v[0] = z.x, v[1] = z.y;
-                    }
-#pragma unroll
-                    for (int i = 0; i < E; ++i) acc[j][i] = fmaf(wp, v[i], acc[j][i]);
+                  float v[E];  // (rows past the last are there, and not written)
+                  if constexpr (D == 128) {
+                    const float4 z = __ldcg(reinterpret_cast<const float4*>(y + 4 * j * D));
+                    v[0] = z.x, v[1] = z.y, v[2] = z.z, v[3] = z.w;
+                  } else {
+                    const float2 z = __ldcg(reinterpret_cast<const float2*>(y + 4 * j * D));
+                    v[0] = z.x, v[1] = z.y;
                   }
+#pragma unroll
+                  for (int i = 0; i < E; ++i) acc[j][i] = fmaf(wp, v[i], acc[j][i]);
                 }
               }
             }
@@ -856,127 +898,134 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
   } else {
     tc::fewer_registers<kRegsRest>();
-    if (warp == 16) {
-    // ------------------------------------------------------------- copies
-    // A lane holds a block: 32 block ids, then their scales, are loaded at a
-    // time, a batch of whole tiles ahead of the one in use.
-    struct Batch {
-      int h, tiles, pages;  // tiles of the batch, blocks of its segment from its first on
-      int id;
-      float ks, vs;
-    } now, nxt;
-    const int pages_per_tile = kTile >> a.bs_log2;
-    int n_seg = -1, tile = 0, tile_end = 0, seg_b = 0, seg_h = 0, seg_pages = 0;
-    bool more = true;
-    const int per_batch = 32 / pages_per_tile;
-    auto load_ids = [&](Batch& x) {
-      x.tiles = 0;
-      if (tile >= tile_end) {
-        if (n_seg >= 0 && more) leave(n_seg);
-        const Segment* s = more ? segment(++n_seg) : nullptr;
-        if (s == nullptr) {
-          more = false;
-          return;
+    if (warp == kCopyWarp || warp == kCopyWarp + 3) {
+      // ------------------------------------------------------------- copies
+      // A lane holds a block: 32 block ids, then their scales, are loaded at a
+      // time, a batch of whole tiles ahead of the one in use.
+      struct Batch {
+        int h, tiles, pages;  // tiles of the batch, blocks of its segment from its first on
+        int id;
+        float scale;
+      } now, nxt;
+      const bool is_v = warp != kCopyWarp;
+      const float* scales = is_v ? a.v_scale : a.k_scale;
+      const CUtensorMap* map = is_v ? &v_map : &k_map;
+      unsigned char* tiles = is_v ? v_tiles : k_tiles;
+      uint64_t* full = is_v ? sh.v_full : sh.k_full;
+      uint64_t* empty = is_v ? sh.v_empty : sh.k_empty;
+      const int pages_log2 = 7 - a.bs_log2, pages_per_tile = 1 << pages_log2;
+      int n_seg = -1, tile = 0, tile_end = 0, seg_b = 0, seg_h = 0, seg_pages = 0;
+      bool more = true;
+      auto load_ids = [&](Batch& x) {
+        x.tiles = 0;
+        if (tile >= tile_end) {
+          if (n_seg >= 0 && more) leave(n_seg);
+          const Segment* s = more ? segment(++n_seg) : nullptr;
+          if (s == nullptr) {
+            more = false;
+            return;
+          }
+          tile = s->tile0;
+          tile_end = s->tile1;
+          seg_b = s->b;
+          seg_h = s->h;
+          seg_pages = (s->len + a.bs - 1) >> a.bs_log2;
         }
-        tile = s->tile0;
-        tile_end = s->tile1;
-        seg_b = s->b;
-        seg_h = s->h;
-        seg_pages = (s->len + a.bs - 1) >> a.bs_log2;
-      }
-      x.tiles = min(per_batch, tile_end - tile);
-      x.h = seg_h;
-      const int page0 = tile * pages_per_tile;
-      x.pages = max(0, seg_pages - page0);
-      x.id = -1;
-      if (lane < x.pages && lane < x.tiles * pages_per_tile)
-        x.id = __ldg(a.table + static_cast<long long>(seg_b) * a.max_blocks + page0 + lane);
-      tile += x.tiles;
-    };
-    auto load_scales = [&](Batch& x) {
-      x.ks = x.vs = 0.f;
-      if (x.tiles > 0 && x.id >= 0 && x.id < a.num_blocks) {
-        x.ks = __ldg(a.k_scale + static_cast<long long>(x.id) * a.H + x.h);
-        x.vs = __ldg(a.v_scale + static_cast<long long>(x.id) * a.H + x.h);
-      }
-    };
-    if (lane == 0) {
-      tc::prefetch_map(&k_map);
-      tc::prefetch_map(&v_map);
-    }
-    load_ids(now);
-    load_scales(now);
-    int slot = 0, round = 0, k = 0;
-    while (now.tiles > 0) {
-      load_ids(nxt);
-      for (int i = 0; i < now.tiles; ++i, ++k) {
-        const int pages = max(0, min(pages_per_tile, now.pages - i * pages_per_tile));
-        const int src = (i * pages_per_tile + lane) & 31;
-        const int id = __shfl_sync(0xFFFFFFFFu, now.id, src);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          if (round > 0) wait(kv ? sh.v_empty[slot] : sh.k_empty[slot], (round - 1) & 1);
-          const uint32_t bar = ptx::smem_addr(kv ? &sh.v_full[slot] : &sh.k_full[slot]);
-          if (lane == 0) ptx::mbar_arrive_expect_tx(bar, pages * a.bs * D);
+        x.tiles = min(32 >> pages_log2, tile_end - tile);
+        x.h = seg_h;
+        const int page0 = tile << pages_log2;
+        x.pages = max(0, seg_pages - page0);
+        x.id = -1;
+        if (lane < x.pages && lane < x.tiles << pages_log2)
+          x.id = __ldg(a.table + static_cast<long long>(seg_b) * a.max_blocks + page0 + lane);
+        tile += x.tiles;
+      };
+      auto load_scales = [&](Batch& x) {
+        x.scale = 0.f;
+        if (x.tiles > 0 && x.id >= 0 && x.id < a.num_blocks) x.scale = __ldg(scales + static_cast<long long>(x.id) * a.H + x.h);
+      };
+      if (lane == 0) tc::prefetch_map(map);
+      load_ids(now);
+      load_scales(now);
+      int slot = 0, round = 0, k = 0;
+      while (now.tiles > 0) {
+        load_ids(nxt);
+        for (int i = 0; i < now.tiles; ++i, ++k) {
+          const int first = i << pages_log2;
+          const int pages = max(0, min(pages_per_tile, now.pages - first));
+          if (round > 0) wait(empty[slot], (round - 1) & 1);
+          const uint32_t bar = ptx::smem_addr(&full[slot]);
+          const uint32_t dst = ptx::smem_addr(tiles + slot * L::kTileBytes);
+          if (tc::elect()) ptx::mbar_arrive_expect_tx(bar, pages * a.bs * D);
           __syncwarp();
-          if (lane < pages)
-            tc::load_4d(ptx::smem_addr((kv ? v_tiles : k_tiles) + slot * L::kTileBytes + lane * a.bs * D),
-                        kv ? &v_map : &k_map, 0, 0, now.h, id, bar);
+          for (int j = 0; j < pages; ++j) {
+            const int id = __shfl_sync(0xFFFFFFFFu, now.id, first + j);
+            if (tc::elect()) tc::load_4d(dst + j * a.bs * D, map, 0, 0, now.h, id, bar);
+          }
+          __syncwarp();
+          if (++slot == a.ring) slot = 0, ++round;
+          if (i == 0) load_scales(nxt);  // its ids have had a tile's time
+          const int sr = k % kScaleRing;
+          if (k >= kScaleRing) wait(sh.sc_empty[sr], (k / kScaleRing - 1) & 1);
+          const float scale = __shfl_sync(0xFFFFFFFFu, now.scale, (first + lane) & 31);
+          if (is_v) {
+            const float vmax = tc::warp_max(lane < pages_per_tile ? scale : 0.f);
+            if (lane == 0) sh.scales[sr].vmax = vmax;
+          }
+          if (lane < pages_per_tile) (is_v ? sh.scales[sr].vs : sh.scales[sr].ks)[lane] = is_v ? scale : scale * a.scale_log2e;
+          warp_arrive(sh.sc_full[sr]);
         }
-        if (++slot == a.ring) slot = 0, ++round;
-        if (i == 0) load_scales(nxt);  // its ids have had a tile's time
-        const int sr = k % kScaleRing;
-        if (k >= kScaleRing) wait(sh.sc_empty[sr], (k / kScaleRing - 1) & 1);
-        const float ks = __shfl_sync(0xFFFFFFFFu, now.ks, src), vs = __shfl_sync(0xFFFFFFFFu, now.vs, src);
-        const float vmax = tc::warp_max(lane < pages_per_tile ? vs : 0.f);
-        if (lane < pages_per_tile) {
-          sh.scales[sr].ks[lane] = ks * a.scale_log2e;
-          sh.scales[sr].vs[lane] = vs;
-        }
-        if (lane == 0) sh.scales[sr].vmax = vmax;
-        warp_arrive(sh.sc_full[sr]);
+        now = nxt;
       }
-      now = nxt;
-    }
-    // no copy is in flight when the CTA ends: every slot used has been filled
-    Waiter drain;
-    const int used = round > 0 ? a.ring : slot;
-    for (int i = 0; i < used; ++i) {
-      drain(sh.k_full[i], (i < slot ? round : round - 1) & 1);
-      drain(sh.v_full[i], (i < slot ? round : round - 1) & 1);
-    }
-    wait.dead |= drain.dead;
-    } else if (warp == 17) {
+      // no copy is in flight when the CTA ends: every slot used has been filled
+      Waiter drain;
+      const int used = round > 0 ? a.ring : slot;
+      for (int i = 0; i < used; ++i) drain(full[i], (i < slot ? round : round - 1) & 1);
+      wait.dead |= drain.dead;
+    } else if (warp == kCopyWarp + 1) {
       // --------------------------------------------------- first products
       const uint64_t swz = D == 128 ? tc::kSwizzle128 : tc::kSwizzle64;
       const uint64_t kd0 = tc::smem_desc(ptx::smem_addr(k_tiles), 16, 8 * D, swz);
       const uint64_t qd0 = tc::smem_desc(ptx::smem_addr(q_hi), 128, 8 * D, tc::kSwizzleNone);
       const uint64_t qd1 = tc::smem_desc(ptx::smem_addr(q_lo), 128, 8 * D, tc::kSwizzleNone);
-      int k = 0, slot = 0, round = 0;
+      int slot = 0, round = 0, buffers = 0;
+      Turns turns;
       for (int n_seg = 0;; ++n_seg) {
         const Segment* seg = segment(n_seg);
         if (seg == nullptr) break;
-        const uint32_t is = tc::instr(kTile, (seg->rows + 15) / 16 * 16, false, false);
+        const Mode mode(seg->rows);
+        const uint32_t is = tc::instr(kTile, 16 * mode.m, false, false);
         const int tiles = seg->tile1 - seg->tile0;
+        if (mode.buffers != buffers) {
+          // the buffers lie elsewhere now: none is in use (P is not written
+          // before scores are there)
+          for (int b = 0; b < 4; ++b) {
+            wait(sh.s_empty[b], (turns.bits >> b & 1) ^ 1);
+            wait(sh.pv_done[b], (turns.bits >> b & 1) ^ 1);
+          }
+          buffers = mode.buffers;
+        }
         wait(sh.q_full, n_seg & 1);
-        for (int i = 0; i < tiles; ++i, ++k) {
+        for (int i = 0; i < tiles; ++i) {
           const uint64_t kd = kd0 + slot * (L::kTileBytes / 16);
-          const uint32_t dst = tmem + (k & 1) * kAttnRows;
+          const int buf = mode.buffer(i);
+          const uint32_t dst = tmem + buf * mode.s_cols();
           wait(sh.k_full[slot], round & 1);
-          if (k >= 2) wait(sh.s_empty[k & 1], ((k >> 1) - 1) & 1);
+          wait(sh.s_empty[buf], turns.of(mode, i) ^ 1);
           tc::fence_after();
           if (tc::elect()) {
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) tc::mma_e4m3(dst, kd + j * 2, qd0 + j * 16, is, j > 0);
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) tc::mma_e4m3(dst, kd + j * 2, qd1 + j * 16, is, true);
-            tc::commit(ptx::smem_addr(&sh.s_full[k & 1]));
+            tc::commit(ptx::smem_addr(&sh.s_full[buf]));
             tc::commit(ptx::smem_addr(&sh.k_empty[slot]));
             if (i + 1 == tiles) tc::commit(ptx::smem_addr(&sh.q_empty));
           }
           __syncwarp();
           if (++slot == a.ring) slot = 0, ++round;
         }
+        turns.pass(mode, tiles);
         leave(n_seg);
       }
       // all products are done before the tensor memory goes back
@@ -985,60 +1034,68 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       __syncwarp();
       drain(sh.done[0], 0);
       wait.dead |= drain.dead;
-    } else if (warp == 18) {
+    } else {
       // -------------------------------------------------- second products
       const uint64_t vd0 = tc::smem_desc(ptx::smem_addr(v_half), kTile * 128, 1024, tc::kSwizzle128);
       const uint64_t pd0 = tc::smem_desc(ptx::smem_addr(p_at), 128, 16 * kTile, tc::kSwizzleNone);
+      Walker walk(a, u0, u1, sh.b0, sh.ub0);
+      int listed = 0;
+      bool more = true;
+      auto list = [&]() {  // one more segment, or the list's end
+        if (!more) return;
+        const int n = listed++;
+        if (n >= kSegRing) wait(sh.seg_empty[n % kSegRing], (n / kSegRing - 1) & 1);
+        Segment s;
+        more = walk.next(s);
+        if (!more) s.tile1 = -1;
+        if (lane == 0) sh.seg[n % kSegRing] = s;
+        warp_arrive(sh.seg_full[n % kSegRing]);
+      };
+      for (int i = 0; i < kSegAhead; ++i) list();
+      Turns turns;
       int k = 0;
       for (int n_seg = 0;; ++n_seg) {
         const Segment* seg = segment(n_seg);
         if (seg == nullptr) break;
         const int par = n_seg & 1;
-        const bool by_rows = seg->rows > kHalfRows;
-        const uint32_t io = tc::instr(D, (seg->rows + 15) / 16 * 16, true, true);
+        const Mode mode(seg->rows);
+        const uint32_t io = tc::instr(D, 16 * mode.m, true, true);
         const int tiles = seg->tile1 - seg->tile0;
         if (n_seg >= 2) wait(sh.o_empty[par], ((n_seg >> 1) - 1) & 1);
         for (int i = 0; i < tiles; ++i, ++k) {
+          const int buf = mode.buffer(i);
           const uint64_t vd = vd0 + (k & 1) * (L::kHalfBytes / 16);
-          const uint64_t pd = pd0 + (k & 1) * (L::p_bytes(a.rows) / 16);
-          const uint32_t dst = tmem + (2 + par) * kAttnRows + (by_rows ? 0 : (k & 1) * kHalfRows);
-          const bool add = i >= (by_rows ? 1 : 2);
+          const uint64_t pd = pd0 + buf * (p_stride(mode) / 16);
+          const uint32_t dst = tmem + (2 + par) * kAttnRows + (i & (mode.by_tile - 1)) * mode.o_cols();
+          const bool add = i >= mode.by_tile;
           wait(sh.f_full[k & 1], (k >> 1) & 1);
-          wait(sh.p_full[k & 1], (k >> 1) & 1);
+          wait(sh.p_full[buf], turns.of(mode, i));
           tc::fence_after();
           if (tc::elect()) {
 #pragma unroll
             for (int j = 0; j < kTile / 16; ++j) tc::mma_f16(dst, vd + j * 128, pd + j * 16, io, add || j > 0);
-            tc::commit(ptx::smem_addr(&sh.pv_done[k & 1]));
+            tc::commit(ptx::smem_addr(&sh.pv_done[buf]));
+            tc::commit(ptx::smem_addr(&sh.f_empty[k & 1]));
             if (i + 1 == tiles) tc::commit(ptx::smem_addr(&sh.o_full[par]));
           }
           __syncwarp();
         }
+        turns.pass(mode, tiles);
         leave(n_seg);
+        list();
       }
+      while (more) list();  // (only where a wait gave up)
       Waiter drain;
       if (tc::elect()) tc::commit(ptx::smem_addr(&sh.done[1]));
       __syncwarp();
       drain(sh.done[1], 0);
       wait.dead |= drain.dead;
-    } else {
-      // -------------------------------------------------- list of segments
-      Walker walk(a, u0, u1, sh.b0, sh.ub0);
-      for (int n_seg = 0;; ++n_seg) {
-        if (n_seg >= kSegRing) wait(sh.seg_empty[n_seg % kSegRing], (n_seg / kSegRing - 1) & 1);
-        Segment s;
-        const bool more = walk.next(s);
-        if (!more) s.tile1 = -1;
-        if (lane == 0) sh.seg[n_seg % kSegRing] = s;
-        warp_arrive(sh.seg_full[n_seg % kSegRing]);
-        if (!more) break;
-      }
     }
   }
   __syncwarp();
   if (wait.dead) atomicOr(a.err, SPECDEC_DEV_ERR_TIMEOUT);
   __syncthreads();
-  if (warp == 17) tc::dealloc(tmem, kTmemCols);
+  if (warp == kCopyWarp) tc::dealloc(tmem, kTmemCols);
 }
 
 }  // namespace specdec

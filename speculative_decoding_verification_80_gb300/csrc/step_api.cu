@@ -321,7 +321,7 @@ extern "C" specdec_status_t spec_attention(const void* q, int64_t q_token_stride
   // A row group is as long as the call's rows allow: fewer rows leave more
   // shared memory to the tiles in flight.
   const int64_t rows = static_cast<int64_t>(T) * (Hq / H);
-  a.rows = static_cast<int32_t>(rows >= kAttnRows ? kAttnRows : (rows + 15) / 16 * 16);
+  a.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : kAttnRows;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = D == 64 ? launch_attention<64>(a, k_cache, v_cache, st) : launch_attention<128>(a, k_cache, v_cache, st);
   return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;

@@ -96,70 +96,97 @@ constexpr float kSlack = 9.f;
 
 // Part of a (request, head, row group) that one CTA works on.  tile1 < 0 ends
 // the list.
+//
+// How its tiles go over the softmax groups and their buffers goes by m, the
+// 16s of rows: groups of different tiles are 4, 2 or 1 (by_log2), buffers of S
+// and P 4 of up to 32 rows, or 2 (buf_log2).
 struct Segment {
   int b, h, row0, rows;       // rows of this group
   int q0, kv, len;            // first token, positions before it, positions of the group
   int tile0, tile1, tiles;    // tiles of this part, and of the whole
-  long long first;            // unit of the whole's first tile
+  uint32_t first;             // unit of the whole's first tile
+  int m, by_log2, buf_log2;
+  // columns of a buffer of S, and of one of a parity's Os
+  __device__ int s_cols() const { return 128 >> buf_log2; }
+  __device__ int o_cols() const { return kAttnRows >> by_log2; }
+  // Arrivals of a group's warp: all of a tile's make 16.
+  __device__ uint32_t weight(int part) const { return m == 3 ? (part == 0 ? 2 : 1) : (m == 1 ? 4 : m == 2 ? 2 : 1); }
+};
+
+// Parities of four barriers that are used in turn, buffer i % buffers for tile
+// i of a segment; what every role of the CTA knows without asking.
+struct Turns {
+  uint32_t bits = 0;
+  __device__ __forceinline__ uint32_t of(int i, int buf_log2) const {
+    return ((bits >> (i & ((1 << buf_log2) - 1))) ^ static_cast<uint32_t>(i >> buf_log2)) & 1;
+  }
+  __device__ __forceinline__ void pass(int tiles, int buf_log2) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int uses = (tiles + (1 << buf_log2) - 1 - b) >> buf_log2;  // (not past the last buffer)
+      if (b < 1 << buf_log2) bits ^= static_cast<uint32_t>(uses & 1) << b;
+    }
+  }
 };
 
 // Goes through the segments of units [u, end).
 struct Walker {
   const AttnArgs& a;
-  long long u, end, ub;  // ub: first unit of request b
+  uint32_t u, end, ub;  // ub: first unit of request b
+  uint32_t per_head;
   int b, G, q0, q, kv;
-  long long per_head;
 
-  __device__ Walker(const AttnArgs& args, long long u0, long long u1, int b0, long long ub0)
-      : a(args), u(u0), end(u1), ub(ub0), b(b0), G(args.Hq / args.H) {
-    if (u < end) load();
-  }
-  // positions of the row group that ends before row `last`
-  static __device__ int length(const AttnArgs& a, int kv, int G, int row_end) {
+  __device__ Walker(const AttnArgs& args, uint32_t u0, uint32_t u1, int b0, uint32_t ub0)
+      : a(args), u(u0), end(u1), ub(ub0), per_head(0), b(b0 - 1), G(args.Hq / args.H), q0(0), q(0), kv(0) {}
+  // positions of the row group that ends before row `row_end`
+  static __device__ __forceinline__ int length(const AttnArgs& a, int kv, int G, int row_end) {
     const long long n = static_cast<long long>(kv) + (row_end - 1) / G + 1;
-    const long long cap = static_cast<long long>(a.max_blocks) * a.bs;
-    return static_cast<int>(n < 0 ? 0 : (n < cap ? n : cap));
+    return static_cast<int>(max(0LL, min(n, static_cast<long long>(a.max_blocks) << a.bs_log2)));
   }
-  static __device__ int tiles_of(int len) { return len <= 0 ? 1 : (len + kTile - 1) / kTile; }
-  static __device__ long long units_per_head(const AttnArgs& a, int kv, int G, int q) {
-    long long n = 0;
+  static __device__ __forceinline__ int tiles_of(int len) { return max(1, (len + kTile - 1) / kTile); }
+  static __device__ __forceinline__ uint32_t units_per_head(const AttnArgs& a, int kv, int G, int q) {
+    uint32_t n = 0;
+#pragma unroll 1
     for (int r = 0; r < q * G; r += a.rows) n += tiles_of(length(a, kv, G, min(q * G, r + a.rows)));
     return n;
   }
-  static __device__ void request(const AttnArgs& a, int b, int& q0, int& q, int& kv) {
+  static __device__ __forceinline__ void request(const AttnArgs& a, int b, int& q0, int& q, int& kv) {
     q0 = max(0, min(__ldg(a.cu_tokens + b), a.T));
     const int q1 = max(0, min(__ldg(a.cu_tokens + b + 1), a.T));
     q = max(0, q1 - q0);
     kv = __ldg(a.kv_len + b);
   }
-  __device__ void load() {
-    request(a, b, q0, q, kv);
-    per_head = units_per_head(a, kv, G, q);
-  }
   __device__ bool next(Segment& s) {
     if (u >= end) return false;
-    while (u >= ub + per_head * a.H) {
+#pragma unroll 1
+    while (u - ub >= per_head * a.H) {
       ub += per_head * a.H;
       ++b;
-      load();
+      request(a, b, q0, q, kv);
+      per_head = units_per_head(a, kv, G, q);
     }
-    const long long o = u - ub;
+    uint32_t rem = u - ub;
     s.b = b;
-    s.h = static_cast<int>(o / per_head);
-    long long rem = o - s.h * per_head;
+    s.h = static_cast<int>(rem / per_head);
+    rem -= s.h * per_head;
     s.q0 = q0;
     s.kv = kv;
-    for (s.row0 = 0;; s.row0 += a.rows) {
+    s.row0 = 0;
+#pragma unroll 1
+    for (;; s.row0 += a.rows) {
       const int row_end = min(q * G, s.row0 + a.rows);
       s.rows = row_end - s.row0;
       s.len = length(a, kv, G, row_end);
       s.tiles = tiles_of(s.len);
-      if (rem < s.tiles) break;
+      if (rem < static_cast<uint32_t>(s.tiles)) break;
       rem -= s.tiles;
     }
     s.tile0 = static_cast<int>(rem);
-    s.tile1 = static_cast<int>(min(static_cast<long long>(s.tiles), rem + (end - u)));
+    s.tile1 = static_cast<int>(min(static_cast<uint32_t>(s.tiles), rem + (end - u)));
     s.first = u - rem;
+    s.m = (s.rows + 15) / 16;
+    s.by_log2 = s.m == 1 ? 2 : (s.m == 2 ? 1 : 0);
+    s.buf_log2 = s.m <= 2 ? 2 : 1;
     u += s.tile1 - s.tile0;
     return true;
   }
@@ -171,35 +198,6 @@ struct ScaleEntry {
   float vmax;            // the tile's largest
 };
 
-// How the tiles of a segment go over the softmax groups and their buffers.
-struct Mode {
-  int m;        // 16s of rows
-  int by_tile;  // groups of different tiles: 4, 2 or 1
-  int buffers;  // of S and P: 4 of up to 32 rows, or 2
-  __device__ explicit Mode(int rows) : m((rows + 15) / 16) {
-    by_tile = m == 1 ? 4 : (m == 2 ? 2 : 1);
-    buffers = m <= 2 ? 4 : 2;
-  }
-  __device__ int buffer(int i) const { return i & (buffers - 1); }
-  // columns of a buffer of S, and of one of a parity's Os
-  __device__ int s_cols() const { return buffers == 4 ? 32 : 64; }
-  __device__ int o_cols() const { return kAttnRows / by_tile; }
-  // Arrivals of a group's warp: all of a tile's make 16.
-  __device__ uint32_t weight(int part) const { return m == 3 ? (part == 0 ? 2 : 1) : 4 / m; }
-};
-
-// Parities of four barriers that are used in turn, buffer i % buffers for tile
-// i of a segment; what every role of the CTA knows without asking.
-struct Turns {
-  uint32_t bits = 0;
-  __device__ uint32_t of(const Mode& mode, int i) const {
-    return ((bits >> mode.buffer(i)) ^ static_cast<uint32_t>(i / mode.buffers)) & 1;
-  }
-  __device__ void pass(const Mode& mode, int tiles) {
-    for (int b = 0; b < mode.buffers; ++b) bits ^= static_cast<uint32_t>(((tiles + mode.buffers - 1 - b) / mode.buffers) & 1) << b;
-  }
-};
-
 struct AttnShared {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
   uint64_t s_full[4], s_empty[4], p_full[4], pv_done[4], f_full[2], f_empty[2], o_full[2], o_empty[2];
@@ -207,9 +205,9 @@ struct AttnShared {
   uint64_t sc_full[kScaleRing], sc_empty[kScaleRing], seg_full[kSegRing], seg_empty[kSegRing], done[2];
   uint32_t tmem;
   int32_t b0;
-  long long ub0;
+  uint32_t ub0;
   Segment seg[kSegRing];
-  long long part[32];
+  uint32_t part[32];
   alignas(16) float2 col[kGroups][kGroupRows];  // {row scale, reference} of each group's rows
   float wmax[kGroups][4][kGroupRows];  // a warp's largest score of each of its group's rows
   float fac[kGroups][kGroupRows];      // factors from a row's reference to its next
@@ -250,6 +248,7 @@ struct Waiter {
   __device__ __forceinline__ void operator()(const uint64_t& bar, uint32_t parity) {
     if (dead) return;
     const uint32_t at = ptx::smem_addr(&bar);
+#pragma unroll 1
     for (uint32_t n = SPECDEC_ATTN_WAIT_TRIES; !tc::try_wait(at, parity);)
       if (--n == 0) {
         dead = true;
@@ -369,45 +368,45 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (warp == kCopyWarp) tc::alloc(ptx::smem_addr(&sh.tmem), kTmemCols);
 
   // Units of all requests, and where this CTA's begin.
-  long long u0, u1, chunk;
+  uint32_t u0, u1, chunk;
   {
     const int per = (a.B + kAttnThreads - 1) / kAttnThreads;
     const int lo = min(a.B, tid * per), hi = min(a.B, lo + per);
-    long long mine = 0;
-    for (int b = lo; b < hi; ++b) {
-      int q0, q, kv;
-      Walker::request(a, b, q0, q, kv);
-      mine += Walker::units_per_head(a, kv, G, q) * a.H;
-    }
-    long long s = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long o = __shfl_up_sync(0xFFFFFFFFu, s, d);
-      if (lane >= d) s += o;
-    }
-    if (lane == 31) sh.part[warp] = s;
-    __syncthreads();
-    long long before = s - mine, total = 0;
-    for (int w = 0; w < kAttnThreads / 32; ++w) {
-      if (w < warp) before += sh.part[w];
-      total += sh.part[w];
-    }
-    chunk = (total + gridDim.x - 1) / gridDim.x;
-    u0 = min(total, static_cast<long long>(blockIdx.x) * chunk);
-    u1 = min(total, u0 + chunk);
-    if (u0 < u1 && before <= u0 && u0 < before + mine) {  // one thread
-      long long at = before;
+    uint32_t before = 0, mine = 0;
+    // first the sum of this thread's requests, then the request of unit u0
+    // where it is among them
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      uint32_t at = before;
+#pragma unroll 1
       for (int b = lo; b < hi; ++b) {
         int q0, q, kv;
         Walker::request(a, b, q0, q, kv);
-        const long long n = Walker::units_per_head(a, kv, G, q) * a.H;
-        if (u0 < at + n) {
+        const uint32_t n = Walker::units_per_head(a, kv, G, q) * a.H;
+        if (pass == 1 && at <= u0 && u0 < at + n) {
           sh.b0 = b;
           sh.ub0 = at;
-          break;
         }
         at += n;
       }
+      if (pass == 1) break;
+      mine = at;
+      uint32_t s = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, s, d);
+        if (lane >= d) s += o;
+      }
+      if (lane == 31) sh.part[warp] = s;
+      __syncthreads();
+      // a lane for each warp
+      const uint32_t w = lane < kAttnThreads / 32 ? sh.part[lane] : 0;
+      const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, w);
+      before = s - mine + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0);
+      chunk = (total + gridDim.x - 1) / gridDim.x;
+      u0 = min(total, blockIdx.x * chunk);
+      u1 = min(total, u0 + chunk);
+      if (u0 >= u1 || before > u0 || u0 >= before + mine) break;
     }
     tc::fence_before();
     __syncthreads();
@@ -423,7 +422,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     return wait.dead || s->tile1 < 0 ? nullptr : s;
   };
   // bytes of a buffer of P
-  auto p_stride = [&](const Mode& mode) { return (mode.buffers == 4 ? min(a.rows, 32) : kAttnRows) * (kTile * 2); };
+  auto p_stride = [&](int buf_log2) { return (buf_log2 == 2 ? min(a.rows, 32) : kAttnRows) * (kTile * 2); };
   auto leave = [&](int n) { warp_arrive(sh.seg_empty[n % kSegRing]); };
 
   if (warp < kValueWarp) {
@@ -434,21 +433,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     float x[kGroupRows], l[kGroupRows];
     const float4* col = reinterpret_cast<const float4*>(sh.col[grp]);
     Turns turns;
-    int k0 = 0;  // tiles of the segments before
+    uint32_t k0 = 0;  // tiles of the segments before
     for (int n_seg = 0;; ++n_seg) {
       const Segment* seg = segment(n_seg);
       // (and the last segment's rows are no longer read)
       if (named_any(1 + grp, 128, seg == nullptr)) break;
       const int par = n_seg & 1;
-      const Mode mode(seg->rows);
-      const int part = grp & (kGroups / mode.by_tile - 1);  // of the rows
-      const int turn = mode.by_tile == 1 ? 0 : (mode.by_tile == 2 ? grp >> 1 : grp);
+      const int by_log2 = seg->by_log2, buf_log2 = seg->buf_log2, step = 1 << by_log2;
+      const int part = grp & ((kGroups >> by_log2) - 1), turn = grp >> (2 - by_log2);
       const int r0 = part * kGroupRows;
-      const uint32_t weight = mode.weight(part);
+      const uint32_t weight = seg->weight(part);
       const int tiles = seg->tile1 - seg->tile0, len = seg->len;
       const int all_see = seg->kv + seg->row0 / G;  // last position that all rows attend to
       const int pos_first = seg->tile0 * kTile;
-      const uint32_t o_at = tmem + lanes + (2 + par) * kAttnRows + turn * mode.o_cols() + r0;
+      const uint32_t o_at = tmem + lanes + (2 + par) * kAttnRows + turn * seg->o_cols() + r0;
+      const uint32_t s_first = tmem + lanes + r0;
+      const int s_cols = seg->s_cols(), p_bytes = p_stride(buf_log2);
+      unsigned char* p_first = p_at + (r0 / 8) * (16 * kTile) + t_in * 16;
       float vref = 1.f, vinv = 1.f;
 #pragma unroll
       for (int r = 0; r < kGroupRows; ++r) l[r] = 0.f;
@@ -456,9 +457,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (t_in < kGroupRows) sh.col[grp][t_in] = make_float2(sh.qs[par][r0 + t_in], 0.f);
       named_barrier(1 + grp, 128);
       bool first = true;
-      for (int i = part < mode.m ? turn : tiles; i < tiles; i += mode.by_tile) {
-        const int k = k0 + i, buf = mode.buffer(i), pos0 = pos_first + i * kTile, pos = pos0 + t_in;
-        const uint32_t phase = turns.of(mode, i);
+#pragma unroll 1
+      for (int i = part < seg->m ? turn : tiles; i < tiles; i += step) {
+        const uint32_t k = k0 + i;
+        const int buf = i & ((1 << buf_log2) - 1), pos0 = pos_first + i * kTile, pos = pos0 + t_in;
+        const uint32_t phase = turns.of(i, buf_log2);
         const bool masked = pos0 + kTile - 1 > all_see || pos0 + kTile > len;
         const ScaleEntry& sc = sh.scales[k % kScaleRing];
         wait(sh.sc_full[k % kScaleRing], (k / kScaleRing) & 1);
@@ -466,8 +469,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         warp_arrive(sh.sc_empty[k % kScaleRing], weight);
         wait(sh.s_full[buf], phase);
         tc::fence_after();
-        const uint32_t s_at = tmem + lanes + buf * mode.s_cols() + r0;
+        const uint32_t s_at = s_first + buf * s_cols;
         bool renew = first;
+#pragma unroll 1
         for (;;) {
           if (renew) {
             // New references: the rows' largest scores so far, and the largest
@@ -492,7 +496,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               }
               if (lane < 8) sh.wmax[grp][warp & 3][c + lane] = mine;
             }
-            if (!first) wait(sh.pv_done[mode.buffer(i - mode.by_tile)], turns.of(mode, i - mode.by_tile));  // O rests
+            if (!first) wait(sh.pv_done[(i - step) & ((1 << buf_log2) - 1)], turns.of(i - step, buf_log2));  // O rests
             tc::fence_after();
             named_barrier(1 + grp, 128);
             if (t_in < kGroupRows) {
@@ -561,14 +565,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           w[r >> 1] = tc::f16x2(p0 * vr, p1 * vr);
         }
         wait(sh.pv_done[buf], phase ^ 1);
-        unsigned char* p = p_at + buf * p_stride(mode) + (r0 / 8) * (16 * kTile) + t_in * 16;
+        unsigned char* p = p_first + buf * p_bytes;
         *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
         *reinterpret_cast<uint4*>(p + 16 * kTile) = make_uint4(w[4], w[5], w[6], w[7]);
         tc::fence_smem();
         warp_arrive(sh.p_full[buf], weight);
       }
       k0 += tiles;
-      turns.pass(mode, tiles);
+      turns.pass(tiles, buf_log2);
       // sums and references for the output warps
       const float s = warp_sums16(l);
       if ((lane & 1) == 0) sh.lsum[par][grp][warp & 3][lane >> 1] = s;
@@ -583,52 +587,54 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // of the request's: zeros.  New positions are not seen by all rows: their
     // NaN leave the product, where 0 times NaN would spoil rows that do not
     // see them, and are noted for the output.
-    tc::fewer_registers<kRegsValues>();
     const int t_in = tid - 32 * kValueWarp;
-    int k = 0, slot = 0, round = 0;
+    // rows as the copies swizzle them, and rows of 64 f16 (128 bytes) as the
+    // second product reads them, the two halves of D one after the other: 16
+    // bytes are where the row's number changes their own
+    const uint32_t from_row = ptx::smem_addr(v_tiles) + (D == 128 ? t_in * 128 + ((t_in & 7) << 4) : t_in * 64 + (((t_in >> 1) & 3) << 4));
+    const uint32_t to_row = ptx::smem_addr(v_half) + t_in * 128 + ((t_in & 7) << 4);
+    uint32_t k = 0;
+    int slot = 0, round = 0;
     for (int n_seg = 0;; ++n_seg) {
       const Segment* seg = segment(n_seg);
       if (seg == nullptr) break;
       const int par = n_seg & 1, tile1 = seg->tile1, kv = seg->kv, len = seg->len;
       wait(sh.meta_full[par], (n_seg >> 1) & 1);  // nanpos is set
+#pragma unroll 1
       for (int t = seg->tile0; t < tile1; ++t, ++k) {
-        const int pos0 = t * kTile, pos = pos0 + t_in;
-        const unsigned char* from = v_tiles + slot * L::kTileBytes;
-        unsigned char* to = v_half + (k & 1) * L::kHalfBytes;
+        const int pos = t * kTile + t_in;
+        const uint32_t from = from_row + slot * L::kTileBytes, to = to_row + (k & 1) * L::kHalfBytes;
         wait(sh.v_full[slot], round & 1);
         uint4 c[D / 16];
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) c[i] = *reinterpret_cast<const uint4*>(from + swizzled<D>(t_in, i * 16));
+        for (int i = 0; i < D / 16; ++i) c[i] = tc::ld_shared(from ^ (i << 4));
         warp_arrive(sh.v_empty[slot]);
         if (++slot == a.ring) slot = 0, ++round;
-        if (pos0 + kTile > min(kv, len)) {
-          if (pos >= len) {
+        const uint32_t keep = pos < len ? 0xFFFFFFFFu : 0;
+        uint32_t nan = 0;  // the top bit of a byte: its code, or an earlier one's, is NaN
+        if (k >= 2) wait(sh.f_empty[k & 1], ((k >> 1) - 1) & 1);
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) c[i] = make_uint4(0, 0, 0, 0);
-          } else if (pos >= kv) {
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t w[4] = {c[i].x & keep, c[i].y & keep, c[i].z & keep, c[i].w & keep};
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+          for (int j = 0; j < 4; ++j) nan |= (w[j] & 0x7F7F7F7Fu) + 0x01010101u;
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                for (int e = 0; e < 4; ++e)
-                  if (((w[j] >> (8 * e)) & 0x7F) == 0x7F) {
-                    w[j] &= ~(0xFFu << (8 * e));
-                    atomicMin(&sh.nanpos[par][i * 16 + j * 4 + e], pos);
-                  }
-              c[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t lo = w[2 * j], hi = w[2 * j + 1];
+            tc::st_shared((to ^ (((2 * i + j) & 7) << 4)) + (i >> 2) * (kTile * 128),
+                          make_uint4(tc::f16x2_of_e4m3x2(lo), tc::f16x2_of_e4m3x2(lo >> 16), tc::f16x2_of_e4m3x2(hi),
+                                     tc::f16x2_of_e4m3x2(hi >> 16)));
           }
         }
-        if (k >= 2) wait(sh.f_empty[k & 1], ((k >> 1) - 1) & 1);
-        // rows of 64 values (128 bytes), swizzled; the two halves of D one after the other
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 q = c[i >> 1];
-          const uint32_t lo = (i & 1) ? q.z : q.x, hi = (i & 1) ? q.w : q.y;
-          const uint4 h = make_uint4(tc::f16x2_of_e4m3x2(lo & 0xFFFFu), tc::f16x2_of_e4m3x2(lo >> 16),
-                                     tc::f16x2_of_e4m3x2(hi & 0xFFFFu), tc::f16x2_of_e4m3x2(hi >> 16));
-          *reinterpret_cast<uint4*>(to + (i >> 3) * (kTile * 128) + t_in * 128 + (((i & 7) ^ (t_in & 7)) << 4)) = h;
+        if (pos >= kv && (nan & 0x80808080u)) {
+#pragma unroll 1
+          for (int x = 0; x < D; ++x) {
+            const uint32_t at = (to ^ (((x >> 3) & 7) << 4)) + (x >> 6) * (kTile * 128) + (x & 7) * 2;
+            if ((tc::ld_shared_u16(at) & 0x7FFF) > 0x7C00) {
+              tc::st_shared_u16(at, 0);
+              atomicMin(&sh.nanpos[par][x], pos);
+            }
+          }
         }
         tc::fence_smem();
         warp_arrive(sh.f_full[k & 1]);
@@ -705,33 +711,34 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       warp_arrive(sh.q_full);
       warp_arrive(sh.meta_full[par]);
     };
-    const Segment* nxt = segment(0);
-    if (nxt != nullptr) {
-      load_q(*nxt);
-      store_q(*nxt, 0);
-    }
-    for (int n_seg = 0;; ++n_seg) {
-      if (named_any(5, 128, nxt == nullptr)) break;
+    Segment seg;
+    for (int n_seg = -1;; ++n_seg) {
+      // the next segment's Q, where there is one, before this one's O
       const int par = n_seg & 1;
-      const Segment seg = *nxt;
-      nxt = segment(n_seg + 1);
-      if (nxt != nullptr) {
+      const Segment* nxt = segment(n_seg + 1);
+      const bool more = !named_any(5, 128, nxt == nullptr);
+      if (more) {
         load_q(*nxt);
-        wait(sh.q_empty, n_seg & 1);
+        if (n_seg >= 0) wait(sh.q_empty, n_seg & 1);
         store_q(*nxt, par ^ 1);
       }
+      if (n_seg < 0) {
+        if (!more) break;
+        seg = *nxt;
+        continue;
+      }
       wait(sh.l_full[par], (n_seg >> 1) & 1);
-      const Mode mode(seg.rows);
+      const int by_tile = 1 << seg.by_log2, o_cols = seg.o_cols();
       const bool whole = seg.tile0 == 0 && seg.tile1 == seg.tiles;
       if (ot < seg.rows) {
         // a group whose sum is 0 has nothing, whatever its reference and O
-        const int r = ot % kGroupRows, part = ot / kGroupRows, parts = kGroups / mode.by_tile;
+        const int r = ot % kGroupRows, part = ot / kGroupRows, parts = kGroups >> seg.by_log2;
         float s[kGroups], M = -INFINITY, f[kGroups], sum = 0.f;
 #pragma unroll
         for (int j = 0; j < kGroups; ++j) {
           s[j] = 0.f;
           const int g = j * parts + part;  // of turn j
-          if (j < mode.by_tile) {
+          if (j < by_tile) {
 #pragma unroll
             for (int w = 0; w < 4; ++w) s[j] += sh.lsum[par][g][w][r];
             if (s[j] != 0.f) M = fmaxf(M, sh.mrun[par][g][r]);
@@ -761,6 +768,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       int tok = seg.row0 / G, g = seg.row0 % G;  // of row r
       __nv_bfloat16* dst = a.out + (static_cast<long long>(seg.q0 + tok) * a.Hq + seg.h * G + g) * D + d;
       const long long next_tok = static_cast<long long>(a.Hq - (G - 1)) * D;  // from a token's last head to the next's first
+#pragma unroll 1
       for (int c = 0; c < seg.rows; c += 8) {
         float o[8];
         tc::ld8(o_at + c, o);
@@ -772,9 +780,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           o[e] = f != 0.f ? o[e] * f : 0.f;
         }
 #pragma unroll 1
-        for (int j = 1; j < mode.by_tile; ++j) {
+        for (int j = 1; j < by_tile; ++j) {
           float y[8];
-          tc::ld8(o_at + j * mode.o_cols() + c, y);
+          tc::ld8(o_at + j * o_cols + c, y);
           tc::wait_ld();
           tc::ready(y);
 #pragma unroll
@@ -811,19 +819,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           rec[kAttnRows * 128 + kAttnRows + ot] = sh.fin[ot].x;
         }
         // the last of the item's CTAs joins the parts
-        const long long c0 = seg.first / chunk, c1 = (seg.first + seg.tiles - 1) / chunk;
+        const uint32_t c0 = seg.first / chunk, c1 = (seg.first + seg.tiles - 1) / chunk;
         __threadfence();
         named_barrier(5, 128);
-        if (ot == 0) sh.last = ptx::atom_add_acq_rel(a.counters + c0, 1u) == static_cast<uint32_t>(c1 - c0);
+        if (ot == 0) sh.last = ptx::atom_add_acq_rel(a.counters + c0, 1u) == c1 - c0;
         named_barrier(5, 128);
         if (sh.last) {
           __threadfence();
           const int pieces = static_cast<int>(c1 - c0) + 1;
           const int first_slot = static_cast<int>(c0) * 2 + (seg.first % chunk == 0 ? 0 : 1);
           auto record = [&](int p) {
-            return a.partial + static_cast<long long>(p == 0 ? first_slot : (c0 + p) * 2) * kPartialFloats;
+            return a.partial + static_cast<size_t>(p == 0 ? first_slot : static_cast<int>(c0 + p) * 2) * kPartialFloats;
           };
           constexpr int E = D / 32;  // a lane's values
+#pragma unroll 1
           for (int r4 = 0; r4 < seg.rows; r4 += 16) {
             // rows r4 + ow, + 4, + 8, + 12 at once, for their loads' sake
             float M[4], sum[4], acc[4][E];
@@ -834,6 +843,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
               for (int i = 0; i < E; ++i) acc[j][i] = 0.f;
             }
+#pragma unroll 1
             for (int p0 = 0; p0 < pieces; p0 += 32) {
               // a lane for each piece: its references and sums
               float m[4], n[4], w[4];
@@ -895,6 +905,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
       }
       leave(n_seg);
+      if (!more) break;
+      seg = *nxt;
     }
   } else {
     tc::fewer_registers<kRegsRest>();
@@ -945,11 +957,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (x.tiles > 0 && x.id >= 0 && x.id < a.num_blocks) x.scale = __ldg(scales + static_cast<long long>(x.id) * a.H + x.h);
       };
       if (lane == 0) tc::prefetch_map(map);
-      load_ids(now);
-      load_scales(now);
-      int slot = 0, round = 0, k = 0;
-      while (now.tiles > 0) {
+      now.tiles = 0;
+      int slot = 0, round = 0;
+      uint32_t k = 0;
+#pragma unroll 1
+      for (;;) {
         load_ids(nxt);
+        if (now.tiles == 0) load_scales(nxt);
+#pragma unroll 1
         for (int i = 0; i < now.tiles; ++i, ++k) {
           const int first = i << pages_log2;
           const int pages = max(0, min(pages_per_tile, now.pages - first));
@@ -958,6 +973,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const uint32_t dst = ptx::smem_addr(tiles + slot * L::kTileBytes);
           if (tc::elect()) ptx::mbar_arrive_expect_tx(bar, pages * a.bs * D);
           __syncwarp();
+#pragma unroll 1
           for (int j = 0; j < pages; ++j) {
             const int id = __shfl_sync(0xFFFFFFFFu, now.id, first + j);
             if (tc::elect()) tc::load_4d(dst + j * a.bs * D, map, 0, 0, now.h, id, bar);
@@ -965,7 +981,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           __syncwarp();
           if (++slot == a.ring) slot = 0, ++round;
           if (i == 0) load_scales(nxt);  // its ids have had a tile's time
-          const int sr = k % kScaleRing;
+          const uint32_t sr = k % kScaleRing;
           if (k >= kScaleRing) wait(sh.sc_empty[sr], (k / kScaleRing - 1) & 1);
           const float scale = __shfl_sync(0xFFFFFFFFu, now.scale, (first + lane) & 31);
           if (is_v) {
@@ -975,6 +991,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (lane < pages_per_tile) (is_v ? sh.scales[sr].vs : sh.scales[sr].ks)[lane] = is_v ? scale : scale * a.scale_log2e;
           warp_arrive(sh.sc_full[sr]);
         }
+        if (nxt.tiles == 0) break;
         now = nxt;
       }
       // no copy is in flight when the CTA ends: every slot used has been filled
@@ -988,30 +1005,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const uint64_t kd0 = tc::smem_desc(ptx::smem_addr(k_tiles), 16, 8 * D, swz);
       const uint64_t qd0 = tc::smem_desc(ptx::smem_addr(q_hi), 128, 8 * D, tc::kSwizzleNone);
       const uint64_t qd1 = tc::smem_desc(ptx::smem_addr(q_lo), 128, 8 * D, tc::kSwizzleNone);
-      int slot = 0, round = 0, buffers = 0;
+      int slot = 0, round = 0, was = 0;
       Turns turns;
       for (int n_seg = 0;; ++n_seg) {
         const Segment* seg = segment(n_seg);
         if (seg == nullptr) break;
-        const Mode mode(seg->rows);
-        const uint32_t is = tc::instr(kTile, 16 * mode.m, false, false);
-        const int tiles = seg->tile1 - seg->tile0;
-        if (mode.buffers != buffers) {
+        const uint32_t is = tc::instr(kTile, 16 * seg->m, false, false);
+        const int tiles = seg->tile1 - seg->tile0, buf_log2 = seg->buf_log2, s_cols = seg->s_cols();
+        if (buf_log2 != was) {
           // the buffers lie elsewhere now: none is in use (P is not written
           // before scores are there)
+#pragma unroll 1
           for (int b = 0; b < 4; ++b) {
             wait(sh.s_empty[b], (turns.bits >> b & 1) ^ 1);
             wait(sh.pv_done[b], (turns.bits >> b & 1) ^ 1);
           }
-          buffers = mode.buffers;
+          was = buf_log2;
         }
         wait(sh.q_full, n_seg & 1);
+#pragma unroll 1
         for (int i = 0; i < tiles; ++i) {
           const uint64_t kd = kd0 + slot * (L::kTileBytes / 16);
-          const int buf = mode.buffer(i);
-          const uint32_t dst = tmem + buf * mode.s_cols();
+          const int buf = i & ((1 << buf_log2) - 1);
+          const uint32_t dst = tmem + buf * s_cols;
           wait(sh.k_full[slot], round & 1);
-          wait(sh.s_empty[buf], turns.of(mode, i) ^ 1);
+          wait(sh.s_empty[buf], turns.of(i, buf_log2) ^ 1);
           tc::fence_after();
           if (tc::elect()) {
 #pragma unroll
@@ -1025,7 +1043,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           __syncwarp();
           if (++slot == a.ring) slot = 0, ++round;
         }
-        turns.pass(mode, tiles);
+        turns.pass(tiles, buf_log2);
         leave(n_seg);
       }
       // all products are done before the tensor memory goes back
@@ -1042,7 +1060,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       int listed = 0;
       bool more = true;
       auto list = [&]() {  // one more segment, or the list's end
-        if (!more) return;
         const int n = listed++;
         if (n >= kSegRing) wait(sh.seg_empty[n % kSegRing], (n / kSegRing - 1) & 1);
         Segment s;
@@ -1051,25 +1068,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (lane == 0) sh.seg[n % kSegRing] = s;
         warp_arrive(sh.seg_full[n % kSegRing]);
       };
-      for (int i = 0; i < kSegAhead; ++i) list();
       Turns turns;
-      int k = 0;
+      uint32_t k = 0;
       for (int n_seg = 0;; ++n_seg) {
+#pragma unroll 1
+        while (more && listed < n_seg + kSegAhead) list();
         const Segment* seg = segment(n_seg);
         if (seg == nullptr) break;
         const int par = n_seg & 1;
-        const Mode mode(seg->rows);
-        const uint32_t io = tc::instr(D, 16 * mode.m, true, true);
+        const int by_log2 = seg->by_log2, buf_log2 = seg->buf_log2, o_cols = seg->o_cols(), p_bytes = p_stride(buf_log2);
+        const uint32_t io = tc::instr(D, 16 * seg->m, true, true);
         const int tiles = seg->tile1 - seg->tile0;
         if (n_seg >= 2) wait(sh.o_empty[par], ((n_seg >> 1) - 1) & 1);
+#pragma unroll 1
         for (int i = 0; i < tiles; ++i, ++k) {
-          const int buf = mode.buffer(i);
+          const int buf = i & ((1 << buf_log2) - 1);
           const uint64_t vd = vd0 + (k & 1) * (L::kHalfBytes / 16);
-          const uint64_t pd = pd0 + buf * (p_stride(mode) / 16);
-          const uint32_t dst = tmem + (2 + par) * kAttnRows + (i & (mode.by_tile - 1)) * mode.o_cols();
-          const bool add = i >= mode.by_tile;
+          const uint64_t pd = pd0 + buf * (p_bytes / 16);
+          const uint32_t dst = tmem + (2 + par) * kAttnRows + (i & ((1 << by_log2) - 1)) * o_cols;
+          const bool add = i >> by_log2 != 0;
           wait(sh.f_full[k & 1], (k >> 1) & 1);
-          wait(sh.p_full[buf], turns.of(mode, i));
+          wait(sh.p_full[buf], turns.of(i, buf_log2));
           tc::fence_after();
           if (tc::elect()) {
 #pragma unroll
@@ -1080,11 +1099,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           __syncwarp();
         }
-        turns.pass(mode, tiles);
+        turns.pass(tiles, buf_log2);
         leave(n_seg);
-        list();
       }
-      while (more) list();  // (only where a wait gave up)
       Waiter drain;
       if (tc::elect()) tc::commit(ptx::smem_addr(&sh.done[1]));
       __syncwarp();

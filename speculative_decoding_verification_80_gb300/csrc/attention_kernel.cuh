@@ -15,6 +15,9 @@
 // cores as it lies in the cache.  Q, bf16 scaled by a power of two a row, is
 // the sum of two e4m3 numbers: a value of 8 significant bits is its nearest
 // number of 4 bits plus a remainder of 4 (exact to 2^-18 of the row's largest).
+// The two are rows of one B operand, so K is read from shared memory once, and
+// the softmax adds their columns: shared memory's 128 bytes a cycle, of which a
+// tile takes most, are the next limit after HBM.
 //
 // Second product: f16 x f16.  An e4m3 V is exact in f16, and one group of
 // warps turns V's tiles over while the softmax is at work; P in f16 has 11
@@ -75,7 +78,7 @@ constexpr int kGroups = 4;
 constexpr int kValueWarp = 16, kOutputWarp = 20, kCopyWarp = 24;
 constexpr int kAttnThreads = 28 * 32;
 // Registers a thread: 72 at launch, moved to where they are needed.
-constexpr int kRegsValues = 72, kRegsOutput = 80, kRegsRest = 64;
+constexpr int kRegsValues = 72, kRegsOutput = 88, kRegsRest = 56;
 static_assert(512 * 72 + 128 * (kRegsValues + kRegsOutput + kRegsRest) <= 72 * kAttnThreads,
               "the warpgroups' registers are those of the launch");
 constexpr int kScaleRing = 8;
@@ -83,7 +86,8 @@ constexpr int kSegRing = 8;
 constexpr int kSegAhead = 6;    // segments listed ahead of the second products'
 constexpr int kMaxRing = 8;     // tiles of K, and of V, in shared memory
 constexpr int kMaxPages = 8;    // blocks of a tile
-constexpr uint32_t kTmemCols = 256;  // S twice, O twice
+constexpr uint32_t kTmemCols = 512;  // S (both halves of Q) in 256, O twice in 128
+constexpr int kOutAt = 256;          // O's first column
 constexpr int kPartialFloats = kAttnRows * 128 + 2 * kAttnRows;
 // P = 2^kPScale at the reference score; a score may pass it by 2^kSlack
 // before P would leave f16.
@@ -107,7 +111,7 @@ struct Segment {
   uint32_t first;             // unit of the whole's first tile
   int m, by_log2, buf_log2;
   // columns of a buffer of S, and of one of a parity's Os
-  __device__ int s_cols() const { return 128 >> buf_log2; }
+  __device__ int s_cols() const { return 256 >> buf_log2; }
   __device__ int o_cols() const { return kAttnRows >> by_log2; }
   // Arrivals of a group's warp: all of a tile's make 16.
   __device__ uint32_t weight(int part) const { return m == 3 ? (part == 0 ? 2 : 1) : (m == 1 ? 4 : m == 2 ? 2 : 1); }
@@ -216,8 +220,10 @@ struct AttnShared {
   float lsum[2][kGroups][4][kGroupRows];  // sums of the softmax warps
   float mrun[2][kGroups][kGroupRows];  // and their groups' references
   float vref[2][kGroups];
-  alignas(16) float4 of[kAttnRows];    // factors of the groups' Os
+  alignas(16) float of[kAttnRows][kGroups];  // factors of the groups' Os
   float2 fin[kAttnRows];               // {sum (or its inverse), reference}
+  int32_t sees[kAttnRows];             // last position of each row
+  long long out_at[kAttnRows];         // where its output is
   int32_t nanpos[2][128];              // first new position whose value is NaN in a dimension
   ScaleEntry scales[kScaleRing];
   int32_t last;
@@ -321,9 +327,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   unsigned char* k_tiles = base + L::tiles_at();
   unsigned char* v_tiles = k_tiles + a.ring * L::kTileBytes;
   unsigned char* v_half = v_tiles + a.ring * L::kTileBytes;
-  unsigned char* q_hi = v_half + 2 * L::kHalfBytes;
-  unsigned char* q_lo = q_hi + L::q_bytes(a.rows);
-  unsigned char* p_at = q_lo + L::q_bytes(a.rows);
+  unsigned char* q_at = v_half + 2 * L::kHalfBytes;
+  unsigned char* p_at = q_at + 2 * L::q_bytes(a.rows);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = a.Hq / a.H;
 
@@ -446,9 +451,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int tiles = seg->tile1 - seg->tile0, len = seg->len;
       const int all_see = seg->kv + seg->row0 / G;  // last position that all rows attend to
       const int pos_first = seg->tile0 * kTile;
-      const uint32_t o_at = tmem + lanes + (2 + par) * kAttnRows + turn * seg->o_cols() + r0;
+      const uint32_t o_at = tmem + lanes + kOutAt + par * kAttnRows + turn * seg->o_cols() + r0;
       const uint32_t s_first = tmem + lanes + r0;
-      const int s_cols = seg->s_cols(), p_bytes = p_stride(buf_log2);
+      const int s_cols = seg->s_cols(), p_bytes = p_stride(buf_log2), rest_at = 16 * seg->m;
       unsigned char* p_first = p_at + (r0 / 8) * (16 * kTile) + t_in * 16;
       float vref = 1.f, vinv = 1.f;
 #pragma unroll
@@ -483,13 +488,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
 #pragma unroll 1
             for (int c = 0; c < kGroupRows; c += 8) {
-              float v[8], mine = -INFINITY;
+              float v[8], rest[8], mine = -INFINITY;
               tc::ld8(s_at + c, v);
+              tc::ld8(s_at + rest_at + c, rest);
               tc::wait_ld();
               tc::ready(v);
+              tc::ready(rest);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                float y = v[e] * ks * sh.col[grp][c + e].x;
+                float y = (v[e] + rest[e]) * ks * sh.col[grp][c + e].x;
                 if (masked && pos > sh.limit[par][r0 + c + e]) y = -INFINITY;
                 y = tc::warp_max(y);
                 if (lane == e) mine = y;
@@ -527,16 +534,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
           }
           // scores over the rows' references
+          float rest[kGroupRows];
           tc::ld8(s_at, x);
+          tc::ld8(s_at + rest_at, rest);
           tc::ld8(s_at + 8, x + 8);
+          tc::ld8(s_at + rest_at + 8, rest + 8);
           tc::wait_ld();
           tc::ready(x);
           tc::ready(x + 8);
+          tc::ready(rest);
+          tc::ready(rest + 8);
 #pragma unroll
           for (int r = 0; r < kGroupRows; r += 2) {
             const float4 w = col[r >> 1];
-            x[r] = fmaf(x[r] * ks, w.x, -w.y);
-            x[r + 1] = fmaf(x[r + 1] * ks, w.z, -w.w);
+            x[r] = fmaf((x[r] + rest[r]) * ks, w.x, -w.y);
+            x[r + 1] = fmaf((x[r + 1] + rest[r + 1]) * ks, w.z, -w.w);
           }
           if (masked) {
 #pragma unroll
@@ -610,23 +622,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int i = 0; i < D / 16; ++i) c[i] = tc::ld_shared(from ^ (i << 4));
         warp_arrive(sh.v_empty[slot]);
         if (++slot == a.ring) slot = 0, ++round;
-        const uint32_t keep = pos < len ? 0xFFFFFFFFu : 0;
-        uint32_t nan = 0;  // the top bit of a byte: its code, or an earlier one's, is NaN
+        uint32_t nan = 0;
+        if (t * kTile + kTile > min(kv, len)) {
+          const uint32_t keep = pos < len ? 0xFFFFFFFFu : 0;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            c[i].x &= keep, c[i].y &= keep, c[i].z &= keep, c[i].w &= keep;
+            // the top bit of a byte: its code is NaN
+            nan |= ((c[i].x & 0x7F7F7F7Fu) + 0x01010101u) | ((c[i].y & 0x7F7F7F7Fu) + 0x01010101u) |
+                   ((c[i].z & 0x7F7F7F7Fu) + 0x01010101u) | ((c[i].w & 0x7F7F7F7Fu) + 0x01010101u);
+          }
+          nan = pos >= kv ? nan & 0x80808080u : 0;
+        }
         if (k >= 2) wait(sh.f_empty[k & 1], ((k >> 1) - 1) & 1);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          const uint32_t w[4] = {c[i].x & keep, c[i].y & keep, c[i].z & keep, c[i].w & keep};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) nan |= (w[j] & 0x7F7F7F7Fu) + 0x01010101u;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint32_t lo = w[2 * j], hi = w[2 * j + 1];
+            const uint32_t lo = j ? c[i].z : c[i].x, hi = j ? c[i].w : c[i].y;
             tc::st_shared((to ^ (((2 * i + j) & 7) << 4)) + (i >> 2) * (kTile * 128),
                           make_uint4(tc::f16x2_of_e4m3x2(lo), tc::f16x2_of_e4m3x2(lo >> 16), tc::f16x2_of_e4m3x2(hi),
                                      tc::f16x2_of_e4m3x2(hi >> 16)));
           }
         }
-        if (pos >= kv && (nan & 0x80808080u)) {
+        if (nan) {
 #pragma unroll 1
           for (int x = 0; x < D; ++x) {
             const uint32_t at = (to ^ (((x >> 3) & 7) << 4)) + (x >> 6) * (kTile * 128) + (x & 7) * 2;
@@ -652,35 +671,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint4 qv[kVec];
     const int qr = ot >> 1, half = ot & 1;  // two threads a row of Q
     auto load_q = [&](const Segment& s) {
-      if (qr < s.rows) {
-        const int row = s.row0 + qr;
-        const uint4* p = reinterpret_cast<const uint4*>(a.q + (s.q0 + row / G) * a.q_stride + (s.h * G + row % G) * D +
-                                                        half * (D / 2));
+      const int row = s.row0 + min(qr, s.rows - 1);
+      const uint4* p = reinterpret_cast<const uint4*>(a.q + (s.q0 + row / G) * a.q_stride + (s.h * G + row % G) * D +
+                                                      half * (D / 2));
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) qv[i] = __ldg(p + i);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) qv[i] = make_uint4(0, 0, 0, 0);
-      }
+      for (int i = 0; i < kVec; ++i) qv[i] = __ldg(p + i);
     };
     auto store_q = [&](const Segment& s, int par) {
-      if (qr < (s.rows + 15) / 16 * 16) {
-        float amax = 0.f;
-        bool bad = false;
+      if (qr < 16 * s.m) {
+        // the largest magnitude's bits (bf16 in both halves; no number is above infinity)
+        uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
-          float f[8];
-          unpack16<__nv_bfloat16>(qv[i], f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            bad |= !isfinite(f[e]);
-            amax = fmaxf(amax, fabsf(f[e]));
-          }
+          top = __vmaxu2(top, qv[i].x & 0x7FFF7FFFu);
+          top = __vmaxu2(top, qv[i].y & 0x7FFF7FFFu);
+          top = __vmaxu2(top, qv[i].z & 0x7FFF7FFFu);
+          top = __vmaxu2(top, qv[i].w & 0x7FFF7FFFu);
         }
-        const uint32_t pair = 3u << (lane & 30);
-        amax = fmaxf(amax, __shfl_xor_sync(pair, amax, 1));
-        bad = __shfl_xor_sync(pair, static_cast<int>(bad), 1) || bad;
-        const float sc = pow2_scale(amax), inv = bad ? 0.f : pow2_inverse(sc);
+        top = max(top >> 16, top & 0xFFFFu);
+        top = max(top, __shfl_xor_sync(3u << (lane & 30), top, 1));
+        const bool in = qr < s.rows, bad = top >= 0x7F80u;
+        const float sc = pow2_scale(__uint_as_float(top << 16)), inv = bad || !in ? 0.f : pow2_inverse(sc);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
           float f[8];
@@ -698,12 +709,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           // 8 rows x 16 bytes lie together, then the rows' next 16 bytes
           const int at_x = half * (D / 2) + i * 8;
           const int at = (qr >> 3) * (8 * D) + (at_x >> 4) * 128 + (qr & 7) * 16 + (at_x & 15);
-          *reinterpret_cast<uint2*>(q_hi + at) = make_uint2(hw[0], hw[1]);
-          *reinterpret_cast<uint2*>(q_lo + at) = make_uint2(lw[0], lw[1]);
+          *reinterpret_cast<uint2*>(q_at + at) = make_uint2(hw[0], hw[1]);
+          *reinterpret_cast<uint2*>(q_at + s.m * 16 * D + at) = make_uint2(lw[0], lw[1]);
         }
         if (half == 0) {
           sh.qs[par][qr] = bad ? __uint_as_float(0x7FFFFFFFu) : (sc > 0.f ? sc : 1.f);
-          sh.limit[par][qr] = qr < s.rows ? min(s.kv + (s.row0 + qr) / G, s.len - 1) : -1;
+          sh.limit[par][qr] = in ? min(s.kv + (s.row0 + qr) / G, s.len - 1) : -1;
         }
       }
       sh.nanpos[par][ot] = 0x7FFFFFFF;
@@ -755,8 +766,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
         }
         if (whole) sum = sum == 0.f ? 0.f : 1.f / sum;
-        sh.of[ot] = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4*>(sh.of[ot]) = make_float4(f[0], f[1], f[2], f[3]);
         sh.fin[ot] = make_float2(sum, M);
+        const int row = seg.row0 + ot, tok = row / G;
+        sh.sees[ot] = seg.kv + tok;
+        sh.out_at[ot] = (static_cast<long long>(seg.q0 + tok) * a.Hq + seg.h * G + (row - tok * G)) * D;
       }
       named_barrier(5, 128);
       wait(sh.o_full[par], (n_seg >> 1) & 1);
@@ -764,51 +778,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int nan_at = sh.nanpos[par][d];
       const int slot = static_cast<int>(blockIdx.x) * 2 + (n_seg == 0 ? 0 : 1);
       float* rec = a.partial + static_cast<long long>(slot) * kPartialFloats;
-      const uint32_t o_at = tmem + (static_cast<uint32_t>(ow * 32) << 16) + (2 + par) * kAttnRows;
-      int tok = seg.row0 / G, g = seg.row0 % G;  // of row r
-      __nv_bfloat16* dst = a.out + (static_cast<long long>(seg.q0 + tok) * a.Hq + seg.h * G + g) * D + d;
-      const long long next_tok = static_cast<long long>(a.Hq - (G - 1)) * D;  // from a token's last head to the next's first
+      const uint32_t o_at = tmem + (static_cast<uint32_t>(ow * 32) << 16) + kOutAt + par * kAttnRows;
 #pragma unroll 1
       for (int c = 0; c < seg.rows; c += 8) {
-        float o[8];
-        tc::ld8(o_at + c, o);
-        tc::wait_ld();
-        tc::ready(o);
+        float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float f = sh.of[c + e].x;
-          o[e] = f != 0.f ? o[e] * f : 0.f;
-        }
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
 #pragma unroll 1
-        for (int j = 1; j < by_tile; ++j) {
-          float y[8];
+        for (int j = 0; j < by_tile; j += 2) {  // two groups' Os
+          float y[8], z[8];
           tc::ld8(o_at + j * o_cols + c, y);
+          if (by_tile > 1) tc::ld8(o_at + (j + 1) * o_cols + c, z);
           tc::wait_ld();
           tc::ready(y);
+          tc::ready(z);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float f = reinterpret_cast<const float*>(&sh.of[c + e])[j];
-            if (f != 0.f) o[e] = fmaf(y[e], f, o[e]);
+            const float2 f = *reinterpret_cast<const float2*>(&sh.of[c + e][j]);
+            if (f.x != 0.f) v[e] = fmaf(y[e], f.x, v[e]);
+            if (f.y != 0.f) v[e] = fmaf(z[e], f.y, v[e]);
           }
         }
+        const int rows = min(8, seg.rows - c);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (c + e < seg.rows) {
-            float v = o[e];
-            if (nan_at <= seg.kv + tok) v = __uint_as_float(0x7FFFFFFFu);
-            if (whole) {
-              if (owns) *dst = __float2bfloat16_rn(v * sh.fin[c + e].x);
-            } else if (owns) {
-              rec[(c + e) * D + d] = v;
-            }
-            if (++g == G) {
-              g = 0;
-              ++tok;
-              dst += next_tok;
-            } else {
-              dst += D;
-            }
-          }
+        for (int e = 0; e < 8; ++e)
+          if (nan_at <= sh.sees[c + e]) v[e] = __uint_as_float(0x7FFFFFFFu);
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < rows && owns) a.out[sh.out_at[c + e] + d] = __float2bfloat16_rn(v[e] * sh.fin[c + e].x);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < rows && owns) rec[(c + e) * D + d] = v[e];
         }
       }
       tc::fence_before();
@@ -833,11 +835,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           };
           constexpr int E = D / 32;  // a lane's values
 #pragma unroll 1
-          for (int r4 = 0; r4 < seg.rows; r4 += 16) {
-            // rows r4 + ow, + 4, + 8, + 12 at once, for their loads' sake
-            float M[4], sum[4], acc[4][E];
+          for (int r4 = 0; r4 < seg.rows; r4 += 8) {
+            // rows r4 + ow and r4 + ow + 4 at once
+            float M[2], sum[2], acc[2][E];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2; ++j) {
               M[j] = -INFINITY;
               sum[j] = 0.f;
 #pragma unroll
@@ -846,16 +848,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll 1
             for (int p0 = 0; p0 < pieces; p0 += 32) {
               // a lane for each piece: its references and sums
-              float m[4], n[4], w[4];
+              float m[2], n[2], w[2];
               const float* q = record(min(p0 + lane, pieces - 1)) + kAttnRows * 128 + r4 + ow;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
+              for (int j = 0; j < 2; ++j) {
                 const bool in = p0 + lane < pieces && r4 + ow + 4 * j < seg.rows;
                 m[j] = in ? __ldcg(q + 4 * j) : 0.f;
                 n[j] = in ? __ldcg(q + kAttnRows + 4 * j) : 0.f;
               }
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
+              for (int j = 0; j < 2; ++j) {
                 const float M_new = fmaxf(M[j], tc::warp_max(n[j] != 0.f ? m[j] : -INFINITY));
                 const float f = M[j] > -INFINITY ? tc::ex2(M[j] - M_new) : 0.f;
                 w[j] = n[j] != 0.f ? tc::ex2(m[j] - M_new) : 0.f;
@@ -872,7 +874,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               for (int p = 0; p < here; ++p) {
                 const float* y = record(p0 + p) + (r4 + ow) * D + lane * E;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 2; ++j) {
                   const float wp = __shfl_sync(0xFFFFFFFFu, w[j], p);
                   float v[E];  // (rows past the last are there, and not written)
                   if constexpr (D == 128) {
@@ -888,12 +890,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int row = seg.row0 + r4 + ow + 4 * j;
-              if (r4 + ow + 4 * j >= seg.rows) break;
+            for (int j = 0; j < 2; ++j) {
+              const int r = r4 + ow + 4 * j;
+              if (r >= seg.rows) break;
               const float inv = sum[j] == 0.f ? 0.f : 1.f / sum[j];
-              uint32_t* to = reinterpret_cast<uint32_t*>(
-                  a.out + (static_cast<long long>(seg.q0 + row / G) * a.Hq + seg.h * G + row % G) * D + lane * E);
+              uint32_t* to = reinterpret_cast<uint32_t*>(a.out + sh.out_at[r] + lane * E);
 #pragma unroll
               for (int i = 0; i < E; i += 2) {
                 const __nv_bfloat162 y = __floats2bfloat162_rn(acc[j][i] * inv, acc[j][i + 1] * inv);
@@ -1003,14 +1004,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       // --------------------------------------------------- first products
       const uint64_t swz = D == 128 ? tc::kSwizzle128 : tc::kSwizzle64;
       const uint64_t kd0 = tc::smem_desc(ptx::smem_addr(k_tiles), 16, 8 * D, swz);
-      const uint64_t qd0 = tc::smem_desc(ptx::smem_addr(q_hi), 128, 8 * D, tc::kSwizzleNone);
-      const uint64_t qd1 = tc::smem_desc(ptx::smem_addr(q_lo), 128, 8 * D, tc::kSwizzleNone);
+      const uint64_t qd0 = tc::smem_desc(ptx::smem_addr(q_at), 128, 8 * D, tc::kSwizzleNone);
       int slot = 0, round = 0, was = 0;
       Turns turns;
       for (int n_seg = 0;; ++n_seg) {
         const Segment* seg = segment(n_seg);
         if (seg == nullptr) break;
-        const uint32_t is = tc::instr(kTile, 16 * seg->m, false, false);
+        const uint32_t is = tc::instr(kTile, 32 * seg->m, false, false);
         const int tiles = seg->tile1 - seg->tile0, buf_log2 = seg->buf_log2, s_cols = seg->s_cols();
         if (buf_log2 != was) {
           // the buffers lie elsewhere now: none is in use (P is not written
@@ -1034,8 +1034,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (tc::elect()) {
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) tc::mma_e4m3(dst, kd + j * 2, qd0 + j * 16, is, j > 0);
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) tc::mma_e4m3(dst, kd + j * 2, qd1 + j * 16, is, true);
             tc::commit(ptx::smem_addr(&sh.s_full[buf]));
             tc::commit(ptx::smem_addr(&sh.k_empty[slot]));
             if (i + 1 == tiles) tc::commit(ptx::smem_addr(&sh.q_empty));
@@ -1085,7 +1083,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const int buf = i & ((1 << buf_log2) - 1);
           const uint64_t vd = vd0 + (k & 1) * (L::kHalfBytes / 16);
           const uint64_t pd = pd0 + buf * (p_bytes / 16);
-          const uint32_t dst = tmem + (2 + par) * kAttnRows + (i & ((1 << by_log2) - 1)) * o_cols;
+          const uint32_t dst = tmem + kOutAt + par * kAttnRows + (i & ((1 << by_log2) - 1)) * o_cols;
           const bool add = i >> by_log2 != 0;
           wait(sh.f_full[k & 1], (k >> 1) & 1);
           wait(sh.p_full[buf], turns.of(i, buf_log2));

@@ -73,13 +73,14 @@ constexpr int kTile = 128;      // positions of a tile
 constexpr int kAttnRows = 64;   // most rows of a tile
 constexpr int kGroupRows = 16;  // of a softmax group
 constexpr int kGroups = 4;
-// Warps: 0-15 softmax, 16-19 V to f16, 20-23 Q and O, 24 copies of K, 25 first
-// products, 26 second products and the list of segments, 27 copies of V.
-constexpr int kValueWarp = 16, kOutputWarp = 20, kCopyWarp = 24;
-constexpr int kAttnThreads = 28 * 32;
-// Registers a thread: 72 at launch, moved to where they are needed.
-constexpr int kRegsValues = 72, kRegsOutput = 88, kRegsRest = 56;
-static_assert(512 * 72 + 128 * (kRegsValues + kRegsOutput + kRegsRest) <= 72 * kAttnThreads,
+// Warps: 0-15 softmax, 16-23 V to f16 (four a tile), 24-27 Q and O, 28 copies of
+// K, 29 first products, 30 second products and the list of segments, 31 copies
+// of V.
+constexpr int kValueWarp = 16, kOutputWarp = 24, kCopyWarp = 28;
+constexpr int kAttnThreads = 32 * 32;
+// Registers a thread: 64 at launch, moved to where they are needed.
+constexpr int kRegsSoftmax = 72, kRegsValues = 48, kRegsOutput = 72, kRegsRest = 56;
+static_assert(512 * kRegsSoftmax + 256 * kRegsValues + 128 * (kRegsOutput + kRegsRest) <= 64 * kAttnThreads,
               "the warpgroups' registers are those of the launch");
 constexpr int kScaleRing = 8;
 constexpr int kSegRing = 8;
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       init(sh.o_full[i], 1);
       init(sh.o_empty[i], 4);
       init(sh.meta_full[i], 4);
-      init(sh.l_full[i], 20);
+      init(sh.l_full[i], 24);
     }
     for (int i = 0; i < kScaleRing; ++i) {
       init(sh.sc_full[i], 2);
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     init(sh.done[1], 1);
     for (int i = 0; i < kSegRing; ++i) {
       init(sh.seg_full[i], 1);
-      init(sh.seg_empty[i], 28);
+      init(sh.seg_empty[i], 32);
     }
     ptx::fence_mbarrier_init();
     sh.b0 = 0;
@@ -433,6 +434,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (warp < kValueWarp) {
     // ------------------------------------------------------------ softmax
     // A thread has one position and the 16 rows of its group.
+    tc::more_registers<kRegsSoftmax>();
     const int grp = warp >> 2, t_in = tid & 127, page = t_in >> a.bs_log2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     float x[kGroupRows], l[kGroupRows];
@@ -599,29 +601,36 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // of the request's: zeros.  New positions are not seen by all rows: their
     // NaN leave the product, where 0 times NaN would spoil rows that do not
     // see them, and are noted for the output.
-    const int t_in = tid - 32 * kValueWarp;
+    tc::fewer_registers<kRegsValues>();
+    const int grp = (warp - kValueWarp) >> 2, t_in = tid & 127;
     // rows as the copies swizzle them, and rows of 64 f16 (128 bytes) as the
     // second product reads them, the two halves of D one after the other: 16
     // bytes are where the row's number changes their own
     const uint32_t from_row = ptx::smem_addr(v_tiles) + (D == 128 ? t_in * 128 + ((t_in & 7) << 4) : t_in * 64 + (((t_in >> 1) & 3) << 4));
     const uint32_t to_row = ptx::smem_addr(v_half) + t_in * 128 + ((t_in & 7) << 4);
-    uint32_t k = 0;
-    int slot = 0, round = 0;
+    // the group's tiles are those whose number k is of its parity
+    const uint32_t to = to_row + grp * L::kHalfBytes;
+    uint32_t k0 = 0;  // tiles of the segments before
+    int slot = grp, round = 0;
     for (int n_seg = 0;; ++n_seg) {
       const Segment* seg = segment(n_seg);
       if (seg == nullptr) break;
-      const int par = n_seg & 1, tile1 = seg->tile1, kv = seg->kv, len = seg->len;
+      const int par = n_seg & 1, tile0 = seg->tile0, tiles = seg->tile1 - tile0, kv = seg->kv, len = seg->len;
       wait(sh.meta_full[par], (n_seg >> 1) & 1);  // nanpos is set
 #pragma unroll 1
-      for (int t = seg->tile0; t < tile1; ++t, ++k) {
-        const int pos = t * kTile + t_in;
-        const uint32_t from = from_row + slot * L::kTileBytes, to = to_row + (k & 1) * L::kHalfBytes;
+      for (int i = (k0 ^ grp) & 1; i < tiles; i += 2) {
+        const uint32_t k = k0 + i;
+        const int t = tile0 + i, pos = t * kTile + t_in;
+        const uint32_t from = from_row + slot * L::kTileBytes;
+        // (the slot's last tile may have been the other group's)
+        if (round > 0) wait(sh.v_empty[slot], (round - 1) & 1);
         wait(sh.v_full[slot], round & 1);
         uint4 c[D / 16];
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) c[i] = tc::ld_shared(from ^ (i << 4));
         warp_arrive(sh.v_empty[slot]);
-        if (++slot == a.ring) slot = 0, ++round;
+        slot += 2;
+        if (slot >= a.ring) slot -= a.ring, ++round;
         uint32_t nan = 0;
         if (t * kTile + kTile > min(kv, len)) {
           const uint32_t keep = pos < len ? 0xFFFFFFFFu : 0;
@@ -634,7 +643,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           nan = pos >= kv ? nan & 0x80808080u : 0;
         }
-        if (k >= 2) wait(sh.f_empty[k & 1], ((k >> 1) - 1) & 1);
+        if (k >= 2) wait(sh.f_empty[grp], ((k >> 1) - 1) & 1);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
 #pragma unroll
@@ -656,8 +665,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
         }
         tc::fence_smem();
-        warp_arrive(sh.f_full[k & 1]);
+        warp_arrive(sh.f_full[grp]);
       }
+      k0 += tiles;
       warp_arrive(sh.l_full[par]);
       leave(n_seg);
     }
@@ -1012,17 +1022,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (seg == nullptr) break;
         const uint32_t is = tc::instr(kTile, 32 * seg->m, false, false);
         const int tiles = seg->tile1 - seg->tile0, buf_log2 = seg->buf_log2, s_cols = seg->s_cols();
-        if (buf_log2 != was) {
-          // the buffers lie elsewhere now: none is in use (P is not written
-          // before scores are there)
-#pragma unroll 1
-          for (int b = 0; b < 4; ++b) {
-            wait(sh.s_empty[b], (turns.bits >> b & 1) ^ 1);
-            wait(sh.pv_done[b], (turns.bits >> b & 1) ^ 1);
-          }
-          was = buf_log2;
-        }
         wait(sh.q_full, n_seg & 1);
+        if (seg->m != was) {
+          // Other groups use the buffers now, or they lie elsewhere: the last
+          // segment's second products are over first.  (So a group has seen
+          // each use of a buffer since, as a wait for a parity needs.  O of the
+          // segment before that has been drained: this Q is there.)
+          if (n_seg > 0) wait(sh.o_full[(n_seg - 1) & 1], ((n_seg - 1) >> 1) & 1);
+          was = seg->m;
+        }
 #pragma unroll 1
         for (int i = 0; i < tiles; ++i) {
           const uint64_t kd = kd0 + slot * (L::kTileBytes / 16);

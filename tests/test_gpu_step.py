@@ -360,6 +360,22 @@ def test_attention_many_requests_of_mixed_lengths():
     _check_attn(c, _attn_gpu(c))
 
 
+@pytest.mark.parametrize("D,bs,H", [(128, 16, 4), (64, 32, 4), (128, 64, 8)])
+def test_attention_many_tiles_a_cta_and_rows_of_every_count(D, bs, H):
+    # some twenty tiles a CTA, in segments of 8 to 64 rows next to one another
+    rng = np.random.default_rng(D + H)
+    B = 160 // H
+    new = [1 + (3 * b) % 8 for b in range(B)]
+    kv = rng.integers(1200, 3000, B).tolist()
+    kv[3], kv[7], kv[11] = 0, 100, 130
+    c = _attn_case(rng, new, kv, 8 * H, H, D, bs)
+    out = _attn_gpu(c)
+    _check_attn(c, out)
+    ws = sd.new_attention_workspace()
+    for _ in range(20):
+        assert torch.equal(_attn_gpu(c, workspace=ws), out)
+
+
 def test_attention_a_sink_and_a_long_faint_tail():
     # one position far above 4000 others: the others' weights are below 2^-14 of its, together not
     D, bs = 128, 16

@@ -73,13 +73,13 @@ constexpr int kTile = 128;      // positions of a tile
 constexpr int kAttnRows = 64;   // most rows of a tile
 constexpr int kGroupRows = 16;  // of a softmax group
 constexpr int kGroups = 4;
-// Warps: 0-15 softmax, 16-23 V to f16 (four a tile), 24-27 Q and O, 28 copies of
+// Warps: 0-15 softmax, 16-23 V to f16 (four a half of D), 24-27 Q and O, 28 copies of
 // K, 29 first products, 30 second products and the list of segments, 31 copies
 // of V.
 constexpr int kValueWarp = 16, kOutputWarp = 24, kCopyWarp = 28;
 constexpr int kAttnThreads = 32 * 32;
 // Registers a thread: 64 at launch, moved to where they are needed.
-constexpr int kRegsSoftmax = 72, kRegsValues = 48, kRegsOutput = 72, kRegsRest = 56;
+constexpr int kRegsSoftmax = 72, kRegsValues = 40, kRegsOutput = 80, kRegsRest = 64;
 static_assert(512 * kRegsSoftmax + 256 * kRegsValues + 128 * (kRegsOutput + kRegsRest) <= 64 * kAttnThreads,
               "the warpgroups' registers are those of the launch");
 constexpr int kScaleRing = 8;
@@ -94,9 +94,9 @@ constexpr int kPartialFloats = kAttnRows * 128 + 2 * kAttnRows;
 // before P would leave f16.
 constexpr float kPScale = 64.f;
 constexpr float kSlack = 9.f;
-// A wait gives up after this many tries of at most a microsecond each.
-#ifndef SPECDEC_ATTN_WAIT_TRIES
-#define SPECDEC_ATTN_WAIT_TRIES 2000000u
+// A wait gives up after this many cycles (a second).
+#ifndef SPECDEC_ATTN_WAIT_CYCLES
+#define SPECDEC_ATTN_WAIT_CYCLES 2000000000u
 #endif
 
 // Part of a (request, head, row group) that one CTA works on.  tile1 < 0 ends
@@ -247,20 +247,28 @@ __device__ __forceinline__ bool named_any(int id, int threads, bool x) {
   return r != 0;
 }
 
+// One warp of a group polls a barrier and the others wait for it at a hardware
+// barrier: polls are shared-memory accesses, and with every warp polling they
+// took a third of the pipe's cycles.
+//
 // A wait that gives up once; after that the thread goes on without waiting, so
 // that every barrier still gets its arrivals, to the end of its segment.  What
 // decides how often a group of warps meets at a barrier is agreed on at one.
 struct Waiter {
   bool dead = false;
+  bool lazy = false;  // sleeps between polls
   __device__ __forceinline__ void operator()(const uint64_t& bar, uint32_t parity) {
-    if (dead) return;
     const uint32_t at = ptx::smem_addr(&bar);
+    if (dead || ptx::mbar_try_wait(at, parity)) return;
+    const uint32_t since = clock();
 #pragma unroll 1
-    for (uint32_t n = SPECDEC_ATTN_WAIT_TRIES; !tc::try_wait(at, parity);)
-      if (--n == 0) {
+    while (!ptx::mbar_try_wait(at, parity)) {
+      if (lazy) __nanosleep(200);
+      if (static_cast<uint32_t>(clock()) - since > SPECDEC_ATTN_WAIT_CYCLES) {
         dead = true;
         break;
       }
+    }
   }
 };
 // Arrivals for the warp, after what all its threads did before.
@@ -339,7 +347,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       init(sh.k_full[i], 1);
       init(sh.k_empty[i], 1);
       init(sh.v_full[i], 1);
-      init(sh.v_empty[i], 4);
+      init(sh.v_empty[i], 8);
     }
     for (int i = 0; i < 4; ++i) {
       init(sh.s_full[i], 1);
@@ -348,7 +356,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       init(sh.pv_done[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      init(sh.f_full[i], 4);
+      init(sh.f_full[i], 8);
       init(sh.f_empty[i], 1);
       init(sh.o_full[i], 1);
       init(sh.o_empty[i], 4);
@@ -436,6 +444,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // A thread has one position and the 16 rows of its group.
     tc::more_registers<kRegsSoftmax>();
     const int grp = warp >> 2, t_in = tid & 127, page = t_in >> a.bs_log2;
+    const bool leader = (warp & 3) == 0;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     float x[kGroupRows], l[kGroupRows];
     const float4* col = reinterpret_cast<const float4*>(sh.col[grp]);
@@ -460,7 +469,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       float vref = 1.f, vinv = 1.f;
 #pragma unroll
       for (int r = 0; r < kGroupRows; ++r) l[r] = 0.f;
-      wait(sh.meta_full[par], (n_seg >> 1) & 1);
+      if (leader) wait(sh.meta_full[par], (n_seg >> 1) & 1);
       if (t_in < kGroupRows) sh.col[grp][t_in] = make_float2(sh.qs[par][r0 + t_in], 0.f);
       named_barrier(1 + grp, 128);
       bool first = true;
@@ -471,11 +480,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const uint32_t phase = turns.of(i, buf_log2);
         const bool masked = pos0 + kTile - 1 > all_see || pos0 + kTile > len;
         const ScaleEntry& sc = sh.scales[k % kScaleRing];
-        wait(sh.sc_full[k % kScaleRing], (k / kScaleRing) & 1);
+        if (leader) {
+          wait(sh.sc_full[k % kScaleRing], (k / kScaleRing) & 1);
+          wait(sh.s_full[buf], phase);
+        }
+        named_barrier(1 + grp, 128);
+        tc::fence_after();
         const float ks = sc.ks[page], vs = sc.vs[page], vmax = sc.vmax;
         warp_arrive(sh.sc_empty[k % kScaleRing], weight);
-        wait(sh.s_full[buf], phase);
-        tc::fence_after();
         const uint32_t s_at = s_first + buf * s_cols;
         bool renew = first;
 #pragma unroll 1
@@ -505,7 +517,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               }
               if (lane < 8) sh.wmax[grp][warp & 3][c + lane] = mine;
             }
-            if (!first) wait(sh.pv_done[(i - step) & ((1 << buf_log2) - 1)], turns.of(i - step, buf_log2));  // O rests
+            if (leader) {
+              if (!first) wait(sh.pv_done[(i - step) & ((1 << buf_log2) - 1)], turns.of(i - step, buf_log2));  // O rests
+              wait(sh.pv_done[buf], phase ^ 1);
+            }
             tc::fence_after();
             named_barrier(1 + grp, 128);
             if (t_in < kGroupRows) {
@@ -562,7 +577,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           for (int r = 2; r < kGroupRows; ++r) top[r & 1] = fmaxf(top[r & 1], x[r]);
           // does P stay within f16 (and the sum within 32 bits)?
           const bool over = fmaxf(top[0], top[1]) > fminf(kSlack - __log2f(vs * vinv), 60.f) || vmax > 4.f * vref;
-          if (renew || !named_any(1 + grp, 128, over)) break;
+          // (and P's buffer has been read)
+          if (renew) break;
+          if (leader) wait(sh.pv_done[buf], phase ^ 1);
+          if (!named_any(1 + grp, 128, over)) break;
           renew = true;
         }
         tc::fence_before();
@@ -578,7 +596,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           l[r + 1] += p1;
           w[r >> 1] = tc::f16x2(p0 * vr, p1 * vr);
         }
-        wait(sh.pv_done[buf], phase ^ 1);
         unsigned char* p = p_first + buf * p_bytes;
         *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
         *reinterpret_cast<uint4*>(p + 16 * kTile) = make_uint4(w[4], w[5], w[6], w[7]);
@@ -602,40 +619,38 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // NaN leave the product, where 0 times NaN would spoil rows that do not
     // see them, and are noted for the output.
     tc::fewer_registers<kRegsValues>();
-    const int grp = (warp - kValueWarp) >> 2, t_in = tid & 127;
+    const int t_in = tid & 127, half = (warp - kValueWarp) >> 2;
+    const bool leader = warp == kValueWarp;
+    constexpr int kVec = D / 32;  // 16-byte loads of half a row
     // rows as the copies swizzle them, and rows of 64 f16 (128 bytes) as the
-    // second product reads them, the two halves of D one after the other: 16
-    // bytes are where the row's number changes their own
-    const uint32_t from_row = ptx::smem_addr(v_tiles) + (D == 128 ? t_in * 128 + ((t_in & 7) << 4) : t_in * 64 + (((t_in >> 1) & 3) << 4));
-    const uint32_t to_row = ptx::smem_addr(v_half) + t_in * 128 + ((t_in & 7) << 4);
-    // the group's tiles are those whose number k is of its parity
-    const uint32_t to = to_row + grp * L::kHalfBytes;
-    uint32_t k0 = 0;  // tiles of the segments before
-    int slot = grp, round = 0;
+    // second product reads them, the two halves of D = 128 one after the other:
+    // 16 bytes are where the row's number changes their own
+    const uint32_t from_row = ptx::smem_addr(v_tiles) + (D == 128 ? t_in * 128 + (((t_in & 7) ^ (half * kVec)) << 4)
+                                                                  : t_in * 64 + ((((t_in >> 1) & 3) ^ (half * kVec)) << 4));
+    const uint32_t to_row = ptx::smem_addr(v_half) + t_in * 128 +
+                            (D == 128 ? ((t_in & 7) << 4) + half * (kTile * 128) : ((t_in & 7) ^ (half * 4)) << 4);
+    uint32_t k = 0;
+    int slot = 0, round = 0;
     for (int n_seg = 0;; ++n_seg) {
       const Segment* seg = segment(n_seg);
-      if (seg == nullptr) break;
-      const int par = n_seg & 1, tile0 = seg->tile0, tiles = seg->tile1 - tile0, kv = seg->kv, len = seg->len;
-      wait(sh.meta_full[par], (n_seg >> 1) & 1);  // nanpos is set
+      if (named_any(6, 256, seg == nullptr)) break;
+      const int par = n_seg & 1, kv = seg->kv, len = seg->len, pos_end = seg->tile1 * kTile;
+      if (leader) wait(sh.meta_full[par], (n_seg >> 1) & 1);  // nanpos is set
 #pragma unroll 1
-      for (int i = (k0 ^ grp) & 1; i < tiles; i += 2) {
-        const uint32_t k = k0 + i;
-        const int t = tile0 + i, pos = t * kTile + t_in;
-        const uint32_t from = from_row + slot * L::kTileBytes;
-        // (the slot's last tile may have been the other group's)
-        if (round > 0) wait(sh.v_empty[slot], (round - 1) & 1);
-        wait(sh.v_full[slot], round & 1);
-        uint4 c[D / 16];
+      for (int pos = seg->tile0 * kTile + t_in; pos < pos_end; pos += kTile, ++k) {
+        const uint32_t from = from_row + slot * L::kTileBytes, to = to_row + (k & 1) * L::kHalfBytes;
+        if (leader) wait(sh.v_full[slot], round & 1);
+        named_barrier(6, 256);
+        uint4 c[kVec];
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) c[i] = tc::ld_shared(from ^ (i << 4));
+        for (int i = 0; i < kVec; ++i) c[i] = tc::ld_shared(from ^ (i << 4));
         warp_arrive(sh.v_empty[slot]);
-        slot += 2;
-        if (slot >= a.ring) slot -= a.ring, ++round;
+        if (++slot == a.ring) slot = 0, ++round;
         uint32_t nan = 0;
-        if (t * kTile + kTile > min(kv, len)) {
+        if (pos - t_in + kTile > min(kv, len)) {
           const uint32_t keep = pos < len ? 0xFFFFFFFFu : 0;
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
+          for (int i = 0; i < kVec; ++i) {
             c[i].x &= keep, c[i].y &= keep, c[i].z &= keep, c[i].w &= keep;
             // the top bit of a byte: its code is NaN
             nan |= ((c[i].x & 0x7F7F7F7Fu) + 0x01010101u) | ((c[i].y & 0x7F7F7F7Fu) + 0x01010101u) |
@@ -643,31 +658,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           nan = pos >= kv ? nan & 0x80808080u : 0;
         }
-        if (k >= 2) wait(sh.f_empty[grp], ((k >> 1) - 1) & 1);
+        if (leader && k >= 2) wait(sh.f_empty[k & 1], ((k >> 1) - 1) & 1);
+        named_barrier(6, 256);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
+        for (int i = 0; i < kVec; ++i) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint32_t lo = j ? c[i].z : c[i].x, hi = j ? c[i].w : c[i].y;
-            tc::st_shared((to ^ (((2 * i + j) & 7) << 4)) + (i >> 2) * (kTile * 128),
+            tc::st_shared(to ^ ((2 * i + j) << 4),
                           make_uint4(tc::f16x2_of_e4m3x2(lo), tc::f16x2_of_e4m3x2(lo >> 16), tc::f16x2_of_e4m3x2(hi),
                                      tc::f16x2_of_e4m3x2(hi >> 16)));
           }
         }
         if (nan) {
 #pragma unroll 1
-          for (int x = 0; x < D; ++x) {
-            const uint32_t at = (to ^ (((x >> 3) & 7) << 4)) + (x >> 6) * (kTile * 128) + (x & 7) * 2;
+          for (int x = 0; x < D / 2; ++x) {
+            const uint32_t at = (to ^ ((x >> 3) << 4)) + (x & 7) * 2;
             if ((tc::ld_shared_u16(at) & 0x7FFF) > 0x7C00) {
               tc::st_shared_u16(at, 0);
-              atomicMin(&sh.nanpos[par][x], pos);
+              atomicMin(&sh.nanpos[par][half * (D / 2) + x], pos);
             }
           }
         }
         tc::fence_smem();
-        warp_arrive(sh.f_full[grp]);
+        warp_arrive(sh.f_full[k & 1]);
       }
-      k0 += tiles;
       warp_arrive(sh.l_full[par]);
       leave(n_seg);
     }
@@ -732,6 +747,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       warp_arrive(sh.q_full);
       warp_arrive(sh.meta_full[par]);
     };
+    wait.lazy = true;
     Segment seg;
     for (int n_seg = -1;; ++n_seg) {
       // the next segment's Q, where there is one, before this one's O

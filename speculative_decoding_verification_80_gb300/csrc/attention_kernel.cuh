@@ -114,7 +114,7 @@ struct Segment {
   // columns of a buffer of S, and of one of a parity's Os
   __device__ int s_cols() const { return 256 >> buf_log2; }
   __device__ int o_cols() const { return kAttnRows >> by_log2; }
-  // Arrivals of a group's warp: all of a tile's make 16.
+  // Arrivals of a group (or of each of its warps): all of a tile's make 4 (16).
   __device__ uint32_t weight(int part) const { return m == 3 ? (part == 0 ? 2 : 1) : (m == 1 ? 4 : m == 2 ? 2 : 1); }
 };
 
@@ -247,23 +247,23 @@ __device__ __forceinline__ bool named_any(int id, int threads, bool x) {
   return r != 0;
 }
 
-// One warp of a group polls a barrier and the others wait for it at a hardware
-// barrier: polls are shared-memory accesses, and with every warp polling they
-// took a third of the pipe's cycles.
+// One warp of a group polls a barrier, with pauses, and the others wait for it
+// at a hardware barrier; where a group meets at one, one thread arrives for it.
+// An SM's barrier operations take 5 to 8 cycles each, one after the other.
 //
 // A wait that gives up once; after that the thread goes on without waiting, so
 // that every barrier still gets its arrivals, to the end of its segment.  What
 // decides how often a group of warps meets at a barrier is agreed on at one.
 struct Waiter {
   bool dead = false;
-  bool lazy = false;  // sleeps between polls
+  bool lazy = false;  // longer pauses
   __device__ __forceinline__ void operator()(const uint64_t& bar, uint32_t parity) {
     const uint32_t at = ptx::smem_addr(&bar);
     if (dead || ptx::mbar_try_wait(at, parity)) return;
     const uint32_t since = clock();
 #pragma unroll 1
     while (!ptx::mbar_try_wait(at, parity)) {
-      if (lazy) __nanosleep(200);
+      __nanosleep(lazy ? 500 : 32);
       if (static_cast<uint32_t>(clock()) - since > SPECDEC_ATTN_WAIT_CYCLES) {
         dead = true;
         break;
@@ -271,11 +271,13 @@ struct Waiter {
     }
   }
 };
+__device__ __forceinline__ void arrive(uint64_t& bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(ptx::smem_addr(&bar)), "r"(n) : "memory");
+}
 // Arrivals for the warp, after what all its threads did before.
 __device__ __forceinline__ void warp_arrive(uint64_t& bar, uint32_t n = 1) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0)
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(ptx::smem_addr(&bar)), "r"(n) : "memory");
+  if ((threadIdx.x & 31) == 0) arrive(bar, n);
 }
 
 // Nearest number of 4 significant bits; the remainder of a number of 8 has 4.
@@ -347,11 +349,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       init(sh.k_full[i], 1);
       init(sh.k_empty[i], 1);
       init(sh.v_full[i], 1);
-      init(sh.v_empty[i], 8);
+      init(sh.v_empty[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
       init(sh.s_full[i], 1);
-      init(sh.s_empty[i], 16);
+      init(sh.s_empty[i], 4);
       init(sh.p_full[i], 16);
       init(sh.pv_done[i], 1);
     }
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     for (int i = 0; i < kScaleRing; ++i) {
       init(sh.sc_full[i], 2);
-      init(sh.sc_empty[i], 16);
+      init(sh.sc_empty[i], 4);
     }
     init(sh.q_full, 4);
     init(sh.q_empty, 1);
@@ -487,7 +489,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         named_barrier(1 + grp, 128);
         tc::fence_after();
         const float ks = sc.ks[page], vs = sc.vs[page], vmax = sc.vmax;
-        warp_arrive(sh.sc_empty[k % kScaleRing], weight);
         const uint32_t s_at = s_first + buf * s_cols;
         bool renew = first;
 #pragma unroll 1
@@ -519,7 +520,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             if (leader) {
               if (!first) wait(sh.pv_done[(i - step) & ((1 << buf_log2) - 1)], turns.of(i - step, buf_log2));  // O rests
-              wait(sh.pv_done[buf], phase ^ 1);
             }
             tc::fence_after();
             named_barrier(1 + grp, 128);
@@ -578,13 +578,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           // does P stay within f16 (and the sum within 32 bits)?
           const bool over = fmaxf(top[0], top[1]) > fminf(kSlack - __log2f(vs * vinv), 60.f) || vmax > 4.f * vref;
           // (and P's buffer has been read)
-          if (renew) break;
           if (leader) wait(sh.pv_done[buf], phase ^ 1);
-          if (!named_any(1 + grp, 128, over)) break;
+          tc::fence_before();
+          if (!named_any(1 + grp, 128, over && !renew)) break;
           renew = true;
         }
-        tc::fence_before();
-        warp_arrive(sh.s_empty[buf], weight);
+        if (leader && lane == 0) {  // all have read the scores and the scales
+          arrive(sh.s_empty[buf], weight);
+          arrive(sh.sc_empty[k % kScaleRing], weight);
+        }
         first = false;
         const float vr = vs * vinv * kPScale;
         // probabilities
@@ -614,10 +616,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
   } else if (warp < kOutputWarp) {
     // ------------------------------------------------------------ V to f16
-    // A thread has one position.  Values past the last position are no numbers
-    // of the request's: zeros.  New positions are not seen by all rows: their
-    // NaN leave the product, where 0 times NaN would spoil rows that do not
-    // see them, and are noted for the output.
+    // A thread has one position, and half of its values.  Values past the last
+    // position are no numbers of the request's: zeros.  New positions are not
+    // seen by all rows: their NaN leave the product, where 0 times NaN would
+    // spoil rows that do not see them, and are noted for the output.
     tc::fewer_registers<kRegsValues>();
     const int t_in = tid & 127, half = (warp - kValueWarp) >> 2;
     const bool leader = warp == kValueWarp;
@@ -644,22 +646,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         uint4 c[kVec];
 #pragma unroll
         for (int i = 0; i < kVec; ++i) c[i] = tc::ld_shared(from ^ (i << 4));
-        warp_arrive(sh.v_empty[slot]);
-        if (++slot == a.ring) slot = 0, ++round;
         uint32_t nan = 0;
         if (pos - t_in + kTile > min(kv, len)) {
           const uint32_t keep = pos < len ? 0xFFFFFFFFu : 0;
 #pragma unroll
           for (int i = 0; i < kVec; ++i) {
             c[i].x &= keep, c[i].y &= keep, c[i].z &= keep, c[i].w &= keep;
-            // the top bit of a byte: its code is NaN
-            nan |= ((c[i].x & 0x7F7F7F7Fu) + 0x01010101u) | ((c[i].y & 0x7F7F7F7Fu) + 0x01010101u) |
-                   ((c[i].z & 0x7F7F7F7Fu) + 0x01010101u) | ((c[i].w & 0x7F7F7F7Fu) + 0x01010101u);
+            nan |= tc::e4m3_nan(c[i].x) | tc::e4m3_nan(c[i].y) | tc::e4m3_nan(c[i].z) | tc::e4m3_nan(c[i].w);
           }
           nan = pos >= kv ? nan & 0x80808080u : 0;
         }
         if (leader && k >= 2) wait(sh.f_empty[k & 1], ((k >> 1) - 1) & 1);
         named_barrier(6, 256);
+        if (leader && lane == 0) ptx::mbar_arrive(ptx::smem_addr(&sh.v_empty[slot]));
+        if (++slot == a.ring) slot = 0, ++round;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
 #pragma unroll

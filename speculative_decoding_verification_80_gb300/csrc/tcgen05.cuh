@@ -159,6 +159,8 @@ __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t codes) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
   return r;
 }
+// The top bit of each byte: whether its code is NaN.  (Other bits say nothing.)
+__device__ __forceinline__ uint32_t e4m3_nan(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; }
 
 }  // namespace tc
 }  // namespace specdec

@@ -109,7 +109,8 @@ struct Segment {
   int b, h, row0, rows;       // rows of this group
   int q0, kv, len;            // first token, positions before it, positions of the group
   int tile0, tile1, tiles;    // tiles of this part, and of the whole
-  uint32_t first;             // unit of the whole's first tile
+  uint32_t first, end;        // units of the whole
+  uint32_t per_tile;
   int m, by_log2, buf_log2;
   // columns of a buffer of S, and of one of a parity's Os
   __device__ int s_cols() const { return 256 >> buf_log2; }
@@ -134,6 +135,20 @@ struct Turns {
   }
 };
 
+// The list is cut by cost: a tile costs 4 to 6 units by its rows' 16s, and an
+// item (a row group of a head) kItemCost more, half before and half after its
+// tiles.  (Measured: 0.64, 0.72 and 0.98 us a tile of 16, 32 and 48 rows of
+// D = 128, 2 us an item.)  A cut within an item falls between tiles; one near
+// its start or end moves there.  A CTA's part is at least kLeastCost, more than
+// a tile, so that none inside an item is without a tile of it.
+constexpr int kItemCost = 12;
+constexpr int kLeastCost = 10;
+__host__ __device__ __forceinline__ uint32_t tile_cost(int rows) { return rows <= 32 ? 4 : (rows <= 48 ? 5 : 6); }
+// Tiles of an item that lie before `cost` units of it.
+__device__ __forceinline__ int tiles_before(uint32_t cost, uint32_t per_tile, int tiles) {
+  return cost <= kItemCost / 2 ? 0 : static_cast<int>(min((cost - kItemCost / 2) / per_tile, static_cast<uint32_t>(tiles)));
+}
+
 // Goes through the segments of units [u, end).
 struct Walker {
   const AttnArgs& a;
@@ -152,7 +167,10 @@ struct Walker {
   static __device__ __forceinline__ uint32_t units_per_head(const AttnArgs& a, int kv, int G, int q) {
     uint32_t n = 0;
 #pragma unroll 1
-    for (int r = 0; r < q * G; r += a.rows) n += tiles_of(length(a, kv, G, min(q * G, r + a.rows)));
+    for (int r = 0; r < q * G; r += a.rows) {
+      const int row_end = min(q * G, r + a.rows);
+      n += tiles_of(length(a, kv, G, row_end)) * tile_cost(row_end - r) + kItemCost;
+    }
     return n;
   }
   static __device__ __forceinline__ void request(const AttnArgs& a, int b, int& q0, int& q, int& kv) {
@@ -162,38 +180,47 @@ struct Walker {
     kv = __ldg(a.kv_len + b);
   }
   __device__ bool next(Segment& s) {
-    if (u >= end) return false;
 #pragma unroll 1
-    while (u - ub >= per_head * a.H) {
-      ub += per_head * a.H;
-      ++b;
-      request(a, b, q0, q, kv);
-      per_head = units_per_head(a, kv, G, q);
-    }
-    uint32_t rem = u - ub;
-    s.b = b;
-    s.h = static_cast<int>(rem / per_head);
-    rem -= s.h * per_head;
-    s.q0 = q0;
-    s.kv = kv;
-    s.row0 = 0;
+    while (u < end) {
 #pragma unroll 1
-    for (;; s.row0 += a.rows) {
-      const int row_end = min(q * G, s.row0 + a.rows);
-      s.rows = row_end - s.row0;
-      s.len = length(a, kv, G, row_end);
-      s.tiles = tiles_of(s.len);
-      if (rem < static_cast<uint32_t>(s.tiles)) break;
-      rem -= s.tiles;
+      while (u - ub >= per_head * a.H) {
+        ub += per_head * a.H;
+        ++b;
+        request(a, b, q0, q, kv);
+        per_head = units_per_head(a, kv, G, q);
+      }
+      uint32_t rem = u - ub, cost, per_tile;
+      s.b = b;
+      s.h = static_cast<int>(rem / per_head);
+      rem -= s.h * per_head;
+      s.q0 = q0;
+      s.kv = kv;
+      s.row0 = 0;
+#pragma unroll 1
+      for (;; s.row0 += a.rows) {
+        const int row_end = min(q * G, s.row0 + a.rows);
+        s.rows = row_end - s.row0;
+        s.len = length(a, kv, G, row_end);
+        s.tiles = tiles_of(s.len);
+        per_tile = tile_cost(s.rows);
+        cost = s.tiles * per_tile + kItemCost;
+        if (rem < cost) break;
+        rem -= cost;
+      }
+      s.first = u - rem;
+      s.end = s.first + cost;
+      s.per_tile = per_tile;
+      const uint32_t to = min(cost, rem + (end - u));
+      s.tile0 = tiles_before(rem, per_tile, s.tiles);
+      s.tile1 = tiles_before(to, per_tile, s.tiles);
+      u += to - rem;
+      if (s.tile0 >= s.tile1) continue;  // a cut before the first or after the last tile
+      s.m = (s.rows + 15) / 16;
+      s.by_log2 = s.m == 1 ? 2 : (s.m == 2 ? 1 : 0);
+      s.buf_log2 = s.m <= 2 ? 2 : 1;
+      return true;
     }
-    s.tile0 = static_cast<int>(rem);
-    s.tile1 = static_cast<int>(min(static_cast<uint32_t>(s.tiles), rem + (end - u)));
-    s.first = u - rem;
-    s.m = (s.rows + 15) / 16;
-    s.by_log2 = s.m == 1 ? 2 : (s.m == 2 ? 1 : 0);
-    s.buf_log2 = s.m <= 2 ? 2 : 1;
-    u += s.tile1 - s.tile0;
-    return true;
+    return false;
   }
 };
 
@@ -201,6 +228,14 @@ struct ScaleEntry {
   float ks[kMaxPages];   // key scale times the scores' factor
   float vs[kMaxPages];   // value scale
   float vmax;            // the tile's largest
+};
+
+// What the output warps know of a row.
+struct alignas(16) RowOut {
+  float4 f;     // factors of the groups' Os
+  int32_t sees; // its last position
+  int32_t at;   // its output, from the first row's token's first head of the group on
+  float sum, ref;
 };
 
 struct AttnShared {
@@ -221,10 +256,7 @@ struct AttnShared {
   float lsum[2][kGroups][4][kGroupRows];  // sums of the softmax warps
   float mrun[2][kGroups][kGroupRows];  // and their groups' references
   float vref[2][kGroups];
-  alignas(16) float of[kAttnRows][kGroups];  // factors of the groups' Os
-  float2 fin[kAttnRows];               // {sum (or its inverse), reference}
-  int32_t sees[kAttnRows];             // last position of each row
-  long long out_at[kAttnRows];         // where its output is
+  RowOut out[kAttnRows];
   int32_t nanpos[2][128];              // first new position whose value is NaN in a dimension
   ScaleEntry scales[kScaleRing];
   int32_t last;
@@ -419,8 +451,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const uint32_t w = lane < kAttnThreads / 32 ? sh.part[lane] : 0;
       const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, w);
       before = s - mine + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0);
-      chunk = (total + gridDim.x - 1) / gridDim.x;
-      u0 = min(total, blockIdx.x * chunk);
+      chunk = max((total + gridDim.x - 1) / gridDim.x, static_cast<uint32_t>(kLeastCost));
+      u0 = min(static_cast<unsigned long long>(total), static_cast<unsigned long long>(blockIdx.x) * chunk);
       u1 = min(total, u0 + chunk);
       if (u0 >= u1 || before > u0 || u0 >= before + mine) break;
     }
@@ -791,73 +823,82 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             f[j] = w * sh.vref[par][g];
           }
         }
-        if (whole) sum = sum == 0.f ? 0.f : 1.f / sum;
-        *reinterpret_cast<float4*>(sh.of[ot]) = make_float4(f[0], f[1], f[2], f[3]);
-        sh.fin[ot] = make_float2(sum, M);
+        const float scale = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
         const int row = seg.row0 + ot, tok = row / G;
-        sh.sees[ot] = seg.kv + tok;
-        sh.out_at[ot] = (static_cast<long long>(seg.q0 + tok) * a.Hq + seg.h * G + (row - tok * G)) * D;
+        RowOut& ro = sh.out[ot];
+        ro.f = make_float4(f[0] * scale, f[1] * scale, f[2] * scale, f[3] * scale);
+        ro.sees = seg.kv + tok;
+        ro.at = ((tok - seg.row0 / G) * a.Hq + row - tok * G) * D;
+        ro.sum = sum;
+        ro.ref = M;
       }
       named_barrier(5, 128);
       wait(sh.o_full[par], (n_seg >> 1) & 1);
       tc::fence_after();
       const int nan_at = sh.nanpos[par][d];
-      const int slot = static_cast<int>(blockIdx.x) * 2 + (n_seg == 0 ? 0 : 1);
-      float* rec = a.partial + static_cast<long long>(slot) * kPartialFloats;
+      // a CTA's records: of an item from before, and of one that begins here
+      const int slot = static_cast<int>(blockIdx.x) * 2 + (seg.tile0 == 0 ? 1 : 0);
+      float* rec = a.partial + static_cast<size_t>(slot) * kPartialFloats;
+      __nv_bfloat16* dst = a.out + (static_cast<long long>(seg.q0 + seg.row0 / G) * a.Hq + seg.h * G) * D;
       const uint32_t o_at = tmem + (static_cast<uint32_t>(ow * 32) << 16) + kOutAt + par * kAttnRows;
 #pragma unroll 1
       for (int c = 0; c < seg.rows; c += 8) {
         float v[8];
+        tc::ld8(o_at + c, v);
+        tc::wait_ld();
+        tc::ready(v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        for (int e = 0; e < 8; ++e) {
+          const float f = sh.out[c + e].f.x;
+          v[e] = f != 0.f ? v[e] * f : 0.f;
+        }
 #pragma unroll 1
-        for (int j = 0; j < by_tile; j += 2) {  // two groups' Os
-          float y[8], z[8];
+        for (int j = 1; j < by_tile; ++j) {  // the other groups' Os
+          float y[8];
           tc::ld8(o_at + j * o_cols + c, y);
-          if (by_tile > 1) tc::ld8(o_at + (j + 1) * o_cols + c, z);
           tc::wait_ld();
           tc::ready(y);
-          tc::ready(z);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float2 f = *reinterpret_cast<const float2*>(&sh.of[c + e][j]);
-            if (f.x != 0.f) v[e] = fmaf(y[e], f.x, v[e]);
-            if (f.y != 0.f) v[e] = fmaf(z[e], f.y, v[e]);
+            const float f = reinterpret_cast<const float*>(&sh.out[c + e].f)[j];
+            if (f != 0.f) v[e] = fmaf(y[e], f, v[e]);
           }
         }
-        const int rows = min(8, seg.rows - c);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (nan_at <= sh.sees[c + e]) v[e] = __uint_as_float(0x7FFFFFFFu);
-        if (whole) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e < rows && owns) a.out[sh.out_at[c + e] + d] = __float2bfloat16_rn(v[e] * sh.fin[c + e].x);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e < rows && owns) rec[(c + e) * D + d] = v[e];
+        for (int e = 0; e < 8; ++e) {
+          const RowOut& ro = sh.out[c + e];
+          if (nan_at <= ro.sees) v[e] = __uint_as_float(0x7FFFFFFFu);
+          if (c + e < seg.rows && owns) {
+            if (whole)
+              dst[ro.at + d] = __float2bfloat16_rn(v[e]);
+            else
+              rec[(c + e) * D + d] = v[e];
+          }
         }
       }
       tc::fence_before();
       warp_arrive(sh.o_empty[par]);
       if (!whole) {
         if (ot < seg.rows) {
-          rec[kAttnRows * 128 + ot] = sh.fin[ot].y;
-          rec[kAttnRows * 128 + kAttnRows + ot] = sh.fin[ot].x;
+          rec[kAttnRows * 128 + ot] = sh.out[ot].ref;
+          rec[kAttnRows * 128 + kAttnRows + ot] = sh.out[ot].sum;
         }
         // the last of the item's CTAs joins the parts
-        const uint32_t c0 = seg.first / chunk, c1 = (seg.first + seg.tiles - 1) / chunk;
-        __threadfence();
+        // (the item's first and last CTA may have no tile of it)
+        uint32_t c0 = seg.first / chunk, c1 = (seg.end - 1) / chunk;
+        const uint32_t home = c0;
+        if (tiles_before((c0 + 1) * chunk - seg.first, seg.per_tile, seg.tiles) == 0) ++c0;
+        if (c1 > home && tiles_before(c1 * chunk - seg.first, seg.per_tile, seg.tiles) == seg.tiles) --c1;
         named_barrier(5, 128);
-        if (ot == 0) sh.last = ptx::atom_add_acq_rel(a.counters + c0, 1u) == c1 - c0;
+        if (ot == 0) {
+          __threadfence();
+          sh.last = ptx::atom_add_acq_rel(a.counters + home, 1u) == c1 - c0;
+        }
         named_barrier(5, 128);
         if (sh.last) {
-          __threadfence();
           const int pieces = static_cast<int>(c1 - c0) + 1;
-          const int first_slot = static_cast<int>(c0) * 2 + (seg.first % chunk == 0 ? 0 : 1);
           auto record = [&](int p) {
-            return a.partial + static_cast<size_t>(p == 0 ? first_slot : static_cast<int>(c0 + p) * 2) * kPartialFloats;
+            return a.partial + static_cast<size_t>((c0 + p) * 2 + (p == 0 ? 1 : 0)) * kPartialFloats;
           };
           constexpr int E = D / 32;  // a lane's values
 #pragma unroll 1
@@ -920,7 +961,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               const int r = r4 + ow + 4 * j;
               if (r >= seg.rows) break;
               const float inv = sum[j] == 0.f ? 0.f : 1.f / sum[j];
-              uint32_t* to = reinterpret_cast<uint32_t*>(a.out + sh.out_at[r] + lane * E);
+              uint32_t* to = reinterpret_cast<uint32_t*>(dst + sh.out[r].at + lane * E);
 #pragma unroll
               for (int i = 0; i < E; i += 2) {
                 const __nv_bfloat162 y = __floats2bfloat162_rn(acc[j][i] * inv, acc[j][i + 1] * inv);
@@ -928,7 +969,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               }
             }
           }
-          if (ot == 0) ptx::st_relaxed_u32(a.counters + c0, 0u);
+          if (ot == 0) ptx::st_relaxed_u32(a.counters + home, 0u);
         }
       }
       leave(n_seg);
@@ -1000,10 +1041,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const uint32_t dst = ptx::smem_addr(tiles + slot * L::kTileBytes);
           if (tc::elect()) ptx::mbar_arrive_expect_tx(bar, pages * a.bs * D);
           __syncwarp();
-#pragma unroll 1
-          for (int j = 0; j < pages; ++j) {
-            const int id = __shfl_sync(0xFFFFFFFFu, now.id, first + j);
-            if (tc::elect()) tc::load_4d(dst + j * a.bs * D, map, 0, 0, now.h, id, bar);
+          int ids[kMaxPages];
+#pragma unroll
+          for (int j = 0; j < kMaxPages; ++j) ids[j] = __shfl_sync(0xFFFFFFFFu, now.id, (first + j) & 31);
+          if (tc::elect()) {
+#pragma unroll
+            for (int j = 0; j < kMaxPages; ++j)
+              if (j < pages) tc::load_4d(dst + j * a.bs * D, map, 0, 0, now.h, ids[j], bar);
           }
           __syncwarp();
           if (++slot == a.ring) slot = 0, ++round;

@@ -295,10 +295,11 @@ extern "C" specdec_status_t spec_attention(const void* q, int64_t q_token_stride
     return SPECDEC_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < SPECDEC_ATTENTION_WORKSPACE_BYTES)
     return SPECDEC_ERR_WORKSPACE;
-  // The kernel counts tiles of positions, over row groups and heads, in 31 bits.
+  // The kernel counts the cost of tiles of positions, over row groups and
+  // heads, in 31 bits.
   const int64_t groups = static_cast<int64_t>(T) * (Hq / H) / kAttnRows + (T < B ? T : B) + 1;
-  const int64_t most_tiles = (static_cast<int64_t>(max_blocks) * block_size + kTile - 1) / kTile;
-  if (groups > INT32_MAX / H || groups * H > INT32_MAX / most_tiles) return SPECDEC_ERR_UNSUPPORTED;
+  const int64_t most_cost = (static_cast<int64_t>(max_blocks) * block_size + kTile - 1) / kTile * tile_cost(kAttnRows) + kItemCost;
+  if (groups > INT32_MAX / H || groups * H > INT32_MAX / most_cost) return SPECDEC_ERR_UNSUPPORTED;
   AttnArgs a;
   memset(&a, 0, sizeof a);
   a.q = static_cast<const __nv_bfloat16*>(q);

@@ -253,7 +253,7 @@ struct AttnShared {
   float fac[kGroups][kGroupRows];      // factors from a row's reference to its next
   float qs[2][kAttnRows];
   int32_t limit[2][kAttnRows];         // last position a row attends to
-  float lsum[2][kGroups][4][kGroupRows];  // sums of the softmax warps
+  alignas(16) float lsum[2][kGroups][kGroupRows][4];  // sums of the softmax warps
   float mrun[2][kGroups][kGroupRows];  // and their groups' references
   float vref[2][kGroups];
   RowOut out[kAttnRows];
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               tc::ready(rest);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                float y = (v[e] + rest[e]) * ks * sh.col[grp][c + e].x;
+                float y = (v[e] + rest[e]) * ks;
                 if (masked && pos > sh.limit[par][r0 + c + e]) y = -INFINITY;
                 y = tc::warp_max(y);
                 if (lane == e) mine = y;
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             named_barrier(1 + grp, 128);
             if (t_in < kGroupRows) {
               const float m = fmaxf(fmaxf(sh.wmax[grp][0][t_in], sh.wmax[grp][1][t_in]),
-                                    fmaxf(sh.wmax[grp][2][t_in], sh.wmax[grp][3][t_in]));
+                                    fmaxf(sh.wmax[grp][2][t_in], sh.wmax[grp][3][t_in])) * sh.col[grp][t_in].x;
               const float was = sh.col[grp][t_in].y;
               const float now = first ? (m > -INFINITY ? m : 0.f) : fmaxf(was, m);
               sh.col[grp][t_in].y = now;
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       turns.pass(tiles, buf_log2);
       // sums and references for the output warps
       const float s = warp_sums16(l);
-      if ((lane & 1) == 0) sh.lsum[par][grp][warp & 3][lane >> 1] = s;
+      if ((lane & 1) == 0) sh.lsum[par][grp][lane >> 1][warp & 3] = s;
       if (t_in < kGroupRows) sh.mrun[par][grp][t_in] = sh.col[grp][t_in].y;
       if (t_in == 0) sh.vref[par][grp] = vref / kPScale;
       warp_arrive(sh.l_full[par]);
@@ -725,7 +725,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int d = D == 128 ? ot : 16 * ow + (lane & 15);
     const bool owns = D == 128 || lane < 16;
     constexpr int kVec = D / 16;  // 16-byte loads of half a row
-    uint4 qv[kVec];
+    uint4 qv[kVec];   // a thread's values of Q, then their codes and remainders
+    float q_scale;    // of its row
     const int qr = ot >> 1, half = ot & 1;  // two threads a row of Q
     auto load_q = [&](const Segment& s) {
       const int row = s.row0 + min(qr, s.rows - 1);
@@ -733,45 +734,49 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                                       half * (D / 2));
 #pragma unroll
       for (int i = 0; i < kVec; ++i) qv[i] = __ldg(p + i);
+      // the largest magnitude's bits (bf16 in both halves; no number is above infinity)
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        top = __vmaxu2(top, __vmaxu2(qv[i].x & 0x7FFF7FFFu, qv[i].y & 0x7FFF7FFFu));
+        top = __vmaxu2(top, __vmaxu2(qv[i].z & 0x7FFF7FFFu, qv[i].w & 0x7FFF7FFFu));
+      }
+      top = max(top >> 16, top & 0xFFFFu);
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      const bool bad = top >= 0x7F80u;
+      const float sc = pow2_scale(__uint_as_float(top << 16)), inv = qr < s.rows && !bad ? pow2_inverse(sc) : 0.f;
+      q_scale = bad ? __uint_as_float(0x7FFFFFFFu) : (sc > 0.f ? sc : 1.f);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        float f[8];
+        unpack16<__nv_bfloat16>(qv[i], f);
+        uint32_t hw[2], lw[2];
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          float u[4], h[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            u[j] = bad ? 0.f : f[e + j] * inv;
+            h[j] = top4(u[j]);
+          }
+          hw[e >> 2] = tc::e4m3x2(h[0], h[1]) | (tc::e4m3x2(h[2], h[3]) << 16);
+          lw[e >> 2] = tc::e4m3x2(u[0] - h[0], u[1] - h[1]) | (tc::e4m3x2(u[2] - h[2], u[3] - h[3]) << 16);
+        }
+        qv[i] = make_uint4(hw[0], hw[1], lw[0], lw[1]);
+      }
     };
     auto store_q = [&](const Segment& s, int par) {
       if (qr < 16 * s.m) {
-        // the largest magnitude's bits (bf16 in both halves; no number is above infinity)
-        uint32_t top = 0;
+        // 8 rows x 16 bytes lie together, then the rows' next 16 bytes
+        unsigned char* to = q_at + (qr >> 3) * (8 * D) + half * (D / 32 * 128) + (qr & 7) * 16;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          top = __vmaxu2(top, qv[i].x & 0x7FFF7FFFu);
-          top = __vmaxu2(top, qv[i].y & 0x7FFF7FFFu);
-          top = __vmaxu2(top, qv[i].z & 0x7FFF7FFFu);
-          top = __vmaxu2(top, qv[i].w & 0x7FFF7FFFu);
-        }
-        top = max(top >> 16, top & 0xFFFFu);
-        top = max(top, __shfl_xor_sync(3u << (lane & 30), top, 1));
-        const bool in = qr < s.rows, bad = top >= 0x7F80u;
-        const float sc = pow2_scale(__uint_as_float(top << 16)), inv = bad || !in ? 0.f : pow2_inverse(sc);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          float f[8];
-          uint32_t hw[2] = {0, 0}, lw[2] = {0, 0};
-          if (!bad) {
-            unpack16<__nv_bfloat16>(qv[i], f);
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const float u = f[e] * inv, v = f[e + 1] * inv;
-              const float uh = top4(u), vh = top4(v);
-              hw[e >> 2] |= tc::e4m3x2(uh, vh) << (8 * (e & 2));
-              lw[e >> 2] |= tc::e4m3x2(u - uh, v - vh) << (8 * (e & 2));
-            }
-          }
-          // 8 rows x 16 bytes lie together, then the rows' next 16 bytes
-          const int at_x = half * (D / 2) + i * 8;
-          const int at = (qr >> 3) * (8 * D) + (at_x >> 4) * 128 + (qr & 7) * 16 + (at_x & 15);
-          *reinterpret_cast<uint2*>(q_at + at) = make_uint2(hw[0], hw[1]);
-          *reinterpret_cast<uint2*>(q_at + s.m * 16 * D + at) = make_uint2(lw[0], lw[1]);
+        for (int i = 0; i < kVec; i += 2) {
+          *reinterpret_cast<uint4*>(to + i / 2 * 128) = make_uint4(qv[i].x, qv[i].y, qv[i + 1].x, qv[i + 1].y);
+          *reinterpret_cast<uint4*>(to + s.m * 16 * D + i / 2 * 128) = make_uint4(qv[i].z, qv[i].w, qv[i + 1].z, qv[i + 1].w);
         }
         if (half == 0) {
-          sh.qs[par][qr] = bad ? __uint_as_float(0x7FFFFFFFu) : (sc > 0.f ? sc : 1.f);
-          sh.limit[par][qr] = in ? min(s.kv + (s.row0 + qr) / G, s.len - 1) : -1;
+          sh.qs[par][qr] = q_scale;
+          sh.limit[par][qr] = qr < s.rows ? min(s.kv + (s.row0 + qr) / G, s.len - 1) : -1;
         }
       }
       sh.nanpos[par][ot] = 0x7FFFFFFF;
@@ -802,26 +807,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (ot < seg.rows) {
         // a group whose sum is 0 has nothing, whatever its reference and O
         const int r = ot % kGroupRows, part = ot / kGroupRows, parts = kGroups >> seg.by_log2;
-        float s[kGroups], M = -INFINITY, f[kGroups], sum = 0.f;
+        float s[kGroups], m[kGroups], M = -INFINITY, f[kGroups], sum = 0.f;
 #pragma unroll
         for (int j = 0; j < kGroups; ++j) {
-          s[j] = 0.f;
-          const int g = j * parts + part;  // of turn j
-          if (j < by_tile) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) s[j] += sh.lsum[par][g][w][r];
-            if (s[j] != 0.f) M = fmaxf(M, sh.mrun[par][g][r]);
-          }
+          const int g = (j * parts + part) & (kGroups - 1);  // of turn j
+          const float4 w = *reinterpret_cast<const float4*>(sh.lsum[par][g][r]);
+          s[j] = j < by_tile ? (w.x + w.y) + (w.z + w.w) : 0.f;
+          m[j] = s[j] != 0.f ? sh.mrun[par][g][r] : -INFINITY;
+          f[j] = sh.vref[par][g];
+          M = fmaxf(M, m[j]);
         }
 #pragma unroll
         for (int j = 0; j < kGroups; ++j) {
-          f[j] = 0.f;
-          const int g = j * parts + part;
-          if (s[j] != 0.f) {
-            const float w = tc::ex2(sh.mrun[par][g][r] - M);
-            sum += w * s[j];
-            f[j] = w * sh.vref[par][g];
-          }
+          const float w = s[j] != 0.f ? tc::ex2(m[j] - M) : 0.f;
+          sum = s[j] != 0.f ? fmaf(w, s[j], sum) : sum;
+          f[j] = s[j] != 0.f ? w * f[j] : 0.f;
         }
         const float scale = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
         const int row = seg.row0 + ot, tok = row / G;
@@ -841,39 +841,45 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       float* rec = a.partial + static_cast<size_t>(slot) * kPartialFloats;
       __nv_bfloat16* dst = a.out + (static_cast<long long>(seg.q0 + seg.row0 / G) * a.Hq + seg.h * G) * D;
       const uint32_t o_at = tmem + (static_cast<uint32_t>(ow * 32) << 16) + kOutAt + par * kAttnRows;
+      __nv_bfloat16* dst_d = dst + d;
+      float* rec_d = rec + d;
 #pragma unroll 1
       for (int c = 0; c < seg.rows; c += 8) {
-        float v[8];
+        float v[8], f[8];
+        int at[8];
         tc::ld8(o_at + c, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = sh.out[c + e].f.x;
         tc::wait_ld();
         tc::ready(v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float f = sh.out[c + e].f.x;
-          v[e] = f != 0.f ? v[e] * f : 0.f;
-        }
+        for (int e = 0; e < 8; ++e) v[e] = f[e] != 0.f ? v[e] * f[e] : 0.f;
 #pragma unroll 1
         for (int j = 1; j < by_tile; ++j) {  // the other groups' Os
           float y[8];
           tc::ld8(o_at + j * o_cols + c, y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = reinterpret_cast<const float*>(&sh.out[c + e].f)[j];
           tc::wait_ld();
           tc::ready(y);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float f = reinterpret_cast<const float*>(&sh.out[c + e].f)[j];
-            if (f != 0.f) v[e] = fmaf(y[e], f, v[e]);
-          }
+          for (int e = 0; e < 8; ++e) v[e] = f[e] != 0.f ? fmaf(y[e], f[e], v[e]) : v[e];
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const RowOut& ro = sh.out[c + e];
-          if (nan_at <= ro.sees) v[e] = __uint_as_float(0x7FFFFFFFu);
-          if (c + e < seg.rows && owns) {
-            if (whole)
-              dst[ro.at + d] = __float2bfloat16_rn(v[e]);
-            else
-              rec[(c + e) * D + d] = v[e];
-          }
+          const int2 ro = *reinterpret_cast<const int2*>(&sh.out[c + e].sees);
+          at[e] = ro.y;
+          v[e] = nan_at <= ro.x ? __uint_as_float(0x7FFFFFFFu) : v[e];
+        }
+        const int rows = owns ? seg.rows - c : 0;
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < rows) dst_d[at[e]] = __float2bfloat16_rn(v[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < rows) rec_d[(c + e) * D] = v[e];
         }
       }
       tc::fence_before();

@@ -28,22 +28,43 @@ specdec_status_t check_cache(int32_t num_blocks, int32_t block_size, int32_t H, 
   return SPECDEC_OK;
 }
 
-template <typename Elt, bool kVec>
-cudaError_t launch_logits(const LogitArgs& a, cudaStream_t st) {
-  const int smem = a.share * 4;
-  static bool ready[64] = {false};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+// SMs of the current device, which is asked once.
+cudaError_t device_sms(int* dev, int* sms) {
+  static int known[64] = {0};
+  cudaError_t e = cudaGetDevice(dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (*dev < 0 || *dev >= 64) return cudaErrorInvalidDevice;
+  if (known[*dev] == 0) {
+    int n = 0;
+    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev);
+    if (e != cudaSuccess) return e;
+    known[*dev] = n;
+  }
+  *sms = known[*dev];
+  return cudaSuccess;
+}
+
+constexpr int kSmSmem = 228 * 1024;  // of an SM; a CTA takes 1 KB more than it asks for
+
+template <typename Elt>
+cudaError_t launch_logits(LogitArgs a, cudaStream_t st) {
+  using L = LogitLayout<Elt>;
+  static bool ready[64] = {false};
+  int dev = 0, sms = 0;
+  cudaError_t e = device_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
   if (!ready[dev]) {
-    e = cudaFuncSetAttribute(process_logits_kernel<Elt, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             SPECDEC_MAX_VOCAB / kLogitCtas * 4);
+    e = cudaFuncSetAttribute(process_logits_kernel<Elt>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes(kLogitShare));
     if (e != cudaSuccess) return e;
     ready[dev] = true;
   }
-  process_logits_kernel<Elt, kVec>
-      <<<dim3(static_cast<unsigned>(a.B) * kLogitCtas, static_cast<unsigned>(a.row_step)), kLogitThreads, smem, st>>>(a);
+  // Few requests are cut finer, until every SM has work.
+  a.share = kLogitShare;
+  while (a.share > kLogitLeastShare && static_cast<int64_t>(a.B) * ((a.V + a.share - 1) / a.share) < 4 * sms) a.share /= 2;
+  a.chunks = (a.V + a.share - 1) / a.share;
+  const int per_sm = kSmSmem / (L::bytes(a.share) + static_cast<int>(sizeof(LogitShared)) + 1024);
+  const int64_t items = static_cast<int64_t>(a.B) * a.chunks, most = static_cast<int64_t>(sms) * (per_sm < 4 ? per_sm : 4);
+  process_logits_kernel<Elt><<<static_cast<unsigned>(items < most ? items : most), kLogitThreads, L::bytes(a.share), st>>>(a);
   return cudaGetLastError();
 }
 
@@ -85,23 +106,19 @@ cudaError_t launch_attention(AttnArgs a, const void* k_cache, const void* v_cach
   cudaError_t e = cache_map(&km, k_cache, D, a.bs, a.H, a.num_blocks);
   if (e == cudaSuccess) e = cache_map(&vm, v_cache, D, a.bs, a.H, a.num_blocks);
   if (e != cudaSuccess) return e;
-  static int sms[64] = {0};
-  int dev = 0;
-  e = cudaGetDevice(&dev);
+  static bool ready[64] = {false};
+  int dev = 0, sms = 0;
+  e = device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (sms[dev] == 0) {
+  if (!ready[dev]) {
     e = cudaFuncSetAttribute(attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem);
     if (e != cudaSuccess) return e;
-    int n = 0;
-    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    sms[dev] = n;
+    ready[dev] = true;
   }
   using L = AttnLayout<D>;
   const int fit = (kAttnSmem - L::bytes(0, a.rows)) / (2 * L::kTileBytes);
   a.ring = fit < kMaxRing ? fit : kMaxRing;
-  const int grid = sms[dev] < kAttnMaxCtas ? sms[dev] : kAttnMaxCtas;
+  const int grid = sms < kAttnMaxCtas ? sms : kAttnMaxCtas;
   attention_kernel<D><<<grid, kAttnThreads, L::bytes(a.ring, a.rows), st>>>(a, km, vm);
   return cudaGetLastError();
 }
@@ -156,15 +173,9 @@ extern "C" specdec_status_t spec_process_logits(
   a.mask_words = (V + 31) / 32;
   a.mask_rows = mask_rows;
   a.err = error_word;
-  a.share = ((V + kLogitCtas - 1) / kLogitCtas + 31) / 32 * 32;
-  a.row_step = 1;
-  const bool vec = static_cast<uintptr_t>(V) * elt % 16 == 0 && aligned(logits, 16) && aligned(out, 16);
+  a.same_phase = ((reinterpret_cast<uintptr_t>(logits) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0 ? 1 : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (dtype == SPECDEC_F32)
-    e = vec ? launch_logits<float, true>(a, st) : launch_logits<float, false>(a, st);
-  else
-    e = vec ? launch_logits<__nv_bfloat16, true>(a, st) : launch_logits<__nv_bfloat16, false>(a, st);
+  const cudaError_t e = dtype == SPECDEC_F32 ? launch_logits<float>(a, st) : launch_logits<__nv_bfloat16>(a, st);
   return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 

@@ -2,17 +2,23 @@
 // verify step reads (spec_process_logits).
 //
 // Few entries of a row change by a penalty or a bias: those of tokens that the
-// request's history, drafts or biases name.  So the rows go through shared
-// memory as they are, by bulk copies in and out, and only the named entries
-// (and the masked ones) are touched there.
+// request's history, drafts or biases name.  An item is a request and `share`
+// neighbouring entries of the vocabulary; a CTA (one an SM) works on its items
+// in four roles, which run ahead of one another:
 //
-// An item is a request and `share` neighbouring entries of the vocabulary.  A
-// CTA counts the item's tokens in shared memory, a 32-bit word an entry, and
-// lists those it meets; every CTA reads the whole history of its item's request
-// (from L2, after the first).  Then the item's rows pass through a ring of
-// buffers, one load ahead and one store behind the row in work.  In place, a
-// row without a mask is not copied at all: its named entries are changed where
-// they lie.  Bound by the rows' bytes, read and written once.
+//   - a warp copies the items' part of each row, and of its mask, into a ring
+//     in shared memory;
+//   - two teams of four warps take turns in counting the coming items' entries
+//     in the history (a 32-bit word an entry), and list those they meet: every
+//     item reads the whole history of its request, from L2 after the first;
+//   - two teams of eight warps take turns in the rows: they change the listed
+//     entries, a thread each, and set masked ones to -infinity;
+//   - a warp copies the rows out.
+//
+// In place, a row without a mask is not copied: its entries are changed where
+// they lie.  Bound by the rows' bytes, read and written once.  (With an item's
+// steps one after the other, the copies' and the history's latencies took twice
+// the time, however many CTAs an SM had.)
 #pragma once
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -21,11 +27,13 @@
 
 namespace specdec {
 
-constexpr int kLogitThreads = 256;
-constexpr int kLogitRing = 3;        // rows in shared memory
-constexpr int kLogitShare = 4096;    // most entries of an item
-constexpr int kLogitLeastShare = 512;
-constexpr int kBiasList = 512;       // biases of an item kept in shared memory
+constexpr int kLogitTeam = 256;          // threads of a team of the rows
+constexpr int kCountTeam = 128;          // and of one that counts
+constexpr int kLogitThreads = 2 * kLogitTeam + 2 * kCountTeam + 64;
+constexpr int kLogitRowBytes = 16384;    // of a row of an item, at most
+constexpr int kLogitLeastBytes = 1024;
+constexpr int kLogitRing = 6;            // rows in shared memory
+constexpr int kBiasList = 256;           // biases of an item kept in shared memory
 constexpr uint32_t kInPrompt = 1u << 31;
 constexpr uint32_t kHasBias = 1u << 30;
 constexpr uint32_t kIsDraft = 1u << 29;
@@ -34,7 +42,6 @@ constexpr uint32_t kCountMask = kIsDraft - 1;
 #ifndef SPECDEC_LOGIT_WAIT_CYCLES
 #define SPECDEC_LOGIT_WAIT_CYCLES 2000000000ll
 #endif
-
 struct LogitArgs {
   const void* logits;
   void* out;
@@ -77,11 +84,28 @@ __device__ __forceinline__ float elt_to_float(__nv_bfloat16 x) { return __bfloat
 __device__ __forceinline__ void float_to_elt(float x, float& y) { y = x; }
 __device__ __forceinline__ void float_to_elt(float x, __nv_bfloat16& y) { y = __float2bfloat16_rn(x); }
 
-// What an item needs to know of its request, as it stands in the arrays.
+// Sets the entries of 16 bytes whose bit is 0 to -infinity.
+template <typename Elt>
+__device__ __forceinline__ void mask_vector(uint4& y, uint32_t allow) {
+  uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (sizeof(Elt) == 4) {
+      if (!(allow >> i & 1)) w[i] = 0xFF800000u;
+    } else {
+      const uint32_t keep = (allow >> 2 * i & 1) * 0xFFFFu | (allow >> (2 * i + 1) & 1) * 0xFFFF0000u;
+      w[i] = (w[i] & keep) | (0xFF80FF80u & ~keep);
+    }
+  }
+  y = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// What is known of a request, brought into range.
 struct LogitRequest {
   int32_t drafts, history, prompt, lo, hi;
   LogitParams p;
-  __device__ __forceinline__ void load(const LogitArgs& a, int b) {
+  bool bad;
+  __device__ __forceinline__ LogitRequest(const LogitArgs& a, int b) {
     drafts = a.draft_len != nullptr ? __ldg(a.draft_len + b) : a.n_max;
     p.rep = a.repetition != nullptr ? __ldg(a.repetition + b) : 1.f;
     p.pres = a.presence != nullptr ? __ldg(a.presence + b) : 0.f;
@@ -90,11 +114,7 @@ struct LogitRequest {
     prompt = a.history_stride > 0 ? __ldg(a.prompt_len + b) : 0;
     lo = a.bias_offsets != nullptr ? __ldg(a.bias_offsets + b) : 0;
     hi = a.bias_offsets != nullptr ? __ldg(a.bias_offsets + b + 1) : 0;
-  }
-  __device__ __forceinline__ static int rows(const LogitArgs& a, int drafts) { return max(0, min(drafts, a.n_max)) + 1; }
-  // Brings all into range; whether something was out of it.
-  __device__ __forceinline__ bool mend(const LogitArgs& a) {
-    bool bad = drafts < 0 || drafts > a.n_max;
+    bad = drafts < 0 || drafts > a.n_max;
     drafts = max(0, min(drafts, a.n_max));
     if (!(p.rep > 0.f) || isinf(p.rep)) bad = true, p.rep = 1.f;
     if (!isfinite(p.pres)) bad = true, p.pres = 0.f;
@@ -107,307 +127,381 @@ struct LogitRequest {
       lo = max(0, min(lo, a.num_bias));
       hi = max(lo, min(hi, a.num_bias));
     }
-    return bad;
   }
 };
 
-struct LogitShared {
-  uint64_t full[kLogitRing];
-  int32_t listed;            // entries of the list
-  int32_t biases;            // of the item
+// An item as the second role leaves it to the third and fourth.
+struct LogitItem {
+  LogitParams p;
+  int32_t rows, lo, hi;
+  int32_t listed;                       // entries of the list
+  int32_t biases;                       // of the item's entries
   int32_t draft[SPECDEC_MAX_DRAFT];
-  int32_t bias_at[kBiasList];  // entry, from the item's first on
-  float bias[kBiasList];       // value
-  float bias_sum[kBiasList];   // of the entry from here on
-  uint8_t bias_first[kBiasList];  // none of the entry's is before it
+  int32_t mask[SPECDEC_MAX_DRAFT + 1];  // of the rows, -1 for none
+  int32_t bias_at[kBiasList];           // entry, from the item's first on
+  float bias[kBiasList];                // value
+  float bias_sum[kBiasList];            // of the entry from here on
+  bool bias_first[kBiasList];           // none of the entry's is before it
+};
+struct LogitShared {
+  uint64_t row_full[kLogitRing], row_done[kLogitRing], row_empty[kLogitRing], item_full[2], item_empty[2];
+  LogitItem item[2];
 };
 
+// Dynamic shared memory: words of two items, the rows, the lists of two items.
 template <typename Elt>
 struct LogitLayout {
+  // a row may start anywhere in its first 16 bytes
   static __host__ __device__ int row_bytes(int share) { return share * static_cast<int>(sizeof(Elt)) + 16; }
-  static __host__ __device__ int bytes(int share) { return share * 6 + kLogitRing * row_bytes(share); }
+  // a row's mask may start at any word of 16 bytes
+  static __host__ __device__ int slot_bytes(int share) { return row_bytes(share) + share / 8 + 32; }
+  static __host__ __device__ int bytes(int share) { return 2 * share * 6 + kLogitRing * slot_bytes(share); }
 };
 
+__device__ __forceinline__ void logit_barrier(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
 template <typename Elt>
-__global__ void __launch_bounds__(kLogitThreads, 4) process_logits_kernel(const LogitArgs a) {
-  extern __shared__ __align__(16) unsigned char raw[];
+__global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const LogitArgs a) {
+  extern __shared__ __align__(16) uint32_t words_of[];
   __shared__ LogitShared sh;
-  constexpr int kElt = sizeof(Elt);
-  constexpr int N = 16 / kElt;
-  uint32_t* words = reinterpret_cast<uint32_t*>(raw);
-  unsigned char* ring = raw + a.share * 4;
-  const int row_bytes = LogitLayout<Elt>::row_bytes(a.share);
-  uint16_t* list = reinterpret_cast<uint16_t*>(ring + kLogitRing * row_bytes);
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int items = a.B * a.chunks;
-  const int rows_max = a.n_max + 1;
+  constexpr int kElt = sizeof(Elt), N = 16 / kElt;
+  const int row_bytes = LogitLayout<Elt>::row_bytes(a.share), slot_bytes = LogitLayout<Elt>::slot_bytes(a.share);
+  unsigned char* ring = reinterpret_cast<unsigned char*>(words_of + 2 * a.share);
+  uint16_t* list_of = reinterpret_cast<uint16_t*>(ring + kLogitRing * slot_bytes);
+  const int rows_max = a.n_max + 1, items = a.B * a.chunks, grid = gridDim.x;
   const bool in_place = a.out == a.logits;
-  const char* in_base = static_cast<const char*>(a.logits);
-  const uintptr_t in_first = reinterpret_cast<uintptr_t>(in_base);
+  const uintptr_t in_first = reinterpret_cast<uintptr_t>(a.logits);
   const uintptr_t in_end = in_first + static_cast<unsigned long long>(a.B) * rows_max * a.V * kElt;
-  bool dead = false;
-
-  // byte of entry v0 of row j of request b
-  auto at = [&](int b, int j, int v0) { return ((static_cast<long long>(b) * rows_max + j) * a.V + v0) * kElt; };
-
-  if (tid == 0) {
-    for (int i = 0; i < kLogitRing; ++i) ptx::mbar_init(ptx::smem_addr(&sh.full[i]), 1);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kLogitRing; ++i) {
+      ptx::mbar_init(ptx::smem_addr(&sh.row_full[i]), 1);
+      ptx::mbar_init(ptx::smem_addr(&sh.row_done[i]), kLogitTeam / 32);
+      ptx::mbar_init(ptx::smem_addr(&sh.row_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(ptx::smem_addr(&sh.item_full[i]), 1);
+      ptx::mbar_init(ptx::smem_addr(&sh.item_empty[i]), 2 * kLogitTeam / 32 + 1);
+      sh.item[i].listed = 0;
+    }
     ptx::fence_mbarrier_init();
-    sh.listed = 0;
   }
-  for (int i = tid; i < a.share / 4; i += kLogitThreads) reinterpret_cast<uint4*>(words)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < a.share / 2; i += kLogitThreads) reinterpret_cast<uint4*>(words_of)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
 
-  // The first warp goes ahead through the rows that are copied, in order.
-  int next_item = blockIdx.x;  // of the coming rows
-  unsigned long long next_rows = 0;
-  bool next_last = false;      // row 64 is one of them
-  int ahead_drafts = 0, ahead_mask[2] = {-1, -1};  // of the item after that
-  auto look_ahead = [&](int item) {
-    if (item >= items) return;
-    const int b = item / a.chunks;
-    ahead_drafts = a.draft_len != nullptr ? __ldg(a.draft_len + b) : a.n_max;
-    if (in_place && a.mask_rows != nullptr) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (lane + 32 * i < rows_max) ahead_mask[i] = __ldg(a.mask_rows + static_cast<long long>(b) * rows_max + lane + 32 * i);
-    }
+  // A wait that gives up once; after that the thread goes on without waiting.
+  bool dead = false;
+  auto wait = [&](const uint64_t& bar, uint32_t parity) {
+    if (!dead) dead = !ptx::mbar_wait_bounded(ptx::smem_addr(&bar), parity, SPECDEC_LOGIT_WAIT_CYCLES);
   };
-  auto take_ahead = [&]() {
-    const int rows = LogitRequest::rows(a, ahead_drafts);
-    next_rows = rows >= 64 ? ~0ull : (1ull << rows) - 1;
-    next_last = rows > 64;
-    if (in_place) {
-      const uint32_t m0 = __ballot_sync(0xFFFFFFFFu, ahead_mask[0] >= 0 && ahead_mask[0] < a.mask_count);
-      const uint32_t m1 = __ballot_sync(0xFFFFFFFFu, ahead_mask[1] >= 0 && ahead_mask[1] < a.mask_count);
-      next_rows &= static_cast<unsigned long long>(m1) << 32 | m0;
-    }
-  };
-  int loads = 0;
-  auto load_next = [&]() {
-    while (next_item < items) {
-      int j = -1;
-      if (next_rows != 0) {
-        j = __ffsll(next_rows) - 1;
-        next_rows &= next_rows - 1;
-      } else if (next_last) {
-        j = 64;
-        next_last = false;
+  // A CTA's i-th item.  (Which of a request's items it is changes from one to
+  // the next: low ids, and so work, are often the first's.)
+  auto item_of = [&](int i) { return i * grid + static_cast<int>((blockIdx.x + 7u * i) % grid); };
+  auto row_at = [&](int b, int j, int v0) { return (static_cast<long long>(b) * rows_max + j) * a.V + v0; };
+  // Bytes [from, to) are copied as whole 16 bytes, as far as they are of the
+  // tensor [first, end): what is not the item's among them is not used, and
+  // what is left out of the item's (`head` and `tail` bytes) the third role
+  // reads.
+  struct Span {
+    uintptr_t lo, hi;
+    int head, tail;
+    __device__ __forceinline__ Span(uintptr_t from, uintptr_t to, uintptr_t first, uintptr_t end)
+        : lo(from & ~static_cast<uintptr_t>(15)), hi((to + 15) & ~static_cast<uintptr_t>(15)), head(0), tail(0) {
+      if (lo < first) {
+        lo += 16;
+        head = static_cast<int>(min(lo, to) - from);
       }
-      if (j >= 0) {
-        const int b = next_item / a.chunks, v0 = (next_item - b * a.chunks) * a.share;
-        const uintptr_t from = in_first + at(b, j, v0), to = from + min(a.share, a.V - v0) * kElt;
-        // whole 16 bytes, as far as they are the tensor's
-        uintptr_t lo = from & ~static_cast<uintptr_t>(15), hi = (to + 15) & ~static_cast<uintptr_t>(15);
-        uint32_t dst = ptx::smem_addr(ring + loads % kLogitRing * row_bytes);
-        if (lo < in_first) lo += 16, dst += 16;
-        if (hi > in_end) hi -= 16;
-        const uint32_t bar = ptx::smem_addr(&sh.full[loads % kLogitRing]);
-        if (lane == 0) {
-          const uint32_t bytes = hi > lo ? static_cast<uint32_t>(hi - lo) : 0;
-          ptx::mbar_arrive_expect_tx(bar, bytes);
-          if (bytes != 0) ptx::bulk_g2s_nohint(dst, reinterpret_cast<const void*>(lo), bytes, bar);
-        }
-        ++loads;
-        return;
+      if (hi > end) {
+        hi -= 16;
+        tail = static_cast<int>(to - max(hi, from + head));
       }
-      next_item += gridDim.x;
-      take_ahead();
-      look_ahead(next_item + gridDim.x);
     }
+    __device__ __forceinline__ uint32_t bytes() const { return hi > lo ? static_cast<uint32_t>(hi - lo) : 0; }
   };
-  LogitRequest ahead;
-  if (static_cast<int>(blockIdx.x) < items) ahead.load(a, blockIdx.x / a.chunks);
-  if (tid < 32) {
-    look_ahead(next_item);
-    take_ahead();
-    look_ahead(next_item + gridDim.x);
-    for (int i = 0; i < kLogitRing; ++i) load_next();
-  }
+  auto row_span = [&](int b, int j, int v0, int n) {
+    const uintptr_t from = in_first + row_at(b, j, v0) * kElt;
+    return Span(from, from + n * kElt, in_first, in_end);
+  };
+  const uintptr_t mask_first = reinterpret_cast<uintptr_t>(a.mask);
+  auto mask_at = [&](int m, int v0) { return mask_first + (static_cast<long long>(m) * a.mask_words + (v0 >> 5)) * 4; };
+  auto mask_span = [&](int m, int v0, int n) {
+    const uintptr_t from = mask_at(m, v0);
+    return Span(from, from + (n + 31) / 32 * 4, mask_first, mask_first + static_cast<long long>(a.mask_count) * a.mask_words * 4);
+  };
+  int rows_copied = 0;  // counted by each role but the second
 
-  int step = 0;  // rows copied
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int b = item / a.chunks, v0 = (item - b * a.chunks) * a.share, n = min(a.share, a.V - v0);
-    LogitRequest rq = ahead;
-    if (item + static_cast<int>(gridDim.x) < items) ahead.load(a, (item + gridDim.x) / a.chunks);
-    if (rq.mend(a) && a.err != nullptr && v0 == 0 && tid == 0) atomicOr(a.err, SPECDEC_DEV_ERR_PENALTY);
-    const LogitParams p = rq.p;
-    auto add = [&](int v, uint32_t flag) {  // an entry is named: counted, or flagged
-      const uint32_t off = static_cast<uint32_t>(v) - static_cast<uint32_t>(v0);
-      if (off >= static_cast<uint32_t>(n)) return;
-      const uint32_t old = flag == 1 ? atomicAdd(words + off, 1u) : atomicOr(words + off, flag);
-      if (old == 0) list[atomicAdd(&sh.listed, 1)] = static_cast<uint16_t>(off);
+  auto warp_arrive = [&](const uint64_t& bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(ptx::smem_addr(&bar));
+  };
+
+  if (threadIdx.x >= 2 * kLogitTeam + 2 * kCountTeam + 32) {
+    // ---------------------------------------------------------- rows out of the ring
+    const int lane = threadIdx.x & 31;
+    for (int i = 0; item_of(i) < items; ++i) {
+      const int item = item_of(i), b = item / a.chunks, v0 = (item - b * a.chunks) * a.share, n = min(a.share, a.V - v0);
+      const LogitItem& it = sh.item[i & 1];
+      wait(sh.item_full[i & 1], i >> 1 & 1);
+#pragma unroll 1
+      for (int j = 0; j < it.rows; ++j) {
+        if (in_place && it.mask[j] < 0) continue;
+        const int slot = rows_copied % kLogitRing;
+        wait(sh.row_done[slot], rows_copied / kLogitRing & 1);
+        ++rows_copied;
+        // whole 16 bytes by a copy, the ends by threads
+        const long long at = row_at(b, j, v0);
+        const Elt* row = reinterpret_cast<const Elt*>(ring + slot * slot_bytes + static_cast<int>((in_first + at * kElt) & 15));
+        Elt* dst = static_cast<Elt*>(a.out) + at;
+        const int first = a.same_phase ? min(n, static_cast<int>(-reinterpret_cast<uintptr_t>(dst) & 15) / kElt) : n, count = (n - first) / N * N;
+        if (lane == 0 && count > 0)
+          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst + first), "r"(ptx::smem_addr(row + first)),
+                       "r"(count * kElt)
+                       : "memory");
+        for (int e = lane; e < first; e += 32) dst[e] = row[e];
+        if (lane < n - first - count) dst[first + count + lane] = row[first + count + lane];
+        if (lane == 0) {
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        }
+        warp_arrive(sh.row_empty[slot]);
+      }
+      warp_arrive(sh.item_empty[i & 1]);
+    }
+  } else if (threadIdx.x >= 2 * kLogitTeam + 2 * kCountTeam) {
+    // ---------------------------------------------------------- rows into the ring
+    const int lane = threadIdx.x & 31;
+    int next_drafts = 0, next_mask[3];
+    auto look_ahead = [&](int item) {
+      if (item >= items) return;
+      const int b = item / a.chunks;
+      next_drafts = a.draft_len != nullptr ? __ldg(a.draft_len + b) : a.n_max;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const int j = lane + 32 * k;
+        next_mask[k] = a.mask_rows != nullptr && j < rows_max ? __ldg(a.mask_rows + static_cast<long long>(b) * rows_max + j) : -1;
+      }
     };
-    const int32_t* h = a.history + static_cast<long long>(b) * a.history_stride;
-    constexpr int kIds = 8;  // in flight a thread
-    for (int i0 = tid; i0 < rq.history; i0 += kIds * kLogitThreads) {
-      int id[kIds];
-#pragma unroll
-      for (int k = 0; k < kIds; ++k) id[k] = i0 + k * kLogitThreads < rq.history ? __ldg(h + i0 + k * kLogitThreads) : -1;
-#pragma unroll
-      for (int k = 0; k < kIds; ++k) add(id[k], i0 + k * kLogitThreads < rq.prompt ? kInPrompt : 1u);
+    look_ahead(item_of(0));
+    for (int i = 0; item_of(i) < items; ++i) {
+      const int item = item_of(i), b = item / a.chunks, v0 = (item - b * a.chunks) * a.share, n = min(a.share, a.V - v0);
+      const int rows = max(0, min(next_drafts, a.n_max)) + 1;
+      const int masks[3] = {next_mask[0], next_mask[1], next_mask[2]};
+      look_ahead(item_of(i + 1));
+#pragma unroll 1
+      for (int j = 0; j < rows; ++j) {
+        const int m = __shfl_sync(0xFFFFFFFFu, j < 32 ? masks[0] : j < 64 ? masks[1] : masks[2], j & 31);
+        const bool masked = m >= 0 && m < a.mask_count;
+        if (in_place && !masked) continue;
+        const int slot = rows_copied % kLogitRing;
+        if (rows_copied >= kLogitRing) wait(sh.row_empty[slot], (rows_copied / kLogitRing - 1) & 1);
+        ++rows_copied;
+        if (lane == 0) {
+          const Span row = row_span(b, j, v0, n);
+          const uint32_t bar = ptx::smem_addr(&sh.row_full[slot]), dst = ptx::smem_addr(ring + slot * slot_bytes);
+          uint32_t bytes = row.bytes();
+          if (masked) bytes += mask_span(m, v0, n).bytes();
+          ptx::mbar_arrive_expect_tx(bar, bytes);
+          if (row.bytes() != 0) ptx::bulk_g2s_nohint(dst + (row.head != 0 ? 16 : 0), reinterpret_cast<const void*>(row.lo), row.bytes(), bar);
+          if (masked) {
+            const Span mask = mask_span(m, v0, n);
+            if (mask.bytes() != 0)
+              ptx::bulk_g2s_nohint(dst + row_bytes + (mask.head != 0 ? 16 : 0), reinterpret_cast<const void*>(mask.lo), mask.bytes(), bar);
+          }
+        }
+        __syncwarp();
+      }
     }
-    if (tid < rq.drafts) {
-      const int v = __ldg(a.draft_tokens + static_cast<long long>(b) * a.n_max + tid);
-      sh.draft[tid] = v;
-      add(v, kIsDraft);
-    }
-    if (rq.lo < rq.hi) {
-      // the item's biases, in their order
-      if (tid < 32) {
+    // no copy is in flight when the CTA ends
+    const bool was = dead;
+    dead = false;
+    for (int k = max(0, rows_copied - kLogitRing); k < rows_copied; ++k) wait(sh.row_full[k % kLogitRing], k / kLogitRing & 1);
+    dead |= was;
+  } else if (threadIdx.x >= 2 * kLogitTeam) {
+    // ---------------------------------------------------------- named entries
+    const int tid = threadIdx.x % kCountTeam, team = 1 + (threadIdx.x - 2 * kLogitTeam) / kCountTeam;  // 1 or 2
+    for (int i = team - 1; item_of(i) < items; i += 2) {
+      const int item = item_of(i), b = item / a.chunks, v0 = (item - b * a.chunks) * a.share, n = min(a.share, a.V - v0);
+      LogitItem& it = sh.item[i & 1];
+      uint32_t* words = words_of + (i & 1) * a.share;
+      uint16_t* list = list_of + (i & 1) * a.share;
+      const LogitRequest rq(a, b);
+      if (rq.bad && a.err != nullptr && v0 == 0 && tid == 0) atomicOr(a.err, SPECDEC_DEV_ERR_PENALTY);
+      if (i >= 2) wait(sh.item_empty[i & 1], ((i >> 1) - 1) & 1);
+      const int was = it.listed;
+      for (int k = tid; k < was; k += kCountTeam) words[list[k]] = 0;
+      logit_barrier(team, kCountTeam);
+      if (tid == 0) {
+        it.p = rq.p;
+        it.rows = rq.drafts + 1;
+        it.lo = rq.lo;
+        it.hi = rq.hi;
+        it.listed = it.biases = 0;
+      }
+      if (tid <= rq.drafts) {
+        const int m = a.mask_rows != nullptr ? __ldg(a.mask_rows + static_cast<long long>(b) * rows_max + tid) : -1;
+        it.mask[tid] = m < a.mask_count ? m : -1;
+      }
+      int draft = -1;
+      if (tid < rq.drafts) it.draft[tid] = draft = __ldg(a.draft_tokens + static_cast<long long>(b) * a.n_max + tid);
+      logit_barrier(team, kCountTeam);
+      auto add = [&](int v, uint32_t flag) {  // counted, or flagged
+        const uint32_t off = static_cast<uint32_t>(v) - static_cast<uint32_t>(v0);
+        if (off >= static_cast<uint32_t>(n)) return;
+        const uint32_t old = flag == 1 ? atomicAdd(words + off, 1u) : atomicOr(words + off, flag);
+        if (old == 0) list[atomicAdd(&it.listed, 1)] = static_cast<uint16_t>(off);
+      };
+      {
+        // ids by fours where they lie on 16 bytes
+        const int32_t* h = a.history + static_cast<long long>(b) * a.history_stride;
+        const int head = min(rq.history, static_cast<int>(-(reinterpret_cast<uintptr_t>(h) >> 2) & 3)), fours = (rq.history - head) / 4;
+        if (tid < head) add(__ldg(h + tid), tid < rq.prompt ? kInPrompt : 1u);
+        const int tail = head + 4 * fours + tid;
+        if (tail < rq.history) add(__ldg(h + tail), tail < rq.prompt ? kInPrompt : 1u);
+        const int4* h4 = reinterpret_cast<const int4*>(h + head);
+        constexpr int kFours = 4;  // in flight a thread
+        for (int i0 = tid; i0 < fours; i0 += kFours * kCountTeam) {
+          int4 id[kFours];
+#pragma unroll
+          for (int k = 0; k < kFours; ++k) id[k] = i0 + k * kCountTeam < fours ? __ldg(h4 + i0 + k * kCountTeam) : make_int4(-1, -1, -1, -1);
+#pragma unroll
+          for (int k = 0; k < kFours; ++k) {
+            const int at = head + 4 * (i0 + k * kCountTeam);
+            const int v[4] = {id[k].x, id[k].y, id[k].z, id[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) add(v[e], at + e < rq.prompt ? kInPrompt : 1u);
+          }
+        }
+      }
+      add(draft, kIsDraft);
+      if (tid < 32) {  // the biases, in their order
         int count = 0;
-        for (int i = rq.lo + lane; i - lane < rq.hi; i += 32) {
-          const int v = i < rq.hi ? __ldg(a.bias_ids + i) : -1;
+        for (int k0 = rq.lo; k0 < rq.hi; k0 += 32) {
+          const int v = k0 + tid < rq.hi ? __ldg(a.bias_ids + k0 + tid) : -1;
           const bool mine = v >= v0 && v < v0 + n;
           const uint32_t m = __ballot_sync(0xFFFFFFFFu, mine);
           if (mine) {
-            const int k = count + __popc(m & ((1u << lane) - 1));
+            const int k = count + __popc(m & ((1u << tid) - 1));
             if (k < kBiasList) {
-              sh.bias_at[k] = v - v0;
-              sh.bias[k] = __ldg(a.bias_values + i);
+              it.bias_at[k] = v - v0;
+              it.bias[k] = __ldg(a.bias_values + k0 + tid);
             }
             add(v, kHasBias);
           }
           count += __popc(m);
         }
-        if (lane == 0) sh.biases = count;
+        if (tid == 0) it.biases = count;
       }
-    } else if (tid == 0) {
-      sh.biases = 0;
-    }
-    __syncthreads();
-    const int listed = sh.listed, biases = sh.biases;
-    const bool few = biases <= kBiasList;  // all of them are in shared memory
-    if (biases > 0 && few) {
-      for (int i = tid; i < biases; i += kLogitThreads) {
-        bool is_first = true;
-        for (int k = 0; k < i; ++k) is_first = is_first && sh.bias_at[k] != sh.bias_at[i];
-        float sum = 0.f;
-        for (int k = i; k < biases; ++k)
-          if (sh.bias_at[k] == sh.bias_at[i]) sum += sh.bias[k];
-        sh.bias_first[i] = is_first;
-        sh.bias_sum[i] = sum;
-      }
-      __syncthreads();
-    }
-
-    for (int j = 0; j <= rq.drafts; ++j) {
-      int m = a.mask_rows != nullptr ? __ldg(a.mask_rows + static_cast<long long>(b) * rows_max + j) : -1;
-      const bool masked = m >= 0 && m < a.mask_count;
-      const bool copied = !in_place || masked || j == 64;
-      const long long at_row = at(b, j, v0);
-      const int ph = static_cast<int>((in_first + at_row) & 15);
-      unsigned char* buf = ring + step % kLogitRing * row_bytes;
-      Elt* row;
-      if (copied) {
-        if (!dead && !ptx::mbar_wait_bounded(ptx::smem_addr(&sh.full[step % kLogitRing]), step / kLogitRing & 1, SPECDEC_LOGIT_WAIT_CYCLES))
-          dead = true;
-        row = reinterpret_cast<Elt*>(buf + ph);
-        // what the copy left out at the tensor's ends
-        const uintptr_t from = in_first + at_row, to = from + static_cast<uintptr_t>(n) * kElt;
-        const bool head = (from & ~static_cast<uintptr_t>(15)) < in_first, tail = ((to + 15) & ~static_cast<uintptr_t>(15)) > in_end;
-        if (head || tail) {
-          const Elt* src = reinterpret_cast<const Elt*>(from);
-          const int first = head ? min(n, (16 - ph) / kElt) : 0;
-          const int last = tail ? max(first, n - static_cast<int>(to & 15) / kElt) : n;
-          if (tid < first) row[tid] = src[tid];
-          if (last + tid < n) row[last + tid] = src[last + tid];
-          __syncthreads();
+      logit_barrier(team, kCountTeam);
+      const int biases = it.biases;
+      if (biases > 0 && biases <= kBiasList) {
+        for (int q = tid; q < biases; q += kCountTeam) {
+          float sum = 0.f;
+          bool is_first = true;
+          for (int k = q; k < biases; ++k)
+            if (it.bias_at[k] == it.bias_at[q]) sum += it.bias[k];
+          for (int k = 0; k < q; ++k) is_first = is_first && it.bias_at[k] != it.bias_at[q];
+          it.bias_sum[q] = sum;
+          it.bias_first[q] = is_first;
         }
-      } else {
-        row = reinterpret_cast<Elt*>(static_cast<char*>(a.out) + at_row);
+        logit_barrier(team, kCountTeam);
       }
-      auto change = [&](int off, uint32_t word, float bias, bool biased) {
+      if (tid == 0) ptx::mbar_arrive(ptx::smem_addr(&sh.item_full[i & 1]));
+    }
+  } else {
+    // ---------------------------------------------------------- the rows
+    const int tid = threadIdx.x % kLogitTeam, team = threadIdx.x / kLogitTeam;
+    constexpr uint32_t kAll = (1u << N) - 1;
+    for (int i = 0; item_of(i) < items; ++i) {
+      const int item = item_of(i), b = item / a.chunks, v0 = (item - b * a.chunks) * a.share, n = min(a.share, a.V - v0);
+      const LogitItem& it = sh.item[i & 1];
+      const uint32_t* words = words_of + (i & 1) * a.share;
+      const uint16_t* list = list_of + (i & 1) * a.share;
+      wait(sh.item_full[i & 1], i >> 1 & 1);
+      const int rows = it.rows, listed = it.listed, biases = it.biases;
+      const bool few = biases <= kBiasList;  // all of them are in shared memory
+      const LogitParams p = it.p;
+      auto change = [&](Elt* row, int j, int off, uint32_t word, float bias, bool biased) {
         uint32_t c = word & kCountMask;
-        if (word & kIsDraft) {
-          for (int k = 0; k < j; ++k) c += sh.draft[k] == v0 + off;
-        }
+        if (word & kIsDraft)
+          for (int d = 0; d < j; ++d) c += it.draft[d] == v0 + off;
         if (c == 0 && !(word & kInPrompt) && !biased) return;
-        Elt x = row[off];
-        float_to_elt(penalised(elt_to_float(x), c, word & kInPrompt, bias, p), x);
-        row[off] = x;
+        float_to_elt(penalised(elt_to_float(row[off]), c, word & kInPrompt, bias, p), row[off]);
       };
-      for (int i = tid; i < listed; i += kLogitThreads) {
-        const int off = list[i];
+      // the q-th listed entry; and those with biases
+      auto change_listed = [&](Elt* row, int j, int q) {
+        const int off = list[q];
         const uint32_t word = words[off];
         const bool biased = word & kHasBias;
         float bias = 0.f;
         if (biased) {
-          if (few) continue;  // below
-          for (int k = rq.lo; k < rq.hi; ++k)
+          if (few) return;
+          for (int k = it.lo; k < it.hi; ++k)
             if (__ldg(a.bias_ids + k) == v0 + off) bias += __ldg(a.bias_values + k);
         }
-        change(off, word, bias, biased);
-      }
-      if (few) {
-        for (int i = tid; i < biases; i += kLogitThreads)
-          if (sh.bias_first[i]) change(sh.bias_at[i], words[sh.bias_at[i]], sh.bias_sum[i], true);
-      }
-      if (!copied) continue;
-      if (masked) {
-        __syncthreads();
-        const uint32_t* mask = a.mask + static_cast<long long>(m) * a.mask_words;
-        for (int i = tid; i * 16 < ph + n * kElt; i += kLogitThreads) {
-          const int v = v0 + i * N - ph / kElt;  // the vector's first entry
-          const uint32_t all = (1u << N) - 1;
-          uint32_t allow;
-          if (v >= 0) {
-            const int w = v >> 5;
-            allow = __funnelshift_r(__ldg(mask + w), __ldg(mask + min(w + 1, a.mask_words - 1)), v & 31);
-          } else {
-            allow = __ldg(mask) << -v;
-          }
-          if ((allow & all) != all) {
-            Elt* x = reinterpret_cast<Elt*>(buf + i * 16);
-            union {
-              uint4 q;
-              Elt e[N];
-            } y;
-            y.q = *reinterpret_cast<const uint4*>(x);
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-              if (!((allow >> e) & 1)) float_to_elt(-INFINITY, y.e[e]);
-            *reinterpret_cast<uint4*>(x) = y.q;
-          }
+        change(row, j, off, word, bias, biased);
+      };
+      auto change_biased = [&](Elt* row, int j, int q) {
+        if (it.bias_first[q]) change(row, j, it.bias_at[q], words[it.bias_at[q]], it.bias_sum[q], true);
+      };
+      if (in_place) {
+        // where they lie: every pair of an entry and a row is a thread's
+        Elt* out = static_cast<Elt*>(a.out) + row_at(b, 0, v0);
+        for (int q = threadIdx.x; q < (listed + (few ? biases : 0)) * rows; q += 2 * kLogitTeam) {
+          const int e = q / rows, j = q - e * rows;
+          if (it.mask[j] >= 0) continue;
+          Elt* row = out + static_cast<long long>(j) * a.V;
+          if (e < listed)
+            change_listed(row, j, e);
+          else
+            change_biased(row, j, e - listed);
         }
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncthreads();
-      // out: whole 16 bytes by a copy, the ends by threads
-      Elt* dst = reinterpret_cast<Elt*>(static_cast<char*>(a.out) + at_row);
-      int first = 0, last = 0;
-      if (a.same_phase) {
-        first = min(n, ph == 0 ? 0 : (16 - ph) / kElt);
-        last = max(first, n - ((ph + n * kElt) & 15) / kElt);
-        if (tid < first) dst[tid] = row[tid];
-      }
-      if (tid < 32) {
-        if (lane == 0) {
-          if (last > first)
-            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst + first),
-                         "r"(ptx::smem_addr(row + first)), "r"((last - first) * kElt)
-                         : "memory");
-          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          // the store before this one has left its buffer, and all threads theirs
-          asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+#pragma unroll 1
+      for (int j = 0; j < rows; ++j) {
+        const int m = it.mask[j];
+        if (in_place && m < 0) continue;
+        const int r = rows_copied++;
+        if ((r & 1) != team) continue;
+        const int slot = r % kLogitRing;
+        unsigned char* buf = ring + slot * slot_bytes;
+        const uintptr_t from = in_first + row_at(b, j, v0) * kElt;
+        const int ph = static_cast<int>(from & 15);
+        Elt* row = reinterpret_cast<Elt*>(buf + ph);
+        const Span s = row_span(b, j, v0, n);
+        wait(sh.row_full[slot], r / kLogitRing & 1);
+        // what the copies left out at the tensors' ends, by bytes
+        auto fill = [&](unsigned char* dst, uintptr_t from, int bytes, const Span& s) {
+          const unsigned char* src = reinterpret_cast<const unsigned char*>(from);
+          if (tid < s.head) dst[tid] = src[tid];
+          if (tid < s.tail) dst[bytes - s.tail + tid] = src[bytes - s.tail + tid];
+        };
+        if (s.head + s.tail > 0) {
+          fill(buf + ph, from, n * kElt, s);
+          logit_barrier(3 + team, kLogitTeam);
         }
-        __syncwarp();
-        if (step > 0) load_next();
+        for (int q = tid; q < listed; q += kLogitTeam) change_listed(row, j, q);
+        for (int q = tid; few && q < biases; q += kLogitTeam) change_biased(row, j, q);
+        if (m >= 0) {
+          const Span ms = mask_span(m, v0, n);
+          const uint32_t* mask = reinterpret_cast<const uint32_t*>(buf + row_bytes + (mask_at(m, v0) & 15));
+          if (ms.head + ms.tail > 0) fill(buf + row_bytes + (mask_at(m, v0) & 15), mask_at(m, v0), (n + 31) / 32 * 4, ms);
+          logit_barrier(3 + team, kLogitTeam);
+          const int last = (n - 1) >> 5;
+#pragma unroll 4
+          for (int i = tid; i * 16 < ph + n * kElt; i += kLogitTeam) {
+            const int v = i * N - ph / kElt;  // the vector's first entry, from the item's on (below 0: entries of no one)
+            const uint32_t allow = v < 0 ? mask[0] << -v : __funnelshift_r(mask[v >> 5], mask[min((v >> 5) + 1, last)], v & 31);
+            if ((allow & kAll) == kAll) continue;
+            uint4* x = reinterpret_cast<uint4*>(buf + i * 16);
+            uint4 y = *x;
+            mask_vector<Elt>(y, allow);
+            *x = y;
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        warp_arrive(sh.row_done[slot]);
       }
-      for (int i = last + tid; i < n; i += kLogitThreads) dst[i] = row[i];
-      ++step;
+      warp_arrive(sh.item_empty[i & 1]);
     }
-    // the words as they were
-    __syncthreads();
-    for (int i = tid; i < listed; i += kLogitThreads) words[list[i]] = 0;
-    if (tid == 0) sh.listed = 0;
-    __syncthreads();
-  }
-  if (tid == 0) {
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    // after a wait that gave up: no copy is in flight when the CTA ends
-    for (int i = max(0, loads - kLogitRing); dead && i < loads; ++i)
-      ptx::mbar_wait_bounded(ptx::smem_addr(&sh.full[i % kLogitRing]), i / kLogitRing & 1, SPECDEC_LOGIT_WAIT_CYCLES);
   }
   if (dead && a.err != nullptr) atomicOr(a.err, SPECDEC_DEV_ERR_TIMEOUT);
 }

@@ -44,27 +44,25 @@ cudaError_t device_sms(int* dev, int* sms) {
   return cudaSuccess;
 }
 
-constexpr int kSmSmem = 228 * 1024;  // of an SM; a CTA takes 1 KB more than it asks for
-
 template <typename Elt>
 cudaError_t launch_logits(LogitArgs a, cudaStream_t st) {
   using L = LogitLayout<Elt>;
+  constexpr int kElt = sizeof(Elt);
   static bool ready[64] = {false};
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
   if (!ready[dev]) {
-    e = cudaFuncSetAttribute(process_logits_kernel<Elt>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes(kLogitShare));
+    e = cudaFuncSetAttribute(process_logits_kernel<Elt>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes(kLogitRowBytes / kElt));
     if (e != cudaSuccess) return e;
     ready[dev] = true;
   }
   // Few requests are cut finer, until every SM has work.
-  a.share = kLogitShare;
-  while (a.share > kLogitLeastShare && static_cast<int64_t>(a.B) * ((a.V + a.share - 1) / a.share) < 4 * sms) a.share /= 2;
+  a.share = kLogitRowBytes / kElt;
+  while (a.share * kElt > kLogitLeastBytes && static_cast<int64_t>(a.B) * ((a.V + a.share - 1) / a.share) < 2 * sms) a.share /= 2;
   a.chunks = (a.V + a.share - 1) / a.share;
-  const int per_sm = kSmSmem / (L::bytes(a.share) + static_cast<int>(sizeof(LogitShared)) + 1024);
-  const int64_t items = static_cast<int64_t>(a.B) * a.chunks, most = static_cast<int64_t>(sms) * (per_sm < 4 ? per_sm : 4);
-  process_logits_kernel<Elt><<<static_cast<unsigned>(items < most ? items : most), kLogitThreads, L::bytes(a.share), st>>>(a);
+  const int items = a.B * a.chunks;
+  process_logits_kernel<Elt><<<static_cast<unsigned>(items < sms ? items : sms), kLogitThreads, L::bytes(a.share), st>>>(a);
   return cudaGetLastError();
 }
 

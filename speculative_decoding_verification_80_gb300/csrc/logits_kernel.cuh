@@ -260,12 +260,14 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
         if (lane < n - first - count) dst[first + count + lane] = row[first + count + lane];
         if (lane == 0) {
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
         }
-        warp_arrive(sh.row_empty[slot]);
+        // the row before this one has left
+        if (rows_copied > 1) warp_arrive(sh.row_empty[(rows_copied - 2) % kLogitRing]);
       }
       warp_arrive(sh.item_empty[i & 1]);
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   } else if (threadIdx.x >= 2 * kLogitTeam + 2 * kCountTeam) {
     // ---------------------------------------------------------- rows into the ring
     const int lane = threadIdx.x & 31;
@@ -325,6 +327,29 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
       uint16_t* list = list_of + (i & 1) * a.share;
       const LogitRequest rq(a, b);
       if (rq.bad && a.err != nullptr && v0 == 0 && tid == 0) atomicOr(a.err, SPECDEC_DEV_ERR_PENALTY);
+      // what does not need the item's place is on its way while that is waited for
+      const int m = a.mask_rows != nullptr && tid < rows_max ? __ldg(a.mask_rows + static_cast<long long>(b) * rows_max + tid) : -1;
+      const int draft = tid < rq.drafts ? __ldg(a.draft_tokens + static_cast<long long>(b) * a.n_max + tid) : -1;
+      // ids by fours where they lie on 16 bytes
+      const int32_t* h = a.history + static_cast<long long>(b) * a.history_stride;
+      const int head = min(rq.history, static_cast<int>(-(reinterpret_cast<uintptr_t>(h) >> 2) & 3)), fours = (rq.history - head) / 4;
+      const int4* h4 = reinterpret_cast<const int4*>(h + head);
+      const int tail = head + 4 * fours + tid;
+      const int id_head = tid < head ? __ldg(h + tid) : -1, id_tail = tail < rq.history ? __ldg(h + tail) : -1;
+      constexpr int kFours = 4;  // in flight a thread
+      int4 id[kFours];
+      auto load_ids = [&](int i0) {
+#pragma unroll
+        for (int k = 0; k < kFours; ++k) id[k] = i0 + k * kCountTeam < fours ? __ldg(h4 + i0 + k * kCountTeam) : make_int4(-1, -1, -1, -1);
+      };
+      load_ids(tid);
+      int bias_id = -1;
+      float bias_value = 0.f;
+      auto load_bias = [&](int k) {
+        bias_id = k < rq.hi ? __ldg(a.bias_ids + k) : -1;
+        bias_value = k < rq.hi ? __ldg(a.bias_values + k) : 0.f;
+      };
+      if (tid < 32) load_bias(rq.lo + tid);
       if (i >= 2) wait(sh.item_empty[i & 1], ((i >> 1) - 1) & 1);
       const int was = it.listed;
       for (int k = tid; k < was; k += kCountTeam) words[list[k]] = 0;
@@ -336,12 +361,8 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
         it.hi = rq.hi;
         it.listed = it.biases = 0;
       }
-      if (tid <= rq.drafts) {
-        const int m = a.mask_rows != nullptr ? __ldg(a.mask_rows + static_cast<long long>(b) * rows_max + tid) : -1;
-        it.mask[tid] = m < a.mask_count ? m : -1;
-      }
-      int draft = -1;
-      if (tid < rq.drafts) it.draft[tid] = draft = __ldg(a.draft_tokens + static_cast<long long>(b) * a.n_max + tid);
+      if (tid <= rq.drafts) it.mask[tid] = m < a.mask_count ? m : -1;
+      if (tid < rq.drafts) it.draft[tid] = draft;
       logit_barrier(team, kCountTeam);
       auto add = [&](int v, uint32_t flag) {  // counted, or flagged
         const uint32_t off = static_cast<uint32_t>(v) - static_cast<uint32_t>(v0);
@@ -349,40 +370,32 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
         const uint32_t old = flag == 1 ? atomicAdd(words + off, 1u) : atomicOr(words + off, flag);
         if (old == 0) list[atomicAdd(&it.listed, 1)] = static_cast<uint16_t>(off);
       };
-      {
-        // ids by fours where they lie on 16 bytes
-        const int32_t* h = a.history + static_cast<long long>(b) * a.history_stride;
-        const int head = min(rq.history, static_cast<int>(-(reinterpret_cast<uintptr_t>(h) >> 2) & 3)), fours = (rq.history - head) / 4;
-        if (tid < head) add(__ldg(h + tid), tid < rq.prompt ? kInPrompt : 1u);
-        const int tail = head + 4 * fours + tid;
-        if (tail < rq.history) add(__ldg(h + tail), tail < rq.prompt ? kInPrompt : 1u);
-        const int4* h4 = reinterpret_cast<const int4*>(h + head);
-        constexpr int kFours = 4;  // in flight a thread
-        for (int i0 = tid; i0 < fours; i0 += kFours * kCountTeam) {
-          int4 id[kFours];
+      add(id_head, tid < rq.prompt ? kInPrompt : 1u);
+      add(id_tail, tail < rq.prompt ? kInPrompt : 1u);
+#pragma unroll 1
+      for (int i0 = tid; i0 < fours; i0 += kFours * kCountTeam) {
+        if (i0 != tid) load_ids(i0);
 #pragma unroll
-          for (int k = 0; k < kFours; ++k) id[k] = i0 + k * kCountTeam < fours ? __ldg(h4 + i0 + k * kCountTeam) : make_int4(-1, -1, -1, -1);
+        for (int k = 0; k < kFours; ++k) {
+          const int at = head + 4 * (i0 + k * kCountTeam);
+          const int v[4] = {id[k].x, id[k].y, id[k].z, id[k].w};
 #pragma unroll
-          for (int k = 0; k < kFours; ++k) {
-            const int at = head + 4 * (i0 + k * kCountTeam);
-            const int v[4] = {id[k].x, id[k].y, id[k].z, id[k].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) add(v[e], at + e < rq.prompt ? kInPrompt : 1u);
-          }
+          for (int e = 0; e < 4; ++e) add(v[e], at + e < rq.prompt ? kInPrompt : 1u);
         }
       }
       add(draft, kIsDraft);
       if (tid < 32) {  // the biases, in their order
         int count = 0;
         for (int k0 = rq.lo; k0 < rq.hi; k0 += 32) {
-          const int v = k0 + tid < rq.hi ? __ldg(a.bias_ids + k0 + tid) : -1;
+          if (k0 != rq.lo) load_bias(k0 + tid);
+          const int v = bias_id;
           const bool mine = v >= v0 && v < v0 + n;
           const uint32_t m = __ballot_sync(0xFFFFFFFFu, mine);
           if (mine) {
             const int k = count + __popc(m & ((1u << tid) - 1));
             if (k < kBiasList) {
               it.bias_at[k] = v - v0;
-              it.bias[k] = __ldg(a.bias_values + k0 + tid);
+              it.bias[k] = bias_value;
             }
             add(v, kHasBias);
           }

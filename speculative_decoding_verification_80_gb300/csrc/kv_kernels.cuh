@@ -8,6 +8,14 @@
 namespace specdec {
 
 // ------------------------------------------------------------ kv_block_step
+//
+// Prefix sums over the requests (blocks asked for, then tokens, blocks taken
+// and given of those that are granted), then the slots of the tokens and the
+// table's new entries.  A few KB to some MB: bound by latency, so one launch
+// and few dependent loads.  A cluster of 8 CTAs: each makes the whole plan for
+// itself, in shared memory, and after all have read the lengths (the outputs
+// may be the same arrays) they share the writing.  A thread writes four
+// neighbouring tokens, whose request it finds by bisection in shared memory.
 struct BlockArgs {
   int32_t B, bs, max_blocks, num_blocks, capacity;
   const int32_t* kv_len;
@@ -25,37 +33,48 @@ struct BlockArgs {
   int32_t* slot_map;
   int32_t* positions;
   uint32_t* err;
-  int32_t fill;  // 1: the plan kernel also writes tables and slots
+  int32_t vec;  // slot_map and positions lie on 16 bytes
 };
 
 constexpr int kBlockThreads = 1024;
+constexpr int kBlockCtas = 8;
 
-// Exclusive prefix sum over the block of one value a thread; `total` is the
-// sum.  `part` holds a warp's sum each.
-__device__ __forceinline__ long long block_prefix(long long x, long long* part, long long* total) {
+// Exclusive prefix sums over the block of N values a thread; `total` are the
+// sums.  `part` holds a warp's sums each.
+template <int N>
+__device__ __forceinline__ void block_prefix(const long long (&x)[N], long long (*part)[N], long long (&before)[N], long long (&total)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long s = x;
+  long long s[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i] = x[i];
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xFFFFFFFFu, s, d);
-    if (lane >= d) s += o;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const long long o = __shfl_up_sync(0xFFFFFFFFu, s[i], d);
+      if (lane >= d) s[i] += o;
+    }
   }
   __syncthreads();  // the last use of `part` is over
-  if (lane == 31) part[warp] = s;
-  __syncthreads();
-  if (warp == 0) {
-    long long w = lane < kBlockThreads / 32 ? part[lane] : 0;
+  if (lane == 31) {
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long o = __shfl_up_sync(0xFFFFFFFFu, w, d);
-      if (lane >= d) w += o;
-    }
-    part[lane] = w;
+    for (int i = 0; i < N; ++i) part[warp][i] = s[i];
   }
   __syncthreads();
-  *total = part[kBlockThreads / 32 - 1];
-  return s - x + (warp > 0 ? part[warp - 1] : 0);
+  // every warp sums the warps' for itself
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    long long w = part[lane][i], mine = lane < warp ? w : 0;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      w += __shfl_xor_sync(0xFFFFFFFFu, w, d);
+      mine += __shfl_xor_sync(0xFFFFFFFFu, mine, d);
+    }
+    total[i] = w;
+    before[i] = mine + s[i] - x[i];
+  }
 }
+static_assert(kBlockThreads / 32 == 32, "a lane for each warp");
 
 // The index b in [0, n) with cu[b] <= t < cu[b + 1]; cu is non-decreasing,
 // cu[0] <= t < cu[n].
@@ -71,38 +90,74 @@ __device__ __forceinline__ int owner_of(const int32_t* cu, int n, int t) {
   return lo;
 }
 
-// Slot and position of new token t of request b, and the table entries that
-// the step fills; both read the ring and the entries that were there before.
-__device__ __forceinline__ void fill_token(const BlockArgs& a, int head, int t, int total) {
-  if (t >= total) {
-    a.slot_map[t] = -1;
-    a.positions[t] = -1;
-    return;
-  }
-  const int b = owner_of(a.cu_tokens, a.B, t);
-  const int p = a.kv_len_out[b] + (t - a.cu_tokens[b]);
-  const int j = p / a.bs;
-  const int taken = a.cu_blocks[b + 1] - a.cu_blocks[b];
-  const int before = a.held_out[b] - taken;
-  int block;
-  if (taken > 0 && j >= before)
-    block = a.ring[static_cast<int>((static_cast<long long>(head) + a.cu_blocks[b] + (j - before)) % a.num_blocks)];
-  else
-    block = a.table[static_cast<long long>(b) * a.max_blocks + j];
-  a.slot_map[t] = block * a.bs + p % a.bs;
-  a.positions[t] = p;
-}
-__device__ __forceinline__ void fill_block(const BlockArgs& a, int head, int i) {
-  const int b = owner_of(a.cu_blocks, a.B, i);
-  const int k = i - a.cu_blocks[b];
-  const int before = a.held_out[b] - (a.cu_blocks[b + 1] - a.cu_blocks[b]);
-  a.table[static_cast<long long>(b) * a.max_blocks + before + k] =
-      a.ring[static_cast<int>((static_cast<long long>(head) + i) % a.num_blocks)];
+// What a step decides, as the writing needs it: the outputs' arrays, or copies
+// in shared memory.
+struct BlockPlan {
+  int32_t* cu_tokens;  // [B + 1]
+  int32_t* cu_blocks;  // [B + 1]
+  int32_t* kept;       // [B]
+  int32_t* held;       // [B] blocks after the step
+};
+
+// (before < 2 N)
+__device__ __forceinline__ int ring_at(const BlockArgs& a, int head, long long i) {
+  long long at = head + i;
+  if (at >= a.num_blocks) at -= a.num_blocks;
+  if (at >= a.num_blocks) at -= a.num_blocks;
+  return static_cast<int>(at);
 }
 
-// One CTA: lengths, grants and their prefix sums, and the blocks that go back.
-__global__ void __launch_bounds__(kBlockThreads) block_plan_kernel(const BlockArgs a) {
-  __shared__ long long part[32];
+// Slots and positions of tokens t .. t + 3; reads the ring and the entries that
+// were there before.
+__device__ __forceinline__ void fill_tokens(const BlockArgs& a, const BlockPlan& plan, int bs_log2, int head, int t, int total) {
+  int slot[4], pos[4], b = -1, end = 0, kept = 0, first = 0, taken_at = 0, before = 0, j_last = -1, block = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    slot[k] = pos[k] = -1;
+    if (t + k >= total) continue;
+    if (t + k >= end) {
+      b = owner_of(plan.cu_tokens, a.B, t + k);
+      first = plan.cu_tokens[b];
+      end = plan.cu_tokens[b + 1];
+      kept = plan.kept[b];
+      taken_at = plan.cu_blocks[b];
+      before = plan.held[b];
+      const int taken = plan.cu_blocks[b + 1] - taken_at;
+      before = taken > 0 ? before - taken : 0x7FFFFFFF;
+      j_last = -1;
+    }
+    const int p = kept + (t + k - first), j = p >> bs_log2;
+    if (j != j_last) {
+      block = j >= before ? a.ring[ring_at(a, head, static_cast<long long>(taken_at) + (j - before))]
+                          : a.table[static_cast<long long>(b) * a.max_blocks + j];
+      j_last = j;
+    }
+    slot[k] = (block << bs_log2) + (p & ((1 << bs_log2) - 1));
+    pos[k] = p;
+  }
+  if (a.vec && t + 4 <= a.capacity) {
+    *reinterpret_cast<int4*>(a.slot_map + t) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    *reinterpret_cast<int4*>(a.positions + t) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (t + k >= a.capacity) break;
+      a.slot_map[t + k] = slot[k];
+      a.positions[t + k] = pos[k];
+    }
+  }
+}
+// The i-th block taken goes into its table.
+__device__ __forceinline__ void fill_block(const BlockArgs& a, const BlockPlan& plan, int head, int i) {
+  const int b = owner_of(plan.cu_blocks, a.B, i);
+  const int at = plan.held[b] - plan.cu_blocks[b + 1] + i;
+  a.table[static_cast<long long>(b) * a.max_blocks + at] = a.ring[ring_at(a, head, i)];
+}
+
+// The step's lengths, grants and prefix sums, by one CTA of a cluster of
+// `ctas`; and the blocks that go back, of its share of the requests.
+__device__ __forceinline__ int block_plan(const BlockArgs& a, const BlockPlan& plan, int rank, int ctas, int* ring_out, uint32_t* bad_out) {
+  __shared__ long long part1[32][1], part3[32][3];
   const int tid = threadIdx.x, lane = tid & 31;
   const int N = a.num_blocks;
   int head = a.ring_state[0], count = a.ring_state[1];
@@ -112,13 +167,13 @@ __global__ void __launch_bounds__(kBlockThreads) block_plan_kernel(const BlockAr
     head = head < 0 || head >= N ? 0 : head;
     count = max(0, min(count, N));
   }
-  long long asked = 0, took = 0, gave = 0, tokens = 0;
+  long long asked = 0, tokens = 0, took = 0, gave = 0;
   for (int b0 = 0; b0 < a.B; b0 += kBlockThreads) {
     const int b = b0 + tid;
     const bool in = b < a.B;
     int kept = 0, want = 0, held = 0, need = 0;
     if (in) {
-      const int fresh = a.new_tokens[b];
+      const int fresh = a.new_tokens[b], len = a.kv_len[b], accepted = a.accepted_len != nullptr ? a.accepted_len[b] : -1;
       held = a.held[b];
       if (held < 0 || held > a.max_blocks) {
         bad = 1;
@@ -126,8 +181,7 @@ __global__ void __launch_bounds__(kBlockThreads) block_plan_kernel(const BlockAr
       }
       want = max(fresh, 0);
       if (fresh >= 0) {
-        long long k = a.kv_len[b];
-        if (a.accepted_len != nullptr) k += max(a.accepted_len[b], -1) + 1LL;
+        long long k = len + (max(accepted, -1) + 1LL);
         if (k < 0 || k > static_cast<long long>(held) * a.bs) {
           bad = 1;
           k = max(0LL, min(k, static_cast<long long>(held) * a.bs));
@@ -138,30 +192,29 @@ __global__ void __launch_bounds__(kBlockThreads) block_plan_kernel(const BlockAr
     }
     const bool fits = need <= a.max_blocks;
     const int grow = fits ? max(need - held, 0) : 0;
-    long long sum;
-    const long long at = asked + block_prefix(grow, part, &sum);
-    asked += sum;
-    const bool granted = in && fits && (grow == 0 || at + grow <= count);
+    long long x1[1] = {grow}, before1[1], sum1[1];
+    block_prefix(x1, part1, before1, sum1);
+    const bool granted = in && fits && (grow == 0 || asked + before1[0] + grow <= count);
+    asked += sum1[0];
     if (in && !granted) bad = 1;
     const int taken = granted ? grow : 0;
     const int given = granted ? max(held - need, 0) : 0;
-    const long long tok_at = tokens + block_prefix(granted ? want : 0, part, &sum);
-    tokens += sum;
-    const long long give_at = gave + block_prefix(given, part, &sum);
-    gave += sum;
-    // grants are a prefix of the requests that ask for blocks, so the blocks
-    // taken before b are those asked for before it while grants last
-    const long long take_at = took + block_prefix(taken, part, &sum);
-    took += sum;
+    // (grants are a prefix of the requests that ask for blocks)
+    long long x[3] = {granted ? want : 0, taken, given}, before[3], sum[3];
+    block_prefix(x, part3, before, sum);
+    const long long tok_at = tokens + before[0], take_at = took + before[1], give_at = gave + before[2];
+    tokens += sum[0];
+    took += sum[1];
+    gave += sum[2];
     if (in) {
       if (tok_at + want > a.capacity && granted) bad = 1;
-      a.kv_len_out[b] = kept;
-      a.held_out[b] = held + taken - given;
-      a.cu_tokens[b] = static_cast<int>(min(tok_at, static_cast<long long>(a.capacity)));
-      a.cu_blocks[b] = static_cast<int>(take_at);
+      plan.kept[b] = kept;
+      plan.held[b] = held + taken - given;
+      plan.cu_tokens[b] = static_cast<int>(min(tok_at, static_cast<long long>(a.capacity)));
+      plan.cu_blocks[b] = static_cast<int>(take_at);
     }
     // blocks that go back, a warp to a request
-    uint32_t m = __ballot_sync(0xFFFFFFFFu, given > 0);
+    uint32_t m = (b0 + tid) / 32 % ctas == rank ? __ballot_sync(0xFFFFFFFFu, given > 0) : 0;
     while (m) {
       const int src = __ffs(m) - 1;
       m &= m - 1;
@@ -174,27 +227,67 @@ __global__ void __launch_bounds__(kBlockThreads) block_plan_kernel(const BlockAr
     }
   }
   if (tid == 0) {
-    a.cu_tokens[a.B] = static_cast<int>(min(tokens, static_cast<long long>(a.capacity)));
-    a.cu_blocks[a.B] = static_cast<int>(took);
-    a.ring_state_out[0] = static_cast<int>((head + took) % N);
-    a.ring_state_out[1] = static_cast<int>(min(static_cast<long long>(N), count - took + gave));
+    plan.cu_tokens[a.B] = static_cast<int>(min(tokens, static_cast<long long>(a.capacity)));
+    plan.cu_blocks[a.B] = static_cast<int>(took);
   }
-  if (bad && a.err != nullptr) atomicOr(a.err, SPECDEC_DEV_ERR_BLOCKS);
-  if (!a.fill) return;
-  __syncthreads();
-  const int total = a.cu_tokens[a.B], blocks = a.cu_blocks[a.B];
-  for (int t = tid; t < a.capacity; t += kBlockThreads) fill_token(a, head, t, total);
-  for (int i = tid; i < blocks; i += kBlockThreads) fill_block(a, head, i);
+  ring_out[0] = ring_at(a, head, took);
+  ring_out[1] = static_cast<int>(min(static_cast<long long>(N), count - took + gave));
+  *bad_out = bad;
+  return head;
 }
 
-// Many CTAs: the same for long prompts.
-__global__ void block_fill_kernel(const BlockArgs a) {
-  const int total = a.cu_tokens[a.B], blocks = a.cu_blocks[a.B];
-  const int N = a.num_blocks;
+// Requests whose plan fits shared memory: all in one launch.
+constexpr int kBlockShared = 8192;  // requests
+__global__ void __cluster_dims__(kBlockCtas, 1, 1) __launch_bounds__(kBlockThreads) block_step_kernel(const BlockArgs a) {
+  extern __shared__ __align__(16) int32_t plan_words[];
+  const BlockPlan plan = {plan_words, plan_words + (a.B + 1), plan_words + 2 * (a.B + 1), plan_words + 3 * (a.B + 1)};
+  const int tid = threadIdx.x, rank = blockIdx.x, bs_log2 = __ffs(a.bs) - 1;
+  int ring[2];
+  uint32_t bad;
+  const int head = block_plan(a, plan, rank, kBlockCtas, ring, &bad);
+  // All have read what the outputs may overwrite.  (Blocks that went back lie
+  // behind the ring's free ones, which are read below.)
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  const int me = rank * kBlockThreads + tid;
+  for (int b = me; b <= a.B; b += kBlockCtas * kBlockThreads) {
+    a.cu_tokens[b] = plan.cu_tokens[b];
+    a.cu_blocks[b] = plan.cu_blocks[b];
+    if (b < a.B) {
+      a.kv_len_out[b] = plan.kept[b];
+      a.held_out[b] = plan.held[b];
+    }
+  }
+  if (me == 0) {
+    a.ring_state_out[0] = ring[0];
+    a.ring_state_out[1] = ring[1];
+  }
+  if (rank == 0 && bad && a.err != nullptr) atomicOr(a.err, SPECDEC_DEV_ERR_BLOCKS);
+  const int total = plan.cu_tokens[a.B], blocks = plan.cu_blocks[a.B];
+  for (int t = 4 * me; t < a.capacity; t += 4 * kBlockCtas * kBlockThreads) fill_tokens(a, plan, bs_log2, head, t, total);
+  for (int i = me; i < blocks; i += kBlockCtas * kBlockThreads) fill_block(a, plan, head, i);
+}
+
+// More requests, or many tokens: the plan by one CTA, in the outputs' arrays,
+// then the rest by many.
+__global__ void __launch_bounds__(kBlockThreads) block_plan_kernel(const BlockArgs a) {
+  const BlockPlan plan = {a.cu_tokens, a.cu_blocks, a.kv_len_out, a.held_out};
+  int ring[2];
+  uint32_t bad;
+  block_plan(a, plan, 0, 1, ring, &bad);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    a.ring_state_out[0] = ring[0];
+    a.ring_state_out[1] = ring[1];
+  }
+  if (bad && a.err != nullptr) atomicOr(a.err, SPECDEC_DEV_ERR_BLOCKS);
+}
+__global__ void __launch_bounds__(256) block_fill_kernel(const BlockArgs a) {
+  const BlockPlan plan = {a.cu_tokens, a.cu_blocks, a.kv_len_out, a.held_out};
+  const int total = a.cu_tokens[a.B], blocks = a.cu_blocks[a.B], N = a.num_blocks, bs_log2 = __ffs(a.bs) - 1;
   const int head = static_cast<int>((static_cast<long long>(a.ring_state_out[0]) + N - blocks) % N);
-  const int t = static_cast<int>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (t < a.capacity) fill_token(a, head, t, total);
-  for (int i = t; i < blocks; i += static_cast<int>(gridDim.x) * blockDim.x) fill_block(a, head, i);
+  const int me = static_cast<int>(blockIdx.x) * blockDim.x + threadIdx.x, all = static_cast<int>(gridDim.x) * blockDim.x;
+  for (int i = me; i < blocks; i += all) fill_block(a, plan, head, i);
+  if (4LL * me < a.capacity) fill_tokens(a, plan, bs_log2, head, 4 * me, total);
 }
 
 // ---------------------------------------------------------------- kv_append

@@ -177,8 +177,8 @@ extern "C" specdec_status_t spec_process_logits(
   return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 
-// Capacity up to which one CTA writes the slots too.
-constexpr int32_t kFillInPlan = 8192;
+// Tokens up to which the plan's cluster writes the slots too.
+constexpr int32_t kFillInPlan = 1 << 20;
 
 extern "C" specdec_status_t kv_block_step(int32_t B, int32_t block_size, int32_t max_blocks, int32_t num_blocks,
                                           const int32_t* kv_len, const int32_t* accepted_len,
@@ -220,12 +220,19 @@ extern "C" specdec_status_t kv_block_step(int32_t B, int32_t block_size, int32_t
   a.slot_map = slot_map;
   a.positions = positions;
   a.err = error_word;
-  a.fill = capacity <= kFillInPlan ? 1 : 0;
+  a.vec = capacity > 0 && aligned(slot_map, 16) && aligned(positions, 16) ? 1 : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  block_plan_kernel<<<1, kBlockThreads, 0, st>>>(a);
-  if (!a.fill) {
+  if (B <= kBlockShared && capacity <= kFillInPlan) {
+    const int bytes = 4 * (B + 1) * static_cast<int>(sizeof(int32_t));
+    if (bytes > 40 * 1024 && cudaFuncSetAttribute(block_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                  4 * (kBlockShared + 1) * static_cast<int>(sizeof(int32_t))) != cudaSuccess)
+      return SPECDEC_ERR_CUDA;
+    block_step_kernel<<<kBlockCtas, kBlockThreads, bytes, st>>>(a);
+  } else {
+    block_plan_kernel<<<1, kBlockThreads, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
-    block_fill_kernel<<<static_cast<unsigned>((capacity + 255) / 256), 256, 0, st>>>(a);
+    const int64_t threads = (static_cast<int64_t>(capacity) + 3) / 4;
+    block_fill_kernel<<<static_cast<unsigned>(threads < 256 ? 1 : (threads + 255) / 256), 256, 0, st>>>(a);
   }
   return launched();
 }

@@ -298,10 +298,13 @@ struct AppendArgs {
   float* scale[2];
   const int32_t* slot_map;
   int32_t T, H, bs, num_blocks;
-  int32_t window;  // tokens whose runs' starts one CTA takes
+  int32_t window;   // tokens whose runs' starts one CTA takes
+  int32_t team;     // threads of a run's head, 32 to 256
+  int32_t pairs;    // heads of k and v that one CTA takes
 };
 
-constexpr int kAppendThreads = 128;
+constexpr int kAppendThreads = 256;
+constexpr int kAppendVecs = 16;  // 16-byte loads of a thread
 constexpr int kMaxBlockSize = 128;
 
 // The least power of two s with amax <= 448 s, for a finite amax > 0; 0 of 0.
@@ -349,84 +352,143 @@ __device__ __forceinline__ void unpack16<__nv_bfloat16>(const uint4& q, float* f
   }
 }
 
-// Simple form: a CTA per (window of tokens, head, k or v) goes through the
-// runs that start in its window.
+// Bits (as a float) of the largest finite magnitude of 16 bytes.
+template <typename Elt>
+__device__ __forceinline__ uint32_t finite_top(const uint4& q);
+template <>
+__device__ __forceinline__ uint32_t finite_top<float>(const uint4& q) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = w[i] & 0x7FFFFFFFu;
+    top = max(top, u < 0x7F800000u ? u : 0);
+  }
+  return top;
+}
+template <>
+__device__ __forceinline__ uint32_t finite_top<__nv_bfloat16>(const uint4& q) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = w[i] << 16 & 0x7FFF0000u, hi = w[i] & 0x7FFF0000u;
+    top = max(top, max(lo < 0x7F800000u ? lo : 0, hi < 0x7F800000u ? hi : 0));
+  }
+  return top;
+}
+
+// A team of warps takes a run's rows of one head of k or v: as many threads as
+// hold a whole block's rows in registers, 16 loads of 16 bytes each, so that
+// the rows are read once and all at a time.  A CTA has the runs that start in
+// its window of tokens; its teams go through their pairs of a run and a head.
+// Bound by the rows read and the codes written.
 template <typename Elt, int D>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(const AppendArgs a) {
   constexpr int E = 16 / sizeof(Elt);  // values of a 16-byte load
   constexpr int VR = D / E;            // loads of a row
-  __shared__ int32_t slots[kMaxBlockSize * 2 + 1];
-  __shared__ float red[kAppendThreads / 32];
-  const int tid = threadIdx.x;
-  const int h = blockIdx.y, which = blockIdx.z;
+  constexpr int kSpan = 2 * kMaxBlockSize;
+  __shared__ int32_t slots[kSpan + 1];
+  __shared__ uint32_t breaks[kSpan / 32 + 1];  // tokens that do not go on in the run before them
+  __shared__ int32_t starts[kMaxBlockSize], runs;
+  __shared__ uint32_t red[kAppendThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31;
   const long long t0 = static_cast<long long>(blockIdx.x) * a.window;
   const int span = static_cast<int>(min(static_cast<long long>(a.window) + a.bs, a.T - t0));  // tokens looked at
-  const long long most = static_cast<long long>(a.num_blocks) * a.bs;
+  const int most = a.num_blocks * a.bs, bs_log2 = __ffs(a.bs) - 1;
   for (int i = tid; i <= span; i += kAppendThreads) {
     const long long t = t0 + i - 1;
-    int s = t >= 0 ? __ldg(a.slot_map + t) : -1;
-    if (s >= most) s = -1;
-    slots[i] = s;
+    const int s = t >= 0 ? __ldg(a.slot_map + t) : -1;
+    slots[i] = s >= most ? -1 : s;
   }
+  if (tid == 0) runs = 0;
   __syncthreads();
-  const char* x = static_cast<const char*>(a.x[which]) + h * a.head_stride[which];
-  const int owned = min(a.window, span);
-  for (int i = 0; i < owned;) {
-    const int s = slots[i + 1], before = slots[i];
-    const int block = s / a.bs, off = s - block * a.bs;
-    if (s < 0 || (before >= 0 && before + 1 == s && off != 0)) {  // none, or inside a run
-      ++i;
-      continue;
+  {
+    const int i = tid;  // (the span is at most the CTA's threads)
+    const int s = i < span ? slots[i + 1] : -1, before = i < span ? slots[i] : -1;
+    const bool starts_here = s >= 0 && !(before >= 0 && before + 1 == s && (s & (a.bs - 1)) != 0);
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, s < 0 || starts_here);
+    if (lane == 0) breaks[tid >> 5] = m;
+    if (starts_here && i < a.window) starts[atomicAdd(&runs, 1)] = i;
+  }
+  static_assert(kSpan <= kAppendThreads, "a thread for each token looked at");
+  __syncthreads();
+  const int team = tid / a.team, teams = kAppendThreads / a.team, k0 = tid - team * a.team;
+  const int pair0 = blockIdx.y * a.pairs, pairs = min(a.pairs, 2 * a.H - pair0);
+  auto team_barrier = [&]() {
+    if (a.team == 32)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(a.team) : "memory");
+  };
+  for (int item = team; item < runs * pairs; item += teams) {
+    const int run = item / pairs, pair = pair0 + item - run * pairs;
+    const int which = pair >= a.H ? 1 : 0, h = pair - which * a.H, i = starts[run], s = slots[i + 1];
+    const int block = s >> bs_log2, off = s & (a.bs - 1);
+    // the run goes on to the next break
+    int n = min(span - i, a.bs - off);
+    {
+      const int w = (i + 1) >> 5;
+      uint32_t m = breaks[w] & (0xFFFFFFFFu << ((i + 1) & 31));
+      int at = w;
+      while (m == 0 && ++at < kSpan / 32) m = breaks[at];
+      if (m != 0) n = min(n, at * 32 + __ffs(m) - 1 - i);
     }
-    int n = 1;
-    while (i + n < span && off + n < a.bs && slots[i + n + 1] == s + n) ++n;
-    const char* row = x + (t0 + i) * a.token_stride[which];
-    float amax = 0.f;
-    for (int k = tid; k < n * VR; k += kAppendThreads) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + (k / VR) * a.token_stride[which]) + k % VR);
-      float f[E];
-      unpack16<Elt>(q, f);
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (isfinite(f[e])) amax = fmaxf(amax, fabsf(f[e]));
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-    __syncthreads();
-    if ((tid & 31) == 0) red[tid >> 5] = amax;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, red[w]);
-    float* sp = a.scale[which] + static_cast<long long>(block) * a.H + h;
+    const long long stride = which ? a.token_stride[1] : a.token_stride[0];
+    const char* row = static_cast<const char*>(which ? a.x[1] : a.x[0]) + h * (which ? a.head_stride[1] : a.head_stride[0]) + (t0 + i) * stride;
+    float* sp = (which ? a.scale[1] : a.scale[0]) + static_cast<long long>(block) * a.H + h;
+    uint8_t* tile = (which ? a.cache[1] : a.cache[0]) + (static_cast<long long>(block) * a.H + h) * a.bs * D;
     const float old = off > 0 ? *sp : 0.f;
+    uint4 x[kAppendVecs];
+#pragma unroll
+    for (int v = 0; v < kAppendVecs; ++v) {
+      const int k = k0 + v * a.team;
+      x[v] = k < n * VR ? __ldg(reinterpret_cast<const uint4*>(row + (k / VR) * stride) + k % VR) : make_uint4(0, 0, 0, 0);
+    }
+    uint32_t top = 0;  // the largest finite magnitude's bits
+#pragma unroll
+    for (int v = 0; v < kAppendVecs; ++v) top = max(top, finite_top<Elt>(x[v]));
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (a.team > 32) {
+      if (lane == 0) red[tid >> 5] = top;
+      team_barrier();
+      top = __reduce_max_sync(0xFFFFFFFFu, lane < a.team / 32 ? red[team * (a.team / 32) + lane] : 0);
+    }
+    const float amax = __uint_as_float(top);
     const float now = fmaxf(pow2_scale(amax), pow2_ceil(old));
     const float inv = pow2_inverse(now);
-    uint8_t* tile = a.cache[which] + (static_cast<long long>(block) * a.H + h) * a.bs * D;
     if (off > 0 && now > old) {  // the older tokens move to the new scale
       const float ratio = old * inv;
-      for (int k = tid; k < off * (D / 2); k += kAppendThreads) {
-        uint16_t* c = reinterpret_cast<uint16_t*>(tile) + k;
-        const float2 f = e4m3_values(*c);
-        *c = static_cast<uint16_t>(e4m3_pair(f.x * ratio, f.y * ratio));
+      for (int k = k0; k < off * (D / 16); k += a.team) {
+        uint4* c = reinterpret_cast<uint4*>(tile) + k;
+        uint4 q = *c;
+        uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 lo = e4m3_values(w[e] & 0xFFFFu), hi = e4m3_values(w[e] >> 16);
+          w[e] = e4m3_pair(lo.x * ratio, lo.y * ratio) | e4m3_pair(hi.x * ratio, hi.y * ratio) << 16;
+        }
+        *c = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
-    __syncthreads();  // everyone has read the old scale
-    if (tid == 0) *sp = now;
-    for (int k = tid; k < n * VR; k += kAppendThreads) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + (k / VR) * a.token_stride[which]) + k % VR);
+    uint8_t* to = tile + off * D;
+#pragma unroll
+    for (int v = 0; v < kAppendVecs; ++v) {
+      const int k = k0 + v * a.team;
+      if (k >= n * VR) continue;
       float f[E];
-      unpack16<Elt>(q, f);
-      uint8_t* c = tile + (off + k / VR) * D + (k % VR) * E;
+      unpack16<Elt>(x[v], f);
       uint32_t w[E / 4];
 #pragma unroll
       for (int e = 0; e < E / 4; ++e)
         w[e] = e4m3_pair(f[4 * e] * inv, f[4 * e + 1] * inv) | (e4m3_pair(f[4 * e + 2] * inv, f[4 * e + 3] * inv) << 16);
       if (E == 8)
-        *reinterpret_cast<uint2*>(c) = make_uint2(w[0], w[E / 4 - 1]);
+        reinterpret_cast<uint2*>(to)[k] = make_uint2(w[0], w[E / 4 - 1]);
       else
-        *reinterpret_cast<uint32_t*>(c) = w[0];
+        reinterpret_cast<uint32_t*>(to)[k] = w[0];
     }
-    i += n;
+    team_barrier();  // everyone has read the old scale, and `red`
+    if (k0 == 0) *sp = now;
   }
 }
 

@@ -272,10 +272,18 @@ extern "C" specdec_status_t kv_append(const void* k, const void* v, specdec_dtyp
   a.H = H;
   a.bs = block_size;
   a.num_blocks = num_blocks;
-  // A few thousand CTAs where there are tokens for them.
-  const int64_t w = static_cast<int64_t>(T) * H * 2 / 4096;
-  a.window = static_cast<int32_t>(w < 1 ? 1 : (w > block_size ? block_size : w));
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(T) + a.window - 1) / a.window), static_cast<unsigned>(H), 2);
+  // A team holds a block's rows: 16 loads of 16 bytes a thread.
+  const int64_t loads = static_cast<int64_t>(block_size) * D * elt / 16;
+  a.team = 32;
+  while (a.team * kAppendVecs < loads) a.team *= 2;
+  a.pairs = kAppendThreads / a.team < 2 * H ? kAppendThreads / a.team : 2 * H;
+  const unsigned splits = static_cast<unsigned>((2 * H + a.pairs - 1) / a.pairs);
+  // Windows of a block's tokens, or fewer while that leaves SMs without work.
+  int dev = 0, sms = 0;
+  if (device_sms(&dev, &sms) != cudaSuccess) return SPECDEC_ERR_CUDA;
+  a.window = block_size;
+  while (a.window > 1 && static_cast<int64_t>(T) * splits < static_cast<int64_t>(a.window) * 4 * sms) a.window /= 2;
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(T) + a.window - 1) / a.window), splits);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == SPECDEC_F32) {
     if (D == 64)

@@ -12,6 +12,12 @@ import torch
 
 from . import _check, _dtype_code, _need, _on, _one_device, _ptr, _stream, load_library
 
+# A decode step's calls last some microseconds on the GPU: their checks use one
+# look at each tensor, and the long way round only to say what is wrong.
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+I32, F32, BF16 = torch.int32, torch.float32, torch.bfloat16
+
 DEV_ERR_BLOCKS, DEV_ERR_PENALTY = 32, 64
 ATTENTION_WORKSPACE_BYTES = 64 << 20
 E4M3 = torch.float8_e4m3fn
@@ -20,10 +26,41 @@ E4M3 = torch.float8_e4m3fn
 STEP_EXPORTS = ("kv_block_step", "kv_append", "spec_attention", "spec_process_logits")
 
 
-def _error_word(t: Optional[torch.Tensor]):
-    if t is not None and t.numel() * t.element_size() < 4:
+def _device(t: torch.Tensor, stream) -> int:
+    """The index of the device of a call's first tensor, which is the current
+    one; -2 where it is on none (after the other checks _on_stream says so)."""
+    dev = t.get_device()
+    if dev < 0:
+        return -2
+    if stream is not None or dev != _current_device():
+        _one_device(t, stream=stream)
+    return dev
+
+
+def _at(t: Optional[torch.Tensor], n: int, what: str, dtype, dev: int):
+    """Address of a contiguous tensor of n elements of dtype on a device."""
+    if t is None:
+        return None
+    if t.numel() != n or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _need(t, n, what, dtype)
+        if dev >= 0:
+            _ptr(t)
+            _one_device(t)
+    return t.data_ptr()
+
+
+def _word(t: Optional[torch.Tensor], dev: int):
+    if t is None:
+        return None
+    if t.numel() * t.element_size() < 4:
         raise ValueError("error_word must hold at least 4 bytes")
-    return _ptr(t)
+    return _at(t, t.numel(), "error_word", t.dtype, dev)
+
+
+def _on_stream(stream, dev: int):
+    if dev < 0:
+        raise ValueError("spec-decode tensors must live on a CUDA device")
+    return _current_stream(dev) if stream is None else _stream(stream)
 
 
 class BlockStep(NamedTuple):
@@ -62,59 +99,58 @@ def kv_block_step(block_table: torch.Tensor, kv_len: torch.Tensor, held: torch.T
         raise ValueError("block_table must be [B, max_blocks]")
     B, width = block_table.shape
     blocks = free_ring.numel()
-    i32 = torch.int32
-    _need(block_table, B * width, "block_table", i32)
-    _need(kv_len, B, "kv_len", i32)
-    _need(held, B, "held", i32)
-    _need(new_tokens, B, "new_tokens", i32)
-    _need(accepted_len, B, "accepted_len", i32)
-    _need(free_ring, blocks, "free_ring", i32)
-    _need(ring_state, 2, "ring_state", i32)
     if capacity < 0:
         raise ValueError("capacity must not be negative")
+    dev = _device(block_table, stream)
+    fixed = (_at(kv_len, B, "kv_len", I32, dev), _at(accepted_len, B, "accepted_len", I32, dev),
+             _at(new_tokens, B, "new_tokens", I32, dev), _at(held, B, "held", I32, dev),
+             _at(block_table, B * width, "block_table", I32, dev), _at(free_ring, blocks, "free_ring", I32, dev),
+             _at(ring_state, 2, "ring_state", I32, dev))
     if out is None:
+        # one allocation; slot_map and positions lie on 16 bytes
+        pad = -capacity % 4
+        sizes = [capacity, pad, capacity, B, B, 2, B + 1, B + 1]
         with _on(stream):
-            # one allocation, each part on a 16-byte boundary
-            sizes = (B, B, 2, B + 1, B + 1, capacity, capacity)
-            buf = torch.empty(sum((n + 3) // 4 * 4 for n in sizes), dtype=i32, device=block_table.device)
-            parts, at = [], 0
-            for n in sizes:
-                parts.append(buf[at:at + n])
-                at += (n + 3) // 4 * 4
-            out = BlockStep(*parts)
+            buf = torch.empty(sum(sizes), dtype=I32, device=block_table.device)
+        slot_map, _, positions, *rest = buf.split_with_sizes(sizes)
+        out = BlockStep(*rest, slot_map, positions)
+        at = buf.data_ptr()
+        small = at + 4 * (2 * capacity + pad)
+        results = (small, small + 4 * B, small + 8 * B, small + 8 * B + 8, small + 12 * B + 12, at,
+                   at + 4 * (capacity + pad))
     else:
-        for t, n, what in zip(out, (B, B, 2, B + 1, B + 1, capacity, capacity), BlockStep._fields):
-            _need(t, n, f"out.{what}", i32)
-    _one_device(block_table, kv_len, held, new_tokens, accepted_len, free_ring, ring_state, *out, error_word,
-                stream=stream)
-    _check(load_library().kv_block_step(
-        B, block_size, width, blocks, _ptr(kv_len), _ptr(accepted_len), _ptr(new_tokens), _ptr(held),
-        _ptr(block_table), _ptr(free_ring), _ptr(ring_state), _ptr(out.kv_len), _ptr(out.held), _ptr(out.ring_state),
-        _ptr(out.cu_tokens), _ptr(out.cu_blocks), _ptr(out.slot_map), _ptr(out.positions), capacity,
-        _error_word(error_word), _stream(stream)), "kv_block_step")
+        results = [_at(t, n, f"out.{what}", I32, dev)
+                   for t, n, what in zip(out, (B, B, 2, B + 1, B + 1, capacity, capacity), BlockStep._fields)]
+    _check(load_library().kv_block_step(B, block_size, width, blocks, *fixed, *results, capacity,
+                                        _word(error_word, dev), _on_stream(stream, dev)), "kv_block_step")
     return out
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale):
-    """Shape (num_blocks, H, block_size, D) of a cache after its checks."""
-    if k_cache.dim() != 4 or k_cache.dtype != E4M3 or v_cache.dtype != E4M3:
+def _cache(k_cache, v_cache, k_scale, v_scale, dev: int):
+    """Shape (num_blocks, H, block_size, D) of a cache and the addresses of
+    its four parts, after its checks."""
+    if k_cache.dim() != 4 or k_cache.dtype is not E4M3 or v_cache.dtype is not E4M3:
         raise TypeError("k_cache and v_cache must be [num_blocks, H, block_size, D] of float8_e4m3fn")
-    if v_cache.shape != k_cache.shape:
+    shape = k_cache.shape
+    if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have one shape")
-    blocks, H, bs, D = k_cache.shape
-    _need(k_scale, blocks * H, "k_scale", torch.float32)
-    _need(v_scale, blocks * H, "v_scale", torch.float32)
-    return blocks, H, bs, D
+    blocks, H, bs, D = shape
+    n = blocks * H
+    return blocks, H, bs, D, (_at(k_cache, n * bs * D, "k_cache", E4M3, dev), _at(v_cache, n * bs * D, "v_cache", E4M3, dev),
+                              _at(k_scale, n, "k_scale", F32, dev), _at(v_scale, n, "v_scale", F32, dev))
 
 
-def _strided(x: torch.Tensor, what: str):
-    """Pointer and the strides of tokens and heads of [T, H, D] rows whose D
+def _strided(x: torch.Tensor, what: str, dev: int):
+    """Address and the strides of tokens and heads of [T, H, D] rows whose D
     values are contiguous."""
-    if not x.is_cuda:
-        raise ValueError("spec-decode tensors must live on a CUDA device")
-    if x.stride(2) != 1:
+    if x.get_device() != dev and dev >= 0:
+        if not x.is_cuda:
+            raise ValueError("spec-decode tensors must live on a CUDA device")
+        _one_device(x)
+    token, head, one = x.stride()
+    if one != 1:
         raise ValueError(f"the last dimension of {what} must be contiguous")
-    return ctypes.c_void_p(x.data_ptr()), x.stride(0), x.stride(1)
+    return x.data_ptr(), token, head
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -122,19 +158,18 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_cache:
     """Writes the keys and values [T, H, D] (bf16 or fp32; views of a fused
     projection will do) of new tokens into the cache at slot_map [T] (see
     include/specdec_step.h)."""
-    blocks, H, bs, D = _cache(k_cache, v_cache, k_scale, v_scale)
+    dev = _device(k, stream)
+    blocks, H, bs, D, cache = _cache(k_cache, v_cache, k_scale, v_scale, dev)
     if k.dim() != 3 or v.shape != k.shape or k.shape[1:] != (H, D):
         raise ValueError("k and v must be [T, H, D] with the cache's H and D")
     if v.dtype != k.dtype:
         raise TypeError("k and v must have one dtype")
     T = k.shape[0]
-    _need(slot_map, T, "slot_map", torch.int32)
-    _one_device(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, stream=stream)
-    kp, kt, kh = _strided(k, "k")
-    vp, vt, vh = _strided(v, "v")
-    _check(load_library().kv_append(kp, vp, _dtype_code(k), T, H, D, kt, kh, vt, vh, _ptr(slot_map), blocks, bs,
-                                    _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _stream(stream)),
-           "kv_append")
+    slots = _at(slot_map, T, "slot_map", I32, dev)
+    kp, kt, kh = _strided(k, "k", dev)
+    vp, vt, vh = _strided(v, "v", dev)
+    _check(load_library().kv_append(kp, vp, _dtype_code(k), T, H, D, kt, kh, vt, vh, slots, blocks, bs, *cache,
+                                    _on_stream(stream, dev)), "kv_append")
 
 
 def new_attention_workspace(device=None, stream=None) -> torch.Tensor:
@@ -150,36 +185,35 @@ def spec_attention(q: torch.Tensor, cu_tokens: torch.Tensor, kv_len: torch.Tenso
     """Attention of the new tokens' queries [T, Hq, D] (bf16) over the cache,
     causal among the new tokens (see include/specdec_step.h).  `scale`
     defaults to 1 / sqrt(D).  Returns [T, Hq, D] bf16."""
-    blocks, H, bs, D = _cache(k_cache, v_cache, k_scale, v_scale)
-    if q.dim() != 3 or q.shape[2] != D or q.dtype != torch.bfloat16:
+    dev = _device(q, stream)
+    blocks, H, bs, D, cache = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    if q.dim() != 3 or q.shape[2] != D or q.dtype is not BF16:
         raise TypeError("q must be [T, Hq, D] of bfloat16 with the cache's D")
     T, Hq, _ = q.shape
     B = kv_len.numel()
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B, max_blocks]")
     width = block_table.shape[1]
-    _need(cu_tokens, B + 1, "cu_tokens", torch.int32)
-    _need(kv_len, B, "kv_len", torch.int32)
-    _need(block_table, B * width, "block_table", torch.int32)
     if scale is not None and not scale > 0:
         raise ValueError("scale must be positive")
     if out is None:
         with _on(stream):
-            out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
+            out = torch.empty(T, Hq, D, dtype=BF16, device=q.device)
     elif out.shape != q.shape:
         raise ValueError("out must be [T, Hq, D]")
-    _need(out, T * Hq * D, "out", torch.bfloat16)
+    lengths = (_at(cu_tokens, B + 1, "cu_tokens", I32, dev), _at(kv_len, B, "kv_len", I32, dev),
+               _at(block_table, B * width, "block_table", I32, dev))
+    to = _at(out, T * Hq * D, "out", BF16, dev)
     if workspace is None:
         workspace = new_attention_workspace(device=q.device, stream=stream)
-    _one_device(q, cu_tokens, kv_len, block_table, k_cache, v_cache, k_scale, v_scale, out, workspace, stream=stream)
-    qp, qt, qh = _strided(q, "q")
+    qp, qt, qh = _strided(q, "q", dev)
     if qh != D and Hq > 1:
         raise ValueError("the heads of q must be contiguous")
-    _check(load_library().spec_attention(qp, qt if T > 1 else Hq * D, T, Hq, H, D, B, _ptr(cu_tokens), _ptr(kv_len),
-                                         _ptr(block_table), width, blocks, bs, _ptr(k_cache), _ptr(v_cache),
-                                         _ptr(k_scale), _ptr(v_scale), 0.0 if scale is None else float(scale),
-                                         _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)),
-           "spec_attention")
+    size = workspace.numel()
+    _check(load_library().spec_attention(qp, qt if T > 1 else Hq * D, T, Hq, H, D, B, *lengths, width, blocks, bs,
+                                         *cache, 0.0 if scale is None else float(scale), to,
+                                         _at(workspace, size, "workspace", workspace.dtype, dev), size,
+                                         _on_stream(stream, dev)), "spec_attention")
     return out
 
 
@@ -199,51 +233,51 @@ def spec_process_logits(logits: torch.Tensor, history: Optional[torch.Tensor] = 
         raise ValueError("logits must be [B, n_max+1, V]")
     B, rows, V = logits.shape
     n_max = rows - 1
-    i32, f32 = torch.int32, torch.float32
-    if out is None:
-        out = logits
-    elif out.shape != logits.shape or out.dtype != logits.dtype:
-        raise ValueError("out must be of logits' shape and dtype")
+    dev = _device(logits, stream)
+    dtype = logits.dtype
+    at = _at(logits, B * rows * V, "logits", dtype, dev)
+    if out is None or out is logits:
+        out, to = logits, at
+    else:
+        if out.shape != logits.shape or out.dtype != dtype:
+            raise ValueError("out must be of logits' shape and dtype")
+        to = _at(out, B * rows * V, "out", dtype, dev)
     S = 0
+    past = (None, 0, None, None)
     if history is not None:
         if history.dim() != 2:
             raise ValueError("history must be [B, S]")
         S = history.shape[1]
-        _need(history, B * S, "history", i32)
         if prompt_len is None or history_len is None:
             raise ValueError("history needs prompt_len and history_len")
-        _need(prompt_len, B, "prompt_len", i32)
-        _need(history_len, B, "history_len", i32)
+        lens = _at(prompt_len, B, "prompt_len", I32, dev), _at(history_len, B, "history_len", I32, dev)
+        ids = _at(history, B * S, "history", I32, dev)
+        if S:
+            past = (ids, S, *lens)
     if n_max > 0 and draft_tokens is None:
         raise ValueError("rows after the first need draft_tokens")
-    _need(draft_tokens, B * n_max, "draft_tokens", i32)
-    _need(draft_len, B, "draft_len", i32)
-    for t, what in ((repetition, "repetition"), (presence, "presence"), (frequency, "frequency")):
-        _need(t, B, what, f32)
+    drafts = (_at(draft_tokens, B * n_max, "draft_tokens", I32, dev), _at(draft_len, B, "draft_len", I32, dev))
+    penalties = (_at(repetition, B, "repetition", F32, dev), _at(presence, B, "presence", F32, dev),
+                 _at(frequency, B, "frequency", F32, dev))
     num_bias = 0
+    biases = (None, None, None)
     if bias_offsets is not None:
         if bias_ids is None or bias_values is None:
             raise ValueError("bias_offsets needs bias_ids and bias_values")
-        _need(bias_offsets, B + 1, "bias_offsets", i32)
         num_bias = bias_ids.numel()
-        _need(bias_ids, num_bias, "bias_ids", i32)
-        _need(bias_values, num_bias, "bias_values", f32)
-    masks = 0
+        biases = (_at(bias_offsets, B + 1, "bias_offsets", I32, dev), _at(bias_ids, num_bias, "bias_ids", I32, dev),
+                  _at(bias_values, num_bias, "bias_values", F32, dev))
     if (mask is None) != (mask_rows is None):
         raise ValueError("mask and mask_rows go together")
+    masks, words, named = 0, None, None
     if mask is not None:
         if mask.dim() != 2 or mask.shape[1] != (V + 31) // 32:
             raise ValueError("mask must be [masks, ceil(V / 32)]")
         masks = mask.shape[0]
-        _need(mask, masks * mask.shape[1], "mask", i32)
-        _need(mask_rows, B * rows, "mask_rows", i32)
+        words, named = _at(mask, masks * mask.shape[1], "mask", I32, dev), _at(mask_rows, B * rows, "mask_rows", I32, dev)
         if masks == 0:
-            mask = mask_rows = None
-    _one_device(logits, out, history, prompt_len, history_len, draft_tokens, draft_len, repetition, presence, frequency,
-                bias_offsets, bias_ids, bias_values, mask, mask_rows, error_word, stream=stream)
-    _check(load_library().spec_process_logits(
-        _ptr(logits), _ptr(out), _dtype_code(logits), B, n_max, V, _ptr(history) if S else None, S,
-        _ptr(prompt_len) if S else None, _ptr(history_len) if S else None, _ptr(draft_tokens), _ptr(draft_len),
-        _ptr(repetition), _ptr(presence), _ptr(frequency), _ptr(bias_offsets), _ptr(bias_ids), _ptr(bias_values),
-        num_bias, _ptr(mask), masks, _ptr(mask_rows), _error_word(error_word), _stream(stream)), "spec_process_logits")
+            words = named = None
+    _check(load_library().spec_process_logits(at, to, _dtype_code(logits), B, n_max, V, *past, *drafts, *penalties,
+                                              *biases, num_bias, words, masks, named, _word(error_word, dev),
+                                              _on_stream(stream, dev)), "spec_process_logits")
     return out

@@ -12,10 +12,10 @@ namespace specdec {
 // Prefix sums over the requests (blocks asked for, then tokens, blocks taken
 // and given of those that are granted), then the slots of the tokens and the
 // table's new entries.  A few KB to some MB: bound by latency, so one launch
-// and few dependent loads.  A cluster of 8 CTAs: each makes the whole plan for
-// itself, in shared memory, and after all have read the lengths (the outputs
-// may be the same arrays) they share the writing.  A thread writes four
-// neighbouring tokens, whose request it finds by bisection in shared memory.
+// and few dependent loads.  Each CTA makes the whole plan for itself, in shared
+// memory, and writes its share of the tokens: a thread four neighbouring ones,
+// whose request it finds by bisection.  (A cluster would let the outputs be the
+// inputs' arrays, but its launch alone costs the host 15 us.)
 struct BlockArgs {
   int32_t B, bs, max_blocks, num_blocks, capacity;
   const int32_t* kv_len;
@@ -37,41 +37,49 @@ struct BlockArgs {
 };
 
 constexpr int kBlockThreads = 1024;
-constexpr int kBlockCtas = 8;
 
-// Exclusive prefix sums over the block of N values a thread; `total` are the
-// sums.  `part` holds a warp's sums each.
+// Sums that stay at the largest int: what they are compared with is no larger.
+__device__ __forceinline__ uint32_t capped_sum(uint32_t x, uint32_t y) { return min(x + y, 0x7FFFFFFFu); }
+
+// Exclusive prefix sums over the block of N values a thread (each at most the
+// largest int); `total` are the sums.  `part` holds a warp's sums each, and
+// then those before it.
 template <int N>
-__device__ __forceinline__ void block_prefix(const long long (&x)[N], long long (*part)[N], long long (&before)[N], long long (&total)[N]) {
+__device__ __forceinline__ void block_prefix(const uint32_t (&x)[N], uint32_t (*part)[N], uint32_t (&before)[N], uint32_t (&total)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long s[N];
+  uint32_t s[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) s[i] = x[i];
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const long long o = __shfl_up_sync(0xFFFFFFFFu, s[i], d);
-      if (lane >= d) s[i] += o;
+      const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, s[i], d);
+      if (lane >= d) s[i] = capped_sum(s[i], o);
     }
   }
   __syncthreads();  // the last use of `part` is over
   if (lane == 31) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) part[warp][i] = s[i];
+    for (int i = 0; i < N; ++i) part[warp + 1][i] = s[i];
   }
   __syncthreads();
-  // every warp sums the warps' for itself
+  if (warp < N) {
+    uint32_t w = part[lane + 1][warp];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, w, d);
+      if (lane >= d) w = capped_sum(w, o);
+    }
+    part[lane + 1][warp] = w;
+    if (lane == 0) part[0][warp] = 0;
+  }
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    long long w = part[lane][i], mine = lane < warp ? w : 0;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      w += __shfl_xor_sync(0xFFFFFFFFu, w, d);
-      mine += __shfl_xor_sync(0xFFFFFFFFu, mine, d);
-    }
-    total[i] = w;
-    before[i] = mine + s[i] - x[i];
+    total[i] = part[32][i];
+    const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, s[i], 1);
+    before[i] = capped_sum(part[warp][i], lane > 0 ? up : 0);
   }
 }
 static_assert(kBlockThreads / 32 == 32, "a lane for each warp");
@@ -154,10 +162,10 @@ __device__ __forceinline__ void fill_block(const BlockArgs& a, const BlockPlan& 
   a.table[static_cast<long long>(b) * a.max_blocks + at] = a.ring[ring_at(a, head, i)];
 }
 
-// The step's lengths, grants and prefix sums, by one CTA of a cluster of
-// `ctas`; and the blocks that go back, of its share of the requests.
+// The step's lengths, grants and prefix sums, by one CTA of `ctas` that do the
+// same; and the blocks that go back, of its share of the requests.
 __device__ __forceinline__ int block_plan(const BlockArgs& a, const BlockPlan& plan, int rank, int ctas, int* ring_out, uint32_t* bad_out) {
-  __shared__ long long part1[32][1], part3[32][3];
+  __shared__ uint32_t part1[33][1], part3[33][3];
   const int tid = threadIdx.x, lane = tid & 31;
   const int N = a.num_blocks;
   int head = a.ring_state[0], count = a.ring_state[1];
@@ -167,7 +175,7 @@ __device__ __forceinline__ int block_plan(const BlockArgs& a, const BlockPlan& p
     head = head < 0 || head >= N ? 0 : head;
     count = max(0, min(count, N));
   }
-  long long asked = 0, tokens = 0, took = 0, gave = 0;
+  uint32_t asked = 0, tokens = 0, took = 0, gave = 0;
   for (int b0 = 0; b0 < a.B; b0 += kBlockThreads) {
     const int b = b0 + tid;
     const bool in = b < a.B;
@@ -192,25 +200,27 @@ __device__ __forceinline__ int block_plan(const BlockArgs& a, const BlockPlan& p
     }
     const bool fits = need <= a.max_blocks;
     const int grow = fits ? max(need - held, 0) : 0;
-    long long x1[1] = {grow}, before1[1], sum1[1];
+    const uint32_t x1[1] = {static_cast<uint32_t>(grow)};
+    uint32_t before1[1], sum1[1];
     block_prefix(x1, part1, before1, sum1);
-    const bool granted = in && fits && (grow == 0 || asked + before1[0] + grow <= count);
-    asked += sum1[0];
+    const bool granted = in && fits && (grow == 0 || capped_sum(capped_sum(asked, before1[0]), grow) <= static_cast<uint32_t>(count));
+    asked = capped_sum(asked, sum1[0]);
     if (in && !granted) bad = 1;
     const int taken = granted ? grow : 0;
     const int given = granted ? max(held - need, 0) : 0;
     // (grants are a prefix of the requests that ask for blocks)
-    long long x[3] = {granted ? want : 0, taken, given}, before[3], sum[3];
+    const uint32_t x[3] = {static_cast<uint32_t>(granted ? want : 0), static_cast<uint32_t>(taken), static_cast<uint32_t>(given)};
+    uint32_t before[3], sum[3];
     block_prefix(x, part3, before, sum);
-    const long long tok_at = tokens + before[0], take_at = took + before[1], give_at = gave + before[2];
-    tokens += sum[0];
-    took += sum[1];
-    gave += sum[2];
+    const uint32_t tok_at = capped_sum(tokens, before[0]), take_at = capped_sum(took, before[1]), give_at = capped_sum(gave, before[2]);
+    tokens = capped_sum(tokens, sum[0]);
+    took = capped_sum(took, sum[1]);
+    gave = capped_sum(gave, sum[2]);
     if (in) {
-      if (tok_at + want > a.capacity && granted) bad = 1;
+      if (granted && tok_at + want > static_cast<uint32_t>(a.capacity)) bad = 1;
       plan.kept[b] = kept;
       plan.held[b] = held + taken - given;
-      plan.cu_tokens[b] = static_cast<int>(min(tok_at, static_cast<long long>(a.capacity)));
+      plan.cu_tokens[b] = static_cast<int>(min(tok_at, static_cast<uint32_t>(a.capacity)));
       plan.cu_blocks[b] = static_cast<int>(take_at);
     }
     // blocks that go back, a warp to a request
@@ -220,36 +230,36 @@ __device__ __forceinline__ int block_plan(const BlockArgs& a, const BlockPlan& p
       m &= m - 1;
       const int n = __shfl_sync(0xFFFFFFFFu, given, src);
       const int from = __shfl_sync(0xFFFFFFFFu, held - given, src);
-      const long long to = __shfl_sync(0xFFFFFFFFu, give_at, src);
+      const uint32_t to = __shfl_sync(0xFFFFFFFFu, give_at, src);
       const long long row = static_cast<long long>(b - lane + src) * a.max_blocks;
       for (int i = lane; i < n; i += 32)
         a.ring[static_cast<int>((static_cast<long long>(head) + count + to + i) % N)] = a.table[row + from + i];
     }
   }
   if (tid == 0) {
-    plan.cu_tokens[a.B] = static_cast<int>(min(tokens, static_cast<long long>(a.capacity)));
+    plan.cu_tokens[a.B] = static_cast<int>(min(tokens, static_cast<uint32_t>(a.capacity)));
     plan.cu_blocks[a.B] = static_cast<int>(took);
   }
   ring_out[0] = ring_at(a, head, took);
-  ring_out[1] = static_cast<int>(min(static_cast<long long>(N), count - took + gave));
+  ring_out[1] = static_cast<int>(min(static_cast<uint32_t>(N), capped_sum(count - took, gave)));
   *bad_out = bad;
   return head;
 }
 
-// Requests whose plan fits shared memory: all in one launch.
+// All in one launch, where no output is an input's array (another CTA may
+// still read it) and the plan fits shared memory.  Blocks that go back lie
+// behind the ring's free ones and in other rows than those that are taken.
 constexpr int kBlockShared = 8192;  // requests
-__global__ void __cluster_dims__(kBlockCtas, 1, 1) __launch_bounds__(kBlockThreads) block_step_kernel(const BlockArgs a) {
+__global__ void __launch_bounds__(kBlockThreads) block_step_kernel(const BlockArgs a) {
   extern __shared__ __align__(16) int32_t plan_words[];
   const BlockPlan plan = {plan_words, plan_words + (a.B + 1), plan_words + 2 * (a.B + 1), plan_words + 3 * (a.B + 1)};
-  const int tid = threadIdx.x, rank = blockIdx.x, bs_log2 = __ffs(a.bs) - 1;
+  const int rank = blockIdx.x, bs_log2 = __ffs(a.bs) - 1;
   int ring[2];
   uint32_t bad;
-  const int head = block_plan(a, plan, rank, kBlockCtas, ring, &bad);
-  // All have read what the outputs may overwrite.  (Blocks that went back lie
-  // behind the ring's free ones, which are read below.)
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-  const int me = rank * kBlockThreads + tid;
-  for (int b = me; b <= a.B; b += kBlockCtas * kBlockThreads) {
+  const int head = block_plan(a, plan, rank, gridDim.x, ring, &bad);
+  __syncthreads();
+  const int me = rank * kBlockThreads + threadIdx.x, all = static_cast<int>(gridDim.x) * kBlockThreads;
+  for (int b = me; b <= a.B; b += all) {
     a.cu_tokens[b] = plan.cu_tokens[b];
     a.cu_blocks[b] = plan.cu_blocks[b];
     if (b < a.B) {
@@ -263,12 +273,11 @@ __global__ void __cluster_dims__(kBlockCtas, 1, 1) __launch_bounds__(kBlockThrea
   }
   if (rank == 0 && bad && a.err != nullptr) atomicOr(a.err, SPECDEC_DEV_ERR_BLOCKS);
   const int total = plan.cu_tokens[a.B], blocks = plan.cu_blocks[a.B];
-  for (int t = 4 * me; t < a.capacity; t += 4 * kBlockCtas * kBlockThreads) fill_tokens(a, plan, bs_log2, head, t, total);
-  for (int i = me; i < blocks; i += kBlockCtas * kBlockThreads) fill_block(a, plan, head, i);
+  for (long long t = 4LL * me; t < a.capacity; t += 4LL * all) fill_tokens(a, plan, bs_log2, head, static_cast<int>(t), total);
+  for (int i = me; i < blocks; i += all) fill_block(a, plan, head, i);
 }
 
-// More requests, or many tokens: the plan by one CTA, in the outputs' arrays,
-// then the rest by many.
+// Otherwise: the plan by one CTA, in the outputs' arrays, then the rest by many.
 __global__ void __launch_bounds__(kBlockThreads) block_plan_kernel(const BlockArgs a) {
   const BlockPlan plan = {a.cu_tokens, a.cu_blocks, a.kv_len_out, a.held_out};
   int ring[2];
@@ -413,82 +422,89 @@ __global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(const AppendA
   }
   static_assert(kSpan <= kAppendThreads, "a thread for each token looked at");
   __syncthreads();
-  const int team = tid / a.team, teams = kAppendThreads / a.team, k0 = tid - team * a.team;
   const int pair0 = blockIdx.y * a.pairs, pairs = min(a.pairs, 2 * a.H - pair0);
-  auto team_barrier = [&]() {
-    if (a.team == 32)
-      __syncwarp();
-    else
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(a.team) : "memory");
-  };
-  for (int item = team; item < runs * pairs; item += teams) {
-    const int run = item / pairs, pair = pair0 + item - run * pairs;
-    const int which = pair >= a.H ? 1 : 0, h = pair - which * a.H, i = starts[run], s = slots[i + 1];
-    const int block = s >> bs_log2, off = s & (a.bs - 1);
-    // the run goes on to the next break
-    int n = min(span - i, a.bs - off);
-    {
-      const int w = (i + 1) >> 5;
-      uint32_t m = breaks[w] & (0xFFFFFFFFu << ((i + 1) & 31));
-      int at = w;
-      while (m == 0 && ++at < kSpan / 32) m = breaks[at];
-      if (m != 0) n = min(n, at * 32 + __ffs(m) - 1 - i);
-    }
-    const long long stride = which ? a.token_stride[1] : a.token_stride[0];
-    const char* row = static_cast<const char*>(which ? a.x[1] : a.x[0]) + h * (which ? a.head_stride[1] : a.head_stride[0]) + (t0 + i) * stride;
-    float* sp = (which ? a.scale[1] : a.scale[0]) + static_cast<long long>(block) * a.H + h;
-    uint8_t* tile = (which ? a.cache[1] : a.cache[0]) + (static_cast<long long>(block) * a.H + h) * a.bs * D;
-    const float old = off > 0 ? *sp : 0.f;
-    uint4 x[kAppendVecs];
-#pragma unroll
-    for (int v = 0; v < kAppendVecs; ++v) {
-      const int k = k0 + v * a.team;
-      x[v] = k < n * VR ? __ldg(reinterpret_cast<const uint4*>(row + (k / VR) * stride) + k % VR) : make_uint4(0, 0, 0, 0);
-    }
-    uint32_t top = 0;  // the largest finite magnitude's bits
-#pragma unroll
-    for (int v = 0; v < kAppendVecs; ++v) top = max(top, finite_top<Elt>(x[v]));
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    if (a.team > 32) {
-      if (lane == 0) red[tid >> 5] = top;
-      team_barrier();
-      top = __reduce_max_sync(0xFFFFFFFFu, lane < a.team / 32 ? red[team * (a.team / 32) + lane] : 0);
-    }
-    const float amax = __uint_as_float(top);
-    const float now = fmaxf(pow2_scale(amax), pow2_ceil(old));
-    const float inv = pow2_inverse(now);
-    if (off > 0 && now > old) {  // the older tokens move to the new scale
-      const float ratio = old * inv;
-      for (int k = k0; k < off * (D / 16); k += a.team) {
-        uint4* c = reinterpret_cast<uint4*>(tile) + k;
-        uint4 q = *c;
-        uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 lo = e4m3_values(w[e] & 0xFFFFu), hi = e4m3_values(w[e] >> 16);
-          w[e] = e4m3_pair(lo.x * ratio, lo.y * ratio) | e4m3_pair(hi.x * ratio, hi.y * ratio) << 16;
-        }
-        *c = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
-    uint8_t* to = tile + off * D;
-#pragma unroll
-    for (int v = 0; v < kAppendVecs; ++v) {
-      const int k = k0 + v * a.team;
-      if (k >= n * VR) continue;
-      float f[E];
-      unpack16<Elt>(x[v], f);
-      uint32_t w[E / 4];
-#pragma unroll
-      for (int e = 0; e < E / 4; ++e)
-        w[e] = e4m3_pair(f[4 * e] * inv, f[4 * e + 1] * inv) | (e4m3_pair(f[4 * e + 2] * inv, f[4 * e + 3] * inv) << 16);
-      if (E == 8)
-        reinterpret_cast<uint2*>(to)[k] = make_uint2(w[0], w[E / 4 - 1]);
+  // Runs that a warp holds are a warp's, longer ones a team's.
+#pragma unroll 1
+  for (int width = a.team;; width = 32) {
+    const int team = tid / width, k0 = tid - team * width;
+    auto team_barrier = [&]() {
+      if (width == 32)
+        __syncwarp();
       else
-        reinterpret_cast<uint32_t*>(to)[k] = w[0];
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(width) : "memory");
+    };
+#pragma unroll 1
+    for (int item = team; item < runs * pairs; item += kAppendThreads / width) {
+      const int run = item / pairs, pair = pair0 + item - run * pairs;
+      const int which = pair >= a.H ? 1 : 0, h = pair - which * a.H, i = starts[run], s = slots[i + 1];
+      const int block = s >> bs_log2, off = s & (a.bs - 1);
+      // the run goes on to the next break
+      int n = min(span - i, a.bs - off);
+      {
+        const int w = (i + 1) >> 5;
+        uint32_t m = breaks[w] & (0xFFFFFFFFu << ((i + 1) & 31));
+        int at = w;
+        while (m == 0 && ++at < kSpan / 32) m = breaks[at];
+        if (m != 0) n = min(n, at * 32 + __ffs(m) - 1 - i);
+      }
+      if ((width == 32) != (n * VR <= 32 * kAppendVecs)) continue;
+      const long long stride = which ? a.token_stride[1] : a.token_stride[0];
+      const char* row = static_cast<const char*>(which ? a.x[1] : a.x[0]) + h * (which ? a.head_stride[1] : a.head_stride[0]) + (t0 + i) * stride;
+      float* sp = (which ? a.scale[1] : a.scale[0]) + static_cast<long long>(block) * a.H + h;
+      uint8_t* tile = (which ? a.cache[1] : a.cache[0]) + (static_cast<long long>(block) * a.H + h) * a.bs * D;
+      const float old = off > 0 ? *sp : 0.f;
+      uint4 x[kAppendVecs];
+#pragma unroll
+      for (int v = 0; v < kAppendVecs; ++v) {
+        const int k = k0 + v * width;
+        x[v] = k < n * VR ? __ldg(reinterpret_cast<const uint4*>(row + (k / VR) * stride) + k % VR) : make_uint4(0, 0, 0, 0);
+      }
+      uint32_t top = 0;  // the largest finite magnitude's bits
+#pragma unroll
+      for (int v = 0; v < kAppendVecs; ++v) top = max(top, finite_top<Elt>(x[v]));
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      if (width > 32) {
+        if (lane == 0) red[tid >> 5] = top;
+        team_barrier();
+        top = __reduce_max_sync(0xFFFFFFFFu, lane < width / 32 ? red[team * (width / 32) + lane] : 0);
+      }
+      const float amax = __uint_as_float(top);
+      const float now = fmaxf(pow2_scale(amax), pow2_ceil(old));
+      const float inv = pow2_inverse(now);
+      if (off > 0 && now > old) {  // the older tokens move to the new scale
+        const float ratio = old * inv;
+        for (int k = k0; k < off * (D / 16); k += width) {
+          uint4* c = reinterpret_cast<uint4*>(tile) + k;
+          uint4 q = *c;
+          uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 lo = e4m3_values(w[e] & 0xFFFFu), hi = e4m3_values(w[e] >> 16);
+            w[e] = e4m3_pair(lo.x * ratio, lo.y * ratio) | e4m3_pair(hi.x * ratio, hi.y * ratio) << 16;
+          }
+          *c = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      uint8_t* to = tile + off * D;
+#pragma unroll
+      for (int v = 0; v < kAppendVecs; ++v) {
+        const int k = k0 + v * width;
+        if (k >= n * VR) continue;
+        float f[E];
+        unpack16<Elt>(x[v], f);
+        uint32_t w[E / 4];
+#pragma unroll
+        for (int e = 0; e < E / 4; ++e)
+          w[e] = e4m3_pair(f[4 * e] * inv, f[4 * e + 1] * inv) | (e4m3_pair(f[4 * e + 2] * inv, f[4 * e + 3] * inv) << 16);
+        if (E == 8)
+          reinterpret_cast<uint2*>(to)[k] = make_uint2(w[0], w[E / 4 - 1]);
+        else
+          reinterpret_cast<uint32_t*>(to)[k] = w[0];
+      }
+      team_barrier();  // everyone has read the old scale, and `red`
+      if (k0 == 0) *sp = now;
     }
-    team_barrier();  // everyone has read the old scale, and `red`
-    if (k0 == 0) *sp = now;
+    if (width == 32) break;
   }
 }
 

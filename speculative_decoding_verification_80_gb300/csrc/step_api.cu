@@ -177,9 +177,6 @@ extern "C" specdec_status_t spec_process_logits(
   return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 
-// Tokens up to which the plan's cluster writes the slots too.
-constexpr int32_t kFillInPlan = 1 << 20;
-
 extern "C" specdec_status_t kv_block_step(int32_t B, int32_t block_size, int32_t max_blocks, int32_t num_blocks,
                                           const int32_t* kv_len, const int32_t* accepted_len,
                                           const int32_t* new_tokens, const int32_t* held, int32_t* block_table,
@@ -222,12 +219,14 @@ extern "C" specdec_status_t kv_block_step(int32_t B, int32_t block_size, int32_t
   a.err = error_word;
   a.vec = capacity > 0 && aligned(slot_map, 16) && aligned(positions, 16) ? 1 : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (B <= kBlockShared && capacity <= kFillInPlan) {
+  const bool apart = kv_len_out != kv_len && held_out != held && ring_state_out != ring_state;
+  if (apart && B <= kBlockShared) {
     const int bytes = 4 * (B + 1) * static_cast<int>(sizeof(int32_t));
     if (bytes > 40 * 1024 && cudaFuncSetAttribute(block_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                   4 * (kBlockShared + 1) * static_cast<int>(sizeof(int32_t))) != cudaSuccess)
       return SPECDEC_ERR_CUDA;
-    block_step_kernel<<<kBlockCtas, kBlockThreads, bytes, st>>>(a);
+    const int64_t ctas = (static_cast<int64_t>(capacity) + 4 * kBlockThreads - 1) / (4 * kBlockThreads);
+    block_step_kernel<<<static_cast<unsigned>(ctas < 1 ? 1 : (ctas > 128 ? 128 : ctas)), kBlockThreads, bytes, st>>>(a);
   } else {
     block_plan_kernel<<<1, kBlockThreads, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
@@ -276,13 +275,13 @@ extern "C" specdec_status_t kv_append(const void* k, const void* v, specdec_dtyp
   const int64_t loads = static_cast<int64_t>(block_size) * D * elt / 16;
   a.team = 32;
   while (a.team * kAppendVecs < loads) a.team *= 2;
-  a.pairs = kAppendThreads / a.team < 2 * H ? kAppendThreads / a.team : 2 * H;
+  a.pairs = kAppendThreads / 32 < 2 * H ? kAppendThreads / 32 : 2 * H;
   const unsigned splits = static_cast<unsigned>((2 * H + a.pairs - 1) / a.pairs);
   // Windows of a block's tokens, or fewer while that leaves SMs without work.
   int dev = 0, sms = 0;
   if (device_sms(&dev, &sms) != cudaSuccess) return SPECDEC_ERR_CUDA;
   a.window = block_size;
-  while (a.window > 1 && static_cast<int64_t>(T) * splits < static_cast<int64_t>(a.window) * 4 * sms) a.window /= 2;
+  while (a.window > 1 && static_cast<int64_t>(T) * splits < static_cast<int64_t>(a.window) * 2 * sms) a.window /= 2;
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(T) + a.window - 1) / a.window), splits);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == SPECDEC_F32) {

@@ -33,7 +33,7 @@ struct BlockArgs {
   int32_t* slot_map;
   int32_t* positions;
   uint32_t* err;
-  int32_t vec;  // slot_map and positions lie on 16 bytes
+  int32_t slots_vec, positions_vec;  // they lie on 16 bytes
 };
 
 constexpr int kBlockThreads = 1024;
@@ -143,17 +143,17 @@ __device__ __forceinline__ void fill_tokens(const BlockArgs& a, const BlockPlan&
     slot[k] = (block << bs_log2) + (p & ((1 << bs_log2) - 1));
     pos[k] = p;
   }
-  if (a.vec && t + 4 <= a.capacity) {
-    *reinterpret_cast<int4*>(a.slot_map + t) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-    *reinterpret_cast<int4*>(a.positions + t) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-  } else {
+  auto store = [&](int32_t* to, const int (&x)[4], bool vec) {
+    if (vec && t + 4 <= a.capacity) {
+      *reinterpret_cast<int4*>(to + t) = make_int4(x[0], x[1], x[2], x[3]);
+    } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (t + k >= a.capacity) break;
-      a.slot_map[t + k] = slot[k];
-      a.positions[t + k] = pos[k];
+      for (int k = 0; k < 4; ++k)
+        if (t + k < a.capacity) to[t + k] = x[k];
     }
-  }
+  };
+  store(a.slot_map, slot, a.slots_vec);
+  store(a.positions, pos, a.positions_vec);
 }
 // The i-th block taken goes into its table.
 __device__ __forceinline__ void fill_block(const BlockArgs& a, const BlockPlan& plan, int head, int i) {

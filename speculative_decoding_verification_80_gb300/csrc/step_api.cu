@@ -217,7 +217,8 @@ extern "C" specdec_status_t kv_block_step(int32_t B, int32_t block_size, int32_t
   a.slot_map = slot_map;
   a.positions = positions;
   a.err = error_word;
-  a.vec = capacity > 0 && aligned(slot_map, 16) && aligned(positions, 16) ? 1 : 0;
+  a.slots_vec = aligned(slot_map, 16) ? 1 : 0;
+  a.positions_vec = aligned(positions, 16) ? 1 : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool apart = kv_len_out != kv_len && held_out != held && ring_state_out != ring_state;
   if (apart && B <= kBlockShared) {

@@ -107,17 +107,13 @@ def kv_block_step(block_table: torch.Tensor, kv_len: torch.Tensor, held: torch.T
              _at(block_table, B * width, "block_table", I32, dev), _at(free_ring, blocks, "free_ring", I32, dev),
              _at(ring_state, 2, "ring_state", I32, dev))
     if out is None:
-        # one allocation; slot_map and positions lie on 16 bytes
-        pad = -capacity % 4
-        sizes = [capacity, pad, capacity, B, B, 2, B + 1, B + 1]
+        # one allocation, in the fields' order (slot_map lies on 16 bytes)
         with _on(stream):
-            buf = torch.empty(sum(sizes), dtype=I32, device=block_table.device)
-        slot_map, _, positions, *rest = buf.split_with_sizes(sizes)
-        out = BlockStep(*rest, slot_map, positions)
+            buf = torch.empty(4 * B + 4 + 2 * capacity, dtype=I32, device=block_table.device)
+        out = BlockStep._make(buf.unsafe_split_with_sizes((B, B, 2, B + 1, B + 1, capacity, capacity)))
         at = buf.data_ptr()
-        small = at + 4 * (2 * capacity + pad)
-        results = (small, small + 4 * B, small + 8 * B, small + 8 * B + 8, small + 12 * B + 12, at,
-                   at + 4 * (capacity + pad))
+        slots = at + 16 * B + 16
+        results = (at, at + 4 * B, at + 8 * B, at + 8 * B + 8, at + 12 * B + 12, slots, slots + 4 * capacity)
     else:
         results = [_at(t, n, f"out.{what}", I32, dev)
                    for t, n, what in zip(out, (B, B, 2, B + 1, B + 1, capacity, capacity), BlockStep._fields)]

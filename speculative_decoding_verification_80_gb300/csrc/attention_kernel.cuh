@@ -73,9 +73,9 @@ constexpr int kTile = 128;      // positions of a tile
 constexpr int kAttnRows = 64;   // most rows of a tile
 constexpr int kGroupRows = 16;  // of a softmax group
 constexpr int kGroups = 4;
-// Warps: 0-15 softmax, 16-23 V to f16 (four a half of D), 24-27 Q and O, 28 copies of
-// K, 29 first products, 30 second products and the list of segments, 31 copies
-// of V.
+// Warps: 0-15 softmax (and what the CTA has to join), 16-23 V to f16 (four a
+// half of D), 24-27 Q and O, 28 copies of K, 29 first products, 30 second
+// products and the list of segments, 31 copies of V.
 constexpr int kValueWarp = 16, kOutputWarp = 24, kCopyWarp = 28;
 constexpr int kAttnThreads = 32 * 32;
 // Registers a thread: 64 at launch, moved to where they are needed.
@@ -238,10 +238,16 @@ struct alignas(16) RowOut {
   float sum, ref;
 };
 
+// An item whose last part this CTA has finished.
+struct Join {
+  uint32_t cta0;  // of the first part
+  int32_t pieces, row0, rows, q0, h;
+};
+
 struct AttnShared {
   uint64_t k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
   uint64_t s_full[4], s_empty[4], p_full[4], pv_done[4], f_full[2], f_empty[2], o_full[2], o_empty[2];
-  uint64_t q_full, q_empty, meta_full[2], l_full[2];
+  uint64_t q_full, q_empty, meta_full[2], l_full[2], out_done;
   uint64_t sc_full[kScaleRing], sc_empty[kScaleRing], seg_full[kSegRing], seg_empty[kSegRing], done[2];
   uint32_t tmem;
   int32_t b0;
@@ -259,7 +265,8 @@ struct AttnShared {
   RowOut out[kAttnRows];
   int32_t nanpos[2][128];              // first new position whose value is NaN in a dimension
   ScaleEntry scales[kScaleRing];
-  int32_t last;
+  Join join[2];  // of the item begun before this CTA's part, and of its last
+  int32_t joins;
 };
 
 __device__ __forceinline__ void named_barrier(int id, int threads) {
@@ -295,7 +302,7 @@ struct Waiter {
     const uint32_t since = clock();
 #pragma unroll 1
     while (!ptx::mbar_try_wait(at, parity)) {
-      __nanosleep(lazy ? 500 : 32);
+      __nanosleep(lazy ? 200 : 32);
       if (static_cast<uint32_t>(clock()) - since > SPECDEC_ATTN_WAIT_CYCLES) {
         dead = true;
         break;
@@ -402,6 +409,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       init(sh.sc_empty[i], 4);
     }
     init(sh.q_full, 4);
+    init(sh.out_done, 4);
     init(sh.q_empty, 1);
     init(sh.done[0], 1);
     init(sh.done[1], 1);
@@ -412,6 +420,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     ptx::fence_mbarrier_init();
     sh.b0 = 0;
     sh.ub0 = 0;
+    sh.joins = 0;
   }
   if (warp == kCopyWarp) tc::alloc(ptx::smem_addr(&sh.tmem), kTmemCols);
 
@@ -645,6 +654,50 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (t_in == 0) sh.vref[par][grp] = vref / kPScale;
       warp_arrive(sh.l_full[par]);
       leave(n_seg);
+    }
+    // The items that this CTA has finished: their parts are added up in their
+    // order, a warp for 64 dimensions of a row.
+    if (leader) wait(sh.out_done, 0);
+    named_barrier(1 + grp, 128);
+    const int joins = sh.joins;
+#pragma unroll 1
+    for (int i = 0; i < joins; ++i) {
+      const Join& J = sh.join[i];
+      auto record = [&](int p) {
+        return a.partial + static_cast<size_t>((J.cta0 + p) * 2 + (p == 0 ? 1 : 0)) * kPartialFloats;
+      };
+#pragma unroll 1
+      for (int task = warp; task < J.rows * (D / 64); task += kValueWarp) {
+        const int r = task / (D / 64), x = task % (D / 64) * 64 + lane * 2;
+        float M = -INFINITY, sum = 0.f, acc[2] = {0.f, 0.f};
+#pragma unroll 1
+        for (int p0 = 0; p0 < J.pieces; p0 += 32) {
+          // a lane for each piece: its reference and sum
+          const float* q = record(min(p0 + lane, J.pieces - 1)) + kAttnRows * 128 + r;
+          const float m = __ldcg(q), n = p0 + lane < J.pieces ? __ldcg(q + kAttnRows) : 0.f;
+          const float M_new = fmaxf(M, tc::warp_max(n != 0.f ? m : -INFINITY));
+          const float f = M > -INFINITY ? tc::ex2(M - M_new) : 0.f, w = n != 0.f ? tc::ex2(m - M_new) : 0.f;
+          M = M_new;
+          float part = n != 0.f ? w * n : 0.f;
+#pragma unroll
+          for (int s = 16; s > 0; s >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, s);
+          sum = fmaf(sum, f, part);
+          acc[0] *= f;
+          acc[1] *= f;
+          const int here = min(32, J.pieces - p0);
+#pragma unroll 8
+          for (int p = 0; p < here; ++p) {
+            const float wp = __shfl_sync(0xFFFFFFFFu, w, p);
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(record(p0 + p) + r * D + x));
+            acc[0] = fmaf(wp, y.x, acc[0]);
+            acc[1] = fmaf(wp, y.y, acc[1]);
+          }
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int row = J.row0 + r, tok = row / G;
+        *reinterpret_cast<__nv_bfloat162*>(a.out + (static_cast<long long>(J.q0 + tok) * a.Hq + J.h * G + row - tok * G) * D + x) =
+            __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
+      }
     }
   } else if (warp < kOutputWarp) {
     // ------------------------------------------------------------ V to f16
@@ -898,90 +951,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         named_barrier(5, 128);
         if (ot == 0) {
           __threadfence();
-          sh.last = ptx::atom_add_acq_rel(a.counters + home, 1u) == c1 - c0;
-        }
-        named_barrier(5, 128);
-        if (sh.last) {
-          const int pieces = static_cast<int>(c1 - c0) + 1;
-          auto record = [&](int p) {
-            return a.partial + static_cast<size_t>((c0 + p) * 2 + (p == 0 ? 1 : 0)) * kPartialFloats;
-          };
-          constexpr int E = D / 32;  // a lane's values
-#pragma unroll 1
-          for (int r4 = 0; r4 < seg.rows; r4 += 8) {
-            // rows r4 + ow and r4 + ow + 4 at once
-            float M[2], sum[2], acc[2][E];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              M[j] = -INFINITY;
-              sum[j] = 0.f;
-#pragma unroll
-              for (int i = 0; i < E; ++i) acc[j][i] = 0.f;
-            }
-#pragma unroll 1
-            for (int p0 = 0; p0 < pieces; p0 += 32) {
-              // a lane for each piece: its references and sums
-              float m[2], n[2], w[2];
-              const float* q = record(min(p0 + lane, pieces - 1)) + kAttnRows * 128 + r4 + ow;
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const bool in = p0 + lane < pieces && r4 + ow + 4 * j < seg.rows;
-                m[j] = in ? __ldcg(q + 4 * j) : 0.f;
-                n[j] = in ? __ldcg(q + kAttnRows + 4 * j) : 0.f;
-              }
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const float M_new = fmaxf(M[j], tc::warp_max(n[j] != 0.f ? m[j] : -INFINITY));
-                const float f = M[j] > -INFINITY ? tc::ex2(M[j] - M_new) : 0.f;
-                w[j] = n[j] != 0.f ? tc::ex2(m[j] - M_new) : 0.f;
-                M[j] = M_new;
-                float part = w[j] * n[j];
-#pragma unroll
-                for (int s = 16; s > 0; s >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, s);
-                sum[j] = fmaf(sum[j], f, part);
-#pragma unroll
-                for (int i = 0; i < E; ++i) acc[j][i] *= f;
-              }
-              const int here = min(32, pieces - p0);
-#pragma unroll 4
-              for (int p = 0; p < here; ++p) {
-                const float* y = record(p0 + p) + (r4 + ow) * D + lane * E;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  const float wp = __shfl_sync(0xFFFFFFFFu, w[j], p);
-                  float v[E];  // (rows past the last are there, and not written)
-                  if constexpr (D == 128) {
-                    const float4 z = __ldcg(reinterpret_cast<const float4*>(y + 4 * j * D));
-                    v[0] = z.x, v[1] = z.y, v[2] = z.z, v[3] = z.w;
-                  } else {
-                    const float2 z = __ldcg(reinterpret_cast<const float2*>(y + 4 * j * D));
-                    v[0] = z.x, v[1] = z.y;
-                  }
-#pragma unroll
-                  for (int i = 0; i < E; ++i) acc[j][i] = fmaf(wp, v[i], acc[j][i]);
-                }
-              }
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int r = r4 + ow + 4 * j;
-              if (r >= seg.rows) break;
-              const float inv = sum[j] == 0.f ? 0.f : 1.f / sum[j];
-              uint32_t* to = reinterpret_cast<uint32_t*>(dst + sh.out[r].at + lane * E);
-#pragma unroll
-              for (int i = 0; i < E; i += 2) {
-                const __nv_bfloat162 y = __floats2bfloat162_rn(acc[j][i] * inv, acc[j][i + 1] * inv);
-                to[i / 2] = *reinterpret_cast<const uint32_t*>(&y);
-              }
-            }
+          if (ptx::atom_add_acq_rel(a.counters + home, 1u) == c1 - c0) {
+            ptx::st_relaxed_u32(a.counters + home, 0u);
+            sh.join[sh.joins++] = Join{c0, static_cast<int>(c1 - c0) + 1, seg.row0, seg.rows, seg.q0, seg.h};
           }
-          if (ot == 0) ptx::st_relaxed_u32(a.counters + home, 0u);
         }
       }
       leave(n_seg);
       if (!more) break;
       seg = *nxt;
     }
+    warp_arrive(sh.out_done);
   } else {
     tc::fewer_registers<kRegsRest>();
     if (warp == kCopyWarp || warp == kCopyWarp + 3) {

@@ -787,6 +787,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                                       half * (D / 2));
 #pragma unroll
       for (int i = 0; i < kVec; ++i) qv[i] = __ldg(p + i);
+    };
+    auto convert_q = [&](const Segment& s) {
       // the largest magnitude's bits (bf16 in both halves; no number is above infinity)
       uint32_t top = 0;
 #pragma unroll
@@ -838,22 +840,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       warp_arrive(sh.meta_full[par]);
     };
     wait.lazy = true;
-    Segment seg;
+    // Q is asked for two segments ahead and made one ahead, before this one's O.
+    const Segment* next = segment(0);
+    bool more = !named_any(5, 128, next == nullptr);
+    if (more) load_q(*next);
+    const Segment* at_seg = nullptr;
     for (int n_seg = -1;; ++n_seg) {
-      // the next segment's Q, where there is one, before this one's O
       const int par = n_seg & 1;
-      const Segment* nxt = segment(n_seg + 1);
-      const bool more = !named_any(5, 128, nxt == nullptr);
+      const Segment* after = nullptr;
+      bool more_after = false;
       if (more) {
-        load_q(*nxt);
+        convert_q(*next);
         if (n_seg >= 0) wait(sh.q_empty, n_seg & 1);
-        store_q(*nxt, par ^ 1);
+        store_q(*next, par ^ 1);
+        after = segment(n_seg + 2);
+        more_after = !named_any(5, 128, after == nullptr);
+        if (more_after) load_q(*after);
       }
       if (n_seg < 0) {
         if (!more) break;
-        seg = *nxt;
+        at_seg = next;
+        next = after;
+        more = more_after;
         continue;
       }
+      const Segment& seg = *at_seg;
       wait(sh.l_full[par], (n_seg >> 1) & 1);
       const int by_tile = 1 << seg.by_log2, o_cols = seg.o_cols();
       const bool whole = seg.tile0 == 0 && seg.tile1 == seg.tiles;
@@ -959,7 +970,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       leave(n_seg);
       if (!more) break;
-      seg = *nxt;
+      at_seg = next;
+      next = after;
+      more = more_after;
     }
     warp_arrive(sh.out_done);
   } else {

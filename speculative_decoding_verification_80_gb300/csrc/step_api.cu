@@ -272,10 +272,11 @@ extern "C" specdec_status_t kv_append(const void* k, const void* v, specdec_dtyp
   a.H = H;
   a.bs = block_size;
   a.num_blocks = num_blocks;
-  // A team holds a block's rows: 16 loads of 16 bytes a thread.
+  // A team holds a block's rows: 8 loads of 16 bytes a thread, or 16.
   const int64_t loads = static_cast<int64_t>(block_size) * D * elt / 16;
+  const int vecs = loads <= 8 * kAppendThreads ? 8 : 16;
   a.team = 32;
-  while (a.team * kAppendVecs < loads) a.team *= 2;
+  while (a.team * vecs < loads) a.team *= 2;
   a.pairs = kAppendThreads / 32 < 2 * H ? kAppendThreads / 32 : 2 * H;
   const unsigned splits = static_cast<unsigned>((2 * H + a.pairs - 1) / a.pairs);
   // Windows of a block's tokens, or fewer while that leaves SMs without work.
@@ -287,14 +288,16 @@ extern "C" specdec_status_t kv_append(const void* k, const void* v, specdec_dtyp
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == SPECDEC_F32) {
     if (D == 64)
-      append_kernel<float, 64><<<grid, kAppendThreads, 0, st>>>(a);
+      append_kernel<float, 64, 8><<<grid, kAppendThreads, 0, st>>>(a);
+    else if (vecs == 8)
+      append_kernel<float, 128, 8><<<grid, kAppendThreads, 0, st>>>(a);
     else
-      append_kernel<float, 128><<<grid, kAppendThreads, 0, st>>>(a);
+      append_kernel<float, 128, 16><<<grid, kAppendThreads, 0, st>>>(a);
   } else {
     if (D == 64)
-      append_kernel<__nv_bfloat16, 64><<<grid, kAppendThreads, 0, st>>>(a);
+      append_kernel<__nv_bfloat16, 64, 8><<<grid, kAppendThreads, 0, st>>>(a);
     else
-      append_kernel<__nv_bfloat16, 128><<<grid, kAppendThreads, 0, st>>>(a);
+      append_kernel<__nv_bfloat16, 128, 8><<<grid, kAppendThreads, 0, st>>>(a);
   }
   return launched();
 }

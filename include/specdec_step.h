@@ -132,10 +132,17 @@ specdec_status_t kv_append(const void* k, const void* v, specdec_dtype_t dtype, 
  *   scale        factor of the scores; 0 selects 1 / sqrt(D).
  *   workspace    SPECDEC_ATTENTION_WORKSPACE_BYTES, zero-filled once before
  *                its first use; every call leaves it ready for the next.  One
- *                workspace serves one call in flight at a time.
+ *                workspace serves one call in flight at a time.  Its first
+ *                word is the device error word (specdec_get_error reads it):
+ *                after SPECDEC_DEV_ERR_TIMEOUT the call's outputs have no
+ *                meaning and the workspace has to be zero-filled again.
  * Scores, their maxima and sums and the output's sums are held in 32 bits;
- * probabilities enter the second product with 8 significant bits, relative to
- * the largest of 128 neighbouring positions.
+ * keys and values are taken as they are in the cache, queries to 2^-18 of a
+ * row's largest.  Probabilities enter the second product in f16, 64 times
+ * their size over a reference (a score that later ones pass by 2^9 at most):
+ * 11 significant bits down to 2^-20 of it, nothing below 2^-31.
+ * SPECDEC_ERR_UNSUPPORTED also where the tiles of 128 positions, over heads
+ * and groups of 64 rows, could pass some 400 million.
  */
 #define SPECDEC_ATTENTION_WORKSPACE_BYTES (64u << 20)
 specdec_status_t spec_attention(const void* q, int64_t q_token_stride, int32_t T, int32_t Hq, int32_t H, int32_t D,
@@ -163,6 +170,7 @@ specdec_status_t spec_attention(const void* q, int64_t q_token_stride, int32_t T
  *   mask          [mask_count, ceil(V / 32)] words: bit v % 32 of word v / 32
  *                 allows token v.  mask_rows [B, n_max+1] names each row's
  *                 mask, -1 for none.  NULL: none.
+ * history_stride stays below 2^29.
  * For token v of row j, with c = times it was made (drafts before j among
  * them), in 32 bits and rounded once:
  *   l = logit; made or in the prompt: l > 0 ? l / repetition : l * repetition;

@@ -57,7 +57,8 @@ cudaError_t launch_logits(LogitArgs a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     ready[dev] = true;
   }
-  // Few requests are cut finer, until every SM has work.
+  // Few requests are cut finer, until every SM has two items.  (Eight would
+  // double the history's reading: 64 requests take 50 us instead of 35.)
   a.share = kLogitRowBytes / kElt;
   while (a.share * kElt > kLogitLeastBytes && static_cast<int64_t>(a.B) * ((a.V + a.share - 1) / a.share) < 2 * sms) a.share /= 2;
   a.chunks = (a.V + a.share - 1) / a.share;
@@ -134,7 +135,9 @@ extern "C" specdec_status_t spec_process_logits(
     const uint32_t* mask, int32_t mask_count, const int32_t* mask_rows, uint32_t* error_word, void* stream) {
   if (dtype != SPECDEC_F32 && dtype != SPECDEC_BF16) return SPECDEC_ERR_INVALID_ARG;
   if (B < 0 || n_max < 0 || V <= 0 || history_stride < 0 || num_bias < 0 || mask_count < 0) return SPECDEC_ERR_INVALID_ARG;
-  if (V > SPECDEC_MAX_VOCAB || n_max > SPECDEC_MAX_DRAFT || B > SPECDEC_MAX_BATCH) return SPECDEC_ERR_UNSUPPORTED;
+  if (V > SPECDEC_MAX_VOCAB || n_max > SPECDEC_MAX_DRAFT || B > SPECDEC_MAX_BATCH ||
+      history_stride > static_cast<int32_t>(kCountMask))
+    return SPECDEC_ERR_UNSUPPORTED;
   if (B == 0) return SPECDEC_OK;
   if (logits == nullptr || out == nullptr) return SPECDEC_ERR_INVALID_ARG;
   const uintptr_t elt = dtype == SPECDEC_F32 ? 4 : 2;

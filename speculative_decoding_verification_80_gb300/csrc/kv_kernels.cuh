@@ -361,29 +361,20 @@ __device__ __forceinline__ void unpack16<__nv_bfloat16>(const uint4& q, float* f
   }
 }
 
-// Bits (as a float) of the largest finite magnitude of 16 bytes.
+// The largest magnitude of 16 bytes and `top`, in bits: for bf16 one in each
+// half.  No number is above infinity.
 template <typename Elt>
-__device__ __forceinline__ uint32_t finite_top(const uint4& q);
-template <>
-__device__ __forceinline__ uint32_t finite_top<float>(const uint4& q) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t u = w[i] & 0x7FFFFFFFu;
-    top = max(top, u < 0x7F800000u ? u : 0);
-  }
-  return top;
+__device__ __forceinline__ uint32_t max_bits(uint32_t top, const uint4& q) {
+  if (sizeof(Elt) == 4)
+    return max(max(top, q.x & 0x7FFFFFFFu), max(q.y & 0x7FFFFFFFu, max(q.z & 0x7FFFFFFFu, q.w & 0x7FFFFFFFu)));
+  return __vmaxu2(__vmaxu2(top, q.x & 0x7FFF7FFFu), __vmaxu2(q.y & 0x7FFF7FFFu, __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu)));
 }
-template <>
-__device__ __forceinline__ uint32_t finite_top<__nv_bfloat16>(const uint4& q) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = w[i] << 16 & 0x7FFF0000u, hi = w[i] & 0x7FFF0000u;
-    top = max(top, max(lo < 0x7F800000u ? lo : 0, hi < 0x7F800000u ? hi : 0));
-  }
+// The largest finite one, as a float's bits.
+template <typename Elt>
+__device__ __forceinline__ uint32_t finite_max_bits(uint32_t top, const uint4& q) {
+  float f[16 / sizeof(Elt)];
+  unpack16<Elt>(q, f);
+  for (float x : f) top = max(top, fabsf(x) < INFINITY ? __float_as_uint(fabsf(x)) : 0);
   return top;
 }
 
@@ -392,13 +383,16 @@ __device__ __forceinline__ uint32_t finite_top<__nv_bfloat16>(const uint4& q) {
 // the rows are read once and all at a time.  A CTA has the runs that start in
 // its window of tokens; its teams go through their pairs of a run and a head,
 // and runs that a warp holds are a warp's.  Bound by the rows read and the codes
-// written: on 50 000 bf16 tokens of 8 heads of 128 in blocks of 64, 71 us (308
-// MB, 4.3 TB/s) with 8 loads a thread, 83 us with 16 (two CTAs an SM instead
-// of three).  16 is for blocks of 64 KB, which 8 would not hold.
+// written, as long as few instructions are spent on a value: on 50 000 bf16
+// tokens of 8 heads of 128 in blocks of 64 (308 MB) 54 us, 5.7 TB/s, with 8
+// loads a thread and four CTAs an SM; 60 with three; 83 with 16 loads and two,
+// which is left for blocks of 64 KB.  Asking for the next pair's rows before
+// this one's codes are made costs a CTA, and 14 us.
 template <typename Elt, int D, int kVecs>
-__global__ void __launch_bounds__(kAppendThreads, kVecs <= 8 ? 3 : 2) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, kVecs <= 8 ? 4 : 2) append_kernel(const AppendArgs a) {
   constexpr int E = 16 / sizeof(Elt);  // values of a 16-byte load
   constexpr int VR = D / E;            // loads of a row
+  static_assert(32 % VR == 0, "a warp's threads hold whole rows");
   constexpr int kSpan = 2 * kMaxBlockSize;
   __shared__ int32_t slots[kSpan + 1];
   __shared__ uint32_t breaks[kSpan / 32 + 1];  // tokens that do not go on in the run before them
@@ -456,20 +450,34 @@ __global__ void __launch_bounds__(kAppendThreads, kVecs <= 8 ? 3 : 2) append_ker
       float* sp = (which ? a.scale[1] : a.scale[0]) + static_cast<long long>(block) * a.H + h;
       uint8_t* tile = (which ? a.cache[1] : a.cache[0]) + (static_cast<long long>(block) * a.H + h) * a.bs * D;
       const float old = off > 0 ? *sp : 0.f;
+      // (a team's threads hold whole rows: a thread's loads are as far from
+      // their rows' starts)
+      const char* from = row + (k0 / VR) * stride + (k0 % VR) * 16;
+      const long long step = width / VR * stride;
       uint4 x[kVecs];
 #pragma unroll
-      for (int v = 0; v < kVecs; ++v) {
-        const int k = k0 + v * width;
-        x[v] = k < n * VR ? __ldg(reinterpret_cast<const uint4*>(row + (k / VR) * stride) + k % VR) : make_uint4(0, 0, 0, 0);
-      }
-      uint32_t top = 0;  // the largest finite magnitude's bits
+      for (int v = 0; v < kVecs; ++v, from += step)
+        x[v] = k0 + v * width < n * VR ? __ldg(reinterpret_cast<const uint4*>(from)) : make_uint4(0, 0, 0, 0);
+      uint32_t top = 0;
+      auto team_max = [&]() {
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        if (width > 32) {
+          if (lane == 0) red[tid >> 5] = top;
+          team_barrier();
+          top = __reduce_max_sync(0xFFFFFFFFu, lane < width / 32 ? red[team * (width / 32) + lane] : 0);
+        }
+      };
 #pragma unroll
-      for (int v = 0; v < kVecs; ++v) top = max(top, finite_top<Elt>(x[v]));
-      top = __reduce_max_sync(0xFFFFFFFFu, top);
-      if (width > 32) {
-        if (lane == 0) red[tid >> 5] = top;
+      for (int v = 0; v < kVecs; ++v) top = max_bits<Elt>(top, x[v]);
+      if (sizeof(Elt) == 2) top = max(top << 16, top & 0xFFFF0000u);
+      team_max();
+      if (top >= 0x7F800000u) {  // infinities and NaN do not count
         team_barrier();
-        top = __reduce_max_sync(0xFFFFFFFFu, lane < width / 32 ? red[team * (width / 32) + lane] : 0);
+        top = 0;
+#pragma unroll 1
+        for (int k = k0; k < n * VR; k += width)
+          top = finite_max_bits<Elt>(top, __ldg(reinterpret_cast<const uint4*>(row + (k / VR) * stride) + k % VR));
+        team_max();
       }
       const float amax = __uint_as_float(top);
       const float now = fmaxf(pow2_scale(amax), pow2_ceil(old));
@@ -488,11 +496,10 @@ __global__ void __launch_bounds__(kAppendThreads, kVecs <= 8 ? 3 : 2) append_ker
           *c = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      uint8_t* to = tile + off * D;
+      uint8_t* to = tile + off * D + k0 * E;
 #pragma unroll
-      for (int v = 0; v < kVecs; ++v) {
-        const int k = k0 + v * width;
-        if (k >= n * VR) continue;
+      for (int v = 0; v < kVecs; ++v, to += width * E) {
+        if (k0 + v * width >= n * VR) break;
         float f[E];
         unpack16<Elt>(x[v], f);
         uint32_t w[E / 4];
@@ -500,9 +507,9 @@ __global__ void __launch_bounds__(kAppendThreads, kVecs <= 8 ? 3 : 2) append_ker
         for (int e = 0; e < E / 4; ++e)
           w[e] = e4m3_pair(f[4 * e] * inv, f[4 * e + 1] * inv) | (e4m3_pair(f[4 * e + 2] * inv, f[4 * e + 3] * inv) << 16);
         if (E == 8)
-          reinterpret_cast<uint2*>(to)[k] = make_uint2(w[0], w[E / 4 - 1]);
+          *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[E / 4 - 1]);
         else
-          reinterpret_cast<uint32_t*>(to)[k] = w[0];
+          *reinterpret_cast<uint32_t*>(to) = w[0];
       }
       team_barrier();  // everyone has read the old scale, and `red`
       if (k0 == 0) *sp = now;

@@ -643,3 +643,89 @@ def test_process_logits_feeds_the_verify_step():
     assert acc.tolist() == wrong.tolist()
     for b in range(B):
         assert out[b, :wrong[b] + 1].tolist() == path[b, :wrong[b] + 1].tolist()
+
+
+# ------------------------------------------- where the kernels' parts meet
+
+@pytest.mark.parametrize("B,capacity", [(8192, 20000), (8193, 20000), (3000, 3)])
+@pytest.mark.parametrize("alias", [False, True])
+def test_block_step_many_requests(B, capacity, alias):
+    rng = np.random.default_rng(B)
+    c = _block_case(rng, B, 16, 3, spare=B // 2, most_new=5)
+    _check_blocks(c, 16, capacity, alias=alias)
+
+
+def test_block_step_positions_at_any_alignment():
+    rng = np.random.default_rng(2)
+    for capacity in (1, 2, 3, 5, 31, 33):
+        c = _block_case(rng, 9, 16, 4, spare=30, most_new=4)
+        _check_blocks(c, 16, capacity)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_long_runs_with_infinities_and_nan(D, dtype):
+    # whole blocks of 128: a team's runs, and the longest a block can have
+    rng = np.random.default_rng(D)
+    H, bs, N = 3, 128, 7
+    kc, ks = _cache(rng, N, H, bs, D)
+    vc, vs = _cache(rng, N, H, bs, D)
+    slots = np.concatenate([np.arange(2 * bs, 3 * bs), np.arange(5 * bs + 1, 6 * bs), np.arange(60), 3 * bs + np.arange(90, 128)])
+    x = torch.randn(len(slots), 2 * H, D, generator=torch.Generator(device="cuda").manual_seed(D), device="cuda").to(dtype)
+    x[17, 0, 5] = float("inf")
+    x[150, 1, 9] = -float("inf")
+    x[150, 1, 10] = float("nan")
+    x[270, 4, 0] = float("nan")
+    _check_append(x[:, :H], x[:, H:], slots, kc, vc, ks, vs)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("a,b,w", [(0, 0, 1), (1, 1, 2), (3, 3, 3), (1, 2, 0), (5, 0, 1)])
+def test_process_logits_at_any_alignment(a, b, w, dtype):
+    # logits, out and masks that start a, b and w elements past 16 bytes; rows of an odd length
+    rng = np.random.default_rng(10 * a + b)
+    B, n, V = 3, 2, 9001
+    c = _logit_case(rng, B, n, V, 200)
+    x = torch.tensor(rng.normal(0, 3, (B, n + 1, V))).to(dtype).cuda()
+    at = lambda t, k: torch.cat([t.new_full((k,), 9), t.flatten(), t.new_full((3,), 9)])[k:k + t.numel()].view(t.shape)  # noqa: E731
+    args = {k: dev(v) for k, v in c.items()}
+    args["mask"] = at(args["mask"], w)
+    src, out = at(x, a), at(torch.full_like(x, 77.0), b)
+    assert src.data_ptr() % 16 == a * x.element_size() % 16 and out.data_ptr() % 16 == b * x.element_size() % 16
+    sd.spec_process_logits(src, out=out, **args)
+    wait_gpu()
+    _check_logits(x, c, out, 77.0)
+    sd.spec_process_logits(src, **args)
+    wait_gpu()
+    _check_logits(x, c, src, x.double().cpu().numpy())
+    # nothing around the tensors has changed
+    for t, k in ((src, a), (out, b)):
+        whole = t.as_strided((k + t.numel() + 3,), (1,), 0)
+        assert (whole[:k] == 9).all() and (whole[-3:] == 9).all()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_process_logits_many_items_and_the_most_rows(in_place):
+    # more items than two for each SM, requests with 1 to 65 rows, some rows without a mask
+    rng = np.random.default_rng(31)
+    for B, n, V in ((700, 1, 700), (40, 64, 600), (160, 3, 17000)):
+        c = _logit_case(rng, B, n, V, 60, biases=4)
+        x = torch.tensor(rng.normal(0, 3, (B, n + 1, V))).to(torch.bfloat16).cuda()
+        _check_logits(x, c, _run_logits(x, c, in_place=in_place), x.double().cpu().numpy() if in_place else 77.0)
+
+
+def test_process_logits_more_biases_than_an_item_lists():
+    rng = np.random.default_rng(32)
+    B, n, V = 4, 1, 300
+    c = _logit_case(rng, B, n, V, 30, biases=900)
+    x = torch.tensor(rng.normal(0, 3, (B, n + 1, V))).to(torch.float32).cuda()
+    # (its biases meet in one value: as many additions as there are)
+    want, mag = ref.process_logits(x.double().cpu().numpy(), **c)
+    got = _run_logits(x, c).double().cpu().numpy()
+    most = int(np.diff(c["bias_offsets"]).max())
+    for b in range(B):
+        rows = c["draft_len"][b] + 1
+        w, g, m = want[b, :rows], got[b, :rows], mag[b, :rows]
+        inf = np.isinf(w)
+        assert (g[inf] == w[inf]).all()
+        assert (np.abs(g[~inf] - w[~inf]) <= (12 + most) * 2.0 ** -24 * m[~inf]).all()

@@ -19,8 +19,8 @@
 // they lie.  Bound by the rows' bytes, read and written once.  (With an item's
 // steps one after the other, the copies' and the history's latencies took twice
 // the time, however many CTAs an SM had.)  Measured: 64 requests of up to 5
-// rows of 128256 bf16 (132 MB) 33 us, 4.0 TB/s; 256 of up to 8 rows of 152064
-// (980 MB) 200 us, 4.9 TB/s, of which the copies alone are 178 us.  Rows of 8
+// rows of 128256 bf16 (132 MB) 34 us, 3.8 TB/s; 256 of up to 8 rows of 152064
+// (980 MB) 200 us, 4.9 TB/s, of which the copies alone are 166 us.  Rows of 8
 // KB in a ring of 12 take 53 and 309 us, and equal parts of all rows in their
 // order, one for each CTA, 39 and 257 us: CTAs that work side by side on one
 // request's rows keep what they read close together.
@@ -67,7 +67,7 @@ struct LogitArgs {
   int32_t mask_count, mask_words;
   const int32_t* mask_rows;
   uint32_t* err;
-  int32_t share;       // vocabulary entries of an item, a multiple of 32
+  int32_t share;       // vocabulary entries of an item, a multiple of 128 (a mask of them is whole 16 bytes)
   int32_t chunks;      // items of a request
   int32_t same_phase;  // logits and out are alike modulo 16 bytes
 };

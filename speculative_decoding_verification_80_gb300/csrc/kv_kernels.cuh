@@ -15,7 +15,7 @@ namespace specdec {
 // and few dependent loads.  Each CTA makes the whole plan for itself, in shared
 // memory, and writes its share of the tokens: a thread four neighbouring ones,
 // whose request it finds by bisection.  Measured on the device: 12 us for 1024
-// requests of 5600 tokens in all, 8 us for 512 prompts of 640 000 (5 MB), 36 us
+// requests of 5600 tokens in all, 9 us for 512 prompts of 640 000 (5 MB), 36 us
 // with 8 CTAs in a cluster, which would let the outputs be the inputs' arrays.
 struct BlockArgs {
   int32_t B, bs, max_blocks, num_blocks, capacity;

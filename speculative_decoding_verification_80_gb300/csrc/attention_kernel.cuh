@@ -74,8 +74,8 @@ struct AttnArgs {
   uint32_t* err;
   uint32_t* counters;  // one for each CTA, zero between calls
   float* partial;      // two records for each CTA
-  int32_t ring;        // tiles of K, and of V, in shared memory
-  int32_t rows;        // most rows of a tile, a multiple of 16
+  int32_t k_ring, v_ring;  // tiles of K and of V in shared memory
+  int32_t rows;        // most rows of a tile: 16, 32 or 64
 };
 
 constexpr int kTile = 128;      // positions of a tile
@@ -373,8 +373,8 @@ struct AttnLayout {
   // of all buffers: four of up to 32 rows or two of 64
   static __host__ __device__ int p_bytes(int rows) { return (rows <= 32 ? 4 * rows : 2 * rows) * kTile * 2; }
   static __host__ __device__ int tiles_at() { return (static_cast<int>(sizeof(AttnShared)) + 1023) / 1024 * 1024; }
-  static __host__ __device__ int bytes(int ring, int rows) {
-    return 1024 + tiles_at() + 2 * ring * kTileBytes + 2 * kHalfBytes + 2 * q_bytes(rows) + p_bytes(rows);
+  static __host__ __device__ int bytes(int tiles, int rows) {
+    return tiles_at() + tiles * kTileBytes + 2 * kHalfBytes + 2 * q_bytes(rows) + p_bytes(rows);
   }
 };
 
@@ -382,12 +382,13 @@ template <int D>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using L = AttnLayout<D>;
-  extern __shared__ __align__(16) unsigned char raw[];
-  unsigned char* base = raw + ((1024u - (ptx::smem_addr(raw) & 1023u)) & 1023u);
+  // (The kernel has no other shared memory, so this begins where an SM's does,
+  // past the 1 KB that the system keeps.)
+  extern __shared__ __align__(1024) unsigned char base[];
   AttnShared& sh = *reinterpret_cast<AttnShared*>(base);
   unsigned char* k_tiles = base + L::tiles_at();
-  unsigned char* v_tiles = k_tiles + a.ring * L::kTileBytes;
-  unsigned char* v_half = v_tiles + a.ring * L::kTileBytes;
+  unsigned char* v_tiles = k_tiles + a.k_ring * L::kTileBytes;
+  unsigned char* v_half = v_tiles + a.v_ring * L::kTileBytes;
   unsigned char* q_at = v_half + 2 * L::kHalfBytes;
   unsigned char* p_at = q_at + 2 * L::q_bytes(a.rows);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
   if (tid == 0) {
     auto init = [](uint64_t& bar, uint32_t n) { ptx::mbar_init(ptx::smem_addr(&bar), n); };
-    for (int i = 0; i < a.ring; ++i) {
+    for (int i = 0; i < kMaxRing; ++i) {
       init(sh.k_full[i], 1);
       init(sh.k_empty[i], 1);
       init(sh.v_full[i], 1);
@@ -755,7 +756,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (leader && k >= 2) wait(sh.f_empty[k & 1], ((k >> 1) - 1) & 1);
         named_barrier(6, 256);
         if (leader && lane == 0) ptx::mbar_arrive(ptx::smem_addr(&sh.v_empty[slot]));
-        if (++slot == a.ring) slot = 0, ++round;
+        if (++slot == a.v_ring) slot = 0, ++round;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
 #pragma unroll
@@ -1003,6 +1004,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       unsigned char* tiles = is_v ? v_tiles : k_tiles;
       uint64_t* full = is_v ? sh.v_full : sh.k_full;
       uint64_t* empty = is_v ? sh.v_empty : sh.k_empty;
+      const int ring = is_v ? a.v_ring : a.k_ring;
       const int pages_log2 = 7 - a.bs_log2, pages_per_tile = 1 << pages_log2;
       int n_seg = -1, tile = 0, tile_end = 0, seg_b = 0, seg_h = 0, seg_pages = 0;
       bool more = true;
@@ -1060,7 +1062,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               if (j < pages) tc::load_4d(dst + j * a.bs * D, map, 0, 0, now.h, ids[j], bar);
           }
           __syncwarp();
-          if (++slot == a.ring) slot = 0, ++round;
+          if (++slot == ring) slot = 0, ++round;
           if (i == 0) load_scales(nxt);  // its ids have had a tile's time
           const uint32_t sr = k % kScaleRing;
           if (k >= kScaleRing) wait(sh.sc_empty[sr], (k / kScaleRing - 1) & 1);
@@ -1077,7 +1079,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       // no copy is in flight when the CTA ends: every slot used has been filled
       Waiter drain;
-      const int used = round > 0 ? a.ring : slot;
+      const int used = round > 0 ? ring : slot;
       for (int i = 0; i < used; ++i) drain(full[i], (i < slot ? round : round - 1) & 1);
       wait.dead |= drain.dead;
     } else if (warp == kCopyWarp + 1) {
@@ -1117,7 +1119,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (i + 1 == tiles) tc::commit(ptx::smem_addr(&sh.q_empty));
           }
           __syncwarp();
-          if (++slot == a.ring) slot = 0, ++round;
+          if (++slot == a.k_ring) slot = 0, ++round;
         }
         turns.pass(tiles, buf_log2);
         leave(n_seg);

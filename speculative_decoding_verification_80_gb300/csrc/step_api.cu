@@ -115,10 +115,13 @@ cudaError_t launch_attention(AttnArgs a, const void* k_cache, const void* v_cach
     ready[dev] = true;
   }
   using L = AttnLayout<D>;
-  const int fit = (kAttnSmem - L::bytes(0, a.rows)) / (2 * L::kTileBytes);
-  a.ring = fit < kMaxRing ? fit : kMaxRing;
+  // As many tiles as there is room for: they are what is on its way from HBM.
+  int tiles = (kAttnSmem - L::bytes(0, a.rows)) / L::kTileBytes;
+  tiles = tiles < 2 * kMaxRing ? tiles : 2 * kMaxRing;
+  a.v_ring = tiles / 2;
+  a.k_ring = tiles - a.v_ring;
   const int grid = sms < kAttnMaxCtas ? sms : kAttnMaxCtas;
-  attention_kernel<D><<<grid, kAttnThreads, L::bytes(a.ring, a.rows), st>>>(a, km, vm);
+  attention_kernel<D><<<grid, kAttnThreads, L::bytes(tiles, a.rows), st>>>(a, km, vm);
   return cudaGetLastError();
 }
 
@@ -325,11 +328,6 @@ extern "C" specdec_status_t spec_attention(const void* q, int64_t q_token_stride
     return SPECDEC_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < SPECDEC_ATTENTION_WORKSPACE_BYTES)
     return SPECDEC_ERR_WORKSPACE;
-  // The kernel counts the cost of tiles of positions, over row groups and
-  // heads, in 31 bits.
-  const int64_t groups = static_cast<int64_t>(T) * (Hq / H) / kAttnRows + (T < B ? T : B) + 1;
-  const int64_t most_cost = (static_cast<int64_t>(max_blocks) * block_size + kTile - 1) / kTile * tile_cost(kAttnRows) + kItemCost;
-  if (groups > INT32_MAX / H || groups * H > INT32_MAX / most_cost) return SPECDEC_ERR_UNSUPPORTED;
   AttnArgs a;
   memset(&a, 0, sizeof a);
   a.q = static_cast<const __nv_bfloat16*>(q);
@@ -353,10 +351,18 @@ extern "C" specdec_status_t spec_attention(const void* q, int64_t q_token_stride
   a.err = reinterpret_cast<uint32_t*>(ws);
   a.counters = reinterpret_cast<uint32_t*>(ws + 256);
   a.partial = reinterpret_cast<float*>(ws + kPartialAt);
-  // A row group is as long as the call's rows allow: fewer rows leave more
-  // shared memory to the tiles in flight.
-  const int64_t rows = static_cast<int64_t>(T) * (Hq / H);
-  a.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : kAttnRows;
+  // Rows of a group.  Few leave shared memory to the tiles on their way (8
+  // tiles of K and V of D = 128 with 16 rows, 7 with 32, 6 with 64); a request
+  // of more rows is read once for each of its groups.  How the tokens lie is
+  // known on the device only: as many for each request where that is possible,
+  // or evenly spread, with the longest near twice the mean.
+  const int64_t rows = static_cast<int64_t>(T) * (Hq / H), likely = T % B == 0 ? rows / B : 7 * rows / (4 * B);
+  a.rows = likely <= 16 ? 16 : likely <= 32 ? 32 : kAttnRows;
+  // The kernel counts the cost of tiles of positions, over row groups and
+  // heads, in 31 bits.
+  const int64_t groups = rows / a.rows + (T < B ? T : B) + 1;
+  const int64_t most_cost = (static_cast<int64_t>(max_blocks) * block_size + kTile - 1) / kTile * tile_cost(a.rows) + kItemCost;
+  if (groups > INT32_MAX / H || groups * H > INT32_MAX / most_cost) return SPECDEC_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = D == 64 ? launch_attention<64>(a, k_cache, v_cache, st) : launch_attention<128>(a, k_cache, v_cache, st);
   return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;

@@ -103,9 +103,10 @@ constexpr int kPartialFloats = kAttnRows * 128 + 2 * kAttnRows;
 // before P would leave f16.
 constexpr float kPScale = 64.f;
 constexpr float kSlack = 9.f;
-// A wait gives up after this many cycles (a second).
-#ifndef SPECDEC_ATTN_WAIT_CYCLES
-#define SPECDEC_ATTN_WAIT_CYCLES 2000000000u
+// A wait gives up after this many looks, a pause of 32 ns or more between two
+// (half a second or more).
+#ifndef SPECDEC_ATTN_WAIT_LOOKS
+#define SPECDEC_ATTN_WAIT_LOOKS (1u << 24)
 #endif
 
 // Part of a (request, head, row group) that one CTA works on.  tile1 < 0 ends
@@ -304,20 +305,22 @@ __device__ __forceinline__ bool named_any(int id, int threads, bool x) {
 // A wait that gives up once; after that the thread goes on without waiting, so
 // that every barrier still gets its arrivals, to the end of its segment.  What
 // decides how often a group of warps meets at a barrier is agreed on at one.
+// (It is in some 50 places, and the instruction cache is small: it counts looks
+// where a clock would take twice the code.)
 struct Waiter {
-  bool dead = false;
-  bool lazy = false;  // longer pauses
-  __device__ __forceinline__ void operator()(const uint64_t& bar, uint32_t parity) {
+  uint32_t looks = SPECDEC_ATTN_WAIT_LOOKS;  // 0: gave up
+  __device__ __forceinline__ bool dead() const { return looks == 0; }
+  __device__ __forceinline__ void operator()(const uint64_t& bar, uint32_t parity, uint32_t pause = 32) {
     const uint32_t at = ptx::smem_addr(&bar);
-    if (dead || ptx::mbar_try_wait(at, parity)) return;
-    const uint32_t since = clock();
+    uint32_t left = looks;
 #pragma unroll 1
     while (!ptx::mbar_try_wait(at, parity)) {
-      __nanosleep(lazy ? 200 : 32);
-      if (static_cast<uint32_t>(clock()) - since > SPECDEC_ATTN_WAIT_CYCLES) {
-        dead = true;
+      if (left == 0) {
+        looks = 0;
         break;
       }
+      --left;
+      __nanosleep(pause);
     }
   }
 };
@@ -486,9 +489,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   // The n-th segment, or null at the list's end; and the warp is done with it.
   auto segment = [&](int n) -> const Segment* {
     wait(sh.seg_full[n % kSegRing], (n / kSegRing) & 1);
-    wait.dead = __any_sync(0xFFFFFFFFu, wait.dead);
+    if (__any_sync(0xFFFFFFFFu, wait.dead())) wait.looks = 0;
     const Segment* s = &sh.seg[n % kSegRing];
-    return wait.dead || s->tile1 < 0 ? nullptr : s;
+    return wait.dead() || s->tile1 < 0 ? nullptr : s;
   };
   // bytes of a buffer of P
   auto p_stride = [&](int buf_log2) { return (buf_log2 == 2 ? min(a.rows, 32) : kAttnRows) * (kTile * 2); };
@@ -851,7 +854,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       warp_arrive(sh.q_full);
       warp_arrive(sh.meta_full[par]);
     };
-    wait.lazy = true;
     // Q is asked for two segments ahead and made one ahead, before this one's O.
     const Segment* next = segment(0);
     bool more = !named_any(5, 128, next == nullptr);
@@ -863,7 +865,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       bool more_after = false;
       if (more) {
         convert_q(*next);
-        if (n_seg >= 0) wait(sh.q_empty, n_seg & 1);
+        if (n_seg >= 0) wait(sh.q_empty, n_seg & 1, 200);
         store_q(*next, par ^ 1);
         after = segment(n_seg + 2);
         more_after = !named_any(5, 128, after == nullptr);
@@ -877,7 +879,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         continue;
       }
       const Segment& seg = *at_seg;
-      wait(sh.l_full[par], (n_seg >> 1) & 1);
+      wait(sh.l_full[par], (n_seg >> 1) & 1, 200);
       const int by_tile = 1 << seg.by_log2, o_cols = seg.o_cols();
       const bool whole = seg.tile0 == 0 && seg.tile1 == seg.tiles;
       if (ot < seg.rows) {
@@ -909,7 +911,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ro.ref = M;
       }
       named_barrier(5, 128);
-      wait(sh.o_full[par], (n_seg >> 1) & 1);
+      wait(sh.o_full[par], (n_seg >> 1) & 1, 200);
       tc::fence_after();
       const int nan_at = sh.nanpos[par][d];
       // a CTA's records: of an item from before, and of one that begins here
@@ -1081,7 +1083,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       Waiter drain;
       const int used = round > 0 ? ring : slot;
       for (int i = 0; i < used; ++i) drain(full[i], (i < slot ? round : round - 1) & 1);
-      wait.dead |= drain.dead;
+      if (drain.dead()) wait.looks = 0;
     } else if (warp == kCopyWarp + 1) {
       // --------------------------------------------------- first products
       const uint64_t swz = D == 128 ? tc::kSwizzle128 : tc::kSwizzle64;
@@ -1129,7 +1131,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (tc::elect()) tc::commit(ptx::smem_addr(&sh.done[0]));
       __syncwarp();
       drain(sh.done[0], 0);
-      wait.dead |= drain.dead;
+      if (drain.dead()) wait.looks = 0;
     } else {
       // -------------------------------------------------- second products
       const uint64_t vd0 = tc::smem_desc(ptx::smem_addr(v_half), kTile * 128, 1024, tc::kSwizzle128);
@@ -1184,11 +1186,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (tc::elect()) tc::commit(ptx::smem_addr(&sh.done[1]));
       __syncwarp();
       drain(sh.done[1], 0);
-      wait.dead |= drain.dead;
+      if (drain.dead()) wait.looks = 0;
     }
   }
   __syncwarp();
-  if (wait.dead) atomicOr(a.err, SPECDEC_DEV_ERR_TIMEOUT);
+  if (wait.dead()) atomicOr(a.err, SPECDEC_DEV_ERR_TIMEOUT);
   __syncthreads();
   if (warp == kCopyWarp) tc::dealloc(tmem, kTmemCols);
 }

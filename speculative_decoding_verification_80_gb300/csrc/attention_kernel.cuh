@@ -88,7 +88,7 @@ constexpr int kGroups = 4;
 constexpr int kValueWarp = 16, kOutputWarp = 24, kCopyWarp = 28;
 constexpr int kAttnThreads = 32 * 32;
 // Registers a thread: 64 at launch, moved to where they are needed.
-constexpr int kRegsSoftmax = 72, kRegsValues = 40, kRegsOutput = 80, kRegsRest = 64;
+constexpr int kRegsSoftmax = 72, kRegsValues = 48, kRegsOutput = 64, kRegsRest = 64;
 static_assert(512 * kRegsSoftmax + 256 * kRegsValues + 128 * (kRegsOutput + kRegsRest) <= 64 * kAttnThreads,
               "the warpgroups' registers are those of the launch");
 constexpr int kScaleRing = 8;
@@ -788,7 +788,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
   } else if (warp < kCopyWarp) {
     // ------------------------------------------------------------- Q and O
-    tc::more_registers<kRegsOutput>();
+    tc::fewer_registers<kRegsOutput>();
     const int ot = tid - 32 * kOutputWarp, ow = ot >> 5;
     const int d = D == 128 ? ot : 16 * ow + (lane & 15);
     const bool owns = D == 128 || lane < 16;

@@ -42,13 +42,15 @@
 // CTA that finishes last, in the order of the parts.
 //
 // Bound by the cache's bytes while a part lasts: a tile of D = 128 is 32 KB, of
-// which an SM's share of HBM brings one in 0.74 us, and takes 0.6 to 1 us.
+// which an SM's share of HBM brings one in 0.74 us, and takes 0.77 us at 16
+// rows, 0.89 at 32 and 1.27 at 64, where the softmax is next.
 // From one (request, head) to the next some 7 us pass in which the next first
 // tile's search, the last products and O's way out are only partly covered;
 // that is what keeps many short parts from HBM's rate.  Measured: 64 requests
-// of 5 tokens over 8000 positions (598 MB) 157 us, 3.8 TB/s; one of 2 over
-// 131000 (269 MB) 64 us, 4.2 TB/s; 256 of up to 8 over 4000 (1208 MB) 287 us,
-// 4.2 TB/s; one of one over 700 11 us.
+// of 5 tokens over 8000 positions (598 MB) 150 us, 4.0 TB/s; one of 2 over
+// 131000 (269 MB) 60 us, 4.4 TB/s; 256 of up to 8 over 4000 (1208 MB) 274 us,
+// 4.4 TB/s; 32 of one over 18000 (665 MB) 116 us, 5.8 TB/s; one of one over
+// 700 14 us.
 #pragma once
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -87,7 +89,8 @@ constexpr int kGroups = 4;
 // products and the list of segments, 31 copies of V.
 constexpr int kValueWarp = 16, kOutputWarp = 24, kCopyWarp = 28;
 constexpr int kAttnThreads = 32 * 32;
-// Registers a thread: 64 at launch, moved to where they are needed.
+// Registers a thread: 64 at launch, moved to where they are needed.  (40 for V
+// spill in its loop: 66 us where one long request takes 60.)
 constexpr int kRegsSoftmax = 72, kRegsValues = 48, kRegsOutput = 64, kRegsRest = 64;
 static_assert(512 * kRegsSoftmax + 256 * kRegsValues + 128 * (kRegsOutput + kRegsRest) <= 64 * kAttnThreads,
               "the warpgroups' registers are those of the launch");

@@ -147,3 +147,18 @@ def test_plain_scale_is_the_least_power_of_two():
     for amax in (1e-30, 2.0 ** -9, 1.0, 1.75, 447.9, 448.0, 448.1, 1e20):
         s = ref.pow2_scale(amax)
         assert amax <= 448 * s and amax > 448 * s / 2
+
+
+def test_step_refuses_what_its_counters_cannot_hold(lib):
+    # a history of 2^29 ids: a token's count keeps 29 bits
+    def logits(S):
+        return lib.spec_process_logits(fake, fake, 1, 2, 0, 100, fake, S, fake, fake, None, None, None, None, None, None, None,
+                                       None, 0, None, 0, None, None, None)
+
+    assert logits(1 << 29) == 2
+    # tiles of positions times heads and groups of rows: their cost keeps 31 bits
+    def attention(T, width):
+        return lib.spec_attention(fake, 8192, T, 64, 8, 128, 1, fake, fake, fake, width, 100, 16, fake, fake, fake, fake, 0.0,
+                                  fake, fake, 64 << 20, None)
+
+    assert attention(1 << 20, 1 << 26) == 2

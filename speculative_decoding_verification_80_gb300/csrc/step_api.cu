@@ -226,6 +226,8 @@ extern "C" specdec_status_t kv_block_step(int32_t B, int32_t block_size, int32_t
   a.slots_vec = aligned(slot_map, 16) ? 1 : 0;
   a.positions_vec = aligned(positions, 16) ? 1 : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // One launch spares the host the second; on the device both forms take as long
+  // (12.3 and 9.1 us for 1024 requests and 512 prompts in one, 11.1 and 9.5 in two).
   const bool apart = kv_len_out != kv_len && held_out != held && ring_state_out != ring_state;
   if (apart && B <= kBlockShared) {
     const int bytes = 4 * (B + 1) * static_cast<int>(sizeof(int32_t));
@@ -355,7 +357,9 @@ extern "C" specdec_status_t spec_attention(const void* q, int64_t q_token_stride
   // tiles of K and V of D = 128 with 16 rows, 7 with 32, 6 with 64); a request
   // of more rows is read once for each of its groups.  How the tokens lie is
   // known on the device only: as many for each request where that is possible,
-  // or evenly spread, with the longest near twice the mean.
+  // or evenly spread, with the longest near twice the mean.  (128 requests of
+  // one token over 4500: 141 us with 16 rows, 147 with 64; 256 of up to 32 rows:
+  // 285 with 32, 287 with 64.)
   const int64_t rows = static_cast<int64_t>(T) * (Hq / H), likely = T % B == 0 ? rows / B : 7 * rows / (4 * B);
   a.rows = likely <= 16 ? 16 : likely <= 32 ? 32 : kAttnRows;
   // The kernel counts the cost of tiles of positions, over row groups and

@@ -55,6 +55,7 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include "attention_cut.cuh"
 #include "kv_kernels.cuh"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
@@ -147,22 +148,6 @@ struct Turns {
     }
   }
 };
-
-// The list is cut by cost: a tile costs 4 to 6 units by its rows' 16s, and an
-// item (a row group of a head) kItemCost more, half before and half after its
-// tiles.  (Measured: 0.64, 0.72 and 0.98 us a tile of 16, 32 and 48 rows of
-// D = 128, 2 us an item.)  A cut within an item falls between tiles; one near
-// its start or end moves there.  A CTA's part is at least kLeastCost, more than
-// a tile, so that none inside an item is without a tile of it.  (An item's cost
-// of 12, 20, 32 and 44 units: 158, 160, 163 and 167 us on 64 requests, 64, 62,
-// 63 and 62 us on one long one, 296, 299, 309 and 312 us on 256.)
-constexpr int kItemCost = 12;
-constexpr int kLeastCost = 10;
-__host__ __device__ __forceinline__ uint32_t tile_cost(int rows) { return rows <= 32 ? 4 : (rows <= 48 ? 5 : 6); }
-// Tiles of an item that lie before `cost` units of it.
-__device__ __forceinline__ int tiles_before(uint32_t cost, uint32_t per_tile, int tiles) {
-  return cost <= kItemCost / 2 ? 0 : static_cast<int>(min((cost - kItemCost / 2) / per_tile, static_cast<uint32_t>(tiles)));
-}
 
 // Goes through the segments of units [u, end).
 struct Walker {
@@ -971,17 +956,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           rec[kAttnRows * 128 + kAttnRows + ot] = sh.out[ot].sum;
         }
         // the last of the item's CTAs joins the parts
-        // (the item's first and last CTA may have no tile of it)
-        uint32_t c0 = seg.first / chunk, c1 = (seg.end - 1) / chunk;
-        const uint32_t home = c0;
-        if (tiles_before((c0 + 1) * chunk - seg.first, seg.per_tile, seg.tiles) == 0) ++c0;
-        if (c1 > home && tiles_before(c1 * chunk - seg.first, seg.per_tile, seg.tiles) == seg.tiles) --c1;
+        const ItemCtas on = item_ctas(seg.first, seg.end, seg.per_tile, seg.tiles, chunk);
         named_barrier(5, 128);
         if (ot == 0) {
           __threadfence();
-          if (ptx::atom_add_acq_rel(a.counters + home, 1u) == c1 - c0) {
-            ptx::st_relaxed_u32(a.counters + home, 0u);
-            sh.join[sh.joins++] = Join{c0, static_cast<int>(c1 - c0) + 1, seg.row0, seg.rows, seg.q0, seg.h};
+          if (ptx::atom_add_acq_rel(a.counters + on.home, 1u) == on.c1 - on.c0) {
+            ptx::st_relaxed_u32(a.counters + on.home, 0u);
+            sh.join[sh.joins++] = Join{on.c0, static_cast<int>(on.c1 - on.c0) + 1, seg.row0, seg.rows, seg.q0, seg.h};
           }
         }
       }

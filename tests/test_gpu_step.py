@@ -729,3 +729,17 @@ def test_process_logits_more_biases_than_an_item_lists():
         inf = np.isinf(w)
         assert (g[inf] == w[inf]).all()
         assert (np.abs(g[~inf] - w[~inf]) <= (12 + most) * 2.0 ** -24 * m[~inf]).all()
+
+
+@pytest.mark.parametrize("new,kv,Hq,H,D", [
+    ([14], [300], 64, 8, 128), ([13], [249], 64, 8, 128), ([22], [300], 64, 8, 64), ([28], [300], 32, 8, 64),
+    ([6, 6, 8], [16, 3231, 260], 8, 1, 64)])
+def test_attention_items_that_begin_at_the_end_of_a_part(new, kv, Hq, H, D):
+    # two CTAs of an item's have no tile of it; the workspace is ready for the next call all the same
+    c = _attn_case(np.random.default_rng(len(new) + new[0]), new, kv, Hq, H, D, 16)
+    ws = sd.new_attention_workspace()
+    for _ in range(2):
+        _check_attn(c, _attn_gpu(c, workspace=ws))
+        assert not ws[:64 * 1024].any()
+    other = _attn_case(np.random.default_rng(5), [2], [20000], 8, 1, 128, 64)
+    _check_attn(other, _attn_gpu(other, workspace=ws))

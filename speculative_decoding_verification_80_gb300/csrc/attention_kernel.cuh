@@ -950,20 +950,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       tc::fence_before();
       warp_arrive(sh.o_empty[par]);
-      if (!whole) {
-        if (ot < seg.rows) {
-          rec[kAttnRows * 128 + ot] = sh.out[ot].ref;
-          rec[kAttnRows * 128 + kAttnRows + ot] = sh.out[ot].sum;
-        }
+      if (!whole && ot < seg.rows) {
+        rec[kAttnRows * 128 + ot] = sh.out[ot].ref;
+        rec[kAttnRows * 128 + kAttnRows + ot] = sh.out[ot].sum;
+      }
+      // All have read sh.out and nanpos, which the next turn writes, and written
+      // their part of the record.
+      named_barrier(5, 128);
+      if (!whole && ot == 0) {
         // the last of the item's CTAs joins the parts
         const ItemCtas on = item_ctas(seg.first, seg.end, seg.per_tile, seg.tiles, chunk);
-        named_barrier(5, 128);
-        if (ot == 0) {
-          __threadfence();
-          if (ptx::atom_add_acq_rel(a.counters + on.home, 1u) == on.c1 - on.c0) {
-            ptx::st_relaxed_u32(a.counters + on.home, 0u);
-            sh.join[sh.joins++] = Join{on.c0, static_cast<int>(on.c1 - on.c0) + 1, seg.row0, seg.rows, seg.q0, seg.h};
-          }
+        __threadfence();
+        if (ptx::atom_add_acq_rel(a.counters + on.home, 1u) == on.c1 - on.c0) {
+          ptx::st_relaxed_u32(a.counters + on.home, 0u);
+          sh.join[sh.joins++] = Join{on.c0, static_cast<int>(on.c1 - on.c0) + 1, seg.row0, seg.rows, seg.q0, seg.h};
         }
       }
       leave(n_seg);

@@ -743,3 +743,32 @@ def test_attention_items_that_begin_at_the_end_of_a_part(new, kv, Hq, H, D):
         assert not ws[:64 * 1024].any()
     other = _attn_case(np.random.default_rng(5), [2], [20000], 8, 1, 128, 64)
     _check_attn(other, _attn_gpu(other, workspace=ws))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_many_short_items_a_cta(D):
+    # items of 8 to 64 rows and one to three tiles next to one another, several whole ones a CTA: what the output
+    # warps keep of one must not meet the next
+    rng = np.random.default_rng(100 + D)
+    B, H = 170, 6
+    new = rng.integers(1, 9, B).tolist()
+    kv = rng.integers(0, 260, B).tolist()
+    c = _attn_case(rng, new, kv, 8 * H, H, D, 16)
+    ws = sd.new_attention_workspace()
+    base = _attn_gpu(c, workspace=ws)
+    _check_attn(c, base)
+    for _ in range(20):
+        assert torch.equal(_attn_gpu(c, workspace=ws), base)
+    # values of new tokens that are no numbers, in a dimension of every (request, head)
+    want = torch.zeros(base.shape, dtype=torch.bool)
+    for b in range(B):
+        for h in range(H):
+            i, d = int(rng.integers(0, new[b])), int(rng.integers(0, D))
+            p = kv[b] + i
+            c["codes"][1][c["table"][b, p // 16], h, p % 16, d] = 0x7F
+            want[int(c["cu"][b]) + i:int(c["cu"][b + 1]), 8 * h:8 * h + 8, d] = True
+    want = want.cuda()
+    for _ in range(20):
+        got = _attn_gpu(c, workspace=ws)
+        assert torch.equal(torch.isnan(got), want)
+        assert torch.equal(got[~want], base[~want])

@@ -171,6 +171,8 @@ specdec_status_t spec_attention(const void* q, int64_t q_token_stride, int32_t T
  *                 allows token v.  mask_rows [B, n_max+1] names each row's
  *                 mask, -1 for none.  NULL: none.
  * history_stride stays below 2^29.
+ * After SPECDEC_DEV_ERR_TIMEOUT in the error word (a device wait ran out) the
+ * rows that the call writes have no meaning; nothing else is touched.
  * For token v of row j, with c = times it was made (drafts before j among
  * them), in 32 bits and rounded once:
  *   l = logit; made or in the prompt: l > 0 ? l / repetition : l * repetition;

@@ -65,7 +65,7 @@ def verify_digest() -> str:
     """Digest of the sources the verify kernel is built from."""
     return source_digest(skip=("mtp_kernel.cuh", "shard_kernels.cuh", "shard_api.cu", "specdec_shard.h", "step_api.cu",
                                "attention_cut.cuh", "attention_kernel.cuh", "kv_kernels.cuh", "logits_kernel.cuh",
-                               "tcgen05.cuh", "specdec_step.h"))
+                               "tcgen05.cuh", "waits.cuh", "specdec_step.h"))
 
 
 def _up_to_date() -> bool:

@@ -59,6 +59,7 @@
 #include "kv_kernels.cuh"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
+#include "waits.cuh"
 
 namespace specdec {
 
@@ -107,11 +108,6 @@ constexpr int kPartialFloats = kAttnRows * 128 + 2 * kAttnRows;
 // before P would leave f16.
 constexpr float kPScale = 64.f;
 constexpr float kSlack = 9.f;
-// A wait gives up after this many looks, a pause of 32 ns or more between two
-// (half a second or more).
-#ifndef SPECDEC_ATTN_WAIT_LOOKS
-#define SPECDEC_ATTN_WAIT_LOOKS (1u << 24)
-#endif
 
 // Part of a (request, head, row group) that one CTA works on.  tile1 < 0 ends
 // the list.
@@ -269,49 +265,9 @@ struct AttnShared {
   int32_t joins;
 };
 
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-// Whether `x` holds for any thread of the barrier.
-__device__ __forceinline__ bool named_any(int id, int threads, bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(x)), "r"(id), "r"(threads)
-      : "memory");
-  return r != 0;
-}
-
 // One warp of a group polls a barrier, with pauses, and the others wait for it
 // at a hardware barrier; where a group meets at one, one thread arrives for it.
 // An SM's barrier operations take 5 to 8 cycles each, one after the other.
-//
-// A wait that gives up once; after that the thread goes on without waiting, so
-// that every barrier still gets its arrivals, to the end of its segment.  What
-// decides how often a group of warps meets at a barrier is agreed on at one.
-// (It is in some 50 places, and the instruction cache is small: it counts looks
-// where a clock would take twice the code.)
-struct Waiter {
-  uint32_t looks = SPECDEC_ATTN_WAIT_LOOKS;  // 0: gave up
-  __device__ __forceinline__ bool dead() const { return looks == 0; }
-  __device__ __forceinline__ void operator()(const uint64_t& bar, uint32_t parity, uint32_t pause = 32) {
-    const uint32_t at = ptx::smem_addr(&bar);
-    uint32_t left = looks;
-#pragma unroll 1
-    while (!ptx::mbar_try_wait(at, parity)) {
-      if (left == 0) {
-        looks = 0;
-        break;
-      }
-      --left;
-      __nanosleep(pause);
-    }
-  }
-};
 __device__ __forceinline__ void arrive(uint64_t& bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(ptx::smem_addr(&bar)), "r"(n) : "memory");
 }

@@ -29,6 +29,7 @@
 #include <stdint.h>
 
 #include "ptx.cuh"
+#include "waits.cuh"
 
 namespace specdec {
 
@@ -43,10 +44,6 @@ constexpr uint32_t kInPrompt = 1u << 31;
 constexpr uint32_t kHasBias = 1u << 30;
 constexpr uint32_t kIsDraft = 1u << 29;  // (a history is shorter than that)
 constexpr uint32_t kCountMask = kIsDraft - 1;
-// A wait gives up after this many cycles (a second).
-#ifndef SPECDEC_LOGIT_WAIT_CYCLES
-#define SPECDEC_LOGIT_WAIT_CYCLES 2000000000ll
-#endif
 struct LogitArgs {
   const void* logits;
   void* out;
@@ -163,8 +160,6 @@ struct LogitLayout {
   static __host__ __device__ int bytes(int share) { return 2 * share * 6 + kLogitRing * slot_bytes(share); }
 };
 
-__device__ __forceinline__ void logit_barrier(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
-
 template <typename Elt>
 __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const LogitArgs a) {
   extern __shared__ __align__(16) uint32_t words_of[];
@@ -193,11 +188,9 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
   for (int i = threadIdx.x; i < a.share / 2; i += kLogitThreads) reinterpret_cast<uint4*>(words_of)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
 
-  // A wait that gives up once; after that the thread goes on without waiting.
-  bool dead = false;
-  auto wait = [&](const uint64_t& bar, uint32_t parity) {
-    if (!dead) dead = !ptx::mbar_wait_bounded(ptx::smem_addr(&bar), parity, SPECDEC_LOGIT_WAIT_CYCLES);
-  };
+  // Where a wait for an item runs out, its role ends there: what the item's place
+  // holds then is not looked at.  The other roles' waits run out in turn.
+  Waiter wait;
   // A CTA's i-th item.  (Which of a request's items it is changes from one to
   // the next: low ids, and so work, are often the first's.)
   auto item_of = [&](int i) { return i * grid + static_cast<int>((blockIdx.x + 7u * i) % grid); };
@@ -234,6 +227,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
   };
   int rows_copied = 0;  // counted by each role but the second
 
+  auto gave_up = [&]() { return __any_sync(0xFFFFFFFFu, wait.dead()); };  // any thread of the warp
   auto warp_arrive = [&](const uint64_t& bar) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(ptx::smem_addr(&bar));
@@ -246,11 +240,13 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
       const int item = item_of(i), b = item / a.chunks, v0 = (item - b * a.chunks) * a.share, n = min(a.share, a.V - v0);
       const LogitItem& it = sh.item[i & 1];
       wait(sh.item_full[i & 1], i >> 1 & 1);
+      if (gave_up()) break;
 #pragma unroll 1
       for (int j = 0; j < it.rows; ++j) {
         if (in_place && it.mask[j] < 0) continue;
         const int slot = rows_copied % kLogitRing;
         wait(sh.row_done[slot], rows_copied / kLogitRing & 1);
+        if (gave_up()) break;
         ++rows_copied;
         // whole 16 bytes by a copy, the ends by threads
         const long long at = row_at(b, j, v0);
@@ -288,7 +284,8 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
       }
     };
     look_ahead(item_of(0));
-    for (int i = 0; item_of(i) < items; ++i) {
+    bool stop = false;
+    for (int i = 0; item_of(i) < items && !stop; ++i) {
       const int item = item_of(i), b = item / a.chunks, v0 = (item - b * a.chunks) * a.share, n = min(a.share, a.V - v0);
       const int rows = max(0, min(next_drafts, a.n_max)) + 1;
       const int masks[3] = {next_mask[0], next_mask[1], next_mask[2]};
@@ -300,6 +297,10 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
         if (in_place && !masked) continue;
         const int slot = rows_copied % kLogitRing;
         if (rows_copied >= kLogitRing) wait(sh.row_empty[slot], (rows_copied / kLogitRing - 1) & 1);
+        if (gave_up()) {
+          stop = true;
+          break;
+        }
         ++rows_copied;
         if (lane == 0) {
           const Span row = row_span(b, j, v0, n);
@@ -318,10 +319,9 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
       }
     }
     // no copy is in flight when the CTA ends
-    const bool was = dead;
-    dead = false;
-    for (int k = max(0, rows_copied - kLogitRing); k < rows_copied; ++k) wait(sh.row_full[k % kLogitRing], k / kLogitRing & 1);
-    dead |= was;
+    Waiter drain;
+    for (int k = max(0, rows_copied - kLogitRing); k < rows_copied; ++k) drain(sh.row_full[k % kLogitRing], k / kLogitRing & 1);
+    if (drain.dead()) wait.looks = 0;
   } else if (threadIdx.x >= 2 * kLogitTeam) {
     // ---------------------------------------------------------- named entries
     const int tid = threadIdx.x % kCountTeam, team = 1 + (threadIdx.x - 2 * kLogitTeam) / kCountTeam;  // 1 or 2
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
       if (i >= 2) wait(sh.item_empty[i & 1], ((i >> 1) - 1) & 1);
       const int was = it.listed;
       for (int k = tid; k < was; k += kCountTeam) words[list[k]] = 0;
-      logit_barrier(team, kCountTeam);
+      if (named_any(team, kCountTeam, wait.dead())) break;
       if (tid == 0) {
         it.p = rq.p;
         it.rows = rq.drafts + 1;
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
       }
       if (tid <= rq.drafts) it.mask[tid] = m < a.mask_count ? m : -1;
       if (tid < rq.drafts) it.draft[tid] = draft;
-      logit_barrier(team, kCountTeam);
+      named_barrier(team, kCountTeam);
       auto add = [&](int v, uint32_t flag) {  // counted, or flagged
         const uint32_t off = static_cast<uint32_t>(v) - static_cast<uint32_t>(v0);
         if (off >= static_cast<uint32_t>(n)) return;
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
         }
         if (tid == 0) it.biases = count;
       }
-      logit_barrier(team, kCountTeam);
+      named_barrier(team, kCountTeam);
       const int biases = it.biases;
       if (biases > 0 && biases <= kBiasList) {
         for (int q = tid; q < biases; q += kCountTeam) {
@@ -420,8 +420,13 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
           it.bias_sum[q] = sum;
           it.bias_first[q] = is_first;
         }
-        logit_barrier(team, kCountTeam);
+        named_barrier(team, kCountTeam);
       }
+#ifdef SPECDEC_TEST_WAIT_RUNS_OUT
+      // Failure-path test builds only: the first CTA keeps its second item to
+      // itself, so every other role's wait of that CTA runs out in turn.
+      if (blockIdx.x == 0 && i == 1) continue;
+#endif
       if (tid == 0) ptx::mbar_arrive(ptx::smem_addr(&sh.item_full[i & 1]));
     }
   } else {
@@ -434,6 +439,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
       const uint32_t* words = words_of + (i & 1) * a.share;
       const uint16_t* list = list_of + (i & 1) * a.share;
       wait(sh.item_full[i & 1], i >> 1 & 1);
+      if (named_any(3 + team, kLogitTeam, wait.dead())) break;
       const int rows = it.rows, listed = it.listed, biases = it.biases;
       const bool few = biases <= kBiasList;  // all of them are in shared memory
       const LogitParams p = it.p;
@@ -494,7 +500,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
         };
         if (s.head + s.tail > 0) {
           fill(buf + ph, from, n * kElt, s);
-          logit_barrier(3 + team, kLogitTeam);
+          named_barrier(3 + team, kLogitTeam);
         }
         for (int q = tid; q < listed; q += kLogitTeam) change_listed(row, j, q);
         for (int q = tid; few && q < biases; q += kLogitTeam) change_biased(row, j, q);
@@ -502,7 +508,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
           const Span ms = mask_span(m, v0, n);
           const uint32_t* mask = reinterpret_cast<const uint32_t*>(buf + row_bytes + (mask_at(m, v0) & 15));
           if (ms.head + ms.tail > 0) fill(buf + row_bytes + (mask_at(m, v0) & 15), mask_at(m, v0), (n + 31) / 32 * 4, ms);
-          logit_barrier(3 + team, kLogitTeam);
+          named_barrier(3 + team, kLogitTeam);
           const int last = (n - 1) >> 5;
 #pragma unroll 4
           for (int i = tid; i * 16 < ph + n * kElt; i += kLogitTeam) {
@@ -521,7 +527,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
       warp_arrive(sh.item_empty[i & 1]);
     }
   }
-  if (dead && a.err != nullptr) atomicOr(a.err, SPECDEC_DEV_ERR_TIMEOUT);
+  if (wait.dead() && a.err != nullptr) atomicOr(a.err, SPECDEC_DEV_ERR_TIMEOUT);
 }
 
 }  // namespace specdec

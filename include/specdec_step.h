@@ -48,7 +48,9 @@ extern "C" {
                                        that is not a positive finite number
                                        (taken as 1), a presence or frequency
                                        penalty that is not finite (taken as 0),
-                                       or a length out of range (clamped) */
+                                       a length out of range (clamped), or a
+                                       row's mask outside [-1, mask_count) (the
+                                       row is not masked) */
 
 /*
  * kv_block_step — block tables and slot maps from request lengths.

@@ -331,7 +331,6 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
       uint32_t* words = words_of + (i & 1) * a.share;
       uint16_t* list = list_of + (i & 1) * a.share;
       const LogitRequest rq(a, b);
-      if (rq.bad && a.err != nullptr && v0 == 0 && tid == 0) atomicOr(a.err, SPECDEC_DEV_ERR_PENALTY);
       // what does not need the item's place is on its way while that is waited for
       const int m = a.mask_rows != nullptr && tid < rows_max ? __ldg(a.mask_rows + static_cast<long long>(b) * rows_max + tid) : -1;
       const int draft = tid < rq.drafts ? __ldg(a.draft_tokens + static_cast<long long>(b) * a.n_max + tid) : -1;
@@ -366,7 +365,9 @@ __global__ void __launch_bounds__(kLogitThreads, 1) process_logits_kernel(const 
         it.hi = rq.hi;
         it.listed = it.biases = 0;
       }
-      if (tid <= rq.drafts) it.mask[tid] = m < a.mask_count ? m : -1;
+      const bool no_mask = tid <= rq.drafts && (m < -1 || m >= a.mask_count);
+      if (((rq.bad && tid == 0) || no_mask) && a.err != nullptr && v0 == 0) atomicOr(a.err, SPECDEC_DEV_ERR_PENALTY);
+      if (tid <= rq.drafts) it.mask[tid] = no_mask ? -1 : m;
       if (tid < rq.drafts) it.draft[tid] = draft;
       named_barrier(team, kCountTeam);
       auto add = [&](int v, uint32_t flag) {  // counted, or flagged

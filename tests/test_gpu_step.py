@@ -772,3 +772,25 @@ def test_attention_many_short_items_a_cta(D):
         got = _attn_gpu(c, workspace=ws)
         assert torch.equal(torch.isnan(got), want)
         assert torch.equal(got[~want], base[~want])
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("bad", [3, 1 << 30, -2, -2**31])
+def test_process_logits_reports_masks_that_are_not_there(bad, in_place):
+    rng = np.random.default_rng(33)
+    B, n, V = 3, 2, 700
+    c = _logit_case(rng, B, n, V, 20, ragged=False)
+    c["mask_rows"][:] = rng.integers(-1, 3, (B, n + 1))
+    c["draft_len"][2] = 1
+    x = torch.tensor(rng.normal(0, 3, (B, n + 1, V))).float().cuda()
+    untouched = x.double().cpu().numpy() if in_place else 77.0
+    err = err_word()
+    # a row that is not there may name anything
+    c["mask_rows"][2, 2] = bad
+    _check_logits(x, c, _run_logits(x, c, in_place=in_place, err=err), untouched)
+    assert err.item() == 0
+    c["mask_rows"][1, 2] = bad
+    got = _run_logits(x, c, in_place=in_place, err=err)
+    assert err.item() == sd.DEV_ERR_PENALTY
+    c["mask_rows"][1, 2] = -1  # as a row without a mask
+    _check_logits(x, c, got, untouched)

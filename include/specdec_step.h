@@ -83,6 +83,10 @@ extern "C" {
  *   (cu_tokens ends there) and set SPECDEC_DEV_ERR_BLOCKS.
  *   Table entries at and past held_out have no meaning.
  * kv_len_out, held_out and ring_state_out may be the inputs themselves.
+ * Without requests (B = 0) the arrays that have an element a request are not
+ * looked at and the other outputs are written all the same (no tokens, no
+ * blocks, the ring as it was); nothing is where ring_state is not memory of a
+ * device.
  */
 specdec_status_t kv_block_step(int32_t B, int32_t block_size, int32_t max_blocks, int32_t num_blocks,
                                const int32_t* kv_len, const int32_t* accepted_len, const int32_t* new_tokens,

@@ -20,6 +20,17 @@ specdec_status_t launched() { return cudaGetLastError() == cudaSuccess ? SPECDEC
 
 bool block_size_ok(int32_t bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128; }
 
+// Whether p is memory that the CUDA runtime gave out (false without a device).
+bool on_device(const void* p) {
+  cudaPointerAttributes at;
+  if (p == nullptr) return false;
+  if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged;
+}
+
 // The cache's shape: INVALID_ARG, UNSUPPORTED or OK.
 specdec_status_t check_cache(int32_t num_blocks, int32_t block_size, int32_t H, int32_t D) {
   if (num_blocks <= 0 || block_size <= 0 || H <= 0 || D <= 0) return SPECDEC_ERR_INVALID_ARG;
@@ -195,10 +206,13 @@ extern "C" specdec_status_t kv_block_step(int32_t B, int32_t block_size, int32_t
   if (static_cast<int64_t>(num_blocks) * block_size > INT32_MAX ||
       static_cast<int64_t>(max_blocks) * block_size > INT32_MAX)
     return SPECDEC_ERR_UNSUPPORTED;
-  if (B == 0) return SPECDEC_OK;
-  if (kv_len == nullptr || new_tokens == nullptr || held == nullptr || block_table == nullptr || free_ring == nullptr ||
-      ring_state == nullptr || kv_len_out == nullptr || held_out == nullptr || ring_state_out == nullptr ||
-      cu_tokens == nullptr || cu_blocks == nullptr)
+  // A step without requests has no arrays of them, but leaves its other outputs
+  // as any step does, unless there is no ring on a device.
+  if (B == 0 && !on_device(ring_state)) return SPECDEC_OK;
+  if (B > 0 && (kv_len == nullptr || new_tokens == nullptr || held == nullptr || block_table == nullptr ||
+                kv_len_out == nullptr || held_out == nullptr))
+    return SPECDEC_ERR_INVALID_ARG;
+  if (free_ring == nullptr || ring_state == nullptr || ring_state_out == nullptr || cu_tokens == nullptr || cu_blocks == nullptr)
     return SPECDEC_ERR_INVALID_ARG;
   if (capacity > 0 && (slot_map == nullptr || positions == nullptr)) return SPECDEC_ERR_INVALID_ARG;
   BlockArgs a;

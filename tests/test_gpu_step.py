@@ -794,3 +794,34 @@ def test_process_logits_reports_masks_that_are_not_there(bad, in_place):
     assert err.item() == sd.DEV_ERR_PENALTY
     c["mask_rows"][1, 2] = -1  # as a row without a mask
     _check_logits(x, c, got, untouched)
+
+
+@pytest.mark.parametrize("capacity", [0, 5, 5000])
+@pytest.mark.parametrize("alias", [False, True])
+def test_block_step_without_requests_leaves_its_outputs(capacity, alias):
+    e = lambda *s: torch.empty(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    ring, state = torch.arange(7, dtype=torch.int32, device="cuda"), dev(np.array([5, 4], dtype=np.int32))
+    fill = lambda n: torch.full((n,), 99, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = sd.BlockStep(e(0), e(0), state if alias else fill(2), fill(1), fill(1), fill(capacity), fill(capacity))
+    err = err_word()
+    step = sd.kv_block_step(e(0, 3), e(0), e(0), e(0), ring, state, 16, capacity, out=out, error_word=err)
+    wait_gpu()
+    assert step.ring_state.tolist() == [5, 4] and step.cu_tokens.tolist() == [0] and step.cu_blocks.tolist() == [0]
+    assert (step.slot_map == -1).all() and (step.positions == -1).all()
+    assert ring.tolist() == list(range(7)) and state.tolist() == [5, 4] and err.item() == 0
+    # outputs of its own; in a graph; and the ring's state is looked at as ever
+    junk = [torch.full((4 + 2 * capacity,), 99, dtype=torch.int32, device="cuda") for _ in range(3)]
+    del junk
+    step = sd.kv_block_step(e(0, 3), e(0), e(0), e(0), ring, state, 16, capacity)
+    wait_gpu()
+    assert step.ring_state.tolist() == [5, 4] and step.cu_tokens.tolist() == [0] and (step.slot_map == -1).all()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sd.kv_block_step(e(0, 3), e(0), e(0), e(0), ring, state, 16, capacity, out=out, error_word=err)
+    for t in out:
+        if t is not state:
+            t.fill_(99)
+    state[1] = 9
+    g.replay()
+    wait_gpu()
+    assert out.ring_state.tolist() == [5, 7] and (out.positions == -1).all() and err.item() == sd.DEV_ERR_BLOCKS

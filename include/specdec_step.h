@@ -109,8 +109,8 @@ specdec_status_t kv_block_step(int32_t B, int32_t block_size, int32_t max_blocks
  * older ones.  (No two runs of a call may share a block.)  Per run and head
  * the scale is the least power of two that brings the largest magnitude
  * within 448, the type's largest number, and at least the block's scale where
- * it has older tokens, whose codes are then rescaled; 0 when all are 0.
- * Codes are rounded to the nearest, ties to even; infinities become the
+ * it has older tokens, whose codes are then rescaled; 0 when all that is finite
+ * is 0.  Codes are rounded to the nearest, ties to even; infinities become the
  * largest number and do not count for the scale, NaN stays NaN.
  */
 specdec_status_t kv_append(const void* k, const void* v, specdec_dtype_t dtype, int32_t T, int32_t H, int32_t D,

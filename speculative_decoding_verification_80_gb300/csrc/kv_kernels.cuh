@@ -481,7 +481,8 @@ __global__ void __launch_bounds__(kAppendThreads, kVecs <= 8 ? 4 : 2) append_ker
       }
       const float amax = __uint_as_float(top);
       const float now = fmaxf(pow2_scale(amax), pow2_ceil(old));
-      const float inv = pow2_inverse(now);
+      // (scale 0: the finite values are zeros, and an infinity stays one for its code)
+      const float inv = now > 0.f ? pow2_inverse(now) : 1.f;
       if (off > 0 && now > old) {  // the older tokens move to the new scale
         const float ratio = old * inv;
         for (int k = k0; k < off * (D / 16); k += width) {

@@ -825,3 +825,23 @@ def test_block_step_without_requests_leaves_its_outputs(capacity, alias):
     g.replay()
     wait_gpu()
     assert out.ring_state.tolist() == [5, 7] and (out.positions == -1).all() and err.item() == sd.DEV_ERR_BLOCKS
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,n", [(64, 1), (128, 5), (128, 16)])
+def test_append_infinities_among_zeros_are_the_largest_number(D, n, dtype):
+    # scale 0: the codes are still numbers (448 times 0 is 0; a NaN would spoil every query that sees it)
+    kc = np.full((4, 1, 16, D), 0x11, dtype=np.uint8)
+    zero, two = np.zeros((4, 1), dtype=np.float32), np.full((4, 1), 2.0, dtype=np.float32)
+    x = torch.zeros(n, 1, D, device="cuda").to(dtype)
+    x[0, 0, 1], x[n - 1, 0, 2], x[n - 1, 0, 7] = float("inf"), -float("inf"), float("nan")
+    want = np.zeros((n, D))
+    want[0, 1], want[n - 1, 2], want[n - 1, 7] = 448, -448, np.nan
+    # into an empty block, behind a block's older tokens of scale 0, and behind some of scale 2
+    for first, scale, after in ((16, two, 0.0), (32 + 16 - n, zero, 0.0), (48 + 16 - n, two, 0.0 if n == 16 else 2.0)):
+        slots = np.arange(first, first + n)
+        got = _run_append(x, -x, slots, (kc, kc, scale, scale))
+        for codes, scales, sign in ((got[0], got[2], 1), (got[1], got[3], -1)):
+            b, o = first // 16, first % 16
+            assert np.array_equal(ref.VALUES[codes[b, 0, o:o + n]], sign * want, equal_nan=True)
+            assert (codes[b, 0, :o] == 0x11).all() and scales[b, 0] == after

@@ -80,7 +80,9 @@ typedef enum { SPECDEC_F32 = 0, SPECDEC_BF16 = 1 } specdec_dtype_t;
                                           outputs are incomplete; the workspace is
                                           re-armed by the call itself */
 #define SPECDEC_DEV_ERR_SEGMENT 16u    /* mtp_shift_insert: a segment outside [0, R)
-                                          or a_b outside [0, n_b]; left unchanged */
+                                          or a_b outside [0, n_b]; left unchanged.
+                                          spec_attention: cu_tokens that decrease
+                                          or leave [0, T] */
 
 /* Largest supported sizes. */
 #define SPECDEC_MAX_VOCAB 262144 /* 2^18 */

@@ -126,6 +126,10 @@ specdec_status_t kv_append(const void* k, const void* v, specdec_dtype_t dtype, 
  *                contiguous.  Hq is a multiple of H; query head h reads key
  *                and value head h / (Hq / H).
  *   cu_tokens    [B+1]: request b's tokens are cu_tokens[b] .. cu_tokens[b+1]-1.
+ *                Values outside [0, T] are clamped and a decrease is a request
+ *                without tokens; either sets SPECDEC_DEV_ERR_SEGMENT.  Where
+ *                requests overlap so often that their tiles pass the count
+ *                below, nothing is computed.
  *   kv_len       [B]: tokens in the cache before these; these tokens' own keys
  *                and values are in the cache (kv_append), so token i of
  *                request b attends to positions 0 .. kv_len[b] + i.

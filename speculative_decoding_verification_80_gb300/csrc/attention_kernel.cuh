@@ -389,8 +389,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int per = (a.B + kAttnThreads - 1) / kAttnThreads;
     const int lo = min(a.B, tid * per), hi = min(a.B, lo + per);
     uint32_t before = 0, mine = 0;
+    bool bad = false;
     // first the sum of this thread's requests, then the request of unit u0
-    // where it is among them
+    // where it is among them (sums stay at the largest int, which requests that
+    // do not overlap cannot reach: the call is refused before)
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
       uint32_t at = before;
@@ -403,7 +405,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           sh.b0 = b;
           sh.ub0 = at;
         }
-        at += n;
+        at = capped_sum(at, n);
+        const int first = __ldg(a.cu_tokens + b), end = __ldg(a.cu_tokens + b + 1);
+        bad |= first < 0 || end < first || end > a.T;
       }
       if (pass == 1) break;
       mine = at;
@@ -411,19 +415,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, s, d);
-        if (lane >= d) s += o;
+        if (lane >= d) s = capped_sum(s, o);
       }
       if (lane == 31) sh.part[warp] = s;
       __syncthreads();
       // a lane for each warp
       const uint32_t w = lane < kAttnThreads / 32 ? sh.part[lane] : 0;
-      const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, w);
+      // requests that overlap may have more units than can be counted: none then
+      const unsigned long long all = (static_cast<unsigned long long>(__reduce_add_sync(0xFFFFFFFFu, w >> 16)) << 16) +
+                                     __reduce_add_sync(0xFFFFFFFFu, w & 0xFFFFu);
+      const uint32_t total = all < 0x7FFFFFFFull ? static_cast<uint32_t>(all) : 0;
+      bad |= all >= 0x7FFFFFFFull;
       before = s - mine + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0);
       chunk = max((total + gridDim.x - 1) / gridDim.x, static_cast<uint32_t>(kLeastCost));
       u0 = min(static_cast<unsigned long long>(total), static_cast<unsigned long long>(blockIdx.x) * chunk);
       u1 = min(total, u0 + chunk);
       if (u0 >= u1 || before > u0 || u0 >= before + mine) break;
     }
+    if (bad && blockIdx.x == 0) atomicOr(a.err, SPECDEC_DEV_ERR_SEGMENT);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();

@@ -845,3 +845,37 @@ def test_append_infinities_among_zeros_are_the_largest_number(D, n, dtype):
             b, o = first // 16, first % 16
             assert np.array_equal(ref.VALUES[codes[b, 0, o:o + n]], sign * want, equal_nan=True)
             assert (codes[b, 0, :o] == 0x11).all() and scales[b, 0] == after
+
+
+def test_attention_reports_requests_that_decrease_or_leave_the_tokens():
+    rng = np.random.default_rng(40)
+    c = _attn_case(rng, [2, 2, 0], [60, 90, 10], 8, 2, 64, 16)
+    ws = sd.new_attention_workspace()
+    want = _attn_gpu(c, workspace=ws)
+    assert sd.get_error(ws) == 0
+    for cu in ([0, 2, 9, 4], [-3, 2, 4, 1], [0, 2, 4, -1], [0, 2, 5, 5]):
+        c["cu"] = np.array(cu, dtype=np.int32)
+        assert torch.equal(_attn_gpu(c, workspace=ws), want)
+        assert sd.get_error(ws) == sd.DEV_ERR_SEGMENT
+    c["cu"] = np.array([0, 2, 4, 4], dtype=np.int32)
+    assert torch.equal(_attn_gpu(c, workspace=ws), want)
+    assert sd.get_error(ws) == 0
+
+
+def test_attention_requests_that_overlap_past_its_count():
+    # 64 tokens that every second of 4096 requests claims: 10^10 units in all
+    B, T, H, D, bs, width = 4096, 64, 64, 64, 128, 8192
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, T] * (B // 2) + [0], **i32)
+    kv = torch.full((B,), width * bs - T, **i32)
+    table = torch.zeros(B, width, **i32)
+    cache = torch.zeros(1, H, bs, D, dtype=torch.uint8, device="cuda").view(E4M3)
+    scale = torch.ones(1, H, device="cuda")
+    q = torch.randn(T, H, D, device="cuda").to(torch.bfloat16)
+    out = torch.full_like(q, 77.0)
+    ws = sd.new_attention_workspace()
+    sd.spec_attention(q, cu, kv, table, cache, cache, scale, scale, out=out, workspace=ws)
+    wait_gpu()
+    assert (out == 77.0).all() and sd.get_error(ws) == sd.DEV_ERR_SEGMENT and not ws.any()
+    c = _attn_case(np.random.default_rng(41), [3, 5], [400, 77], 16, 2, 64, 16)
+    _check_attn(c, _attn_gpu(c, workspace=ws))

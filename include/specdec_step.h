@@ -152,7 +152,8 @@ specdec_status_t kv_append(const void* k, const void* v, specdec_dtype_t dtype, 
  * their size over a reference (a score that later ones pass by 2^9 at most):
  * 11 significant bits down to 2^-20 of it, nothing below 2^-31.
  * SPECDEC_ERR_UNSUPPORTED also where the tiles of 128 positions, over heads
- * and groups of 64 rows, could pass some 400 million.
+ * and groups of 64 rows, could pass some 400 million, or where
+ * max_blocks * block_size + T passes 2^31 - 1.
  */
 #define SPECDEC_ATTENTION_WORKSPACE_BYTES (64u << 20)
 specdec_status_t spec_attention(const void* q, int64_t q_token_stride, int32_t T, int32_t Hq, int32_t H, int32_t D,

@@ -173,7 +173,7 @@ struct Walker {
     q0 = max(0, min(__ldg(a.cu_tokens + b), a.T));
     const int q1 = max(0, min(__ldg(a.cu_tokens + b + 1), a.T));
     q = max(0, q1 - q0);
-    kv = __ldg(a.kv_len + b);
+    kv = min(__ldg(a.kv_len + b), a.max_blocks << a.bs_log2);  // (positions behind the row's end: sums with it stay in 32 bits)
   }
   __device__ bool next(Segment& s) {
 #pragma unroll 1

@@ -334,7 +334,7 @@ extern "C" specdec_status_t spec_attention(const void* q, int64_t q_token_stride
   const specdec_status_t chk = check_cache(num_blocks, block_size, H, D);
   if (chk != SPECDEC_OK) return chk;
   if (Hq % H != 0 || !(scale >= 0.f) || scale > 3e38f) return SPECDEC_ERR_INVALID_ARG;
-  if (B > SPECDEC_MAX_BATCH || static_cast<int64_t>(max_blocks) * block_size > INT32_MAX) return SPECDEC_ERR_UNSUPPORTED;
+  if (B > SPECDEC_MAX_BATCH || static_cast<int64_t>(max_blocks) * block_size + T > INT32_MAX) return SPECDEC_ERR_UNSUPPORTED;
   if (T == 0 || B == 0) return SPECDEC_OK;
   if (q == nullptr || cu_tokens == nullptr || kv_len == nullptr || block_table == nullptr || k_cache == nullptr ||
       v_cache == nullptr || k_scale == nullptr || v_scale == nullptr || out == nullptr)

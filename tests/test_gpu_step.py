@@ -879,3 +879,17 @@ def test_attention_requests_that_overlap_past_its_count():
     assert (out == 77.0).all() and sd.get_error(ws) == sd.DEV_ERR_SEGMENT and not ws.any()
     c = _attn_case(np.random.default_rng(41), [3, 5], [400, 77], 16, 2, 64, 16)
     _check_attn(c, _attn_gpu(c, workspace=ws))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_lengths_far_past_the_table(D):
+    # all tokens attend to what the table's row holds, however long the request is said to be
+    c = _attn_case(np.random.default_rng(42), [3, 5, 2], [400, 77, 250], 16, 2, D, 16)
+    c["table"] = np.maximum(c["table"][:, :4], 0)
+    c["codes"] = [np.where((x & 0x7F) == 0x7F, 0, x).astype(np.uint8) for x in c["codes"]]
+    c["kv"][:] = 1000
+    want = _attn_gpu(c)
+    _check_attn(c, want)
+    for far in (2**31 - 1, 2**31 - 3, 1 << 30):
+        c["kv"][:] = far
+        assert torch.equal(_attn_gpu(c), want)

@@ -162,3 +162,13 @@ def test_step_refuses_what_its_counters_cannot_hold(lib):
                                   fake, fake, 64 << 20, None)
 
     assert attention(1 << 20, 1 << 26) == 2
+
+
+def test_attention_refuses_positions_past_32_bits(lib):
+    def attention(T, width):
+        return lib.spec_attention(fake, 8, T, 1, 1, 64, 1, fake, fake, fake, width, 100, 16, fake, fake, fake, fake, 0.0, fake,
+                                  fake, 64 << 20, None)
+
+    # (the token stride is refused where the sizes are not)
+    assert attention(16, (1 << 27) - 1) == 2 and attention(1 << 20, (1 << 27) - 1000) == 2
+    assert attention(15, (1 << 27) - 1) == 1

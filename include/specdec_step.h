@@ -147,7 +147,7 @@ specdec_status_t kv_append(const void* k, const void* v, specdec_dtype_t dtype, 
  *                after SPECDEC_DEV_ERR_TIMEOUT the call's outputs have no
  *                meaning and the workspace has to be zero-filled again.
  * Scores, their maxima and sums and the output's sums are held in 32 bits;
- * keys and values are taken as they are in the cache, queries to 2^-18 of a
+ * keys and values are taken as they are in the cache, queries to 2^-21 of a
  * row's largest.  Probabilities enter the second product in f16, 64 times
  * their size over a reference (a score that later ones pass by 2^9 at most):
  * 11 significant bits down to 2^-20 of it, nothing below 2^-31.

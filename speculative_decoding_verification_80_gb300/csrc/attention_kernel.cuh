@@ -14,7 +14,8 @@
 // First product: e4m3 x e4m3 with 32-bit sums.  K goes from HBM to the tensor
 // cores as it lies in the cache.  Q, bf16 scaled by a power of two a row, is
 // the sum of two e4m3 numbers: a value of 8 significant bits is its nearest
-// number of 4 bits plus a remainder of 4 (exact to 2^-18 of the row's largest).
+// number of 4 bits plus a remainder of 4, held 16 times its size so that e4m3's
+// least step, 2^-9, is 2^-13 of it (exact to 2^-21 of the row's largest).
 // The two are rows of one B operand, so K is read from shared memory once, and
 // the softmax adds their columns: shared memory's 128 bytes a cycle, of which a
 // tile takes most, are the next limit after HBM.
@@ -277,10 +278,14 @@ __device__ __forceinline__ void warp_arrive(uint64_t& bar, uint32_t n = 1) {
   if ((threadIdx.x & 31) == 0) arrive(bar, n);
 }
 
-// Nearest number of 4 significant bits; the remainder of a number of 8 has 4.
+// Nearest e4m3 number (|x| at most 448): 4 significant bits, below 2^-6 whole
+// steps of 2^-9, which is the last bit of 1.5 * 2^14.  What is left of a number of
+// 8 bits has 4.
 __device__ __forceinline__ float top4(float x) {
-  return __uint_as_float((__float_as_uint(x) + 0x80000u) & 0xFFF00000u);
+  constexpr float kFar = 24576.f;
+  return fabsf(x) < 0x1p-6f ? (x + kFar) - kFar : __uint_as_float((__float_as_uint(x) + 0x80000u) & 0xFFF00000u);
 }
+constexpr float kRest = 16.f;  // times the remainder's size (of 448 at most 16: 256)
 
 // Byte x of row t in a tile of K or V (rows of D bytes) as the copies swizzle it.
 template <int D>
@@ -520,7 +525,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               tc::ready(rest);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                float y = (v[e] + rest[e]) * ks;
+                float y = fmaf(rest[e], 1.f / kRest, v[e]) * ks;
                 if (masked && pos > sh.limit[par][r0 + c + e]) y = -INFINITY;
                 y = tc::warp_max(y);
                 if (lane == e) mine = y;
@@ -573,8 +578,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
           for (int r = 0; r < kGroupRows; r += 2) {
             const float4 w = col[r >> 1];
-            x[r] = fmaf((x[r] + rest[r]) * ks, w.x, -w.y);
-            x[r + 1] = fmaf((x[r + 1] + rest[r + 1]) * ks, w.z, -w.w);
+            x[r] = fmaf(fmaf(rest[r], 1.f / kRest, x[r]) * ks, w.x, -w.y);
+            x[r + 1] = fmaf(fmaf(rest[r + 1], 1.f / kRest, x[r + 1]) * ks, w.z, -w.w);
           }
           if (masked) {
 #pragma unroll
@@ -783,7 +788,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             h[j] = top4(u[j]);
           }
           hw[e >> 2] = tc::e4m3x2(h[0], h[1]) | (tc::e4m3x2(h[2], h[3]) << 16);
-          lw[e >> 2] = tc::e4m3x2(u[0] - h[0], u[1] - h[1]) | (tc::e4m3x2(u[2] - h[2], u[3] - h[3]) << 16);
+          lw[e >> 2] = tc::e4m3x2((u[0] - h[0]) * kRest, (u[1] - h[1]) * kRest) |
+                       (tc::e4m3x2((u[2] - h[2]) * kRest, (u[3] - h[3]) * kRest) << 16);
         }
         qv[i] = make_uint4(hw[0], hw[1], lw[0], lw[1]);
       }

@@ -893,3 +893,34 @@ def test_attention_lengths_far_past_the_table(D):
     for far in (2**31 - 1, 2**31 - 3, 1 << 30):
         c["kv"][:] = far
         assert torch.equal(_attn_gpu(c), want)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_queries_far_below_their_rows_largest(D):
+    # the largest of a row meets keys of 0, so the scores are those of the rest: 2^-16 to 2^-9 of it
+    rng = np.random.default_rng(D)
+    c = _attn_case(rng, [1], [1], 8, 1, D, 16, stale=False)
+    u = np.exp2(-8.0) * np.array([2.34375, 1.25, 1.2578125, 0.6171875, 0.31, 0.155, 0.08, 0.04])[:, None] * np.ones((8, D))
+    u[3:] *= rng.uniform(1, 2, (5, D))
+    signs = np.where(rng.random(D) < 0.5, -1.0, 1.0)
+    q = u * signs
+    q[:, 0] = 225.0
+    c["q"] = torch.tensor(q[None]).to(torch.bfloat16)
+    block = c["table"][0, 0]
+    for p in (0, 1):  # two positions with opposite keys and values
+        key = np.where(signs * (1 - 2 * p) > 0, ref.to_e4m3(448.0), ref.to_e4m3(-448.0))
+        key[0] = 0
+        c["codes"][0][block, 0, p] = key
+        c["codes"][1][block, 0, p] = ref.to_e4m3(1.0 - 2 * p)
+    c["scales"][0][:] = c["scales"][1][:] = 1.0
+    qs = c["q"].double().numpy()
+    for r in range(8):
+        # every row's scores are +-0.5; a query's values are off by 2^-14 at most, which the softmax's quotient
+        # takes twice; the rest as in _check_attn
+        s = 0.5 / (448 * np.abs(qs[0, r, 1:]).sum())
+        want, mag, _ = ref.attention(qs, c["cu"], c["kv"], c["table"], c["codes"][0], c["codes"][1], c["scales"][0],
+                                     c["scales"][1], s)
+        got = _attn_gpu(c, scale=s).double().cpu().numpy()
+        off = 2.0 ** -14 * 448 * (D - 1) * s
+        tol = 2.0 ** -8 * np.abs(want[0, r]) + (2.0 ** -8 + 2 * off) * mag[0, r]
+        assert (np.abs(got[0, r] - want[0, r]) <= tol).all(), (r, got[0, r, 0], want[0, r, 0], tol[0])

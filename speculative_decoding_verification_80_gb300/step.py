@@ -146,7 +146,10 @@ def _strided(x: torch.Tensor, what: str, dev: int):
     token, head, one = x.stride()
     if one != 1:
         raise ValueError(f"the last dimension of {what} must be contiguous")
-    return x.data_ptr(), token, head
+    T, H, D = x.shape
+    # (one token, or one head, is as far from the next as it would be if contiguous)
+    head = head if H > 1 else D
+    return x.data_ptr(), token if T > 1 else H * head, head
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -203,10 +206,10 @@ def spec_attention(q: torch.Tensor, cu_tokens: torch.Tensor, kv_len: torch.Tenso
     if workspace is None:
         workspace = new_attention_workspace(device=q.device, stream=stream)
     qp, qt, qh = _strided(q, "q", dev)
-    if qh != D and Hq > 1:
+    if qh != D:
         raise ValueError("the heads of q must be contiguous")
     size = workspace.numel()
-    _check(load_library().spec_attention(qp, qt if T > 1 else Hq * D, T, Hq, H, D, B, *lengths, width, blocks, bs,
+    _check(load_library().spec_attention(qp, qt, T, Hq, H, D, B, *lengths, width, blocks, bs,
                                          *cache, 0.0 if scale is None else float(scale), to,
                                          _at(workspace, size, "workspace", workspace.dtype, dev), size,
                                          _on_stream(stream, dev)), "spec_attention")

@@ -924,3 +924,21 @@ def test_attention_queries_far_below_their_rows_largest(D):
         off = 2.0 ** -14 * 448 * (D - 1) * s
         tol = 2.0 ** -8 * np.abs(want[0, r]) + (2.0 ** -8 + 2 * off) * mag[0, r]
         assert (np.abs(got[0, r] - want[0, r]) <= tol).all(), (r, got[0, r, 0], want[0, r, 0], tol[0])
+
+
+def test_strides_of_a_single_token_or_head_do_not_matter():
+    rng = np.random.default_rng(43)
+    buf = torch.randn(8 * 64, device="cuda").to(torch.bfloat16)
+    kc, ks = _cache(rng, 4, 8, 16, 64)
+    _check_append(buf.as_strided((1, 8, 64), (7, 64, 1)), buf.as_strided((1, 8, 64), (1, 64, 1)), np.array([21]), kc, kc, ks, ks)
+    kc, ks = _cache(rng, 4, 1, 16, 64)
+    slots = np.arange(20, 28)
+    _check_append(buf.as_strided((8, 1, 64), (64, 3, 1)), buf.as_strided((8, 1, 64), (64, 0, 1)), slots, kc, kc, ks, ks)
+    c = _attn_case(rng, [8], [30], 1, 1, 64, 16)
+    c["q"] = buf.view(8, 1, 64).cpu()
+    out = _attn_gpu(c)
+    assert torch.equal(_attn_gpu(c, q=buf.as_strided((8, 1, 64), (64, 5, 1))), out)
+    c = _attn_case(rng, [1], [30], 8, 1, 64, 16)
+    c["q"] = buf.view(1, 8, 64).cpu()
+    out = _attn_gpu(c)
+    assert torch.equal(_attn_gpu(c, q=buf.as_strided((1, 8, 64), (3, 64, 1))), out)

@@ -208,10 +208,11 @@ def spec_attention(q: torch.Tensor, cu_tokens: torch.Tensor, kv_len: torch.Tenso
     qp, qt, qh = _strided(q, "q", dev)
     if qh != D:
         raise ValueError("the heads of q must be contiguous")
-    size = workspace.numel()
+    words = workspace.numel()
+    size = words * workspace.element_size()
     _check(load_library().spec_attention(qp, qt, T, Hq, H, D, B, *lengths, width, blocks, bs,
                                          *cache, 0.0 if scale is None else float(scale), to,
-                                         _at(workspace, size, "workspace", workspace.dtype, dev), size,
+                                         _at(workspace, words, "workspace", workspace.dtype, dev), size,
                                          _on_stream(stream, dev)), "spec_attention")
     return out
 

@@ -942,3 +942,12 @@ def test_strides_of_a_single_token_or_head_do_not_matter():
     c["q"] = buf.view(1, 8, 64).cpu()
     out = _attn_gpu(c)
     assert torch.equal(_attn_gpu(c, q=buf.as_strided((1, 8, 64), (3, 64, 1))), out)
+
+
+@pytest.mark.parametrize("dtype", [torch.uint8, torch.int32, torch.float64])
+def test_attention_workspaces_of_any_type(dtype):
+    c = _attn_case(np.random.default_rng(44), [3], [400], 16, 2, 64, 16)
+    ws = torch.zeros(sd.ATTENTION_WORKSPACE_BYTES // torch.empty(0, dtype=dtype).element_size(), dtype=dtype, device="cuda")
+    _check_attn(c, _attn_gpu(c, workspace=ws))
+    with pytest.raises(sd.SpecDecError, match="WORKSPACE"):
+        _attn_gpu(c, workspace=ws[:-1])

@@ -139,7 +139,7 @@ specdec_status_t kv_append(const void* k, const void* v, specdec_dtype_t dtype, 
  *                attends to what the row holds, and a token that thereby
  *                attends to nothing gets zeros.
  *   block ids outside [0, num_blocks) read as blocks of zeros.
- *   scale        factor of the scores; 0 selects 1 / sqrt(D).
+ *   scale        factor of the scores, at most 2.3e38; 0 selects 1 / sqrt(D).
  *   workspace    SPECDEC_ATTENTION_WORKSPACE_BYTES, zero-filled once before
  *                its first use; every call leaves it ready for the next.  One
  *                workspace serves one call in flight at a time.  Its first

@@ -2,6 +2,7 @@
 // checks, launch shapes and launches.  The declarations, with the meaning of
 // every argument, are in include/specdec_step.h.
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -333,7 +334,8 @@ extern "C" specdec_status_t spec_attention(const void* q, int64_t q_token_stride
   if (T < 0 || B < 0 || Hq <= 0 || max_blocks <= 0) return SPECDEC_ERR_INVALID_ARG;
   const specdec_status_t chk = check_cache(num_blocks, block_size, H, D);
   if (chk != SPECDEC_OK) return chk;
-  if (Hq % H != 0 || !(scale >= 0.f) || scale > 3e38f) return SPECDEC_ERR_INVALID_ARG;
+  constexpr float kLog2e = 1.4426950408889634f;
+  if (Hq % H != 0 || !(scale >= 0.f) || !(scale * kLog2e <= FLT_MAX)) return SPECDEC_ERR_INVALID_ARG;
   if (B > SPECDEC_MAX_BATCH || static_cast<int64_t>(max_blocks) * block_size + T > INT32_MAX) return SPECDEC_ERR_UNSUPPORTED;
   if (T == 0 || B == 0) return SPECDEC_OK;
   if (q == nullptr || cu_tokens == nullptr || kv_len == nullptr || block_table == nullptr || k_cache == nullptr ||
@@ -362,7 +364,7 @@ extern "C" specdec_status_t spec_attention(const void* q, int64_t q_token_stride
   a.bs_log2 = block_size == 16 ? 4 : block_size == 32 ? 5 : block_size == 64 ? 6 : 7;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  a.scale_log2e = (scale > 0.f ? scale : (D == 64 ? 0.125f : 0.08838834764831845f)) * 1.4426950408889634f;
+  a.scale_log2e = (scale > 0.f ? scale : (D == 64 ? 0.125f : 0.08838834764831845f)) * kLog2e;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   a.err = reinterpret_cast<uint32_t*>(ws);
   a.counters = reinterpret_cast<uint32_t*>(ws + 256);

@@ -172,3 +172,12 @@ def test_attention_refuses_positions_past_32_bits(lib):
     # (the token stride is refused where the sizes are not)
     assert attention(16, (1 << 27) - 1) == 2 and attention(1 << 20, (1 << 27) - 1000) == 2
     assert attention(15, (1 << 27) - 1) == 1
+
+
+def test_attention_refuses_a_scale_whose_product_with_log2_e_overflows(lib):
+    def attention(scale, stride=8):
+        return lib.spec_attention(fake, stride, 5, 1, 1, 64, 1, fake, fake, fake, 8, 100, 16, fake, fake, fake, fake, scale, fake,
+                                  None, 64 << 20, None)
+
+    # (without a workspace the call goes no further)
+    assert attention(2.9e38, 64) == 1 and attention(2.37e38, 64) == 1 and attention(2.3e38, 64) == 3

@@ -278,14 +278,8 @@ __device__ __forceinline__ void warp_arrive(uint64_t& bar, uint32_t n = 1) {
   if ((threadIdx.x & 31) == 0) arrive(bar, n);
 }
 
-// Nearest e4m3 number (|x| at most 448): 4 significant bits, below 2^-6 whole
-// steps of 2^-9, which is the last bit of 1.5 * 2^14.  What is left of a number of
-// 8 bits has 4.
-__device__ __forceinline__ float top4(float x) {
-  constexpr float kFar = 24576.f;
-  return fabsf(x) < 0x1p-6f ? (x + kFar) - kFar : __uint_as_float((__float_as_uint(x) + 0x80000u) & 0xFFF00000u);
-}
-constexpr float kRest = 16.f;  // times the remainder's size (of 448 at most 16: 256)
+// Q's remainder is held so many times its size (of 448 it is at most 16: 256).
+constexpr float kRest = 16.f;
 
 // Byte x of row t in a tile of K or V (rows of D bytes) as the copies swizzle it.
 template <int D>
@@ -774,22 +768,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const bool bad = top >= 0x7F80u;
       const float sc = pow2_scale(__uint_as_float(top << 16)), inv = qr < s.rows && !bad ? pow2_inverse(sc) : 0.f;
       q_scale = bad ? __uint_as_float(0x7FFFFFFFu) : (sc > 0.f ? sc : 1.f);
+      const uint32_t keep = bad ? 0 : 0xFFFFFFFFu;
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
         float f[8];
-        unpack16<__nv_bfloat16>(qv[i], f);
-        uint32_t hw[2], lw[2];
+        unpack16<__nv_bfloat16>(make_uint4(qv[i].x & keep, qv[i].y & keep, qv[i].z & keep, qv[i].w & keep), f);
+        // the nearest codes, and those of what they leave
+        uint32_t hw[2] = {0, 0}, lw[2] = {0, 0};
 #pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-          float u[4], h[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            u[j] = bad ? 0.f : f[e + j] * inv;
-            h[j] = top4(u[j]);
-          }
-          hw[e >> 2] = tc::e4m3x2(h[0], h[1]) | (tc::e4m3x2(h[2], h[3]) << 16);
-          lw[e >> 2] = tc::e4m3x2((u[0] - h[0]) * kRest, (u[1] - h[1]) * kRest) |
-                       (tc::e4m3x2((u[2] - h[2]) * kRest, (u[3] - h[3]) * kRest) << 16);
+        for (int e = 0; e < 4; ++e) {
+          const float u0 = f[2 * e] * inv, u1 = f[2 * e + 1] * inv;
+          const uint32_t h = e4m3_pair(u0, u1);
+          const float2 hf = e4m3_values(h);
+          const uint32_t l = e4m3_pair((u0 - hf.x) * kRest, (u1 - hf.y) * kRest);
+          hw[e >> 1] |= h << 16 * (e & 1);
+          lw[e >> 1] |= l << 16 * (e & 1);
         }
         qv[i] = make_uint4(hw[0], hw[1], lw[0], lw[1]);
       }

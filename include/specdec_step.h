@@ -106,7 +106,9 @@ specdec_status_t kv_block_step(int32_t B, int32_t block_size, int32_t max_blocks
  *              skipped.
  * Neighbouring tokens in neighbouring slots of one block form a run; blocks
  * fill from their start, so the tokens before a run's first are the block's
- * older ones.  (No two runs of a call may share a block.)  Per run and head
+ * older ones.  (No two runs of a call may share a block: tokens that are skipped
+ * between others of a block make two runs of it, which write its scale both, and
+ * what it holds then has no meaning.)  Per run and head
  * the scale is the least power of two that brings the largest magnitude
  * within 448, the type's largest number, and at least the block's scale where
  * it has older tokens, whose codes are then rescaled; 0 when all that is finite
@@ -148,9 +150,10 @@ specdec_status_t kv_append(const void* k, const void* v, specdec_dtype_t dtype, 
  *                meaning and the workspace has to be zero-filled again.
  * Scores, their maxima and sums and the output's sums are held in 32 bits;
  * keys and values are taken as they are in the cache, queries to 2^-21 of a
- * row's largest.  Probabilities enter the second product in f16, 64 times
- * their size over a reference (a score that later ones pass by 2^9 at most):
- * 11 significant bits down to 2^-20 of it, nothing below 2^-31.
+ * row's largest.  Probabilities enter the second product in f16, times their
+ * block's value scale over the largest that the request's tiles have had, and
+ * 64 times their size over a reference (a score that later ones pass by 2^9 at
+ * most): 11 significant bits down to 2^-20 of it, nothing below 2^-31.
  * SPECDEC_ERR_UNSUPPORTED also where the tiles of 128 positions, over heads
  * and groups of 64 rows, could pass some 400 million, or where
  * max_blocks * block_size + T passes 2^31 - 1.
@@ -166,7 +169,8 @@ specdec_status_t spec_attention(const void* q, int64_t q_token_stride, int32_t T
 /*
  * spec_process_logits — penalties, biases and grammar masks.
  *
- *   logits, out   [B, n_max+1, V] of dtype, contiguous; out may be logits.
+ *   logits, out   [B, n_max+1, V] of dtype, contiguous; out may be logits (with
+ *                 long histories a call in place takes longer).
  *                 Rows j > draft_len[b] are neither read nor written.
  *   history       [B, history_stride] int32: a request's prompt, then the
  *                 tokens made so far; prompt_len [B] and history_len [B] say
@@ -182,8 +186,9 @@ specdec_status_t spec_attention(const void* q, int64_t q_token_stride, int32_t T
  *                 allows token v.  mask_rows [B, n_max+1] names each row's
  *                 mask, -1 for none.  NULL: none.
  * history_stride stays below 2^29.
- * After SPECDEC_DEV_ERR_TIMEOUT in the error word (a device wait ran out) the
- * rows that the call writes have no meaning; nothing else is touched.
+ * After SPECDEC_DEV_ERR_TIMEOUT in the error word (a device wait ran out; not
+ * known without an error word) the rows that the call writes have no meaning;
+ * nothing else is touched.
  * For token v of row j, with c = times it was made (drafts before j among
  * them), in 32 bits and rounded once:
  *   l = logit; made or in the prompt: l > 0 ? l / repetition : l * repetition;

@@ -4,8 +4,9 @@
 //
 // The list is cut by cost: a tile costs 4 to 6 units by its rows' 16s, and an
 // item (a row group of a head) kItemCost more, half before and half after its
-// tiles.  (Measured: 0.64, 0.72 and 0.98 us a tile of 16, 32 and 48 rows of
-// D = 128, 2 us an item.)  A cut within an item falls between tiles; one near
+// tiles.  (Measured when the costs were set: 0.64, 0.72 and 0.98 us a tile of
+// 16, 32 and 48 rows of D = 128, 2 us an item; a tile takes 0.67, 0.74 and 1.09
+// now.)  A cut within an item falls between tiles; one near
 // its start or end moves there, so the CTAs at an item's ends may have units of
 // it and no tile: as many as two at its start, since its first tile ends at
 // kItemCost / 2 + 6 units and a CTA's part may be kLeastCost.  (An item's cost

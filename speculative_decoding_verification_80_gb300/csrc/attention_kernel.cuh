@@ -21,8 +21,9 @@
 // tile takes most, are the next limit after HBM.
 //
 // Second product: f16 x f16.  An e4m3 V is exact in f16, and one group of
-// warps turns V's tiles over while the softmax is at work; P in f16 has 11
-// bits down to 2^-20 of its reference and 2^-31 of it is lost.  (P as two e4m3
+// warps turns V's tiles over while the softmax is at work; P, times its block's
+// value scale over the largest met so far, in f16 has 11 bits down to 2^-20 of
+// its reference and 2^-31 of it is lost.  (P as two e4m3
 // numbers needs no such step, but loses what is below 2^-22 of the largest,
 // which a faint tail after one strong position is, and costs twice the
 // arithmetic a probability.)
@@ -43,14 +44,15 @@
 // CTA that finishes last, in the order of the parts.
 //
 // Bound by the cache's bytes while a part lasts: a tile of D = 128 is 32 KB, of
-// which an SM's share of HBM brings one in 0.74 us, and takes 0.77 us at 16
-// rows, 0.89 at 32 and 1.27 at 64, where the softmax is next.
+// which an SM's share of a copy's rate brings one in 0.74 us, and takes 0.67 us
+// at 16 rows and 0.74 at 32; from 33 to 48 rows it takes 1.09 us and 1.14 at 64,
+// from HBM or L2 alike: there the softmax is next.
 // From one (request, head) to the next some 7 us pass in which the next first
 // tile's search, the last products and O's way out are only partly covered;
 // that is what keeps many short parts from HBM's rate.  Measured: 64 requests
-// of 5 tokens over 8000 positions (598 MB) 150 us, 4.0 TB/s; one of 2 over
-// 131000 (269 MB) 60 us, 4.4 TB/s; 256 of up to 8 over 4000 (1208 MB) 274 us,
-// 4.4 TB/s; 32 of one over 18000 (665 MB) 116 us, 5.8 TB/s; one of one over
+// of up to 5 tokens over up to 8000 positions (598 MB) 149 us, 4.0 TB/s; one of 2
+// over 131000 (269 MB) 61 us, 4.4 TB/s; 256 of up to 8 over up to 4000 (1208 MB)
+// 275 us, 4.4 TB/s; 32 of one over 18000 (665 MB) 116 us, 5.8 TB/s; one of one over
 // 700 14 us.
 #pragma once
 #include <cuda_bf16.h>

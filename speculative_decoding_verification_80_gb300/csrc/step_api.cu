@@ -372,8 +372,9 @@ extern "C" specdec_status_t spec_attention(const void* q, int64_t q_token_stride
   // Rows of a group.  Few leave shared memory to the tiles on their way (8
   // tiles of K and V of D = 128 with 16 rows, 7 with 32, 6 with 64); a request
   // of more rows is read once for each of its groups.  How the tokens lie is
-  // known on the device only: as many for each request where that is possible,
-  // or evenly spread, with the longest near twice the mean.  (128 requests of
+  // known on the device only, and this guess is about speed alone: as many for
+  // each request where that is possible (which may still not be so), else evenly
+  // spread, with the longest near twice the mean.  (128 requests of
   // one token over 4500: 141 us with 16 rows, 147 with 64; 256 of up to 32 rows:
   // 285 with 32, 287 with 64.)
   const int64_t rows = static_cast<int64_t>(T) * (Hq / H), likely = T % B == 0 ? rows / B : 7 * rows / (4 * B);

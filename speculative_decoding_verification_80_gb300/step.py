@@ -183,7 +183,9 @@ def spec_attention(q: torch.Tensor, cu_tokens: torch.Tensor, kv_len: torch.Tenso
                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Attention of the new tokens' queries [T, Hq, D] (bf16) over the cache,
     causal among the new tokens (see include/specdec_step.h).  `scale`
-    defaults to 1 / sqrt(D).  Returns [T, Hq, D] bf16."""
+    defaults to 1 / sqrt(D).  Without a workspace the call makes one, 64 MB
+    filled with zeros every time: a loop keeps one of its own
+    (new_attention_workspace).  Returns [T, Hq, D] bf16."""
     dev = _device(q, stream)
     blocks, H, bs, D, cache = _cache(k_cache, v_cache, k_scale, v_scale, dev)
     if q.dim() != 3 or q.shape[2] != D or q.dtype is not BF16:

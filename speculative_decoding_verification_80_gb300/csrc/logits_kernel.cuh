@@ -18,9 +18,10 @@
 // In place, a row without a mask is not copied: its entries are changed where
 // they lie, which pays while few are (64 requests with histories of up to 2048
 // ids: 30 us without masks; 256 with up to 8192, so that one entry in 18 has a
-// sector read and written for it: 450 us, where copies take 200).  Bound by the rows' bytes, read and written once.  (With an item's
-// steps one after the other, the copies' and the history's latencies took twice
-// the time, however many CTAs an SM had.)  Measured: 64 requests of up to 5
+// sector read and written for it: 450 us, where copies take 200).  Bound by the
+// rows' bytes, read and written once.  (With an item's steps one after the other,
+// the copies' and the history's latencies took twice the time, however many CTAs
+// an SM had.)  Measured: 64 requests of up to 5
 // rows of 128256 bf16 (132 MB) 35 us, 3.8 TB/s; 256 of up to 8 rows of 152064
 // (980 MB) 200 us, 4.9 TB/s, of which the copies alone are 166 us.  Rows of 8
 // KB in a ring of 12 take 53 and 309 us, and equal parts of all rows in their

@@ -10,7 +10,14 @@
  *   spec_attention       attention of the new tokens (one of a decode step,
  *                        n + 1 of a verify step, a prompt's) over that cache;
  *   spec_process_logits  penalties for repeated tokens, biases and grammar
- *                        masks on the rows that spec_verify reads.
+ *                        masks on the rows that spec_verify reads;
+ *   spec_sample          tokens drawn with temperature, top-k, top-p and min-p
+ *                        from given random numbers, and the rows cut to what
+ *                        may be drawn, as spec_verify reads them;
+ *   spec_rotary          rotary positions of queries and keys;
+ *   kv_fork, kv_compact  requests that go on from others' tokens, and the blocks
+ *                        in use moved to the lowest ids: tables, holders, ring;
+ *   kv_copy              the copies of blocks that both ask for.
  *
  * "Accelerating Sonar through speculation" (Perplexity Research, 2025) names
  * their places in the loop: §Inference with speculative decoding (KV pages
@@ -51,6 +58,10 @@ extern "C" {
                                        a length out of range (clamped), or a
                                        row's mask outside [-1, mask_count) (the
                                        row is not masked) */
+#define SPECDEC_DEV_ERR_SAMPLE 128u /* spec_sample: a top-p below 0, a min-p outside
+                                       [0, 1] or a random number outside [0, 1)
+                                       (clamped; NaN as 1, 0 and 0), or a row
+                                       without a number above -infinity */
 
 /*
  * kv_block_step — block tables and slot maps from request lengths.
@@ -203,6 +214,150 @@ specdec_status_t spec_process_logits(const void* logits, void* out, specdec_dtyp
                                      const float* bias_values, int32_t num_bias, const uint32_t* mask,
                                      int32_t mask_count, const int32_t* mask_rows, uint32_t* error_word,
                                      void* stream);
+
+/*
+ * spec_sample — truncated sampling: the draft's tokens, and rows for spec_verify.
+ *
+ *   logits        [B, n_max+1, V] of dtype, contiguous.  NaN counts as -infinity.
+ *   out           as logits, may be logits, or NULL: the rows with -infinity for
+ *                 every id that is not kept.  (A verify step wants the draft's
+ *                 rows and the target's cut alike.)
+ *   draft_len     [B] or NULL (n_max): rows j > draft_len[b] are neither read nor
+ *                 written, and their tokens are -1.
+ *   temperature   [B] float or NULL (1): 0, or what spec_verify takes as 0 (above
+ *                 3e38 too; SPECDEC_DEV_ERR_TEMPERATURE), keeps the largest logit
+ *                 alone.
+ *   top_k         [B] int32 or NULL: 0 and below, and V and above, keep all.
+ *   top_p, min_p  [B] float or NULL (1 and above, 0: keep all).
+ *   uniform       [B, n_max+1] float in [0, 1), and
+ *   tokens        [B, n_max+1] int32: a token drawn of each row; both or neither.
+ * Per row, with weights w = exp((logit - largest) / temperature) and the ids in
+ * order of their logits, the largest first and equal ones by id: kept are the
+ * first top_k; of those the shortest beginning whose weights sum to at least
+ * top_p times that of all of them (one id at least); of those the ids with
+ * w >= min_p.  The token is the first of the kept, in this order, up to which the
+ * weights sum to more than uniform times that of all kept.  A row without a
+ * number above -infinity gives -1 and keeps nothing; infinite logits are equal,
+ * and the others count as -infinity beside them.
+ * Weights are whole numbers of 2^-45 of the largest, within 2^-40 of their value,
+ * and all sums are exact.
+ */
+specdec_status_t spec_sample(const void* logits, void* out, specdec_dtype_t dtype, int32_t B, int32_t n_max, int32_t V,
+                             const int32_t* draft_len, const float* temperature, const int32_t* top_k,
+                             const float* top_p, const float* min_p, const float* uniform, int32_t* tokens,
+                             uint32_t* error_word, void* stream);
+
+/*
+ * spec_rotary — rotary positions of the new tokens' queries and keys.
+ *
+ *   q, k          [T, Hq, D] and [T, H, D] of dtype; token t's head h starts at
+ *                 t * token_stride + h * head_stride elements, its D values are
+ *                 contiguous.  Hq or H may be 0 (their pointers are not looked at).
+ *   q_out, k_out  the same, with strides of their own; the inputs themselves with
+ *                 their strides, or memory that no input shares.
+ *   positions     [T] int32, as kv_block_step lists them; rows of tokens with
+ *                 negative ones are left as they were.
+ *   turns         [rotary_dim / 2]: what pair i turns by a position, in 2^-64 of a
+ *                 whole turn (frequency / 2 pi * 2^64, rounded).
+ *   rotary_dim    values of a head that are turned, its first ones; even.  The
+ *                 others are as they were (copied to other outputs).
+ *   interleaved   0: values i and i + rotary_dim / 2 are a pair; 1: 2 i and 2 i + 1.
+ *   factor        of the turned values, positive.
+ * A pair (a, b) becomes factor * (a cos - b sin, a sin + b cos) in 32 bits, rounded
+ * once.  The angle is position * turns[i] in whole numbers: at any position its
+ * sine and cosine are within 2^-21.  D is at most 1024.
+ */
+specdec_status_t spec_rotary(const void* q, const void* k, specdec_dtype_t dtype, int32_t T, int32_t Hq, int32_t H,
+                             int32_t D, int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                             int64_t k_head_stride, const int32_t* positions, const uint64_t* turns,
+                             int32_t rotary_dim, int32_t interleaved, float factor, void* q_out,
+                             int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out,
+                             int64_t k_out_token_stride, int64_t k_out_head_stride, void* stream);
+
+/*
+ * Holders of a block: shares [num_blocks] int32 says how many requests, or other
+ * users of the cache, hold a block beside the first.  kv_block_step knows nothing
+ * of it: what it hands out has one holder and shares 0.  It gives back whatever it
+ * takes from a request, so requests that hold shared blocks are ended, or cut back
+ * into them, by kv_fork.  Nor does it or kv_append look whether a block that is
+ * written has other holders: after kv_fork none has.
+ *
+ * The workspace of kv_fork and kv_compact: specdec_page_workspace_bytes(num_blocks)
+ * bytes, zero-filled once before its first use; every call leaves it ready for the
+ * next.  One workspace serves one call in flight at a time.
+ */
+size_t specdec_page_workspace_bytes(int32_t num_blocks);
+
+/*
+ * kv_fork — requests that go on from the tokens of others: several continuations of
+ * a prompt, beams that choose their parents anew, a step back, an end.
+ *
+ * Inputs (device int32):
+ *   block_table [P, max_blocks], held [P], kv_len [P], accepted_len [P] or NULL: the
+ *                 old requests, as kv_block_step leaves them; request p has
+ *                 kv_len[p] + accepted_len[p] + 1 tokens (NULL: kv_len[p]).
+ *   parent      [B]: the old request that new request b goes on from, -1 for none
+ *                 (it has no tokens).  An old request without children ends.
+ *   keep        [B] or NULL: tokens of the parent's that b keeps, at most (below 0: 0).
+ *   shares, free_ring, ring_state  as above and as for kv_block_step.
+ * New request b names its parent's first ceil(t / block_size) blocks for its t
+ * tokens.  A request whose last block is part-filled will write it: where others
+ * hold that block too, it takes a block of its own from the ring's head, in request
+ * order, and asks for a copy; where all its holders are such requests the last one
+ * keeps it.  Without blocks left, the request keeps its full blocks' tokens only and
+ * SPECDEC_DEV_ERR_BLOCKS is set.  Blocks that no one holds any more go to the ring's
+ * tail in order of their ids.
+ * Outputs (device int32):
+ *   table_out [B, max_blocks] (-1 past a request's blocks), held_out [B],
+ *   kv_len_out [B]: tokens (a next kv_block_step has no accepted_len, or -1);
+ *   shares_out [num_blocks], ring_state_out [2]; free_ring's tail in place;
+ *   copies [B, 2] and count [1]: for kv_copy, from and to; those past count have no
+ *                 meaning.
+ * shares_out and ring_state_out may be the inputs; the tables, kv_len and held may
+ * not.  Out of range: a parent is none, a length is clamped to what is held, held to
+ * the table's width, a block id is left where it is; each sets SPECDEC_DEV_ERR_BLOCKS.
+ */
+specdec_status_t kv_fork(int32_t P, int32_t B, int32_t block_size, int32_t max_blocks, int32_t num_blocks,
+                         const int32_t* block_table, const int32_t* kv_len, const int32_t* accepted_len,
+                         const int32_t* held, const int32_t* parent, const int32_t* keep, const int32_t* shares,
+                         int32_t* free_ring, const int32_t* ring_state, int32_t* table_out, int32_t* kv_len_out,
+                         int32_t* held_out, int32_t* shares_out, int32_t* ring_state_out, int32_t* copies,
+                         int32_t* count, void* workspace, size_t workspace_bytes, uint32_t* error_word, void* stream);
+
+/*
+ * kv_compact — blocks in use to the lowest ids, so that the cache's end is free.
+ *
+ * Blocks in use are those that the ring does not list; with n of them, the i-th in
+ * use from id n on, in order, moves to the i-th free one before n.  The ring then
+ * lists n .. num_blocks - 1 from its start.
+ * Outputs (device int32), each may be its input:
+ *   table_out [B, max_blocks] (-1 past held), shares_out [num_blocks],
+ *   ring_out [num_blocks] (what is behind its free ids is left), ring_state_out [2];
+ *   renamed [num_blocks]: a block's new id, -1 for a free one, for other holders;
+ *   copies [num_blocks / 2, 2] and count [1]: for kv_copy.
+ * An entry that names no block, or a free one, becomes -1 and sets
+ * SPECDEC_DEV_ERR_BLOCKS, as do ids of the ring out of range, which are passed over.
+ */
+specdec_status_t kv_compact(int32_t B, int32_t max_blocks, int32_t num_blocks, const int32_t* block_table,
+                            const int32_t* held, const int32_t* shares, const int32_t* free_ring,
+                            const int32_t* ring_state, int32_t* table_out, int32_t* shares_out, int32_t* ring_out,
+                            int32_t* ring_state_out, int32_t* renamed, int32_t* copies, int32_t* count,
+                            void* workspace, size_t workspace_bytes, uint32_t* error_word, void* stream);
+
+/*
+ * kv_copy — copies of blocks, codes and scales, in every layer's cache.
+ *
+ *   copies   [capacity, 2] int32: from and to; count [1] int32 on the device says how
+ *            many of them hold (at most capacity).  No block is written twice, or
+ *            both read and written.  Ids out of range, and a block onto itself, are
+ *            passed over.
+ *   caches   host array of 4 * layers device pointers, a layer's k_cache, v_cache
+ *            (16-byte aligned), k_scale and v_scale in turn; it is read in the call.
+ * A launch for every 64 layers.
+ */
+specdec_status_t kv_copy(const int32_t* copies, const int32_t* count, int32_t capacity, int32_t layers,
+                         void* const* caches, int32_t num_blocks, int32_t block_size, int32_t H, int32_t D,
+                         void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,7 +1,7 @@
 """GB300 speculative-decoding verify/accept and MTP shift/insert.
 
 A thin ctypes binding over libspecdec.so (include/specdec.h; the operators
-around the verify step, include/specdec_step.h, are in step.py).  The functions
+around the verify step, include/specdec_step.h, are in step.py and pages.py).  The functions
 keep the C names; they only marshal torch tensors into device pointers, sizes
 and the current CUDA stream.  Every step of the computation runs in the
 library's kernels; there is no fallback: if the library is missing or no GPU
@@ -22,7 +22,9 @@ __all__ = [
     "spec_verify_shard_rank", "ShardOps", "shard_exchange_buffers", "bytes_read", "mtp_shift_insert", "get_error", "launch_shape", "F32", "BF16",
     "DEV_ERR_TOKEN", "DEV_ERR_DRAFT_LEN", "DEV_ERR_TEMPERATURE", "DEV_ERR_TIMEOUT", "DEV_ERR_SEGMENT",
     "kv_block_step", "BlockStep", "kv_append", "spec_attention", "new_attention_workspace", "spec_process_logits",
-    "DEV_ERR_BLOCKS", "DEV_ERR_PENALTY", "ATTENTION_WORKSPACE_BYTES",
+    "spec_sample", "spec_rotary", "rotary_turns", "rotary_frequencies",
+    "kv_fork", "Fork", "kv_compact", "Compaction", "kv_copy", "kv_layers", "KvLayers", "new_page_workspace", "page_workspace_bytes",
+    "DEV_ERR_BLOCKS", "DEV_ERR_PENALTY", "DEV_ERR_SAMPLE", "ATTENTION_WORKSPACE_BYTES",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -563,5 +565,8 @@ def get_error(workspace: torch.Tensor) -> int:
     return bits.value
 
 
-from .step import (ATTENTION_WORKSPACE_BYTES, DEV_ERR_BLOCKS, DEV_ERR_PENALTY, BlockStep, kv_append,  # noqa: E402
-                   kv_block_step, new_attention_workspace, spec_attention, spec_process_logits)
+from .step import (ATTENTION_WORKSPACE_BYTES, DEV_ERR_BLOCKS, DEV_ERR_PENALTY, DEV_ERR_SAMPLE, BlockStep,  # noqa: E402
+                   kv_append, kv_block_step, new_attention_workspace, rotary_frequencies, rotary_turns, spec_attention,
+                   spec_process_logits, spec_rotary, spec_sample)
+from .pages import (Compaction, Fork, KvLayers, kv_compact, kv_copy, kv_fork, kv_layers,  # noqa: E402
+                    new_page_workspace, page_workspace_bytes)

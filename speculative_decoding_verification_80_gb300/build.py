@@ -65,7 +65,9 @@ def verify_digest() -> str:
     """Digest of the sources the verify kernel is built from."""
     return source_digest(skip=("mtp_kernel.cuh", "shard_kernels.cuh", "shard_api.cu", "specdec_shard.h", "step_api.cu",
                                "attention_cut.cuh", "attention_kernel.cuh", "kv_kernels.cuh", "logits_kernel.cuh",
-                               "tcgen05.cuh", "waits.cuh", "specdec_step.h"))
+                               "tcgen05.cuh", "waits.cuh", "specdec_step.h", "host_checks.cuh", "sample_api.cu",
+                               "sample_kernel.cuh", "sample_weight.cuh", "rotary_kernel.cuh", "pages_api.cu",
+                               "page_kernels.cuh", "block_prefix.cuh"))
 
 
 def _up_to_date() -> bool:

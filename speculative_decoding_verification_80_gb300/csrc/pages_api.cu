@@ -1,0 +1,186 @@
+// pages_api.cu — the C ABI of the paged cache's forks, moves and copies: argument
+// checks, launch shapes and launches.  The declarations, with the meaning of every
+// argument, are in include/specdec_step.h.
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "specdec_step.h"
+
+#include "host_checks.cuh"
+#include "page_kernels.cuh"
+
+namespace specdec {
+namespace {
+
+size_t page_words(int64_t N) { return static_cast<size_t>(5 * N + 2 * ((N + 31) / 32) + SPECDEC_MAX_BATCH + 2); }
+
+PageWork page_work(void* workspace, int64_t N) {
+  uint32_t* at = static_cast<uint32_t*>(workspace);
+  const int64_t words = (N + 31) / 32;
+  PageWork w;
+  w.olds = at;
+  w.news = w.olds + N;
+  w.writers = w.news + N;
+  w.last = w.writers + N;
+  w.marks = w.last + N;
+  w.gone = w.marks + words;
+  w.rank = reinterpret_cast<int32_t*>(w.gone + words);
+  w.number = w.rank + N;
+  w.ring = w.number + SPECDEC_MAX_BATCH;
+  return w;
+}
+
+specdec_status_t check_workspace(const void* workspace, size_t bytes, int64_t N) {
+  return workspace == nullptr || !aligned(workspace, 16) || bytes < page_words(N) * 4 ? SPECDEC_ERR_WORKSPACE : SPECDEC_OK;
+}
+
+// CTAs for some number of items at so many a CTA.
+unsigned ctas_for(int64_t items, int64_t each) {
+  const int64_t n = (items + each - 1) / each;
+  return static_cast<unsigned>(n < 1 ? 1 : (n > kPageCtas ? kPageCtas : n));
+}
+
+}  // namespace
+}  // namespace specdec
+
+using namespace specdec;
+
+extern "C" size_t specdec_page_workspace_bytes(int32_t num_blocks) { return num_blocks > 0 ? page_words(num_blocks) * 4 : 0; }
+
+extern "C" specdec_status_t kv_fork(int32_t P, int32_t B, int32_t block_size, int32_t max_blocks, int32_t num_blocks,
+                                    const int32_t* block_table, const int32_t* kv_len, const int32_t* accepted_len,
+                                    const int32_t* held, const int32_t* parent, const int32_t* keep,
+                                    const int32_t* shares, int32_t* free_ring, const int32_t* ring_state,
+                                    int32_t* table_out, int32_t* kv_len_out, int32_t* held_out, int32_t* shares_out,
+                                    int32_t* ring_state_out, int32_t* copies, int32_t* count, void* workspace,
+                                    size_t workspace_bytes, uint32_t* error_word, void* stream) {
+  if (P < 0 || B < 0 || block_size <= 0 || max_blocks <= 0 || num_blocks <= 0) return SPECDEC_ERR_INVALID_ARG;
+  if (!block_size_ok(block_size) || P > SPECDEC_MAX_BATCH || B > SPECDEC_MAX_BATCH) return SPECDEC_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_blocks) * block_size > INT32_MAX || static_cast<int64_t>(max_blocks) * block_size > INT32_MAX)
+    return SPECDEC_ERR_UNSUPPORTED;
+  if (shares == nullptr || free_ring == nullptr || ring_state == nullptr || shares_out == nullptr || ring_state_out == nullptr ||
+      count == nullptr)
+    return SPECDEC_ERR_INVALID_ARG;
+  if (P > 0 && (block_table == nullptr || kv_len == nullptr || held == nullptr)) return SPECDEC_ERR_INVALID_ARG;
+  if (B > 0 && (parent == nullptr || table_out == nullptr || kv_len_out == nullptr || held_out == nullptr || copies == nullptr))
+    return SPECDEC_ERR_INVALID_ARG;
+  // a request reads its parent's numbers, which another may replace
+  if ((P > 0 && B > 0 && (table_out == block_table || kv_len_out == kv_len || held_out == held)) || (B > 0 && kv_len_out == accepted_len))
+    return SPECDEC_ERR_INVALID_ARG;
+  const specdec_status_t ws = check_workspace(workspace, workspace_bytes, num_blocks);
+  if (ws != SPECDEC_OK) return ws;
+  ForkArgs a;
+  memset(&a, 0, sizeof a);
+  a.P = P;
+  a.B = B;
+  a.bs_log2 = block_size == 16 ? 4 : block_size == 32 ? 5 : block_size == 64 ? 6 : 7;
+  a.max_blocks = max_blocks;
+  a.num_blocks = num_blocks;
+  a.table = block_table;
+  a.kv_len = kv_len;
+  a.accepted_len = accepted_len;
+  a.held = held;
+  a.parent = parent;
+  a.keep = keep;
+  a.shares = shares;
+  a.ring = free_ring;
+  a.ring_state = ring_state;
+  a.table_out = table_out;
+  a.kv_len_out = kv_len_out;
+  a.held_out = held_out;
+  a.shares_out = shares_out;
+  a.ring_state_out = ring_state_out;
+  a.copies = copies;
+  a.count = count;
+  a.err = error_word;
+  a.work = page_work(workspace, num_blocks);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  constexpr int kWarps = kPageThreads / 32;
+  fork_count_kernel<<<ctas_for(static_cast<int64_t>(P) + B, kWarps), kPageThreads, 0, st>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
+  fork_plan_kernel<<<1 + ctas_for(num_blocks, kBlockThreads), kBlockThreads, 0, st>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
+  const unsigned block_ctas = ctas_for(num_blocks, 4 * kPageThreads);
+  fork_finish_kernel<<<block_ctas + ctas_for(B, kWarps), kPageThreads, 0, st>>>(a, static_cast<int>(block_ctas));
+  return launched();
+}
+
+extern "C" specdec_status_t kv_compact(int32_t B, int32_t max_blocks, int32_t num_blocks, const int32_t* block_table,
+                                       const int32_t* held, const int32_t* shares, const int32_t* free_ring,
+                                       const int32_t* ring_state, int32_t* table_out, int32_t* shares_out,
+                                       int32_t* ring_out, int32_t* ring_state_out, int32_t* renamed, int32_t* copies,
+                                       int32_t* count, void* workspace, size_t workspace_bytes, uint32_t* error_word,
+                                       void* stream) {
+  if (B < 0 || max_blocks <= 0 || num_blocks <= 0) return SPECDEC_ERR_INVALID_ARG;
+  if (B > SPECDEC_MAX_BATCH || num_blocks > (1 << 27)) return SPECDEC_ERR_UNSUPPORTED;
+  if (shares == nullptr || free_ring == nullptr || ring_state == nullptr || shares_out == nullptr || ring_out == nullptr ||
+      ring_state_out == nullptr || renamed == nullptr || copies == nullptr || count == nullptr)
+    return SPECDEC_ERR_INVALID_ARG;
+  if (B > 0 && (block_table == nullptr || held == nullptr || table_out == nullptr)) return SPECDEC_ERR_INVALID_ARG;
+  const specdec_status_t ws = check_workspace(workspace, workspace_bytes, num_blocks);
+  if (ws != SPECDEC_OK) return ws;
+  CompactArgs a;
+  memset(&a, 0, sizeof a);
+  a.B = B;
+  a.max_blocks = max_blocks;
+  a.num_blocks = num_blocks;
+  a.table = block_table;
+  a.held = held;
+  a.shares = shares;
+  a.ring = free_ring;
+  a.ring_state = ring_state;
+  a.table_out = table_out;
+  a.shares_out = shares_out;
+  a.ring_out = ring_out;
+  a.ring_state_out = ring_state_out;
+  a.renamed = renamed;
+  a.copies = copies;
+  a.count = count;
+  a.err = error_word;
+  a.work = page_work(workspace, num_blocks);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  compact_mark_kernel<<<ctas_for(num_blocks, kPageThreads), kPageThreads, 0, st>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
+  compact_plan_kernel<<<ctas_for(num_blocks, 4 * kPageThreads), kPageThreads, 0, st>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
+  const unsigned block_ctas = ctas_for(num_blocks, kPageThreads);
+  compact_finish_kernel<<<block_ctas + ctas_for(B, kPageThreads / 32), kPageThreads, 0, st>>>(a, static_cast<int>(block_ctas));
+  return launched();
+}
+
+extern "C" specdec_status_t kv_copy(const int32_t* copies, const int32_t* count, int32_t capacity, int32_t layers,
+                                    void* const* caches, int32_t num_blocks, int32_t block_size, int32_t H, int32_t D,
+                                    void* stream) {
+  if (capacity < 0 || layers < 0 || num_blocks <= 0 || block_size <= 0 || H <= 0 || D <= 0) return SPECDEC_ERR_INVALID_ARG;
+  if (!block_size_ok(block_size) || (D != 64 && D != 128) || H > 65535 || static_cast<int64_t>(num_blocks) * block_size > INT32_MAX)
+    return SPECDEC_ERR_UNSUPPORTED;
+  if (capacity == 0 || layers == 0) return SPECDEC_OK;
+  if (copies == nullptr || count == nullptr || caches == nullptr) return SPECDEC_ERR_INVALID_ARG;
+  for (int64_t i = 0; i < 4LL * layers; ++i)
+    if (caches[i] == nullptr || !aligned(caches[i], i % 4 < 2 ? 16 : 4)) return SPECDEC_ERR_INVALID_ARG;
+  int dev = 0, sms = 0;
+  if (device_sms(&dev, &sms) != cudaSuccess) return SPECDEC_ERR_CUDA;
+  CopyArgs a;
+  a.capacity = capacity;
+  a.num_blocks = num_blocks;
+  a.H = H;
+  a.bytes = static_cast<int64_t>(H) * block_size * D;
+  a.chunk = static_cast<int32_t>(a.bytes < 4096 ? a.bytes : 4096);
+  a.chunks = static_cast<int32_t>((a.bytes + a.chunk - 1) / a.chunk);
+  a.pairs = copies;
+  a.count = count;
+  for (int32_t l0 = 0; l0 < layers; l0 += kCopyLayers) {
+    a.layers = layers - l0 < kCopyLayers ? layers - l0 : kCopyLayers;
+    for (int l = 0; l < a.layers; ++l) {
+      void* const* c = caches + 4LL * (l0 + l);
+      a.layer[l] = {c[0], c[1], static_cast<float*>(c[2]), static_cast<float*>(c[3])};
+    }
+    // as many warps as there can be parts, at most eight CTAs an SM
+    const int64_t parts = static_cast<int64_t>(capacity) * a.layers * 2 * a.chunks;
+    const int64_t ctas = (parts + kPageThreads / 32 - 1) / (kPageThreads / 32);
+    copy_kernel<<<static_cast<unsigned>(ctas < 8 * sms ? ctas : 8 * sms), kPageThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
+  }
+  return SPECDEC_OK;
+}

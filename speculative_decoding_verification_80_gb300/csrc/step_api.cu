@@ -9,28 +9,12 @@
 #include "specdec_step.h"
 
 #include "attention_kernel.cuh"
+#include "host_checks.cuh"
 #include "kv_kernels.cuh"
 #include "logits_kernel.cuh"
 
 namespace specdec {
 namespace {
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-specdec_status_t launched() { return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA; }
-
-bool block_size_ok(int32_t bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128; }
-
-// Whether p is memory that the CUDA runtime gave out (false without a device).
-bool on_device(const void* p) {
-  cudaPointerAttributes at;
-  if (p == nullptr) return false;
-  if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
-  return at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged;
-}
 
 // The cache's shape: INVALID_ARG, UNSUPPORTED or OK.
 specdec_status_t check_cache(int32_t num_blocks, int32_t block_size, int32_t H, int32_t D) {
@@ -38,22 +22,6 @@ specdec_status_t check_cache(int32_t num_blocks, int32_t block_size, int32_t H, 
   if (!block_size_ok(block_size) || (D != 64 && D != 128)) return SPECDEC_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(num_blocks) * block_size > INT32_MAX || H > 65535) return SPECDEC_ERR_UNSUPPORTED;
   return SPECDEC_OK;
-}
-
-// SMs of the current device, which is asked once.
-cudaError_t device_sms(int* dev, int* sms) {
-  static int known[64] = {0};
-  cudaError_t e = cudaGetDevice(dev);
-  if (e != cudaSuccess) return e;
-  if (*dev < 0 || *dev >= 64) return cudaErrorInvalidDevice;
-  if (known[*dev] == 0) {
-    int n = 0;
-    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev);
-    if (e != cudaSuccess) return e;
-    known[*dev] = n;
-  }
-  *sms = known[*dev];
-  return cudaSuccess;
 }
 
 template <typename Elt>

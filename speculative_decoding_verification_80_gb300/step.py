@@ -1,11 +1,13 @@
 """The operators of a decode step around the verify call (include/specdec_step.h):
-block tables and slot maps, the 8-bit cache's writer, attention over it, and
-logit processing.  As in the rest of the package, the functions keep the C
+block tables and slot maps, the 8-bit cache's writer, attention over it, logit
+processing, sampling and rotary positions (forks and moves of the cache's blocks
+are in pages.py).  As in the rest of the package, the functions keep the C
 names and only marshal tensors: every computation runs in the library's
 kernels, on the current CUDA stream or the one given."""
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import NamedTuple, Optional
 
 import torch
@@ -18,12 +20,13 @@ _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
 I32, F32, BF16 = torch.int32, torch.float32, torch.bfloat16
 
-DEV_ERR_BLOCKS, DEV_ERR_PENALTY = 32, 64
+DEV_ERR_BLOCKS, DEV_ERR_PENALTY, DEV_ERR_SAMPLE = 32, 64, 128
 ATTENTION_WORKSPACE_BYTES = 64 << 20
 E4M3 = torch.float8_e4m3fn
 
 # Every symbol the header declares.
-STEP_EXPORTS = ("kv_block_step", "kv_append", "spec_attention", "spec_process_logits")
+STEP_EXPORTS = ("kv_block_step", "kv_append", "spec_attention", "spec_process_logits", "spec_sample", "spec_rotary",
+                "kv_fork", "kv_compact", "kv_copy")
 
 
 def _device(t: torch.Tensor, stream) -> int:
@@ -82,8 +85,17 @@ def declare(L) -> None:
     L.kv_append.argtypes = [P, P, ci, i32, i32, i32, i64, i64, i64, i64, P, i32, i32, P, P, P, P, P]
     L.spec_attention.argtypes = [P, i64, i32, i32, i32, i32, i32, P, P, P, i32, i32, i32, P, P, P, P, f32, P, P, sz, P]
     L.spec_process_logits.argtypes = [P, P, ci, i32, i32, i32, P, i32, P, P, P, P, P, P, P, P, P, P, i32, P, i32, P, P, P]
+    if hasattr(L, "spec_sample"):
+        L.spec_sample.argtypes = [P, P, ci, i32, i32, i32, P, P, P, P, P, P, P, P, P]
+        L.spec_rotary.argtypes = [P, P, ci, i32, i32, i32, i32, i64, i64, i64, i64, P, P, i32, i32, f32, P, i64, i64, P, i64, i64, P]
+        L.kv_fork.argtypes = [i32] * 5 + [P] * 17 + [sz, P, P]
+        L.kv_compact.argtypes = [i32] * 3 + [P] * 13 + [sz, P, P]
+        L.kv_copy.argtypes = [P, P, i32, i32, P, i32, i32, i32, i32, P]
+        L.specdec_page_workspace_bytes.argtypes = [i32]
+        L.specdec_page_workspace_bytes.restype = sz
     for name in STEP_EXPORTS:
-        getattr(L, name).restype = ci
+        if hasattr(L, name):
+            getattr(L, name).restype = ci
 
 
 def kv_block_step(block_table: torch.Tensor, kv_len: torch.Tensor, held: torch.Tensor, new_tokens: torch.Tensor,
@@ -283,3 +295,157 @@ def spec_process_logits(logits: torch.Tensor, history: Optional[torch.Tensor] = 
                                               *biases, num_bias, words, masks, named, _word(error_word, dev),
                                               _on_stream(stream, dev)), "spec_process_logits")
     return out
+
+
+def spec_sample(logits: torch.Tensor, temperature: Optional[torch.Tensor] = None, top_k: Optional[torch.Tensor] = None,
+                top_p: Optional[torch.Tensor] = None, min_p: Optional[torch.Tensor] = None,
+                uniform: Optional[torch.Tensor] = None, draft_len: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None, tokens: Optional[torch.Tensor] = None,
+                error_word: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Truncated sampling on logits [B, n_max+1, V] (see include/specdec_step.h).
+    With `uniform` [B, n_max+1], random numbers in [0, 1), a token of each row
+    is drawn; with `out` (may be `logits`) the rows are cut to what may be
+    drawn, as spec_verify reads them.  Returns the tokens [B, n_max+1], int32
+    (`tokens` where given), or None without `uniform`."""
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, n_max+1, V]")
+    B, rows, V = logits.shape
+    dev = _device(logits, stream)
+    dtype = logits.dtype
+    at = _at(logits, B * rows * V, "logits", dtype, dev)
+    if out is None:
+        to = None
+    elif out is logits:
+        to = at
+    else:
+        if out.shape != logits.shape or out.dtype != dtype:
+            raise ValueError("out must be of logits' shape and dtype")
+        to = _at(out, B * rows * V, "out", dtype, dev)
+    if uniform is None:
+        if tokens is not None:
+            raise ValueError("tokens need uniform")
+        if out is None:
+            raise ValueError("nothing to do: give uniform, out or both")
+    elif tokens is None:
+        with _on(stream):
+            tokens = torch.empty(B, rows, dtype=I32, device=logits.device)
+    _check(load_library().spec_sample(at, to, _dtype_code(logits), B, rows - 1, V, _at(draft_len, B, "draft_len", I32, dev),
+                                      _at(temperature, B, "temperature", F32, dev), _at(top_k, B, "top_k", I32, dev),
+                                      _at(top_p, B, "top_p", F32, dev), _at(min_p, B, "min_p", F32, dev),
+                                      _at(uniform, B * rows, "uniform", F32, dev), _at(tokens, B * rows, "tokens", I32, dev),
+                                      _word(error_word, dev), _on_stream(stream, dev)), "spec_sample")
+    return tokens
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[dict] = None):
+    """Angles a position of each pair, base^(-2 i / rotary_dim), and the factor
+    of the turned values, as 64-bit floats.  `scaling` is for contexts longer
+    than the training's, by `factor`:
+
+    * ``type="linear"``: all frequencies over the factor;
+    * ``type="ntk"``: the base times factor^(rotary_dim / (rotary_dim - 2));
+    * ``type="yarn"`` (Peng et al., "YaRN", 2023) with `original` tokens of
+      context in training: pairs of more than `fast` (32) turns in it stay, those
+      of less than `slow` (1) are scaled, between is a ramp over the pairs, and the
+      result is scaled by 0.1 ln(factor) + 1 (or `attention`);
+    * ``type="bands"``: pairs of more than `high` turns in `original` tokens stay,
+      those of less than `low` are scaled, between is a ramp over the turns."""
+    if rotary_dim <= 0 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and positive")
+    if not (base > 1 and math.isfinite(base)):
+        raise ValueError("base must be above 1")
+    half = rotary_dim // 2
+    freq = [base ** (-2.0 * i / rotary_dim) for i in range(half)]
+    if scaling is None:
+        return freq, 1.0
+    kind, rest = scaling.get("type"), {k: v for k, v in scaling.items() if k not in ("type", "factor")}
+    by = float(scaling.get("factor", 0.0))
+    if not (by >= 1 and math.isfinite(by)):
+        raise ValueError("scaling needs a factor of at least 1")
+    names = {"linear": (), "ntk": (), "yarn": ("original", "fast", "slow", "attention"), "bands": ("original", "low", "high")}
+    if kind not in names or set(rest) - set(names[kind]):
+        raise ValueError(f"scaling is linear, ntk, yarn or bands with their own values, got {scaling}")
+    if kind == "linear":
+        return [f / by for f in freq], 1.0
+    if kind == "ntk":
+        if rotary_dim == 2:
+            raise ValueError("ntk scaling needs more than one pair")
+        base = base * by ** (rotary_dim / (rotary_dim - 2.0))
+        return [base ** (-2.0 * i / rotary_dim) for i in range(half)], 1.0
+    length = float(rest.get("original", 0.0))
+    if not (length > 0 and math.isfinite(length)):
+        raise ValueError(f"{kind} scaling needs the original context's length")
+    if kind == "yarn":
+        fast, slow = float(rest.get("fast", 32.0)), float(rest.get("slow", 1.0))
+        if not (fast >= slow > 0):
+            raise ValueError("yarn scaling needs fast >= slow > 0")
+        pair = lambda turns: rotary_dim * math.log(length / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))  # noqa: E731
+        low, high = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rotary_dim - 1)
+        ramp = [min(max((i - low) / max(high - low, 1e-3), 0.0), 1.0) for i in range(half)]
+        factor = float(rest.get("attention") or 0.1 * math.log(by) + 1.0)
+        return [f * (1.0 - r) + f / by * r for f, r in zip(freq, ramp)], factor
+    low, high = float(rest.get("low", 1.0)), float(rest.get("high", 4.0))
+    if not (high > low > 0):
+        raise ValueError("bands scaling needs high > low > 0")
+    keep = [min(max((length * f / (2.0 * math.pi) - low) / (high - low), 0.0), 1.0) for f in freq]
+    return [f * r + f / by * (1.0 - r) for f, r in zip(freq, keep)], 1.0
+
+
+def rotary_turns(rotary_dim: int, base: float = 10000.0, scaling: Optional[dict] = None, device=None):
+    """What spec_rotary takes, made once for a model: `turns` [rotary_dim / 2]
+    int64, each pair's frequency (see rotary_frequencies) in 2^-64 of a turn a
+    position, and the factor."""
+    freq, factor = rotary_frequencies(rotary_dim, base, scaling)
+    words = [round(f / (2.0 * math.pi) * 2.0 ** 64) & ((1 << 64) - 1) for f in freq]
+    turns = torch.tensor([w - (1 << 64) if w >> 63 else w for w in words], dtype=torch.int64)
+    return turns.to(device or "cuda"), factor
+
+
+def spec_rotary(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.Tensor, turns: torch.Tensor,
+                layout: str = "half", factor: float = 1.0, q_out: Optional[torch.Tensor] = None,
+                k_out: Optional[torch.Tensor] = None, stream=None):
+    """Rotary positions of queries [T, Hq, D] and keys [T, H, D] (bf16 or fp32;
+    views of a fused projection will do; one of them may be None) at positions
+    [T] (see include/specdec_step.h).  `turns` and `factor` are rotary_turns';
+    twice the turns' number of each head's values are turned, in pairs (i, i +
+    half of them) with ``layout="half"`` or (2 i, 2 i + 1) with
+    ``layout="pairs"``.  In place, or into q_out and k_out.  Returns both."""
+    one = q if q is not None else k
+    if one is None:
+        raise ValueError("spec_rotary needs q or k")
+    if one.dim() != 3:
+        raise ValueError("q and k must be [T, heads, D]")
+    if layout not in ("half", "pairs"):
+        raise ValueError("layout must be 'half' or 'pairs'")
+    dev = _device(one, stream)
+    T, _, D = one.shape
+    dtype = one.dtype
+    sides = []
+    for x, y, what in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            if y is not None:
+                raise ValueError(f"{what}_out without {what}")
+            sides.append((0, (None, 0, 0), (None, 0, 0)))
+            continue
+        if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D:
+            raise ValueError("q and k must be [T, heads, D] with one T and D")
+        if x.dtype is not dtype:
+            raise TypeError("q and k must have one dtype")
+        src = _strided(x, what, dev)
+        if y is None or y is x:
+            sides.append((x.shape[1], src, src))
+            continue
+        if y.shape != x.shape:
+            raise ValueError(f"{what}_out must be of {what}'s shape")
+        if y.dtype is not dtype:
+            raise TypeError(f"{what}_out must be of {what}'s dtype")
+        sides.append((x.shape[1], src, _strided(y, f"{what}_out", dev)))
+    pairs = turns.numel()
+    if pairs == 0 or 2 * pairs > D:
+        raise ValueError("turns must hold a value for each pair of a head")
+    (Hq, (qp, qt, qh), (qo, qot, qoh)), (H, (kp, kt, kh), (ko, kot, koh)) = sides
+    _check(load_library().spec_rotary(qp, kp, _dtype_code(one), T, Hq, H, D, qt, qh, kt, kh,
+                                      _at(positions, T, "positions", I32, dev), _at(turns, pairs, "turns", torch.int64, dev),
+                                      2 * pairs, int(layout == "pairs"), float(factor), qo, qot, qoh, ko, kot, koh,
+                                      _on_stream(stream, dev)), "spec_rotary")
+    return q if q_out is None else q_out, k if k_out is None else k_out

@@ -21,13 +21,25 @@ cudaError_t launch_sample(const SampleArgs& a, cudaStream_t st) {
   cudaError_t e = device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
   if (!ready[dev]) {
-    e = cudaFuncSetAttribute(sample_kernel<Elt>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SampleShared));
+    e = cudaFuncSetAttribute(sample_kernel<Elt>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SampleSmem<Elt>));
     if (e != cudaSuccess) return e;
     ready[dev] = true;
   }
-  const unsigned rows = static_cast<unsigned>(a.B) * static_cast<unsigned>(a.n_max + 1);
-  sample_kernel<Elt><<<rows, kSampleThreads, sizeof(SampleShared), st>>>(a);
-  return cudaGetLastError();
+  const int64_t rows = static_cast<int64_t>(a.B) * (a.n_max + 1);
+  int ctas = 1;
+  while (ctas < kSampleClusterMax && 2 * ctas * rows <= 2 * sms && a.V * static_cast<int>(sizeof(Elt)) >= 16384 * ctas) ctas *= 2;
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3(static_cast<unsigned>(rows * ctas));
+  config.blockDim = dim3(kSampleThreads);
+  config.dynamicSmemBytes = sizeof(SampleSmem<Elt>);
+  config.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  config.attrs = &attr;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, sample_kernel<Elt>, a, ctas);
 }
 
 // The widest load that a call's addresses, strides and parts allow, in values.

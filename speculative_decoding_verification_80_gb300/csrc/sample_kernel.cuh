@@ -5,554 +5,757 @@
 // in order of the ids), and the token drawn is where that order's running sum of
 // weights passes a share of the whole.  So everything is one question, asked up to
 // four times: at which id of the order does a running count or sum pass a border?
-// It is answered without sorting: a histogram over the weights' exponent gives the
-// bin, then one over the keys of that bin's ids, in three steps of 11, 11 and 10
-// bits, the logit; ids of that logit are counted in their order.
+// It is answered without sorting, from a histogram of the logits' first 16 bits
+// (a bf16 logit whole) in shared memory, largest first:
+//
+//   - bf16: ids of a bin have one logit and so one weight, which is made once a bin
+//     and not once an id; a border's bin is its logit.
+//   - fp32: a second pass adds every id's weight to its bin; the ids of a border's
+//     bin are listed and looked at one by one.
+//
+// Bins of 32 have their sums in shared memory too, so that every warp finds a
+// border by itself, in three looks of its lanes, without a barrier.  Then ids of the
+// borders' logits are counted in their order, and the row is written.
+//
+// A row is one cluster's of 1 to 8 CTAs, as few as keep the SMs busy; each has a
+// part of the row, a histogram of it, and a share of the bins to add up.
 #pragma once
-#include <cuda_bf16.h>
-#include <stdint.h>
+#include <cooperative_groups.h>
 
-#include "sample_weight.cuh"
+#include "sample_any.cuh"
 
 namespace specdec {
 
-struct SampleArgs {
-  const void* logits;
-  void* out;              // or NULL
-  int32_t B, n_max, V;
-  const int32_t* draft_len;
-  const float* temperature;
-  const int32_t* top_k;
-  const float* top_p;
-  const float* min_p;
-  const float* uniform;   // or NULL
-  int32_t* tokens;        // or NULL
-  uint32_t* err;
+constexpr int kSampleClusterMax = 8;
+constexpr int kNear = 1024;   // ids of a border's bin that are listed (fp32)
+
+// Bins of a logit's first 16 bits, the largest first: magnitudes from 2^12 down
+// have one for each 7 bits of mantissa; what is above is in the outermost bins and
+// what is below in the two of zero.
+template <typename Elt>
+struct SampleBinsOf {
+  static constexpr bool kWhole = sizeof(Elt) == 2;
+  static constexpr int kBins = kWhole ? 16384 : 8192;
+  static constexpr int kGroups = kBins / 32;
+  static constexpr int kHalf = kBins / 2;
+  static constexpr uint32_t kTop = (127 + 12) << 7;          // 2^12 and above
+  static constexpr uint32_t kBase = kTop - (kHalf - 1);      // below the least
+
+  // of two logits' bits at once, a half each
+  static __device__ __forceinline__ uint32_t two(uint32_t w) {
+    const uint32_t m = __vminu2(__vmaxu2(w & 0x7FFF7FFFu, kBase * 0x10001u), kTop * 0x10001u) - (kBase - kHalf) * 0x10001u;
+    uint32_t negative;  // a mask in each half
+    asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(negative) : "r"(w));
+    return m ^ (~negative & (kBins - 1) * 0x10001u);
+  }
+  static __device__ __forceinline__ int one(float x) {
+    const uint32_t b = __float_as_uint(x), m = min(max((b >> 16) & 0x7FFFu, kBase), kTop) - (kBase - kHalf);
+    return static_cast<int>((b >> 31) != 0 ? m : m ^ (kBins - 1));
+  }
+  // the logit of a bin of a whole bf16 (not of those of zero and the outermost)
+  static __device__ __forceinline__ float value(int bin) {
+    const uint32_t m = static_cast<uint32_t>(bin < kHalf ? bin ^ (kBins - 1) : bin) - kHalf;
+    const uint32_t b = m == 0 ? 0 : (m + kBase) | (bin < kHalf ? 0u : 0x8000u);
+    return __uint_as_float(b << 16);
+  }
 };
-
-constexpr int kSampleThreads = 512;
-constexpr int kSampleBins = 2048;  // 1/32 of a power of two each
-constexpr int kSampleList = 4096;  // ids of a bin that are kept in shared memory
-constexpr int kSampleWarps = kSampleThreads / 32;
-constexpr uint32_t kKeyFloor = 0x007FFFFFu;  // -infinity's
-
-// Larger for a larger number; finite x, or an infinity.
-__device__ __forceinline__ uint32_t key_of(float x) {
-  const uint32_t u = __float_as_uint(x);
-  return u ^ ((u >> 31) != 0 ? 0xFFFFFFFFu : 0x80000000u);
-}
-__device__ __forceinline__ float of_key(uint32_t k) {
-  return __uint_as_float(k ^ ((k >> 31) != 0 ? 0x80000000u : 0xFFFFFFFFu));
-}
-
-// NaN counts as -infinity, and -0 as 0.
-__device__ __forceinline__ float plain_logit(float x) { return x == x ? x + 0.f : -INFINITY; }
 
 template <typename Elt>
-struct SampleRow {
-  static constexpr int E = 16 / sizeof(Elt);
-  const Elt* p;  // on 16 bytes: the row starts `phase` elements later
-  int phase, V, vecs;
-
-  __device__ __forceinline__ SampleRow(const Elt* row, int V_) : V(V_) {
-    phase = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(Elt));
-    p = row - phase;
-    vecs = (phase + V + E - 1) / E;
-  }
-  // Logits of the ids E j - phase and on; -infinity where there are none.
-  __device__ __forceinline__ void load(int j, float (&x)[E]) const {
-    const int first = E * j - phase;
-    if (first >= 0 && first + E <= V) {
-      const uint4 q = reinterpret_cast<const uint4*>(p)[j];  // (the row may be cut in place)
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (sizeof(Elt) == 2) {
-          x[(2 * i) % E] = plain_logit(__uint_as_float(w[i] << 16));
-          x[(2 * i + 1) % E] = plain_logit(__uint_as_float(w[i] & 0xFFFF0000u));
-        } else {
-          x[i % E] = plain_logit(__uint_as_float(w[i]));
-        }
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        x[e] = first + e >= 0 && first + e < V ? plain_logit(static_cast<float>(p[static_cast<long long>(E) * j + e])) : -INFINITY;
-    }
-  }
+struct SampleBinsShared;
+template <>
+struct SampleBinsShared<__nv_bfloat16> {
+  uint32_t count[16384];
+};
+template <>
+struct SampleBinsShared<float> {
+  uint32_t count[8192], lo[8192], hi[8192];  // halves of the sums
+  uint32_t near_key[kNear];
+  unsigned long long near_weight[kNear];
 };
 
-struct SampleShared {
-  uint32_t count[kSampleBins];
-  uint32_t lo[kSampleBins], hi[kSampleBins];  // halves of the sums
-  uint32_t list[kSampleList];
+struct SampleAnswer {
+  uint32_t key, ids, all, bad;
+  unsigned long long sum, count;
+};
+
+template <typename Elt>
+struct SampleFast {
+  static constexpr int kGroups = SampleBinsOf<Elt>::kGroups;
+  alignas(16) SampleBinsShared<Elt> bins;
+  unsigned long long group_sum[kGroups + 2];  // of 32 bins, then before them
+  uint32_t group_count[kGroups + 2];
   ExpPair table[256];
-  unsigned long long warp_sum[kSampleWarps + 1];
-  uint32_t warp_count[kSampleWarps + 1];
-  // answers
-  unsigned long long sum_before;
-  uint32_t count_before, bin, ids, listed;
-  float best[kSampleWarps];
-  int best_id[kSampleWarps];
-  WeightScale scale;
-  unsigned long long least;  // weight of min-p
-};
-
-__device__ __forceinline__ void add_weight(SampleShared& s, int bin, unsigned long long w) {
-  const uint32_t lo = static_cast<uint32_t>(w);
-  uint32_t hi = static_cast<uint32_t>(w >> 32);
-  if (lo != 0) {
-    const uint32_t old = atomicAdd(&s.lo[bin], lo);
-    hi += old + lo < old ? 1 : 0;
-  }
-  if (hi != 0) atomicAdd(&s.hi[bin], hi);
-}
-
-// Sums over the CTA of a count and a weight before each thread's own, and the
-// whole.  All threads call it.
-__device__ __forceinline__ void sample_prefix(SampleShared& s, uint32_t c, unsigned long long w, uint32_t* c_before,
-                                              unsigned long long* w_before, uint32_t* c_all, unsigned long long* w_all) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t cs = c;
-  unsigned long long ws = w;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const uint32_t co = __shfl_up_sync(0xFFFFFFFFu, cs, d);
-    const unsigned long long wo = __shfl_up_sync(0xFFFFFFFFu, ws, d);
-    if (lane >= d) cs += co, ws += wo;
-  }
-  __syncthreads();
-  if (lane == 31) s.warp_count[warp] = cs, s.warp_sum[warp] = ws;
-  __syncthreads();
-  uint32_t cb = 0, ca = 0;
-  unsigned long long wb = 0, wa = 0;
-#pragma unroll
-  for (int i = 0; i < kSampleWarps; ++i) {
-    if (i == warp) cb = ca, wb = wa;
-    ca += s.warp_count[i];
-    wa += s.warp_sum[i];
-  }
-  *c_before = cb + cs - c;
-  *w_before = wb + ws - w;
-  *c_all = ca;
-  *w_all = wa;
-}
-
-// The bins in shared memory with the sums before each, in registers.
-constexpr int kBinsOfThread = kSampleBins / kSampleThreads;
-struct BinSums {
-  uint32_t c[kBinsOfThread + 1];
-  unsigned long long w[kBinsOfThread + 1];
-  uint32_t c_all;
-  unsigned long long w_all;
-};
-__device__ __forceinline__ void sum_bins(SampleShared& s, BinSums& b) {
-  const int first = threadIdx.x * kBinsOfThread;
-  uint32_t c[kBinsOfThread], ct = 0;
-  unsigned long long w[kBinsOfThread], wt = 0;
-#pragma unroll
-  for (int i = 0; i < kBinsOfThread; ++i) {
-    c[i] = s.count[first + i];
-    w[i] = (static_cast<unsigned long long>(s.hi[first + i]) << 32) + s.lo[first + i];
-    ct += c[i];
-    wt += w[i];
-  }
-  sample_prefix(s, ct, wt, &b.c[0], &b.w[0], &b.c_all, &b.w_all);
-#pragma unroll
-  for (int i = 0; i < kBinsOfThread; ++i) b.c[i + 1] = b.c[i] + c[i], b.w[i + 1] = b.w[i] + w[i];
-}
-__device__ __forceinline__ void clear_bins(SampleShared& s) {
-  for (int i = threadIdx.x; i < kSampleBins; i += kSampleThreads) s.count[i] = s.lo[i] = s.hi[i] = 0;
-}
-
-// What a border is counted in: ids up to `target` of them (1 and on), or weight
-// up to `target` of it, or more than `target` of it; or the logits from the key
-// `target` on.
-enum SampleBorder { kByCount, kBySumTo, kBySumPast, kByKey };
-
-// Whether a running value passes the border between `before` and `after`.
-__device__ __forceinline__ bool crosses(SampleBorder by, uint32_t c0, uint32_t c1, unsigned long long w0,
-                                        unsigned long long w1, unsigned long long target) {
-  if (by == kByCount) return c0 < target && target <= c1;
-  if (by == kBySumTo) return w0 < target && target <= w1;
-  return w0 <= target && target < w1;
-}
-
-// The bin in which the border lies, for all threads; the sums before it are in s.
-// One bin has to be the answer.
-__device__ __forceinline__ int find_bin(SampleShared& s, const BinSums& b, SampleBorder by, unsigned long long target) {
-#pragma unroll
-  for (int i = 0; i < kBinsOfThread; ++i)
-    if (crosses(by, b.c[i], b.c[i + 1], b.w[i], b.w[i + 1], target)) {
-      s.bin = threadIdx.x * kBinsOfThread + i;
-      s.count_before = b.c[i];
-      s.sum_before = b.w[i];
-      s.ids = b.c[i + 1] - b.c[i];
-    }
-  __syncthreads();
-  return s.bin;
-}
-
-// A place in the order: ids of larger keys, then the first `ids` of those of `key`.
-struct SamplePlace {
-  uint32_t key, ids, all;        // all: ids of that key
-  unsigned long long sum;        // weight before the key's ids
+  unsigned long long warp_sum[kSampleWarps];
+  uint32_t warp_count[kSampleWarps][2];
+  // what the cluster's CTAs tell each other
+  uint32_t top[kSampleClusterMax], flag[kSampleClusterMax];
+  int32_t id[kSampleClusterMax];
+  uint32_t same[kSampleClusterMax][2];
+  int32_t found[2];
+  uint32_t listed;
+  SampleAnswer answer;
+  SampleAsk ask;
 };
 
 template <typename Elt>
-struct Sampler {
+union SampleSmem {
+  SampleFast<Elt> fast;
+  SampleShared any;
+};
+
+// A bin and what is before it.
+struct SampleBin {
+  int bin;
+  uint32_t c0, c;
+  unsigned long long w0, w;
+};
+
+// Sum over a warp, of less than 2^64 in all.
+__device__ __forceinline__ unsigned long long warp_sum64(unsigned long long w) {
+  const uint32_t a = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(w) & 0x3FFFFFu);
+  const uint32_t b = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(w >> 22) & 0x3FFFFFu);
+  const uint32_t c = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(w >> 44));
+  return a + (static_cast<unsigned long long>(b) << 22) + (static_cast<unsigned long long>(c) << 44);
+}
+
+template <typename Elt>
+struct SampleJob {
+  using Bins = SampleBinsOf<Elt>;
   static constexpr int E = SampleRow<Elt>::E;
-  SampleShared& s;
+  static constexpr int kGroups = Bins::kGroups;
+  SampleFast<Elt>& s;
   const SampleRow<Elt> row;
-  float top;       // the largest logit
-  bool infinite;   // it is infinite: the others have no weight
+  cooperative_groups::cluster_group cluster;
+  int ctas, rank;
+  int j0, j1;       // this CTA's vectors
+  float top;        // the largest logit
   WeightScale scale;
 
-  __device__ __forceinline__ float relative(float x) const { return infinite ? (x == INFINITY ? 0.f : -INFINITY) : x; }
-  __device__ __forceinline__ unsigned long long weight(float x) const { return sample_weight(x, infinite ? 0.f : top, scale, s.table); }
-  // (monotone: each step rounds a monotone function)
-  __device__ __forceinline__ int bin_of(float x) const {
-    const float t = (x - (infinite ? 0.f : top)) * (scale.hi * -32.f);
-    return t < static_cast<float>(kSampleBins - 1) ? static_cast<int>(t) : kSampleBins - 1;
-  }
-
-  template <typename F>
-  __device__ __forceinline__ void each(F f) const {
-#pragma unroll 2
-    for (int j = threadIdx.x; j < row.vecs; j += kSampleThreads) {
-      float x[E];
-      row.load(j, x);
-#pragma unroll
-      for (int e = 0; e < E; ++e) f(relative(x[e]), E * j + e - row.phase);
-    }
-  }
-
-  // Within the bin that find_bin gave: the key at which the border lies.
-  __device__ __forceinline__ SamplePlace refine(SampleBorder by, unsigned long long target) {
-    const int bin = s.bin;
-    const uint32_t ids = s.ids;
-    uint32_t c0 = s.count_before;
-    unsigned long long w0 = s.sum_before;
-    const bool in_list = ids <= kSampleList;
-    __syncthreads();
-    if (in_list) {
-      if (threadIdx.x == 0) s.listed = 0;
+  __device__ __forceinline__ SampleFast<Elt>& of(int cta) const { return *cluster.map_shared_rank(&s, cta); }
+  __device__ __forceinline__ void meet() const {
+    if (ctas > 1)
+      cluster.sync();
+    else
       __syncthreads();
-      each([&](float x, int) {
-        if (x != -INFINITY && bin_of(x) == bin) s.list[atomicAdd(&s.listed, 1)] = key_of(x);
-      });
-    }
-    uint32_t key = 0, all = 0;
-    int shift = 32;
+  }
+  __device__ __forceinline__ unsigned long long weight(float x) const { return sample_weight(x, top, scale, s.table); }
+
+  // f(words, j) for this CTA's whole vectors, four on their way at a time, and
+  // g(logit's bits, id) for the ids at the row's ends that have none.
+  template <typename F, typename G>
+  __device__ __forceinline__ void each(F f, G g) const {
+    const int lo = max(j0, row.phase != 0 ? 1 : 0), hi = min(j1, (row.phase + row.V) / E);
+    const uint4* p = reinterpret_cast<const uint4*>(row.p);
+    int j = lo + threadIdx.x;
 #pragma unroll 1
-    for (int bits = 11; shift > 0; bits = shift < 11 ? shift : 11) {
-      const uint32_t above = key;  // the bits found so far
-      const int was = shift;
-      shift -= bits;
-      __syncthreads();
-      clear_bins(s);
-      __syncthreads();
-      auto one = [&](uint32_t k) {
-        if (was < 32 && (k >> was) != (above >> was)) return;
-        // the largest first
-        const int at = ((1 << bits) - 1) - static_cast<int>((k >> shift) & ((1u << bits) - 1));
-        atomicAdd(&s.count[at], 1u);
-        if (by != kByCount) add_weight(s, at, weight(of_key(k)));
-      };
-      if (in_list) {
-        for (uint32_t i = threadIdx.x; i < ids; i += kSampleThreads) one(s.list[i]);
-      } else {
-        each([&](float x, int) {
-          if (x != -INFINITY && bin_of(x) == bin) one(key_of(x));
-        });
-      }
-      __syncthreads();
-      BinSums b;
-      sum_bins(s, b);
-      int at;
-      if (by == kByKey) {
-        // the bin that the key itself is in, whether it has ids or not
-        at = ((1 << bits) - 1) - static_cast<int>((static_cast<uint32_t>(target) >> shift) & ((1u << bits) - 1));
-        if (at / kBinsOfThread == threadIdx.x) {
+    for (; j + 3 * kSampleThreads < hi; j += 4 * kSampleThreads) {
+      uint4 q[4];
 #pragma unroll
-          for (int i = 0; i < kBinsOfThread; ++i)
-            if (i == at % kBinsOfThread) s.count_before = b.c[i], s.sum_before = b.w[i], s.ids = b.c[i + 1] - b.c[i];
+      for (int i = 0; i < 4; ++i) q[i] = p[j + i * kSampleThreads];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f(q[i], j + i * kSampleThreads);
+    }
+#pragma unroll 1
+    for (; j < hi; j += kSampleThreads) f(p[j], j);
+    // (a row within one vector has its ids at one end or the other)
+    if (threadIdx.x < 2 * E) {
+      const int v = threadIdx.x < E ? 0 : row.vecs - 1, i = E * v + static_cast<int>(threadIdx.x % E) - row.phase;
+      const bool whole = E * v >= row.phase && E * (v + 1) <= row.phase + row.V;
+      if (v >= j0 && v < j1 && !whole && (threadIdx.x < E || row.vecs > 1) && i >= 0 && i < row.V) g(bits(row.p[i + row.phase]), i);
+    }
+  }
+  static __device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x); }
+  static __device__ __forceinline__ uint32_t bits(__nv_bfloat16 x) { return __bfloat16_as_ushort(x); }
+  static __device__ __forceinline__ float logit(uint32_t b) { return plain_logit(__uint_as_float(sizeof(Elt) == 2 ? b << 16 : b)); }
+  // f(logit, id) for all of this CTA's ids.
+  template <typename F>
+  __device__ __forceinline__ void each_id(F f) const {
+    each(
+        [&](const uint4& q, int j) {
+          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+          const int id = E * j - row.phase;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (sizeof(Elt) == 2) {
+              f(logit(w[i] & 0xFFFFu), id + 2 * i);
+              f(logit(w[i] >> 16), id + 2 * i + 1);
+            } else {
+              f(logit(w[i]), id + i);
+            }
+          }
+        },
+        [&](uint32_t b, int id) { f(logit(b), id); });
+  }
+
+  // A bin's count and sum, over the cluster, from the CTA that added them up.
+  __device__ __forceinline__ void bin_of_cluster(int bin, uint32_t* c, unsigned long long* w) const {
+    const SampleFast<Elt>& o = ctas > 1 ? of(bin / 32 / (kGroups / ctas)) : s;
+    *c = o.bins.count[bin];
+    if constexpr (sizeof(Elt) == 2)
+      *w = *c != 0 ? *c * weight(Bins::value(bin)) : 0;
+    else
+      *w = (static_cast<unsigned long long>(o.bins.hi[bin]) << 32) + o.bins.lo[bin];
+  }
+
+  // Adds the CTAs' histograms up, a share of the bins each, and the sums of every
+  // 32 bins, which all CTAs get.
+  __device__ __forceinline__ void add_up() {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = kGroups / ctas;
+    for (int g = rank * share + warp; g < (rank + 1) * share; g += kSampleWarps) {
+      const int bin = 32 * g + lane;
+      uint32_t c = 0;
+      unsigned long long w = 0;
+      for (int o = 0; o < ctas; ++o) {
+        const SampleFast<Elt>& x = ctas > 1 ? of(o) : s;
+        c += x.bins.count[bin];
+        if constexpr (sizeof(Elt) == 4) w += (static_cast<unsigned long long>(x.bins.hi[bin]) << 32) + x.bins.lo[bin];
+      }
+      if (ctas > 1) {
+        s.bins.count[bin] = c;
+        if constexpr (sizeof(Elt) == 4) s.bins.lo[bin] = static_cast<uint32_t>(w), s.bins.hi[bin] = static_cast<uint32_t>(w >> 32);
+      }
+      unsigned long long ws = 0;
+      if constexpr (sizeof(Elt) == 2) {
+        if (__any_sync(0xFFFFFFFFu, c != 0)) ws = warp_sum64(c != 0 ? c * weight(Bins::value(bin)) : 0);
+      } else {
+        ws = warp_sum64(w);
+      }
+      const uint32_t cs = __reduce_add_sync(0xFFFFFFFFu, c);
+      if (lane < ctas) {
+        SampleFast<Elt>& x = ctas > 1 ? of(lane) : s;
+        x.group_count[g] = cs;
+        x.group_sum[g] = ws;
+      }
+    }
+    meet();
+    // sums before each group
+    uint32_t c = 0, cs;
+    unsigned long long w = 0, ws;
+    if (threadIdx.x < kGroups) c = s.group_count[threadIdx.x], w = s.group_sum[threadIdx.x];
+    cs = c, ws = w;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t co = __shfl_up_sync(0xFFFFFFFFu, cs, d);
+      const unsigned long long wo = __shfl_up_sync(0xFFFFFFFFu, ws, d);
+      if (lane >= d) cs += co, ws += wo;
+    }
+    if (lane == 31) s.warp_count[warp][0] = cs, s.warp_sum[warp] = ws;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) cs += s.warp_count[i][0], ws += s.warp_sum[i];
+    if (threadIdx.x < kGroups) {
+      s.group_count[threadIdx.x] = cs - c;
+      s.group_sum[threadIdx.x] = ws - w;
+      if (threadIdx.x == kGroups - 1) s.group_count[kGroups] = cs, s.group_sum[kGroups] = ws;
+    }
+    __syncthreads();
+  }
+
+  // The bin in which a border lies, by each warp for itself; false if there is none.
+  __device__ __forceinline__ bool find(SampleBorder by, unsigned long long target, SampleBin* f) const {
+    constexpr int kStep = kGroups / 32;
+    const int lane = threadIdx.x & 31;
+    auto passed = [&](uint32_t c, unsigned long long w) { return by == kByCount ? c >= target : (by == kBySumTo ? w >= target : w > target); };
+    uint32_t m = __ballot_sync(0xFFFFFFFFu, passed(s.group_count[(lane + 1) * kStep], s.group_sum[(lane + 1) * kStep]));
+    if (m == 0) return false;
+    int g = (__ffs(m) - 1) * kStep;
+    m = __ballot_sync(0xFFFFFFFFu, lane >= kStep - 1 || passed(s.group_count[g + lane + 1], s.group_sum[g + lane + 1]));
+    g += __ffs(m) - 1;
+    within(g, [&](uint32_t c0, uint32_t c1, unsigned long long w0, unsigned long long w1, int) { return passed(c1, w1); }, f);
+    return true;
+  }
+  // The bin itself and what is before it.
+  __device__ __forceinline__ void look_up(int bin, SampleBin* f) const {
+    within(bin >> 5, [&](uint32_t, uint32_t, unsigned long long, unsigned long long, int lane) { return lane >= (bin & 31); }, f);
+  }
+  template <typename F>
+  __device__ __forceinline__ void within(int g, F passed, SampleBin* f) const {
+    const int lane = threadIdx.x & 31;
+    uint32_t c;
+    unsigned long long w;
+    bin_of_cluster(32 * g + lane, &c, &w);
+    uint32_t c1 = c;
+    unsigned long long w1 = w;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t co = __shfl_up_sync(0xFFFFFFFFu, c1, d);
+      const unsigned long long wo = __shfl_up_sync(0xFFFFFFFFu, w1, d);
+      if (lane >= d) c1 += co, w1 += wo;
+    }
+    c1 += s.group_count[g];
+    w1 += s.group_sum[g];
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, lane == 31 || passed(c1 - c, c1, w1 - w, w1, lane));
+    const int at = __ffs(m) - 1;
+    f->bin = 32 * g + at;
+    f->c0 = __shfl_sync(0xFFFFFFFFu, c1 - c, at);
+    f->c = __shfl_sync(0xFFFFFFFFu, c, at);
+    f->w0 = __shfl_sync(0xFFFFFFFFu, w1 - w, at);
+    f->w = __shfl_sync(0xFFFFFFFFu, w, at);
+  }
+
+  // The key at which a border lies within its bin; for kByKey the key is the border
+  // and all ids from it on are before it.  False: the bin does not say (for all CTAs
+  // alike).
+  __device__ __forceinline__ bool resolve(const SampleBin& f, SampleBorder by, unsigned long long target, SamplePlace* p) {
+    if constexpr (sizeof(Elt) == 2) {
+      if (f.bin == 0 || f.bin >= Bins::kBins - 1 || f.bin == Bins::kHalf - 1 || f.bin == Bins::kHalf) return false;
+      p->key = key_of(Bins::value(f.bin));
+      p->all = f.c;
+      p->sum = f.w0;
+      const unsigned long long w = weight(Bins::value(f.bin));
+      p->ids = by == kByCount ? static_cast<uint32_t>(target) - f.c0
+                              : static_cast<uint32_t>(by == kByKey ? f.c : (by == kBySumTo ? (target - f.w0 + w - 1) / w : (target - f.w0) / w + 1));
+      return true;
+    } else {
+      SampleFast<Elt>& lead = ctas > 1 ? of(0) : s;
+      each_id([&](float x, int) {
+        if (x != -INFINITY && Bins::one(x) == f.bin) {
+          const uint32_t at = atomicAdd(&lead.listed, 1u);
+          if (at < kNear) lead.bins.near_key[at] = key_of(x);
+        }
+      });
+      meet();
+      if (rank == 0) {
+        const uint32_t n = s.listed;
+        if (threadIdx.x == 0) s.answer.bad = n > kNear ? 1 : 0, s.answer.sum = 0, s.answer.count = 0;
+        if (n <= kNear) {
+          for (uint32_t i = threadIdx.x; i < n; i += kSampleThreads) s.bins.near_weight[i] = weight(of_key(s.bins.near_key[i]));
+          __syncthreads();
+          for (uint32_t i = threadIdx.x; i < n; i += kSampleThreads) {
+            const uint32_t key = s.bins.near_key[i];
+            const unsigned long long w = s.bins.near_weight[i];
+            if (by == kByKey) {
+              if (key >= static_cast<uint32_t>(target)) atomicAdd(&s.answer.count, 1ull), atomicAdd(&s.answer.sum, w);
+              continue;
+            }
+            uint32_t c0 = 0, same = 0;
+            unsigned long long w0 = 0;
+#pragma unroll 2
+            for (uint32_t o = 0; o < n; ++o) {
+              const uint32_t other = s.bins.near_key[o];
+              if (other > key) ++c0, w0 += s.bins.near_weight[o];
+              if (other == key) ++same;
+            }
+            c0 += f.c0;
+            w0 += f.w0;
+            if (crosses(by, c0, c0 + same, w0, w0 + same * w, target)) {  // (one key, whose ids all say the same)
+              s.answer.key = key;
+              s.answer.all = same;
+              s.answer.sum = w0;
+              s.answer.ids = by == kByCount ? static_cast<uint32_t>(target) - c0
+                                            : static_cast<uint32_t>(by == kBySumTo ? (target - w0 + w - 1) / w : (target - w0) / w + 1);
+            }
+          }
         }
         __syncthreads();
-      } else {
-        unsigned long long rest = target - (by == kByCount ? c0 : w0);
-        at = find_bin(s, b, by, rest);
+        if (by == kByKey && threadIdx.x == 0) {
+          s.answer.key = static_cast<uint32_t>(target);
+          s.answer.all = s.answer.ids = 0;
+          s.answer.sum += f.w0;
+        }
+        __syncthreads();
+        if (ctas > 1 && threadIdx.x >= 32 && threadIdx.x < 32 * ctas && threadIdx.x % 32 == 0) of(threadIdx.x / 32).answer = s.answer;
+        if (threadIdx.x == 0) s.listed = 0;
       }
-      c0 += s.count_before;
-      w0 += s.sum_before;
-      all = s.ids;
-      key = above | (static_cast<uint32_t>(((1 << bits) - 1) - at) << shift);
+      meet();
+      const SampleAnswer a = s.answer;
+      p->key = a.key;
+      p->ids = a.ids;
+      p->all = a.all;
+      p->sum = a.sum;
+      return a.bad == 0;
     }
-    __syncthreads();
-    SamplePlace p;
-    p.key = key;
-    p.all = all;
-    p.sum = w0;
-    if (by == kByCount) {
-      p.ids = static_cast<uint32_t>(target) - c0;
-    } else if (by == kByKey) {
-      p.ids = all;
-    } else {
-      const unsigned long long w = weight(of_key(key)), rest = target - w0;
-      p.ids = static_cast<uint32_t>(by == kBySumTo ? (rest + w - 1) / w : rest / w + 1);
-    }
-    return p;
   }
 
-  // The id of the nth (1 and on) of the ids with this key, in their order.
-  __device__ __forceinline__ int nth(uint32_t key, uint32_t n) {
+  // The ids that are the first[i]-th (1 and on; 0: none) of those with key[i].
+  __device__ __forceinline__ void nth(const uint32_t (&key)[2], const uint32_t (&first)[2], int (&id)[2]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int share = (row.vecs + kSampleWarps - 1) / kSampleWarps, j0 = min(warp * share, row.vecs), j1 = min(j0 + share, row.vecs);
-    uint32_t mine = 0;
-    for (int j = j0 + lane; j < j1; j += 32) {
+    const int part = (j1 - j0 + kSampleWarps - 1) / kSampleWarps, v0 = min(j1, j0 + warp * part), v1 = min(j1, v0 + part);
+    auto count = [&](int j, uint32_t (&n)[2]) {
       float x[E];
       row.load(j, x);
 #pragma unroll
-      for (int e = 0; e < E; ++e) mine += x[e] != -INFINITY && key_of(relative(x[e])) == key ? 1 : 0;
-    }
-    mine = __reduce_add_sync(0xFFFFFFFFu, mine);
-    __syncthreads();
-    if (lane == 0) s.warp_count[warp] = mine;
-    if (threadIdx.x == 0) s.bin = 0;
-    __syncthreads();
-    uint32_t before = 0;
-    for (int i = 0; i < warp; ++i) before += s.warp_count[i];
-    if (before < n && n <= before + mine) {
-      uint32_t left = n - before;
-      for (int j = j0; j < j1; j += 32) {
-        float x[E];
-        uint32_t here = 0;
-        if (j + lane < j1) {
-          row.load(j + lane, x);
+      for (int e = 0; e < E; ++e) {
+        const uint32_t k = key_of(x[e]);
+        n[0] += k == key[0] ? 1 : 0;
+        n[1] += k == key[1] ? 1 : 0;
+      }
+    };
+    uint32_t mine[2] = {0, 0};
+#pragma unroll 4
+    for (int j = v0 + lane; j < v1; j += 32) count(j, mine);
 #pragma unroll
-          for (int e = 0; e < E; ++e) here += x[e] != -INFINITY && key_of(relative(x[e])) == key ? 1 : 0;
-        }
-        uint32_t upto = here;
+    for (int i = 0; i < 2; ++i) {
+      mine[i] = __reduce_add_sync(0xFFFFFFFFu, mine[i]);
+      if (lane == 0) s.warp_count[warp][i] = mine[i];
+    }
+    __syncthreads();
+    if (threadIdx.x < 2 * ctas) {
+      const int i = threadIdx.x & 1;
+      uint32_t n = 0;
+      for (int w = 0; w < kSampleWarps; ++w) n += s.warp_count[w][i];
+      of(threadIdx.x >> 1).same[rank][i] = n;
+    }
+    meet();
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      uint32_t before = 0;
+      for (int o = 0; o < rank; ++o) before += s.same[o][i];
+      for (int w = 0; w < warp; ++w) before += s.warp_count[w][i];
+      if (!(before < first[i] && first[i] <= before + mine[i])) continue;
+      uint32_t left = first[i] - before;
+      for (int j = v0; j < v1; j += 32) {
+        uint32_t here[2] = {0, 0};
+        if (j + lane < v1) count(j + lane, here);
+        uint32_t upto = here[i];
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
           if (lane >= d) upto += o;
         }
-        if (here != 0 && upto - here < left && left <= upto) {
-          uint32_t k = upto - here;
+        if (here[i] != 0 && upto - here[i] < left && left <= upto) {
+          uint32_t k = upto - here[i];
+          float x[E];
+          row.load(j + lane, x);
+          int at = 0;
 #pragma unroll
           for (int e = 0; e < E; ++e)
-            if (x[e] != -INFINITY && key_of(relative(x[e])) == key && ++k == left) s.bin = E * (j + lane) + e - row.phase;
+            if (key_of(x[e]) == key[i] && ++k == left) at = E * (j + lane) + e - row.phase;
+          for (int o = 0; o < ctas; ++o) of(o).found[i] = at;
         }
         const uint32_t sum = __shfl_sync(0xFFFFFFFFu, upto, 31);
         if (left <= sum) break;
         left -= sum;
       }
     }
+    meet();
+    id[0] = s.found[0];
+    id[1] = s.found[1];
+  }
+
+  // This CTA's part of the row, -infinity for ids whose key is below `key`, or is it
+  // and whose id is past `last`.
+  __device__ __forceinline__ void write(Elt* out, uint32_t key, int last) const {
+    const bool same = (reinterpret_cast<uintptr_t>(out) & 15) == row.phase * sizeof(Elt);
+    const float least = of_key(key), next = of_key(key + 1);  // (key is not infinity's)
+    const Elt none = static_cast<Elt>(-INFINITY);
+    each(
+        [&](const uint4& q, int j) {
+          const int first = E * j - row.phase;
+          uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (sizeof(Elt) == 2) {
+              const int id = first + 2 * i;
+              const bool a = __uint_as_float(w[i] << 16) >= (id <= last ? least : next);
+              const bool b = __uint_as_float(w[i] & 0xFFFF0000u) >= (id + 1 <= last ? least : next);
+              w[i] = (a ? w[i] & 0xFFFFu : 0xFF80u) | (b ? w[i] & 0xFFFF0000u : 0xFF800000u);
+            } else {
+              w[i] = __uint_as_float(w[i]) >= (first + i <= last ? least : next) ? w[i] : 0xFF800000u;
+            }
+          }
+          if (same) {
+            *reinterpret_cast<uint4*>(out + first) = make_uint4(w[0], w[1], w[2], w[3]);
+          } else if constexpr (sizeof(Elt) == 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              out[first + 2 * i] = __ushort_as_bfloat16(static_cast<unsigned short>(w[i]));
+              out[first + 2 * i + 1] = __ushort_as_bfloat16(static_cast<unsigned short>(w[i] >> 16));
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[first + i] = __uint_as_float(w[i]);
+          }
+        },
+        [&](uint32_t b, int id) {
+          const float x = logit(b);
+          out[id] = x >= (id <= last ? least : next) ? static_cast<Elt>(x) : none;
+        });
+  }
+
+  // The row with one id left (or none: -1), and that id's logit.
+  __device__ __forceinline__ void write_one(Elt* out, int id) const {
+    const Elt none = static_cast<Elt>(-INFINITY);
+    const Elt* in = row.p + row.phase;
+    Elt kept = none;
+    const int phase = static_cast<int>((reinterpret_cast<uintptr_t>(out) & 15) / sizeof(Elt)), vecs = (phase + row.V + E - 1) / E;
+    if (id >= 0) kept = in[id];
+    if (row.p + row.phase == out && ctas > 1) cluster.sync();  // (in place: everyone has read it)
+    if (row.p + row.phase == out && ctas == 1) __syncthreads();
+    const int share = (vecs + ctas - 1) / ctas, a = min(vecs, rank * share), b = min(vecs, a + share);
+    const uint32_t word = sizeof(Elt) == 2 ? 0xFF80FF80u : 0xFF800000u;
+    for (int j = a + static_cast<int>(threadIdx.x); j < b; j += kSampleThreads) {
+      const int first = E * j - phase;
+      if (first >= 0 && first + E <= row.V && !(id >= first && id < first + E)) {
+        *reinterpret_cast<uint4*>(out + first) = make_uint4(word, word, word, word);
+      } else {
+#pragma unroll 1
+        for (int e = 0; e < E; ++e)
+          if (first + e >= 0 && first + e < row.V) out[first + e] = first + e == id ? kept : none;
+      }
+    }
+  }
+
+  // The largest logit's key and its first id, over the cluster.
+  __device__ __forceinline__ void largest(uint32_t* key, int* id) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float best = -INFINITY;
+    int at = 0x7FFFFFFF;
+    each_id([&](float x, int i) {
+      if (x > best || (x == best && i < at && x != -INFINITY)) best = x, at = i;
+    });
+    uint32_t k = key_of(best);
+    const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, k);
+    uint32_t who = __reduce_min_sync(0xFFFFFFFFu, k == most ? static_cast<uint32_t>(at) : 0x7FFFFFFFu);
+    if (lane == 0) s.warp_count[warp][0] = most, s.warp_count[warp][1] = who;
     __syncthreads();
-    const int id = s.bin;
-    __syncthreads();
-    return id;
+    if (threadIdx.x < ctas) {
+      k = 0, who = 0x7FFFFFFF;
+      for (int w = 0; w < kSampleWarps; ++w) {
+        const uint32_t o = s.warp_count[w][0], i = s.warp_count[w][1];
+        if (o > k || (o == k && i < who)) k = o, who = i;
+      }
+      of(threadIdx.x).top[rank] = k;
+      of(threadIdx.x).id[rank] = static_cast<int>(who);
+    }
+    meet();
+    *key = 0, *id = 0x7FFFFFFF;
+    for (int o = 0; o < ctas; ++o)
+      if (s.top[o] > *key) *key = s.top[o], *id = s.id[o];  // (the first CTA has the lower ids)
   }
 };
 
-// The row with -infinity for the ids that are not kept: keys above `key`, and ids
-// up to `last` of those that have it.
+// A key whose weight is enough, the least that a logit of `Elt` can have, by each
+// warp for itself; `no` has too little.
 template <typename Elt>
-__device__ __forceinline__ void write_cut_row(const SampleRow<Elt>& row, Elt* out, uint32_t key, int last, bool infinite) {
-  constexpr int E = SampleRow<Elt>::E;
-  const Elt none = static_cast<Elt>(-INFINITY);
-  const bool same = (reinterpret_cast<uintptr_t>(out) & 15) == row.phase * sizeof(Elt);
-  for (int j = threadIdx.x; j < row.vecs; j += kSampleThreads) {
-    float x[E];
-    row.load(j, x);
-    const int first = E * j - row.phase;
-    __align__(16) Elt y[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float r = infinite ? (x[e] == INFINITY ? 0.f : -INFINITY) : x[e];
-      const uint32_t k = key_of(r);
-      y[e] = r != -INFINITY && (k > key || (k == key && first + e <= last)) ? static_cast<Elt>(x[e]) : none;
-    }
-    if (same && first >= 0 && first + E <= row.V) {
-      *reinterpret_cast<uint4*>(out + first) = *reinterpret_cast<const uint4*>(y);
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (first + e >= 0 && first + e < row.V) out[first + e] = y[e];
-    }
+__device__ __forceinline__ uint32_t least_key(const SampleJob<Elt>& job, uint32_t no, uint32_t yes, unsigned long long least) {
+  // (keys of bf16 logits differ in their first half)
+  constexpr int kShift = sizeof(Elt) == 2 ? 16 : 0;
+  constexpr uint32_t kRest = (1u << kShift) - 1;
+  const int lane = threadIdx.x & 31;
+  // negative logits' keys end in ones, the others' in zeros
+  auto logit = [&](uint32_t k) { return of_key(kShift == 0 ? k : (k << kShift) | ((k >> 15) != 0 ? 0 : kRest)); };
+  no >>= kShift;
+  yes >>= kShift;
+  while (yes - no > 1) {
+    const uint32_t step = (yes - no + 31) / 32, at = no + step * (lane + 1);
+    const bool enough = at >= yes || job.weight(logit(at)) >= least;
+    const int first = __ffs(__ballot_sync(0xFFFFFFFFu, enough)) - 1;
+    yes = min(no + step * (first + 1), yes);
+    no += step * first;
   }
+  return key_of(logit(yes));
 }
 
-// One CTA a row.
+// One cluster a row.
 template <typename Elt>
-__global__ void __launch_bounds__(kSampleThreads, 3) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) sample_kernel(const SampleArgs a, int ctas) {
   extern __shared__ __align__(16) unsigned char sample_smem[];
-  SampleShared& s = *reinterpret_cast<SampleShared*>(sample_smem);
-  constexpr int E = SampleRow<Elt>::E;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / (a.n_max + 1), j = blockIdx.x - b * (a.n_max + 1);
-  const long long r = blockIdx.x;
+  using Bins = SampleBinsOf<Elt>;
+  SampleSmem<Elt>& smem = *reinterpret_cast<SampleSmem<Elt>*>(sample_smem);
+  SampleFast<Elt>& s = smem.fast;
+  const int tid = threadIdx.x;
+  const int rank = ctas > 1 ? static_cast<int>(blockIdx.x % ctas) : 0;
+  const long long r = blockIdx.x / ctas;
+  const int b = static_cast<int>(r / (a.n_max + 1)), place = static_cast<int>(r - static_cast<long long>(b) * (a.n_max + 1));
   uint32_t bad = 0;
   int n = a.draft_len != nullptr ? a.draft_len[b] : a.n_max;
   if (n < 0 || n > a.n_max) {
     bad |= SPECDEC_DEV_ERR_DRAFT_LEN;
     n = max(0, min(n, a.n_max));
   }
-  if (j > n) {
-    if (tid == 0 && a.tokens != nullptr) a.tokens[r] = -1;
-    if (tid == 0 && j == n + 1 && bad != 0 && a.err != nullptr) atomicOr(a.err, bad);
+  const bool first = rank == 0 && tid == 0;
+  if (place > n) {
+    if (first && a.tokens != nullptr) a.tokens[r] = -1;
+    if (first && bad != 0 && a.err != nullptr) atomicOr(a.err, bad);
     return;
   }
   const Elt* logits = static_cast<const Elt*>(a.logits) + r * a.V;
   Elt* out = a.out != nullptr ? static_cast<Elt*>(a.out) + r * a.V : nullptr;
-  const float T = a.temperature != nullptr ? a.temperature[b] : 1.f;
-  const bool cold = !(T >= 1e-6f) || T > 3e38f;
-  if (cold && T != 0.f) bad |= SPECDEC_DEV_ERR_TEMPERATURE;
-  int k = a.top_k != nullptr ? a.top_k[b] : 0;
-  if (k <= 0 || k > a.V) k = a.V;
-  float p = a.top_p != nullptr ? a.top_p[b] : 1.f, m = a.min_p != nullptr ? a.min_p[b] : 0.f;
-  float u = a.uniform != nullptr ? a.uniform[r] : 0.f;
-  if (!(p >= 0.f) || !(m <= 1.f) || !(m >= 0.f)) {
-    bad |= SPECDEC_DEV_ERR_SAMPLE;
-    if (!(p >= 0.f)) p = 1.f;
-    if (!(m >= 0.f)) m = 0.f;
-    if (!(m <= 1.f)) m = 1.f;
+  int32_t* token = a.tokens != nullptr ? a.tokens + r : nullptr;
+  SampleAsk ask;
+  {
+    const float T = a.temperature != nullptr ? a.temperature[b] : 1.f;
+    float m = a.min_p != nullptr ? a.min_p[b] : 0.f;
+    ask.p = a.top_p != nullptr ? a.top_p[b] : 1.f;
+    ask.u = a.uniform != nullptr ? a.uniform[r] : 0.f;
+    ask.k = a.top_k != nullptr ? a.top_k[b] : 0;
+    if (ask.k <= 0 || ask.k > a.V) ask.k = a.V;
+    ask.cold = !(T >= 1e-6f) || T > 3e38f;
+    if (ask.cold && T != 0.f) bad |= SPECDEC_DEV_ERR_TEMPERATURE;
+    if (!(ask.p >= 0.f) || !(m <= 1.f) || !(m >= 0.f)) {
+      bad |= SPECDEC_DEV_ERR_SAMPLE;
+      if (!(ask.p >= 0.f)) ask.p = 1.f;
+      m = !(m >= 0.f) ? 0.f : fminf(m, 1.f);
+    }
+    if (!(ask.u >= 0.f && ask.u < 1.f)) {
+      bad |= SPECDEC_DEV_ERR_SAMPLE;
+      ask.u = ask.u >= 1.f ? 1.f - 0x1p-24f : 0.f;
+    }
+    // (64-bit arithmetic by one thread: it has 1/64 of the rate)
+    if (tid == 0) {
+      const double c = ask.cold ? 1.0 : 1.4426950408889634074 / static_cast<double>(T);
+      ask.scale.hi = static_cast<float>(c);
+      ask.scale.lo = static_cast<float>(c - static_cast<double>(ask.scale.hi));
+      ask.least = m > 0.f ? static_cast<unsigned long long>(ceil(static_cast<double>(m) * static_cast<double>(kWeightOne))) : 0;
+      s.ask = ask;
+    }
   }
-  if (!(u >= 0.f && u < 1.f)) {
-    bad |= SPECDEC_DEV_ERR_SAMPLE;
-    u = u >= 1.f ? 1.f - 0x1p-24f : 0.f;
-  }
-  if (tid < 256) s.table[tid] = kExp2Table[tid];
-  if (tid == 0) {
-    const double c = cold ? 1.0 : 1.4426950408889634074 / static_cast<double>(T);
-    s.scale.hi = static_cast<float>(c);
-    s.scale.lo = static_cast<float>(c - static_cast<double>(s.scale.hi));
-    s.least = static_cast<unsigned long long>(ceil(static_cast<double>(m) * static_cast<double>(kWeightOne)));
-  }
-  const SampleRow<Elt> row(logits, a.V);
-  // the largest logit, and the first id that has it
-  float best = -INFINITY;
-  int best_id = 0x7FFFFFFF;
-#pragma unroll 4
-  for (int v = tid; v < row.vecs; v += kSampleThreads) {
-    float x[E];
-    row.load(v, x);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (x[e] > best) best = x[e], best_id = E * v + e - row.phase;
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    const float o = __shfl_xor_sync(0xFFFFFFFFu, best, d);
-    const int id = __shfl_xor_sync(0xFFFFFFFFu, best_id, d);
-    if (o > best || (o == best && id < best_id)) best = o, best_id = id;
-  }
-  if (lane == 0) s.best[warp] = best, s.best_id[warp] = best_id;
-  clear_bins(s);
-  __syncthreads();
-#pragma unroll 1
-  for (int i = 0; i < kSampleWarps; ++i)
-    if (s.best[i] > best || (s.best[i] == best && s.best_id[i] < best_id)) best = s.best[i], best_id = s.best_id[i];
-  if (best == -INFINITY) {
-    bad |= SPECDEC_DEV_ERR_SAMPLE;
-    best_id = -1;
-  }
-  if (tid == 0 && bad != 0 && a.err != nullptr) atomicOr(a.err, bad);
-  const bool infinite = best == INFINITY;
-  if (cold || k == 1 || best == -INFINITY) {
-    if (tid == 0 && a.tokens != nullptr) a.tokens[r] = best_id;
-    if (out != nullptr) write_cut_row(row, out, infinite ? key_of(0.f) : key_of(best), best_id, infinite);
+  SampleRow<Elt> row(logits, a.V);
+  const int share = (row.vecs + ctas - 1) / ctas;
+  SampleJob<Elt> job = {s, row, cooperative_groups::this_cluster(), ctas, rank, min(row.vecs, rank * share),
+                        min(row.vecs, rank * share + share), 0.f, {}};
+  if (ask.cold || ask.k == 1) {
+    uint32_t key;
+    int id;
+    if (ctas > 1) job.cluster.sync();  // (the others have begun)
+    job.largest(&key, &id);
+    if (key <= kKeyFloor) bad |= SPECDEC_DEV_ERR_SAMPLE, id = -1;
+    if (first && token != nullptr) *token = id;
+    if (first && bad != 0 && a.err != nullptr) atomicOr(a.err, bad);
+    if (out != nullptr) job.write_one(out, id);
+    if (ctas > 1) job.cluster.sync();
     return;
   }
 
-  Sampler<Elt> f = {s, row, best, infinite, s.scale};
-  f.each([&](float x, int) {
-    if (x == -INFINITY) return;
-    const int bin = f.bin_of(x);
-    atomicAdd(&s.count[bin], 1u);
-    add_weight(s, bin, f.weight(x));
-  });
+  // the histogram, and the largest logit
+  {
+    uint4* z = reinterpret_cast<uint4*>(&s.bins);
+    constexpr int kClear = (sizeof(Elt) == 2 ? 1 : 3) * Bins::kBins / 4;
+    for (int i = tid; i < kClear; i += kSampleThreads) z[i] = make_uint4(0, 0, 0, 0);
+    if (tid < 256) s.table[tid] = kExp2Table[tid];
+    if (tid == 0) s.listed = 0;
+  }
   __syncthreads();
-  BinSums sums;
-  sum_bins(s, sums);
-  // what is kept: larger keys, and the first ids of this one; its weight
-  SamplePlace kept = {kKeyFloor + 1, 0, 0, sums.w_all};
-  unsigned long long weight = sums.w_all;
-  if (static_cast<uint32_t>(k) < sums.c_all) {
-    find_bin(s, sums, kByCount, k);
-    // (the sums before the key are needed as well: by key, once it is known)
-    kept = f.refine(kByCount, k);
-    const uint32_t ids = kept.ids;
-    const int bin = f.bin_of(of_key(kept.key));
-    __syncthreads();
-    if (bin / kBinsOfThread == tid) {
+  ask = s.ask;
+  job.scale = ask.scale;
+  bool simple = true;
+  const bool counted = sizeof(Elt) == 2 || ask.k < a.V;
+  if constexpr (sizeof(Elt) == 2) {
+    uint32_t least = 0xFFFFFFFFu, far = 0;
+    auto add = [&](uint32_t bin, uint32_t b16) {
+      if (bin < Bins::kBins - 1)
+        atomicAdd(&s.bins.count[bin], 1u);
+      else
+        far |= b16 < 0xFF80u ? 1 : 0;  // (not -infinity, and no NaN)
+    };
+    job.each(
+        [&](const uint4& q, int) {
+          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int i = 0; i < kBinsOfThread; ++i)
-        if (i == bin % kBinsOfThread) s.bin = bin, s.count_before = sums.c[i], s.sum_before = sums.w[i], s.ids = sums.c[i + 1] - sums.c[i];
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t d = Bins::two(w[i]);
+            least = __vminu2(least, d);
+            add(d & 0xFFFFu, w[i] & 0xFFFFu);
+            add(d >> 16, w[i] >> 16);
+          }
+        },
+        [&](uint32_t b16, int) {
+          const uint32_t d = Bins::two(b16) & 0xFFFFu;
+          least = __vminu2(least, d | 0xFFFF0000u);
+          add(d, b16);
+        });
+    least = __reduce_min_sync(0xFFFFFFFFu, min(least & 0xFFFFu, least >> 16));
+    far = __reduce_or_sync(0xFFFFFFFFu, far);
+    if ((tid & 31) == 0) s.warp_count[tid >> 5][0] = least, s.warp_count[tid >> 5][1] = far;
+    if (ctas > 1) job.cluster.sync();  // (the others have begun, and read no memory of before)
+    __syncthreads();
+    if (tid < ctas) {
+      for (int w = 0; w < kSampleWarps; ++w) least = min(least, s.warp_count[w][0]), far |= s.warp_count[w][1];
+      job.of(tid).top[rank] = least;
+      job.of(tid).flag[rank] = far;
     }
-    __syncthreads();
-    kept = f.refine(kByKey, kept.key);
-    kept.ids = ids;
-    weight = kept.sum + ids * f.weight(of_key(kept.key));
-  }
-  if (p < 1.f) {
-    const double goal = ceil(static_cast<double>(p) * static_cast<double>(weight));
-    unsigned long long target = static_cast<unsigned long long>(goal);
-    target = target < 1 ? 1 : (target > weight ? weight : target);
-    __syncthreads();
-    find_bin(s, sums, kBySumTo, target);
-    const SamplePlace at = f.refine(kBySumTo, target);
-    // (a beginning of what top-k left)
-    if (at.key > kept.key || (at.key == kept.key && at.ids < kept.ids)) {
-      kept = at;
-      weight = kept.sum + kept.ids * f.weight(of_key(kept.key));
+    job.meet();
+    least = Bins::kBins, far = 0;
+    for (int o = 0; o < ctas; ++o) least = min(least, s.top[o]), far |= s.flag[o];
+    // rows whose order or weights the bins do not tell
+    const int top = static_cast<int>(least);
+    simple = top > 0 && top < Bins::kBins - 1 && top != Bins::kHalf - 1 && top != Bins::kHalf;
+    job.top = Bins::value(top);
+    if (simple && far != 0)
+      simple = (job.top + 4096.f) * ask.scale.hi > 49.f && ask.k == a.V;
+    if (simple && ask.scale.hi > 2955.f) simple = false;  // (below 2^-52 weights may differ: temperatures under 2^-11)
+  } else {
+    uint32_t key;
+    int id;
+    if (ctas > 1) job.cluster.sync();
+    job.largest(&key, &id);
+    simple = key > kKeyFloor && key < key_of(INFINITY);
+    job.top = of_key(key);
+    if (simple) {
+      job.each_id([&](float x, int) {
+        if (x == -INFINITY) return;
+        const int bin = Bins::one(x);
+        if (counted) atomicAdd(&s.bins.count[bin], 1u);
+        const unsigned long long w = job.weight(x);
+        const uint32_t lo = static_cast<uint32_t>(w);
+        uint32_t hi = static_cast<uint32_t>(w >> 32);
+        if (lo != 0) {
+          const uint32_t old = atomicAdd(&s.bins.lo[bin], lo);
+          hi += old + lo < old ? 1 : 0;
+        }
+        if (hi != 0) atomicAdd(&s.bins.hi[bin], hi);
+      });
+      job.meet();
     }
   }
-  if (m > 0.f && f.weight(kept.key > kKeyFloor + 1 ? of_key(kept.key) : -3.4e38f) < s.least) {
-    // the least key with enough weight: 32 of them are looked at a time
-    __syncthreads();
-    if (warp == 0) {
-      uint32_t no = kept.key, yes = key_of(infinite ? 0.f : best);  // no < yes; yes has enough
-      while (yes - no > 1) {
-        const uint32_t step = (yes - no + 31) / 32, at = no + step * (lane + 1);
-        const bool enough = at >= yes || f.weight(of_key(at)) >= s.least;
-        const int first = __ffs(__ballot_sync(0xFFFFFFFFu, enough)) - 1;
-        const uint32_t up = min(no + step * (first + 1), yes);
-        no = no + step * first;
-        yes = up;
+
+  SamplePlace kept = {kKeyFloor + 1, 0, 0, 0}, drawn = {0, 0, 0, 0};
+  if (simple) {
+    job.add_up();
+    SampleBin f;
+    unsigned long long weight = s.group_sum[Bins::kGroups];
+    if (ask.k < a.V && job.find(kByCount, ask.k, &f)) {
+      simple = job.resolve(f, kByCount, ask.k, &kept);
+      weight = kept.sum + kept.ids * job.weight(of_key(kept.key));
+    }
+    if (simple && ask.p < 1.f) {
+      unsigned long long target = static_cast<unsigned long long>(ceil(static_cast<double>(ask.p) * static_cast<double>(weight)));
+      target = target < 1 ? 1 : (target > weight ? weight : target);
+      SamplePlace at;
+      job.find(kBySumTo, target, &f);
+      simple = job.resolve(f, kBySumTo, target, &at);
+      // (a beginning of what top-k left)
+      if (simple && (at.key > kept.key || (at.key == kept.key && at.ids < kept.ids))) {
+        kept = at;
+        weight = kept.sum + kept.ids * job.weight(of_key(kept.key));
       }
-      if (lane == 0) s.listed = yes;
     }
-    __syncthreads();
-    const uint32_t key = s.listed;
-    const int bin = f.bin_of(of_key(key));
-    __syncthreads();
-    if (bin / kBinsOfThread == tid) {
-#pragma unroll
-      for (int i = 0; i < kBinsOfThread; ++i)
-        if (i == bin % kBinsOfThread) s.bin = bin, s.count_before = sums.c[i], s.sum_before = sums.w[i], s.ids = sums.c[i + 1] - sums.c[i];
+    if (simple && ask.least > 0 && (kept.key <= kKeyFloor + 1 || job.weight(of_key(kept.key)) < ask.least)) {
+      const uint32_t key = least_key(job, kept.key, key_of(job.top), ask.least);
+      job.look_up(Bins::one(of_key(key)), &f);
+      simple = job.resolve(f, kByKey, key, &kept);
+      kept.key = key;
+      kept.ids = kept.all;
+      weight = sizeof(Elt) == 2 ? kept.sum + f.w : kept.sum;
     }
-    __syncthreads();
-    kept = f.refine(kByKey, key);
-    weight = kept.sum + kept.ids * f.weight(of_key(kept.key));
-  }
-  if (a.tokens != nullptr) {
-    int id = best_id;
-    if (a.uniform != nullptr) {
-      unsigned long long target = static_cast<unsigned long long>(static_cast<double>(u) * static_cast<double>(weight));
+    if (simple && token != nullptr) {
+      unsigned long long target = static_cast<unsigned long long>(static_cast<double>(ask.u) * static_cast<double>(weight));
       if (target >= weight) target = weight - 1;
-      __syncthreads();
-      find_bin(s, sums, kBySumPast, target);
-      const SamplePlace at = f.refine(kBySumPast, target);
-      id = f.nth(at.key, at.ids);
+      job.find(kBySumPast, target, &f);
+      simple = job.resolve(f, kBySumPast, target, &drawn);
     }
-    if (tid == 0) a.tokens[r] = id;
   }
-  if (out != nullptr) {
-    const int last = kept.ids < kept.all ? f.nth(kept.key, kept.ids) : a.V;
-    write_cut_row(row, out, kept.key, last, infinite);
+  if (!simple) {
+    // by the first CTA alone, whose memory nobody reads any more
+    job.meet();
+    if (rank == 0) {
+      if (!sample_any(smem.any, row, ask, out, token)) bad |= SPECDEC_DEV_ERR_SAMPLE;
+      if (first && bad != 0 && a.err != nullptr) atomicOr(a.err, bad);
+    }
+    return;
   }
+  if (first && bad != 0 && a.err != nullptr) atomicOr(a.err, bad);
+  int last = a.V;
+  const bool part = out != nullptr && kept.ids < kept.all;
+  if (token != nullptr || part) {
+    const uint32_t keys[2] = {drawn.key, kept.key}, ids[2] = {token != nullptr ? drawn.ids : 0, part ? kept.ids : 0};
+    int id[2];
+    job.nth(keys, ids, id);
+    if (first && token != nullptr) *token = id[0];
+    if (part) last = id[1];
+  }
+  if (out != nullptr) job.write(out, kept.key, last);
+  if (ctas > 1) job.cluster.sync();  // (memory that others may still read)
 }
 
 }  // namespace specdec

@@ -13,9 +13,10 @@
 //   - fp32: a second pass adds every id's weight to its bin; the ids of a border's
 //     bin are listed and looked at one by one.
 //
-// Bins of 32 have their sums in shared memory too, so that every warp finds a
-// border by itself, in three looks of its lanes, without a barrier.  Then ids of the
-// borders' logits are counted in their order, and the row is written.
+// Groups of 16 bins have their sums in shared memory too, so that a warp finds a
+// border by itself, in three looks of its lanes, without a barrier.  The row is
+// written in a last pass, which marks where ids of the borders' logits are: those
+// past a border in the order of the ids are taken back, and one is the token.
 //
 // A row is one cluster's of 1 to 8 CTAs, as few as keep the SMs busy; each has a
 // part of the row, a histogram of it, and a share of the bins to add up.
@@ -27,19 +28,18 @@
 namespace specdec {
 
 constexpr int kSampleClusterMax = 8;
-constexpr int kNear = 1024;   // ids of a border's bin that are listed (fp32)
+constexpr int kNear = 512;    // ids of a border's bin that are listed (fp32)
+constexpr int kSampleGroups = kSampleThreads;  // of neighbouring bins, whose sums are kept
 
 // Bins of a logit's first 16 bits, the largest first: magnitudes from 2^12 down
 // have one for each 7 bits of mantissa; what is above is in the outermost bins and
 // what is below in the two of zero.
 template <typename Elt>
 struct SampleBinsOf {
-  static constexpr bool kWhole = sizeof(Elt) == 2;
-  static constexpr int kBins = kWhole ? 16384 : 8192;
-  static constexpr int kGroups = kBins / 32;
+  static constexpr int kBins = 8192;
   static constexpr int kHalf = kBins / 2;
   static constexpr uint32_t kTop = (127 + 12) << 7;          // 2^12 and above
-  static constexpr uint32_t kBase = kTop - (kHalf - 1);      // below the least
+  static constexpr uint32_t kBase = kTop - (kHalf - 1);      // about 2^-20 and below
 
   // of two logits' bits at once, a half each
   static __device__ __forceinline__ uint32_t two(uint32_t w) {
@@ -64,7 +64,7 @@ template <typename Elt>
 struct SampleBinsShared;
 template <>
 struct SampleBinsShared<__nv_bfloat16> {
-  uint32_t count[16384];
+  uint32_t count[8192];
 };
 template <>
 struct SampleBinsShared<float> {
@@ -73,6 +73,11 @@ struct SampleBinsShared<float> {
   unsigned long long near_weight[kNear];
 };
 
+// A bit for each vector of a CTA's part in which a border's logit is: in the bins'
+// place, once these are done with.
+constexpr int kMarkWords = (SPECDEC_MAX_VOCAB / 4 + 2 + 31) / 32;
+static_assert(sizeof(uint32_t) * kMarkWords <= sizeof(SampleBinsShared<__nv_bfloat16>), "the marks lie where the bins were");
+
 struct SampleAnswer {
   uint32_t key, ids, all, bad;
   unsigned long long sum, count;
@@ -80,10 +85,12 @@ struct SampleAnswer {
 
 template <typename Elt>
 struct SampleFast {
-  static constexpr int kGroups = SampleBinsOf<Elt>::kGroups;
-  alignas(16) SampleBinsShared<Elt> bins;
-  unsigned long long group_sum[kGroups + 2];  // of 32 bins, then before them
-  uint32_t group_count[kGroups + 2];
+  union {
+    alignas(16) SampleBinsShared<Elt> bins;
+    uint32_t marks[kMarkWords];
+  };
+  unsigned long long group_sum[kSampleGroups + 2];  // of 16 bins, then before them
+  uint32_t group_count[kSampleGroups + 2];
   ExpPair table[256];
   unsigned long long warp_sum[kSampleWarps];
   uint32_t warp_count[kSampleWarps][2];
@@ -91,8 +98,11 @@ struct SampleFast {
   uint32_t top[kSampleClusterMax], flag[kSampleClusterMax];
   int32_t id[kSampleClusterMax];
   uint32_t same[kSampleClusterMax][2];
-  int32_t found[2];
   uint32_t listed;
+  unsigned long long zero[2];   // sums of the bins of zero
+  bool zeroed;                  // they are in use
+  SamplePlace kept, drawn;
+  bool simple;
   SampleAnswer answer;
   SampleAsk ask;
 };
@@ -110,19 +120,12 @@ struct SampleBin {
   unsigned long long w0, w;
 };
 
-// Sum over a warp, of less than 2^64 in all.
-__device__ __forceinline__ unsigned long long warp_sum64(unsigned long long w) {
-  const uint32_t a = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(w) & 0x3FFFFFu);
-  const uint32_t b = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(w >> 22) & 0x3FFFFFu);
-  const uint32_t c = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(w >> 44));
-  return a + (static_cast<unsigned long long>(b) << 22) + (static_cast<unsigned long long>(c) << 44);
-}
-
 template <typename Elt>
 struct SampleJob {
   using Bins = SampleBinsOf<Elt>;
   static constexpr int E = SampleRow<Elt>::E;
-  static constexpr int kGroups = Bins::kGroups;
+  static constexpr int kGroups = kSampleGroups;
+  static constexpr int kOfGroup = Bins::kBins / kGroups;
   SampleFast<Elt>& s;
   const SampleRow<Elt> row;
   cooperative_groups::cluster_group cluster;
@@ -189,43 +192,58 @@ struct SampleJob {
 
   // A bin's count and sum, over the cluster, from the CTA that added them up.
   __device__ __forceinline__ void bin_of_cluster(int bin, uint32_t* c, unsigned long long* w) const {
-    const SampleFast<Elt>& o = ctas > 1 ? of(bin / 32 / (kGroups / ctas)) : s;
+    const SampleFast<Elt>& o = ctas > 1 ? of(bin / (Bins::kBins / ctas)) : s;
     *c = o.bins.count[bin];
     if constexpr (sizeof(Elt) == 2)
-      *w = *c != 0 ? *c * weight(Bins::value(bin)) : 0;
+      *w = *c == 0 ? 0 : (s.zeroed && (bin == Bins::kHalf - 1 || bin == Bins::kHalf) ? s.zero[bin - (Bins::kHalf - 1)] : *c * weight(Bins::value(bin)));
     else
       *w = (static_cast<unsigned long long>(o.bins.hi[bin]) << 32) + o.bins.lo[bin];
   }
 
   // Adds the CTAs' histograms up, a share of the bins each, and the sums of every
-  // 32 bins, which all CTAs get.
+  // group, which all CTAs get.  A group is one thread's, or as many threads' as
+  // there are CTAs.
   __device__ __forceinline__ void add_up() {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = kGroups / ctas;
-    for (int g = rank * share + warp; g < (rank + 1) * share; g += kSampleWarps) {
-      const int bin = 32 * g + lane;
-      uint32_t c = 0;
-      unsigned long long w = 0;
-      for (int o = 0; o < ctas; ++o) {
-        const SampleFast<Elt>& x = ctas > 1 ? of(o) : s;
-        c += x.bins.count[bin];
-        if constexpr (sizeof(Elt) == 4) w += (static_cast<unsigned long long>(x.bins.hi[bin]) << 32) + x.bins.lo[bin];
-      }
-      if (ctas > 1) {
-        s.bins.count[bin] = c;
-        if constexpr (sizeof(Elt) == 4) s.bins.lo[bin] = static_cast<uint32_t>(w), s.bins.hi[bin] = static_cast<uint32_t>(w >> 32);
-      }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, of_thread = kOfGroup / ctas;
+    const int me = rank * kSampleThreads + threadIdx.x;
+    {
+      uint32_t cs = 0;
       unsigned long long ws = 0;
-      if constexpr (sizeof(Elt) == 2) {
-        if (__any_sync(0xFFFFFFFFu, c != 0)) ws = warp_sum64(c != 0 ? c * weight(Bins::value(bin)) : 0);
-      } else {
-        ws = warp_sum64(w);
+#pragma unroll 2
+      for (int i = 0; i < of_thread; i += 2) {
+        const int bin = me * of_thread + i;
+        uint2 c = make_uint2(0, 0);
+        unsigned long long w = 0, x = 0;
+        for (int o = 0; o < ctas; ++o) {
+          const SampleFast<Elt>& from = ctas > 1 ? of(o) : s;
+          const uint2 d = *reinterpret_cast<const uint2*>(&from.bins.count[bin]);
+          c.x += d.x, c.y += d.y;
+          if constexpr (sizeof(Elt) == 4) {
+            const uint2 lo = *reinterpret_cast<const uint2*>(&from.bins.lo[bin]), hi = *reinterpret_cast<const uint2*>(&from.bins.hi[bin]);
+            w += (static_cast<unsigned long long>(hi.x) << 32) + lo.x;
+            x += (static_cast<unsigned long long>(hi.y) << 32) + lo.y;
+          }
+        }
+        if (ctas > 1) {
+          *reinterpret_cast<uint2*>(&s.bins.count[bin]) = c;
+          if constexpr (sizeof(Elt) == 4) {
+            *reinterpret_cast<uint2*>(&s.bins.lo[bin]) = make_uint2(static_cast<uint32_t>(w), static_cast<uint32_t>(x));
+            *reinterpret_cast<uint2*>(&s.bins.hi[bin]) = make_uint2(static_cast<uint32_t>(w >> 32), static_cast<uint32_t>(x >> 32));
+          }
+        }
+        if constexpr (sizeof(Elt) == 2) {
+          if ((c.x | c.y) != 0) w = c.x * weight(Bins::value(bin)), x = c.y * weight(Bins::value(bin + 1));
+        }
+        cs += c.x + c.y;
+        ws += w + x;
       }
-      const uint32_t cs = __reduce_add_sync(0xFFFFFFFFu, c);
-      if (lane < ctas) {
-        SampleFast<Elt>& x = ctas > 1 ? of(lane) : s;
-        x.group_count[g] = cs;
-        x.group_sum[g] = ws;
+      for (int d = 1; d < ctas; d <<= 1) {
+        cs += __shfl_xor_sync(0xFFFFFFFFu, cs, d);
+        ws += __shfl_xor_sync(0xFFFFFFFFu, ws, d);
       }
+      SampleFast<Elt>& to = ctas > 1 ? of(threadIdx.x % ctas) : s;
+      to.group_count[me / ctas] = cs;
+      to.group_sum[me / ctas] = ws;
     }
     meet();
     // sums before each group
@@ -250,6 +268,32 @@ struct SampleJob {
     __syncthreads();
   }
 
+  // The bins of zero have logits up to 2^-20, whose weights differ by that over T:
+  // where they matter, each id's own weight is added.
+  __device__ __forceinline__ void add_zeros() {
+    uint32_t c[2];
+    unsigned long long w[2];
+    bin_of_cluster(Bins::kHalf - 1, &c[0], &w[0]);
+    bin_of_cluster(Bins::kHalf, &c[1], &w[1]);
+    if (!(static_cast<float>(w[0] + w[1]) * scale.hi * 0x1p21f > static_cast<float>(s.group_sum[kGroups]))) return;
+    meet();
+    unsigned long long mine[2] = {0, 0};
+    each_id([&](float x, int) {
+      const int bin = Bins::one(x) - (Bins::kHalf - 1);
+      if (x != -INFINITY && (bin == 0 || bin == 1)) mine[bin] += weight(x);
+    });
+    for (int i = 0; i < 2; ++i)
+      if (mine[i] != 0)
+        for (int o = 0; o < ctas; ++o) atomicAdd(&of(o).zero[i], mine[i]);
+    meet();
+    const unsigned long long more[2] = {s.zero[0] - w[0], s.zero[1] - w[1]};
+    constexpr int kFirst = (Bins::kHalf - 1) / kOfGroup;
+    for (int g = threadIdx.x; g <= kGroups; g += kSampleThreads) s.group_sum[g] += (g > kFirst ? more[0] : 0) + (g > kFirst + 1 ? more[1] : 0);
+    if (threadIdx.x == 0) s.zeroed = true;
+    __syncthreads();
+  }
+  __device__ __forceinline__ bool decide(const SampleAsk& ask, bool draw, SamplePlace* kept, SamplePlace* drawn);
+
   // The bin in which a border lies, by each warp for itself; false if there is none.
   __device__ __forceinline__ bool find(SampleBorder by, unsigned long long target, SampleBin* f) const {
     constexpr int kStep = kGroups / 32;
@@ -265,27 +309,27 @@ struct SampleJob {
   }
   // The bin itself and what is before it.
   __device__ __forceinline__ void look_up(int bin, SampleBin* f) const {
-    within(bin >> 5, [&](uint32_t, uint32_t, unsigned long long, unsigned long long, int lane) { return lane >= (bin & 31); }, f);
+    within(bin / kOfGroup, [&](uint32_t, uint32_t, unsigned long long, unsigned long long, int lane) { return lane >= bin % kOfGroup; }, f);
   }
   template <typename F>
   __device__ __forceinline__ void within(int g, F passed, SampleBin* f) const {
     const int lane = threadIdx.x & 31;
-    uint32_t c;
-    unsigned long long w;
-    bin_of_cluster(32 * g + lane, &c, &w);
+    uint32_t c = 0;
+    unsigned long long w = 0;
+    if (lane < kOfGroup) bin_of_cluster(kOfGroup * g + lane, &c, &w);
     uint32_t c1 = c;
     unsigned long long w1 = w;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
+    for (int d = 1; d < kOfGroup; d <<= 1) {
       const uint32_t co = __shfl_up_sync(0xFFFFFFFFu, c1, d);
       const unsigned long long wo = __shfl_up_sync(0xFFFFFFFFu, w1, d);
       if (lane >= d) c1 += co, w1 += wo;
     }
     c1 += s.group_count[g];
     w1 += s.group_sum[g];
-    const uint32_t m = __ballot_sync(0xFFFFFFFFu, lane == 31 || passed(c1 - c, c1, w1 - w, w1, lane));
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, lane >= kOfGroup - 1 || passed(c1 - c, c1, w1 - w, w1, lane));
     const int at = __ffs(m) - 1;
-    f->bin = 32 * g + at;
+    f->bin = kOfGroup * g + at;
     f->c0 = __shfl_sync(0xFFFFFFFFu, c1 - c, at);
     f->c = __shfl_sync(0xFFFFFFFFu, c, at);
     f->w0 = __shfl_sync(0xFFFFFFFFu, w1 - w, at);
@@ -366,91 +410,47 @@ struct SampleJob {
     }
   }
 
-  // The ids that are the first[i]-th (1 and on; 0: none) of those with key[i].
-  __device__ __forceinline__ void nth(const uint32_t (&key)[2], const uint32_t (&first)[2], int (&id)[2]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int part = (j1 - j0 + kSampleWarps - 1) / kSampleWarps, v0 = min(j1, j0 + warp * part), v1 = min(j1, v0 + part);
-    auto count = [&](int j, uint32_t (&n)[2]) {
-      float x[E];
-      row.load(j, x);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const uint32_t k = key_of(x[e]);
-        n[0] += k == key[0] ? 1 : 0;
-        n[1] += k == key[1] ? 1 : 0;
-      }
-    };
-    uint32_t mine[2] = {0, 0};
-#pragma unroll 4
-    for (int j = v0 + lane; j < v1; j += 32) count(j, mine);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      mine[i] = __reduce_add_sync(0xFFFFFFFFu, mine[i]);
-      if (lane == 0) s.warp_count[warp][i] = mine[i];
-    }
+  // Room for the marks, where no one reads the bins any more.
+  __device__ __forceinline__ void clear_marks() {
+    meet();
+    for (int i = threadIdx.x; i <= (j1 - j0) / 32; i += kSampleThreads) s.marks[i] = 0;
     __syncthreads();
-    if (threadIdx.x < 2 * ctas) {
-      const int i = threadIdx.x & 1;
-      uint32_t n = 0;
-      for (int w = 0; w < kSampleWarps; ++w) n += s.warp_count[w][i];
-      of(threadIdx.x >> 1).same[rank][i] = n;
-    }
-    meet();
-#pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-      uint32_t before = 0;
-      for (int o = 0; o < rank; ++o) before += s.same[o][i];
-      for (int w = 0; w < warp; ++w) before += s.warp_count[w][i];
-      if (!(before < first[i] && first[i] <= before + mine[i])) continue;
-      uint32_t left = first[i] - before;
-      for (int j = v0; j < v1; j += 32) {
-        uint32_t here[2] = {0, 0};
-        if (j + lane < v1) count(j + lane, here);
-        uint32_t upto = here[i];
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-          if (lane >= d) upto += o;
-        }
-        if (here[i] != 0 && upto - here[i] < left && left <= upto) {
-          uint32_t k = upto - here[i];
-          float x[E];
-          row.load(j + lane, x);
-          int at = 0;
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (key_of(x[e]) == key[i] && ++k == left) at = E * (j + lane) + e - row.phase;
-          for (int o = 0; o < ctas; ++o) of(o).found[i] = at;
-        }
-        const uint32_t sum = __shfl_sync(0xFFFFFFFFu, upto, 31);
-        if (left <= sum) break;
-        left -= sum;
-      }
-    }
-    meet();
-    id[0] = s.found[0];
-    id[1] = s.found[1];
   }
-
-  // This CTA's part of the row, -infinity for ids whose key is below `key`, or is it
-  // and whose id is past `last`.
-  __device__ __forceinline__ void write(Elt* out, uint32_t key, int last) const {
-    const bool same = (reinterpret_cast<uintptr_t>(out) & 15) == row.phase * sizeof(Elt);
-    const float least = of_key(key), next = of_key(key + 1);  // (key is not infinity's)
-    const Elt none = static_cast<Elt>(-INFINITY);
+  // This CTA's part of the row, -infinity for ids whose key is below `least_kept`;
+  // vectors with ids of key[i], where there is one (not 0), are marked.
+  __device__ __forceinline__ void write(Elt* out, uint32_t least_kept, const uint32_t (&key)[2]) {
+    const bool same = out != nullptr && (reinterpret_cast<uintptr_t>(out) & 15) == row.phase * sizeof(Elt);
+    const float least = of_key(least_kept), none = -INFINITY, nan = __uint_as_float(0x7FFFFFFFu);
+    const bool look = key[0] != 0 || key[1] != 0;
+    const float tie[2] = {key[0] != 0 ? of_key(key[0]) : nan, key[1] != 0 ? of_key(key[1]) : nan};
+    auto mark = [&](int j) { atomicOr(&s.marks[(j - j0) >> 5], 1u << ((j - j0) & 31)); };
+    const __nv_bfloat162 least2 = __float2bfloat162_rn(least);  // (bf16 rows' borders are bf16)
+    const __nv_bfloat162 tie2[2] = {__float2bfloat162_rn(tie[0]), __float2bfloat162_rn(tie[1])};
     each(
         [&](const uint4& q, int j) {
           const int first = E * j - row.phase;
           uint32_t w[4] = {q.x, q.y, q.z, q.w};
+          if (look) {
+            uint32_t tied = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if constexpr (sizeof(Elt) == 2) {
+                const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+                tied |= __heq2_mask(x, tie2[0]) | __heq2_mask(x, tie2[1]);
+              } else {
+                tied |= __uint_as_float(w[i]) == tie[0] || __uint_as_float(w[i]) == tie[1] ? 1u : 0;
+              }
+            }
+            if (tied != 0) mark(j);
+          }
+          if (out == nullptr) return;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (sizeof(Elt) == 2) {
-              const int id = first + 2 * i;
-              const bool a = __uint_as_float(w[i] << 16) >= (id <= last ? least : next);
-              const bool b = __uint_as_float(w[i] & 0xFFFF0000u) >= (id + 1 <= last ? least : next);
-              w[i] = (a ? w[i] & 0xFFFFu : 0xFF80u) | (b ? w[i] & 0xFFFF0000u : 0xFF800000u);
+            if constexpr (sizeof(Elt) == 2) {
+              const uint32_t m = __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), least2);
+              w[i] = (w[i] & m) | (~m & 0xFF80FF80u);
             } else {
-              w[i] = __uint_as_float(w[i]) >= (first + i <= last ? least : next) ? w[i] : 0xFF800000u;
+              w[i] = __uint_as_float(w[i]) >= least ? w[i] : 0xFF800000u;
             }
           }
           if (same) {
@@ -468,8 +468,89 @@ struct SampleJob {
         },
         [&](uint32_t b, int id) {
           const float x = logit(b);
-          out[id] = x >= (id <= last ? least : next) ? static_cast<Elt>(x) : none;
+          if (x == tie[0] || x == tie[1]) mark((id + row.phase) / E);
+          if (out != nullptr) out[id] = static_cast<Elt>(x >= least ? x : none);
         });
+  }
+
+  // f(id, which) for the ids of key[which] in the vectors that word `i` marks, in
+  // their order.  (In place the row still has them.)
+  template <typename F>
+  __device__ __forceinline__ void tied(int i, const uint32_t (&key)[2], F f) const {
+#pragma unroll 1
+    for (uint32_t m = s.marks[i]; m != 0; m &= m - 1) {
+      const int j = j0 + 32 * i + __ffs(m) - 1;
+      float x[E];
+      row.load(j, x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t k = key_of(x[e]);
+        if (k == key[0]) f(E * j + e - row.phase, 0);
+        if (k == key[1]) f(E * j + e - row.phase, 1);
+      }
+    }
+  }
+  // Of the ids with key[i], the ids[0]-th is the token, and those past the ids[1]-th
+  // are not kept.
+  __device__ __forceinline__ void settle(Elt* out, int32_t* token, const uint32_t (&key)[2], const uint32_t (&ids)[2]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // a thread has neighbouring words
+    const int words = (j1 - j0 + 31) / 32, part = (words + kSampleThreads - 1) / kSampleThreads;
+    const int w0 = min(words, static_cast<int>(threadIdx.x) * part), w1 = min(words, w0 + part);
+    __syncthreads();
+    uint32_t n[2] = {0, 0}, upto[2];
+    for (int i = w0; i < w1; ++i) tied(i, key, [&](int, int which) { ++n[which]; });
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      upto[i] = n[i];
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, upto[i], d);
+        if (lane >= d) upto[i] += o;
+      }
+      if (lane == 31) s.warp_count[warp][i] = upto[i];
+    }
+    __syncthreads();
+    if (ctas > 1) {
+      if (threadIdx.x < 2 * ctas) {
+        uint32_t all = 0;
+        for (int w = 0; w < kSampleWarps; ++w) all += s.warp_count[w][threadIdx.x & 1];
+        of(threadIdx.x >> 1).same[rank][threadIdx.x & 1] = all;
+      }
+      cluster.sync();
+    }
+    bool past = false;  // whether this thread has ids that are not kept
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      for (int w = 0; w < warp; ++w) upto[i] += s.warp_count[w][i];
+      if (ctas > 1)
+        for (int o = 0; o < rank; ++o) upto[i] += s.same[o][i];
+      upto[i] -= n[i];
+      if (i == 0)
+        past = past || (ids[0] > upto[0] && ids[0] <= upto[0] + n[0]);
+      else
+        past = past || (ids[1] != 0 && upto[1] + n[1] > ids[1]);
+    }
+    if (!past) return;
+    for (int i = w0; i < w1; ++i)
+      tied(i, key, [&](int id, int which) {
+        const uint32_t at = ++upto[which];
+        if (which == 0 && at == ids[0]) *token = id;
+        if (which == 1 && at > ids[1]) out[id] = static_cast<Elt>(-INFINITY);
+      });
+  }
+
+  // Whether a logit of the row is finite and -4096 or below (bf16).
+  __device__ __forceinline__ bool any_far() {
+    bool far = false;
+    each_id([&](float x, int) { far |= x <= -4096.f && x != -INFINITY; });
+    far = __syncthreads_or(far) != 0;
+    if (ctas > 1) {
+      if (threadIdx.x < ctas) of(threadIdx.x).flag[rank] = far ? 1 : 0;
+      cluster.sync();
+      for (int o = 0; o < ctas; ++o) far |= s.flag[o] != 0;
+    }
+    return far;
   }
 
   // The row with one id left (or none: -1), and that id's logit.
@@ -544,6 +625,45 @@ __device__ __forceinline__ uint32_t least_key(const SampleJob<Elt>& job, uint32_
     no += step * first;
   }
   return key_of(logit(yes));
+}
+
+// What is kept and which logit is drawn; false: the bins do not say.  bf16: by any
+// warp, fp32: by all.
+template <typename Elt>
+__device__ __forceinline__ bool SampleJob<Elt>::decide(const SampleAsk& ask, bool draw, SamplePlace* kept, SamplePlace* drawn) {
+  SampleBin f;
+  unsigned long long weights = s.group_sum[kGroups];
+  if (ask.k < row.V && find(kByCount, ask.k, &f)) {
+    if (!resolve(f, kByCount, ask.k, kept)) return false;
+    weights = kept->sum + kept->ids * weight(of_key(kept->key));
+  }
+  if (ask.p < 1.f) {
+    unsigned long long target = static_cast<unsigned long long>(ceil(static_cast<double>(ask.p) * static_cast<double>(weights)));
+    target = target < 1 ? 1 : (target > weights ? weights : target);
+    SamplePlace at;
+    find(kBySumTo, target, &f);
+    if (!resolve(f, kBySumTo, target, &at)) return false;
+    // (a beginning of what top-k left)
+    if (at.key > kept->key || (at.key == kept->key && at.ids < kept->ids)) {
+      *kept = at;
+      weights = kept->sum + kept->ids * weight(of_key(kept->key));
+    }
+  }
+  if (ask.least > 0 && (kept->key <= kKeyFloor + 1 || weight(of_key(kept->key)) < ask.least)) {
+    const uint32_t key = least_key(*this, kept->key, key_of(top), ask.least);
+    look_up(Bins::one(of_key(key)), &f);
+    if (!resolve(f, kByKey, key, kept)) return false;
+    kept->key = key;
+    kept->ids = kept->all;
+    weights = sizeof(Elt) == 2 ? kept->sum + f.w : kept->sum;
+  }
+  if (draw) {
+    unsigned long long target = static_cast<unsigned long long>(static_cast<double>(ask.u) * static_cast<double>(weights));
+    if (target >= weights) target = weights - 1;
+    find(kBySumPast, target, &f);
+    if (!resolve(f, kBySumPast, target, drawn)) return false;
+  }
+  return true;
 }
 
 // One cluster a row.
@@ -623,7 +743,7 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
     constexpr int kClear = (sizeof(Elt) == 2 ? 1 : 3) * Bins::kBins / 4;
     for (int i = tid; i < kClear; i += kSampleThreads) z[i] = make_uint4(0, 0, 0, 0);
     if (tid < 256) s.table[tid] = kExp2Table[tid];
-    if (tid == 0) s.listed = 0;
+    if (tid == 0) s.listed = 0, s.zeroed = false, s.zero[0] = s.zero[1] = 0;
   }
   __syncthreads();
   ask = s.ask;
@@ -631,12 +751,14 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
   bool simple = true;
   const bool counted = sizeof(Elt) == 2 || ask.k < a.V;
   if constexpr (sizeof(Elt) == 2) {
-    uint32_t least = 0xFFFFFFFFu, far = 0;
-    auto add = [&](uint32_t bin, uint32_t b16) {
-      if (bin < Bins::kBins - 1)
-        atomicAdd(&s.bins.count[bin], 1u);
-      else
-        far |= b16 < 0xFF80u ? 1 : 0;  // (not -infinity, and no NaN)
+    uint32_t least = 0xFFFFFFFFu;
+    // (-infinity's bin is not counted: a masked row's ids would wait for one another)
+    const uint32_t counts = static_cast<uint32_t>(__cvta_generic_to_shared(s.bins.count));
+    auto add = [&](uint32_t bin) {
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "setp.lt.u32 p, %1, %2;\n\t"
+          "@p red.shared::cta.add.u32 [%0], 1;\n\t}" ::"r"(counts + 4 * bin), "r"(bin), "n"(Bins::kBins - 1) : "memory");
     };
     job.each(
         [&](const uint4& q, int) {
@@ -645,35 +767,30 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
           for (int i = 0; i < 4; ++i) {
             const uint32_t d = Bins::two(w[i]);
             least = __vminu2(least, d);
-            add(d & 0xFFFFu, w[i] & 0xFFFFu);
-            add(d >> 16, w[i] >> 16);
+            add(d & 0xFFFFu);
+            add(d >> 16);
           }
         },
         [&](uint32_t b16, int) {
           const uint32_t d = Bins::two(b16) & 0xFFFFu;
           least = __vminu2(least, d | 0xFFFF0000u);
-          add(d, b16);
+          add(d);
         });
     least = __reduce_min_sync(0xFFFFFFFFu, min(least & 0xFFFFu, least >> 16));
-    far = __reduce_or_sync(0xFFFFFFFFu, far);
-    if ((tid & 31) == 0) s.warp_count[tid >> 5][0] = least, s.warp_count[tid >> 5][1] = far;
-    if (ctas > 1) job.cluster.sync();  // (the others have begun, and read no memory of before)
+    if ((tid & 31) == 0) s.warp_count[tid >> 5][0] = least;
+    if (ctas > 1) job.cluster.sync();  // (the others have begun)
     __syncthreads();
     if (tid < ctas) {
-      for (int w = 0; w < kSampleWarps; ++w) least = min(least, s.warp_count[w][0]), far |= s.warp_count[w][1];
+      for (int w = 0; w < kSampleWarps; ++w) least = min(least, s.warp_count[w][0]);
       job.of(tid).top[rank] = least;
-      job.of(tid).flag[rank] = far;
     }
     job.meet();
-    least = Bins::kBins, far = 0;
-    for (int o = 0; o < ctas; ++o) least = min(least, s.top[o]), far |= s.flag[o];
+    least = Bins::kBins;
+    for (int o = 0; o < ctas; ++o) least = min(least, s.top[o]);
     // rows whose order or weights the bins do not tell
     const int top = static_cast<int>(least);
     simple = top > 0 && top < Bins::kBins - 1 && top != Bins::kHalf - 1 && top != Bins::kHalf;
     job.top = Bins::value(top);
-    if (simple && far != 0)
-      simple = (job.top + 4096.f) * ask.scale.hi > 49.f && ask.k == a.V;
-    if (simple && ask.scale.hi > 2955.f) simple = false;  // (below 2^-52 weights may differ: temperatures under 2^-11)
   } else {
     uint32_t key;
     int id;
@@ -702,37 +819,22 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
   SamplePlace kept = {kKeyFloor + 1, 0, 0, 0}, drawn = {0, 0, 0, 0};
   if (simple) {
     job.add_up();
-    SampleBin f;
-    unsigned long long weight = s.group_sum[Bins::kGroups];
-    if (ask.k < a.V && job.find(kByCount, ask.k, &f)) {
-      simple = job.resolve(f, kByCount, ask.k, &kept);
-      weight = kept.sum + kept.ids * job.weight(of_key(kept.key));
-    }
-    if (simple && ask.p < 1.f) {
-      unsigned long long target = static_cast<unsigned long long>(ceil(static_cast<double>(ask.p) * static_cast<double>(weight)));
-      target = target < 1 ? 1 : (target > weight ? weight : target);
-      SamplePlace at;
-      job.find(kBySumTo, target, &f);
-      simple = job.resolve(f, kBySumTo, target, &at);
-      // (a beginning of what top-k left)
-      if (simple && (at.key > kept.key || (at.key == kept.key && at.ids < kept.ids))) {
-        kept = at;
-        weight = kept.sum + kept.ids * job.weight(of_key(kept.key));
+    if constexpr (sizeof(Elt) == 2) {
+      // logits of -4096 and below are not counted: they have no weight and are not kept, or the row is another's
+      const uint32_t ids = s.group_count[kSampleGroups];
+      if ((ask.k < a.V && static_cast<uint32_t>(ask.k) > ids) || !((job.top + 4096.f) * ask.scale.hi > 49.f)) simple = !job.any_far();
+      if (simple) job.add_zeros();
+      // every warp could, but one is enough
+      if (simple) {
+        if (tid < 32) {
+          const bool sure = job.decide(ask, token != nullptr, &kept, &drawn);
+          if (tid == 0) s.kept = kept, s.drawn = drawn, s.simple = sure;
+        }
+        __syncthreads();
+        kept = s.kept, drawn = s.drawn, simple = s.simple;
       }
-    }
-    if (simple && ask.least > 0 && (kept.key <= kKeyFloor + 1 || job.weight(of_key(kept.key)) < ask.least)) {
-      const uint32_t key = least_key(job, kept.key, key_of(job.top), ask.least);
-      job.look_up(Bins::one(of_key(key)), &f);
-      simple = job.resolve(f, kByKey, key, &kept);
-      kept.key = key;
-      kept.ids = kept.all;
-      weight = sizeof(Elt) == 2 ? kept.sum + f.w : kept.sum;
-    }
-    if (simple && token != nullptr) {
-      unsigned long long target = static_cast<unsigned long long>(static_cast<double>(ask.u) * static_cast<double>(weight));
-      if (target >= weight) target = weight - 1;
-      job.find(kBySumPast, target, &f);
-      simple = job.resolve(f, kBySumPast, target, &drawn);
+    } else {
+      simple = job.decide(ask, token != nullptr, &kept, &drawn);
     }
   }
   if (!simple) {
@@ -745,16 +847,13 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
     return;
   }
   if (first && bad != 0 && a.err != nullptr) atomicOr(a.err, bad);
-  int last = a.V;
   const bool part = out != nullptr && kept.ids < kept.all;
-  if (token != nullptr || part) {
-    const uint32_t keys[2] = {drawn.key, kept.key}, ids[2] = {token != nullptr ? drawn.ids : 0, part ? kept.ids : 0};
-    int id[2];
-    job.nth(keys, ids, id);
-    if (first && token != nullptr) *token = id[0];
-    if (part) last = id[1];
-  }
-  if (out != nullptr) job.write(out, kept.key, last);
+  const uint32_t keys[2] = {token != nullptr ? drawn.key : 0, part ? kept.key : 0};
+  const uint32_t ids[2] = {token != nullptr ? drawn.ids : 0, part ? kept.ids : 0};
+  const bool some = token != nullptr || part;
+  if (some) job.clear_marks();
+  if (some || out != nullptr) job.write(out, kept.key, keys);
+  if (some) job.settle(out, token, keys, ids);
   if (ctas > 1) job.cluster.sync();  // (memory that others may still read)
 }
 

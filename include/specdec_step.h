@@ -239,7 +239,7 @@ specdec_status_t spec_process_logits(const void* logits, void* out, specdec_dtyp
  * weights sum to more than uniform times that of all kept.  A row without a
  * number above -infinity gives -1 and keeps nothing; infinite logits are equal,
  * and the others count as -infinity beside them.
- * Weights are whole numbers of 2^-45 of the largest, within 2^-40 of their value,
+ * Weights are whole numbers of 2^-44 of the largest, within 2^-40 of their value,
  * and all sums are exact.
  */
 specdec_status_t spec_sample(const void* logits, void* out, specdec_dtype_t dtype, int32_t B, int32_t n_max, int32_t V,

@@ -20,8 +20,11 @@ cudaError_t launch_sample(const SampleArgs& a, cudaStream_t st) {
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
+  // (bf16: a byte for each vector of a CTA's part behind the rest)
+  constexpr size_t kFixed = sizeof(SampleSmem<Elt>);
+  auto bytes = [](int32_t V, int ctas) { return kFixed + (sizeof(Elt) == 2 ? static_cast<size_t>((V / 8 + 2 + ctas - 1) / ctas + 1) : 0); };
   if (!ready[dev]) {
-    e = cudaFuncSetAttribute(sample_kernel<Elt>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SampleSmem<Elt>));
+    e = cudaFuncSetAttribute(sample_kernel<Elt>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes(SPECDEC_MAX_VOCAB, 1)));
     if (e != cudaSuccess) return e;
     ready[dev] = true;
   }
@@ -31,7 +34,7 @@ cudaError_t launch_sample(const SampleArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t config = {};
   config.gridDim = dim3(static_cast<unsigned>(rows * ctas));
   config.blockDim = dim3(kSampleThreads);
-  config.dynamicSmemBytes = sizeof(SampleSmem<Elt>);
+  config.dynamicSmemBytes = bytes(a.V, ctas);
   config.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;

@@ -31,6 +31,18 @@ constexpr int kSampleClusterMax = 8;
 constexpr int kNear = 512;    // ids of a border's bin that are listed (fp32)
 constexpr int kSampleGroups = kSampleThreads;  // of neighbouring bins, whose sums are kept
 
+// Of the halves of two words.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t min_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Bins of a logit's first 16 bits, the largest first: magnitudes from 2^12 down
 // have one for each 7 bits of mantissa; what is above is in the outermost bins and
 // what is below in the two of zero.
@@ -41,9 +53,12 @@ struct SampleBinsOf {
   static constexpr uint32_t kTop = (127 + 12) << 7;          // 2^12 and above
   static constexpr uint32_t kBase = kTop - (kHalf - 1);      // about 2^-20 and below
 
+  // A bin in 8 bits: a 16th of a power of two each, and all below 2^-4 in one.
+  static __device__ __forceinline__ uint32_t coarse(uint32_t bin) { return min(bin >> 3, 255u); }
+
   // of two logits' bits at once, a half each
   static __device__ __forceinline__ uint32_t two(uint32_t w) {
-    const uint32_t m = __vminu2(__vmaxu2(w & 0x7FFF7FFFu, kBase * 0x10001u), kTop * 0x10001u) - (kBase - kHalf) * 0x10001u;
+    const uint32_t m = min_u16x2(max_u16x2(w & 0x7FFF7FFFu, kBase * 0x10001u), kTop * 0x10001u) - (kBase - kHalf) * 0x10001u;
     uint32_t negative;  // a mask in each half
     asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(negative) : "r"(w));
     return m ^ (~negative & (kBins - 1) * 0x10001u);
@@ -99,7 +114,7 @@ struct SampleFast {
   int32_t id[kSampleClusterMax];
   uint32_t same[kSampleClusterMax][2];
   uint32_t listed;
-  unsigned long long zero[2];   // sums of the bins of zero
+  unsigned long long zero[2];   // bf16: sums of the bins of zero
   bool zeroed;                  // they are in use
   SamplePlace kept, drawn;
   bool simple;
@@ -127,6 +142,7 @@ struct SampleJob {
   static constexpr int kGroups = kSampleGroups;
   static constexpr int kOfGroup = Bins::kBins / kGroups;
   SampleFast<Elt>& s;
+  uint8_t* largest_of;   // bf16: coarse bin of a vector's largest logit
   const SampleRow<Elt> row;
   cooperative_groups::cluster_group cluster;
   int ctas, rank;
@@ -143,51 +159,78 @@ struct SampleJob {
   }
   __device__ __forceinline__ unsigned long long weight(float x) const { return sample_weight(x, top, scale, s.table); }
 
-  // f(words, j) for this CTA's whole vectors, four on their way at a time, and
-  // g(logit's bits, id) for the ids at the row's ends that have none.
-  template <typename F, typename G>
-  __device__ __forceinline__ void each(F f, G g) const {
-    const int lo = max(j0, row.phase != 0 ? 1 : 0), hi = min(j1, (row.phase + row.V) / E);
+  // A vector's words, -infinity for ids that the row does not have.
+  __device__ __forceinline__ uint4 words(int j) const {
+    const int first = E * j - row.phase;
+    if (first >= 0 && first + E <= row.V) return reinterpret_cast<const uint4*>(row.p)[j];
+    constexpr uint32_t kNone = sizeof(Elt) == 2 ? 0xFF80FF80u : 0xFF800000u;
+    uint32_t w[4] = {kNone, kNone, kNone, kNone};
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (first + e >= 0 && first + e < row.V) {
+        const uint32_t b = bits(row.p[E * j + e]);
+        if (sizeof(Elt) == 2)
+          w[e * 4 / E] = e & 1 ? (w[e * 4 / E] & 0xFFFFu) | b << 16 : (w[e * 4 / E] & 0xFFFF0000u) | b;
+        else
+          w[e % 4] = b;
+      }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // f(words, j) for this CTA's vectors.  kAtOnce are on their way together, and f's
+  // code is there as often: 1 for a long one, which asks for the next before its own.
+  template <int kAtOnce, typename F>
+  __device__ __forceinline__ void each(F f) const {
+    const int lo = max(j0, row.phase != 0 ? 1 : 0), hi = min(j1, (row.phase + row.V) / E);  // whole ones
     const uint4* p = reinterpret_cast<const uint4*>(row.p);
     int j = lo + threadIdx.x;
+    if constexpr (kAtOnce > 1) {
 #pragma unroll 1
-    for (; j + 3 * kSampleThreads < hi; j += 4 * kSampleThreads) {
-      uint4 q[4];
+      for (; j + (kAtOnce - 1) * kSampleThreads < hi; j += kAtOnce * kSampleThreads) {
+        uint4 q[kAtOnce];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = p[j + i * kSampleThreads];
+        for (int i = 0; i < kAtOnce; ++i) q[i] = p[j + i * kSampleThreads];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f(q[i], j + i * kSampleThreads);
+        for (int i = 0; i < kAtOnce; ++i) f(q[i], j + i * kSampleThreads);
+      }
     }
+    // the rest, and the row's ends, one by one
+    uint4 ahead = j < hi ? p[j] : make_uint4(0, 0, 0, 0);
+    const int end = threadIdx.x == 0 && row.phase != 0 && j0 == 0 ? 0
+                    : threadIdx.x == 32 && j1 == row.vecs && row.vecs > hi && (row.vecs > 1 || row.phase == 0) ? row.vecs - 1 : -1;
 #pragma unroll 1
-    for (; j < hi; j += kSampleThreads) f(p[j], j);
-    // (a row within one vector has its ids at one end or the other)
-    if (threadIdx.x < 2 * E) {
-      const int v = threadIdx.x < E ? 0 : row.vecs - 1, i = E * v + static_cast<int>(threadIdx.x % E) - row.phase;
-      const bool whole = E * v >= row.phase && E * (v + 1) <= row.phase + row.V;
-      if (v >= j0 && v < j1 && !whole && (threadIdx.x < E || row.vecs > 1) && i >= 0 && i < row.V) g(bits(row.p[i + row.phase]), i);
+    while (true) {
+      const bool inside = j < hi;
+      if (!inside && end < 0) break;
+      const uint4 q = inside ? ahead : words(end);
+      const int at = inside ? j : end;
+      if (inside) {
+        j += kSampleThreads;
+        if (j < hi) ahead = p[j];
+      }
+      f(q, at);
+      if (!inside) break;
     }
   }
   static __device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x); }
   static __device__ __forceinline__ uint32_t bits(__nv_bfloat16 x) { return __bfloat16_as_ushort(x); }
   static __device__ __forceinline__ float logit(uint32_t b) { return plain_logit(__uint_as_float(sizeof(Elt) == 2 ? b << 16 : b)); }
-  // f(logit, id) for all of this CTA's ids.
-  template <typename F>
+  // f(logit, id) for all of this CTA's ids, and for ids that the row does not have,
+  // with -infinity.
+  template <int kAtOnce, typename F>
   __device__ __forceinline__ void each_id(F f) const {
-    each(
-        [&](const uint4& q, int j) {
-          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-          const int id = E * j - row.phase;
+    each<kAtOnce>([&](const uint4& q, int j) {
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      const int id = E * j - row.phase;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (sizeof(Elt) == 2) {
-              f(logit(w[i] & 0xFFFFu), id + 2 * i);
-              f(logit(w[i] >> 16), id + 2 * i + 1);
-            } else {
-              f(logit(w[i]), id + i);
-            }
-          }
-        },
-        [&](uint32_t b, int id) { f(logit(b), id); });
+      for (int i = 0; i < 4; ++i) {
+        if (sizeof(Elt) == 2) {
+          f(logit(w[i] & 0xFFFFu), id + 2 * i);
+          f(logit(w[i] >> 16), id + 2 * i + 1);
+        } else {
+          f(logit(w[i]), id + i);
+        }
+      }
+    });
   }
 
   // A bin's count and sum, over the cluster, from the CTA that added them up.
@@ -268,6 +311,31 @@ struct SampleJob {
     __syncthreads();
   }
 
+  // fp32: every id's weight into its bin; with `counted` the ids are counted too.
+  __device__ __forceinline__ void add_weights(bool counted) {
+    if constexpr (sizeof(Elt) == 4) {
+      each_id<1>([&](float x, int) {
+        if (x == -INFINITY) return;
+        const int bin = Bins::one(x);
+        if (counted) atomicAdd(&s.bins.count[bin], 1u);
+        const unsigned long long w = weight(x);
+        const uint32_t lo = static_cast<uint32_t>(w);
+        uint32_t hi = static_cast<uint32_t>(w >> 32);
+        if (lo != 0) {
+          const uint32_t old = atomicAdd(&s.bins.lo[bin], lo);
+          hi += old + lo < old ? 1 : 0;
+        }
+        if (hi != 0) atomicAdd(&s.bins.hi[bin], hi);
+      });
+      meet();
+    }
+  }
+  __device__ __forceinline__ void clear_bins() {
+    uint4* z = reinterpret_cast<uint4*>(&s.bins);
+    constexpr int kClear = (sizeof(Elt) == 2 ? 1 : 3) * Bins::kBins / 4;
+    for (int i = threadIdx.x; i < kClear; i += kSampleThreads) z[i] = make_uint4(0, 0, 0, 0);
+  }
+
   // The bins of zero have logits up to 2^-20, whose weights differ by that over T:
   // where they matter, each id's own weight is added.
   __device__ __forceinline__ void add_zeros() {
@@ -277,14 +345,24 @@ struct SampleJob {
     bin_of_cluster(Bins::kHalf, &c[1], &w[1]);
     if (!(static_cast<float>(w[0] + w[1]) * scale.hi * 0x1p21f > static_cast<float>(s.group_sum[kGroups]))) return;
     meet();
-    unsigned long long mine[2] = {0, 0};
-    each_id([&](float x, int) {
-      const int bin = Bins::one(x) - (Bins::kHalf - 1);
-      if (x != -INFINITY && (bin == 0 || bin == 1)) mine[bin] += weight(x);
+    auto one = [&](float x) {
+      const int i = Bins::one(x) - (Bins::kHalf - 1);
+      if (x == -INFINITY || (i != 0 && i != 1)) return;
+      const unsigned long long mine = weight(x);
+      for (int o = 0; o < ctas; ++o) atomicAdd(&of(o).zero[i], mine);
+    };
+    each<4>([&](const uint4& q, int) {
+      const uint32_t v[4] = {q.x, q.y, q.z, q.w};
+      uint32_t m = 0xFFFFFFFFu;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = min_u16x2(m, v[i] & 0x7FFF7FFFu);
+      if ((m & 0xFFFFu) > Bins::kBase && (m >> 16) > Bins::kBase) return;
+#pragma unroll 1
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t p = e & 4 ? (e & 2 ? v[3] : v[2]) : (e & 2 ? v[1] : v[0]);
+        one(logit(e & 1 ? p >> 16 : p & 0xFFFFu));
+      }
     });
-    for (int i = 0; i < 2; ++i)
-      if (mine[i] != 0)
-        for (int o = 0; o < ctas; ++o) atomicAdd(&of(o).zero[i], mine[i]);
     meet();
     const unsigned long long more[2] = {s.zero[0] - w[0], s.zero[1] - w[1]};
     constexpr int kFirst = (Bins::kHalf - 1) / kOfGroup;
@@ -351,12 +429,23 @@ struct SampleJob {
       return true;
     } else {
       SampleFast<Elt>& lead = ctas > 1 ? of(0) : s;
-      each_id([&](float x, int) {
-        if (x != -INFINITY && Bins::one(x) == f.bin) {
-          const uint32_t at = atomicAdd(&lead.listed, 1u);
-          if (at < kNear) lead.bins.near_key[at] = key_of(x);
-        }
-      });
+      auto list = [&](float x) {
+        const uint32_t at = atomicAdd(&lead.listed, 1u);
+        if (at < kNear) lead.bins.near_key[at] = key_of(x);
+      };
+      if (f.bin == 0 || f.bin == Bins::kBins - 1 || f.bin == Bins::kHalf - 1 || f.bin == Bins::kHalf) {
+        each_id<1>([&](float x, int) {
+          if (x != -INFINITY && Bins::one(x) == f.bin) list(x);
+        });
+      } else {  // a bin of one beginning of 16 bits
+        const uint32_t first = __float_as_uint(Bins::value(f.bin)) & 0xFFFF0000u;
+        each<4>([&](const uint4& q, int) {
+          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((w[i] ^ first) < 0x10000u) list(__uint_as_float(w[i]));
+        });
+      }
       meet();
       if (rank == 0) {
         const uint32_t n = s.listed;
@@ -420,57 +509,74 @@ struct SampleJob {
   // vectors with ids of key[i], where there is one (not 0), are marked.
   __device__ __forceinline__ void write(Elt* out, uint32_t least_kept, const uint32_t (&key)[2]) {
     const bool same = out != nullptr && (reinterpret_cast<uintptr_t>(out) & 15) == row.phase * sizeof(Elt);
-    const float least = of_key(least_kept), none = -INFINITY, nan = __uint_as_float(0x7FFFFFFFu);
+    const float least = of_key(least_kept), nan = __uint_as_float(0x7FFFFFFFu);
     const bool look = key[0] != 0 || key[1] != 0;
     const float tie[2] = {key[0] != 0 ? of_key(key[0]) : nan, key[1] != 0 ? of_key(key[1]) : nan};
     auto mark = [&](int j) { atomicOr(&s.marks[(j - j0) >> 5], 1u << ((j - j0) & 31)); };
-    const __nv_bfloat162 least2 = __float2bfloat162_rn(least);  // (bf16 rows' borders are bf16)
-    const __nv_bfloat162 tie2[2] = {__float2bfloat162_rn(tie[0]), __float2bfloat162_rn(tie[1])};
-    each(
-        [&](const uint4& q, int j) {
-          const int first = E * j - row.phase;
-          uint32_t w[4] = {q.x, q.y, q.z, q.w};
-          if (look) {
+    auto store = [&](const uint32_t (&w)[4], int first) {
+      if (same && first >= 0 && first + E <= row.V) {
+        *reinterpret_cast<uint4*>(out + first) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (first + e >= 0 && first + e < row.V) {
+            if constexpr (sizeof(Elt) == 2)
+              out[first + e] = __ushort_as_bfloat16(static_cast<unsigned short>(e & 1 ? w[e / 2] >> 16 : w[e / 2]));
+            else
+              out[first + e] = __uint_as_float(w[e]);
+          }
+      }
+    };
+    if constexpr (sizeof(Elt) == 2) {
+      const __nv_bfloat162 least2 = __float2bfloat162_rn(least);  // (borders are bf16)
+      const __nv_bfloat162 tie2[2] = {__float2bfloat162_rn(tie[0]), __float2bfloat162_rn(tie[1])};
+      // vectors without a logit to keep, or to mark where nothing is kept, are not read
+      const uint32_t read = Bins::coarse(Bins::one(out != nullptr ? least : tie[0]));
+      constexpr int kAtOnce = 4;
+#pragma unroll 1
+      for (int j = j0 + static_cast<int>(threadIdx.x); j < j1; j += kAtOnce * kSampleThreads) {
+        uint4 q[kAtOnce];
+        bool wanted[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const int at = j + i * kSampleThreads;
+          wanted[i] = at < j1 && largest_of[at - j0] <= read;
+          q[i] = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+          if (wanted[i]) q[i] = words(at);
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const int at = j + i * kSampleThreads;
+          if (at >= j1) break;
+          uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+          if (wanted[i]) {
             uint32_t tied = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if constexpr (sizeof(Elt) == 2) {
-                const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
-                tied |= __heq2_mask(x, tie2[0]) | __heq2_mask(x, tie2[1]);
-              } else {
-                tied |= __uint_as_float(w[i]) == tie[0] || __uint_as_float(w[i]) == tie[1] ? 1u : 0;
-              }
+            for (int l = 0; l < 4; ++l) {
+              const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[l]);
+              tied |= __heq2_mask(x, tie2[0]) | __heq2_mask(x, tie2[1]);
+              const uint32_t m = __hge2_mask(x, least2);
+              w[l] = (w[l] & m) | (~m & 0xFF80FF80u);
             }
-            if (tied != 0) mark(j);
+            if (look && tied != 0) mark(at);
           }
-          if (out == nullptr) return;
+          if (out != nullptr) store(w, E * at - row.phase);
+        }
+      }
+    } else {
+      each<4>([&](const uint4& q, int j) {
+        uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        bool tied = false;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (sizeof(Elt) == 2) {
-              const uint32_t m = __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), least2);
-              w[i] = (w[i] & m) | (~m & 0xFF80FF80u);
-            } else {
-              w[i] = __uint_as_float(w[i]) >= least ? w[i] : 0xFF800000u;
-            }
-          }
-          if (same) {
-            *reinterpret_cast<uint4*>(out + first) = make_uint4(w[0], w[1], w[2], w[3]);
-          } else if constexpr (sizeof(Elt) == 2) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              out[first + 2 * i] = __ushort_as_bfloat16(static_cast<unsigned short>(w[i]));
-              out[first + 2 * i + 1] = __ushort_as_bfloat16(static_cast<unsigned short>(w[i] >> 16));
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) out[first + i] = __uint_as_float(w[i]);
-          }
-        },
-        [&](uint32_t b, int id) {
-          const float x = logit(b);
-          if (x == tie[0] || x == tie[1]) mark((id + row.phase) / E);
-          if (out != nullptr) out[id] = static_cast<Elt>(x >= least ? x : none);
-        });
+        for (int i = 0; i < 4; ++i) {
+          const float x = __uint_as_float(w[i]);
+          tied |= x == tie[0] || x == tie[1];
+          w[i] = x >= least ? w[i] : 0xFF800000u;
+        }
+        if (tied) mark(j);
+        if (out != nullptr) store(w, E * j - row.phase);
+      });
+    }
   }
 
   // f(id, which) for the ids of key[which] in the vectors that word `i` marks, in
@@ -543,7 +649,7 @@ struct SampleJob {
   // Whether a logit of the row is finite and -4096 or below (bf16).
   __device__ __forceinline__ bool any_far() {
     bool far = false;
-    each_id([&](float x, int) { far |= x <= -4096.f && x != -INFINITY; });
+    each_id<4>([&](float x, int) { far |= x <= -4096.f && x != -INFINITY; });
     far = __syncthreads_or(far) != 0;
     if (ctas > 1) {
       if (threadIdx.x < ctas) of(threadIdx.x).flag[rank] = far ? 1 : 0;
@@ -581,7 +687,7 @@ struct SampleJob {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float best = -INFINITY;
     int at = 0x7FFFFFFF;
-    each_id([&](float x, int i) {
+    each_id<4>([&](float x, int i) {
       if (x > best || (x == best && i < at && x != -INFINITY)) best = x, at = i;
     });
     uint32_t k = key_of(best);
@@ -722,7 +828,7 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
   }
   SampleRow<Elt> row(logits, a.V);
   const int share = (row.vecs + ctas - 1) / ctas;
-  SampleJob<Elt> job = {s, row, cooperative_groups::this_cluster(), ctas, rank, min(row.vecs, rank * share),
+  SampleJob<Elt> job = {s, sample_smem + sizeof(SampleSmem<Elt>), row, cooperative_groups::this_cluster(), ctas, rank, min(row.vecs, rank * share),
                         min(row.vecs, rank * share + share), 0.f, {}};
   if (ask.cold || ask.k == 1) {
     uint32_t key;
@@ -739,9 +845,7 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
 
   // the histogram, and the largest logit
   {
-    uint4* z = reinterpret_cast<uint4*>(&s.bins);
-    constexpr int kClear = (sizeof(Elt) == 2 ? 1 : 3) * Bins::kBins / 4;
-    for (int i = tid; i < kClear; i += kSampleThreads) z[i] = make_uint4(0, 0, 0, 0);
+    job.clear_bins();
     if (tid < 256) s.table[tid] = kExp2Table[tid];
     if (tid == 0) s.listed = 0, s.zeroed = false, s.zero[0] = s.zero[1] = 0;
   }
@@ -749,7 +853,6 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
   ask = s.ask;
   job.scale = ask.scale;
   bool simple = true;
-  const bool counted = sizeof(Elt) == 2 || ask.k < a.V;
   if constexpr (sizeof(Elt) == 2) {
     uint32_t least = 0xFFFFFFFFu;
     // (-infinity's bin is not counted: a masked row's ids would wait for one another)
@@ -760,22 +863,19 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
           "setp.lt.u32 p, %1, %2;\n\t"
           "@p red.shared::cta.add.u32 [%0], 1;\n\t}" ::"r"(counts + 4 * bin), "r"(bin), "n"(Bins::kBins - 1) : "memory");
     };
-    job.each(
-        [&](const uint4& q, int) {
-          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    job.template each<4>([&](const uint4& q, int j) {
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      uint32_t first = 0xFFFFFFFFu;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t d = Bins::two(w[i]);
-            least = __vminu2(least, d);
-            add(d & 0xFFFFu);
-            add(d >> 16);
-          }
-        },
-        [&](uint32_t b16, int) {
-          const uint32_t d = Bins::two(b16) & 0xFFFFu;
-          least = __vminu2(least, d | 0xFFFF0000u);
-          add(d);
-        });
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t d = Bins::two(w[i]);
+        first = min_u16x2(first, d);
+        add(d & 0xFFFFu);
+        add(d >> 16);
+      }
+      least = min_u16x2(least, first);
+      job.largest_of[j - job.j0] = static_cast<uint8_t>(Bins::coarse(min(first & 0xFFFFu, first >> 16)));
+    });
     least = __reduce_min_sync(0xFFFFFFFFu, min(least & 0xFFFFu, least >> 16));
     if ((tid & 31) == 0) s.warp_count[tid >> 5][0] = least;
     if (ctas > 1) job.cluster.sync();  // (the others have begun)
@@ -798,22 +898,7 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
     job.largest(&key, &id);
     simple = key > kKeyFloor && key < key_of(INFINITY);
     job.top = of_key(key);
-    if (simple) {
-      job.each_id([&](float x, int) {
-        if (x == -INFINITY) return;
-        const int bin = Bins::one(x);
-        if (counted) atomicAdd(&s.bins.count[bin], 1u);
-        const unsigned long long w = job.weight(x);
-        const uint32_t lo = static_cast<uint32_t>(w);
-        uint32_t hi = static_cast<uint32_t>(w >> 32);
-        if (lo != 0) {
-          const uint32_t old = atomicAdd(&s.bins.lo[bin], lo);
-          hi += old + lo < old ? 1 : 0;
-        }
-        if (hi != 0) atomicAdd(&s.bins.hi[bin], hi);
-      });
-      job.meet();
-    }
+    if (simple) job.add_weights(ask.k < a.V);
   }
 
   SamplePlace kept = {kKeyFloor + 1, 0, 0, 0}, drawn = {0, 0, 0, 0};

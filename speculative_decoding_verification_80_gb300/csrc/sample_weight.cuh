@@ -1,4 +1,4 @@
-// sample_weight.cuh — exp((x - max) / T) as a whole number of 2^-45, for
+// sample_weight.cuh — exp((x - max) / T) as a whole number of 2^-44, for
 // spec_sample.  Host and device: its test compiles it without nvcc.
 //
 // Which tokens a row keeps, and which one is drawn, is decided where running sums
@@ -22,7 +22,7 @@
 
 namespace specdec {
 
-constexpr int kWeightBits = 45;  // of the largest weight: 2^18 of them fit 64 bits
+constexpr int kWeightBits = 44;  // of the largest weight: 2^18 of them fit 64 bits
 constexpr uint64_t kWeightOne = 1ull << kWeightBits;
 
 #if defined(__CUDACC__)
@@ -30,6 +30,7 @@ __device__ __forceinline__ float w_add(float a, float b) { return __fadd_rn(a, b
 __device__ __forceinline__ float w_mul(float a, float b) { return __fmul_rn(a, b); }
 __device__ __forceinline__ float w_fma(float a, float b, float c) { return __fmaf_rn(a, b, c); }
 __device__ __forceinline__ int32_t w_bits(float x) { return __float_as_int(x); }
+__device__ __forceinline__ float w_float(int32_t x) { return __int_as_float(x); }
 #else
 inline float w_add(float a, float b) { return a + b; }  // (compiled without contraction)
 inline float w_mul(float a, float b) { return a * b; }
@@ -38,6 +39,11 @@ inline int32_t w_bits(float x) {
   int32_t i;
   memcpy(&i, &x, 4);
   return i;
+}
+inline float w_float(int32_t x) {
+  float f;
+  memcpy(&f, &x, 4);
+  return f;
 }
 #endif
 
@@ -141,7 +147,7 @@ struct WeightScale {
 };
 
 // x <= max, both finite.  With t = (x - max) log2(e) / T = k + i / 256 + r,
-// |r| <= 2^-9, the weight is 2^k 2^(i / 256) e^(r ln 2).  A weight below 2^-46
+// |r| <= 2^-9, the weight is 2^k 2^(i / 256) e^(r ln 2).  A weight below 2^-45
 // is 0.
 SPECDEC_WEIGHT_FN uint64_t sample_weight(float x, float max, WeightScale s, const ExpPair* table) {
   // x - max and the rest that it leaves, exactly
@@ -172,17 +178,14 @@ SPECDEC_WEIGHT_FN uint64_t sample_weight(float x, float max, WeightScale s, cons
   bl = w_fma(p.hi, al, bl);
   bl = w_fma(p.lo, a, bl);
   bl = w_add(bl, p.lo);
-  const float c = w_add(b, bl), cl = w_add(w_add(b, -c), bl);
-  // c + cl in whole numbers of 2^-27 and 2^-46
-  constexpr float kMagic27 = 1.5f * 0x1p-4f, kMagic46 = 1.5f * 0x1p-23f;
-  const float c1 = w_add(c, kMagic27);
-  const int32_t n1 = w_bits(c1) - w_bits(kMagic27);
-  const float c2 = w_add(w_add(c, -w_add(c1, -kMagic27)), cl);
-  const int32_t n2 = w_bits(w_add(c2, kMagic46)) - w_bits(kMagic46);
-  const int32_t top = (((w_bits(p.hi) & 0x7FFFFF) | 0x800000) << 4) + n1;  // p.hi is in [1, 2)
-  const uint64_t w = static_cast<uint64_t>(static_cast<int64_t>(top) * (1 << 19) + n2);  // in 2^-46
-  const int sh = 1 - (n >> 8);
-  return (w + (1ull << (sh - 1))) >> sh;
+  // times 2^k (at most 1 in all), in whole numbers of 2^-22 and 2^-44
+  const float k = w_float(((n >> 8) + 127) << 23), hi = w_mul(p.hi, k), lo = w_mul(w_add(b, bl), k);
+  const float left = w_mul(w_add(w_add(b, -w_add(b, bl)), bl), k);
+  const float v = w_add(hi, lo), rest2 = w_add(w_add(w_add(hi, -v), lo), left);
+  constexpr float kMagic22 = 3.f, kMagic44 = 1.5f * 0x1p-21f;
+  const float v1 = w_add(v, kMagic22);
+  const float v2 = w_add(w_add(w_add(v, -w_add(v1, -kMagic22)), rest2), kMagic44);
+  return static_cast<uint64_t>(static_cast<int64_t>(w_bits(v1) - w_bits(kMagic22)) * (1 << 22) + (w_bits(v2) - w_bits(kMagic44)));
 }
 
 }  // namespace specdec

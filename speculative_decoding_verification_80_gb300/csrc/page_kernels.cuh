@@ -1,7 +1,12 @@
 // page_kernels.cuh — the blocks of a paged cache beyond a step's growth: requests
 // that go on from others' tokens (kv_fork), blocks moved to the lowest ids
 // (kv_compact), and the copies that both ask for (kv_copy).
+//
+// kv_fork and kv_compact are one cooperative launch each of up to a CTA an SM, whose
+// three steps are a barrier of the grid apart.  A few KB to some MB: bound by latency
+// and, a call, by the host, which three launches cost 7 us and one 4.
 #pragma once
+#include <cooperative_groups.h>
 #include <stdint.h>
 
 #include "block_prefix.cuh"
@@ -47,8 +52,9 @@ struct ForkArgs {
   PageWork work;
 };
 
-constexpr int kPageThreads = 256;
-constexpr int kPageCtas = 304;   // that go over a table or the blocks
+constexpr int kPageThreads = kBlockThreads;
+constexpr int kPageWarps = kPageThreads / 32;
+constexpr int kPageSegment = 256;  // entries of a row that a warp takes
 
 __device__ __forceinline__ int clamped_held(const ForkArgs& a, int p, uint32_t* bad) {
   const int h = a.held[p];
@@ -75,11 +81,14 @@ __device__ __forceinline__ int fork_tokens(const ForkArgs& a, int b, int* parent
   return static_cast<int>(n);
 }
 
-// How often each block is named, and who would write it: a warp a row.
-__global__ void __launch_bounds__(kPageThreads) fork_count_kernel(const ForkArgs a) {
-  const int lane = threadIdx.x & 31, warps = static_cast<int>(gridDim.x) * (kPageThreads / 32);
+// How often each block is named, and who would write it: a warp a part of a row.
+__device__ __forceinline__ void fork_count(const ForkArgs& a) {
+  const int lane = threadIdx.x & 31, warps = static_cast<int>(gridDim.x) * kPageWarps;
+  const int parts = (a.max_blocks + kPageSegment - 1) / kPageSegment;
   uint32_t bad = 0;
-  for (int r = static_cast<int>(blockIdx.x) * (kPageThreads / 32) + (threadIdx.x >> 5); r < a.P + a.B; r += warps) {
+  for (long long i = static_cast<long long>(blockIdx.x) * kPageWarps + (threadIdx.x >> 5); i < static_cast<long long>(a.P + a.B) * parts; i += warps) {
+    // (the rows' first parts first: most rows have no others)
+    const int r = static_cast<int>(i % (a.P + a.B)), j0 = static_cast<int>(i / (a.P + a.B)) * kPageSegment;
     const bool fresh = r >= a.P;
     int p = r, n = 0, part = -1;
     if (fresh) {
@@ -91,7 +100,8 @@ __global__ void __launch_bounds__(kPageThreads) fork_count_kernel(const ForkArgs
     }
     const int32_t* row = a.table + static_cast<long long>(max(p, 0)) * a.max_blocks;
     uint32_t* to = fresh ? a.work.news : a.work.olds;
-    for (int j = lane; j < n; j += 32) {
+#pragma unroll 4
+    for (int j = j0 + lane; j < min(n, j0 + kPageSegment); j += 32) {
       const int x = row[j];
       if (x < 0 || x >= a.num_blocks) {
         bad = 1;
@@ -112,19 +122,20 @@ __device__ __forceinline__ long long holders_of(const ForkArgs& a, int x) {
   return static_cast<long long>(a.shares[x]) + 1 - a.work.olds[x] + a.work.news[x];
 }
 
-// CTA 0: who copies, into which block.  The others: which blocks go back.
-__global__ void __launch_bounds__(kBlockThreads) fork_plan_kernel(const ForkArgs a) {
+// Which blocks go back: the last CTAs.  Who copies, into which block: the first.
+__device__ __forceinline__ void fork_plan(const ForkArgs& a) {
   const int tid = threadIdx.x, lane = tid & 31, N = a.num_blocks;
-  if (blockIdx.x > 0) {
-    const int words = (N + 31) / 32, all = (static_cast<int>(gridDim.x) - 1) * (kBlockThreads / 32);
-    for (int w = (static_cast<int>(blockIdx.x) - 1) * (kBlockThreads / 32) + (tid >> 5); w < words; w += all) {
+  const int ctas = static_cast<int>(gridDim.x), others = ctas > 1 ? ctas - 1 : 1;
+  if (blockIdx.x > 0 || ctas == 1) {
+    const int words = (N + 31) / 32;
+    for (int w = (ctas > 1 ? static_cast<int>(blockIdx.x) - 1 : 0) * kPageWarps + (tid >> 5); w < words; w += others * kPageWarps) {
       const long long x = 32LL * w + lane;
       const bool back = x < N && a.work.olds[x] != 0 && holders_of(a, static_cast<int>(x)) <= 0;
       const uint32_t m = __ballot_sync(0xFFFFFFFFu, back);
       if (lane == 0) a.work.gone[w] = m;
     }
-    return;
   }
+  if (blockIdx.x > 0) return;
   __shared__ uint32_t part[33][1];
   int head = a.ring_state[0], count = a.ring_state[1];
   uint32_t bad = 0, asked = 0;
@@ -168,40 +179,46 @@ __global__ void __launch_bounds__(kBlockThreads) fork_plan_kernel(const ForkArgs
 }
 
 // Bits before word `upto` of `words`, over the CTA.
-template <int kThreads>
 __device__ __forceinline__ uint32_t bits_before(const uint32_t* words, int upto) {
-  __shared__ uint32_t sums[kThreads / 32];
+  __shared__ uint32_t sums[kPageWarps];
   uint32_t n = 0;
-  for (int i = threadIdx.x; i < upto; i += kThreads) n += __popc(words[i]);
+  for (int i = threadIdx.x; i < upto; i += kPageThreads) n += __popc(words[i]);
   n = __reduce_add_sync(0xFFFFFFFFu, n);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = n;
   __syncthreads();
   n = 0;
-  for (int i = 0; i < kThreads / 32; ++i) n += sums[i];
+  for (int i = 0; i < kPageWarps; ++i) n += sums[i];
   return n;
 }
 
+// This CTA's share of a bitmap's words.
+__device__ __forceinline__ void share_of_words(int words, int* w0, int* w1) {
+  const int share = (words + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+  *w0 = min(words, static_cast<int>(blockIdx.x) * share);
+  *w1 = min(words, *w0 + share);
+}
+
 // The new rows, the blocks' holders, the ring's new end, and the counts cleared.
-__global__ void __launch_bounds__(kPageThreads) fork_finish_kernel(const ForkArgs a, int block_ctas) {
+__device__ __forceinline__ void fork_finish(const ForkArgs& a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = a.num_blocks;
-  if (static_cast<int>(blockIdx.x) >= block_ctas) {
-    const int warps = (static_cast<int>(gridDim.x) - block_ctas) * (kPageThreads / 32);
-    for (int b = (static_cast<int>(blockIdx.x) - block_ctas) * (kPageThreads / 32) + warp; b < a.B; b += warps) {
-      const int p = a.parent[b], n = a.held_out[b], number = a.work.number[b];
-      const int32_t* row = a.table + static_cast<long long>(p) * a.max_blocks;
-      int32_t* to = a.table_out + static_cast<long long>(b) * a.max_blocks;
-      for (int j = lane; j < a.max_blocks; j += 32)
-        to[j] = j >= n ? -1 : (number >= 0 && j == n - 1 ? a.copies[2 * number + 1] : row[j]);
+  const long long all = static_cast<long long>(gridDim.x) * kPageThreads;
+  for (long long i = static_cast<long long>(blockIdx.x) * kPageThreads + tid; i < static_cast<long long>(a.B) * a.max_blocks; i += all) {
+    const int b = static_cast<int>(i / a.max_blocks), j = static_cast<int>(i - static_cast<long long>(b) * a.max_blocks), n = a.held_out[b];
+    int x = -1;
+    if (j < n) {
+      const int number = j == n - 1 ? a.work.number[b] : -1;
+      x = number >= 0 ? a.copies[2 * number + 1] : a.table[static_cast<long long>(a.parent[b]) * a.max_blocks + j];
     }
-    return;
+    a.table_out[i] = x;
   }
-  const int words = (N + 31) / 32, share = (words + block_ctas - 1) / block_ctas;
-  const int w0 = min(words, static_cast<int>(blockIdx.x) * share), w1 = min(words, w0 + share);
+  const int words = (N + 31) / 32;
+  int w0, w1;
+  share_of_words(words, &w0, &w1);
   const int head = a.work.ring[0], count = a.work.ring[1];
-  uint32_t before = bits_before<kPageThreads>(a.work.gone, w0);
-  if (blockIdx.x == block_ctas - 1) {
-    const uint32_t gone = bits_before<kPageThreads>(a.work.gone, words);
+  uint32_t before = bits_before(a.work.gone, w0);
+  if (blockIdx.x == gridDim.x - 1) {
+    const uint32_t gone = bits_before(a.work.gone, words);
     if (tid == 0) {
       const int taken = *a.count;
       a.ring_state_out[0] = static_cast<int>((static_cast<long long>(head) + taken) % N);
@@ -209,15 +226,14 @@ __global__ void __launch_bounds__(kPageThreads) fork_finish_kernel(const ForkArg
     }
   }
   // warps take words in turn; a warp's own bits before are counted as it goes
-  for (int w = w0 + warp, from = w0; w < w1; w += kPageThreads / 32) {
+  for (int w = w0 + warp, from = w0; w < w1; w += kPageWarps) {
     for (; from + 32 <= w; from += 32) before += __reduce_add_sync(0xFFFFFFFFu, __popc(a.work.gone[from + lane]));
     const uint32_t near = __reduce_add_sync(0xFFFFFFFFu, from + lane < w ? __popc(a.work.gone[from + lane]) : 0);
     const uint32_t m = a.work.gone[w];
     const long long x = 32LL * w + lane;
     if (x >= N) continue;
     const uint32_t olds = a.work.olds[x];
-    const int was = a.shares[x];
-    int now = was;
+    int now = a.shares[x];
     if (olds != 0) {
       const long long h = holders_of(a, static_cast<int>(x));
       const uint32_t writers = a.work.writers[x];
@@ -229,6 +245,15 @@ __global__ void __launch_bounds__(kPageThreads) fork_finish_kernel(const ForkArg
     if ((m >> lane) & 1)
       a.ring[(static_cast<long long>(head) + count + before + near + __popc(m & ((1u << lane) - 1))) % N] = static_cast<int>(x);
   }
+}
+
+__global__ void __launch_bounds__(kPageThreads) fork_kernel(const ForkArgs a) {
+  const cooperative_groups::grid_group grid = cooperative_groups::this_grid();
+  fork_count(a);
+  grid.sync();
+  fork_plan(a);
+  grid.sync();
+  fork_finish(a);
 }
 
 // --------------------------------------------------------------- kv_compact
@@ -251,7 +276,7 @@ struct CompactArgs {
 };
 
 // A bit for each free block.
-__global__ void __launch_bounds__(kPageThreads) compact_mark_kernel(const CompactArgs a) {
+__device__ __forceinline__ void compact_mark(const CompactArgs& a) {
   const int N = a.num_blocks, all = static_cast<int>(gridDim.x) * kPageThreads;
   int head = a.ring_state[0], count = a.ring_state[1];
   uint32_t bad = 0;
@@ -272,22 +297,23 @@ __global__ void __launch_bounds__(kPageThreads) compact_mark_kernel(const Compac
 
 // With n blocks in use: the i-th in use from n on moves to the i-th free one
 // before it.
-__global__ void __launch_bounds__(kPageThreads) compact_plan_kernel(const CompactArgs a) {
+__device__ __forceinline__ void compact_plan(const CompactArgs& a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = a.num_blocks;
-  const int words = (N + 31) / 32, ctas = static_cast<int>(gridDim.x), share = (words + ctas - 1) / ctas;
-  const int w0 = min(words, static_cast<int>(blockIdx.x) * share), w1 = min(words, w0 + share);
+  const int words = (N + 31) / 32;
+  int w0, w1;
+  share_of_words(words, &w0, &w1);
   const uint32_t* marks = a.work.marks;
-  const uint32_t free_all = bits_before<kPageThreads>(marks, words);
+  const uint32_t free_all = bits_before(marks, words);
   const int n = N - static_cast<int>(free_all);
-  uint32_t holes = bits_before<kPageThreads>(marks, n >> 5);  // free before n
+  uint32_t holes = bits_before(marks, n >> 5);  // free before n
   if ((n & 31) != 0) holes += __popc(marks[n >> 5] & ((1u << (n & 31)) - 1));
-  uint32_t before = bits_before<kPageThreads>(marks, w0);
+  uint32_t before = bits_before(marks, w0);
   if (blockIdx.x == 0 && tid == 0) {
     *a.count = static_cast<int>(holes);
     a.ring_state_out[0] = 0;
     a.ring_state_out[1] = static_cast<int>(free_all);
   }
-  for (int w = w0 + warp, from = w0; w < w1; w += kPageThreads / 32) {
+  for (int w = w0 + warp, from = w0; w < w1; w += kPageWarps) {
     for (; from + 32 <= w; from += 32) before += __reduce_add_sync(0xFFFFFFFFu, __popc(marks[from + lane]));
     const uint32_t near = __reduce_add_sync(0xFFFFFFFFu, from + lane < w ? __popc(marks[from + lane]) : 0);
     const uint32_t m = marks[w];
@@ -312,45 +338,47 @@ __global__ void __launch_bounds__(kPageThreads) compact_plan_kernel(const Compac
 }
 
 // The blocks' new names, in the tables too, and the marks cleared.
-__global__ void __launch_bounds__(kPageThreads) compact_finish_kernel(const CompactArgs a, int block_ctas) {
-  const int tid = threadIdx.x, lane = tid & 31, N = a.num_blocks;
-  if (static_cast<int>(blockIdx.x) < block_ctas) {
-    const int all = block_ctas * kPageThreads;
-    for (long long i = static_cast<long long>(blockIdx.x) * kPageThreads + tid; i < N; i += all) {
-      const int x = static_cast<int>(i), rank = a.work.rank[x];
-      int to = rank == -2 ? x : -1;
-      if (rank >= 0) {
-        to = a.copies[2 * rank + 1];
-        a.shares_out[to] = a.shares[x];
-        a.shares_out[x] = 0;
-      }
-      a.renamed[x] = to;
-      if ((x & 31) == 0) a.work.marks[x >> 5] = 0;
+__device__ __forceinline__ void compact_finish(const CompactArgs& a) {
+  const int N = a.num_blocks;
+  const long long me = static_cast<long long>(blockIdx.x) * kPageThreads + threadIdx.x, all = static_cast<long long>(gridDim.x) * kPageThreads;
+  for (long long i = me; i < N; i += all) {
+    const int x = static_cast<int>(i), rank = a.work.rank[x];
+    int to = rank == -2 ? x : -1;
+    if (rank >= 0) {
+      to = a.copies[2 * rank + 1];
+      a.shares_out[to] = a.shares[x];
+      a.shares_out[x] = 0;
     }
-    return;
+    a.renamed[x] = to;
+    if ((x & 31) == 0) a.work.marks[x >> 5] = 0;
   }
   uint32_t bad = 0;
-  const int warps = (static_cast<int>(gridDim.x) - block_ctas) * (kPageThreads / 32);
-  for (int b = (static_cast<int>(blockIdx.x) - block_ctas) * (kPageThreads / 32) + (tid >> 5); b < a.B; b += warps) {
-    int n = a.held[b];
+  for (long long i = me; i < static_cast<long long>(a.B) * a.max_blocks; i += all) {
+    const int b = static_cast<int>(i / a.max_blocks), j = static_cast<int>(i - static_cast<long long>(b) * a.max_blocks);
+    int n = a.held[b], y = -1;
     if (n < 0 || n > a.max_blocks) bad = 1;
     n = max(0, min(n, a.max_blocks));
-    const int32_t* row = a.table + static_cast<long long>(b) * a.max_blocks;
-    int32_t* to = a.table_out + static_cast<long long>(b) * a.max_blocks;
-    for (int j = lane; j < a.max_blocks; j += 32) {
-      int y = -1;
-      if (j < n) {
-        const int x = row[j], rank = x >= 0 && x < N ? a.work.rank[x] : -1;
-        y = rank == -2 ? x : (rank >= 0 ? a.copies[2 * rank + 1] : -1);
-        if (y < 0) bad = 1;
-      }
-      to[j] = y;
+    if (j < n) {
+      const int x = a.table[i], rank = x >= 0 && x < N ? a.work.rank[x] : -1;
+      y = rank == -2 ? x : (rank >= 0 ? a.copies[2 * rank + 1] : -1);
+      if (y < 0) bad = 1;
     }
+    a.table_out[i] = y;
   }
   if (bad != 0 && a.err != nullptr) atomicOr(a.err, SPECDEC_DEV_ERR_BLOCKS);
 }
 
+__global__ void __launch_bounds__(kPageThreads) compact_kernel(const CompactArgs a) {
+  const cooperative_groups::grid_group grid = cooperative_groups::this_grid();
+  compact_mark(a);
+  grid.sync();
+  compact_plan(a);
+  grid.sync();
+  compact_finish(a);
+}
+
 // ------------------------------------------------------------------ kv_copy
+constexpr int kCopyThreads = 256;
 constexpr int kCopyLayers = 64;  // of a launch
 struct CopyLayer {
   void* k;
@@ -369,13 +397,13 @@ struct CopyArgs {
 };
 
 // A warp takes a part of a block of one layer's keys or values.
-__global__ void __launch_bounds__(kPageThreads) copy_kernel(const __grid_constant__ CopyArgs a) {
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyArgs a) {
   constexpr int kLoads = 8;
   const int lane = threadIdx.x & 31;
   const int count = max(0, min(*a.count, a.capacity));
   const long long items = static_cast<long long>(count) * a.layers * 2 * a.chunks;
-  const long long warps = static_cast<long long>(gridDim.x) * (kPageThreads / 32);
-  for (long long i = static_cast<long long>(blockIdx.x) * (kPageThreads / 32) + (threadIdx.x >> 5); i < items; i += warps) {
+  const long long warps = static_cast<long long>(gridDim.x) * (kCopyThreads / 32);
+  for (long long i = static_cast<long long>(blockIdx.x) * (kCopyThreads / 32) + (threadIdx.x >> 5); i < items; i += warps) {
     const long long block = i / a.chunks;
     const int c = static_cast<int>(i - block * a.chunks);
     const int l2 = static_cast<int>(block % (2 * a.layers));

@@ -35,10 +35,17 @@ specdec_status_t check_workspace(const void* workspace, size_t bytes, int64_t N)
   return workspace == nullptr || !aligned(workspace, 16) || bytes < page_words(N) * 4 ? SPECDEC_ERR_WORKSPACE : SPECDEC_OK;
 }
 
-// CTAs for some number of items at so many a CTA.
-unsigned ctas_for(int64_t items, int64_t each) {
-  const int64_t n = (items + each - 1) / each;
-  return static_cast<unsigned>(n < 1 ? 1 : (n > kPageCtas ? kPageCtas : n));
+// A cooperative launch of as many CTAs as `items` threads' work needs, at most one
+// an SM.
+template <typename Args>
+specdec_status_t launch_page(void (*kernel)(Args), Args& a, int64_t items, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  if (device_sms(&dev, &sms) != cudaSuccess) return SPECDEC_ERR_CUDA;
+  const int64_t ctas = (items + kPageThreads - 1) / kPageThreads;
+  void* args[1] = {&a};
+  const cudaError_t e = cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kernel), dim3(static_cast<unsigned>(ctas < 1 ? 1 : (ctas > sms ? sms : ctas))),
+                                                    dim3(kPageThreads), args, 0, st);
+  return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 
 }  // namespace
@@ -95,15 +102,9 @@ extern "C" specdec_status_t kv_fork(int32_t P, int32_t B, int32_t block_size, in
   a.count = count;
   a.err = error_word;
   a.work = page_work(workspace, num_blocks);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  constexpr int kWarps = kPageThreads / 32;
-  fork_count_kernel<<<ctas_for(static_cast<int64_t>(P) + B, kWarps), kPageThreads, 0, st>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
-  fork_plan_kernel<<<1 + ctas_for(num_blocks, kBlockThreads), kBlockThreads, 0, st>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
-  const unsigned block_ctas = ctas_for(num_blocks, 4 * kPageThreads);
-  fork_finish_kernel<<<block_ctas + ctas_for(B, kWarps), kPageThreads, 0, st>>>(a, static_cast<int>(block_ctas));
-  return launched();
+  // a thread for each entry of the tables or block
+  const int64_t entries = (static_cast<int64_t>(P) + B) * max_blocks;
+  return launch_page(fork_kernel, a, entries > num_blocks ? entries : num_blocks, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" specdec_status_t kv_compact(int32_t B, int32_t max_blocks, int32_t num_blocks, const int32_t* block_table,
@@ -139,14 +140,8 @@ extern "C" specdec_status_t kv_compact(int32_t B, int32_t max_blocks, int32_t nu
   a.count = count;
   a.err = error_word;
   a.work = page_work(workspace, num_blocks);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  compact_mark_kernel<<<ctas_for(num_blocks, kPageThreads), kPageThreads, 0, st>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
-  compact_plan_kernel<<<ctas_for(num_blocks, 4 * kPageThreads), kPageThreads, 0, st>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
-  const unsigned block_ctas = ctas_for(num_blocks, kPageThreads);
-  compact_finish_kernel<<<block_ctas + ctas_for(B, kPageThreads / 32), kPageThreads, 0, st>>>(a, static_cast<int>(block_ctas));
-  return launched();
+  const int64_t entries = static_cast<int64_t>(B) * max_blocks;
+  return launch_page(compact_kernel, a, entries > num_blocks ? entries : num_blocks, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" specdec_status_t kv_copy(const int32_t* copies, const int32_t* count, int32_t capacity, int32_t layers,
@@ -178,8 +173,8 @@ extern "C" specdec_status_t kv_copy(const int32_t* copies, const int32_t* count,
     }
     // as many warps as there can be parts, at most eight CTAs an SM
     const int64_t parts = static_cast<int64_t>(capacity) * a.layers * 2 * a.chunks;
-    const int64_t ctas = (parts + kPageThreads / 32 - 1) / (kPageThreads / 32);
-    copy_kernel<<<static_cast<unsigned>(ctas < 8 * sms ? ctas : 8 * sms), kPageThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    const int64_t ctas = (parts + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
+    copy_kernel<<<static_cast<unsigned>(ctas < 8 * sms ? ctas : 8 * sms), kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
     if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
   }
   return SPECDEC_OK;

@@ -5,10 +5,17 @@ the calls of a step, all of them on one stream and, after the first step, in one
 CUDA graph:
 
     kv_block_step        blocks and slots, from the last step's accepted lengths
+    spec_rotary          (rotary=True) the new tokens' positions
     kv_append            the new tokens' keys and values, 8 bits a value
     spec_attention       the new tokens' queries over the cache
     spec_process_logits  penalties of what the request has made, and its grammar
+    spec_sample          (temperature > 0) drafts drawn from cut rows, and the
+                         target's rows cut alike
     spec_verify          which drafts stand, and the token after them
+
+Between steps, `fork` lets requests go on from others' tokens (several
+continuations of a prompt, beams) and `compact` moves the cache's blocks to its
+start (kv_fork, kv_compact, kv_copy).
 
 Run: python examples/decode_step.py [requests] [steps]
 """
@@ -22,10 +29,12 @@ import speculative_decoding_verification_80_gb300 as sd  # noqa: E402
 
 
 class Decoder:
-    """State of B requests; `allowed` [B, V] (bool) is each one's grammar."""
+    """State of B requests; `allowed` [B, V] (bool) is each one's grammar.  With a
+    temperature above 0, tokens are drawn: from the top_k, the top_p and the ids of
+    min_p times the largest weight."""
 
     def __init__(self, B, drafts=4, V=4096, hidden=512, Hq=16, H=4, D=64, block_size=16, max_len=512, allowed=None,
-                 seed=0):
+                 seed=0, rotary=False, temperature=0.0, top_k=0, top_p=1.0, min_p=0.0):
         g = torch.Generator(device="cuda").manual_seed(seed)
         rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
         i32 = lambda *s, fill=0: torch.full(s, fill, dtype=torch.int32, device="cuda")  # noqa: E731
@@ -47,7 +56,17 @@ class Decoder:
         self.accepted, self.last = i32(B), i32(B)
         self.history, self.history_len, self.prompt_len = i32(B, max_len), i32(B), i32(B)
         self.new_tokens, self.draft_len = i32(B, fill=drafts + 1), i32(B, fill=drafts)
-        self.temperature = torch.zeros(B, device="cuda")
+        f32 = lambda v: torch.full((B,), float(v), device="cuda")  # noqa: E731
+        self.sampled = temperature > 0
+        self.temperature = f32(temperature)
+        self.cut = dict(temperature=self.temperature, top_k=i32(B, fill=top_k), top_p=f32(top_p), min_p=f32(min_p))
+        self.cu_rows = torch.arange(B + 1, dtype=torch.int32, device="cuda") * (drafts + 1)
+        self.random = torch.Generator(device="cuda").manual_seed(seed + 1)
+        self.uniform = torch.empty(B, drafts + 1, device="cuda")
+        self.turns, self.factor = sd.rotary_turns(D) if rotary else (None, 1.0)
+        self.layers = sd.kv_layers([(self.k_cache, self.v_cache, self.k_scale, self.v_scale)])
+        self.shares = i32(blocks)
+        self.page_workspace = sd.new_page_workspace(blocks)
         self.repetition = torch.full((B,), 1.1, device="cuda")
         self.frequency = torch.full((B,), 0.2, device="cuda")
         self.mask = self.mask_rows = None
@@ -64,9 +83,13 @@ class Decoder:
     def _layer(self, tokens, blocks):
         """The new tokens' hidden states after the layer."""
         T = tokens.numel()
-        x = self.embed[tokens] + self.position[blocks.positions.clamp(min=0)]
+        x = self.embed[tokens]
+        if self.turns is None:
+            x = x + self.position[blocks.positions.clamp(min=0)]
         qkv = (x @ self.w_qkv).view(T, self.Hq + 2 * self.H, self.D)
         q, k, v = qkv.split((self.Hq, self.H, self.H), 1)
+        if self.turns is not None:
+            sd.spec_rotary(q, k, blocks.positions, self.turns, factor=self.factor)
         sd.kv_append(k, v, blocks.slot_map, self.k_cache, self.v_cache, self.k_scale, self.v_scale)
         o = sd.spec_attention(q, blocks.cu_tokens, blocks.kv_len, self.table, self.k_cache, self.v_cache, self.k_scale,
                               self.v_scale, workspace=self.attention_workspace)
@@ -87,7 +110,11 @@ class Decoder:
         first = None if self.mask_rows is None else self.mask_rows[:, :1].contiguous()
         sd.spec_process_logits(logits, self.history, self.prompt_len, self.history_len, repetition=self.repetition,
                                frequency=self.frequency, mask=self.mask, mask_rows=first, error_word=self.error)
-        self.last.copy_(logits.view(B, -1).argmax(1))
+        if self.sampled:
+            self.uniform.uniform_(generator=self.random)
+            self.last.copy_(sd.spec_sample(logits, uniform=self.uniform[:, :1].contiguous(), **self.cut).view(-1))
+        else:
+            self.last.copy_(logits.view(B, -1).argmax(1))
         self.history[:, P] = self.last
         self.history_len.add_(1)
         self.accepted.fill_(P - 1)  # all of the prompt stays
@@ -95,9 +122,14 @@ class Decoder:
     def _step(self):
         B, n = self.B, self.n
         # drafts: the head on the embedding alone
-        fed = [self.last]
-        for _ in range(n):
-            fed.append((self.embed[fed[-1]] @ self.w_head.t()).argmax(1).to(torch.int32))
+        fed, rows = [self.last], []
+        for i in range(n):
+            row = self.embed[fed[-1]] @ self.w_head.t()
+            if self.sampled:
+                rows.append(row.view(B, 1, self.V))
+                fed.append(sd.spec_sample(rows[-1], uniform=self.uniform[:, i:i + 1].contiguous(), out=rows[-1], **self.cut).view(-1))
+            else:
+                fed.append(row.argmax(1).to(torch.int32))
         fed = torch.stack(fed, 1)
         drafts = fed[:, 1:].contiguous()
         s = sd.kv_block_step(self.table, self.state.kv_len, self.state.held, self.new_tokens, self.ring, self.state.ring_state,
@@ -107,8 +139,16 @@ class Decoder:
         sd.spec_process_logits(logits, self.history, self.prompt_len, self.history_len, draft_tokens=drafts,
                                draft_len=self.draft_len, repetition=self.repetition, frequency=self.frequency,
                                mask=self.mask, mask_rows=self.mask_rows, error_word=self.error)
-        _, out = sd.spec_verify(logits, None, drafts, self.draft_len, self.temperature, accepted_len=self.accepted,
-                                workspace=self.verify_workspace)
+        if self.sampled:
+            # the target's rows cut as the drafts' were; the verify call's own random numbers follow the position
+            sd.spec_sample(logits, out=logits, **self.cut)
+            draft = torch.cat(rows, 1) if n else logits[:, :0]
+            _, out = sd.spec_verify_packed(logits.view(-1, self.V), draft.view(-1, self.V), self.cu_rows, drafts.view(-1), self.temperature, n,
+                                           accepted_len=self.accepted, pos_offset=self.history_len, workspace=self.verify_workspace)
+            out = out.view(B, n + 1)
+        else:
+            _, out = sd.spec_verify(logits, None, drafts, self.draft_len, self.temperature, accepted_len=self.accepted,
+                                    workspace=self.verify_workspace)
         # the accepted drafts and the token after them are the request's
         j = torch.arange(n + 1, device="cuda")
         at = self.history_len[:, None] + j
@@ -120,6 +160,8 @@ class Decoder:
 
     def step(self):
         """A verify step of all requests: up to n + 1 tokens each."""
+        if self.sampled:
+            self.uniform.uniform_(generator=self.random)
         if self.graph is None:
             self._step()  # (the first also allocates what the graph must not)
             self.graph = torch.cuda.CUDAGraph()
@@ -127,6 +169,30 @@ class Decoder:
                 self._step()
         else:
             self.graph.replay()
+
+    def fork(self, parent):
+        """Request b goes on from the tokens of request parent[b] (int32 [B], each in [0, B))."""
+        f = sd.kv_fork(self.table, self.state.kv_len, self.state.held, parent, self.shares, self.ring, self.state.ring_state,
+                       self.block_size, accepted_len=self.accepted, workspace=self.page_workspace, error_word=self.error)
+        sd.kv_copy(f.copies, f.count, self.layers)
+        self.table.copy_(f.block_table)
+        self.shares.copy_(f.shares)
+        for name in ("kv_len", "held", "ring_state"):
+            getattr(self.state, name).copy_(getattr(f, name))
+        self.accepted.fill_(-1)  # kv_len has them
+        p = parent.long()
+        for x in (self.history, self.history_len, self.prompt_len, self.last):
+            x.copy_(x[p])
+
+    def compact(self):
+        """Blocks in use to the cache's start."""
+        c = sd.kv_compact(self.table, self.state.held, self.shares, self.ring, self.state.ring_state, workspace=self.page_workspace,
+                          error_word=self.error)
+        sd.kv_copy(c.copies, c.count, self.layers)
+        self.table.copy_(c.block_table)
+        self.shares.copy_(c.shares)
+        self.ring.copy_(c.free_ring)
+        self.state.ring_state.copy_(c.ring_state)
 
 
 def main(B=64, steps=20):

@@ -113,13 +113,14 @@ struct SampleFast {
   uint32_t top[kSampleClusterMax], flag[kSampleClusterMax];
   int32_t id[kSampleClusterMax];
   uint32_t same[kSampleClusterMax][2];
-  uint32_t listed;
+  uint32_t listed, least_key;
   unsigned long long zero[2];   // bf16: sums of the bins of zero
   bool zeroed;                  // they are in use
   SamplePlace kept, drawn;
-  bool simple;
+  bool simple, more;
   SampleAnswer answer;
-  SampleAsk ask;
+  WeightScale scale;
+  unsigned long long least;
 };
 
 template <typename Elt>
@@ -134,6 +135,23 @@ struct SampleBin {
   uint32_t c0, c;
   unsigned long long w0, w;
 };
+
+// Of 16 warps' values in shared memory: the sum of those before this warp's, and of
+// all.
+template <typename T>
+__device__ __forceinline__ T sum_of_warps(const T* each, int stride, T* all) {
+  static_assert(kSampleWarps == 16, "a half of the lanes has a warp's each");
+  const int lane = threadIdx.x & 15, warp = threadIdx.x >> 5;
+  const T mine = each[lane * stride];
+  T upto = mine;
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) {
+    const T o = __shfl_up_sync(0xFFFFFFFFu, upto, d, 16);
+    if (lane >= d) upto += o;
+  }
+  *all = __shfl_sync(0xFFFFFFFFu, upto, 15);
+  return __shfl_sync(0xFFFFFFFFu, upto - mine, warp);
+}
 
 template <typename Elt>
 struct SampleJob {
@@ -151,7 +169,16 @@ struct SampleJob {
   WeightScale scale;
 
   __device__ __forceinline__ SampleFast<Elt>& of(int cta) const { return *cluster.map_shared_rank(&s, cta); }
+  // That the others have begun, so that their memory may be written: said early, and
+  // waited for late.
+  __device__ __forceinline__ void say_begun() const {
+    if (ctas > 1) asm volatile("barrier.cluster.arrive;" ::: "memory");
+  }
+  __device__ __forceinline__ void wait_begun() const {
+    if (ctas > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
+  }
   __device__ __forceinline__ void meet() const {
+    __syncwarp();
     if (ctas > 1)
       cluster.sync();
     else
@@ -246,7 +273,7 @@ struct SampleJob {
   // Adds the CTAs' histograms up, a share of the bins each, and the sums of every
   // group, which all CTAs get.  A group is one thread's, or as many threads' as
   // there are CTAs.
-  __device__ __forceinline__ void add_up() {
+  __device__ __forceinline__ void add_up(const SampleAsk& ask) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, of_thread = kOfGroup / ctas;
     const int me = rank * kSampleThreads + threadIdx.x;
     {
@@ -288,12 +315,17 @@ struct SampleJob {
       to.group_count[me / ctas] = cs;
       to.group_sum[me / ctas] = ws;
     }
+    if (ask.least > 0 && warp == kSampleWarps - 1) {
+      const uint32_t key = least_key(kKeyFloor, key_of(top), ask.least);
+      if (lane == 0) s.least_key = key;
+    }
     meet();
     // sums before each group
-    uint32_t c = 0, cs;
-    unsigned long long w = 0, ws;
-    if (threadIdx.x < kGroups) c = s.group_count[threadIdx.x], w = s.group_sum[threadIdx.x];
-    cs = c, ws = w;
+    static_assert(kGroups == kSampleThreads, "a thread for each group");
+    const uint32_t c = s.group_count[threadIdx.x];
+    const unsigned long long w = s.group_sum[threadIdx.x];
+    uint32_t cs = c;
+    unsigned long long ws = w;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const uint32_t co = __shfl_up_sync(0xFFFFFFFFu, cs, d);
@@ -302,12 +334,13 @@ struct SampleJob {
     }
     if (lane == 31) s.warp_count[warp][0] = cs, s.warp_sum[warp] = ws;
     __syncthreads();
-    for (int i = 0; i < warp; ++i) cs += s.warp_count[i][0], ws += s.warp_sum[i];
-    if (threadIdx.x < kGroups) {
-      s.group_count[threadIdx.x] = cs - c;
-      s.group_sum[threadIdx.x] = ws - w;
-      if (threadIdx.x == kGroups - 1) s.group_count[kGroups] = cs, s.group_sum[kGroups] = ws;
-    }
+    uint32_t c_all;
+    unsigned long long w_all;
+    cs += sum_of_warps(&s.warp_count[0][0], 2, &c_all);
+    ws += sum_of_warps(&s.warp_sum[0], 1, &w_all);
+    s.group_count[threadIdx.x] = cs - c;
+    s.group_sum[threadIdx.x] = ws - w;
+    if (threadIdx.x == 0) s.group_count[kGroups] = c_all, s.group_sum[kGroups] = w_all;
     __syncthreads();
   }
 
@@ -336,14 +369,17 @@ struct SampleJob {
     for (int i = threadIdx.x; i < kClear; i += kSampleThreads) z[i] = make_uint4(0, 0, 0, 0);
   }
 
-  // The bins of zero have logits up to 2^-20, whose weights differ by that over T:
-  // where they matter, each id's own weight is added.
+  // The bins of zero have logits up to 2^-20, whose weights differ by that over T.
+  // Whether they matter, by a warp; then each id's own weight is added.
+  __device__ __forceinline__ bool zeros_matter(uint32_t (&c)[2], unsigned long long (&w)[2]) const {
+    bin_of_cluster(Bins::kHalf - 1, &c[0], &w[0]);
+    bin_of_cluster(Bins::kHalf, &c[1], &w[1]);
+    return static_cast<float>(w[0] + w[1]) * scale.hi * 0x1p21f > static_cast<float>(s.group_sum[kGroups]);
+  }
   __device__ __forceinline__ void add_zeros() {
     uint32_t c[2];
     unsigned long long w[2];
-    bin_of_cluster(Bins::kHalf - 1, &c[0], &w[0]);
-    bin_of_cluster(Bins::kHalf, &c[1], &w[1]);
-    if (!(static_cast<float>(w[0] + w[1]) * scale.hi * 0x1p21f > static_cast<float>(s.group_sum[kGroups]))) return;
+    zeros_matter(c, w);
     meet();
     auto one = [&](float x) {
       const int i = Bins::one(x) - (Bins::kHalf - 1);
@@ -371,6 +407,27 @@ struct SampleJob {
     __syncthreads();
   }
   __device__ __forceinline__ bool decide(const SampleAsk& ask, bool draw, SamplePlace* kept, SamplePlace* drawn);
+
+  // The least key of a logit of `Elt` whose weight is enough, by a warp; `no` has too
+  // little and `yes` enough.
+  __device__ __forceinline__ uint32_t least_key(uint32_t no, uint32_t yes, unsigned long long least) const {
+    // (keys of bf16 logits differ in their first half)
+    constexpr int kShift = sizeof(Elt) == 2 ? 16 : 0;
+    constexpr uint32_t kRest = (1u << kShift) - 1;
+    const int lane = threadIdx.x & 31;
+    // negative logits' keys end in ones, the others' in zeros
+    auto logit = [&](uint32_t k) { return of_key(kShift == 0 ? k : (k << kShift) | ((k >> 15) != 0 ? 0 : kRest)); };
+    no >>= kShift;
+    yes >>= kShift;
+    while (yes - no > 1) {
+      const uint32_t step = (yes - no + 31) / 32, at = no + step * (lane + 1);
+      const bool enough = at >= yes || weight(logit(at)) >= least;
+      const int first = __ffs(__ballot_sync(0xFFFFFFFFu, enough)) - 1;
+      yes = min(no + step * (first + 1), yes);
+      no += step * first;
+    }
+    return key_of(logit(yes));
+  }
 
   // The bin in which a border lies, by each warp for itself; false if there is none.
   __device__ __forceinline__ bool find(SampleBorder by, unsigned long long target, SampleBin* f) const {
@@ -628,7 +685,8 @@ struct SampleJob {
     bool past = false;  // whether this thread has ids that are not kept
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      for (int w = 0; w < warp; ++w) upto[i] += s.warp_count[w][i];
+      uint32_t all;
+      upto[i] += sum_of_warps(&s.warp_count[0][i], 2, &all);
       if (ctas > 1)
         for (int o = 0; o < rank; ++o) upto[i] += s.same[o][i];
       upto[i] -= n[i];
@@ -711,28 +769,6 @@ struct SampleJob {
   }
 };
 
-// A key whose weight is enough, the least that a logit of `Elt` can have, by each
-// warp for itself; `no` has too little.
-template <typename Elt>
-__device__ __forceinline__ uint32_t least_key(const SampleJob<Elt>& job, uint32_t no, uint32_t yes, unsigned long long least) {
-  // (keys of bf16 logits differ in their first half)
-  constexpr int kShift = sizeof(Elt) == 2 ? 16 : 0;
-  constexpr uint32_t kRest = (1u << kShift) - 1;
-  const int lane = threadIdx.x & 31;
-  // negative logits' keys end in ones, the others' in zeros
-  auto logit = [&](uint32_t k) { return of_key(kShift == 0 ? k : (k << kShift) | ((k >> 15) != 0 ? 0 : kRest)); };
-  no >>= kShift;
-  yes >>= kShift;
-  while (yes - no > 1) {
-    const uint32_t step = (yes - no + 31) / 32, at = no + step * (lane + 1);
-    const bool enough = at >= yes || job.weight(logit(at)) >= least;
-    const int first = __ffs(__ballot_sync(0xFFFFFFFFu, enough)) - 1;
-    yes = min(no + step * (first + 1), yes);
-    no += step * first;
-  }
-  return key_of(logit(yes));
-}
-
 // What is kept and which logit is drawn; false: the bins do not say.  bf16: by any
 // warp, fp32: by all.
 template <typename Elt>
@@ -755,8 +791,8 @@ __device__ __forceinline__ bool SampleJob<Elt>::decide(const SampleAsk& ask, boo
       weights = kept->sum + kept->ids * weight(of_key(kept->key));
     }
   }
-  if (ask.least > 0 && (kept->key <= kKeyFloor + 1 || weight(of_key(kept->key)) < ask.least)) {
-    const uint32_t key = least_key(*this, kept->key, key_of(top), ask.least);
+  if (ask.least > 0 && s.least_key > kept->key) {
+    const uint32_t key = s.least_key;
     look_up(Bins::one(of_key(key)), &f);
     if (!resolve(f, kByKey, key, kept)) return false;
     kept->key = key;
@@ -781,10 +817,18 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
   SampleFast<Elt>& s = smem.fast;
   const int tid = threadIdx.x;
   const int rank = ctas > 1 ? static_cast<int>(blockIdx.x % ctas) : 0;
-  const long long r = blockIdx.x / ctas;
-  const int b = static_cast<int>(r / (a.n_max + 1)), place = static_cast<int>(r - static_cast<long long>(b) * (a.n_max + 1));
+  const int row_of = static_cast<int>(blockIdx.x / ctas);  // (65536 requests of 65 rows)
+  const int b = row_of / (a.n_max + 1), place = row_of - b * (a.n_max + 1);
+  const long long r = row_of;
   uint32_t bad = 0;
+  // (all loads of the request's numbers at once)
   int n = a.draft_len != nullptr ? a.draft_len[b] : a.n_max;
+  const float T = a.temperature != nullptr ? a.temperature[b] : 1.f;
+  float m = a.min_p != nullptr ? a.min_p[b] : 0.f;
+  SampleAsk ask;
+  ask.p = a.top_p != nullptr ? a.top_p[b] : 1.f;
+  ask.u = a.uniform != nullptr ? a.uniform[r] : 0.f;
+  ask.k = a.top_k != nullptr ? a.top_k[b] : 0;
   if (n < 0 || n > a.n_max) {
     bad |= SPECDEC_DEV_ERR_DRAFT_LEN;
     n = max(0, min(n, a.n_max));
@@ -798,42 +842,27 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
   const Elt* logits = static_cast<const Elt*>(a.logits) + r * a.V;
   Elt* out = a.out != nullptr ? static_cast<Elt*>(a.out) + r * a.V : nullptr;
   int32_t* token = a.tokens != nullptr ? a.tokens + r : nullptr;
-  SampleAsk ask;
-  {
-    const float T = a.temperature != nullptr ? a.temperature[b] : 1.f;
-    float m = a.min_p != nullptr ? a.min_p[b] : 0.f;
-    ask.p = a.top_p != nullptr ? a.top_p[b] : 1.f;
-    ask.u = a.uniform != nullptr ? a.uniform[r] : 0.f;
-    ask.k = a.top_k != nullptr ? a.top_k[b] : 0;
-    if (ask.k <= 0 || ask.k > a.V) ask.k = a.V;
-    ask.cold = !(T >= 1e-6f) || T > 3e38f;
-    if (ask.cold && T != 0.f) bad |= SPECDEC_DEV_ERR_TEMPERATURE;
-    if (!(ask.p >= 0.f) || !(m <= 1.f) || !(m >= 0.f)) {
-      bad |= SPECDEC_DEV_ERR_SAMPLE;
-      if (!(ask.p >= 0.f)) ask.p = 1.f;
-      m = !(m >= 0.f) ? 0.f : fminf(m, 1.f);
-    }
-    if (!(ask.u >= 0.f && ask.u < 1.f)) {
-      bad |= SPECDEC_DEV_ERR_SAMPLE;
-      ask.u = ask.u >= 1.f ? 1.f - 0x1p-24f : 0.f;
-    }
-    // (64-bit arithmetic by one thread: it has 1/64 of the rate)
-    if (tid == 0) {
-      const double c = ask.cold ? 1.0 : 1.4426950408889634074 / static_cast<double>(T);
-      ask.scale.hi = static_cast<float>(c);
-      ask.scale.lo = static_cast<float>(c - static_cast<double>(ask.scale.hi));
-      ask.least = m > 0.f ? static_cast<unsigned long long>(ceil(static_cast<double>(m) * static_cast<double>(kWeightOne))) : 0;
-      s.ask = ask;
-    }
+  if (ask.k <= 0 || ask.k > a.V) ask.k = a.V;
+  ask.cold = !(T >= 1e-6f) || T > 3e38f;
+  if (ask.cold && T != 0.f) bad |= SPECDEC_DEV_ERR_TEMPERATURE;
+  if (!(ask.p >= 0.f) || !(m <= 1.f) || !(m >= 0.f)) {
+    bad |= SPECDEC_DEV_ERR_SAMPLE;
+    if (!(ask.p >= 0.f)) ask.p = 1.f;
+    m = !(m >= 0.f) ? 0.f : fminf(m, 1.f);
+  }
+  if (!(ask.u >= 0.f && ask.u < 1.f)) {
+    bad |= SPECDEC_DEV_ERR_SAMPLE;
+    ask.u = ask.u >= 1.f ? 1.f - 0x1p-24f : 0.f;
   }
   SampleRow<Elt> row(logits, a.V);
   const int share = (row.vecs + ctas - 1) / ctas;
   SampleJob<Elt> job = {s, sample_smem + sizeof(SampleSmem<Elt>), row, cooperative_groups::this_cluster(), ctas, rank, min(row.vecs, rank * share),
                         min(row.vecs, rank * share + share), 0.f, {}};
+  job.say_begun();
   if (ask.cold || ask.k == 1) {
     uint32_t key;
     int id;
-    if (ctas > 1) job.cluster.sync();  // (the others have begun)
+    job.wait_begun();
     job.largest(&key, &id);
     if (key <= kKeyFloor) bad |= SPECDEC_DEV_ERR_SAMPLE, id = -1;
     if (first && token != nullptr) *token = id;
@@ -844,14 +873,17 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
   }
 
   // the histogram, and the largest logit
-  {
-    job.clear_bins();
-    if (tid < 256) s.table[tid] = kExp2Table[tid];
-    if (tid == 0) s.listed = 0, s.zeroed = false, s.zero[0] = s.zero[1] = 0;
-  }
+  job.clear_bins();
+  if (tid < 256) s.table[tid] = kExp2Table[tid];
+  if (tid == 0) s.listed = 0, s.zeroed = false, s.zero[0] = s.zero[1] = 0;
   __syncthreads();
-  ask = s.ask;
-  job.scale = ask.scale;
+  if (tid == kSampleThreads - 1) {
+    // (64-bit arithmetic by one thread, beside the others' work: it has 1/64 of the rate)
+    const double c = 1.4426950408889634074 / static_cast<double>(T);
+    s.scale.hi = static_cast<float>(c);
+    s.scale.lo = static_cast<float>(c - static_cast<double>(s.scale.hi));
+    s.least = m > 0.f ? static_cast<unsigned long long>(ceil(static_cast<double>(m) * static_cast<double>(kWeightOne))) : 0;
+  }
   bool simple = true;
   if constexpr (sizeof(Elt) == 2) {
     uint32_t least = 0xFFFFFFFFu;
@@ -878,8 +910,10 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
     });
     least = __reduce_min_sync(0xFFFFFFFFu, min(least & 0xFFFFu, least >> 16));
     if ((tid & 31) == 0) s.warp_count[tid >> 5][0] = least;
-    if (ctas > 1) job.cluster.sync();  // (the others have begun)
+    job.wait_begun();
     __syncthreads();
+    ask.scale = job.scale = s.scale;
+    ask.least = s.least;
     if (tid < ctas) {
       for (int w = 0; w < kSampleWarps; ++w) least = min(least, s.warp_count[w][0]);
       job.of(tid).top[rank] = least;
@@ -894,8 +928,10 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
   } else {
     uint32_t key;
     int id;
-    if (ctas > 1) job.cluster.sync();
+    job.wait_begun();
     job.largest(&key, &id);
+    ask.scale = job.scale = s.scale;
+    ask.least = s.least;
     simple = key > kKeyFloor && key < key_of(INFINITY);
     job.top = of_key(key);
     if (simple) job.add_weights(ask.k < a.V);
@@ -903,21 +939,25 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
 
   SamplePlace kept = {kKeyFloor + 1, 0, 0, 0}, drawn = {0, 0, 0, 0};
   if (simple) {
-    job.add_up();
+    job.add_up(ask);
     if constexpr (sizeof(Elt) == 2) {
       // logits of -4096 and below are not counted: they have no weight and are not kept, or the row is another's
       const uint32_t ids = s.group_count[kSampleGroups];
       if ((ask.k < a.V && static_cast<uint32_t>(ask.k) > ids) || !((job.top + 4096.f) * ask.scale.hi > 49.f)) simple = !job.any_far();
-      if (simple) job.add_zeros();
       // every warp could, but one is enough
-      if (simple) {
+      for (int again = 0; simple; ++again) {
         if (tid < 32) {
-          const bool sure = job.decide(ask, token != nullptr, &kept, &drawn);
-          if (tid == 0) s.kept = kept, s.drawn = drawn, s.simple = sure;
+          uint32_t c[2];
+          unsigned long long w[2];
+          const bool more = again == 0 && job.zeros_matter(c, w);
+          const bool sure = !more && job.decide(ask, token != nullptr, &kept, &drawn);
+          if (tid == 0) s.kept = kept, s.drawn = drawn, s.simple = sure, s.more = more;
         }
         __syncthreads();
-        kept = s.kept, drawn = s.drawn, simple = s.simple;
+        if (!s.more) break;
+        job.add_zeros();
       }
+      if (simple) kept = s.kept, drawn = s.drawn, simple = s.simple;
     } else {
       simple = job.decide(ask, token != nullptr, &kept, &drawn);
     }

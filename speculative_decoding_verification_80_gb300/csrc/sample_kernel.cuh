@@ -123,6 +123,8 @@ struct SampleFast {
   unsigned long long least;
 };
 
+static_assert(offsetof(SampleFast<__nv_bfloat16>, bins) == 0 && sizeof(SampleBinsShared<__nv_bfloat16>) <= 32768, "16 bits address a count");
+
 template <typename Elt>
 union SampleSmem {
   SampleFast<Elt> fast;
@@ -887,23 +889,23 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
   bool simple = true;
   if constexpr (sizeof(Elt) == 2) {
     uint32_t least = 0xFFFFFFFFu;
-    // (-infinity's bin is not counted: a masked row's ids would wait for one another)
-    const uint32_t counts = static_cast<uint32_t>(__cvta_generic_to_shared(s.bins.count));
-    auto add = [&](uint32_t bin) {
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "setp.lt.u32 p, %1, %2;\n\t"
-          "@p red.shared::cta.add.u32 [%0], 1;\n\t}" ::"r"(counts + 4 * bin), "r"(bin), "n"(Bins::kBins - 1) : "memory");
+    // Both counts' addresses are made at once, in 16 bits each beside the window's own:
+    // the bins are at the start of the CTA's memory, whose place in a cluster is above.
+    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(s.bins.count)), counts = (base & 0xFFFFu) * 0x10001u;
+    const bool placed = (base & 0xFFFFu) <= 0x8000u;
+    auto add = [&](uint32_t d) {
+      const uint32_t at = d * 4 + counts;
+      asm volatile("red.shared::cta.add.u32 [%0], 1;" ::"r"(__byte_perm(at, base, 0x7610)) : "memory");
+      asm volatile("red.shared::cta.add.u32 [%0], 1;" ::"r"(__byte_perm(at, base, 0x7632)) : "memory");
     };
-    job.template each<4>([&](const uint4& q, int j) {
+    if (placed) job.template each<4>([&](const uint4& q, int j) {
       const uint32_t w[4] = {q.x, q.y, q.z, q.w};
       uint32_t first = 0xFFFFFFFFu;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t d = Bins::two(w[i]);
         first = min_u16x2(first, d);
-        add(d & 0xFFFFu);
-        add(d >> 16);
+        add(d);
       }
       least = min_u16x2(least, first);
       job.largest_of[j - job.j0] = static_cast<uint8_t>(Bins::coarse(min(first & 0xFFFFu, first >> 16)));
@@ -914,6 +916,8 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
     __syncthreads();
     ask.scale = job.scale = s.scale;
     ask.least = s.least;
+    // (-infinity and what is -4096 or below it does not count)
+    if (tid == kSampleThreads - 1) s.bins.count[Bins::kBins - 1] = 0;
     if (tid < ctas) {
       for (int w = 0; w < kSampleWarps; ++w) least = min(least, s.warp_count[w][0]);
       job.of(tid).top[rank] = least;
@@ -923,7 +927,7 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
     for (int o = 0; o < ctas; ++o) least = min(least, s.top[o]);
     // rows whose order or weights the bins do not tell
     const int top = static_cast<int>(least);
-    simple = top > 0 && top < Bins::kBins - 1 && top != Bins::kHalf - 1 && top != Bins::kHalf;
+    simple = placed && top > 0 && top < Bins::kBins - 1 && top != Bins::kHalf - 1 && top != Bins::kHalf;
     job.top = Bins::value(top);
   } else {
     uint32_t key;

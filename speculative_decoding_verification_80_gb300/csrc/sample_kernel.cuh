@@ -84,8 +84,13 @@ struct SampleBinsShared<__nv_bfloat16> {
 template <>
 struct SampleBinsShared<float> {
   uint32_t count[8192], lo[8192], hi[8192];  // halves of the sums
-  uint32_t near_key[kNear];
-  unsigned long long near_weight[kNear];
+  union {
+    struct {
+      unsigned long long near_weight[kNear];
+      uint32_t near_key[kNear];
+    };
+    float queue[kSampleWarps][64];  // logits whose weights a warp makes next
+  };
 };
 
 // A bit for each vector of a CTA's part in which a border's logit is: in the bins'
@@ -275,59 +280,60 @@ struct SampleJob {
   // Adds the CTAs' histograms up, a share of the bins each, and the sums of every
   // group, which all CTAs get.  A group is one thread's, or as many threads' as
   // there are CTAs.
-  __device__ __forceinline__ void add_up(const SampleAsk& ask) {
+  // (fp32: the counts, and later the sums)
+  __device__ __forceinline__ void add_up(bool counts, bool sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, of_thread = kOfGroup / ctas;
     const int me = rank * kSampleThreads + threadIdx.x;
-    {
-      uint32_t cs = 0;
-      unsigned long long ws = 0;
+    uint32_t cs = 0;
+    unsigned long long ws = 0;
 #pragma unroll 2
-      for (int i = 0; i < of_thread; i += 2) {
-        const int bin = me * of_thread + i;
-        uint2 c = make_uint2(0, 0);
-        unsigned long long w = 0, x = 0;
-        for (int o = 0; o < ctas; ++o) {
-          const SampleFast<Elt>& from = ctas > 1 ? of(o) : s;
+    for (int i = 0; i < of_thread; i += 2) {
+      const int bin = me * of_thread + i;
+      uint2 c = make_uint2(0, 0);
+      unsigned long long w = 0, x = 0;
+      for (int o = 0; o < ctas; ++o) {
+        const SampleFast<Elt>& from = ctas > 1 ? of(o) : s;
+        if (counts) {
           const uint2 d = *reinterpret_cast<const uint2*>(&from.bins.count[bin]);
           c.x += d.x, c.y += d.y;
-          if constexpr (sizeof(Elt) == 4) {
+        }
+        if constexpr (sizeof(Elt) == 4) {
+          if (sums) {
             const uint2 lo = *reinterpret_cast<const uint2*>(&from.bins.lo[bin]), hi = *reinterpret_cast<const uint2*>(&from.bins.hi[bin]);
             w += (static_cast<unsigned long long>(hi.x) << 32) + lo.x;
             x += (static_cast<unsigned long long>(hi.y) << 32) + lo.y;
           }
         }
-        if (ctas > 1) {
-          *reinterpret_cast<uint2*>(&s.bins.count[bin]) = c;
-          if constexpr (sizeof(Elt) == 4) {
+      }
+      if (ctas > 1) {
+        if (counts) *reinterpret_cast<uint2*>(&s.bins.count[bin]) = c;
+        if constexpr (sizeof(Elt) == 4) {
+          if (sums) {
             *reinterpret_cast<uint2*>(&s.bins.lo[bin]) = make_uint2(static_cast<uint32_t>(w), static_cast<uint32_t>(x));
             *reinterpret_cast<uint2*>(&s.bins.hi[bin]) = make_uint2(static_cast<uint32_t>(w >> 32), static_cast<uint32_t>(x >> 32));
           }
         }
-        if constexpr (sizeof(Elt) == 2) {
-          if ((c.x | c.y) != 0) w = c.x * weight(Bins::value(bin)), x = c.y * weight(Bins::value(bin + 1));
-        }
-        cs += c.x + c.y;
-        ws += w + x;
       }
-      for (int d = 1; d < ctas; d <<= 1) {
-        cs += __shfl_xor_sync(0xFFFFFFFFu, cs, d);
-        ws += __shfl_xor_sync(0xFFFFFFFFu, ws, d);
+      if constexpr (sizeof(Elt) == 2) {
+        if ((c.x | c.y) != 0) w = c.x * weight(Bins::value(bin)), x = c.y * weight(Bins::value(bin + 1));
       }
-      SampleFast<Elt>& to = ctas > 1 ? of(threadIdx.x % ctas) : s;
-      to.group_count[me / ctas] = cs;
-      to.group_sum[me / ctas] = ws;
+      cs += c.x + c.y;
+      ws += w + x;
     }
-    if (ask.least > 0 && warp == kSampleWarps - 1) {
-      const uint32_t key = least_key(kKeyFloor, key_of(top), ask.least);
-      if (lane == 0) s.least_key = key;
+    for (int d = 1; d < ctas; d <<= 1) {
+      cs += __shfl_xor_sync(0xFFFFFFFFu, cs, d);
+      ws += __shfl_xor_sync(0xFFFFFFFFu, ws, d);
     }
+    SampleFast<Elt>& to = ctas > 1 ? of(threadIdx.x % ctas) : s;
+    if (counts) to.group_count[me / ctas] = cs;
+    if (sums) to.group_sum[me / ctas] = ws;
     meet();
     // sums before each group
     static_assert(kGroups == kSampleThreads, "a thread for each group");
     const uint32_t c = s.group_count[threadIdx.x];
     const unsigned long long w = s.group_sum[threadIdx.x];
-    uint32_t cs = c;
-    unsigned long long ws = w;
+    cs = c;
+    ws = w;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const uint32_t co = __shfl_up_sync(0xFFFFFFFFu, cs, d);
@@ -340,19 +346,46 @@ struct SampleJob {
     unsigned long long w_all;
     cs += sum_of_warps(&s.warp_count[0][0], 2, &c_all);
     ws += sum_of_warps(&s.warp_sum[0], 1, &w_all);
-    s.group_count[threadIdx.x] = cs - c;
-    s.group_sum[threadIdx.x] = ws - w;
-    if (threadIdx.x == 0) s.group_count[kGroups] = c_all, s.group_sum[kGroups] = w_all;
+    if (counts) {
+      s.group_count[threadIdx.x] = cs - c;
+      if (threadIdx.x == 0) s.group_count[kGroups] = c_all;
+    }
+    if (sums) {
+      s.group_sum[threadIdx.x] = ws - w;
+      if (threadIdx.x == 0) s.group_sum[kGroups] = w_all;
+    }
     __syncthreads();
   }
+  // min-p's key, by the last warp.
+  __device__ __forceinline__ void find_least(const SampleAsk& ask) {
+    if (ask.least == 0 || threadIdx.x < kSampleThreads - 32) return;
+    const uint32_t key = least_key(kKeyFloor, key_of(top), ask.least);
+    if (threadIdx.x % 32 == 0) s.least_key = key;
+  }
 
-  // fp32: every id's weight into its bin; with `counted` the ids are counted too.
-  __device__ __forceinline__ void add_weights(bool counted) {
+  // The least logit of a bin and those before it (fp32).
+  static __device__ __forceinline__ float end_of(int bin) {
+    if (bin >= Bins::kBins - 1) return -INFINITY;
+    if (bin < Bins::kHalf) return Bins::value(bin);
+    return __uint_as_float(0x80000000u | (static_cast<uint32_t>(bin - Bins::kHalf) + Bins::kBase) << 16 | 0xFFFFu);
+  }
+  // fp32: the weights into the bins.  Of ids that cannot be kept none is needed: those
+  // in a bin past top-k's, and, where no top-p asks for a share of them, min-p's.  A
+  // warp gathers the others and makes 32 weights at once (of a tenth of the ids, each
+  // warp's own few took as long as all).
+  __device__ __forceinline__ void add_weights(const SampleAsk& ask) {
     if constexpr (sizeof(Elt) == 4) {
-      each_id<1>([&](float x, int) {
-        if (x == -INFINITY) return;
+      float least = ask.least > 0 && !(ask.p < 1.f) ? of_key(s.least_key) : -3.402823466e38f;
+      if (ask.k < row.V) {
+        add_up(true, false);
+        SampleBin f;
+        if (find(kByCount, ask.k, &f)) least = fmaxf(least, end_of(f.bin));
+      }
+      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+      float* queue = s.bins.queue[warp];
+      int queued = 0;
+      auto one = [&](float x) {
         const int bin = Bins::one(x);
-        if (counted) atomicAdd(&s.bins.count[bin], 1u);
         const unsigned long long w = weight(x);
         const uint32_t lo = static_cast<uint32_t>(w);
         uint32_t hi = static_cast<uint32_t>(w >> 32);
@@ -361,8 +394,46 @@ struct SampleJob {
           hi += old + lo < old ? 1 : 0;
         }
         if (hi != 0) atomicAdd(&s.bins.hi[bin], hi);
-      });
+      };
+      if (least < -3.4e38f) {
+        // four chains of instructions a thread
+        each_id<1>([&](float x, int) {
+          if (x != -INFINITY) one(x);
+        });
+      } else {
+        // four vectors are on their way; registers move so that the code is there once
+        const uint4 none = make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+        uint4 ahead[4];
+        int j = j0 + 32 * warp + lane;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ahead[i] = j + i * kSampleThreads < j1 ? words(j + i * kSampleThreads) : none;
+#pragma unroll 1
+        for (; j - lane < j1; j += kSampleThreads) {
+          const float f[4] = {__uint_as_float(ahead[0].x), __uint_as_float(ahead[0].y), __uint_as_float(ahead[0].z), __uint_as_float(ahead[0].w)};
+#pragma unroll
+          for (int i = 0; i < 3; ++i) ahead[i] = ahead[i + 1];
+          ahead[3] = j + 4 * kSampleThreads < j1 ? words(j + 4 * kSampleThreads) : none;
+          if (!__any_sync(0xFFFFFFFFu, fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])) >= least)) continue;
+#pragma unroll 1
+          for (int e = 0; e < 4; ++e) {
+            float x = e & 2 ? (e & 1 ? f[3] : f[2]) : (e & 1 ? f[1] : f[0]);
+            const uint32_t m = __ballot_sync(0xFFFFFFFFu, x >= least);
+            if (m == 0) continue;
+            if (x >= least) queue[queued + __popc(m & ((1u << lane) - 1))] = x;
+            queued += __popc(m);
+            if (queued < 32) continue;
+            queued -= 32;
+            __syncwarp();
+            x = queue[queued + lane];
+            __syncwarp();
+            one(x + 0.f);
+          }
+        }
+        __syncwarp();
+        if (lane < queued) one(queue[lane] + 0.f);
+      }
       meet();
+      add_up(false, true);
     }
   }
   __device__ __forceinline__ void clear_bins() {
@@ -498,7 +569,7 @@ struct SampleJob {
         });
       } else {  // a bin of one beginning of 16 bits
         const uint32_t first = __float_as_uint(Bins::value(f.bin)) & 0xFFFF0000u;
-        each<4>([&](const uint4& q, int) {
+        each<8>([&](const uint4& q, int) {
           const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -742,13 +813,18 @@ struct SampleJob {
     }
   }
 
-  // The largest logit's key and its first id, over the cluster.
+  // The largest logit's key and its first id, over the cluster.  With kCounted the ids
+  // are counted in their bins.
+  template <bool kCounted>
   __device__ __forceinline__ void largest(uint32_t* key, int* id) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float best = -INFINITY;
     int at = 0x7FFFFFFF;
-    each_id<4>([&](float x, int i) {
+    each_id<sizeof(Elt) == 4 ? 8 : 4>([&](float x, int i) {
       if (x > best || (x == best && i < at && x != -INFINITY)) best = x, at = i;
+      if constexpr (kCounted) {
+        if (x != -INFINITY) atomicAdd(&s.bins.count[Bins::one(x)], 1u);
+      }
     });
     uint32_t k = key_of(best);
     const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, k);
@@ -865,7 +941,7 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
     uint32_t key;
     int id;
     job.wait_begun();
-    job.largest(&key, &id);
+    job.template largest<false>(&key, &id);
     if (key <= kKeyFloor) bad |= SPECDEC_DEV_ERR_SAMPLE, id = -1;
     if (first && token != nullptr) *token = id;
     if (first && bad != 0 && a.err != nullptr) atomicOr(a.err, bad);
@@ -933,18 +1009,26 @@ __global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) samp
     uint32_t key;
     int id;
     job.wait_begun();
-    job.largest(&key, &id);
+    if (ask.k < a.V)
+      job.template largest<true>(&key, &id);
+    else
+      job.template largest<false>(&key, &id);
     ask.scale = job.scale = s.scale;
     ask.least = s.least;
     simple = key > kKeyFloor && key < key_of(INFINITY);
     job.top = of_key(key);
-    if (simple) job.add_weights(ask.k < a.V);
+    if (simple) {
+      job.find_least(ask);
+      __syncthreads();
+      job.add_weights(ask);
+    }
   }
 
   SamplePlace kept = {kKeyFloor + 1, 0, 0, 0}, drawn = {0, 0, 0, 0};
   if (simple) {
-    job.add_up(ask);
     if constexpr (sizeof(Elt) == 2) {
+      job.find_least(ask);
+      job.add_up(true, true);
       // logits of -4096 and below are not counted: they have no weight and are not kept, or the row is another's
       const uint32_t ids = s.group_count[kSampleGroups];
       if ((ask.k < a.V && static_cast<uint32_t>(ask.k) > ids) || !((job.top + 4096.f) * ask.scale.hi > 49.f)) simple = !job.any_far();

@@ -29,8 +29,13 @@ cudaError_t launch_sample(const SampleArgs& a, cudaStream_t st) {
     ready[dev] = true;
   }
   const int64_t rows = static_cast<int64_t>(a.B) * (a.n_max + 1);
+  // A row's parts: as many as half of the SMs have room for, or two on all of them.
+  // (One row of 128256 bf16 logits in 1, 2, 4 and 8 parts: 26.8, 24.7, 20.6 and 18.5
+  // us; 19 rows 28.7, 24.7, 20.6, 21.7; 38 rows 28.7, 24.7, 25.4, 37.0; 76 rows 28.8,
+  // 26.0, 41, 58; 152 rows 28.8, 32.9.  Of 32003 all take 18.5.)
   int ctas = 1;
-  while (ctas < kSampleClusterMax && 2 * ctas * rows <= 2 * sms && a.V * static_cast<int>(sizeof(Elt)) >= 16384 * ctas) ctas *= 2;
+  if (static_cast<int64_t>(a.V) * sizeof(Elt) >= 65536)
+    while (ctas < kSampleClusterMax && (4 * ctas * rows <= sms || (ctas == 1 && 2 * rows <= sms))) ctas *= 2;
   cudaLaunchConfig_t config = {};
   config.gridDim = dim3(static_cast<unsigned>(rows * ctas));
   config.blockDim = dim3(kSampleThreads);

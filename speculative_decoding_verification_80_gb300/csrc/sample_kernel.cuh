@@ -888,7 +888,7 @@ __device__ __forceinline__ bool SampleJob<Elt>::decide(const SampleAsk& ask, boo
 
 // One cluster a row.
 template <typename Elt>
-__global__ void __launch_bounds__(kSampleThreads, sizeof(Elt) == 2 ? 3 : 2) sample_kernel(const SampleArgs a, int ctas) {
+__global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleArgs a, int ctas) {
   extern __shared__ __align__(16) unsigned char sample_smem[];
   using Bins = SampleBinsOf<Elt>;
   SampleSmem<Elt>& smem = *reinterpret_cast<SampleSmem<Elt>*>(sample_smem);

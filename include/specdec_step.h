@@ -240,7 +240,8 @@ specdec_status_t spec_process_logits(const void* logits, void* out, specdec_dtyp
  * number above -infinity gives -1 and keeps nothing; infinite logits are equal,
  * and the others count as -infinity beside them.
  * Weights are whole numbers of 2^-44 of the largest, within 2^-40 of their value,
- * and all sums are exact.
+ * and their sums are exact.  (bf16 logits within 1.01 * 2^-20 of 0 weigh as 0 does
+ * where that changes the sum by less than 2^-40 of itself.)
  */
 specdec_status_t spec_sample(const void* logits, void* out, specdec_dtype_t dtype, int32_t B, int32_t n_max, int32_t V,
                              const int32_t* draft_len, const float* temperature, const int32_t* top_k,
@@ -253,8 +254,9 @@ specdec_status_t spec_sample(const void* logits, void* out, specdec_dtype_t dtyp
  *   q, k          [T, Hq, D] and [T, H, D] of dtype; token t's head h starts at
  *                 t * token_stride + h * head_stride elements, its D values are
  *                 contiguous.  Hq or H may be 0 (their pointers are not looked at).
- *   q_out, k_out  the same, with strides of their own; the inputs themselves with
- *                 their strides, or memory that no input shares.
+ *   q_out, k_out  the same, with strides of their own, rows apart from one another;
+ *                 the inputs themselves with their strides, or memory that no input
+ *                 shares.
  *   positions     [T] int32, as kv_block_step lists them; rows of tokens with
  *                 negative ones are left as they were.
  *   turns         [rotary_dim / 2]: what pair i turns by a position, in 2^-64 of a
@@ -315,7 +317,8 @@ size_t specdec_page_workspace_bytes(int32_t num_blocks);
  *                 meaning.
  * shares_out and ring_state_out may be the inputs; the tables, kv_len and held may
  * not.  Out of range: a parent is none, a length is clamped to what is held, held to
- * the table's width, a block id is left where it is; each sets SPECDEC_DEV_ERR_BLOCKS.
+ * the table's width, a block id (the ring's too) is left as it is; each sets
+ * SPECDEC_DEV_ERR_BLOCKS.
  */
 specdec_status_t kv_fork(int32_t P, int32_t B, int32_t block_size, int32_t max_blocks, int32_t num_blocks,
                          const int32_t* block_table, const int32_t* kv_len, const int32_t* accepted_len,

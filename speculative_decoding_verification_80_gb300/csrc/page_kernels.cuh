@@ -169,8 +169,10 @@ __device__ __forceinline__ void fork_plan(const ForkArgs& a) {
       a.held_out[b] = full + (partial && (!ask || got) ? 1 : 0);
       a.kv_len_out[b] = ask && !got ? full << a.bs_log2 : tokens;
       if (got) {
+        const int to = a.ring[(static_cast<long long>(head) + number) % N];
+        if (to < 0 || to >= N) bad = 1;
         a.copies[2 * number] = x;
-        a.copies[2 * number + 1] = a.ring[(static_cast<long long>(head) + number) % N];
+        a.copies[2 * number + 1] = to;
       }
     }
   }

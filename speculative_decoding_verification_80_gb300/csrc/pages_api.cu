@@ -116,7 +116,7 @@ extern "C" specdec_status_t kv_compact(int32_t B, int32_t max_blocks, int32_t nu
   if (B < 0 || max_blocks <= 0 || num_blocks <= 0) return SPECDEC_ERR_INVALID_ARG;
   if (B > SPECDEC_MAX_BATCH || num_blocks > (1 << 27)) return SPECDEC_ERR_UNSUPPORTED;
   if (shares == nullptr || free_ring == nullptr || ring_state == nullptr || shares_out == nullptr || ring_out == nullptr ||
-      ring_state_out == nullptr || renamed == nullptr || copies == nullptr || count == nullptr)
+      ring_state_out == nullptr || renamed == nullptr || (copies == nullptr && num_blocks > 1) || count == nullptr)
     return SPECDEC_ERR_INVALID_ARG;
   if (B > 0 && (block_table == nullptr || held == nullptr || table_out == nullptr)) return SPECDEC_ERR_INVALID_ARG;
   const specdec_status_t ws = check_workspace(workspace, workspace_bytes, num_blocks);

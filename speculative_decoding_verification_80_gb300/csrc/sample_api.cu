@@ -164,6 +164,7 @@ extern "C" specdec_status_t spec_rotary(const void* q, const void* k, specdec_dt
     if (x[w] == y[w] && (s[0] != s[2] || s[1] != s[3])) return SPECDEC_ERR_INVALID_ARG;
     // rows of an output lie apart
     if ((T > 1 && s[2] < D) || (a.heads[w] > 1 && s[3] < D)) return SPECDEC_ERR_INVALID_ARG;
+    if (T > 1 && a.heads[w] > 1 && s[2] < (a.heads[w] - 1) * s[3] + D && (s[3] - D) / (T - 1) < s[2]) return SPECDEC_ERR_INVALID_ARG;
     a.x[w] = static_cast<const char*>(x[w]);
     a.y[w] = static_cast<char*>(y[w]);
     a.x_token[w] = s[0] * elt;

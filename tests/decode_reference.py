@@ -118,6 +118,7 @@ def fork(table, kv_len, accepted, held, parent, keep, shares, ring, state, bs):
             tokens[b] = tokens[b] // bs * bs
             continue
         fresh = int(ring[(head + len(copies)) % N])
+        bad |= not 0 <= fresh < N
         copies.append((x, fresh))
         rows[b][-1] = fresh
     for i, x in enumerate(back):

@@ -54,6 +54,8 @@ def test_rotary_refusals(lib):
     assert call(q=P(0x1001)) == 1 and call(qs=(-512, 64)) == 1
     assert call(qos=(1024, 64)) == 1                      # in place with other strides
     assert call(qo=other, qos=(32, 64)) == 1 and call(qo=other, qos=(512, 32)) == 1   # rows of an output that overlap
+    assert call(qo=other, qos=(64, 64)) == 1 and call(qo=other, qos=(500, 64)) == 1 and call(qs=(64, 64)) == 1   # tokens over heads
+    assert call(qs=(64, 319)) == 1                        # heads over tokens
     assert call(D=2000, R=64) == 2 and call(Hq=70000) == 2
     assert call(T=0, q=None) == 0
 

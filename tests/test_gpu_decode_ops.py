@@ -148,6 +148,52 @@ def test_sample_masks_infinities_and_nan(dtype):
     _sample(t, T=np.zeros(10), u=u, bits=sd.DEV_ERR_SAMPLE)
 
 
+def _special_rows(V, rng):
+    lowest = -3.3895e38
+    few = np.full(V, -INF)
+    few[rng.integers(0, V, 30)] = rng.normal(0, 2, 30)
+    return {
+        "equal": np.zeros(V), "equal and low": np.full(V, -9000.0), "two values": np.where(np.arange(V) % 3 == 0, 1.0, 0.5),
+        "whole numbers": rng.integers(-4, 5, V).astype(float), "far": rng.normal(9000, 3, V), "around zero": rng.normal(0, 1e-7, V),
+        "tiny": rng.normal(0, 1e-30, V), "some tiny": np.where(rng.random(V) < 0.3, rng.normal(0, 1e-8, V), rng.normal(0, 1, V)),
+        "lowest value masks": np.where(rng.random(V) < 0.9, lowest, rng.normal(0, 2, V)), "few left": few,
+        "few left by lowest values": np.where(np.isinf(few), lowest, few), "infinite": np.where(np.arange(V) % 5000 == 7, INF, 0.0),
+        "nan": np.where(rng.random(V) < 0.1, math.nan, rng.normal(0, 2, V)), "one high": np.where(np.arange(V) == V - 1, 50.0, rng.normal(0, 2, V)),
+        "negative": -np.abs(rng.normal(20, 5, V)), "down to minus 5000": -5000 * rng.random(V), "high": rng.normal(3900, 100, V),
+        "nothing": np.full(V, -INF)}
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [3001, 70001])
+def test_sample_special_rows(V, dtype):
+    """Rows that the usual way's bins do not tell apart, in one part and (70001) in several."""
+    rng = np.random.default_rng(V + 1)
+    asks = [dict(), dict(k=[100], p=[0.9]), dict(p=[0.97]), dict(k=[20000], m=[0.3]), dict(m=[0.05]), dict(T=[100.0], k=[2500], p=[0.5]),
+            dict(T=[2e-4], p=[0.8])]
+    for name, row in _special_rows(V, rng).items():
+        x = dev(row.astype(np.float32), dtype).view(1, 1, V)
+        for ask in asks:
+            try:
+                _sample(x, u=rng.random((1, 1)).astype(np.float32), bits=sd.DEV_ERR_SAMPLE if name == "nothing" else 0, **ask)
+            except AssertionError as e:
+                raise AssertionError(f"{name}, {ask}") from e
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B", [1, 3, 9, 30, 70, 160])
+def test_sample_row_in_parts(B, dtype):
+    """As many CTAs a row as there is room for, in place and from any element on."""
+    V = 66003
+    rng = np.random.default_rng(B)
+    x = _rows(rng, B, 1, V, dtype, lift=8.0)
+    kw = dict(T=0.5 + rng.random(B), k=rng.choice([0, 1, 30, 3000], B), p=rng.choice([1.0, 0.9], B), m=rng.choice([0.0, 0.1], B),
+              u=rng.random((B, 1)).astype(np.float32))
+    a, _ = _sample(x.clone(), **kw)
+    b, _ = _sample(x.clone(), in_place=True, **kw)
+    c, _ = _sample(torch.empty(x.numel() + 5, dtype=dtype, device="cuda")[5:].view_as(x).copy_(x), **kw)
+    assert torch.equal(a, b) and torch.equal(a, c)
+
+
 def test_sample_reports_bad_values():
     rng = np.random.default_rng(4)
     x = _rows(rng, 6, 2, 999, torch.float32)
@@ -194,9 +240,9 @@ def test_sample_follows_the_shares():
     assert np.abs(got - n * w).max() <= 1  # the borders fall between two of the numbers
 
 
-def test_sample_in_a_graph_and_on_another_stream():
+@pytest.mark.parametrize("B,V", [(5, 32003), (2, 128256), (30, 70001)])
+def test_sample_in_a_graph_and_on_another_stream(B, V):
     rng = np.random.default_rng(9)
-    B, V = 5, 32003
     x = _rows(rng, B, 1, V, torch.bfloat16)
     u = dev(rng.random((B, 1)).astype(np.float32))
     p = torch.full((B,), 0.9, device="cuda")
@@ -460,6 +506,15 @@ def test_fork_reports_bad_values():
         assert _check_fork(c, parent, 16)["bad"]
 
 
+def test_fork_reports_a_bad_block_of_the_ring():
+    c = dict(table=np.array([[2, 0]]), held=[2], kv=np.array([20]), shares=np.zeros(5, dtype=int), ring=np.array([1, 5, -7, 3, 4]),
+             state=np.array([1, 2]))
+    want = _check_fork(c, np.zeros(3, dtype=int), 16)
+    assert want["bad"] and want["copies"] == [(0, 5), (0, -7)]
+    layers = _layers(2, 5, 1, 16, 64)
+    _check_copy(layers, want["copies"] + [(0, 4)], 3, 3)  # (passes the two over)
+
+
 def test_forks_one_after_another_on_one_workspace():
     rng = np.random.default_rng(21)
     c = _pool(rng, 12, 8, 16, spare=200)
@@ -496,6 +551,12 @@ def test_compact(P, W, spare, alias):
     rng = np.random.default_rng(P + spare)
     c = _pool(rng, P, W, 16, spare=spare)
     assert not _check_compact(c, alias)["bad"]
+
+
+def test_compact_of_one_block():
+    c = dict(table=np.array([[0]]), held=np.array([1]), shares=np.array([0]), ring=np.array([-1]), state=np.array([0, 0]))
+    _check_compact(c)
+    _check_compact(c, alias=True)
 
 
 def test_compact_keeps_blocks_that_no_table_names():

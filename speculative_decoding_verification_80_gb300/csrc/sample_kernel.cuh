@@ -83,14 +83,13 @@ struct SampleBinsShared<__nv_bfloat16> {
 };
 template <>
 struct SampleBinsShared<float> {
-  uint32_t count[8192], lo[8192], hi[8192];  // halves of the sums
   union {
-    struct {
-      unsigned long long near_weight[kNear];
-      uint32_t near_key[kNear];
-    };
-    float queue[kSampleWarps][64];  // logits whose weights a warp makes next
+    uint32_t count[8192];
+    float list[8192];  // once the counts are done with: the logits that may be kept
   };
+  uint32_t lo[8192], hi[8192];  // halves of the sums
+  unsigned long long near_weight[kNear];
+  uint32_t near_key[kNear];
 };
 
 // A bit for each vector of a CTA's part in which a border's logit is: in the bins'
@@ -118,7 +117,7 @@ struct SampleFast {
   uint32_t top[kSampleClusterMax], flag[kSampleClusterMax];
   int32_t id[kSampleClusterMax];
   uint32_t same[kSampleClusterMax][2];
-  uint32_t listed, least_key;
+  uint32_t listed, gathered, least_key;
   unsigned long long zero[2];   // bf16: sums of the bins of zero
   bool zeroed;                  // they are in use
   SamplePlace kept, drawn;
@@ -174,6 +173,8 @@ struct SampleJob {
   int j0, j1;       // this CTA's vectors
   float top;        // the largest logit
   WeightScale scale;
+  int in_list = -1;             // fp32: logits in this CTA's list, -1: there is none
+  SampleBin of_k = {-1, 0, 0, 0, 0};  // fp32: top-k's bin and its counts
 
   __device__ __forceinline__ SampleFast<Elt>& of(int cta) const { return *cluster.map_shared_rank(&s, cta); }
   // That the others have begun, so that their memory may be written: said early, and
@@ -369,21 +370,60 @@ struct SampleJob {
     if (bin < Bins::kHalf) return Bins::value(bin);
     return __uint_as_float(0x80000000u | (static_cast<uint32_t>(bin - Bins::kHalf) + Bins::kBase) << 16 | 0xFFFFu);
   }
+  // fp32: this CTA's logits from `least` on into its list, in any order.
+  __device__ __forceinline__ void gather(float least) {
+    if constexpr (sizeof(Elt) == 4) {
+      constexpr int kAtOnce = 4, kRoom = Bins::kBins;
+      const int lane = threadIdx.x & 31;
+      const uint4 none = make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+#pragma unroll 1
+      for (int j = j0 + static_cast<int>(threadIdx.x); j - lane < j1; j += kAtOnce * kSampleThreads) {
+        uint4 q[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) q[i] = j + i * kSampleThreads < j1 ? words(j + i * kSampleThreads) : none;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const float f[4] = {__uint_as_float(q[i].x), __uint_as_float(q[i].y), __uint_as_float(q[i].z), __uint_as_float(q[i].w)};
+          uint32_t m[4], n = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m[e] = __ballot_sync(0xFFFFFFFFu, f[e] >= least), n += __popc(m[e]);
+          if (n == 0) continue;
+          uint32_t at = 0;
+          if (lane == 0) at = atomicAdd(&s.gathered, n);
+          at = __shfl_sync(0xFFFFFFFFu, at, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t mine = at + __popc(m[e] & ((1u << lane) - 1));
+            if (f[e] >= least && mine < kRoom) s.bins.list[mine] = f[e] + 0.f;
+            at += __popc(m[e]);
+          }
+        }
+      }
+      __syncthreads();
+      if (s.gathered <= kRoom) in_list = static_cast<int>(s.gathered);
+    }
+  }
   // fp32: the weights into the bins.  Of ids that cannot be kept none is needed: those
-  // in a bin past top-k's, and, where no top-p asks for a share of them, min-p's.  A
-  // warp gathers the others and makes 32 weights at once (of a tenth of the ids, each
-  // warp's own few took as long as all).
+  // in a bin past top-k's, and, where no top-p asks for a share of them, min-p's.  The
+  // others are listed in the counts' place, where there is room for them, and nothing
+  // but the last pass reads the row again.  (Of 50001 ids the weights of 5000 took 35
+  // us a row, as those of all, when each warp gathered its own 32 at a time.)
   __device__ __forceinline__ void add_weights(const SampleAsk& ask) {
     if constexpr (sizeof(Elt) == 4) {
-      float least = ask.least > 0 && !(ask.p < 1.f) ? of_key(s.least_key) : -3.402823466e38f;
+      float least = of_key(s.least_key);
+      bool few = ask.least > 0 && !(ask.p < 1.f);
       if (ask.k < row.V) {
         add_up(true, false);
-        SampleBin f;
-        if (find(kByCount, ask.k, &f)) least = fmaxf(least, end_of(f.bin));
+        if (find(kByCount, ask.k, &of_k)) {
+          // (the border itself is looked for among them: min-p does not shorten the list)
+          least = end_of(of_k.bin);
+          few = of_k.c0 + of_k.c <= Bins::kBins;
+        } else {
+          of_k.bin = -1;
+        }
+        meet();  // (the counts' readers)
       }
-      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-      float* queue = s.bins.queue[warp];
-      int queued = 0;
+      if (few) gather(least);
       auto one = [&](float x) {
         const int bin = Bins::one(x);
         const unsigned long long w = weight(x);
@@ -395,42 +435,14 @@ struct SampleJob {
         }
         if (hi != 0) atomicAdd(&s.bins.hi[bin], hi);
       };
-      if (least < -3.4e38f) {
+      if (in_list >= 0) {
+#pragma unroll 2
+        for (int i = threadIdx.x; i < in_list; i += kSampleThreads) one(s.bins.list[i]);
+      } else {
         // four chains of instructions a thread
         each_id<1>([&](float x, int) {
           if (x != -INFINITY) one(x);
         });
-      } else {
-        // four vectors are on their way; registers move so that the code is there once
-        const uint4 none = make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
-        uint4 ahead[4];
-        int j = j0 + 32 * warp + lane;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ahead[i] = j + i * kSampleThreads < j1 ? words(j + i * kSampleThreads) : none;
-#pragma unroll 1
-        for (; j - lane < j1; j += kSampleThreads) {
-          const float f[4] = {__uint_as_float(ahead[0].x), __uint_as_float(ahead[0].y), __uint_as_float(ahead[0].z), __uint_as_float(ahead[0].w)};
-#pragma unroll
-          for (int i = 0; i < 3; ++i) ahead[i] = ahead[i + 1];
-          ahead[3] = j + 4 * kSampleThreads < j1 ? words(j + 4 * kSampleThreads) : none;
-          if (!__any_sync(0xFFFFFFFFu, fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])) >= least)) continue;
-#pragma unroll 1
-          for (int e = 0; e < 4; ++e) {
-            float x = e & 2 ? (e & 1 ? f[3] : f[2]) : (e & 1 ? f[1] : f[0]);
-            const uint32_t m = __ballot_sync(0xFFFFFFFFu, x >= least);
-            if (m == 0) continue;
-            if (x >= least) queue[queued + __popc(m & ((1u << lane) - 1))] = x;
-            queued += __popc(m);
-            if (queued < 32) continue;
-            queued -= 32;
-            __syncwarp();
-            x = queue[queued + lane];
-            __syncwarp();
-            one(x + 0.f);
-          }
-        }
-        __syncwarp();
-        if (lane < queued) one(queue[lane] + 0.f);
       }
       meet();
       add_up(false, true);
@@ -563,7 +575,12 @@ struct SampleJob {
         const uint32_t at = atomicAdd(&lead.listed, 1u);
         if (at < kNear) lead.bins.near_key[at] = key_of(x);
       };
-      if (f.bin == 0 || f.bin == Bins::kBins - 1 || f.bin == Bins::kHalf - 1 || f.bin == Bins::kHalf) {
+      if (in_list >= 0) {
+        for (int i = threadIdx.x; i < in_list; i += kSampleThreads) {
+          const float x = s.bins.list[i];
+          if (Bins::one(x) == f.bin) list(x);
+        }
+      } else if (f.bin == 0 || f.bin == Bins::kBins - 1 || f.bin == Bins::kHalf - 1 || f.bin == Bins::kHalf) {
         each_id<1>([&](float x, int) {
           if (x != -INFINITY && Bins::one(x) == f.bin) list(x);
         });
@@ -853,7 +870,17 @@ template <typename Elt>
 __device__ __forceinline__ bool SampleJob<Elt>::decide(const SampleAsk& ask, bool draw, SamplePlace* kept, SamplePlace* drawn) {
   SampleBin f;
   unsigned long long weights = s.group_sum[kGroups];
-  if (ask.k < row.V && find(kByCount, ask.k, &f)) {
+  bool cut = false;  // by top-k
+  if constexpr (sizeof(Elt) == 4) {
+    cut = of_k.bin >= 0;
+    if (cut) {
+      look_up(of_k.bin, &f);  // (its sums; the counts are gone)
+      f.c0 = of_k.c0, f.c = of_k.c;
+    }
+  } else {
+    cut = ask.k < row.V && find(kByCount, ask.k, &f);
+  }
+  if (cut) {
     if (!resolve(f, kByCount, ask.k, kept)) return false;
     weights = kept->sum + kept->ids * weight(of_key(kept->key));
   }
@@ -953,7 +980,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
   // the histogram, and the largest logit
   job.clear_bins();
   if (tid < 256) s.table[tid] = kExp2Table[tid];
-  if (tid == 0) s.listed = 0, s.zeroed = false, s.zero[0] = s.zero[1] = 0;
+  if (tid == 0) s.listed = s.gathered = 0, s.zeroed = false, s.zero[0] = s.zero[1] = 0;
   __syncthreads();
   if (tid == kSampleThreads - 1) {
     // (64-bit arithmetic by one thread, beside the others' work: it has 1/64 of the rate)

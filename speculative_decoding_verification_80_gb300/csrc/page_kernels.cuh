@@ -4,7 +4,9 @@
 //
 // kv_fork and kv_compact are one cooperative launch each of up to a CTA an SM, whose
 // three steps are a barrier of the grid apart.  A few KB to some MB: bound by latency
-// and, a call, by the host, which three launches cost 7 us and one 4.
+// (10 to 16 us on the device for 7 to 4700 moves, most of it the launch, two barriers
+// of the grid and the loads between them) and, a call, by the host, which three
+// launches cost 7 us and one 4.
 #pragma once
 #include <cooperative_groups.h>
 #include <stdint.h>
@@ -398,7 +400,10 @@ struct CopyArgs {
   const int32_t* count;
 };
 
-// A warp takes a part of a block of one layer's keys or values.
+// A warp takes a part of a block of one layer's keys or values: 4 KB, eight loads of 16
+// bytes a lane on their way at once; its first part takes the scales along.  Bytes
+// bound it: 4692 blocks of two layers (615 MB read and written) take 101 us, 6.1 TB/s;
+// 379 blocks of four layers (198 MB) 31 us and 7 of sixteen 6.
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyArgs a) {
   constexpr int kLoads = 8;
   const int lane = threadIdx.x & 31;

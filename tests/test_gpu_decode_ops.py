@@ -194,6 +194,21 @@ def test_sample_row_in_parts(B, dtype):
     assert torch.equal(a, b) and torch.equal(a, c)
 
 
+@pytest.mark.parametrize("B", [1, 40])
+def test_sample_fp32_parts_with_and_without_room(B):
+    """More ids that min-p keeps than some parts of a row can list, none in the others."""
+    rng = np.random.default_rng(B)
+    V = 262144
+    x = rng.normal(-20, 1, (B, 1, V))
+    x[:, :, :65536] = 1 + 7 * rng.random((B, 1, 65536))
+    x = dev(x.astype(np.float32), torch.float32)
+    u = rng.random((B, 1)).astype(np.float32)
+    _sample(x, T=np.full(B, 2.0), m=np.full(B, 0.02), u=u)
+    _sample(x, T=np.full(B, 2.0), m=np.full(B, 0.6), u=u)
+    _sample(x, T=np.full(B, 2.0), k=np.full(B, 8000), m=np.full(B, 0.7), u=u)
+    _sample(x, T=np.full(B, 2.0), k=np.full(B, 40000), p=np.full(B, 0.8), m=np.full(B, 0.1), u=u)
+
+
 def test_sample_reports_bad_values():
     rng = np.random.default_rng(4)
     x = _rows(rng, 6, 2, 999, torch.float32)

@@ -9,7 +9,7 @@
 // Bytes bound it: a token's heads share its sines, which a CTA makes once into shared
 // memory, factor and all, and then has its 256 threads turn 16 bytes of pairs each, two
 // loads and two stores.  Few pairs a token and many tokens: a CTA has several.  50000
-// tokens of 40 heads of 128 in bf16 (1.02 GB) take 162 us, 6.3 TB/s; 512 in fp32 (21
+// tokens of 40 heads of 128 in bf16 (1.02 GB) take 155 us, 6.6 TB/s; 512 in fp32 (21
 // MB) 8.3 us and one 4.2, which are a launch, a position, the sines and the rows one
 // after another.  Products and sums are in 32 bits, and rounded once to bf16.
 #pragma once
@@ -61,7 +61,8 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
     const int32_t angle = static_cast<int32_t>((static_cast<unsigned long long>(static_cast<uint32_t>(p)) * a.turns[c]) >> 32);
     float sn, cs;
     sincospif(static_cast<float>(angle) * 0x1p-31f, &sn, &cs);
-    turn[i] = make_float2(cs * a.factor, sn * a.factor);
+    // (a unit's pairs lie `turned` apart, so that neighbouring lanes read neighbours)
+    turn[t * a.pairs + (c % N) * a.turned + c / N] = make_float2(cs * a.factor, sn * a.factor);
     if (c == 0) position[t] = p;
   }
   __syncthreads();
@@ -77,13 +78,13 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
       *reinterpret_cast<Vec*>(y + at) = *reinterpret_cast<const Vec*>(x + at);
       continue;
     }
-    const float2* r = turn + t * a.pairs + unit * N;
+    const float2* r = turn + t * a.pairs + unit;
     if (kHalf) {
       const int at = unit * N * sizeof(Elt), far = at + a.pairs * sizeof(Elt);
       Vec lo = *reinterpret_cast<const Vec*>(x + at), hi = *reinterpret_cast<const Vec*>(x + far);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const float2 cs = r[e];
+        const float2 cs = r[e * a.turned];
         const float u = rotary_value(lo.v[e]), v = rotary_value(hi.v[e]);
         lo.v[e] = rotary_round<Elt>(u * cs.x - v * cs.y);
         hi.v[e] = rotary_round<Elt>(u * cs.y + v * cs.x);
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
       Vec o[2];
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const float2 cs = r[e];
+        const float2 cs = r[e * a.turned];
         const float u = rotary_value(z[2 * e]), v = rotary_value(z[2 * e + 1]);
         o[2 * e / N].v[2 * e % N] = rotary_round<Elt>(u * cs.x - v * cs.y);
         o[(2 * e + 1) / N].v[(2 * e + 1) % N] = rotary_round<Elt>(u * cs.y + v * cs.x);

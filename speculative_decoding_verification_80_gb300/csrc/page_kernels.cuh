@@ -400,10 +400,10 @@ struct CopyArgs {
   const int32_t* count;
 };
 
-// A warp takes a part of a block of one layer's keys or values: 4 KB, eight loads of 16
-// bytes a lane on their way at once; its first part takes the scales along.  Bytes
-// bound it: 4692 blocks of two layers (615 MB read and written) take 101 us, 6.1 TB/s;
-// 379 blocks of four layers (198 MB) 31 us and 7 of sixteen 6.
+// A warp takes a part of a block of one layer's keys or values: 8 KB, of which eight
+// loads of 16 bytes a lane are on their way at once; its first part takes the scales
+// along.  Bytes bound it: 4692 blocks of two layers (616 MB read and written) take 95
+// us, 6.5 TB/s; 379 blocks of four layers (198 MB) 29 us and 7 of sixteen 6.
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyArgs a) {
   constexpr int kLoads = 8;
   const int lane = threadIdx.x & 31;

@@ -2,11 +2,11 @@
 // that go on from others' tokens (kv_fork), blocks moved to the lowest ids
 // (kv_compact), and the copies that both ask for (kv_copy).
 //
-// kv_fork and kv_compact are one cooperative launch each of up to a CTA an SM, whose
-// three steps are a barrier of the grid apart.  A few KB to some MB: bound by latency
-// (10 to 16 us on the device for 7 to 4700 moves, most of it the launch, two barriers
-// of the grid and the loads between them) and, a call, by the host, which three
-// launches cost 7 us and one 4.
+// kv_fork and kv_compact are one launch each, whose three steps are a barrier of all
+// its CTAs apart: of a cluster for little work, of a cooperative grid of up to a CTA an
+// SM for more.  A few KB to some MB: bound by latency (10 to 17 us on the device for 7
+// to 4700 moves: the launch, two barriers and the loads between them) and, a call, by
+// the host, which three launches cost 7 us and one 4.
 #pragma once
 #include <cooperative_groups.h>
 #include <stdint.h>
@@ -53,6 +53,16 @@ struct ForkArgs {
   uint32_t* err;
   PageWork work;
 };
+
+// All CTAs of the launch, which are one cluster or a cooperative grid.
+constexpr int kPageCluster = 8;
+template <bool kCluster>
+__device__ __forceinline__ void page_sync() {
+  if constexpr (kCluster)
+    cooperative_groups::this_cluster().sync();
+  else
+    cooperative_groups::this_grid().sync();
+}
 
 constexpr int kPageThreads = kBlockThreads;
 constexpr int kPageWarps = kPageThreads / 32;
@@ -251,12 +261,12 @@ __device__ __forceinline__ void fork_finish(const ForkArgs& a) {
   }
 }
 
+template <bool kCluster>
 __global__ void __launch_bounds__(kPageThreads) fork_kernel(const ForkArgs a) {
-  const cooperative_groups::grid_group grid = cooperative_groups::this_grid();
   fork_count(a);
-  grid.sync();
+  page_sync<kCluster>();
   fork_plan(a);
-  grid.sync();
+  page_sync<kCluster>();
   fork_finish(a);
 }
 
@@ -372,12 +382,12 @@ __device__ __forceinline__ void compact_finish(const CompactArgs& a) {
   if (bad != 0 && a.err != nullptr) atomicOr(a.err, SPECDEC_DEV_ERR_BLOCKS);
 }
 
+template <bool kCluster>
 __global__ void __launch_bounds__(kPageThreads) compact_kernel(const CompactArgs a) {
-  const cooperative_groups::grid_group grid = cooperative_groups::this_grid();
   compact_mark(a);
-  grid.sync();
+  page_sync<kCluster>();
   compact_plan(a);
-  grid.sync();
+  page_sync<kCluster>();
   compact_finish(a);
 }
 

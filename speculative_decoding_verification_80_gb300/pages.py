@@ -51,18 +51,24 @@ def _workspace(ws, blocks: int, device, stream, dev: int):
     return ws, _at(ws, words, "workspace", ws.dtype, dev), words * ws.element_size()
 
 
-def _results(out, kind, sizes, shapes, device, dev: int, stream):
-    """The outputs and their addresses: `out`, or parts of one new tensor."""
+def _results(out, kind, sizes, shaped, device, dev: int, stream):
+    """The outputs and their addresses: `out`, or parts of one new tensor, of
+    which some have a shape."""
     if out is not None:
         return out, [_at(t, n, f"out.{what}", I32, dev) for t, n, what in zip(out, sizes, kind._fields)]
-    with _on(stream):
+    if stream is None:
         buf = torch.empty(sum(sizes), dtype=I32, device=device)
+    else:
+        with _on(stream):
+            buf = torch.empty(sum(sizes), dtype=I32, device=device)
     at, addresses = buf.data_ptr(), []
     for n in sizes:
         addresses.append(at)
         at += 4 * n
-    parts = buf.unsafe_split_with_sizes(sizes)
-    return kind._make(p if s is None else p.view(s) for p, s in zip(parts, shapes)), addresses
+    parts = list(buf.unsafe_split_with_sizes(sizes))
+    for i, shape in shaped:
+        parts[i] = parts[i].view(shape)
+    return kind(*parts), addresses
 
 
 def kv_fork(block_table: torch.Tensor, kv_len: torch.Tensor, held: torch.Tensor, parent: torch.Tensor,
@@ -87,7 +93,7 @@ def kv_fork(block_table: torch.Tensor, kv_len: torch.Tensor, held: torch.Tensor,
              _at(keep, B, "keep", I32, dev), _at(shares, N, "shares", I32, dev), _at(free_ring, N, "free_ring", I32, dev),
              _at(ring_state, 2, "ring_state", I32, dev))
     workspace, ws, ws_bytes = _workspace(workspace, N, block_table.device, stream, dev)
-    out, to = _results(out, Fork, (B * width, B, B, N, 2, 2 * B, 1), ((B, width), None, None, None, None, (B, 2), None),
+    out, to = _results(out, Fork, (B * width, B, B, N, 2, 2 * B, 1), ((0, (B, width)), (5, (B, 2))),
                        block_table.device, dev, stream)
     _check(load_library().kv_fork(P, B, block_size, width, N, *fixed, *to, ws, ws_bytes, _word(error_word, dev),
                                   _on_stream(stream, dev)), "kv_fork")
@@ -110,7 +116,7 @@ def kv_compact(block_table: torch.Tensor, held: torch.Tensor, shares: torch.Tens
              _at(free_ring, N, "free_ring", I32, dev), _at(ring_state, 2, "ring_state", I32, dev))
     workspace, ws, ws_bytes = _workspace(workspace, N, block_table.device, stream, dev)
     moves = N // 2
-    out, to = _results(out, Compaction, (B * width, N, N, 2, N, 2 * moves, 1), ((B, width), None, None, None, None, (moves, 2), None),
+    out, to = _results(out, Compaction, (B * width, N, N, 2, N, 2 * moves, 1), ((0, (B, width)), (5, (moves, 2))),
                        block_table.device, dev, stream)
     _check(load_library().kv_compact(B, width, N, *fixed, *to, ws, ws_bytes, _word(error_word, dev), _on_stream(stream, dev)),
            "kv_compact")

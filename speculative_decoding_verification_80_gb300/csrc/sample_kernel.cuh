@@ -17,7 +17,8 @@
 // Groups of 16 bins have their sums in shared memory too, so that a warp finds a
 // border by itself, in three looks of its lanes, without a barrier.  The row is
 // written in a last pass, which marks where ids of the borders' logits are: those
-// past a border in the order of the ids are taken back, and one is the token.
+// past a border in the order of the ids are taken back, and one is the token (fp32
+// tokens mostly come from the list of a bin's ids).
 //
 // A row is one cluster's of 1 to 8 CTAs (the rule is where it is launched); each has
 // a part of the row, a histogram of it, and a share of the bins to add up.  Two CTAs
@@ -28,7 +29,7 @@
 // 256 rows 48 (131 MB, 2.8 TB/s), 832 of 152064 142 (506 MB, 3.6 TB/s).  A row's chain
 // of barriers and looks takes 12 to 14 us of its 34 to 45; the histogram takes 20 (a
 // warp's 32 additions in shared memory some 4 cycles), the pass that writes 11 to 30.
-// Tokens alone of 300 fp32 rows of 50001 take 88 us: a row that top-p alone cuts 72,
+// Tokens alone of 300 fp32 rows of 50001 take 80 us: a row that top-p alone cuts 67,
 // 38 of them for all its weights (some 75 instructions each), and 15 for two lists of
 // a bin's ids, each a pass over the row.  What was no faster: 16384 bins, lists of the
 // bins that have ids, shorter weights for small ones, clusters of two for many rows
@@ -98,11 +99,17 @@ template <>
 struct SampleBinsShared<float> {
   union {
     uint32_t count[8192];
-    float list[8192];  // once the counts are done with: the logits that may be kept
+    // once the counts are done with: the logits that may be kept, or half as many with their ids
+    float list[8192];
+    struct {
+      float list_half[4096];
+      int32_t list_id[4096];
+    };
   };
   uint32_t lo[8192], hi[8192];  // halves of the sums
   unsigned long long near_weight[kNear];
   uint32_t near_key[kNear];
+  int32_t near_id[kNear];
 };
 
 // A bit for each vector of a CTA's part in which a border's logit is: in the bins'
@@ -187,6 +194,7 @@ struct SampleJob {
   float top;        // the largest logit
   WeightScale scale;
   int in_list = -1;             // fp32: logits in this CTA's list, -1: there is none
+  bool with_ids = false;        // fp32: a border's ids are known when its bin is listed
   SampleBin of_k = {-1, 0, 0, 0, 0};  // fp32: top-k's bin and its counts
 
   __device__ __forceinline__ SampleFast<Elt>& of(int cta) const { return *cluster.map_shared_rank(&s, cta); }
@@ -259,6 +267,7 @@ struct SampleJob {
       if (!inside) break;
     }
   }
+  static_assert(kNear <= kSampleThreads, "a thread for each listed id");
   static __device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x); }
   static __device__ __forceinline__ uint32_t bits(__nv_bfloat16 x) { return __bfloat16_as_ushort(x); }
   static __device__ __forceinline__ float logit(uint32_t b) { return plain_logit(__uint_as_float(sizeof(Elt) == 2 ? b << 16 : b)); }
@@ -407,7 +416,10 @@ struct SampleJob {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t mine = at + __popc(m[e] & ((1u << lane) - 1));
-            if (f[e] >= least && mine < kRoom) s.bins.list[mine] = f[e] + 0.f;
+            if (f[e] >= least && mine < kRoom) {
+              s.bins.list[mine] = f[e] + 0.f;
+              if (with_ids && mine < kRoom / 2) s.bins.list_id[mine] = E * (j + i * kSampleThreads) - row.phase + e;
+            }
             at += __popc(m[e]);
           }
         }
@@ -418,8 +430,8 @@ struct SampleJob {
   }
   // fp32: the weights into the bins.  Of ids that cannot be kept none is needed: those
   // in a bin past top-k's, and, where no top-p asks for a share of them, min-p's.  The
-  // others are listed in the counts' place, where there is room for them, and nothing
-  // but the last pass reads the row again.  (Of 50001 ids the weights of 5000 took 35
+  // others are listed in the counts' place, where there is room for them (and for their
+  // ids, for half as many), and nothing but the last pass reads the row again.  (Of 50001 ids the weights of 5000 took 35
   // us a row, as those of all, when each warp gathered its own 32 at a time.)
   __device__ __forceinline__ void add_weights(const SampleAsk& ask) {
     if constexpr (sizeof(Elt) == 4) {
@@ -429,14 +441,18 @@ struct SampleJob {
         add_up(true, false);
         if (find(kByCount, ask.k, &of_k)) {
           // (the border itself is looked for among them: min-p does not shorten the list)
-          least = end_of(of_k.bin);
+          least = fmaxf(end_of(of_k.bin), -3.402823466e38f);  // (-infinity is no id's)
           few = of_k.c0 + of_k.c <= Bins::kBins;
+          with_ids = of_k.c0 + of_k.c <= Bins::kBins / 2;
         } else {
           of_k.bin = -1;
         }
         meet();  // (the counts' readers)
       }
-      if (few) gather(least);
+      if (few)
+        gather(least);
+      else
+        with_ids = true;
       auto one = [&](float x) {
         const int bin = Bins::one(x);
         const unsigned long long w = weight(x);
@@ -504,7 +520,7 @@ struct SampleJob {
     if (threadIdx.x == 0) s.zeroed = true;
     __syncthreads();
   }
-  __device__ __forceinline__ bool decide(const SampleAsk& ask, bool draw, SamplePlace* kept, SamplePlace* drawn);
+  __device__ __forceinline__ bool decide(const SampleAsk& ask, int32_t* token, SamplePlace* kept, SamplePlace* drawn);
 
   // The least key of a logit of `Elt` whose weight is enough, by a warp; `no` has too
   // little and `yes` enough.
@@ -572,7 +588,9 @@ struct SampleJob {
   // The key at which a border lies within its bin; for kByKey the key is the border
   // and all ids from it on are before it.  False: the bin does not say (for all CTAs
   // alike).
-  __device__ __forceinline__ bool resolve(const SampleBin& f, SampleBorder by, unsigned long long target, SamplePlace* p) {
+  // With a `token` (fp32, kBySumPast) it is written where the ids are known, and the
+  // place's key is 0.
+  __device__ __forceinline__ bool resolve(const SampleBin& f, SampleBorder by, unsigned long long target, SamplePlace* p, int32_t* token = nullptr) {
     if constexpr (sizeof(Elt) == 2) {
       if (f.bin == 0 || f.bin >= Bins::kBins - 1 || f.bin == Bins::kHalf - 1 || f.bin == Bins::kHalf) return false;
       p->key = key_of(Bins::value(f.bin));
@@ -584,26 +602,26 @@ struct SampleJob {
       return true;
     } else {
       SampleFast<Elt>& lead = ctas > 1 ? of(0) : s;
-      auto list = [&](float x) {
+      auto list = [&](float x, int id) {
         const uint32_t at = atomicAdd(&lead.listed, 1u);
-        if (at < kNear) lead.bins.near_key[at] = key_of(x);
+        if (at < kNear) lead.bins.near_key[at] = key_of(x), lead.bins.near_id[at] = id;
       };
       if (in_list >= 0) {
         for (int i = threadIdx.x; i < in_list; i += kSampleThreads) {
           const float x = s.bins.list[i];
-          if (Bins::one(x) == f.bin) list(x);
+          if (Bins::one(x) == f.bin) list(x, with_ids ? s.bins.list_id[i] : 0);
         }
       } else if (f.bin == 0 || f.bin == Bins::kBins - 1 || f.bin == Bins::kHalf - 1 || f.bin == Bins::kHalf) {
-        each_id<1>([&](float x, int) {
-          if (x != -INFINITY && Bins::one(x) == f.bin) list(x);
+        each_id<1>([&](float x, int id) {
+          if (x != -INFINITY && Bins::one(x) == f.bin) list(x, id);
         });
       } else {  // a bin of one beginning of 16 bits
         const uint32_t first = __float_as_uint(Bins::value(f.bin)) & 0xFFFF0000u;
-        each<8>([&](const uint4& q, int) {
+        each<8>([&](const uint4& q, int j) {
           const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if ((w[i] ^ first) < 0x10000u) list(__uint_as_float(w[i]));
+            if ((w[i] ^ first) < 0x10000u) list(__uint_as_float(w[i]), E * j - row.phase + i);
         });
       }
       meet();
@@ -645,13 +663,19 @@ struct SampleJob {
           s.answer.all = s.answer.ids = 0;
           s.answer.sum += f.w0;
         }
+        if (token != nullptr && with_ids && n <= kNear && threadIdx.x < n && s.bins.near_key[threadIdx.x] == s.answer.key) {
+          const int id = s.bins.near_id[threadIdx.x];
+          uint32_t before = 0;
+          for (uint32_t o = 0; o < n; ++o) before += s.bins.near_key[o] == s.answer.key && s.bins.near_id[o] < id ? 1 : 0;
+          if (before + 1 == s.answer.ids) *token = id;
+        }
         __syncthreads();
         if (ctas > 1 && threadIdx.x >= 32 && threadIdx.x < 32 * ctas && threadIdx.x % 32 == 0) of(threadIdx.x / 32).answer = s.answer;
         if (threadIdx.x == 0) s.listed = 0;
       }
       meet();
       const SampleAnswer a = s.answer;
-      p->key = a.key;
+      p->key = token != nullptr && with_ids ? 0 : a.key;
       p->ids = a.ids;
       p->all = a.all;
       p->sum = a.sum;
@@ -877,10 +901,10 @@ struct SampleJob {
   }
 };
 
-// What is kept and which logit is drawn; false: the bins do not say.  bf16: by any
+// What is kept and which logit (fp32: or token) is drawn; false: the bins do not say.  bf16: by any
 // warp, fp32: by all.
 template <typename Elt>
-__device__ __forceinline__ bool SampleJob<Elt>::decide(const SampleAsk& ask, bool draw, SamplePlace* kept, SamplePlace* drawn) {
+__device__ __forceinline__ bool SampleJob<Elt>::decide(const SampleAsk& ask, int32_t* token, SamplePlace* kept, SamplePlace* drawn) {
   SampleBin f;
   unsigned long long weights = s.group_sum[kGroups];
   bool cut = false;  // by top-k
@@ -917,11 +941,11 @@ __device__ __forceinline__ bool SampleJob<Elt>::decide(const SampleAsk& ask, boo
     kept->ids = kept->all;
     weights = sizeof(Elt) == 2 ? kept->sum + f.w : kept->sum;
   }
-  if (draw) {
+  if (token != nullptr) {
     unsigned long long target = static_cast<unsigned long long>(static_cast<double>(ask.u) * static_cast<double>(weights));
     if (target >= weights) target = weights - 1;
     find(kBySumPast, target, &f);
-    if (!resolve(f, kBySumPast, target, drawn)) return false;
+    if (!resolve(f, kBySumPast, target, drawn, token)) return false;
   }
   return true;
 }
@@ -1078,7 +1102,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
           uint32_t c[2];
           unsigned long long w[2];
           const bool more = again == 0 && job.zeros_matter(c, w);
-          const bool sure = !more && job.decide(ask, token != nullptr, &kept, &drawn);
+          const bool sure = !more && job.decide(ask, token, &kept, &drawn);
           if (tid == 0) s.kept = kept, s.drawn = drawn, s.simple = sure, s.more = more;
         }
         __syncthreads();
@@ -1087,7 +1111,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
       }
       if (simple) kept = s.kept, drawn = s.drawn, simple = s.simple;
     } else {
-      simple = job.decide(ask, token != nullptr, &kept, &drawn);
+      simple = job.decide(ask, token, &kept, &drawn);
     }
   }
   if (!simple) {
@@ -1101,9 +1125,10 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
   }
   if (first && bad != 0 && a.err != nullptr) atomicOr(a.err, bad);
   const bool part = out != nullptr && kept.ids < kept.all;
+  // (the token, where it is not known yet, and ids of the last logit that is kept)
   const uint32_t keys[2] = {token != nullptr ? drawn.key : 0, part ? kept.key : 0};
   const uint32_t ids[2] = {token != nullptr ? drawn.ids : 0, part ? kept.ids : 0};
-  const bool some = token != nullptr || part;
+  const bool some = keys[0] != 0 || part;
   if (some) job.clear_marks();
   if (some || out != nullptr) job.write(out, kept.key, keys);
   if (some) job.settle(out, token, keys, ids);

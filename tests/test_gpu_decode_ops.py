@@ -194,6 +194,36 @@ def test_sample_row_in_parts(B, dtype):
     assert torch.equal(a, b) and torch.equal(a, c)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [200, 70001])
+def test_sample_border_among_the_lowest(V, dtype):
+    """Top-k's border at logits of -4096 and below, beside masked ones."""
+    rng = np.random.default_rng(V)
+    x = np.full((2, 1, V), -INF)
+    for b in range(2):
+        at = rng.permutation(V)[:45]
+        x[b, 0, at[:40]] = -5000.0 - 64 * rng.integers(0, 9, 40)
+        x[b, 0, at[40:]] = rng.normal(0, 1, 5)
+    x = dev(x.astype(np.float32), dtype)
+    for k in (3, 20, 45, 46, 100):
+        for T in (1.0, 1000.0):
+            _sample(x, T=np.full(2, T), k=np.full(2, k), u=rng.random((2, 1)).astype(np.float32))
+            _sample(x, T=np.full(2, T), k=np.full(2, k), p=np.full(2, 0.9), u=rng.random((2, 1)).astype(np.float32))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("k", [0, 700, 4096, 4097, 9000])
+def test_sample_draws_among_equal_ids(k, dtype):
+    """Tokens of rows with a few hundred values, whose ids' order decides, for lists with and without ids."""
+    rng = np.random.default_rng(k)
+    B, V = 12, 20001
+    x = dev((rng.integers(0, 400, (B, 1, V)) / 64).astype(np.float32), dtype)
+    kw = dict(T=0.5 + rng.random(B), k=np.full(B, k), u=rng.random((B, 1)).astype(np.float32))
+    _sample(x, rows=False, **kw)
+    _sample(x, **kw)
+    _sample(x, p=np.full(B, 0.7), **kw)
+
+
 @pytest.mark.parametrize("B", [1, 40])
 def test_sample_fp32_parts_with_and_without_room(B):
     """More ids that min-p keeps than some parts of a row can list, none in the others."""

@@ -224,6 +224,21 @@ def test_sample_draws_among_equal_ids(k, dtype):
     _sample(x, p=np.full(B, 0.7), **kw)
 
 
+@pytest.mark.parametrize("B,V", [(1, 262144), (3, 128256), (40, 128256), (20, 200003)])
+def test_sample_fp32_borders_in_full_bins(B, V):
+    """Flat rows away from 0, some thousand ids in each bin where borders lie."""
+    rng = np.random.default_rng(V + B)
+    x = dev(rng.normal(6, 2.5, (B, 1, V)).astype(np.float32), torch.float32)
+    u = rng.random((B, 1)).astype(np.float32)
+    T = 1.5 + rng.random(B)
+    _sample(x, T=T, u=u)
+    _sample(x, T=T, p=np.full(B, 0.8), u=u)
+    _sample(x, T=T, k=np.full(B, V // 3), m=np.full(B, 0.02), u=u)
+    _sample(x, T=T, k=np.full(B, 6000), p=np.full(B, 0.7), m=np.full(B, 0.05), u=u)
+    _sample(-x, T=T, p=np.full(B, 0.6), m=np.full(B, 0.1), u=u)
+    _sample(torch.round(8 * x) / 8, T=T, p=np.full(B, 0.6), u=u)  # (and many of each value)
+
+
 @pytest.mark.parametrize("B", [1, 40])
 def test_sample_fp32_parts_with_and_without_room(B):
     """More ids that min-p keeps than some parts of a row can list, none in the others."""

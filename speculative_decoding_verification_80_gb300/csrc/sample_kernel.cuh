@@ -26,7 +26,7 @@
 // instead of 48 on the 256 rows below), four had no room for the bins.
 //
 // Measured on one GB300, cut rows written back: one row of 128256 bf16 logits 18.5 us,
-// 256 rows 48 (131 MB, 2.8 TB/s), 832 of 152064 142 (506 MB, 3.6 TB/s).  A row's chain
+// 256 rows 48 (131 MB, 2.8 TB/s), 832 of 152064 141 (506 MB, 3.6 TB/s).  A row's chain
 // of barriers and looks takes 12 to 14 us of its 34 to 45; the histogram takes 20 (a
 // warp's 32 additions in shared memory some 4 cycles), the pass that writes 11 to 30.
 // Tokens alone of 300 fp32 rows of 50001 take 80 us: a row that top-p alone cuts 67,
@@ -1096,18 +1096,21 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
       // logits of -4096 and below are not counted: they have no weight and are not kept, or the row is another's
       const uint32_t ids = s.group_count[kSampleGroups];
       if ((ask.k < a.V && static_cast<uint32_t>(ask.k) > ids) || !((job.top + 4096.f) * ask.scale.hi > 49.f)) simple = !job.any_far();
-      // every warp could, but one is enough
+      // every warp could, but one is enough, while another looks at the bins of zero
       for (int again = 0; simple; ++again) {
         if (tid < 32) {
+          const bool sure = job.decide(ask, token, &kept, &drawn);
+          if (tid == 0) s.kept = kept, s.drawn = drawn, s.simple = sure;
+        } else if (tid < 64) {
           uint32_t c[2];
           unsigned long long w[2];
           const bool more = again == 0 && job.zeros_matter(c, w);
-          const bool sure = !more && job.decide(ask, token, &kept, &drawn);
-          if (tid == 0) s.kept = kept, s.drawn = drawn, s.simple = sure, s.more = more;
+          if (tid == 32) s.more = more;
         }
         __syncthreads();
         if (!s.more) break;
         job.add_zeros();
+        if (tid < 32) kept = {kKeyFloor + 1, 0, 0, 0};
       }
       if (simple) kept = s.kept, drawn = s.drawn, simple = s.simple;
     } else {

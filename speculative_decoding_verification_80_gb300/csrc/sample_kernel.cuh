@@ -119,7 +119,7 @@ static_assert(sizeof(uint32_t) * kMarkWords <= sizeof(SampleBinsShared<__nv_bflo
 
 struct SampleAnswer {
   uint32_t key, ids, all, bad;
-  unsigned long long sum, count;
+  unsigned long long sum;
 };
 
 template <typename Elt>
@@ -627,7 +627,7 @@ struct SampleJob {
       meet();
       if (rank == 0) {
         const uint32_t n = s.listed;
-        if (threadIdx.x == 0) s.answer.bad = n > kNear ? 1 : 0, s.answer.sum = 0, s.answer.count = 0;
+        if (threadIdx.x == 0) s.answer.bad = n > kNear ? 1 : 0, s.answer.sum = 0;
         if (n <= kNear) {
           for (uint32_t i = threadIdx.x; i < n; i += kSampleThreads) s.bins.near_weight[i] = weight(of_key(s.bins.near_key[i]));
           __syncthreads();
@@ -635,7 +635,7 @@ struct SampleJob {
             const uint32_t key = s.bins.near_key[i];
             const unsigned long long w = s.bins.near_weight[i];
             if (by == kByKey) {
-              if (key >= static_cast<uint32_t>(target)) atomicAdd(&s.answer.count, 1ull), atomicAdd(&s.answer.sum, w);
+              if (key >= static_cast<uint32_t>(target)) atomicAdd(&s.answer.sum, w);
               continue;
             }
             uint32_t c0 = 0, same = 0;

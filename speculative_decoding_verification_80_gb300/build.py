@@ -43,17 +43,11 @@ def _code_only(text: str) -> str:
                   lambda m: m.group(0) if m.group(0).startswith('"') else " ", text, flags=re.S)
 
 
-def source_digest(skip=()) -> str:
-    """Hash of the code the library is built from (kernels, headers, flags),
-    comments aside, so an edit to comments keeps the recorded measurements of
-    the same code valid.  `skip` leaves out source files by name (the verify
-    kernel's digest leaves out the files of the MTP kernel, of the sharded
-    verify and of the operators around the step, which it does not include)."""
+def _digest(files) -> str:
+    """Hash of the code of source files (comments aside, so an edit to comments
+    keeps the recorded measurements of the same code valid) and of the flags."""
     h = hashlib.sha256()
-    files = sorted(glob.glob(os.path.join(CSRC, "*"))) + sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
     for f in files:
-        if os.path.basename(f) in skip:
-            continue
         h.update(os.path.basename(f).encode())
         with open(f, encoding="utf-8") as fh:
             h.update(_code_only(fh.read()).encode())
@@ -61,13 +55,33 @@ def source_digest(skip=()) -> str:
     return h.hexdigest()[:16]
 
 
+def _all_files():
+    return sorted(glob.glob(os.path.join(CSRC, "*"))) + sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def source_digest() -> str:
+    """Digest of the code the library is built from."""
+    return _digest(_all_files())
+
+
+def verify_files():
+    """The sources the verify kernel is built from: api.cu and what it includes,
+    at any depth, but for the MTP kernel."""
+    there = {os.path.basename(f): f for f in _all_files()}
+    found, ask = set(), ["api.cu"]
+    while ask:
+        name = ask.pop()
+        if name in found or name == "mtp_kernel.cuh":
+            continue
+        found.add(name)
+        with open(there[name], encoding="utf-8") as f:
+            ask += [x for x in re.findall(r'^\s*#\s*include\s+"([^"]+)"', f.read(), flags=re.M) if x in there]
+    return [f for name, f in there.items() if name in found]
+
+
 def verify_digest() -> str:
     """Digest of the sources the verify kernel is built from."""
-    return source_digest(skip=("mtp_kernel.cuh", "shard_kernels.cuh", "shard_api.cu", "specdec_shard.h", "step_api.cu",
-                               "attention_cut.cuh", "attention_kernel.cuh", "kv_kernels.cuh", "logits_kernel.cuh",
-                               "tcgen05.cuh", "waits.cuh", "specdec_step.h", "host_checks.cuh", "sample_api.cu",
-                               "sample_kernel.cuh", "sample_weight.cuh", "rotary_kernel.cuh", "pages_api.cu",
-                               "page_kernels.cuh", "block_prefix.cuh"))
+    return _digest(verify_files())
 
 
 def _up_to_date() -> bool:

@@ -34,7 +34,7 @@ def test_verify_digest_has_what_the_verify_kernel_includes(tmp_path, monkeypatch
         with open(path) as f:
             text = f.read()
         with open(path, "w") as f:
-            f.write(text + "\n// a comment\n")
+            f.write(re.sub(r"// ", "// and ", text))
         assert build.verify_digest() == before
         with open(path, "w") as f:
             f.write(text + "\nint x;\n")

@@ -286,7 +286,8 @@ specdec_status_t spec_rotary(const void* q, const void* k, specdec_dtype_t dtype
  *
  * The workspace of kv_fork and kv_compact: specdec_page_workspace_bytes(num_blocks)
  * bytes, zero-filled once before its first use; every call leaves it ready for the
- * next.  One workspace serves one call in flight at a time.
+ * next, which may be of another pool: one workspace, given whole, serves all numbers
+ * of blocks that it has room for, one call in flight at a time.
  */
 size_t specdec_page_workspace_bytes(int32_t num_blocks);
 

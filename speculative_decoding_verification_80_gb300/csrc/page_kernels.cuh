@@ -12,24 +12,9 @@
 #include <stdint.h>
 
 #include "block_prefix.cuh"
+#include "page_work.cuh"
 
 namespace specdec {
-
-// The workspace: what is zero between two calls first (counts of a block's names
-// in the old and new tables, requests that write it, the last of those; a bit a
-// free block), then scratch (a bit a block that goes back, a block's place among
-// the moves, a request's number among those that copy).
-struct PageWork {
-  uint32_t* olds;
-  uint32_t* news;
-  uint32_t* writers;
-  uint32_t* last;       // request + 1
-  uint32_t* marks;
-  uint32_t* gone;
-  int32_t* rank;
-  int32_t* number;
-  int32_t* ring;        // head, count as they were, clamped
-};
 
 // ------------------------------------------------------------------ kv_fork
 struct ForkArgs {

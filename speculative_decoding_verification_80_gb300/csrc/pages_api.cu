@@ -13,24 +13,6 @@
 namespace specdec {
 namespace {
 
-size_t page_words(int64_t N) { return static_cast<size_t>(5 * N + 2 * ((N + 31) / 32) + SPECDEC_MAX_BATCH + 2); }
-
-PageWork page_work(void* workspace, int64_t N) {
-  uint32_t* at = static_cast<uint32_t*>(workspace);
-  const int64_t words = (N + 31) / 32;
-  PageWork w;
-  w.olds = at;
-  w.news = w.olds + N;
-  w.writers = w.news + N;
-  w.last = w.writers + N;
-  w.marks = w.last + N;
-  w.gone = w.marks + words;
-  w.rank = reinterpret_cast<int32_t*>(w.gone + words);
-  w.number = w.rank + N;
-  w.ring = w.number + SPECDEC_MAX_BATCH;
-  return w;
-}
-
 specdec_status_t check_workspace(const void* workspace, size_t bytes, int64_t N) {
   return workspace == nullptr || !aligned(workspace, 16) || bytes < page_words(N) * 4 ? SPECDEC_ERR_WORKSPACE : SPECDEC_OK;
 }
@@ -124,7 +106,7 @@ extern "C" specdec_status_t kv_fork(int32_t P, int32_t B, int32_t block_size, in
   a.copies = copies;
   a.count = count;
   a.err = error_word;
-  a.work = page_work(workspace, num_blocks);
+  a.work = page_work(workspace, workspace_bytes, num_blocks);
   // a thread for each entry of the tables or block
   const int64_t entries = (static_cast<int64_t>(P) + B) * max_blocks;
   return launch_page(fork_kernel<true>, fork_kernel<false>, a, entries > num_blocks ? entries : num_blocks, static_cast<cudaStream_t>(stream));
@@ -162,7 +144,7 @@ extern "C" specdec_status_t kv_compact(int32_t B, int32_t max_blocks, int32_t nu
   a.copies = copies;
   a.count = count;
   a.err = error_word;
-  a.work = page_work(workspace, num_blocks);
+  a.work = page_work(workspace, workspace_bytes, num_blocks);
   const int64_t entries = static_cast<int64_t>(B) * max_blocks;
   return launch_page(compact_kernel<true>, compact_kernel<false>, a, entries > num_blocks ? entries : num_blocks, static_cast<cudaStream_t>(stream));
 }

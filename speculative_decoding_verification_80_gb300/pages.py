@@ -39,7 +39,8 @@ def page_workspace_bytes(num_blocks: int) -> int:
 
 
 def new_page_workspace(num_blocks: int, device=None, stream=None) -> torch.Tensor:
-    """A zero-filled workspace (uint8 tensor) for kv_fork and kv_compact."""
+    """A zero-filled workspace (uint8 tensor) for kv_fork and kv_compact, of pools
+    of up to num_blocks blocks."""
     with _on(stream):
         return torch.zeros(page_workspace_bytes(num_blocks), dtype=torch.uint8, device=device or "cuda")
 

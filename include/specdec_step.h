@@ -316,8 +316,8 @@ size_t specdec_page_workspace_bytes(int32_t num_blocks);
  *   shares_out [num_blocks], ring_state_out [2]; free_ring's tail in place;
  *   copies [B, 2] and count [1]: for kv_copy, from and to; those past count have no
  *                 meaning.
- * shares_out and ring_state_out may be the inputs; the tables, kv_len and held may
- * not.  Out of range: a parent is none, a length is clamped to what is held, held to
+ * shares_out and ring_state_out may be the inputs; no other output lies on an input
+ * or on another output (refused).  Out of range: a parent is none, a length is clamped to what is held, held to
  * the table's width, a block id (the ring's too) is left as it is; each sets
  * SPECDEC_DEV_ERR_BLOCKS.
  */

@@ -25,6 +25,31 @@ inline bool on_device(const void* p) {
   return at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged;
 }
 
+// Memory that a call reads or writes.  An output may be one input where `same` names it.
+struct Span {
+  const void* at;
+  size_t bytes;
+  const void* same = nullptr;
+};
+
+inline bool overlap(const Span& x, const Span& y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.at), b = reinterpret_cast<uintptr_t>(y.at);
+  if (x.at == nullptr || y.at == nullptr || x.bytes == 0 || y.bytes == 0) return false;
+  return a <= b ? b - a < x.bytes : a - b < y.bytes;
+}
+
+// Whether an output lies on another output, or on an input that it may not be.
+template <int I, int O>
+bool outputs_collide(const Span (&in)[I], const Span (&out)[O]) {
+  for (int o = 0; o < O; ++o) {
+    for (int i = 0; i < I; ++i)
+      if (overlap(out[o], in[i]) && !(out[o].at == in[i].at && out[o].same == in[i].at && out[o].bytes == in[i].bytes)) return true;
+    for (int i = 0; i < o; ++i)
+      if (overlap(out[o], out[i])) return true;
+  }
+  return false;
+}
+
 // SMs of the current device, which is asked once.
 inline cudaError_t device_sms(int* dev, int* sms) {
   static int known[64] = {0};

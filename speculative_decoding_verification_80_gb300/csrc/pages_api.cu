@@ -82,6 +82,11 @@ extern "C" specdec_status_t kv_fork(int32_t P, int32_t B, int32_t block_size, in
     return SPECDEC_ERR_INVALID_ARG;
   const specdec_status_t ws = check_workspace(workspace, workspace_bytes, num_blocks);
   if (ws != SPECDEC_OK) return ws;
+  const size_t p4 = 4 * static_cast<size_t>(P), b4 = 4 * static_cast<size_t>(B), n4 = 4 * static_cast<size_t>(num_blocks);
+  const Span in[] = {{block_table, p4 * max_blocks}, {kv_len, p4}, {accepted_len, p4}, {held, p4}, {parent, b4}, {keep, b4}, {shares, n4}, {ring_state, 8}};
+  const Span out[] = {{table_out, b4 * max_blocks}, {kv_len_out, b4}, {held_out, b4}, {shares_out, n4, shares}, {ring_state_out, 8, ring_state},
+                      {free_ring, n4}, {copies, 2 * b4}, {count, 4}, {workspace, workspace_bytes}, {error_word, 4}};
+  if (outputs_collide(in, out)) return SPECDEC_ERR_INVALID_ARG;
   ForkArgs a;
   memset(&a, 0, sizeof a);
   a.P = P;

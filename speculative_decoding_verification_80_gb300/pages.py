@@ -81,9 +81,9 @@ def kv_fork(block_table: torch.Tensor, kv_len: torch.Tensor, held: torch.Tensor,
     (see include/specdec_step.h): blocks are shared, part-filled ones that others
     hold are to be copied (kv_copy with the result's copies and count), and those
     without a holder go back to free_ring, in place.  `out` reuses another fork's
-    tensors (its shares and ring_state may be the inputs themselves).  Without a
-    workspace the call makes one: a loop keeps one of its own
-    (new_page_workspace).  Returns a Fork."""
+    tensors (its shares and ring_state may be the inputs themselves; no other
+    output lies on an input).  Without a workspace the call makes one: a loop
+    keeps one of its own (new_page_workspace).  Returns a Fork."""
     if block_table.dim() != 2:
         raise ValueError("block_table must be [P, max_blocks]")
     P, width = block_table.shape

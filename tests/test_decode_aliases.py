@@ -1,0 +1,54 @@
+"""Outputs of the cache's forks and moves, and of sampling, that lie on inputs or on
+one another: refused on the host (CPU only; every call here is refused, so that none
+launches a kernel)."""
+import ctypes
+
+import pytest
+
+import speculative_decoding_verification_80_gb300 as sd
+
+P = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from speculative_decoding_verification_80_gb300 import build
+
+    build.build()
+    return sd.load_library()
+
+
+FORK = ["block_table", "kv_len", "accepted_len", "held", "parent", "keep", "shares", "free_ring", "ring_state", "table_out", "kv_len_out",
+        "held_out", "shares_out", "ring_state_out", "copies", "count", "workspace", "error_word"]
+
+
+def _fork(lib, **at):
+    """kv_fork of 4 old and 6 new requests, 8 blocks a row, 100 blocks; arrays 64 KB apart but for those in `at`."""
+    p = {name: 0x100000 + 0x10000 * i for i, name in enumerate(FORK[:-2])}
+    p["workspace"], p["error_word"] = 0x10000000, 0x20000000
+    p.update(at)
+    a = [P(p[name]) for name in FORK]
+    return lib.kv_fork(4, 6, 16, 8, 100, *a[:-1], sd.page_workspace_bytes(100), a[-1], None)
+
+
+AT = {name: 0x100000 + 0x10000 * i for i, name in enumerate(FORK[:-2])}
+
+
+@pytest.mark.parametrize("out", ["table_out", "kv_len_out", "held_out", "copies", "count", "free_ring", "workspace", "error_word"])
+@pytest.mark.parametrize("on", ["block_table", "kv_len", "accepted_len", "held", "parent", "keep", "shares", "ring_state"])
+def test_fork_refuses_outputs_on_inputs(lib, out, on):
+    assert _fork(lib, **{out: AT[on]}) == 1
+
+
+@pytest.mark.parametrize("out,on,by", [("shares_out", "shares", 4), ("shares_out", "shares", -4), ("ring_state_out", "ring_state", 4),
+                                       ("shares_out", "ring_state", 0), ("ring_state_out", "shares", 0), ("kv_len_out", "parent", 20),
+                                       ("kv_len_out", "parent", -20), ("held_out", "block_table", 124), ("table_out", "held", -188)])
+def test_fork_refuses_parts_on_parts(lib, out, on, by):
+    assert _fork(lib, **{out: AT[on] + by}) == 1
+
+
+@pytest.mark.parametrize("a,b", [("table_out", "kv_len_out"), ("kv_len_out", "held_out"), ("copies", "table_out"), ("count", "copies"),
+                                 ("shares_out", "free_ring"), ("ring_state_out", "count"), ("workspace", "free_ring"),
+                                 ("workspace", "shares_out")])
+def test_fork_refuses_outputs_on_one_another(lib, a, b):
+    assert _fork(lib, **{a: AT[b]}) == 1

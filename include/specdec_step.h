@@ -334,7 +334,8 @@ specdec_status_t kv_fork(int32_t P, int32_t B, int32_t block_size, int32_t max_b
  * Blocks in use are those that the ring does not list; with n of them, the i-th in
  * use from id n on, in order, moves to the i-th free one before n.  The ring then
  * lists n .. num_blocks - 1 from its start.
- * Outputs (device int32), each may be its input:
+ * Outputs (device int32); the first four may be the inputs of their name, and else no
+ * output lies on an input or on another output (refused):
  *   table_out [B, max_blocks] (-1 past held), shares_out [num_blocks],
  *   ring_out [num_blocks] (what is behind its free ids is left), ring_state_out [2];
  *   renamed [num_blocks]: a block's new id, -1 for a free one, for other holders;

@@ -131,6 +131,11 @@ extern "C" specdec_status_t kv_compact(int32_t B, int32_t max_blocks, int32_t nu
   if (B > 0 && (block_table == nullptr || held == nullptr || table_out == nullptr)) return SPECDEC_ERR_INVALID_ARG;
   const specdec_status_t ws = check_workspace(workspace, workspace_bytes, num_blocks);
   if (ws != SPECDEC_OK) return ws;
+  const size_t b4 = 4 * static_cast<size_t>(B), n4 = 4 * static_cast<size_t>(num_blocks);
+  const Span in[] = {{block_table, b4 * max_blocks}, {held, b4}, {shares, n4}, {free_ring, n4}, {ring_state, 8}};
+  const Span out[] = {{table_out, b4 * max_blocks, block_table}, {shares_out, n4, shares}, {ring_out, n4, free_ring}, {ring_state_out, 8, ring_state},
+                      {renamed, n4}, {copies, 8 * static_cast<size_t>(num_blocks / 2)}, {count, 4}, {workspace, workspace_bytes}, {error_word, 4}};
+  if (outputs_collide(in, out)) return SPECDEC_ERR_INVALID_ARG;
   CompactArgs a;
   memset(&a, 0, sizeof a);
   a.B = B;

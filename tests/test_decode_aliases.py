@@ -52,3 +52,31 @@ def test_fork_refuses_parts_on_parts(lib, out, on, by):
                                  ("workspace", "shares_out")])
 def test_fork_refuses_outputs_on_one_another(lib, a, b):
     assert _fork(lib, **{a: AT[b]}) == 1
+
+
+COMPACT = ["block_table", "held", "shares", "free_ring", "ring_state", "table_out", "shares_out", "ring_out", "ring_state_out", "renamed",
+           "copies", "count", "workspace", "error_word"]
+MOVED = {name: 0x100000 + 0x10000 * i for i, name in enumerate(COMPACT[:-2])}
+
+
+def _compact(lib, **at):
+    """kv_compact of 4 requests, 8 blocks a row, 100 blocks."""
+    p = {**MOVED, "workspace": 0x10000000, "error_word": 0x20000000, **at}
+    a = [P(p[name]) for name in COMPACT]
+    return lib.kv_compact(4, 8, 100, *a[:-1], sd.page_workspace_bytes(100), a[-1], None)
+
+
+@pytest.mark.parametrize("out,on,by", [("table_out", "block_table", 4), ("table_out", "block_table", -124), ("shares_out", "shares", 396),
+                                       ("ring_out", "free_ring", -4), ("ring_state_out", "ring_state", 4), ("shares_out", "free_ring", 0),
+                                       ("ring_out", "shares", 0), ("table_out", "held", 0), ("renamed", "shares", 0), ("renamed", "block_table", 0),
+                                       ("copies", "free_ring", 0), ("count", "ring_state", 0), ("workspace", "shares", 0),
+                                       ("error_word", "held", 12)])
+def test_compact_refuses_outputs_on_other_inputs(lib, out, on, by):
+    assert _compact(lib, **{out: MOVED[on] + by}) == 1
+
+
+@pytest.mark.parametrize("a,b", [("table_out", "renamed"), ("shares_out", "ring_out"), ("copies", "renamed"), ("count", "copies"),
+                                 ("ring_state_out", "count"), ("renamed", "workspace")])
+def test_compact_refuses_outputs_on_one_another(lib, a, b):
+    at = {**MOVED, "workspace": 0x10000000}[b]
+    assert _compact(lib, **{a: at}) == 1

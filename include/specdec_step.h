@@ -231,6 +231,8 @@ specdec_status_t spec_process_logits(const void* logits, void* out, specdec_dtyp
  *   top_p, min_p  [B] float or NULL (1 and above, 0: keep all).
  *   uniform       [B, n_max+1] float in [0, 1), and
  *   tokens        [B, n_max+1] int32: a token drawn of each row; both or neither.
+ * But for out in logits' place, no output lies on an input or on another output
+ * (refused).
  * Per row, with weights w = exp((logit - largest) / temperature) and the ids in
  * order of their logits, the largest first and equal ones by id: kept are the
  * first top_k; of those the shortest beginning whose weights sum to at least

@@ -110,6 +110,10 @@ extern "C" specdec_status_t spec_sample(const void* logits, void* out, specdec_d
     return SPECDEC_ERR_INVALID_ARG;
   const uintptr_t elt = dtype == SPECDEC_F32 ? 4 : 2;
   if (!aligned(logits, elt) || !aligned(out, elt)) return SPECDEC_ERR_INVALID_ARG;
+  const size_t b4 = 4 * static_cast<size_t>(B), r4 = b4 * (static_cast<size_t>(n_max) + 1), bytes = r4 / 4 * V * elt;
+  const Span in[] = {{logits, bytes}, {draft_len, b4}, {temperature, b4}, {top_k, b4}, {top_p, b4}, {min_p, b4}, {uniform, r4}};
+  const Span outs[] = {{out, bytes, logits}, {tokens, r4}, {error_word, 4}};
+  if (outputs_collide(in, outs)) return SPECDEC_ERR_INVALID_ARG;
   SampleArgs a;
   memset(&a, 0, sizeof a);
   a.logits = logits;

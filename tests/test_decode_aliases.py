@@ -80,3 +80,25 @@ def test_compact_refuses_outputs_on_other_inputs(lib, out, on, by):
 def test_compact_refuses_outputs_on_one_another(lib, a, b):
     at = {**MOVED, "workspace": 0x10000000}[b]
     assert _compact(lib, **{a: at}) == 1
+
+
+SAMPLE = ["logits", "out", "draft_len", "temperature", "top_k", "top_p", "min_p", "uniform", "tokens", "error_word"]
+ROWS = {name: 0x1000000 * (i + 1) for i, name in enumerate(SAMPLE)}
+
+
+def _sample(lib, dtype=1, **at):
+    """spec_sample of 3 requests of 2 rows of 1000 logits."""
+    a = [P({**ROWS, **at}[name]) for name in SAMPLE]
+    return lib.spec_sample(*a[:2], dtype, 3, 1, 1000, *a[2:], None)
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("by", [4, -4, 2000, -2000, 11996, -11996])
+def test_sample_refuses_rows_that_overlap(lib, by, dtype):
+    assert _sample(lib, dtype, out=ROWS["logits"] + by) == 1
+
+
+@pytest.mark.parametrize("out,on,by", [("tokens", "logits", 11996), ("tokens", "out", 0), ("tokens", "uniform", 0), ("tokens", "top_k", -20),
+                                       ("out", "uniform", -11996), ("error_word", "tokens", 20), ("error_word", "temperature", 8)])
+def test_sample_refuses_other_overlaps(lib, out, on, by):
+    assert _sample(lib, **{out: ROWS[on] + by}) == 1

@@ -287,25 +287,30 @@ struct Sampler {
   }
 };
 
-// The row with -infinity for the ids that are not kept: keys above `key`, and ids
-// up to `last` of those that have it.
+// The row with -infinity for the ids that are not kept: keys above `key`, and ids up
+// to `last` of those that have it, keep their bits (-0 is 0 in the order alone).
 template <typename Elt>
 __device__ __forceinline__ void write_cut_row(const SampleRow<Elt>& row, Elt* out, uint32_t key, int last, bool infinite) {
   constexpr int E = SampleRow<Elt>::E;
   const Elt none = static_cast<Elt>(-INFINITY);
   const bool same = (reinterpret_cast<uintptr_t>(out) & 15) == row.phase * sizeof(Elt);
   for (int j = threadIdx.x; j < row.vecs; j += kSampleThreads) {
-    float x[E];
-    row.load(j, x);
     const int first = E * j - row.phase;
+    const bool whole = first >= 0 && first + E <= row.V;
     __align__(16) Elt y[E];
+    if (whole) {
+      *reinterpret_cast<uint4*>(y) = reinterpret_cast<const uint4*>(row.p)[j];
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = first + e >= 0 && first + e < row.V ? row.p[static_cast<long long>(E) * j + e] : none;
+    }
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const float r = infinite ? (x[e] == INFINITY ? 0.f : -INFINITY) : x[e];
+      const float x = plain_logit(static_cast<float>(y[e])), r = infinite ? (x == INFINITY ? 0.f : -INFINITY) : x;
       const uint32_t k = key_of(r);
-      y[e] = r != -INFINITY && (k > key || (k == key && first + e <= last)) ? static_cast<Elt>(x[e]) : none;
+      if (!(r != -INFINITY && (k > key || (k == key && first + e <= last)))) y[e] = none;
     }
-    if (same && first >= 0 && first + E <= row.V) {
+    if (same && whole) {
       *reinterpret_cast<uint4*>(out + first) = *reinterpret_cast<const uint4*>(y);
     } else {
 #pragma unroll

@@ -42,3 +42,27 @@ def test_one_workspace_for_pools_of_several_sizes(sizes, order):
             ops._consistent(want, None, 16)
         else:
             assert not ops._check_compact(c, ws=ws)["bad"]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [999, 5003, 70001])
+def test_kept_logits_keep_their_bits(V, dtype):
+    """-0 stays -0, whichever way a row goes: zeros that fill a bin, beside NaN, infinities and finite logits."""
+    rng = np.random.default_rng(V)
+    zeros = np.where(rng.random(V) < 0.5, 0.0, -0.0)
+    high = zeros.copy()
+    high[rng.integers(0, V, 40)] = 5000.0 + 32 * rng.integers(0, 9, 40)
+    nan = np.where(rng.random(V) < 0.1, np.nan, zeros)
+    some = np.where(rng.random(V) < 0.2, zeros, rng.normal(0, 1, V))
+    tiny = np.where(rng.random(V) < 0.5, zeros, rng.normal(0, 1e-8, V))
+    none = np.where(rng.random(V) < 0.5, zeros, -np.inf)
+    word = torch.int16 if dtype is torch.bfloat16 else torch.int32
+    for name, row in dict(zeros=zeros, high=high, nan=nan, some=some, tiny=tiny, none=none).items():
+        x = ops.dev(np.tile(row, (4, 1)).astype(np.float32), dtype).view(4, 1, V)
+        kw = dict(T=[1.0, 5000.0, 1.0, 0.0], k=[0, 0, V // 2, 0], p=[1.0, 0.9, 1.0, 1.0], u=rng.random((4, 1)).astype(np.float32))
+        before = x.clone()
+        for in_place in (False, True):
+            _, out = ops._sample(x, in_place=in_place, **kw)
+            kept = out > -np.inf
+            assert int(kept.sum()) > 0
+            assert torch.equal(out.view(word)[kept], before.view(word)[kept]), (name, in_place)

@@ -26,7 +26,6 @@ struct SampleShared {
   unsigned long long sum_before;
   uint32_t count_before, bin, ids, listed;
   float best[kSampleWarps];
-  int best_id[kSampleWarps];
 };
 
 __device__ __forceinline__ void add_weight(SampleShared& s, int bin, unsigned long long w) {
@@ -320,42 +319,34 @@ __device__ __forceinline__ void write_cut_row(const SampleRow<Elt>& row, Elt* ou
   }
 }
 
-// Returns false for a row without a number above -infinity.
+// For a top-k of 2 and more and a temperature above 0.  Returns false for a row
+// without a number above -infinity.
 template <typename Elt>
 __device__ __noinline__ bool sample_any(SampleShared& s, const SampleRow<Elt> row, const SampleAsk ask, Elt* out, int32_t* token) {
   constexpr int E = SampleRow<Elt>::E;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   __syncthreads();
   if (tid < 256) s.table[tid] = kExp2Table[tid];
-  // the largest logit, and the first id that has it
   float best = -INFINITY;
-  int best_id = 0x7FFFFFFF;
 #pragma unroll 4
   for (int v = tid; v < row.vecs; v += kSampleThreads) {
     float x[E];
     row.load(v, x);
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (x[e] > best) best = x[e], best_id = E * v + e - row.phase;
+    for (int e = 0; e < E; ++e) best = fmaxf(best, x[e]);
   }
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    const float o = __shfl_xor_sync(0xFFFFFFFFu, best, d);
-    const int id = __shfl_xor_sync(0xFFFFFFFFu, best_id, d);
-    if (o > best || (o == best && id < best_id)) best = o, best_id = id;
-  }
-  if (lane == 0) s.best[warp] = best, s.best_id[warp] = best_id;
+  for (int d = 16; d > 0; d >>= 1) best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, d));
+  if (lane == 0) s.best[warp] = best;
   clear_bins(s);
   __syncthreads();
 #pragma unroll 1
-  for (int i = 0; i < kSampleWarps; ++i)
-    if (s.best[i] > best || (s.best[i] == best && s.best_id[i] < best_id)) best = s.best[i], best_id = s.best_id[i];
-  if (best == -INFINITY) best_id = -1;
+  for (int i = 0; i < kSampleWarps; ++i) best = fmaxf(best, s.best[i]);
   const bool infinite = best == INFINITY;
-  if (ask.cold || ask.k == 1 || best == -INFINITY) {
-    if (tid == 0 && token != nullptr) *token = best_id;
-    if (out != nullptr) write_cut_row(row, out, infinite ? key_of(0.f) : key_of(best), best_id, infinite);
-    return best != -INFINITY;
+  if (best == -INFINITY) {
+    if (tid == 0 && token != nullptr) *token = -1;
+    if (out != nullptr) write_cut_row(row, out, kKeyFloor, -1, false);
+    return false;
   }
 
   Sampler<Elt> f = {s, row, best, infinite, ask.scale};

@@ -985,8 +985,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
   Elt* out = a.out != nullptr ? static_cast<Elt*>(a.out) + r * a.V : nullptr;
   int32_t* token = a.tokens != nullptr ? a.tokens + r : nullptr;
   if (ask.k <= 0 || ask.k > a.V) ask.k = a.V;
-  ask.cold = !(T >= 1e-6f) || T > 3e38f;
-  if (ask.cold && T != 0.f) bad |= SPECDEC_DEV_ERR_TEMPERATURE;
+  const bool cold = !(T >= 1e-6f) || T > 3e38f;  // the largest logit alone
+  if (cold && T != 0.f) bad |= SPECDEC_DEV_ERR_TEMPERATURE;
   if (!(ask.p >= 0.f) || !(m <= 1.f) || !(m >= 0.f)) {
     bad |= SPECDEC_DEV_ERR_SAMPLE;
     if (!(ask.p >= 0.f)) ask.p = 1.f;
@@ -1001,7 +1001,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
   SampleJob<Elt> job = {s, sample_smem + sizeof(SampleSmem<Elt>), row, cooperative_groups::this_cluster(), ctas, rank, min(row.vecs, rank * share),
                         min(row.vecs, rank * share + share), 0.f, {}};
   job.say_begun();
-  if (ask.cold || ask.k == 1) {
+  if (cold || ask.k == 1) {
     uint32_t key;
     int id;
     job.wait_begun();

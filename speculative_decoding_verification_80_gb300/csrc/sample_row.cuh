@@ -32,7 +32,6 @@ struct SampleAsk {
   int k;                      // 1 .. V
   unsigned long long least;   // weight that min-p asks for, 0: none
   WeightScale scale;
-  bool cold;                  // the largest logit alone
 };
 
 // Larger for a larger number; finite x, or an infinity.

@@ -128,6 +128,8 @@ struct SamplePlace {
   uint32_t key, ids, all;        // all: ids of that key
   unsigned long long sum;        // weight before the key's ids
 };
+// All ids: as many of the least finite logit as there may be.
+constexpr uint32_t kAnyIds = 0xFFFFFFFFu;
 
 template <typename Elt>
 struct Sampler {
@@ -360,7 +362,7 @@ __device__ __noinline__ bool sample_any(SampleShared& s, const SampleRow<Elt> ro
   BinSums sums;
   sum_bins(s, sums);
   // what is kept: larger keys, and the first ids of this one; its weight
-  SamplePlace kept = {kKeyFloor + 1, 0, 0, sums.w_all};
+  SamplePlace kept = {kKeyFloor + 1, kAnyIds, 0, 0};
   unsigned long long weight = sums.w_all;
   if (static_cast<uint32_t>(ask.k) < sums.c_all) {
     find_bin(s, sums, kByCount, ask.k);

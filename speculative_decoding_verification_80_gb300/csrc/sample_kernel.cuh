@@ -1088,7 +1088,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
     }
   }
 
-  SamplePlace kept = {kKeyFloor + 1, 0, 0, 0}, drawn = {0, 0, 0, 0};
+  SamplePlace kept = {kKeyFloor + 1, kAnyIds, 0, 0}, drawn = {0, 0, 0, 0};
   if (simple) {
     if constexpr (sizeof(Elt) == 2) {
       job.find_least(ask);
@@ -1110,7 +1110,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
         __syncthreads();
         if (!s.more) break;
         job.add_zeros();
-        if (tid < 32) kept = {kKeyFloor + 1, 0, 0, 0};
+        if (tid < 32) kept = {kKeyFloor + 1, kAnyIds, 0, 0};
       }
       if (simple) kept = s.kept, drawn = s.drawn, simple = s.simple;
     } else {

@@ -66,3 +66,18 @@ def test_kept_logits_keep_their_bits(V, dtype):
             kept = out > -np.inf
             assert int(kept.sum()) > 0
             assert torch.equal(out.view(word)[kept], before.view(word)[kept]), (name, in_place)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [2, 300, 5003, 70001])
+def test_sample_borders_among_the_types_lowest_value(V, dtype):
+    """Rows that are masked whole by the type's lowest value, or whose last ids are: all of them are ids as others."""
+    rng = np.random.default_rng(V)
+    x = torch.full((4, 1, V), torch.finfo(dtype).min, dtype=dtype, device="cuda")
+    x[2, 0, ::2] = -float("inf")
+    x[3, 0, :V // 2] = float(x[0, 0, 0]) / 2
+    u = rng.random((4, 1)).astype(np.float32)
+    for kw in (dict(), dict(p=np.full(4, 0.3)), dict(p=np.full(4, 0.71), m=np.full(4, 0.5)), dict(k=np.full(4, max(2, V - 1)), p=np.full(4, 0.9)),
+               dict(p=np.full(4, 0.0))):
+        ops._sample(x, u=u, **kw)
+        ops._sample(x, T=np.full(4, 1e4), u=u, **kw)

@@ -136,15 +136,16 @@ struct Sampler {
   static constexpr int E = SampleRow<Elt>::E;
   SampleShared& s;
   const SampleRow<Elt> row;
-  float top;       // the largest logit
+  float top;       // the largest logit in the unit, 0 if it is infinite
   bool infinite;   // it is infinite: the others have no weight
   WeightScale scale;
+  float unit;      // what logits are taken times
 
   __device__ __forceinline__ float relative(float x) const { return infinite ? (x == INFINITY ? 0.f : -INFINITY) : x; }
-  __device__ __forceinline__ unsigned long long weight(float x) const { return sample_weight(x, infinite ? 0.f : top, scale, s.table); }
+  __device__ __forceinline__ unsigned long long weight(float x) const { return sample_weight(x * unit, top, scale, s.table); }
   // (monotone: each step rounds a monotone function)
   __device__ __forceinline__ int bin_of(float x) const {
-    const float t = (x - (infinite ? 0.f : top)) * (scale.hi * -32.f);
+    const float t = (x * unit - top) * (scale.hi * -32.f);
     return t < static_cast<float>(kSampleBins - 1) ? static_cast<int>(t) : kSampleBins - 1;
   }
 
@@ -351,7 +352,7 @@ __device__ __noinline__ bool sample_any(SampleShared& s, const SampleRow<Elt> ro
     return false;
   }
 
-  Sampler<Elt> f = {s, row, best, infinite, ask.scale};
+  Sampler<Elt> f = {s, row, infinite ? 0.f : best * ask.unit, infinite, ask.scale, ask.unit};
   f.each([&](float x, int) {
     if (x == -INFINITY) return;
     const int bin = f.bin_of(x);
@@ -394,7 +395,7 @@ __device__ __noinline__ bool sample_any(SampleShared& s, const SampleRow<Elt> ro
       weight = kept.sum + kept.ids * f.weight(of_key(kept.key));
     }
   }
-  if (ask.least > 0 && f.weight(kept.key > kKeyFloor + 1 ? of_key(kept.key) : -3.4e38f) < ask.least) {
+  if (ask.least > 0 && f.weight(of_key(kept.key)) < ask.least) {
     // the least key with enough weight: 32 of them are looked at a time
     __syncthreads();
     if (warp == 0) {

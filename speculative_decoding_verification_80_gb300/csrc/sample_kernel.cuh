@@ -950,6 +950,16 @@ __device__ __forceinline__ bool SampleJob<Elt>::decide(const SampleAsk& ask, int
   return true;
 }
 
+__device__ __forceinline__ WeightScale scale_of(double c) {
+  const float hi = static_cast<float>(c);
+  return {hi, static_cast<float>(c - static_cast<double>(hi))};
+}
+// Of higher temperatures the scale's rest ends below the normal floats, and logits that
+// are as far apart as matters have differences above the largest float: their rows are
+// sample_any's, which takes logits in 2^64.  (bf16 rows within 4096 have weights of 1 at
+// such a temperature, whatever is left of the scale.)
+constexpr float kLeastScale = 0x1p-64f;
+
 // One cluster a row.
 template <typename Elt>
 __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleArgs a, int ctas) {
@@ -1021,9 +1031,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
   __syncthreads();
   if (tid == kSampleThreads - 1) {
     // (64-bit arithmetic by one thread, beside the others' work: it has 1/64 of the rate)
-    const double c = 1.4426950408889634074 / static_cast<double>(T);
-    s.scale.hi = static_cast<float>(c);
-    s.scale.lo = static_cast<float>(c - static_cast<double>(s.scale.hi));
+    s.scale = scale_of(1.4426950408889634074 / static_cast<double>(T));
     s.least = m > 0.f ? static_cast<unsigned long long>(ceil(static_cast<double>(m) * static_cast<double>(kWeightOne))) : 0;
   }
   bool simple = true;
@@ -1079,7 +1087,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
       job.template largest<false>(&key, &id);
     ask.scale = job.scale = s.scale;
     ask.least = s.least;
-    simple = key > kKeyFloor && key < key_of(INFINITY);
+    simple = key > kKeyFloor && key < key_of(INFINITY) && job.scale.hi >= kLeastScale;
     job.top = of_key(key);
     if (simple) {
       job.find_least(ask);
@@ -1119,6 +1127,11 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
   }
   if (!simple) {
     // by the first CTA alone, whose memory nobody reads any more
+    ask.unit = 1.f;
+    if (ask.scale.hi < kLeastScale) {
+      ask.unit = 0x1p-64f;
+      ask.scale = scale_of(0x1p64 * 1.4426950408889634074 / static_cast<double>(a.temperature[b]));
+    }
     job.meet();
     if (rank == 0) {
       if (!sample_any(smem.any, row, ask, out, token)) bad |= SPECDEC_DEV_ERR_SAMPLE;

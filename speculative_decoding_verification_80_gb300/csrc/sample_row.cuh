@@ -32,6 +32,7 @@ struct SampleAsk {
   int k;                      // 1 .. V
   unsigned long long least;   // weight that min-p asks for, 0: none
   WeightScale scale;
+  float unit;                 // sample_any: a power of two that logits are taken times, for that scale
 };
 
 // Larger for a larger number; finite x, or an infinity.

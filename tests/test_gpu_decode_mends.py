@@ -81,3 +81,20 @@ def test_sample_borders_among_the_types_lowest_value(V, dtype):
                dict(p=np.full(4, 0.0))):
         ops._sample(x, u=u, **kw)
         ops._sample(x, T=np.full(4, 1e4), u=u, **kw)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T", [2.0 ** 63, 2.0 ** 64, 3e25, 1e34, 1e36, 1e38, 3e38])
+def test_sample_at_the_largest_temperatures(T, dtype):
+    """Logits as far apart as temperatures are high, up to the type's ends."""
+    rng = np.random.default_rng(int(np.log2(T)))
+    for V in (501, 20011):
+        top = min(3.38e38, 4 * T)
+        x = ops.dev(rng.uniform(-top, top, (6, 1, V)).astype(np.float32), dtype)
+        x[1, 0, ::2] = -float("inf")
+        x[2, 0, 1:] = torch.finfo(dtype).min
+        u = rng.random((6, 1)).astype(np.float32)
+        ops._sample(x, T=np.full(6, T), u=u)
+        ops._sample(x, T=np.full(6, T), p=np.full(6, 0.7), u=u)
+        ops._sample(x, T=np.full(6, T), k=np.full(6, V // 3), m=np.full(6, 0.02), u=u)
+        ops._sample(x, T=np.full(6, T), k=np.full(6, V - 7), p=np.full(6, 0.9), m=np.full(6, 0.3), u=u)

@@ -99,7 +99,7 @@ class Decoder:
         """The requests' prompts [B, P]; one token is made."""
         B, P = tokens.shape
         blocks = sd.kv_block_step(self.table, self.state.kv_len, self.state.held, torch.full_like(self.accepted, P),
-                                  self.ring, self.state.ring_state, self.block_size, B * P, error_word=self.error)
+                                  self.ring, self.state.ring_state, self.block_size, B * P, error_word=self.error, shares=self.shares)
         for name in ("kv_len", "held", "ring_state"):
             getattr(self.state, name).copy_(getattr(blocks, name))
         x = self._layer(tokens.reshape(-1), blocks)
@@ -133,7 +133,8 @@ class Decoder:
         fed = torch.stack(fed, 1)
         drafts = fed[:, 1:].contiguous()
         s = sd.kv_block_step(self.table, self.state.kv_len, self.state.held, self.new_tokens, self.ring, self.state.ring_state,
-                             self.block_size, B * (n + 1), accepted_len=self.accepted, out=self.state, error_word=self.error)
+                             self.block_size, B * (n + 1), accepted_len=self.accepted, out=self.state, error_word=self.error,
+                             shares=self.shares)
         x = self._layer(fed.view(-1), s)
         logits = (x @ self.w_head.t()).view(B, n + 1, self.V)
         sd.spec_process_logits(logits, self.history, self.prompt_len, self.history_len, draft_tokens=drafts,

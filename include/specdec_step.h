@@ -108,6 +108,24 @@ specdec_status_t kv_block_step(int32_t B, int32_t block_size, int32_t max_blocks
                                void* stream);
 
 /*
+ * kv_block_step_shared — the same where requests may share blocks (kv_fork).
+ *
+ *   shares   [num_blocks] int32 or NULL (none are shared): a block's holders beside
+ *            the first.
+ * A request that would write a block with other holders, or give one back, is
+ * refused, as one for which no blocks are left: it gets no new tokens, keeps its
+ * tokens and blocks, and sets SPECDEC_DEV_ERR_BLOCKS; others are served.  (kv_fork
+ * ends such a request, or cuts it back, and gives it blocks of its own.)
+ */
+specdec_status_t kv_block_step_shared(int32_t B, int32_t block_size, int32_t max_blocks, int32_t num_blocks,
+                                      const int32_t* kv_len, const int32_t* accepted_len, const int32_t* new_tokens,
+                                      const int32_t* held, int32_t* block_table, int32_t* free_ring,
+                                      const int32_t* ring_state, const int32_t* shares, int32_t* kv_len_out,
+                                      int32_t* held_out, int32_t* ring_state_out, int32_t* cu_tokens,
+                                      int32_t* cu_blocks, int32_t* slot_map, int32_t* positions, int32_t capacity,
+                                      uint32_t* error_word, void* stream);
+
+/*
  * kv_append — keys and values of new tokens into the cache.
  *
  *   k, v       [T, H, D] of dtype (F32 or BF16); token t's head h starts at
@@ -280,11 +298,11 @@ specdec_status_t spec_rotary(const void* q, const void* k, specdec_dtype_t dtype
 
 /*
  * Holders of a block: shares [num_blocks] int32 says how many requests, or other
- * users of the cache, hold a block beside the first.  kv_block_step knows nothing
- * of it: what it hands out has one holder and shares 0.  It gives back whatever it
- * takes from a request, so requests that hold shared blocks are ended, or cut back
- * into them, by kv_fork.  Nor does it or kv_append look whether a block that is
- * written has other holders: after kv_fork none has.
+ * users of the cache, hold a block beside the first.  What kv_block_step hands out has
+ * one holder and shares 0.  Without shares it gives back whatever it takes from a
+ * request, and neither it nor kv_append looks whether a block that is written has other
+ * holders: after kv_fork none has, and requests that hold shared blocks are ended, or
+ * cut back into them, by kv_fork.  kv_block_step_shared looks, and refuses.
  *
  * The workspace of kv_fork and kv_compact: specdec_page_workspace_bytes(num_blocks)
  * bytes, zero-filled once before its first use; every call leaves it ready for the

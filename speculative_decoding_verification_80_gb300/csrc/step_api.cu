@@ -170,6 +170,18 @@ extern "C" specdec_status_t kv_block_step(int32_t B, int32_t block_size, int32_t
                                           int32_t* held_out, int32_t* ring_state_out, int32_t* cu_tokens,
                                           int32_t* cu_blocks, int32_t* slot_map, int32_t* positions,
                                           int32_t capacity, uint32_t* error_word, void* stream) {
+  return kv_block_step_shared(B, block_size, max_blocks, num_blocks, kv_len, accepted_len, new_tokens, held, block_table, free_ring,
+                              ring_state, nullptr, kv_len_out, held_out, ring_state_out, cu_tokens, cu_blocks, slot_map, positions,
+                              capacity, error_word, stream);
+}
+
+extern "C" specdec_status_t kv_block_step_shared(int32_t B, int32_t block_size, int32_t max_blocks, int32_t num_blocks,
+                                                 const int32_t* kv_len, const int32_t* accepted_len,
+                                                 const int32_t* new_tokens, const int32_t* held, int32_t* block_table,
+                                                 int32_t* free_ring, const int32_t* ring_state, const int32_t* shares,
+                                                 int32_t* kv_len_out, int32_t* held_out, int32_t* ring_state_out,
+                                                 int32_t* cu_tokens, int32_t* cu_blocks, int32_t* slot_map,
+                                                 int32_t* positions, int32_t capacity, uint32_t* error_word, void* stream) {
   if (B < 0 || block_size <= 0 || max_blocks <= 0 || num_blocks <= 0 || capacity < 0) return SPECDEC_ERR_INVALID_ARG;
   if (!block_size_ok(block_size) || B > SPECDEC_MAX_BATCH) return SPECDEC_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(num_blocks) * block_size > INT32_MAX ||
@@ -198,6 +210,7 @@ extern "C" specdec_status_t kv_block_step(int32_t B, int32_t block_size, int32_t
   a.table = block_table;
   a.ring = free_ring;
   a.ring_state = ring_state;
+  a.shares = shares;
   a.kv_len_out = kv_len_out;
   a.held_out = held_out;
   a.ring_state_out = ring_state_out;
@@ -214,13 +227,14 @@ extern "C" specdec_status_t kv_block_step(int32_t B, int32_t block_size, int32_t
   const bool apart = kv_len_out != kv_len && held_out != held && ring_state_out != ring_state;
   if (apart && B <= kBlockShared) {
     const int bytes = 4 * (B + 1) * static_cast<int>(sizeof(int32_t));
-    if (bytes > 40 * 1024 && cudaFuncSetAttribute(block_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const auto kernel = shares != nullptr ? block_step_kernel<true> : block_step_kernel<false>;
+    if (bytes > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                   4 * (kBlockShared + 1) * static_cast<int>(sizeof(int32_t))) != cudaSuccess)
       return SPECDEC_ERR_CUDA;
     const int64_t ctas = (static_cast<int64_t>(capacity) + 4 * kBlockThreads - 1) / (4 * kBlockThreads);
-    block_step_kernel<<<static_cast<unsigned>(ctas < 1 ? 1 : (ctas > 128 ? 128 : ctas)), kBlockThreads, bytes, st>>>(a);
+    kernel<<<static_cast<unsigned>(ctas < 1 ? 1 : (ctas > 128 ? 128 : ctas)), kBlockThreads, bytes, st>>>(a);
   } else {
-    block_plan_kernel<<<1, kBlockThreads, 0, st>>>(a);
+    (shares != nullptr ? block_plan_kernel<true> : block_plan_kernel<false>)<<<1, kBlockThreads, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
     const int64_t threads = (static_cast<int64_t>(capacity) + 3) / 4;
     block_fill_kernel<<<static_cast<unsigned>(threads < 256 ? 1 : (threads + 255) / 256), 256, 0, st>>>(a);

@@ -25,7 +25,7 @@ ATTENTION_WORKSPACE_BYTES = 64 << 20
 E4M3 = torch.float8_e4m3fn
 
 # Every symbol the header declares.
-STEP_EXPORTS = ("kv_block_step", "kv_append", "spec_attention", "spec_process_logits", "spec_sample", "spec_rotary",
+STEP_EXPORTS = ("kv_block_step", "kv_block_step_shared", "kv_append", "spec_attention", "spec_process_logits", "spec_sample", "spec_rotary",
                 "kv_fork", "kv_compact", "kv_copy")
 
 
@@ -82,6 +82,8 @@ def declare(L) -> None:
     P, i32, i64, sz, f32, ci = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float,
                                 ctypes.c_int)
     L.kv_block_step.argtypes = [i32] * 4 + [P] * 14 + [i32, P, P]
+    if hasattr(L, "kv_block_step_shared"):
+        L.kv_block_step_shared.argtypes = [i32] * 4 + [P] * 15 + [i32, P, P]
     L.kv_append.argtypes = [P, P, ci, i32, i32, i32, i64, i64, i64, i64, P, i32, i32, P, P, P, P, P]
     L.spec_attention.argtypes = [P, i64, i32, i32, i32, i32, i32, P, P, P, i32, i32, i32, P, P, P, P, f32, P, P, sz, P]
     L.spec_process_logits.argtypes = [P, P, ci, i32, i32, i32, P, i32, P, P, P, P, P, P, P, P, P, P, i32, P, i32, P, P, P]
@@ -101,12 +103,14 @@ def declare(L) -> None:
 def kv_block_step(block_table: torch.Tensor, kv_len: torch.Tensor, held: torch.Tensor, new_tokens: torch.Tensor,
                   free_ring: torch.Tensor, ring_state: torch.Tensor, block_size: int, capacity: int,
                   accepted_len: Optional[torch.Tensor] = None, out: Optional[BlockStep] = None,
-                  error_word: Optional[torch.Tensor] = None, stream=None) -> BlockStep:
+                  error_word: Optional[torch.Tensor] = None, stream=None, shares: Optional[torch.Tensor] = None) -> BlockStep:
     """Blocks and slots of the next tokens from the lengths that the last step
     left on the device (see include/specdec_step.h).  block_table
     [B, max_blocks] and free_ring [num_blocks] are updated in place; `out`
     reuses another step's tensors (its kv_len, held and ring_state may be the
-    inputs themselves).  Returns a BlockStep."""
+    inputs themselves).  With `shares` [num_blocks] (kv_fork's), requests that
+    would write or give back a block that others hold are refused.  Returns a
+    BlockStep."""
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
     B, width = block_table.shape
@@ -129,8 +133,12 @@ def kv_block_step(block_table: torch.Tensor, kv_len: torch.Tensor, held: torch.T
     else:
         results = [_at(t, n, f"out.{what}", I32, dev)
                    for t, n, what in zip(out, (B, B, 2, B + 1, B + 1, capacity, capacity), BlockStep._fields)]
-    _check(load_library().kv_block_step(B, block_size, width, blocks, *fixed, *results, capacity,
-                                        _word(error_word, dev), _on_stream(stream, dev)), "kv_block_step")
+    last = (capacity, _word(error_word, dev), _on_stream(stream, dev))
+    if shares is None:
+        _check(load_library().kv_block_step(B, block_size, width, blocks, *fixed, *results, *last), "kv_block_step")
+    else:
+        _check(load_library().kv_block_step_shared(B, block_size, width, blocks, *fixed, _at(shares, blocks, "shares", I32, dev), *results,
+                                                   *last), "kv_block_step_shared")
     return out
 
 

@@ -161,8 +161,10 @@ extern "C" specdec_status_t spec_rotary(const void* q, const void* k, specdec_dt
   for (int w = 0; w < 2; ++w) {
     if (a.heads[w] == 0) continue;
     const int64_t* s = strides + 4 * w;
+    // (the last row's start stays within 64 bits)
+    const int64_t most[2] = {(INT64_MAX >> 4) / (T > 1 ? T - 1 : 1), (INT64_MAX >> 4) / (a.heads[w] > 1 ? a.heads[w] - 1 : 1)};
     for (int i = 0; i < 4; ++i)
-      if (s[i] < 0 || s[i] > (INT64_MAX >> 34)) return SPECDEC_ERR_INVALID_ARG;
+      if (s[i] < 0 || s[i] > most[i % 2]) return SPECDEC_ERR_INVALID_ARG;
     if (!aligned(x[w], elt) || !aligned(y[w], elt)) return SPECDEC_ERR_INVALID_ARG;
     // in place means in every place
     if (x[w] == y[w] && (s[0] != s[2] || s[1] != s[3])) return SPECDEC_ERR_INVALID_ARG;

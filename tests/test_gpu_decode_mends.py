@@ -98,3 +98,27 @@ def test_sample_at_the_largest_temperatures(T, dtype):
         ops._sample(x, T=np.full(6, T), p=np.full(6, 0.7), u=u)
         ops._sample(x, T=np.full(6, T), k=np.full(6, V // 3), m=np.full(6, 0.02), u=u)
         ops._sample(x, T=np.full(6, T), k=np.full(6, V - 7), p=np.full(6, 0.9), m=np.full(6, 0.3), u=u)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rotary_of_heads_far_apart(dtype):
+    """Keys of a cache in the order of heads, tokens, values, whose heads lie more than 2^29 values apart; and tokens as far apart."""
+    far, D = (1 << 29) + 64, 64
+    size = 2 * far
+    if torch.cuda.mem_get_info()[0] < 3 * size * torch.finfo(dtype).bits // 8:
+        pytest.skip("needs some GB")
+    turns, _ = sd.rotary_turns(D)
+    pos = torch.arange(7, 10, dtype=torch.int32, device="cuda")
+    big = torch.zeros(size, dtype=dtype, device="cuda")
+    for shape, strides in (((3, 2, D), (D, far, 1)), ((2, 3, D), (far, D, 1)), ((1, 2, D), (far, far, 1))):
+        x = torch.randn(shape, device="cuda").to(dtype)
+        want, _ = sd.spec_rotary(x.clone(), None, pos[:shape[0]], turns)
+        view = big.as_strided(shape, strides)
+        view.copy_(x)
+        got, _ = sd.spec_rotary(view, None, pos[:shape[0]], turns)
+        assert torch.equal(got, want)
+        view.zero_()
+        _, out = sd.spec_rotary(None, x, pos[:shape[0]], turns, k_out=view)
+        assert torch.equal(out, want)
+        view.zero_()
+    assert int(big.count_nonzero()) == 0  # and nothing else was written

@@ -273,7 +273,8 @@ specdec_status_t spec_sample(const void* logits, void* out, specdec_dtype_t dtyp
  *
  *   q, k          [T, Hq, D] and [T, H, D] of dtype; token t's head h starts at
  *                 t * token_stride + h * head_stride elements, its D values are
- *                 contiguous.  Hq or H may be 0 (their pointers are not looked at).
+ *                 contiguous.  Hq or H may be 0 (their pointers are not looked at);
+ *                 strides of one token or one head do not matter.
  *   q_out, k_out  the same, with strides of their own, rows apart from one another;
  *                 the inputs themselves with their strides, or memory that no input
  *                 shares.

@@ -160,7 +160,9 @@ extern "C" specdec_status_t spec_rotary(const void* q, const void* k, specdec_dt
   a.heads[1] = H;
   for (int w = 0; w < 2; ++w) {
     if (a.heads[w] == 0) continue;
-    const int64_t* s = strides + 4 * w;
+    // (of one token, or one head, there is no next)
+    const int64_t s[4] = {T > 1 ? strides[4 * w] : 0, a.heads[w] > 1 ? strides[4 * w + 1] : 0, T > 1 ? strides[4 * w + 2] : 0,
+                          a.heads[w] > 1 ? strides[4 * w + 3] : 0};
     // (the last row's start stays within 64 bits)
     const int64_t most[2] = {(INT64_MAX >> 4) / (T > 1 ? T - 1 : 1), (INT64_MAX >> 4) / (a.heads[w] > 1 ? a.heads[w] - 1 : 1)};
     for (int i = 0; i < 4; ++i)

@@ -122,3 +122,25 @@ def test_rotary_of_heads_far_apart(dtype):
         assert torch.equal(out, want)
         view.zero_()
     assert int(big.count_nonzero()) == 0  # and nothing else was written
+
+
+def test_rotary_strides_of_one_token_or_head_do_not_matter():
+    import ctypes
+
+    lib, turns = sd.load_library(), sd.rotary_turns(64)[0]
+    pos = torch.full((1,), 5, dtype=torch.int32, device="cuda")
+    x = torch.randn(1, 4, 64, device="cuda")
+    want, _ = sd.spec_rotary(x.clone(), None, pos, turns)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    y = x.clone()
+    none = (None, 0, 0)
+    torch.cuda.synchronize()
+    assert lib.spec_rotary(p(y), None, 0, 1, 4, 0, 64, 0, 64, 0, 0, p(pos), p(turns), 64, 0, 1.0, p(y), 256, 64, *none, None) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+    y = x.view(4, 1, 64).clone()  # four tokens of one head
+    pos = torch.full((4,), 5, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    assert lib.spec_rotary(p(y), None, 0, 4, 1, 0, 64, 64, 64, 0, 0, p(pos), p(turns), 64, 0, 1.0, p(y), 64, 3, *none, None) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(y.view(1, 4, 64), want)

@@ -390,7 +390,10 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional
         pair = lambda turns: rotary_dim * math.log(length / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))  # noqa: E731
         low, high = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rotary_dim - 1)
         ramp = [min(max((i - low) / max(high - low, 1e-3), 0.0), 1.0) for i in range(half)]
-        factor = float(rest.get("attention") or 0.1 * math.log(by) + 1.0)
+        given = rest.get("attention")
+        factor = 0.1 * math.log(by) + 1.0 if given is None else float(given)
+        if not (factor > 0 and math.isfinite(factor)):
+            raise ValueError("yarn scaling needs a positive attention")
         return [f * (1.0 - r) + f / by * r for f, r in zip(freq, ramp)], factor
     low, high = float(rest.get("low", 1.0)), float(rest.get("high", 4.0))
     if not (high > low > 0):

@@ -29,3 +29,12 @@ def test_yarn_between_its_ends(original, fast, slow, low, high):
         else:
             share = (i - low) / (high - low)
             assert g == pytest.approx(f - share * (f - f / by), rel=1e-14) and f / by < g < f
+
+
+def test_yarn_attention_is_what_is_given():
+    ask = lambda a: sd.rotary_frequencies(64, scaling=dict(type="yarn", factor=4, original=4096, attention=a))  # noqa: E731
+    assert ask(0.5)[1] == 0.5 and ask(1)[1] == 1.0
+    assert ask(None)[1] == pytest.approx(0.1 * math.log(4) + 1)
+    for bad in (0, 0.0, -1.0, math.inf, math.nan):
+        with pytest.raises(ValueError):
+            ask(bad)

@@ -34,6 +34,7 @@ struct RotaryArgs {
 
 constexpr int kRotaryThreads = 256;
 constexpr int kRotaryPairs = 2048;  // of a CTA's tokens, in shared memory
+constexpr int kRotaryTokens = 8;    // of a CTA, at most
 
 template <typename Elt, int N>
 struct RotaryVec {
@@ -54,7 +55,7 @@ template <typename Elt, int N, bool kHalf>
 __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs a) {
   using Vec = RotaryVec<Elt, N>;
   __shared__ float2 turn[kRotaryPairs];
-  __shared__ int32_t position[kRotaryPairs];
+  __shared__ int32_t position[kRotaryTokens];
   const int tid = threadIdx.x, t0 = blockIdx.x * a.group, tokens = min(a.group, a.T - t0);
   for (int i = tid; i < tokens * a.pairs; i += kRotaryThreads) {
     const int t = i / a.pairs, c = i - t * a.pairs, p = a.positions[t0 + t];

@@ -72,7 +72,7 @@ cudaError_t launch_rotary(RotaryArgs a, int D, bool half, cudaStream_t st) {
   int dev = 0, sms = 0;
   const cudaError_t e = device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
-  while (2 * a.group * a.pairs <= kRotaryPairs && a.group < 8 && a.T > 8 * sms * a.group) a.group *= 2;
+  while (2 * a.group * a.pairs <= kRotaryPairs && 2 * a.group <= kRotaryTokens && a.T > 8 * sms * a.group) a.group *= 2;
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(a.T) + a.group - 1) / a.group);
   constexpr int kWide = 16 / static_cast<int>(sizeof(Elt));
   if (half) {

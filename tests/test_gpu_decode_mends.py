@@ -144,3 +144,53 @@ def test_rotary_strides_of_one_token_or_head_do_not_matter():
     assert lib.spec_rotary(p(y), None, 0, 4, 1, 0, 64, 64, 64, 0, 0, p(pos), p(turns), 64, 0, 1.0, p(y), 64, 3, *none, None) == 0
     torch.cuda.synchronize()
     assert torch.equal(y.view(1, 4, 64), want)
+
+
+def test_large_forks_and_compactions_in_a_graph():
+    """As many blocks as take a grid of CTAs, captured and replayed."""
+    rng = np.random.default_rng(17)
+    c = ops._pool(rng, 900, 60, 16, spare=20000)
+    N, B = len(c["ring"]), 1500
+    parent = ops.i32(rng.integers(-1, 900, B))
+    args = [ops.i32(c[n]) for n in ("table", "kv", "held")]
+    shares, ring, state = (ops.i32(c[n]) for n in ("shares", "ring", "state"))
+    ws = sd.new_page_workspace(N)
+    first_ring = ring.clone()
+    fork = sd.kv_fork(*args, parent, shares, ring, state, 16, workspace=ws)
+    packed = sd.kv_compact(fork.block_table, fork.held, fork.shares, ring, fork.ring_state, workspace=ws)
+    after = ring.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fork2 = sd.kv_fork(*args, parent, shares, ring, state, 16, workspace=ws)
+        packed2 = sd.kv_compact(fork2.block_table, fork2.held, fork2.shares, ring, fork2.ring_state, workspace=ws)
+    n, moves, free = int(fork.count), int(packed.count), int(packed.ring_state[1])
+    assert n > 0 and moves > 0
+    for _ in range(2):
+        ring.copy_(first_ring)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(ring, after) and torch.equal(fork.copies[:n], fork2.copies[:n]) and torch.equal(packed.copies[:moves], packed2.copies[:moves])
+        for name in ("block_table", "kv_len", "held", "shares", "ring_state", "count"):
+            assert torch.equal(getattr(fork, name), getattr(fork2, name)), name
+        for name in ("block_table", "shares", "renamed", "ring_state", "count"):
+            assert torch.equal(getattr(packed, name), getattr(packed2, name)), name
+        assert torch.equal(packed.free_ring[:free], packed2.free_ring[:free])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_sample_rows_past_32_bits(dtype):
+    """More than 2^31 logits, cut in place: the last rows as they are alone."""
+    V, R = 262144, 65
+    B = (1 << 31) // (R * V) + 2
+    if torch.cuda.mem_get_info()[0] < 2 * B * R * V * torch.finfo(dtype).bits // 8:
+        pytest.skip("needs some GB")
+    x = torch.empty(B, R, V, dtype=dtype, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(3))
+    u, p = torch.rand(B, R, device="cuda"), torch.full((B,), 0.8, device="cuda")
+    last = x[B - 1:].clone()
+    k = torch.full((B,), 50, dtype=torch.int32, device="cuda")
+    tokens = sd.spec_sample(x, top_k=k, top_p=p, uniform=u, out=x)
+    alone = torch.empty_like(last)
+    want = sd.spec_sample(last, top_k=k[:1], top_p=p[:1], uniform=u[B - 1:].contiguous(), out=alone)
+    torch.cuda.synchronize()
+    assert torch.equal(tokens[B - 1:], want) and torch.equal(x[B - 1], alone[0])
+    assert int((x[0] > -float("inf")).sum(1).max()) <= 50 and int((x[B - 1] > -float("inf")).sum(1).min()) > 0

@@ -22,18 +22,20 @@
 //
 // A row is one cluster's of 1 to 8 CTAs (the rule is where it is launched); each has
 // a part of the row, a histogram of it, and a share of the bins to add up.  Two CTAs
-// an SM, with 64 registers a thread: three with 40 spilt them and were slower (58 us
-// instead of 48 on the 256 rows below), four had no room for the bins.
+// an SM, with 64 registers a thread (28 bytes of bf16's and 16 of fp32's are spilt):
+// three with 40 spilt more and were slower (58 us instead of 48 on the 256 rows below),
+// four had no room for the bins.
 //
 // Measured on one GB300, cut rows written back: one row of 128256 bf16 logits 18.5 us,
 // 256 rows 48 (131 MB, 2.8 TB/s), 832 of 152064 141 (506 MB, 3.6 TB/s).  A row's chain
 // of barriers and looks takes 12 to 14 us of its 34 to 45; the histogram takes 20 (a
 // warp's 32 additions in shared memory some 4 cycles), the pass that writes 11 to 30.
-// Tokens alone of 300 fp32 rows of 50001 take 80 us: a row that top-p alone cuts 67,
-// 38 of them for all its weights (some 75 instructions each), and 15 for two lists of
-// a bin's ids, each a pass over the row.  What was no faster: 16384 bins, lists of the
-// bins that have ids, shorter weights for small ones, clusters of two for many rows
-// (300 fp32 rows: 115 us), ids looked at by several lanes each.
+// Tokens alone of 300 fp32 rows of 50001 (60 MB) take 80 us from L2 and 93 from HBM; a
+// row that top-p alone cuts takes 67 of them, 38 for all its weights (some 75
+// instructions each), and 15 for two lists of a bin's ids, each a pass over the row.
+// What was no faster: 16384 bins, lists of the bins that have ids, shorter weights for
+// small ones, clusters of two for many rows (300 fp32 rows: 115 us), ids looked at by
+// several lanes each.
 #pragma once
 #include <cooperative_groups.h>
 
@@ -954,11 +956,11 @@ __device__ __forceinline__ WeightScale scale_of(double c) {
   const float hi = static_cast<float>(c);
   return {hi, static_cast<float>(c - static_cast<double>(hi))};
 }
-// Of higher temperatures the scale's rest ends below the normal floats, and logits that
-// are as far apart as matters have differences above the largest float: their rows are
-// sample_any's, which takes logits in 2^64.  (bf16 rows within 4096 have weights of 1 at
-// such a temperature, whatever is left of the scale.)
-constexpr float kLeastScale = 0x1p-64f;
+// Of higher temperatures (from 1.8e30 on) the scale's rest ends below the normal floats,
+// and logits that are as far apart as matters have differences above the largest float:
+// their rows are sample_any's, which takes logits in 2^64.  (bf16 rows within 4096 have
+// weights of 1 at such a temperature, whatever is left of the scale.)
+constexpr float kLeastScale = 0x1p-100f;
 
 // One cluster a row.
 template <typename Elt>

@@ -259,8 +259,9 @@ specdec_status_t spec_process_logits(const void* logits, void* out, specdec_dtyp
  * weights sum to more than uniform times that of all kept.  A row without a
  * number above -infinity gives -1 and keeps nothing; infinite logits are equal,
  * and the others count as -infinity beside them.
- * Weights are whole numbers of 2^-44 of the largest, within 2^-40 of their value,
- * and their sums are exact.  (bf16 logits within 1.01 * 2^-20 of 0 weigh as 0 does
+ * Weights are made to within 2^-40 of their value and rounded to whole numbers of 2^-44
+ * of the largest, so that the smallest are 0 and a min_p means its value rounded up to
+ * such a number; their sums are exact.  (bf16 logits within 1.01 * 2^-20 of 0 weigh as 0 does
  * where that changes the sum by less than 2^-40 of itself.)
  */
 specdec_status_t spec_sample(const void* logits, void* out, specdec_dtype_t dtype, int32_t B, int32_t n_max, int32_t V,

@@ -486,7 +486,9 @@ struct SampleJob {
   }
 
   // The bins of zero have logits up to 2^-20, whose weights differ by that over T.
-  // Whether they matter, by a warp; then each id's own weight is added.
+  // Whether they matter, by a warp; then each id's own weight is added.  (One address
+  // for all ids: a row of 128256 logits of which half are 0 takes 0.2 ms with top-k 50,
+  // where one without zeros takes 0.02.)
   __device__ __forceinline__ bool zeros_matter(uint32_t (&c)[2], unsigned long long (&w)[2]) const {
     bin_of_cluster(Bins::kHalf - 1, &c[0], &w[0]);
     bin_of_cluster(Bins::kHalf, &c[1], &w[1]);
